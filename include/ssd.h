@@ -288,6 +288,139 @@ ssd_status ssd_gdn_chunk_fwd_o(const ssd_gdn_dims* d, const float* q, const floa
                                const float* v_new, const float* h, const float* g, float* o,
                                void* stream);
 
+/* Sizes of the linear-attention entry points.  `tokens` rows in all, `nseqs`
+ * sequences (for ssd_linattn_step: nseqs == tokens rows of one token each).
+ *   q, k [tokens, ngroups, kdim], v [tokens, nheads, vdim] in `dtype`; head h
+ *     reads group h / (nheads / ngroups) of q and k.  A row of each is
+ *     contiguous; rows lie q_stride, k_stride, v_stride elements apart (0:
+ *     contiguous), so that they can be column ranges of one projection's output.
+ *   kdim, vdim    16 .. 128, multiples of 16.  Strides: multiples of 16 bytes.
+ *   max_seqlen    no sequence is longer, or 0 if the caller does not know; it
+ *     only guides how the work is cut, a longer sequence is still right.
+ *   nheads <= 4096, nseqs <= 2^20, tokens <= 2^30. */
+typedef struct {
+    int64_t nseqs, tokens, nheads, ngroups, kdim, vdim;
+    int64_t q_stride, k_stride, v_stride;
+    int64_t max_seqlen;
+    int32_t dtype;      /* ssd_dtype of q, k, v, o and their gradients */
+    int32_t reserved;   /* must be 0 */
+} ssd_linattn_dims;
+
+/* Bytes of device workspace of ssd_linattn_fwd (backward = 0) or
+ * ssd_linattn_bwd (backward != 0): the states at the starts of the ranges into
+ * which long sequences are cut when there are few of them, and for the gradient
+ * of shared q and k the per-head terms; 0 if none is needed or `d` is invalid. */
+size_t ssd_linattn_workspace_bytes(const ssd_linattn_dims* d, int backward);
+
+/*
+ * ssd_linattn_fwd -- linear attention with a decay for each head, over a whole
+ * prompt.  With lam = exp(log_decay[h]), for each sequence and head, from
+ * S = init_state (or 0) and for its tokens t in order:
+ *   S <- lam S + v_t k_t^T  (vdim x kdim)        o_t = scale S q_t
+ * evaluated chunk by chunk: fp32 sums and state, o rounded once to `dtype`.
+ *   log_decay    [nheads] fp32, <= 0 (a larger value counts as 0; -inf: no memory).
+ *   cu_seqlens   [nseqs + 1] int32 on the device: sequence s is the rows
+ *                cu_seqlens[s] .. cu_seqlens[s + 1] - 1; cu_seqlens[0] == 0, not
+ *                decreasing, a length of 0 allowed.  Values outside 0 .. tokens
+ *                are clamped.  Rows from cu_seqlens[nseqs] on belong to no
+ *                sequence: their o is 0.  NULL: nseqs equal lengths
+ *                (SSD_ERR_SHAPE unless they divide tokens).
+ *   init_state   [nseqs, nheads, vdim, kdim] fp32, or NULL for 0.
+ *   o            output [tokens, nheads, vdim].
+ *   final_state  output [nseqs, nheads, vdim, kdim] fp32, or NULL to skip; it may
+ *                be init_state itself.  A sequence of no tokens passes its state on.
+ * What other sequences' rows hold, NaN and infinities among it, never reaches a
+ * sequence's results.  The result does not depend on the order in which the GPU
+ * runs the work.  `workspace`: see above.
+ */
+ssd_status ssd_linattn_fwd(const ssd_linattn_dims* d, const void* q, const void* k, const void* v,
+                           const float* log_decay, float scale, const int32_t* cu_seqlens,
+                           const float* init_state, void* o, float* final_state, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/*
+ * ssd_linattn_bwd -- the gradient of ssd_linattn_fwd.  With R the gradient of S,
+ * from R = dfinal_state (or 0) and for a sequence's tokens t in reverse order:
+ *   R <- R + scale dout_t q_t^T;  dk_t = R^T v_t;  dv_t = R k_t;  then R <- lam R
+ *   dq_t = scale S_t^T dout_t                 dinit_state = R after the first token
+ * dq and dk are summed over the heads of a group (in fp32, in the heads' order).
+ * The decays are constants: no gradient is computed for them.
+ *   q, k, v, log_decay, scale, cu_seqlens, init_state   as for ssd_linattn_fwd.
+ *   dout [tokens, nheads, vdim] in `dtype`; dfinal_state like final_state, or
+ *   NULL for 0.  Outputs: dq, dk [tokens, ngroups, kdim], dv [tokens, nheads,
+ *   vdim], all contiguous, in `dtype`; dinit_state fp32, or NULL to skip.
+ * Outputs must not overlap an input or each other (SSD_ERR_ALIAS).
+ */
+ssd_status ssd_linattn_bwd(const ssd_linattn_dims* d, const void* q, const void* k, const void* v,
+                           const void* dout, const float* log_decay, float scale,
+                           const int32_t* cu_seqlens, const float* init_state,
+                           const float* dfinal_state, void* dq, void* dk, void* dv,
+                           float* dinit_state, void* workspace, size_t workspace_bytes,
+                           void* stream);
+
+/*
+ * ssd_linattn_step -- linear attention for one more token of each of nseqs
+ * streams, whose states lie in a cache: row b of q, k, v continues the state in
+ * slot slots[b] (NULL: slot b), which is updated in place, and o[b] is its output.
+ *   slots   [nseqs] int32 on the device.  A value outside 0 .. nslots - 1 marks a
+ *           row without a stream: its o is 0 and no state is touched.  No slot may
+ *           occur twice in a call.
+ *   cache   [nslots, nheads, vdim, kdim] fp32 (the layout of final_state).
+ */
+ssd_status ssd_linattn_step(const ssd_linattn_dims* d, const void* q, const void* k, const void* v,
+                            const float* log_decay, float scale, const int32_t* slots, float* cache,
+                            int64_t nslots, void* o, void* stream);
+
+/* Gate of the block norms: a(z) = 1, z sigmoid(z) or sigmoid(z). */
+typedef enum { SSD_GATE_NONE = 0, SSD_GATE_SILU = 1, SSD_GATE_SIGMOID = 2 } ssd_gate;
+
+/* Sizes of the block norms: rows of `width` columns, 8 .. 16384; width / ngroups
+ * a multiple of 8.  y, z, n in `dtype`; the residual stream r, r_out in `rdtype`
+ * (fp32 beside fp32; either beside bf16).  Rows of y and z lie y_stride and
+ * z_stride elements apart (0: contiguous; multiples of 16 bytes). */
+typedef struct {
+    int64_t tokens, width, ngroups;
+    int64_t y_stride, z_stride;
+    int32_t gate;       /* ssd_gate */
+    float eps;          /* >= 0 */
+    int32_t dtype, rdtype;
+    int32_t reserved;   /* must be 0 */
+} ssd_norm_dims;
+
+/*
+ * ssd_block_norm_fwd -- the norm after a block, its gate, the residual's scale
+ * and the norm before the next block in one pass over each row:
+ *   yh    = y rsqrt(mean over the column's group of y^2 + eps)
+ *   r_out = r + alpha o w_post o a(z) o yh
+ *   n     = w_pre o r_out rsqrt(mean(r_out^2) + eps)
+ * (n from r_out before its rounding to rdtype).
+ *   w_post, alpha   [width] fp32, or NULL for 1.   w_pre [width] fp32 (required).
+ *   z               required unless the gate is SSD_GATE_NONE (then not read).
+ *   r_out           may be r itself (in place).
+ *   rstd_post [tokens, ngroups], rstd_pre [tokens] fp32: the two rsqrt factors,
+ *                   for the gradient; either may be NULL.
+ */
+ssd_status ssd_block_norm_fwd(const ssd_norm_dims* d, const void* r, const void* y, const void* z,
+                              const float* w_post, const float* alpha, const float* w_pre,
+                              void* r_out, void* n, float* rstd_post, float* rstd_pre, void* stream);
+
+/* Bytes of device workspace of ssd_block_norm_bwd; 0 if `d` is invalid or empty. */
+size_t ssd_block_norm_bwd_workspace_bytes(const ssd_norm_dims* d);
+
+/*
+ * ssd_block_norm_bwd -- the gradient of ssd_block_norm_fwd: from dr_out (rdtype)
+ * and dn (dtype), dr (rdtype), dy and dz (dtype, contiguous; dz not written
+ * without a gate), dw_post, dalpha, dw_pre [width] fp32 (the first two may be
+ * NULL to skip).  r, y, z are the forward pass's inputs, rstd_post and rstd_pre
+ * its outputs.  Column sums are added in a fixed order.
+ */
+ssd_status ssd_block_norm_bwd(const ssd_norm_dims* d, const void* r, const void* y, const void* z,
+                              const float* w_post, const float* alpha, const float* w_pre,
+                              const void* dr_out, const void* dn, const float* rstd_post,
+                              const float* rstd_pre, void* dr, void* dy, void* dz, float* dw_post,
+                              float* dalpha, float* dw_pre, void* workspace, size_t workspace_bytes,
+                              void* stream);
+
 /* Size of the fixed device scratch buffer used by ssd_fwd_noalloc: 32 MiB. */
 #define SSD_NOALLOC_WORKSPACE_BYTES ((size_t)32 << 20)
 

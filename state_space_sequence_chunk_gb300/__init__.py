@@ -14,6 +14,10 @@ Entry points (same names as the C ABI):
 * :func:`ssd_chunk_cumsum`, :func:`ssd_fwd_pass_state`,
   :func:`ssd_compute_out` -- the three steps one at a time.
 * :func:`ssd_fwd_workspace_bytes`, :func:`ssd_intermediate_bytes`.
+* :func:`linattn_fwd`, :func:`linattn_bwd`, :func:`linattn_step` -- linear
+  attention with a decay for each head: prompts, their gradient, single tokens.
+* :func:`block_norm_fwd`, :func:`block_norm_bwd` -- the norms before and after a
+  block with its gate and residual scale, and their gradient.
 """
 from __future__ import annotations
 
@@ -35,7 +39,10 @@ EXPORTS = ["ssd_abi_version", "ssd_status_string", "ssd_fwd_workspace_bytes",
            "ssd_fwd_pass_state_scratch_bytes", "ssd_compute_out", "ssd_fwd_noalloc",
            "ssd_take_device_errors", "ssd_debug_withhold_handoffs", "ssd_step",
            "ssd_causal_conv1d", "ssd_gdn_chunk_fwd_h", "ssd_gdn_chunk_fwd_o",
-           "ssd_fwd_host_staging_bytes", "ssd_fwd_host"]
+           "ssd_fwd_host_staging_bytes", "ssd_fwd_host", "ssd_linattn_workspace_bytes",
+           "ssd_linattn_fwd", "ssd_linattn_bwd", "ssd_linattn_step", "ssd_block_norm_fwd",
+           "ssd_block_norm_bwd_workspace_bytes", "ssd_block_norm_bwd"]
+GATES = {None: 0, "silu": 1, "sigmoid": 2}
 
 
 class SSDError(RuntimeError):
@@ -55,6 +62,18 @@ class GdnDims(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("nheads", ctypes.c_int64),
                 ("kdim", ctypes.c_int64), ("vdim", ctypes.c_int64), ("chunk", ctypes.c_int64),
                 ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class LinattnDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in
+                ("nseqs", "tokens", "nheads", "ngroups", "kdim", "vdim", "q_stride", "k_stride",
+                 "v_stride", "max_seqlen")] + [("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class NormDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("tokens", "width", "ngroups", "y_stride", "z_stride")] + [
+        ("gate", ctypes.c_int32), ("eps", ctypes.c_float), ("dtype", ctypes.c_int32),
+        ("rdtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 class Dims(ctypes.Structure):
@@ -115,6 +134,21 @@ def load_library(path: str = LIB_PATH):
         lib.ssd_fwd_host_staging_bytes.restype = sz
         lib.ssd_fwd_host.argtypes = [dp] + [vp] * 10 + [sz, ctypes.c_int, ctypes.POINTER(vp)]
         lib.ssd_fwd_host.restype = ctypes.c_int
+        la, nd, f32, i64 = ctypes.POINTER(LinattnDims), ctypes.POINTER(NormDims), ctypes.c_float, ctypes.c_int64
+        lib.ssd_linattn_workspace_bytes.argtypes = [la, ctypes.c_int]
+        lib.ssd_linattn_workspace_bytes.restype = sz
+        lib.ssd_linattn_fwd.argtypes = [la] + [vp] * 4 + [f32] + [vp] * 5 + [sz, vp]
+        lib.ssd_linattn_fwd.restype = ctypes.c_int
+        lib.ssd_linattn_bwd.argtypes = [la] + [vp] * 5 + [f32] + [vp] * 8 + [sz, vp]
+        lib.ssd_linattn_bwd.restype = ctypes.c_int
+        lib.ssd_linattn_step.argtypes = [la] + [vp] * 4 + [f32, vp, vp, i64, vp, vp]
+        lib.ssd_linattn_step.restype = ctypes.c_int
+        lib.ssd_block_norm_fwd.argtypes = [nd] + [vp] * 11
+        lib.ssd_block_norm_fwd.restype = ctypes.c_int
+        lib.ssd_block_norm_bwd_workspace_bytes.argtypes = [nd]
+        lib.ssd_block_norm_bwd_workspace_bytes.restype = sz
+        lib.ssd_block_norm_bwd.argtypes = [nd] + [vp] * 17 + [sz, vp]
+        lib.ssd_block_norm_bwd.restype = ctypes.c_int
         _lib = lib
         return lib
 
@@ -384,3 +418,220 @@ def ssd_fwd_noalloc(x, dt, A, B, C, D=None, init_state=None, chunk_size: int = 2
     _check(lib.ssd_fwd_noalloc(ctypes.byref(dims), _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C),
                                _ptr(D), _ptr(init_state), _ptr(y), _ptr(final_out), _stream()))
     return y, final_out
+
+
+def _dtype_code(t: torch.Tensor, name: str) -> int:
+    if t.dtype == torch.bfloat16:
+        return SSD_BF16
+    if t.dtype == torch.float32:
+        return SSD_F32
+    raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+
+
+def _typed(t, name: str, dtype, shape):
+    """t, checked: None passes, else dtype and shape have to be these."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    return t
+
+
+def _row_ptr(t, inner: int):
+    """Pointer and row stride of a tensor [rows, ...] whose rows are contiguous
+    (`inner` elements each) and evenly spaced."""
+    if not t.is_cuda:
+        raise ValueError("tensors must be CUDA tensors")
+    want = 1
+    for n, s in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+        if n != 1 and s != want:
+            raise ValueError("each row (all dimensions but the first) must be contiguous")
+        want *= n
+    return ctypes.c_void_p(t.data_ptr()), (t.stride(0) if t.shape[0] > 1 else inner)
+
+
+def _linattn_dims(q, k, v, log_decay, nseqs, max_seqlen):
+    if q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
+        raise ValueError("q and k must be [tokens, G, K] and v [tokens, H, V]")
+    T, G, K = q.shape
+    H, V = v.shape[1:]
+    _typed(k, "k", q.dtype, (T, G, K))
+    _typed(v, "v", q.dtype, (T, H, V))
+    _typed(log_decay, "log_decay", torch.float32, (H,))
+    (qp, qs), (kp, ks), (vp, vs) = _row_ptr(q, G * K), _row_ptr(k, G * K), _row_ptr(v, H * V)
+    d = LinattnDims(nseqs, T, H, G, K, V, qs, ks, vs, int(max_seqlen), _dtype_code(q, "q"), 0)
+    return d, (qp, kp, vp)
+
+
+def _linattn_nseqs(cu_seqlens, nseqs):
+    if cu_seqlens is None:
+        return int(nseqs)
+    if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+        raise ValueError("cu_seqlens must be a 1-D int32 tensor of nseqs + 1 values")
+    return cu_seqlens.numel() - 1
+
+
+def _linattn_workspace(lib, d, backward, workspace, device):
+    need = int(lib.ssd_linattn_workspace_bytes(ctypes.byref(d), backward))
+    if workspace is None and need > 0:
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    return workspace, 0 if workspace is None else workspace.numel() * workspace.element_size()
+
+
+def linattn_fwd(q, k, v, log_decay, cu_seqlens=None, scale: float = None, init_state=None,
+                nseqs: int = 1, max_seqlen: int = 0, return_final_state: bool = True,
+                workspace=None, out=None, final_out=None):
+    """Linear attention with a decay for each head: S_t = exp(log_decay[h]) S_{t-1} +
+    v_t k_t^T, o_t = scale S_t q_t (scale: K**-0.5 if not given).
+
+    q, k [tokens, G, K] and v [tokens, H, V] share one dtype (bfloat16 or float32)
+    and hold the sequences one after another: ``cu_seqlens`` (int32, nseqs + 1) says
+    where each begins, or without it they are ``nseqs`` of equal length.  Their rows
+    may be slices of a wider tensor's.  log_decay [H] and init_state
+    [nseqs, H, V, K] are float32.  ``max_seqlen`` (0: not known) spares the
+    preparations for long sequences where there are none.
+    Returns ``(o [tokens, H, V], final_state [nseqs, H, V, K] float32 or None)``.
+    """
+    lib = load_library()
+    n = _linattn_nseqs(cu_seqlens, nseqs)
+    d, (qp, kp, vp) = _linattn_dims(q, k, v, log_decay, n, max_seqlen)
+    T, H, V = v.shape
+    K = q.shape[2]
+    _typed(init_state, "init_state", torch.float32, (n, H, V, K))
+    o = _typed(out, "out", q.dtype, (T, H, V))
+    if o is None:
+        o = torch.empty((T, H, V), dtype=q.dtype, device=q.device)
+    fin = None
+    if return_final_state:
+        fin = _typed(final_out, "final_out", torch.float32, (n, H, V, K))
+        if fin is None:
+            fin = torch.empty((n, H, V, K), dtype=torch.float32, device=q.device)
+    workspace, nbytes = _linattn_workspace(lib, d, 0, workspace, q.device)
+    _check(lib.ssd_linattn_fwd(ctypes.byref(d), qp, kp, vp, _ptr(log_decay),
+                               K ** -0.5 if scale is None else float(scale), _ptr(cu_seqlens),
+                               _ptr(init_state), _ptr(o), _ptr(fin), _ptr(workspace), nbytes, _stream()))
+    return o, fin
+
+
+def linattn_bwd(q, k, v, dout, log_decay, cu_seqlens=None, scale: float = None, init_state=None,
+                dfinal_state=None, nseqs: int = 1, max_seqlen: int = 0, workspace=None):
+    """The gradient of linattn_fwd from dout [tokens, H, V] and dfinal_state (None: 0).
+    Returns ``(dq, dk, dv, dinit_state)``; dinit_state is None without an init_state."""
+    lib = load_library()
+    n = _linattn_nseqs(cu_seqlens, nseqs)
+    d, (qp, kp, vp) = _linattn_dims(q, k, v, log_decay, n, max_seqlen)
+    T, H, V = v.shape
+    K = q.shape[2]
+    _typed(dout, "dout", q.dtype, (T, H, V))
+    _typed(init_state, "init_state", torch.float32, (n, H, V, K))
+    _typed(dfinal_state, "dfinal_state", torch.float32, (n, H, V, K))
+    new = lambda shape, dt: torch.empty(shape, dtype=dt, device=q.device)
+    dq, dk, dv = new(q.shape, q.dtype), new(k.shape, q.dtype), new(v.shape, q.dtype)
+    d0 = None if init_state is None else new((n, H, V, K), torch.float32)
+    workspace, nbytes = _linattn_workspace(lib, d, 1, workspace, q.device)
+    _check(lib.ssd_linattn_bwd(ctypes.byref(d), qp, kp, vp, _ptr(dout), _ptr(log_decay),
+                               K ** -0.5 if scale is None else float(scale), _ptr(cu_seqlens),
+                               _ptr(init_state), _ptr(dfinal_state), _ptr(dq), _ptr(dk), _ptr(dv),
+                               _ptr(d0), _ptr(workspace), nbytes, _stream()))
+    return dq, dk, dv, d0
+
+
+def linattn_step(q, k, v, log_decay, cache, slots=None, scale: float = None, out=None):
+    """Linear attention for one more token of each row's stream: q, k [b, G, K],
+    v [b, H, V]; ``cache`` [nslots, H, V, K] float32 holds the states and is updated
+    in place; ``slots`` [b] int32 says which is whose (row b's slot is b without it;
+    a negative one marks a row without a stream, whose output is 0).
+    Returns o [b, H, V]."""
+    lib = load_library()
+    d, (qp, kp, vp) = _linattn_dims(q, k, v, log_decay, q.shape[0], 0)
+    b, H, V = v.shape
+    K = q.shape[2]
+    _typed(cache, "cache", torch.float32, (cache.shape[0], H, V, K))
+    _typed(slots, "slots", torch.int32, (b,))
+    o = _typed(out, "out", q.dtype, (b, H, V))
+    if o is None:
+        o = torch.empty((b, H, V), dtype=q.dtype, device=q.device)
+    _check(lib.ssd_linattn_step(ctypes.byref(d), qp, kp, vp, _ptr(log_decay),
+                                K ** -0.5 if scale is None else float(scale), _ptr(slots), _ptr(cache),
+                                cache.shape[0], _ptr(o), _stream()))
+    return o
+
+
+def _norm_dims(r, y, z, w_post, alpha, w_pre, gate, ngroups, eps):
+    if gate not in GATES:
+        raise ValueError(f"gate must be one of {list(GATES)}, got {gate!r}")
+    if y.dim() != 2:
+        raise ValueError("y must be [tokens, width]")
+    T, D = y.shape
+    if tuple(r.shape) != (T, D):
+        raise ValueError(f"r must be {[T, D]}, got {list(r.shape)}")
+    if gate is not None and z is None:
+        raise ValueError("a gate needs z")
+    _typed(z, "z", y.dtype, (T, D))
+    for name, w in (("w_post", w_post), ("alpha", alpha), ("w_pre", w_pre)):
+        _typed(w, name, torch.float32, (D,))
+    yp, ys = _row_ptr(y, D)
+    zp, zs = (None, 0) if z is None or gate is None else _row_ptr(z, D)
+    d = NormDims(T, D, int(ngroups), ys, zs, GATES[gate], float(eps), _dtype_code(y, "y"),
+                 _dtype_code(r, "r"), 0)
+    return d, yp, zp
+
+
+def block_norm_fwd(r, y, w_pre, z=None, w_post=None, alpha=None, gate=None, ngroups: int = 1,
+                   eps: float = 1e-5, return_rstd: bool = False, r_out=None, out=None):
+    """The norm after a block (y in ``ngroups`` groups of columns), its gate
+    (``"silu"`` or ``"sigmoid"`` of z, or None), the residual scale ``alpha`` and the
+    norm before the next block:
+    r_out = r + alpha w_post gate(z) rmsnorm(y), n = w_pre rmsnorm(r_out).
+
+    y, z and n [tokens, width] share one dtype; r and r_out may be float32 beside
+    bfloat16.  The weights are float32 [width].  Rows of y and z may be slices.
+    ``r_out`` may be r.  Returns ``(r_out, n)``, with ``return_rstd`` also the pair
+    of factors that block_norm_bwd needs."""
+    lib = load_library()
+    d, yp, zp = _norm_dims(r, y, z, w_post, alpha, w_pre, gate, ngroups, eps)
+    T, D = y.shape
+    ro = _typed(r_out, "r_out", r.dtype, (T, D))
+    if ro is None:
+        ro = torch.empty((T, D), dtype=r.dtype, device=y.device)
+    n = _typed(out, "out", y.dtype, (T, D))
+    if n is None:
+        n = torch.empty((T, D), dtype=y.dtype, device=y.device)
+    rstd = None
+    if return_rstd:
+        rstd = (torch.empty((T, int(ngroups)), dtype=torch.float32, device=y.device),
+                torch.empty((T,), dtype=torch.float32, device=y.device))
+    _check(lib.ssd_block_norm_fwd(ctypes.byref(d), _ptr(r), yp, zp, _ptr(w_post), _ptr(alpha),
+                                  _ptr(w_pre), _ptr(ro), _ptr(n), _ptr(rstd[0]) if rstd else None,
+                                  _ptr(rstd[1]) if rstd else None, _stream()))
+    return (ro, n, rstd) if return_rstd else (ro, n)
+
+
+def block_norm_bwd(r, y, w_pre, dr_out, dn, rstd, z=None, w_post=None, alpha=None, gate=None,
+                   ngroups: int = 1, eps: float = 1e-5, workspace=None):
+    """The gradient of block_norm_fwd (same inputs, and its ``rstd``) from dr_out and
+    dn.  Returns a dict: dr, dy, dz (None without a gate), dw_pre, dw_post and
+    dalpha (None where the weight is None)."""
+    lib = load_library()
+    d, yp, zp = _norm_dims(r, y, z, w_post, alpha, w_pre, gate, ngroups, eps)
+    T, D = y.shape
+    _typed(dr_out, "dr_out", r.dtype, (T, D))
+    _typed(dn, "dn", y.dtype, (T, D))
+    _typed(rstd[0], "rstd[0]", torch.float32, (T, int(ngroups)))
+    _typed(rstd[1], "rstd[1]", torch.float32, (T,))
+    new = lambda t: torch.empty((T, D), dtype=t.dtype, device=t.device)
+    col = lambda w: None if w is None else torch.empty((D,), dtype=torch.float32, device=y.device)
+    g = {"dr": new(r), "dy": new(y), "dz": None if gate is None else new(z), "dw_pre": col(w_pre),
+         "dw_post": col(w_post), "dalpha": col(alpha)}
+    need = int(lib.ssd_block_norm_bwd_workspace_bytes(ctypes.byref(d)))
+    if workspace is None and need > 0:
+        workspace = torch.empty(need, dtype=torch.uint8, device=y.device)
+    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(lib.ssd_block_norm_bwd(ctypes.byref(d), _ptr(r), yp, zp, _ptr(w_post), _ptr(alpha),
+                                  _ptr(w_pre), _ptr(dr_out), _ptr(dn), _ptr(rstd[0]), _ptr(rstd[1]),
+                                  _ptr(g["dr"]), _ptr(g["dy"]), _ptr(g["dz"]), _ptr(g["dw_post"]),
+                                  _ptr(g["dalpha"]), _ptr(g["dw_pre"]), _ptr(workspace), nbytes,
+                                  _stream()))
+    return g

@@ -1,0 +1,243 @@
+// linattn_api.cu -- the C entry points of linear attention: validation, the
+// cut of long sequences into ranges, workspace layout and launches.
+#include <math.h>
+
+#include "linattn_internal.cuh"
+
+namespace ssd {
+namespace {
+
+struct La {
+    int64_t n, T, H, G, K, V, qs, ks, vs, hpg;
+    int es;
+    LaGeom g;
+    size_t agg_bytes;    // one job's range states
+};
+
+int sm_count() {
+    // without a device (validation on a host that has none) the cut is made for
+    // this GPU's number of SMs
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+        cudaGetLastError();
+        return 152;
+    }
+    return sms;
+}
+
+ssd_status make_la(const ssd_linattn_dims* d, bool packed, La* p) {
+    if (!d) return SSD_ERR_NULL;
+    if (d->dtype != SSD_F32 && d->dtype != SSD_BF16) return SSD_ERR_DTYPE;
+    if (d->reserved != 0 || d->nseqs < 0 || d->tokens < 0 || d->max_seqlen < 0) return SSD_ERR_SHAPE;
+    if (d->nheads < 1 || d->nheads > 4096 || d->ngroups < 1 || d->nheads % d->ngroups != 0)
+        return SSD_ERR_SHAPE;
+    if (d->kdim < 16 || d->kdim > 128 || d->kdim % 16 != 0) return SSD_ERR_SHAPE;
+    if (d->vdim < 16 || d->vdim > 128 || d->vdim % 16 != 0) return SSD_ERR_SHAPE;
+    if (d->nseqs > (1 << 20) || d->tokens > (1LL << 30)) return SSD_ERR_SHAPE;
+    p->n = d->nseqs; p->T = d->tokens; p->H = d->nheads; p->G = d->ngroups;
+    p->K = d->kdim; p->V = d->vdim; p->hpg = p->H / p->G;
+    p->es = d->dtype == SSD_BF16 ? 2 : 4;
+    const int64_t grain = 16 / p->es;
+    p->qs = d->q_stride ? d->q_stride : p->G * p->K;
+    p->ks = d->k_stride ? d->k_stride : p->G * p->K;
+    p->vs = d->v_stride ? d->v_stride : p->H * p->V;
+    if (p->qs < p->G * p->K || p->ks < p->G * p->K || p->vs < p->H * p->V || p->qs % grain ||
+        p->ks % grain || p->vs % grain || p->qs > (1LL << 31) || p->ks > (1LL << 31) || p->vs > (1LL << 31))
+        return SSD_ERR_SHAPE;
+    if (!packed && p->n > 0 && p->T % p->n != 0) return SSD_ERR_SHAPE;
+    if (p->n == 0 && p->T > 0 && !packed) return SSD_ERR_SHAPE;
+
+    LaGeom& g = p->g;
+    g.cu = nullptr;
+    g.nseq = (int)p->n; g.H = (int)p->H; g.T = (int)p->T;
+    g.L = packed || p->n == 0 ? 0 : (int)(p->T / p->n);
+    g.a = nullptr;
+    // Ranges: about four for every SM if the work were spread evenly, none
+    // shorter than 512 tokens.  A sequence that fits one range is not cut; longer
+    // ones pay a second reading of two operands and gain the whole GPU.
+    const int64_t cols = ((p->K > p->V ? p->K : p->V) + kLaCols - 1) / kLaCols;
+    int64_t R = p->T * p->H * cols / (4 * (int64_t)sm_count());
+    R = (R + 127) / 128 * 128;
+    if (R < 512) R = 512;
+    int64_t longest = packed ? (d->max_seqlen ? d->max_seqlen : p->T) : g.L;
+    if (longest > p->T) longest = p->T;
+    g.split = longest > R;
+    g.R = g.split ? (int)R : (int)(p->T > 0 ? (p->T + 127) / 128 * 128 : 128);
+    const int64_t cap = g.split ? p->T / R + p->n + 1 : p->n + 1;
+    if (cap > (1LL << 24)) return SSD_ERR_SHAPE;
+    g.range_cap = (int)cap;
+    p->agg_bytes = g.split ? round_up256((size_t)(cap * p->H * p->K * p->V) * 4) : 0;
+    return SSD_OK;
+}
+
+size_t part_bytes(const La& p) {   // per-head dq and dk, before the sum over a group
+    return p.hpg > 1 ? 2 * round_up256((size_t)(p.T * p.H * p.K) * 4) : 0;
+}
+// bytes from the first to one past the last element of a strided [T, w] operand
+size_t span(int64_t T, int64_t stride, int64_t w, int es) {
+    return T > 0 ? (size_t)((T - 1) * stride + w) * es : 0;
+}
+
+cudaError_t run_jobs(LaParams& p, int dtype, cudaStream_t st) {
+    cudaError_t e = cudaSuccess;
+    if (p.g.split) {
+        e = launch_linattn_simt(p, dtype, 1, st);
+        if (e == cudaSuccess) e = launch_linattn_scan(p, st);
+    }
+    return e != cudaSuccess ? e : launch_linattn_simt(p, dtype, 0, st);
+}
+
+}  // namespace
+}  // namespace ssd
+
+using namespace ssd;
+
+extern "C" {
+
+size_t ssd_linattn_workspace_bytes(const ssd_linattn_dims* d, int backward) {
+    // enough for packed and, where the sizes allow them, equal sequences
+    size_t need = 0;
+    for (int packed = 0; packed < 2; ++packed) {
+        La p;
+        if (make_la(d, packed != 0, &p) != SSD_OK) continue;
+        const size_t b = backward ? 3 * p.agg_bytes + part_bytes(p) : p.agg_bytes;
+        if (b > need) need = b;
+    }
+    return need;
+}
+
+ssd_status ssd_linattn_fwd(const ssd_linattn_dims* d, const void* q, const void* k, const void* v,
+                           const float* log_decay, float scale, const int32_t* cu_seqlens,
+                           const float* init_state, void* o, float* final_state, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+    La p;
+    ssd_status s = make_la(d, cu_seqlens != nullptr, &p);
+    if (s != SSD_OK) return s;
+    if (p.n == 0 && p.T == 0) return SSD_OK;
+    if (!isfinite(scale)) return SSD_ERR_SHAPE;
+    if (!log_decay || (p.T > 0 && (!q || !k || !v || !o))) return SSD_ERR_NULL;
+    if (p.agg_bytes > 0 && !workspace) return SSD_ERR_NULL;
+    if (workspace_bytes < p.agg_bytes) return SSD_ERR_WORKSPACE;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(log_decay) ||
+        !aligned16(cu_seqlens) || !aligned16(init_state) || !aligned16(final_state) ||
+        !aligned16(workspace))
+        return SSD_ERR_ALIGN;
+    const size_t sb = (size_t)(p.n * p.H * p.V * p.K) * 4, ob = (size_t)(p.T * p.H * p.V) * p.es;
+    const Range in[] = {rng(q, span(p.T, p.qs, p.G * p.K, p.es)), rng(k, span(p.T, p.ks, p.G * p.K, p.es)),
+                        rng(v, span(p.T, p.vs, p.H * p.V, p.es)), rng(log_decay, (size_t)p.H * 4),
+                        rng(cu_seqlens, (size_t)(p.n + 1) * 4), rng(init_state, sb)};
+    const Range out[] = {rng(o, ob), rng(workspace, p.agg_bytes), rng(final_state, sb)};
+    for (int i = 0; i < 6; ++i)
+        for (int j = 0; j < 3; ++j)
+            if (overlap(in[i], out[j]) && !(i == 5 && j == 2 && init_state == final_state))
+                return SSD_ERR_ALIAS;
+    for (int i = 0; i < 3; ++i)
+        for (int j = 0; j < i; ++j)
+            if (overlap(out[i], out[j])) return SSD_ERR_ALIAS;
+    if ((s = pre_launch()) != SSD_OK) return s;
+    LaParams lp;
+    lp.g = p.g;
+    lp.g.cu = cu_seqlens;
+    lp.g.a = log_decay;
+    lp.njobs = 1;
+    LaJob& j = lp.job[0];
+    j = LaJob{q, k, v, p.qs, p.ks, p.vs, (int)p.hpg, (int)p.hpg, 1, (int)p.G, (int)p.G, (int)p.H,
+              (int)p.K, (int)p.V, o, 0, 0, 1.f, scale, 1, (int)p.K, init_state, final_state,
+              (float*)workspace};
+    return from_cuda(run_jobs(lp, d->dtype, (cudaStream_t)stream));
+}
+
+ssd_status ssd_linattn_bwd(const ssd_linattn_dims* d, const void* q, const void* k, const void* v,
+                           const void* dout, const float* log_decay, float scale,
+                           const int32_t* cu_seqlens, const float* init_state,
+                           const float* dfinal_state, void* dq, void* dk, void* dv,
+                           float* dinit_state, void* workspace, size_t workspace_bytes,
+                           void* stream) {
+    La p;
+    ssd_status s = make_la(d, cu_seqlens != nullptr, &p);
+    if (s != SSD_OK) return s;
+    if (p.n == 0 && p.T == 0) return SSD_OK;
+    if (!isfinite(scale)) return SSD_ERR_SHAPE;
+    if (!log_decay || (p.T > 0 && (!q || !k || !v || !dout || !dq || !dk || !dv))) return SSD_ERR_NULL;
+    const size_t need = 3 * p.agg_bytes + part_bytes(p);
+    if (need > 0 && !workspace) return SSD_ERR_NULL;
+    if (workspace_bytes < need) return SSD_ERR_WORKSPACE;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(dout) || !aligned16(dq) ||
+        !aligned16(dk) || !aligned16(dv) || !aligned16(log_decay) || !aligned16(cu_seqlens) ||
+        !aligned16(init_state) || !aligned16(dfinal_state) || !aligned16(dinit_state) ||
+        !aligned16(workspace))
+        return SSD_ERR_ALIGN;
+    const size_t sb = (size_t)(p.n * p.H * p.V * p.K) * 4, vb = (size_t)(p.T * p.H * p.V) * p.es,
+                 kb = (size_t)(p.T * p.G * p.K) * p.es;
+    const Range in[] = {rng(q, span(p.T, p.qs, p.G * p.K, p.es)), rng(k, span(p.T, p.ks, p.G * p.K, p.es)),
+                        rng(v, span(p.T, p.vs, p.H * p.V, p.es)), rng(dout, vb),
+                        rng(log_decay, (size_t)p.H * 4), rng(cu_seqlens, (size_t)(p.n + 1) * 4),
+                        rng(init_state, sb), rng(dfinal_state, sb)};
+    const Range out[] = {rng(dq, kb), rng(dk, kb), rng(dv, vb), rng(dinit_state, sb), rng(workspace, need)};
+    for (const Range& a : in)
+        for (const Range& b : out)
+            if (overlap(a, b)) return SSD_ERR_ALIAS;
+    for (int i = 0; i < 5; ++i)
+        for (int j = 0; j < i; ++j)
+            if (overlap(out[i], out[j])) return SSD_ERR_ALIAS;
+    if ((s = pre_launch()) != SSD_OK) return s;
+    char* ws = (char*)workspace;
+    float *agg[3], *part[2] = {nullptr, nullptr};
+    for (int i = 0; i < 3; ++i) agg[i] = (float*)(ws + i * p.agg_bytes);
+    if (p.hpg > 1)
+        for (int i = 0; i < 2; ++i) part[i] = (float*)(ws + 3 * p.agg_bytes + i * (part_bytes(p) / 2));
+    LaParams lp;
+    lp.g = p.g;
+    lp.g.cu = cu_seqlens;
+    lp.g.a = log_decay;
+    lp.njobs = 3;
+    const int G = (int)p.G, H = (int)p.H, K = (int)p.K, V = (int)p.V, hpg = (int)p.hpg;
+    const int64_t os = p.H * p.V;
+    const int shared = hpg > 1;
+    // dq = F(do, v; k): X = S^T of the forward pass
+    lp.job[0] = LaJob{dout, v, k, os, p.vs, p.ks, 1, 1, hpg, H, H, G, V, K, shared ? (void*)part[0] : dq,
+                      shared, 0, 1.f, scale, K, 1, init_state, nullptr, agg[0]};
+    // dk = Frev(v, do; q): X = R
+    lp.job[1] = LaJob{v, dout, q, p.vs, os, p.qs, 1, 1, hpg, H, H, G, V, K, shared ? (void*)part[1] : dk,
+                      shared, 1, scale, 1.f, K, 1, dfinal_state, nullptr, agg[1]};
+    // dv = Frev(k, q; do): X = R^T, which ends as dS_0
+    lp.job[2] = LaJob{k, q, dout, p.ks, p.qs, os, hpg, hpg, 1, G, G, H, K, V, dv,
+                      0, 1, scale, 1.f, 1, K, dfinal_state, dinit_state, agg[2]};
+    cudaStream_t st = (cudaStream_t)stream;
+    cudaError_t e = run_jobs(lp, d->dtype, st);
+    if (shared && p.T > 0) {
+        if (e == cudaSuccess) e = launch_linattn_group_sum(part[0], dq, p.T, G, hpg, K, d->dtype, st);
+        if (e == cudaSuccess) e = launch_linattn_group_sum(part[1], dk, p.T, G, hpg, K, d->dtype, st);
+    }
+    return from_cuda(e);
+}
+
+ssd_status ssd_linattn_step(const ssd_linattn_dims* d, const void* q, const void* k, const void* v,
+                            const float* log_decay, float scale, const int32_t* slots, float* cache,
+                            int64_t nslots, void* o, void* stream) {
+    La p;
+    ssd_status s = make_la(d, true, &p);
+    if (s != SSD_OK) return s;
+    if (p.n != p.T || nslots < 0 || !isfinite(scale)) return SSD_ERR_SHAPE;
+    if (!slots && nslots < p.n) return SSD_ERR_SHAPE;
+    if (p.n * p.H > (1LL << 31) - 1) return SSD_ERR_SHAPE;
+    if (p.n == 0) return SSD_OK;
+    if (!q || !k || !v || !log_decay || !o || (!cache && nslots > 0)) return SSD_ERR_NULL;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(log_decay) ||
+        !aligned16(slots) || !aligned16(cache) || !aligned16(o))
+        return SSD_ERR_ALIGN;
+    const Range in[] = {rng(q, span(p.T, p.qs, p.G * p.K, p.es)), rng(k, span(p.T, p.ks, p.G * p.K, p.es)),
+                        rng(v, span(p.T, p.vs, p.H * p.V, p.es)), rng(log_decay, (size_t)p.H * 4),
+                        rng(slots, (size_t)p.n * 4)};
+    const Range cr = rng(cache, (size_t)(nslots * p.H * p.V * p.K) * 4);
+    const Range orr = rng(o, (size_t)(p.T * p.H * p.V) * p.es);
+    for (const Range& r : in)
+        if (overlap(r, cr) || overlap(r, orr)) return SSD_ERR_ALIAS;
+    if (overlap(cr, orr)) return SSD_ERR_ALIAS;
+    if ((s = pre_launch()) != SSD_OK) return s;
+    return from_cuda(launch_linattn_step(*d, p.qs, p.ks, p.vs, q, k, v, log_decay, scale, slots,
+                                         cache, nslots, o, (cudaStream_t)stream));
+}
+
+}  // extern "C"

@@ -1,0 +1,331 @@
+// linattn_simt.cu -- linear attention on the CUDA cores, and the small kernels
+// shared with the tensor-core form: the scan over ranges and the sum over the
+// heads of a group.
+//
+// Per chunk of 64 tokens with i, j its rows (forwards; backwards the exponents
+// are mirrored):
+//     P = s_in (A B^T) o lam^{i-j} [i >= j]
+//     out = s_out (P C + lam^{i+1} o (A X))
+//     X <- lam^n X + s_in B^T (lam^{n-1-j} o C)
+// in fp32 FMAs on shared-memory tiles: 256 threads, each with a 4 x 4 block of
+// P and of the output and an 8 x 4 block of X.  fp32 operands need it: a TF32
+// product keeps 11 bits of them.
+#include "linattn_internal.cuh"
+
+namespace ssd {
+namespace {
+
+constexpr int kC = 64;            // tokens per chunk
+constexpr int kPitch = kC + 4;    // floats per row of a tile with kC columns
+constexpr int kThreads = 256;
+constexpr int kMaxK = 128;
+
+struct Smem {
+    float At[kMaxK * kPitch];     // A transposed: [k][i]
+    float Bt[kMaxK * kPitch];     // B transposed: [k][j]
+    float X[kMaxK * kPitch];      // state [k][v]
+    float Cv[kC * kPitch];        // C: [j][v]
+    float Pt[kC * kPitch];        // P transposed: [j][i]
+    float lamp[kC + 1];           // lam^0 .. lam^64
+    LaRange rg;
+};
+
+__device__ __forceinline__ float4 ld4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ void unpack(const float* p, float (&f)[4]) {
+    const float4 v = __ldg(reinterpret_cast<const float4*>(p));
+    f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
+}
+__device__ __forceinline__ void unpack(const __nv_bfloat16* p, float (&f)[4]) {
+    const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+    f[0] = __uint_as_float(v.x << 16); f[1] = __uint_as_float(v.x & 0xFFFF0000u);
+    f[2] = __uint_as_float(v.y << 16); f[3] = __uint_as_float(v.y & 0xFFFF0000u);
+}
+
+// rows [t0, t0 + n) of an operand, D columns, transposed into dst[d][row]; rows
+// past n are zero (whatever memory holds there)
+template <typename T>
+__device__ __forceinline__ void load_t(float* dst, const T* src, int64_t stride, int n, int D) {
+    const int row = threadIdx.x & (kC - 1);
+    for (int d = (threadIdx.x / kC) * 4; d < D; d += (kThreads / kC) * 4) {
+        float f[4] = {0.f, 0.f, 0.f, 0.f};
+        if (row < n) unpack(src + (int64_t)row * stride + d, f);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) dst[(d + e) * kPitch + row] = f[e];
+    }
+}
+
+__device__ __forceinline__ void fma44(float (&acc)[4][4], const float4& a, const float4& b) {
+    const float av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+#pragma unroll
+        for (int y = 0; y < 4; ++y) acc[x][y] = fmaf(av[x], bv[y], acc[x][y]);
+}
+
+template <typename T, bool kAgg>
+__global__ void __launch_bounds__(kThreads) linattn_simt(const __grid_constant__ LaParams p) {
+    extern __shared__ __align__(16) uint8_t raw[];
+    Smem& s = *reinterpret_cast<Smem*>(raw);
+    const LaGeom& g = p.g;
+    const LaJob& jb = p.job[blockIdx.z];
+    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    const int nvb = (jb.DV + kLaCols - 1) / kLaCols;
+    const int h = blockIdx.y / nvb, v0 = (blockIdx.y - h * nvb) * kLaCols;
+    if (h >= g.H) return;
+    if (tid < 32) {
+        const LaRange r = la_find(g, blockIdx.x);
+        if (tid == 0) s.rg = r;
+    }
+    const float a2 = la_log2_decay(g.a, h);
+    if (tid <= kC) s.lamp[tid] = exp2f(a2 * (float)tid);
+    __syncthreads();
+    const LaRange rg = s.rg;
+    if (rg.seq < 0) return;
+    const int nv = min(kLaCols, jb.DV - v0);
+    if (rg.seq == g.nseq) {               // tokens of no sequence: zeros
+        if (kAgg) return;
+        for (int i = tid; i < rg.len * nv; i += kThreads) {
+            const int t = i / nv, v = i - t * nv;
+            const int64_t at = ((int64_t)(rg.t0 + t) * g.H + h) * jb.DV + v0 + v;
+            if (jb.out_f32) static_cast<float*>(jb.out)[at] = 0.f;
+            else static_cast<T*>(jb.out)[at] = from_f32<T>(0.f);
+        }
+        return;
+    }
+    const bool cut = g.split && rg.n > 1;
+    const bool last = jb.rev ? rg.r == 0 : rg.r == rg.n - 1;
+    if (kAgg && (!cut || last)) return;
+    const int64_t elems = (int64_t)jb.DK * jb.DV;
+    const int64_t so = ((int64_t)rg.seq * g.H + h) * elems;
+    float* ag = cut ? jb.agg + ((int64_t)blockIdx.x * g.H + h) * elems : nullptr;
+    const float* in = kAgg ? nullptr : (cut ? ag : (jb.init ? jb.init + so : nullptr));
+    for (int i = tid; i < jb.DK * kLaCols; i += kThreads) {
+        const int k = i % jb.DK, v = i / jb.DK;
+        s.X[k * kPitch + v] = in && v < nv ? in[(int64_t)k * jb.sk + (int64_t)(v0 + v) * jb.sv] : 0.f;
+    }
+    const T* Ap = static_cast<const T*>(jb.A) + (int64_t)(h / jb.dA) * jb.DK;
+    const T* Bp = static_cast<const T*>(jb.B) + (int64_t)(h / jb.dB) * jb.DK;
+    const T* Cp = static_cast<const T*>(jb.C) + (int64_t)(h / jb.dC) * jb.DV + v0;
+    const int nch = (rg.len + kC - 1) / kC;
+    float cf_hi, cf_lo;
+    la_decay_pow(g.a, h, kC, cf_hi, cf_lo);
+    for (int ci = 0; ci < nch; ++ci) {
+        const int c = jb.rev ? nch - 1 - ci : ci;
+        const int t0 = rg.t0 + c * kC, n = min(kC, rg.len - c * kC);
+        __syncthreads();
+        if (!kAgg) load_t(s.At, Ap + (int64_t)t0 * jb.sA, jb.sA, n, jb.DK);
+        load_t(s.Bt, Bp + (int64_t)t0 * jb.sB, jb.sB, n, jb.DK);
+        for (int i = tid; i < kC * (kLaCols / 4); i += kThreads) {
+            const int row = i / (kLaCols / 4), v = (i % (kLaCols / 4)) * 4;
+            float f[4] = {0.f, 0.f, 0.f, 0.f};
+            if (row < n && v < nv) unpack(Cp + (int64_t)(t0 + row) * jb.sC + v, f);
+            *reinterpret_cast<float4*>(s.Cv + row * kPitch + v) = make_float4(f[0], f[1], f[2], f[3]);
+        }
+        __syncthreads();
+        if (!kAgg) {
+            float acc[4][4] = {};
+#pragma unroll 4
+            for (int k = 0; k < jb.DK; ++k)
+                fma44(acc, ld4(s.At + k * kPitch + ty * 4), ld4(s.Bt + k * kPitch + tx * 4));
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                const int j = tx * 4 + y;
+                float w[4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const int i = ty * 4 + x, d = jb.rev ? j - i : i - j;
+                    w[x] = d >= 0 ? acc[x][y] * (s.lamp[d] * jb.s_in) : 0.f;
+                }
+                *reinterpret_cast<float4*>(s.Pt + j * kPitch + ty * 4) = make_float4(w[0], w[1], w[2], w[3]);
+            }
+            float o1[4][4] = {}, o2[4][4] = {};
+#pragma unroll 4
+            for (int k = 0; k < jb.DK; ++k)
+                fma44(o1, ld4(s.At + k * kPitch + ty * 4), ld4(s.X + k * kPitch + tx * 4));
+            __syncthreads();
+#pragma unroll 4
+            for (int j = 0; j < kC; ++j)
+                fma44(o2, ld4(s.Pt + j * kPitch + ty * 4), ld4(s.Cv + j * kPitch + tx * 4));
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const int i = ty * 4 + x;
+                if (i >= n || tx * 4 >= nv) continue;
+                const float f = s.lamp[jb.rev ? n - 1 - i : i + 1];
+                float r[4];
+#pragma unroll
+                for (int y = 0; y < 4; ++y) r[y] = jb.s_out * fmaf(f, o1[x][y], o2[x][y]);
+                const int64_t at = ((int64_t)(t0 + i) * g.H + h) * jb.DV + v0 + tx * 4;
+                if (jb.out_f32) {
+                    *reinterpret_cast<float4*>(static_cast<float*>(jb.out) + at) = make_float4(r[0], r[1], r[2], r[3]);
+                } else {
+                    T* dst = static_cast<T*>(jb.out) + at;
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) dst[y] = from_f32<T>(r[y]);
+                }
+            }
+        }
+        // X <- lam^n X + s_in B^T (w o C); every thread reads and writes its own 8 x 4
+        if (ty * 8 < jb.DK) {
+            float u[2][4][4] = {};
+            for (int j = 0; j < n; j += 4) {
+                float4 b[8], cc[4];
+#pragma unroll
+                for (int x = 0; x < 8; ++x) b[x] = ld4(s.Bt + (ty * 8 + x) * kPitch + j);
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    const int jj = j + y;
+                    const float w = jj < n ? s.lamp[jb.rev ? jj + 1 : n - 1 - jj] * jb.s_in : 0.f;
+                    cc[y] = ld4(s.Cv + jj * kPitch + tx * 4);
+                    cc[y].x *= w; cc[y].y *= w; cc[y].z *= w; cc[y].w *= w;
+                }
+#pragma unroll
+                for (int x2 = 0; x2 < 2; ++x2)
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        const float4* bb = b + 4 * x2;
+                        const float4 col = y == 0 ? make_float4(bb[0].x, bb[1].x, bb[2].x, bb[3].x)
+                                         : y == 1 ? make_float4(bb[0].y, bb[1].y, bb[2].y, bb[3].y)
+                                         : y == 2 ? make_float4(bb[0].z, bb[1].z, bb[2].z, bb[3].z)
+                                                  : make_float4(bb[0].w, bb[1].w, bb[2].w, bb[3].w);
+                        fma44(u[x2], col, cc[y]);
+                    }
+            }
+            float hi = cf_hi, lo = cf_lo;
+            if (n < kC) la_decay_pow(g.a, h, n, hi, lo);
+#pragma unroll
+            for (int x2 = 0; x2 < 2; ++x2)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    float* X = s.X + (ty * 8 + 4 * x2 + x) * kPitch + tx * 4;
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) X[y] = fmaf(X[y], hi, fmaf(X[y], lo, u[x2][x][y]));
+                }
+        }
+    }
+    __syncthreads();
+    float* outst = kAgg ? ag : (last && jb.fin ? jb.fin + so : nullptr);
+    if (outst == nullptr) return;
+    for (int i = tid; i < jb.DK * nv; i += kThreads) {
+        const int k = i % jb.DK, v = i / jb.DK;
+        outst[(int64_t)k * jb.sk + (int64_t)(v0 + v) * jb.sv] = s.X[k * kPitch + v];
+    }
+}
+
+// One thread per state element of (sequence, head): walks the sequence's
+// ranges, leaving in agg the state at each range's start.
+__global__ void __launch_bounds__(256) linattn_scan(const __grid_constant__ LaParams p, int eblocks) {
+    const LaGeom& g = p.g;
+    const LaJob& jb = p.job[blockIdx.z];
+    const int seq = blockIdx.x / eblocks, eb = blockIdx.x - seq * eblocks, h = blockIdx.y;
+    __shared__ int s_base, s_lo, s_hi;
+    if (threadIdx.x < 32) {   // ranges before this sequence
+        int sum = 0;
+        for (int s = threadIdx.x; s < seq; s += 32) {
+            int lo, hi;
+            la_bounds(g, s, lo, hi);
+            sum += la_count(g, s, lo, hi);
+        }
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (threadIdx.x == 0) {
+            int lo, hi;
+            la_bounds(g, seq, lo, hi);
+            s_base = sum; s_lo = lo; s_hi = hi;
+        }
+    }
+    __syncthreads();
+    const int n = la_count(g, seq, s_lo, s_hi), len = s_hi - s_lo;
+    if (n <= 1 || s_base + n > g.range_cap) return;
+    const int elems = jb.DK * jb.DV;
+    const int e = (eb * 256 + threadIdx.x) * 4;
+    if (e >= elems) return;
+    float4 S = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (jb.init) S = *reinterpret_cast<const float4*>(jb.init + ((int64_t)seq * g.H + h) * elems + e);
+    float f_hi, f_lo, t_hi, t_lo;
+    la_decay_pow(g.a, h, g.R, f_hi, f_lo);
+    la_decay_pow(g.a, h, len - (n - 1) * g.R, t_hi, t_lo);
+    // four ranges' sums in flight
+    for (int i0 = 0; i0 < n; i0 += 4) {
+        float4 u[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int i = i0 + q, r = jb.rev ? n - 1 - i : i;
+            if (i < n - 1)
+                u[q] = *reinterpret_cast<const float4*>(jb.agg + ((int64_t)(s_base + r) * g.H + h) * elems + e);
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int i = i0 + q, r = jb.rev ? n - 1 - i : i;
+            if (i >= n) break;
+            *reinterpret_cast<float4*>(jb.agg + ((int64_t)(s_base + r) * g.H + h) * elems + e) = S;
+            if (i == n - 1) break;   // the last range's pass writes the final state
+            const float hi = r == n - 1 ? t_hi : f_hi, lo = r == n - 1 ? t_lo : f_lo;
+            S.x = fmaf(S.x, hi, fmaf(S.x, lo, u[q].x));
+            S.y = fmaf(S.y, hi, fmaf(S.y, lo, u[q].y));
+            S.z = fmaf(S.z, hi, fmaf(S.z, lo, u[q].z));
+            S.w = fmaf(S.w, hi, fmaf(S.w, lo, u[q].w));
+        }
+    }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256) linattn_group_sum(const float* __restrict__ part,
+                                                         T* __restrict__ out, int64_t n4, int hpg,
+                                                         int d4) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= n4) return;
+    const int64_t row = i / d4;   // (token, group)
+    const int col = (int)(i - row * d4);
+    const float4* src = reinterpret_cast<const float4*>(part) + row * hpg * d4 + col;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int x = 0; x < hpg; ++x) {
+        const float4 v = src[(int64_t)x * d4];
+        a.x += v.x; a.y += v.y; a.z += v.z; a.w += v.w;
+    }
+    T* dst = out + 4 * i;
+    dst[0] = from_f32<T>(a.x);
+    dst[1] = from_f32<T>(a.y);
+    dst[2] = from_f32<T>(a.z);
+    dst[3] = from_f32<T>(a.w);
+}
+
+template <typename T, bool kAgg>
+cudaError_t go(const LaParams& p, cudaStream_t stream) {
+    int nvb = 1;
+    for (int j = 0; j < p.njobs; ++j) {
+        const int n = (p.job[j].DV + kLaCols - 1) / kLaCols;
+        nvb = n > nvb ? n : nvb;
+    }
+    auto k = linattn_simt<T, kAgg>;
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem));
+    if (e != cudaSuccess) return e;
+    k<<<dim3((unsigned)p.g.range_cap, (unsigned)(p.g.H * nvb), (unsigned)p.njobs), kThreads, sizeof(Smem), stream>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_linattn_simt(const LaParams& p, int dtype, int mode, cudaStream_t stream) {
+    if (dtype == SSD_BF16)
+        return mode ? go<__nv_bfloat16, true>(p, stream) : go<__nv_bfloat16, false>(p, stream);
+    return mode ? go<float, true>(p, stream) : go<float, false>(p, stream);
+}
+
+cudaError_t launch_linattn_scan(const LaParams& p, cudaStream_t stream) {
+    const int elems = p.job[0].DK * p.job[0].DV;   // the same product for every job
+    const int eblocks = (elems / 4 + 255) / 256;
+    linattn_scan<<<dim3((unsigned)(p.g.nseq * eblocks), (unsigned)p.g.H, (unsigned)p.njobs), 256, 0, stream>>>(p, eblocks);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_linattn_group_sum(const float* part, void* out, int64_t T, int G, int hpg, int D,
+                                     int dtype, cudaStream_t stream) {
+    const int64_t n4 = T * G * (D / 4);
+    const unsigned blocks = (unsigned)((n4 + 255) / 256);
+    if (dtype == SSD_BF16)
+        linattn_group_sum<__nv_bfloat16><<<blocks, 256, 0, stream>>>(part, (__nv_bfloat16*)out, n4, hpg, D / 4);
+    else
+        linattn_group_sum<float><<<blocks, 256, 0, stream>>>(part, (float*)out, n4, hpg, D / 4);
+    return cudaGetLastError();
+}
+
+}  // namespace ssd

@@ -13,8 +13,6 @@ constexpr size_t kAlign = 256;
 
 size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
-bool aligned16(const void* p) { return p == nullptr || ((uintptr_t)p & 15u) == 0; }
-
 // Validate sizes; fills `p`.  Does not look at pointers.
 ssd_status make_problem(const ssd_dims* d, Problem* p) {
     if (!d) return SSD_ERR_NULL;
@@ -43,16 +41,6 @@ ssd_status make_problem(const ssd_dims* d, Problem* p) {
 size_t gcs_bytes(const Problem& p) { return (size_t)(p.b * p.H * p.Lp) * sizeof(float); }
 size_t hid_bytes(const Problem& p) { return (size_t)(p.b * p.H * p.nc * p.P * p.N) * p.esize; }
 
-struct Range {
-    uintptr_t lo, hi;  // [lo, hi)
-};
-Range rng(const void* ptr, size_t bytes) {
-    return Range{(uintptr_t)ptr, (uintptr_t)ptr + bytes};
-}
-bool overlap(Range a, Range b) {
-    return a.lo != 0 && b.lo != 0 && a.hi > a.lo && b.hi > b.lo && a.lo < b.hi && b.lo < a.hi;
-}
-
 // The device must be compute capability 10.3 (the kernels are built for sm_103a).
 ssd_status check_arch() {
     int dev = 0;
@@ -68,11 +56,6 @@ ssd_status check_arch() {
     const bool ok = (major == 10 && minor == 3);
     if (dev >= 0 && dev < 64) cached[dev] = ok ? 1 : 2;
     return ok ? SSD_OK : SSD_ERR_ARCH;
-}
-
-ssd_status from_cuda(cudaError_t e) {
-    if (e == cudaSuccess) return SSD_OK;
-    return SSD_ERR_CUDA;
 }
 
 // One page of host memory, page-locked and mapped into every device's address
@@ -115,17 +98,13 @@ unsigned int take_errors() {
     return (a ? 1u : 0u) | (b ? 2u : 0u) | (c ? 4u : 0u);
 }
 
-// Checks made after the arguments are validated and before anything is
-// enqueued: the device's compute capability, then whether a bounded wait in
-// an earlier launch on this device has given up (reported once, as
-// SSD_ERR_TIMEOUT; reporting it synchronises the device and clears the record).
+}  // namespace
+
 ssd_status pre_launch() {
     const ssd_status s = check_arch();
     if (s != SSD_OK) return s;
     return timeout_pending();
 }
-
-}  // namespace
 
 ssd_status timeout_pending() {
     int dev = 0;

@@ -147,6 +147,24 @@ cudaError_t launch_chained(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
+// Argument checks shared by the entry points.
+struct Range {
+    uintptr_t lo, hi;  // [lo, hi)
+};
+inline Range rng(const void* ptr, size_t bytes) {
+    return Range{(uintptr_t)ptr, (uintptr_t)ptr + bytes};
+}
+inline bool overlap(Range a, Range b) {
+    return a.lo != 0 && b.lo != 0 && a.hi > a.lo && b.hi > b.lo && a.lo < b.hi && b.lo < a.hi;
+}
+inline bool aligned16(const void* p) { return p == nullptr || ((uintptr_t)p & 15u) == 0; }
+inline ssd_status from_cuda(cudaError_t e) { return e == cudaSuccess ? SSD_OK : SSD_ERR_CUDA; }
+// Checks made after the arguments are validated and before anything is
+// enqueued: the device's compute capability, then whether a bounded wait in
+// an earlier launch on this device has given up (reported once, as
+// SSD_ERR_TIMEOUT; reporting it synchronises the device and clears the record).
+ssd_status pre_launch();
+
 // Element loads/stores shared by the kernels.
 __device__ __forceinline__ float to_f32(float v) { return v; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
