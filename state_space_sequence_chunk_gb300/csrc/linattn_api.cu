@@ -80,12 +80,17 @@ size_t span(int64_t T, int64_t stride, int64_t w, int es) {
 }
 
 cudaError_t run_jobs(LaParams& p, int dtype, cudaStream_t st) {
+    const int sms = sm_count();
+    auto pass = [&](int mode) {
+        return dtype == SSD_BF16 ? launch_linattn_tc(p, mode, sms, st)
+                                 : launch_linattn_simt(p, dtype, mode, st);
+    };
     cudaError_t e = cudaSuccess;
     if (p.g.split) {
-        e = launch_linattn_simt(p, dtype, 1, st);
+        e = pass(1);
         if (e == cudaSuccess) e = launch_linattn_scan(p, st);
     }
-    return e != cudaSuccess ? e : launch_linattn_simt(p, dtype, 0, st);
+    return e != cudaSuccess ? e : pass(0);
 }
 
 }  // namespace

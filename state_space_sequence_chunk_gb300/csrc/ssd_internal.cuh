@@ -126,6 +126,7 @@ unsigned int take_fwd_pass_state_error();
 // Test hook: nonzero makes fwd_pass_state withhold its range hand-offs.
 cudaError_t set_fwd_pass_state_withhold(unsigned int on);
 unsigned int take_compute_out_error();
+unsigned int take_linattn_error();
 
 // Launch kern on stream, with programmatic dependent launch when pdl is set
 // (the kernel then waits on the previous grid with griddepcontrol.wait before
