@@ -2,38 +2,41 @@
 // tensor cores (bf16 operands, fp32 accumulation and state).
 //
 // One chain is (range of a sequence, head, 64 columns of c), walked in chunks of
-// 128 tokens.  With i, j the rows of a chunk of n tokens (forwards; backwards
-// the exponents are mirrored) and X the state before it:
+// 128 tokens.  With i, j the rows of a chunk (counted from its end when the walk
+// is backwards), n its tokens and X the state before it:
 //     W   = A B^T                                   128 x 128 x DK
-//     P   = s_in W o lam^{i-j} [i >= j]             (bf16, tensor memory)
-//     O1  = A X                                     128 x 64 x DK
-//     O2  = P C                                     128 x 64 x 128
-//     out = s_out (lam^{i+1} o O1 + O2)
-//     U   = B^T (s_in lam^{n-1-j} o C)              DK x 64 x 128
-//     X   <- lam^n X + U
+//     P   = s_in W o lam^{-j} [i >= j]              (bf16, tensor memory)
+//     out = s_out lam^i o (A (lam X) + P C)         128 x 64 x DK, 128 x 64 x 128
+//     U   = B^T (s_in lam^{-j} o C)                 DK x 64 x 128
+//     X   <- lam^n X + lam^{n-1} U
+// (backwards the decay of X and U is one step longer).  Rows and columns carry
+// the decay as separate factors, so that out is one accumulator and P costs one
+// product for each element; that is safe while lam^-127 <= 2^40.  For heads that
+// forget faster the exact form runs: lam^{i-j} element by element, A X and P C
+// in two accumulators, U with weights lam^{n-1-j}.
 // Every operand is read once per chain from HBM (a and b once per 64 columns of
 // c, from L2 the second time) and no state leaves the chip between chunks.
 //
 // Precision.  P and the X that multiplies A are rounded to bf16 (as operands of
 // a product whose result is rounded to bf16).  X itself must not be: it is kept
-// in fp32 registers and U is exact to fp32: C's rows scaled by the decay are
-// split into three bf16 terms (8 bits each) whose products are accumulated from
-// the smallest up, so that the accumulator's roundings are those of the 8 steps
-// of the leading term.  X <- lam^n X + U runs on the CUDA cores, where it is
-// rounded to nearest (the accumulator's rounding is not documented, and a chain
-// adds it up over hundreds of chunks).
+// in fp32 registers and U is exact to fp32: C's scaled rows are cut into three
+// bf16 terms of 8 bits each, multiplied side by side (N = 192) into separate
+// accumulators and added from the smallest up.  X <- lam^n X + U runs on the
+// CUDA cores, where it is rounded to nearest (how the tensor core's accumulator
+// rounds is not documented, and a chain adds it up over hundreds of chunks).
 //
-// Persistent CTAs of 18 warps, one per SM:
+// Persistent CTAs of 22 warps, one per SM:
 //   0-3   P: tensor memory -> decay, mask -> tensor memory (bf16, in place)
 //   4-7   C's scaled terms (a thread owns token row j); zeroes the rows of a
 //         ragged chunk that belong to other tokens, whatever they hold
-//   8-11  X in registers (a thread owns a row of X, 64 columns): bf16 copy for
-//         A X, update with U, stored states
-//   12-15 out (a thread owns a token row)
-//   16    TMA, two stages of A, B and C tiles (80 KB each)
-//   17    MMA issue: U(c), A X(c), P C(c), and W one chunk ahead
-// so that per chunk the tensor pipe (about 1800 cycles for DK = 128) runs while
-// each warpgroup works on another chunk or product.
+//   8-15  X in registers (a thread owns 32 columns of a row): bf16 copy for A X,
+//         update with U, stored states
+//   16-19 out (a thread owns a token row)
+//   20    TMA, two stages of A, B and C tiles (80 KB each)
+//   21    MMA issue: U(c), A X(c), W(c + 1), P C(c)
+// The roles' loops are kept short (packed fp32 arithmetic, little unrolling): six
+// codes run side by side on each scheduler, and fully unrolled they spent most of
+// their time on instruction fetches.
 #include <cuda.h>
 #include <string.h>
 
@@ -49,14 +52,16 @@ __device__ unsigned int g_la_error;  // bit 0: a bounded wait gave up
 constexpr int kC = 128;                       // tokens per chunk
 constexpr int kRow = 128;                     // bytes of a tile row (64 columns)
 constexpr int kAtom = kC * kRow;              // 16 KB: 128 rows of 64 columns
-constexpr int kThreads = 576;
-constexpr int kTmaWarp = 16, kMmaWarp = 17;
+constexpr int kThreads = 704;
+constexpr int kTmaWarp = 20, kMmaWarp = 21;
 constexpr int kStage = 5 * kAtom;             // A (2 atoms), B (2), C (1)
 constexpr int kTerms = 3;
 constexpr int kSmem = 2 * kStage + kTerms * kAtom + kAtom + 1024 + 1024;
 // tensor memory columns
 constexpr uint32_t kW = 0;                    // W / P, two buffers of 128
-constexpr uint32_t kO1 = 256, kO2 = 320, kU = 384;   // U: two buffers of 64
+constexpr uint32_t kO = 256, kU = 320;        // out; U's three terms
+// A head's decay over a chunk's 127 steps is at most 2^kSpan for the factored form.
+constexpr float kSpan = 40.f;
 
 struct TcParams {
     LaParams p;
@@ -73,6 +78,40 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 }
 __device__ __forceinline__ float lo16(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float hi16(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
+// Pairs of floats in one register pair: the packed fp32 instructions do two
+// elements each, rounded as the single ones.
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pair(float a, float b) {
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 pair(uint32_t a, uint32_t b) {
+    return pair(__uint_as_float(a), __uint_as_float(b));
+}
+__device__ __forceinline__ void unpair(f32x2 v, float& a, float& b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack2(f32x2 v) {
+    float a, b;
+    unpair(v, a, b);
+    return pack2(a, b);
+}
 __device__ __forceinline__ void bar_wg(int id) {
     asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory");
 }
@@ -80,6 +119,15 @@ __device__ __forceinline__ void st_v8(void* p, const uint32_t (&w)[8]) {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
                  "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                  : "memory");
+}
+
+__device__ __forceinline__ bool factored(float a2) { return a2 * -127.f <= kSpan; }
+// 2^(a2 n), with the product's rounding put back: n a2 can be as large as kSpan,
+// where a rounding of the exponent would be one of the result's last bits.
+__device__ __forceinline__ float la_exp2(float a2, int n) {
+    const float p = a2 * (float)n, e = fmaf(a2, (float)n, -p);
+    const float r = exp2f(p);
+    return fmaf(r, e * 0.6931471805599453f, r);
 }
 
 // One item of a CTA's list: the columns of one job, of one head, of one range.
@@ -120,16 +168,15 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
     uint64_t* b_empty = bars + 2;     // [2] stage read by every product (commit)
     uint64_t* b_wdone = bars + 4;     // [2] W computed (commit)
     uint64_t* b_pready = bars + 6;    // [2] P written (128)
-    uint64_t* b_udone = bars + 8;     // [2] U computed, terms read (commit)
-    uint64_t* b_ufree = bars + 10;    // [2] U read (128)
-    uint64_t* b_vready = bars + 12;   // terms written (128)
-    uint64_t* b_sready = bars + 13;   // bf16 X written (128)
-    uint64_t* b_xdone = bars + 14;    // A X computed: the bf16 X may change (commit)
-    uint64_t* b_odone = bars + 15;    // O1 and O2 computed (commit)
-    uint64_t* b_ofree = bars + 16;    // O1 and O2 read (128)
-    uint32_t* holder = reinterpret_cast<uint32_t*>(bars + 17);
-    float* lamp = reinterpret_cast<float*>(bars + 18);   // lam^0 .. lam^31
-    float* lampr = lamp + 32;                            // lam^31 .. lam^0
+    uint64_t* b_udone = bars + 8;     // U computed, terms read (commit)
+    uint64_t* b_ufree = bars + 9;     // U read (256)
+    uint64_t* b_vready = bars + 10;   // terms written (128)
+    uint64_t* b_sready = bars + 11;   // bf16 X written (256)
+    uint64_t* b_xdone = bars + 12;    // A X computed: the bf16 X may change (commit)
+    uint64_t* b_odone = bars + 13;    // out computed (commit)
+    uint64_t* b_ofree = bars + 14;    // out read (128)
+    uint32_t* holder = reinterpret_cast<uint32_t*>(bars + 15);
+    float* ptab = reinterpret_cast<float*>(bars + 16);   // [128] column factors of P
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
@@ -138,11 +185,11 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
             mbar_init(smem_u32(b_empty + s), 1);
             mbar_init(smem_u32(b_wdone + s), 1);
             mbar_init(smem_u32(b_pready + s), 128);
-            mbar_init(smem_u32(b_udone + s), 1);
-            mbar_init(smem_u32(b_ufree + s), 128);
         }
+        mbar_init(smem_u32(b_udone), 1);
+        mbar_init(smem_u32(b_ufree), 256);
         mbar_init(smem_u32(b_vready), 128);
-        mbar_init(smem_u32(b_sready), 128);
+        mbar_init(smem_u32(b_sready), 256);
         mbar_init(smem_u32(b_xdone), 1);
         mbar_init(smem_u32(b_odone), 1);
         mbar_init(smem_u32(b_ofree), 128);
@@ -184,11 +231,12 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
     } else if (warp == kMmaWarp) {
         constexpr uint32_t kIdW = make_idesc(1, 128, 128, 0, 0);
         constexpr uint32_t kIdO = make_idesc(1, 128, 64, 0, 1);
-        constexpr uint32_t kIdU = make_idesc(1, 128, 64, 1, 1);
+        constexpr uint32_t kIdU = make_idesc(1, 128, 64 * kTerms, 1, 1);
         for (int it = blockIdx.x; it < tp.items; it += gridDim.x) {
             const Item im = item_of<kAgg>(tp, it);
             if (lane == 0) {
                 const int ks = tp.p.job[im.job].DK / 16;
+                const bool fac = factored(la_log2_decay(g.a, im.h));
                 auto w_product = [&](int cc) {   // W of chunk cc
                     const int s = cc & 1;
                     mbar_wait(smem_u32(b_full + s), (cc >> 1) & 1, err, 1u);
@@ -208,33 +256,26 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                 for (int x = 0; x < im.nch; ++x, ++c) {
                     const int s = c & 1, use = c >> 1;
                     const uint32_t st = smem_u32(smem + s * kStage);
-                    // W one chunk ahead: its buffer's previous P has been read by an
-                    // earlier product of this thread
-                    if (!kAgg && x + 1 < im.nch) w_product(c + 1);
                     if (kAgg) mbar_wait(smem_u32(b_full + s), use & 1, err, 1u);
-                    // U = B^T (scaled C), smallest term first
+                    // U = B^T (scaled C), its three terms side by side: B is read once
                     mbar_wait(smem_u32(b_vready), c & 1, err, 1u);
-                    mbar_wait(smem_u32(b_ufree + s), (use & 1) ^ 1, err, 1u);
+                    mbar_wait(smem_u32(b_ufree), (c & 1) ^ 1, err, 1u);
                     tc_fence_after();
                     {
                         const uint64_t ad = smem_desc_sw128(st + 2 * kAtom, kAtom, 8 * kRow);
+                        const uint64_t bd = smem_desc_sw128(smem_u32(terms), kAtom, 8 * kRow);
 #pragma unroll
-                        for (int q = kTerms - 1; q >= 0; --q) {
-                            const uint64_t bd = smem_desc_sw128(smem_u32(terms) + q * kAtom, 8 * kRow, 8 * kRow);
-#pragma unroll
-                            for (int kk = 0; kk < 8; ++kk) {
-                                const uint64_t o = (uint64_t)((kk * 16 * kRow) >> 4);
-                                mma_f16_ss(tmem + kU + s * 64, ad + o, bd + o, kIdU,
-                                           (q < kTerms - 1 || kk > 0) ? 1u : 0u);
-                            }
+                        for (int kk = 0; kk < 8; ++kk) {
+                            const uint64_t o = (uint64_t)((kk * 16 * kRow) >> 4);
+                            mma_f16_ss(tmem + kU, ad + o, bd + o, kIdU, kk > 0 ? 1u : 0u);
                         }
                     }
-                    mma_commit(smem_u32(b_udone + s));
+                    mma_commit(smem_u32(b_udone));
                     if (kAgg) {
                         mma_commit(smem_u32(b_empty + s));
                         continue;
                     }
-                    // O1 = A X
+                    // out = A X
                     mbar_wait(smem_u32(b_sready), c & 1, err, 1u);
                     mbar_wait(smem_u32(b_ofree), (c & 1) ^ 1, err, 1u);
                     tc_fence_after();
@@ -244,22 +285,30 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
 #pragma unroll
                         for (int kk = 0; kk < 8; ++kk)
                             if (kk < ks)
-                                mma_f16_ss(tmem + kO1, ad + (uint64_t)(((kk / 4) * kAtom + (kk % 4) * 32) >> 4),
+                                mma_f16_ss(tmem + kO, ad + (uint64_t)(((kk / 4) * kAtom + (kk % 4) * 32) >> 4),
                                            bd + (uint64_t)((kk * 16 * kRow) >> 4), kIdO, kk > 0 ? 1u : 0u);
                     }
                     mma_commit(smem_u32(b_xdone));
-                    // O2 = P C
+                    // W of the next chunk before this chunk's last product, if its
+                    // tiles are there: P is then built a whole chunk ahead.  Its
+                    // buffer's last readers were waited for by the products above.
+                    const bool next = x + 1 < im.nch;
+                    const bool early = next && mbar_try_wait(smem_u32(b_full + (s ^ 1)), ((c + 1) >> 1) & 1);
+                    if (early) w_product(c + 1);
+                    // out += P C; in the exact form, beside P's columns in W's buffer
                     mbar_wait(smem_u32(b_pready + s), use & 1, err, 1u);
                     tc_fence_after();
                     {
                         const uint64_t bd = smem_desc_sw128(st + 4 * kAtom, 8 * kRow, 8 * kRow);
+                        const uint32_t to = fac ? tmem + kO : tmem + kW + s * 128 + 64;
 #pragma unroll
                         for (int kk = 0; kk < 8; ++kk)
-                            mma_f16_ts(tmem + kO2, tmem + kW + s * 128 + kk * 8,
-                                       bd + (uint64_t)((kk * 16 * kRow) >> 4), kIdO, kk > 0 ? 1u : 0u);
+                            mma_f16_ts(to, tmem + kW + s * 128 + kk * 8,
+                                       bd + (uint64_t)((kk * 16 * kRow) >> 4), kIdO, (fac || kk > 0) ? 1u : 0u);
                     }
                     mma_commit(smem_u32(b_odone));
                     mma_commit(smem_u32(b_empty + s));
+                    if (next && !early) w_product(c + 1);
                 }
             }
             __syncwarp();
@@ -274,13 +323,14 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                 if (im.nch == 0) continue;
                 const LaJob& jb = tp.p.job[im.job];
                 const float a2 = la_log2_decay(g.a, im.h);
-                bar_wg(1);                      // the tables' last readers are done
-                if (warp == 0) {
-                    lamp[lane] = exp2f(a2 * (float)lane);
-                    lampr[31 - lane] = exp2f(a2 * (float)lane);
-                }
+                const bool fac = factored(a2);
+                bar_wg(1);                      // the table's last readers are done
+                // factored: lam^{-j'} s_in; exact: lam^j (the first 32 are used) and,
+                // from 32 on, lam^{31-j}
+                ptab[row] = fac ? la_exp2(-a2, jb.rev ? kC - 1 - row : row) * jb.s_in
+                                : exp2f(a2 * (float)(row < 32 ? row : max(63 - row, 0)));
                 bar_wg(1);
-                const float4* vt = reinterpret_cast<const float4*>(jb.rev ? lamp : lampr);
+                const float4* vt = reinterpret_cast<const float4*>(jb.rev ? ptab : ptab + 32);
                 for (int x = 0; x < im.nch; ++x, ++c) {
                     const int s = c & 1, ci = jb.rev ? im.nch - 1 - x : x;
                     const int n = min(kC, im.rg.len - ci * kC);
@@ -289,6 +339,7 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                     const uint32_t base = tmem + lane_off + kW + s * 128;
                     // in place: block b's 16 packed columns lie within columns that
                     // blocks up to b held
+#pragma unroll 1
                     for (int b = 0; b < 4; ++b) {
                         const int rel = jb.rev ? b - warp : warp - b;
                         uint32_t o[16];
@@ -300,13 +351,31 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                             __syncwarp();
                             tmem_ld_x32(base + b * 32, v);
                             tmem_wait_ld();
-                            if (rel == 0) {
-                                // the block on the diagonal: a select, never a product,
-                                // drops what is above it
+                            if (fac) {
+                                const ulonglong2* ct = reinterpret_cast<const ulonglong2*>(ptab + b * 32);
+#pragma unroll
+                                for (int e4 = 0; e4 < 8; ++e4) {
+                                    const ulonglong2 t = ct[e4];
+                                    float x0, x1, x2, x3;
+                                    unpair(mul2(pair(v[4 * e4], v[4 * e4 + 1]), t.x), x0, x1);
+                                    unpair(mul2(pair(v[4 * e4 + 2], v[4 * e4 + 3]), t.y), x2, x3);
+                                    v[4 * e4] = __float_as_uint(x0);
+                                    v[4 * e4 + 1] = __float_as_uint(x1);
+                                    v[4 * e4 + 2] = __float_as_uint(x2);
+                                    v[4 * e4 + 3] = __float_as_uint(x3);
+                                }
+                                // on the diagonal a select, never a product, drops what
+                                // is above it
+                                if (rel == 0) {
+#pragma unroll
+                                    for (int e = 0; e < 32; ++e)
+                                        if (jb.rev ? e < lane : e > lane) v[e] = 0u;
+                                }
+                            } else if (rel == 0) {
 #pragma unroll
                                 for (int e = 0; e < 32; ++e) {
                                     const int d = jb.rev ? e - lane : lane - e;
-                                    const float w = lamp[d & 31] * jb.s_in;
+                                    const float w = ptab[d & 31] * jb.s_in;
                                     v[e] = d >= 0 ? __float_as_uint(__uint_as_float(v[e]) * w) : 0u;
                                 }
                             } else {
@@ -346,32 +415,40 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
             const Item im = item_of<kAgg>(tp, it);
             const LaJob& jb = tp.p.job[im.job];
             const float a2 = la_log2_decay(g.a, im.h);
+            const bool fac = factored(a2);
+            const float wf = la_exp2(-a2, jb.rev ? kC - 1 - row : row) * jb.s_in;
             for (int x = 0; x < im.nch; ++x, ++c) {
                 const int s = c & 1, ci = jb.rev ? im.nch - 1 - x : x;
                 const int n = min(kC, im.rg.len - ci * kC);
-                const float w = exp2f(a2 * (float)(jb.rev ? row + 1 : n - 1 - row)) * jb.s_in;
+                const float w = fac ? wf : exp2f(a2 * (float)(jb.rev ? row + 1 : n - 1 - row)) * jb.s_in;
+                const f32x2 w2 = pair(w, w);
                 mbar_wait(smem_u32(b_full + s), (c >> 1) & 1, err, 1u);
-                if (c > 0) mbar_wait(smem_u32(b_udone + ((c - 1) & 1)), ((c - 1) >> 1) & 1, err, 1u);
+                if (c > 0) mbar_wait(smem_u32(b_udone), (c - 1) & 1, err, 1u);
                 uint8_t* st = smem + s * kStage;
                 if (row < n) {
-#pragma unroll
+#pragma unroll 2
                     for (int ch = 0; ch < 8; ++ch) {
                         const int at = row * kRow + ((ch ^ (row & 7)) << 4);
                         const uint4 q = *reinterpret_cast<const uint4*>(st + 4 * kAtom + at);
                         const uint32_t in[4] = {q.x, q.y, q.z, q.w};
-                        uint32_t t0[4], t1[4], t2[4];
+                        uint32_t t[kTerms][4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            float a = lo16(in[e]) * w, b = hi16(in[e]) * w;
-                            t0[e] = pack2(a, b);
-                            a -= lo16(t0[e]);
-                            b -= hi16(t0[e]);
-                            t1[e] = pack2(a, b);
-                            t2[e] = pack2(a - lo16(t1[e]), b - hi16(t1[e]));
+                            // 24 bits as three times 8, cut off rather than rounded:
+                            // the three add up to the product exactly
+                            f32x2 r = mul2(pair(lo16(in[e]), hi16(in[e])), w2);
+#pragma unroll
+                            for (int y = 0; y < kTerms; ++y) {
+                                float a, b;
+                                unpair(r, a, b);
+                                t[y][e] = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+                                if (y + 1 < kTerms)
+                                    r = add2(r, pair(-hi16(__float_as_uint(a)), -hi16(__float_as_uint(b))));
+                            }
                         }
-                        *reinterpret_cast<uint4*>(terms + at) = make_uint4(t0[0], t0[1], t0[2], t0[3]);
-                        *reinterpret_cast<uint4*>(terms + kAtom + at) = make_uint4(t1[0], t1[1], t1[2], t1[3]);
-                        *reinterpret_cast<uint4*>(terms + 2 * kAtom + at) = make_uint4(t2[0], t2[1], t2[2], t2[3]);
+#pragma unroll
+                        for (int y = 0; y < kTerms; ++y)
+                            *reinterpret_cast<uint4*>(terms + y * kAtom + at) = make_uint4(t[y][0], t[y][1], t[y][2], t[y][3]);
                     }
                 } else {
                     // a row of other tokens: nothing of it may reach a product
@@ -391,72 +468,95 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                 mbar_arrive(smem_u32(b_vready));
             }
         }
-    } else if (warp < 12) {
+    } else if (warp < 16) {
         // ===================== X =====================
-        const int k = (warp - 8) * 32 + lane;           // X's row = tensor-memory lane
-        const uint32_t lane_off = (uint32_t)((warp - 8) * 32) << 16;
+        const int k = (warp & 3) * 32 + lane;           // X's row = tensor-memory lane
+        const int vc = warp < 12 ? 0 : 32;              // X's columns: 32 a thread
+        const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
         for (int it = blockIdx.x; it < tp.items; it += gridDim.x) {
             const Item im = item_of<kAgg>(tp, it);
             if (im.skip || im.rg.seq == g.nseq) continue;
             const LaJob& jb = tp.p.job[im.job];
-            const int nv = min(kLaCols, jb.DV - im.v0);
+            const int nv = min(kLaCols, jb.DV - im.v0) - vc;
             const int64_t elems = (int64_t)jb.DK * jb.DV;
-            const int64_t at = (int64_t)k * jb.sk + (int64_t)im.v0 * jb.sv;
+            const int64_t at = (int64_t)k * jb.sk + (int64_t)(im.v0 + vc) * jb.sv;
             const int64_t so = ((int64_t)im.rg.seq * g.H + im.h) * elems + at;
             // the range's number is the item's: item = ((range H + h) jobs + job) nvb + vb
             const int ridx = it / tp.nvb / tp.p.njobs / g.H;
             float* ag = im.cut ? jb.agg + ((int64_t)ridx * g.H + im.h) * elems + at : nullptr;
             const float* in = kAgg ? nullptr : (im.cut ? ag : (jb.init ? jb.init + so : nullptr));
-            float X[64];
+            f32x2 X[16];
+            {
+                float x0[32];
 #pragma unroll
-            for (int v = 0; v < 64; ++v)
-                X[v] = in != nullptr && k < jb.DK && v < nv ? in[(int64_t)v * jb.sv] : 0.f;
+                for (int v = 0; v < 32; ++v)
+                    x0[v] = in != nullptr && k < jb.DK && v < nv ? in[(int64_t)v * jb.sv] : 0.f;
+#pragma unroll
+                for (int v = 0; v < 16; ++v) X[v] = pair(x0[2 * v], x0[2 * v + 1]);
+            }
+            const float a2 = la_log2_decay(g.a, im.h);
+            const bool fac = factored(a2);
             float f_hi, f_lo;
             la_decay_pow(g.a, im.h, kC, f_hi, f_lo);
             for (int x = 0; x < im.nch; ++x, ++c) {
                 const int s = c & 1, ci = jb.rev ? im.nch - 1 - x : x;
                 const int n = min(kC, im.rg.len - ci * kC);
                 if (!kAgg) {
+                    // in the factored form the row factor of out is lam^{i'}
+                    const float m = fac ? la_exp2(a2, jb.rev ? n - kC : 1) : 1.f;
+                    const f32x2 m2 = pair(m, m);
                     if (c > 0) mbar_wait(smem_u32(b_xdone), (c - 1) & 1, err, 1u);
 #pragma unroll
-                    for (int ch = 0; ch < 8; ++ch)
-                        *reinterpret_cast<uint4*>(xs + k * kRow + ((ch ^ (k & 7)) << 4)) =
-                            make_uint4(pack2(X[8 * ch], X[8 * ch + 1]), pack2(X[8 * ch + 2], X[8 * ch + 3]),
-                                       pack2(X[8 * ch + 4], X[8 * ch + 5]), pack2(X[8 * ch + 6], X[8 * ch + 7]));
+                    for (int ch = 0; ch < 4; ++ch)
+                        *reinterpret_cast<uint4*>(xs + k * kRow + (((vc / 8 + ch) ^ (k & 7)) << 4)) =
+                            make_uint4(pack2(mul2(X[4 * ch], m2)), pack2(mul2(X[4 * ch + 1], m2)),
+                                       pack2(mul2(X[4 * ch + 2], m2)), pack2(mul2(X[4 * ch + 3], m2)));
                     fence_proxy_async_smem();
                     mbar_arrive(smem_u32(b_sready));
                 }
                 float hi = f_hi, lo = f_lo;
                 if (n < kC) la_decay_pow(g.a, im.h, n, hi, lo);
-                mbar_wait(smem_u32(b_udone + s), (c >> 1) & 1, err, 1u);
+                const float cu = fac ? la_exp2(a2, jb.rev ? kC : n - 1) : 1.f;
+                mbar_wait(smem_u32(b_udone), c & 1, err, 1u);
                 tc_fence_after();
+                const f32x2 hi2 = pair(hi, hi), lo2 = pair(lo, lo), cu2 = pair(cu, cu);
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    uint32_t u[32];
+                for (int q = 0; q < 2; ++q) {
+                    uint32_t u[kTerms][16];
                     __syncwarp();
-                    tmem_ld_x32(tmem + lane_off + kU + s * 64 + half * 32, u);
+#pragma unroll
+                    for (int y = 0; y < kTerms; ++y)
+                        tmem_ld_x16(tmem + lane_off + kU + y * 64 + vc + q * 16, u[y]);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        float& X1 = X[half * 32 + e];
-                        X1 = fmaf(X1, hi, fmaf(X1, lo, __uint_as_float(u[e])));
+                    for (int e = 0; e < 8; ++e) {
+                        const f32x2 u2 = add2(pair(u[0][2 * e], u[0][2 * e + 1]),
+                                              add2(pair(u[1][2 * e], u[1][2 * e + 1]), pair(u[2][2 * e], u[2][2 * e + 1])));
+                        f32x2& X2 = X[q * 8 + e];
+                        X2 = fma2(X2, hi2, fma2(X2, lo2, mul2(cu2, u2)));
                     }
                 }
                 tc_fence_before();
-                mbar_arrive(smem_u32(b_ufree + s));
+                mbar_arrive(smem_u32(b_ufree));
             }
             float* outst = kAgg ? ag : (im.last && jb.fin ? jb.fin + so : nullptr);
             if (outst != nullptr && k < jb.DK) {
 #pragma unroll
-                for (int v = 0; v < 64; ++v)
-                    if (v < nv) outst[(int64_t)v * jb.sv] = X[v];
+                for (int v = 0; v < 16; ++v) {
+                    float x0, x1;
+                    unpair(X[v], x0, x1);
+                    if (2 * v < nv) {   // nv is a multiple of 16
+                        outst[(int64_t)(2 * v) * jb.sv] = x0;
+                        outst[(int64_t)(2 * v + 1) * jb.sv] = x1;
+                    }
+                }
             }
             __syncwarp();
         }
     } else if (!kAgg) {
         // ===================== out =====================
-        const int i = (warp - 12) * 32 + lane;
-        const uint32_t lane_off = (uint32_t)((warp - 12) * 32) << 16;
+        const int i = (warp - 16) * 32 + lane;
+        const uint32_t lane_off = (uint32_t)((warp - 16) * 32) << 16;
         for (int it = blockIdx.x; it < tp.items; it += gridDim.x) {
             const Item im = item_of<kAgg>(tp, it);
             const LaJob& jb = tp.p.job[im.job];
@@ -471,50 +571,54 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                 }
             }
             const float a2 = la_log2_decay(g.a, im.h);
+            const bool fac = factored(a2);
             for (int x = 0; x < im.nch; ++x, ++c) {
                 const int ci = jb.rev ? im.nch - 1 - x : x;
                 const int n = min(kC, im.rg.len - ci * kC);
-                const float f = exp2f(a2 * (float)(jb.rev ? n - 1 - i : i + 1)) * jb.s_out;
+                const float f = jb.s_out * (fac ? la_exp2(a2, jb.rev ? kC - 1 - i : i)
+                                                : exp2f(a2 * (float)(jb.rev ? n - 1 - i : i + 1)));
                 const int64_t e0 = (int64_t)(im.rg.t0 + ci * kC + i) * os + oh;
                 mbar_wait(smem_u32(b_odone), c & 1, err, 1u);
                 tc_fence_after();
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    uint32_t p[32], q[32];
+                const f32x2 f2 = pair(f, f), s2 = pair(jb.s_out, jb.s_out);
+#pragma unroll 1
+                for (int b = 0; b < 4; ++b) {   // 16 columns at a time
+                    uint32_t p[16];
+                    f32x2 r[8];
                     __syncwarp();
-                    tmem_ld_x32(tmem + lane_off + kO1 + half * 32, p);
-                    tmem_ld_x32(tmem + lane_off + kO2 + half * 32, q);
-                    tmem_wait_ld();
-                    if (half == 1) {
+                    tmem_ld_x16(tmem + lane_off + kO + b * 16, p);
+                    if (fac) {
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) r[e] = mul2(f2, pair(p[2 * e], p[2 * e + 1]));
+                    } else {
+                        uint32_t q[16];
+                        tmem_ld_x16(tmem + lane_off + kW + (c & 1) * 128 + 64 + b * 16, q);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            r[e] = fma2(f2, pair(p[2 * e], p[2 * e + 1]), mul2(s2, pair(q[2 * e], q[2 * e + 1])));
+                    }
+                    if (b == 3) {
                         tc_fence_before();
                         mbar_arrive(smem_u32(b_ofree));
                     }
-                    if (i < n) {
+                    if (i < n && b * 16 < nv) {
+                        const int64_t e = e0 + b * 16;
+                        if (jb.out_f32) {
+                            ulonglong2* d = reinterpret_cast<ulonglong2*>(static_cast<float*>(jb.out) + e);
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            p[e] = __float_as_uint(fmaf(f, __uint_as_float(p[e]), jb.s_out * __uint_as_float(q[e])));
+                            for (int y = 0; y < 4; ++y) d[y] = make_ulonglong2(r[2 * y], r[2 * y + 1]);
+                        } else {
+                            uint32_t w[8];
 #pragma unroll
-                        for (int b = 0; b < 2; ++b) {
-                            if (half * 32 + b * 16 >= nv) continue;
-                            const int64_t e = e0 + half * 32 + b * 16;
-                            if (jb.out_f32) {
-                                uint4* d = reinterpret_cast<uint4*>(static_cast<float*>(jb.out) + e);
-#pragma unroll
-                                for (int y = 0; y < 4; ++y)
-                                    d[y] = make_uint4(p[b * 16 + 4 * y], p[b * 16 + 4 * y + 1],
-                                                      p[b * 16 + 4 * y + 2], p[b * 16 + 4 * y + 3]);
+                            for (int y = 0; y < 8; ++y) w[y] = pack2(r[y]);
+                            __nv_bfloat16* d = static_cast<__nv_bfloat16*>(jb.out) + e;
+                            if ((reinterpret_cast<uintptr_t>(d) & 31) == 0) {
+                                st_v8(d, w);
                             } else {
-                                uint32_t w[8];
-#pragma unroll
-                                for (int y = 0; y < 8; ++y)
-                                    w[y] = pack2(__uint_as_float(p[b * 16 + 2 * y]), __uint_as_float(p[b * 16 + 2 * y + 1]));
-                                __nv_bfloat16* d = static_cast<__nv_bfloat16*>(jb.out) + e;
-                                if ((reinterpret_cast<uintptr_t>(d) & 31) == 0) {
-                                    st_v8(d, w);
-                                } else {
-                                    reinterpret_cast<uint4*>(d)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-                                    reinterpret_cast<uint4*>(d)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-                                }
+                                reinterpret_cast<uint4*>(d)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                                reinterpret_cast<uint4*>(d)[1] = make_uint4(w[4], w[5], w[6], w[7]);
                             }
                         }
                     }
