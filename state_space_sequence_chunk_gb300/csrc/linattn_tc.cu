@@ -25,15 +25,16 @@
 // CUDA cores, where it is rounded to nearest (how the tensor core's accumulator
 // rounds is not documented, and a chain adds it up over hundreds of chunks).
 //
-// Persistent CTAs of 22 warps, one per SM:
-//   0-3   P: tensor memory -> decay, mask -> tensor memory (bf16, in place)
-//   4-7   C's scaled terms (a thread owns token row j); zeroes the rows of a
+// Persistent CTAs of 26 warps, one per SM:
+//   0-7   P: tensor memory -> decay, mask -> tensor memory (bf16, in place; two
+//         warpgroups, half of the columns each)
+//   8-11  C's scaled terms (a thread owns token row j); zeroes the rows of a
 //         ragged chunk that belong to other tokens, whatever they hold
-//   8-15  X in registers (a thread owns 32 columns of a row): bf16 copy for A X,
+//   12-19 X in registers (a thread owns 32 columns of a row): bf16 copy for A X,
 //         update with U, stored states
-//   16-19 out (a thread owns a token row)
-//   20    TMA, two stages of A, B and C tiles (80 KB each)
-//   21    MMA issue: U(c), A X(c), W(c + 1), P C(c)
+//   20-23 out (a thread owns a token row)
+//   24    TMA, two stages of A, B and C tiles (80 KB each)
+//   25    MMA issue: U(c), A X(c), W(c + 1), P C(c)
 // The roles' loops are kept short (packed fp32 arithmetic, little unrolling): six
 // codes run side by side on each scheduler, and fully unrolled they spent most of
 // their time on instruction fetches.
@@ -52,8 +53,8 @@ __device__ unsigned int g_la_error;  // bit 0: a bounded wait gave up
 constexpr int kC = 128;                       // tokens per chunk
 constexpr int kRow = 128;                     // bytes of a tile row (64 columns)
 constexpr int kAtom = kC * kRow;              // 16 KB: 128 rows of 64 columns
-constexpr int kThreads = 704;
-constexpr int kTmaWarp = 20, kMmaWarp = 21;
+constexpr int kThreads = 832;
+constexpr int kTmaWarp = 24, kMmaWarp = 25;
 constexpr int kStage = 5 * kAtom;             // A (2 atoms), B (2), C (1)
 constexpr int kTerms = 3;
 constexpr int kSmem = 2 * kStage + kTerms * kAtom + kAtom + 1024 + 1024;
@@ -112,13 +113,39 @@ __device__ __forceinline__ uint32_t pack2(f32x2 v) {
     unpair(v, a, b);
     return pack2(a, b);
 }
-__device__ __forceinline__ void bar_wg(int id) {
-    asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory");
+// Shared memory by its 32-bit address: through generic pointers these accesses
+// take the path of global loads.
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+    return v;
 }
+__device__ __forceinline__ float lds32(uint32_t a) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+__device__ __forceinline__ void sts32(uint32_t a, float v) {
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
+}
+__device__ __forceinline__ void bar_p() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 __device__ __forceinline__ void st_v8(void* p, const uint32_t (&w)[8]) {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
                  "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                  : "memory");
+}
+
+// mbar_wait with its slow path out of line: the roles' loops share the
+// instruction cache.
+__device__ __noinline__ void wait_slow(uint32_t bar, uint32_t parity, unsigned int* err) {
+    mbar_wait(bar, parity, err, 1u);
+}
+__device__ __forceinline__ void wait_on(uint32_t bar, uint32_t parity, unsigned int* err) {
+    if (!mbar_try_wait(bar, parity)) wait_slow(bar, parity, err);
 }
 
 __device__ __forceinline__ bool factored(float a2) { return a2 * -127.f <= kSpan; }
@@ -137,7 +164,7 @@ struct Item {
     bool cut, last, skip;
 };
 template <bool kAgg>
-__device__ __forceinline__ Item item_of(const TcParams& tp, int it) {
+__device__ __noinline__ Item item_of(const TcParams& tp, int it) {
     Item r;
     __syncwarp();   // la_find is collective
     const int vb = it % tp.nvb;
@@ -155,6 +182,33 @@ __device__ __forceinline__ Item item_of(const TcParams& tp, int it) {
     return r;
 }
 
+// One lane of a converged warp.  The compiler knows such a branch to be uniform
+// and keeps what it computes in uniform registers: an MMA then takes 3
+// instructions to issue, in a branch of lane 0 it takes 8 and more (and some 200
+// cycles, which bound the kernel).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+    return p != 0u;
+}
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+// Up to 8 products of 16 along the contraction, overwriting d.  An operand is
+// K-major (two 64-wide tiles side by side) or MN-major (rows of the contraction).
+template <bool kAK, bool kBK>
+__device__ __forceinline__ void mma_steps(uint32_t d, uint64_t a, uint64_t b, int steps, uint32_t idesc) {
+    const auto one = [&](int kk) {
+        const uint32_t ok = (uint32_t)((kk / 4) * kAtom + (kk % 4) * 32) >> 4, om = (uint32_t)(kk * 16 * kRow) >> 4;
+        mma_f16_ss(d, a + (kAK ? ok : om), b + (kBK ? ok : om), idesc, kk > 0 ? 1u : 0u);
+    };
+    if (steps == 8) {
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) one(kk);
+    } else {
+#pragma unroll 1
+        for (int kk = 0; kk < steps; ++kk) one(kk);
+    }
+}
+
 template <bool kAgg>
 __global__ void __launch_bounds__(kThreads, 1)
 linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps maps) {
@@ -164,27 +218,31 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
     uint8_t* terms = smem + 2 * kStage;
     uint8_t* xs = terms + kTerms * kAtom;
     uint64_t* bars = reinterpret_cast<uint64_t*>(xs + kAtom);
-    uint64_t* b_full = bars;          // [2] stage loaded (tx)
-    uint64_t* b_empty = bars + 2;     // [2] stage read by every product (commit)
-    uint64_t* b_wdone = bars + 4;     // [2] W computed (commit)
-    uint64_t* b_pready = bars + 6;    // [2] P written (128)
-    uint64_t* b_udone = bars + 8;     // U computed, terms read (commit)
-    uint64_t* b_ufree = bars + 9;     // U read (256)
-    uint64_t* b_vready = bars + 10;   // terms written (128)
-    uint64_t* b_sready = bars + 11;   // bf16 X written (256)
-    uint64_t* b_xdone = bars + 12;    // A X computed: the bf16 X may change (commit)
-    uint64_t* b_odone = bars + 13;    // out computed (commit)
-    uint64_t* b_ofree = bars + 14;    // out read (128)
-    uint32_t* holder = reinterpret_cast<uint32_t*>(bars + 15);
-    float* ptab = reinterpret_cast<float*>(bars + 16);   // [128] column factors of P
+    uint64_t* b_fab = bars;           // [2] stage's A and B loaded (tx)
+    uint64_t* b_fc = bars + 2;        // [2] stage's C loaded (tx)
+    uint64_t* b_eab = bars + 4;       // [2] A and B read by every product (commit)
+    uint64_t* b_ec = bars + 6;        // [2] C read by every product (commit)
+    uint64_t* b_wdone = bars + 8;     // [2] W computed (commit)
+    uint64_t* b_pready = bars + 10;   // [2] P written (256)
+    uint64_t* b_udone = bars + 12;    // U computed, terms read (commit)
+    uint64_t* b_ufree = bars + 13;    // U read (256)
+    uint64_t* b_vready = bars + 14;   // terms written (128)
+    uint64_t* b_sready = bars + 15;   // bf16 X written (256)
+    uint64_t* b_xdone = bars + 16;    // A X computed: the bf16 X may change (commit)
+    uint64_t* b_odone = bars + 17;    // out computed (commit)
+    uint64_t* b_ofree = bars + 18;    // out read (128)
+    uint32_t* holder = reinterpret_cast<uint32_t*>(bars + 19);
+    const uint32_t ptab = smem_u32(bars + 20);   // [128] fp32: column factors of P
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int s = 0; s < 2; ++s) {
-            mbar_init(smem_u32(b_full + s), 1);
-            mbar_init(smem_u32(b_empty + s), 1);
+            mbar_init(smem_u32(b_fab + s), 1);
+            mbar_init(smem_u32(b_fc + s), 1);
+            mbar_init(smem_u32(b_eab + s), 1);
+            mbar_init(smem_u32(b_ec + s), 1);
             mbar_init(smem_u32(b_wdone + s), 1);
-            mbar_init(smem_u32(b_pready + s), 128);
+            mbar_init(smem_u32(b_pready + s), 256);
         }
         mbar_init(smem_u32(b_udone), 1);
         mbar_init(smem_u32(b_ufree), 256);
@@ -199,7 +257,7 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *holder;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *holder, 0);
     unsigned int* err = &g_la_error;
     const LaGeom& g = tp.p.g;
     // every role walks the same items and counts chunks in c: barrier phases
@@ -207,6 +265,7 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
     int c = 0;
 
     if (warp == kTmaWarp) {
+#pragma unroll 1
         for (int it = blockIdx.x; it < tp.items; it += gridDim.x) {
             const Item im = item_of<kAgg>(tp, it);
             const LaJob& jb = tp.p.job[im.job];
@@ -214,16 +273,20 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                 const int ka = (jb.DK + 63) / 64;
                 const CUtensorMap* m = maps.m[im.job];
                 const int ha = im.h / jb.dA, hb = im.h / jb.dB, hc = im.h / jb.dC;
+#pragma unroll 1
                 for (int x = 0; x < im.nch; ++x, ++c) {
                     const int s = c & 1, t = im.rg.t0 + (jb.rev ? im.nch - 1 - x : x) * kC;
-                    mbar_wait(smem_u32(b_empty + s), ((c >> 1) & 1) ^ 1, err, 1u);
-                    const uint32_t fb = smem_u32(b_full + s), st = smem_u32(smem + s * kStage);
-                    mbar_arrive_expect_tx(fb, ((kAgg ? 1 : 2) * ka + 1) * kAtom);
+                    const uint32_t free = ((c >> 1) & 1) ^ 1, st = smem_u32(smem + s * kStage);
+                    const uint32_t fab = smem_u32(b_fab + s), fc = smem_u32(b_fc + s);
+                    wait_on(smem_u32(b_eab + s), free, err);
+                    mbar_arrive_expect_tx(fab, (kAgg ? 1 : 2) * ka * kAtom);
                     for (int a = 0; a < ka; ++a) {
-                        if (!kAgg) tma_load_3d(st + a * kAtom, m + 0, fb, a * 64, ha, t);
-                        tma_load_3d(st + (2 + a) * kAtom, m + 1, fb, a * 64, hb, t);
+                        if (!kAgg) tma_load_3d(st + a * kAtom, m + 0, fab, a * 64, ha, t);
+                        tma_load_3d(st + (2 + a) * kAtom, m + 1, fab, a * 64, hb, t);
                     }
-                    tma_load_3d(st + 4 * kAtom, m + 2, fb, im.v0, hc, t);
+                    wait_on(smem_u32(b_ec + s), free, err);
+                    mbar_arrive_expect_tx(fc, kAtom);
+                    tma_load_3d(st + 4 * kAtom, m + 2, fc, im.v0, hc, t);
                 }
             }
             __syncwarp();
@@ -232,175 +295,164 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
         constexpr uint32_t kIdW = make_idesc(1, 128, 128, 0, 0);
         constexpr uint32_t kIdO = make_idesc(1, 128, 64, 0, 1);
         constexpr uint32_t kIdU = make_idesc(1, 128, 64 * kTerms, 1, 1);
+#pragma unroll 1
         for (int it = blockIdx.x; it < tp.items; it += gridDim.x) {
             const Item im = item_of<kAgg>(tp, it);
-            if (lane == 0) {
-                const int ks = tp.p.job[im.job].DK / 16;
-                const bool fac = factored(la_log2_decay(g.a, im.h));
-                auto w_product = [&](int cc) {   // W of chunk cc
-                    const int s = cc & 1;
-                    mbar_wait(smem_u32(b_full + s), (cc >> 1) & 1, err, 1u);
-                    tc_fence_after();
-                    const uint32_t st = smem_u32(smem + s * kStage);
-                    const uint64_t ad = smem_desc_sw128(st, 16, 8 * kRow);
-                    const uint64_t bd = smem_desc_sw128(st + 2 * kAtom, 16, 8 * kRow);
-#pragma unroll
-                    for (int kk = 0; kk < 8; ++kk)
-                        if (kk < ks) {
-                            const uint64_t o = (uint64_t)(((kk / 4) * kAtom + (kk % 4) * 32) >> 4);
-                            mma_f16_ss(tmem + kW + s * 128, ad + o, bd + o, kIdW, kk > 0 ? 1u : 0u);
-                        }
-                    mma_commit(smem_u32(b_wdone + s));
-                };
-                if (!kAgg && im.nch > 0) w_product(c);
-                for (int x = 0; x < im.nch; ++x, ++c) {
-                    const int s = c & 1, use = c >> 1;
-                    const uint32_t st = smem_u32(smem + s * kStage);
-                    if (kAgg) mbar_wait(smem_u32(b_full + s), use & 1, err, 1u);
-                    // U = B^T (scaled C), its three terms side by side: B is read once
-                    mbar_wait(smem_u32(b_vready), c & 1, err, 1u);
-                    mbar_wait(smem_u32(b_ufree), (c & 1) ^ 1, err, 1u);
-                    tc_fence_after();
-                    {
-                        const uint64_t ad = smem_desc_sw128(st + 2 * kAtom, kAtom, 8 * kRow);
-                        const uint64_t bd = smem_desc_sw128(smem_u32(terms), kAtom, 8 * kRow);
-#pragma unroll
-                        for (int kk = 0; kk < 8; ++kk) {
-                            const uint64_t o = (uint64_t)((kk * 16 * kRow) >> 4);
-                            mma_f16_ss(tmem + kU, ad + o, bd + o, kIdU, kk > 0 ? 1u : 0u);
+            const int nch = uniform(im.nch), ks = uniform(tp.p.job[im.job].DK / 16);
+            const int fac = uniform(factored(la_log2_decay(g.a, im.h)) ? 1 : 0);
+            if (elect_one()) {
+                // x = -1: the W of the item's first chunk
+#pragma unroll 1
+                for (int x = kAgg ? 0 : -1; x < nch; ++x) {
+                    const int cc = c + x, s = cc & 1, use = cc >> 1;
+                    const uint32_t st = smem_u32(smem) + s * kStage;
+                    const int s1 = s ^ 1, use1 = (cc + 1) >> 1;
+                    const uint32_t st1 = smem_u32(smem) + s1 * kStage;
+                    // W of the next chunk goes first, if its tiles are there (and the exact
+                    // form does not hold its buffer): P is then built a chunk ahead, and
+                    // the tensor pipe has work while the last out is read.
+                    bool w_due = !kAgg && x + 1 < nch;
+                    if (x >= 0) {
+                        if (kAgg) mbar_wait(smem_u32(b_fab + s), use & 1, err, 1u);
+                        // U = B^T (scaled C), its three terms side by side: B is read once
+                        mbar_wait(smem_u32(b_vready), cc & 1, err, 1u);
+                        mbar_wait(smem_u32(b_ufree), (cc & 1) ^ 1, err, 1u);
+                        tc_fence_after();
+                        mma_steps<false, false>(tmem + kU, smem_desc_sw128(st + 2 * kAtom, kAtom, 8 * kRow),
+                                                smem_desc_sw128(smem_u32(terms), kAtom, 8 * kRow), 8, kIdU);
+                        mma_commit(smem_u32(b_udone));
+                        if (kAgg) {
+                            mma_commit(smem_u32(b_eab + s));
+                            mma_commit(smem_u32(b_ec + s));
                         }
                     }
-                    mma_commit(smem_u32(b_udone));
-                    if (kAgg) {
-                        mma_commit(smem_u32(b_empty + s));
-                        continue;
-                    }
-                    // out = A X
-                    mbar_wait(smem_u32(b_sready), c & 1, err, 1u);
-                    mbar_wait(smem_u32(b_ofree), (c & 1) ^ 1, err, 1u);
-                    tc_fence_after();
-                    {
-                        const uint64_t ad = smem_desc_sw128(st, 16, 8 * kRow);
-                        const uint64_t bd = smem_desc_sw128(smem_u32(xs), 8 * kRow, 8 * kRow);
-#pragma unroll
-                        for (int kk = 0; kk < 8; ++kk)
-                            if (kk < ks)
-                                mma_f16_ss(tmem + kO, ad + (uint64_t)(((kk / 4) * kAtom + (kk % 4) * 32) >> 4),
-                                           bd + (uint64_t)((kk * 16 * kRow) >> 4), kIdO, kk > 0 ? 1u : 0u);
-                    }
-                    mma_commit(smem_u32(b_xdone));
-                    // W of the next chunk before this chunk's last product, if its
-                    // tiles are there: P is then built a whole chunk ahead.  Its
-                    // buffer's last readers were waited for by the products above.
-                    const bool next = x + 1 < im.nch;
-                    const bool early = next && mbar_try_wait(smem_u32(b_full + (s ^ 1)), ((c + 1) >> 1) & 1);
-                    if (early) w_product(c + 1);
-                    // out += P C; in the exact form, beside P's columns in W's buffer
-                    mbar_wait(smem_u32(b_pready + s), use & 1, err, 1u);
-                    tc_fence_after();
-                    {
+                    if (kAgg) continue;
+                    const auto w_product = [&]() {
+                        w_due = false;
+                        mbar_wait(smem_u32(b_fab + s1), use1 & 1, err, 1u);
+                        tc_fence_after();
+                        mma_steps<true, true>(tmem + kW + s1 * 128, smem_desc_sw128(st1, 16, 8 * kRow),
+                                              smem_desc_sw128(st1 + 2 * kAtom, 16, 8 * kRow), ks, kIdW);
+                        mma_commit(smem_u32(b_wdone + s1));
+                    };
+                    if (x >= 0) {
+                        if (w_due && fac && mbar_try_wait(smem_u32(b_fab + s1), use1 & 1)) w_product();
+                        // out = A X
+                        mbar_wait(smem_u32(b_sready), cc & 1, err, 1u);
+                        mbar_wait(smem_u32(b_ofree), (cc & 1) ^ 1, err, 1u);
+                        tc_fence_after();
+                        mma_steps<true, false>(tmem + kO, smem_desc_sw128(st, 16, 8 * kRow),
+                                               smem_desc_sw128(smem_u32(xs), 8 * kRow, 8 * kRow), ks, kIdO);
+                        mma_commit(smem_u32(b_xdone));
+                        mma_commit(smem_u32(b_eab + s));
+                        // out += P C; in the exact form, beside P's columns in W's buffer
+                        mbar_wait(smem_u32(b_fc + s), use & 1, err, 1u);
+                        mbar_wait(smem_u32(b_pready + s), use & 1, err, 1u);
+                        tc_fence_after();
                         const uint64_t bd = smem_desc_sw128(st + 4 * kAtom, 8 * kRow, 8 * kRow);
-                        const uint32_t to = fac ? tmem + kO : tmem + kW + s * 128 + 64;
+                        const uint32_t to = tmem + (fac ? kO : kW + s * 128 + 64);
+                        const uint32_t pa = tmem + kW + s * 128, pb = pa + (fac ? 32 : 0);
 #pragma unroll
                         for (int kk = 0; kk < 8; ++kk)
-                            mma_f16_ts(to, tmem + kW + s * 128 + kk * 8,
-                                       bd + (uint64_t)((kk * 16 * kRow) >> 4), kIdO, (fac || kk > 0) ? 1u : 0u);
+                            mma_f16_ts(to, (kk < 4 ? pa : pb) + kk * 8, bd + (uint64_t)((kk * 16 * kRow) >> 4),
+                                       kIdO, kk > 0 ? 1u : (uint32_t)fac);
+                        mma_commit(smem_u32(b_odone));
+                        mma_commit(smem_u32(b_ec + s));
                     }
-                    mma_commit(smem_u32(b_odone));
-                    mma_commit(smem_u32(b_empty + s));
-                    if (next && !early) w_product(c + 1);
+                    if (w_due) w_product();
                 }
             }
             __syncwarp();
+            c += nch;
         }
-    } else if (warp < 4) {
+    } else if (warp < 8) {
         // ===================== P =====================
         if (!kAgg) {
-            const int row = warp * 32 + lane;
-            const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
+            const int quad = warp & 3, row = quad * 32 + lane;
+            const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
+#pragma unroll 1
             for (int it = blockIdx.x; it < tp.items; it += gridDim.x) {
                 const Item im = item_of<kAgg>(tp, it);
                 if (im.nch == 0) continue;
                 const LaJob& jb = tp.p.job[im.job];
                 const float a2 = la_log2_decay(g.a, im.h);
                 const bool fac = factored(a2);
-                bar_wg(1);                      // the table's last readers are done
+                bar_p();                        // the table's last readers are done
                 // factored: lam^{-j'} s_in; exact: lam^j (the first 32 are used) and,
                 // from 32 on, lam^{31-j}
-                ptab[row] = fac ? la_exp2(-a2, jb.rev ? kC - 1 - row : row) * jb.s_in
-                                : exp2f(a2 * (float)(row < 32 ? row : max(63 - row, 0)));
-                bar_wg(1);
-                const float4* vt = reinterpret_cast<const float4*>(jb.rev ? ptab : ptab + 32);
+                if (warp < 4) sts32(ptab + 4 * row, fac ? la_exp2(-a2, jb.rev ? kC - 1 - row : row) * jb.s_in
+                                          : exp2f(a2 * (float)(row < 32 ? row : max(63 - row, 0))));
+                bar_p();
+                const uint32_t vt = jb.rev ? ptab : ptab + 32 * 4;
+#pragma unroll 1
                 for (int x = 0; x < im.nch; ++x, ++c) {
                     const int s = c & 1, ci = jb.rev ? im.nch - 1 - x : x;
                     const int n = min(kC, im.rg.len - ci * kC);
-                    mbar_wait(smem_u32(b_wdone + s), (c >> 1) & 1, err, 1u);
+                    wait_on(smem_u32(b_wdone + s), (c >> 1) & 1, err);
                     tc_fence_after();
                     const uint32_t base = tmem + lane_off + kW + s * 128;
-                    // in place: block b's 16 packed columns lie within columns that
-                    // blocks up to b held
+                    // 16 columns at a time, in place: each half's packed columns lie
+                    // within its own and behind its reads.  (The exact form needs the
+                    // upper half's columns for its second accumulator, so one warpgroup
+                    // packs all into the lower.)
+                    const int b0 = warp < 4 ? 0 : fac ? 4 : 8, b1 = warp < 4 && fac ? 4 : 8;
 #pragma unroll 1
-                    for (int b = 0; b < 4; ++b) {
-                        const int rel = jb.rev ? b - warp : warp - b;
-                        uint32_t o[16];
+                    for (int b = b0; b < b1; ++b) {
+                        const int rel = jb.rev ? (b >> 1) - quad : quad - (b >> 1);
+                        uint32_t o[8];
                         if (rel < 0) {
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) o[e] = 0u;
+                            for (int e = 0; e < 8; ++e) o[e] = 0u;
                         } else {
-                            uint32_t v[32];
+                            const int j0 = b * 16;
+                            uint32_t v[16];
+                            f32x2 r[8];
                             __syncwarp();
-                            tmem_ld_x32(base + b * 32, v);
-                            tmem_wait_ld();
-                            if (fac) {
-                                const ulonglong2* ct = reinterpret_cast<const ulonglong2*>(ptab + b * 32);
+                            tmem_ld_x16(base + j0, v);
+                            if (fac || rel > 0) {
+                                const uint32_t ct = fac ? ptab + 4 * j0 : vt + 4 * (j0 & 31);
+                                uint4 t[4];
 #pragma unroll
-                                for (int e4 = 0; e4 < 8; ++e4) {
-                                    const ulonglong2 t = ct[e4];
-                                    float x0, x1, x2, x3;
-                                    unpair(mul2(pair(v[4 * e4], v[4 * e4 + 1]), t.x), x0, x1);
-                                    unpair(mul2(pair(v[4 * e4 + 2], v[4 * e4 + 3]), t.y), x2, x3);
-                                    v[4 * e4] = __float_as_uint(x0);
-                                    v[4 * e4 + 1] = __float_as_uint(x1);
-                                    v[4 * e4 + 2] = __float_as_uint(x2);
-                                    v[4 * e4 + 3] = __float_as_uint(x3);
+                                for (int e4 = 0; e4 < 4; ++e4) t[e4] = lds128(ct + 16 * e4);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int e4 = 0; e4 < 4; ++e4) {
+                                    r[2 * e4] = mul2(pair(v[4 * e4], v[4 * e4 + 1]), pair(t[e4].x, t[e4].y));
+                                    r[2 * e4 + 1] = mul2(pair(v[4 * e4 + 2], v[4 * e4 + 3]), pair(t[e4].z, t[e4].w));
                                 }
-                                // on the diagonal a select, never a product, drops what
-                                // is above it
-                                if (rel == 0) {
+                                if (!fac) {
+                                    // lam^{i-j} as a row factor times a column factor, both <= 1
+                                    const float u = exp2f(a2 * (float)(jb.rev ? (j0 & ~31) - row : row - (j0 & ~31) - 31)) * jb.s_in;
+                                    const f32x2 u2 = pair(u, u);
 #pragma unroll
-                                    for (int e = 0; e < 32; ++e)
-                                        if (jb.rev ? e < lane : e > lane) v[e] = 0u;
-                                }
-                            } else if (rel == 0) {
-#pragma unroll
-                                for (int e = 0; e < 32; ++e) {
-                                    const int d = jb.rev ? e - lane : lane - e;
-                                    const float w = ptab[d & 31] * jb.s_in;
-                                    v[e] = d >= 0 ? __float_as_uint(__uint_as_float(v[e]) * w) : 0u;
+                                    for (int e = 0; e < 8; ++e) r[e] = mul2(r[e], u2);
                                 }
                             } else {
-                                // lam^{i-j} as a row factor times a column factor, both <= 1
-                                const float u = exp2f(a2 * (float)(jb.rev ? b * 32 - row : row - b * 32 - 31)) * jb.s_in;
+                                tmem_wait_ld();
 #pragma unroll
-                                for (int e4 = 0; e4 < 8; ++e4) {
-                                    const float4 t = vt[e4];
-                                    v[4 * e4] = __float_as_uint(__uint_as_float(v[4 * e4]) * (u * t.x));
-                                    v[4 * e4 + 1] = __float_as_uint(__uint_as_float(v[4 * e4 + 1]) * (u * t.y));
-                                    v[4 * e4 + 2] = __float_as_uint(__uint_as_float(v[4 * e4 + 2]) * (u * t.z));
-                                    v[4 * e4 + 3] = __float_as_uint(__uint_as_float(v[4 * e4 + 3]) * (u * t.w));
+                                for (int e = 0; e < 8; ++e) {
+                                    const int d = (j0 & 31) + 2 * e - lane;   // above the diagonal: masked below
+                                    r[e] = mul2(pair(v[2 * e], v[2 * e + 1]),
+                                                pair(lds32(ptab + 4 * ((jb.rev ? d : -d) & 31)) * jb.s_in,
+                                                     lds32(ptab + 4 * ((jb.rev ? d + 1 : -d - 1) & 31)) * jb.s_in));
                                 }
                             }
-                            if (n < kC && jb.rev) {   // later rows than the chunk has
 #pragma unroll
-                                for (int e = 0; e < 32; ++e)
-                                    if (b * 32 + e >= n) v[e] = 0u;
+                            for (int e = 0; e < 8; ++e) o[e] = pack2(r[e]);
+                            // a select, never a product, drops what is above the diagonal
+                            // or (backwards) past the chunk's tokens: columns lo .. hi stay
+                            if (rel == 0 || (n < kC && jb.rev)) {
+                                const int lo = (jb.rev && rel == 0 ? row : 0) - j0;
+                                const int hi = (jb.rev ? n - 1 : rel == 0 ? row : kC) - j0;
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) {
+                                    if (2 * e < lo || 2 * e > hi) o[e] &= 0xFFFF0000u;
+                                    if (2 * e + 1 < lo || 2 * e + 1 > hi) o[e] &= 0x0000FFFFu;
+                                }
                             }
-#pragma unroll
-                            for (int e = 0; e < 16; ++e)
-                                o[e] = pack2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
                         }
                         __syncwarp();
-                        tmem_st_x16(base + b * 16, o);
+                        tmem_st_x8(base + b * 8 + (b0 == 4 ? 32 : 0), o);
                     }
                     tmem_wait_st();
                     tc_fence_before();
@@ -408,28 +460,31 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                 }
             }
         }
-    } else if (warp < 8) {
+    } else if (warp < 12) {
         // ===================== scaled terms of C =====================
-        const int row = (warp - 4) * 32 + lane;
+        const int row = (warp - 8) * 32 + lane;
+#pragma unroll 1
         for (int it = blockIdx.x; it < tp.items; it += gridDim.x) {
             const Item im = item_of<kAgg>(tp, it);
             const LaJob& jb = tp.p.job[im.job];
             const float a2 = la_log2_decay(g.a, im.h);
             const bool fac = factored(a2);
             const float wf = la_exp2(-a2, jb.rev ? kC - 1 - row : row) * jb.s_in;
+#pragma unroll 1
             for (int x = 0; x < im.nch; ++x, ++c) {
                 const int s = c & 1, ci = jb.rev ? im.nch - 1 - x : x;
                 const int n = min(kC, im.rg.len - ci * kC);
                 const float w = fac ? wf : exp2f(a2 * (float)(jb.rev ? row + 1 : n - 1 - row)) * jb.s_in;
                 const f32x2 w2 = pair(w, w);
-                mbar_wait(smem_u32(b_full + s), (c >> 1) & 1, err, 1u);
-                if (c > 0) mbar_wait(smem_u32(b_udone), (c - 1) & 1, err, 1u);
-                uint8_t* st = smem + s * kStage;
+                wait_on(smem_u32(b_fc + s), (c >> 1) & 1, err);
+                if (n < kC) wait_on(smem_u32(b_fab + s), (c >> 1) & 1, err);
+                if (c > 0) wait_on(smem_u32(b_udone), (c - 1) & 1, err);
+                const uint32_t st = smem_u32(smem + s * kStage), tm = smem_u32(terms);
                 if (row < n) {
-#pragma unroll 2
+#pragma unroll 1
                     for (int ch = 0; ch < 8; ++ch) {
                         const int at = row * kRow + ((ch ^ (row & 7)) << 4);
-                        const uint4 q = *reinterpret_cast<const uint4*>(st + 4 * kAtom + at);
+                        const uint4 q = lds128(st + 4 * kAtom + at);
                         const uint32_t in[4] = {q.x, q.y, q.z, q.w};
                         uint32_t t[kTerms][4];
 #pragma unroll
@@ -448,31 +503,29 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                         }
 #pragma unroll
                         for (int y = 0; y < kTerms; ++y)
-                            *reinterpret_cast<uint4*>(terms + y * kAtom + at) = make_uint4(t[y][0], t[y][1], t[y][2], t[y][3]);
+                            sts128(tm + y * kAtom + at, t[y][0], t[y][1], t[y][2], t[y][3]);
                     }
                 } else {
                     // a row of other tokens: nothing of it may reach a product
-                    const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
+#pragma unroll 1
                     for (int ch = 0; ch < 8; ++ch) {
                         const int at = row * kRow + (ch << 4);
-                        *reinterpret_cast<uint4*>(st + 2 * kAtom + at) = z;
-                        *reinterpret_cast<uint4*>(st + 3 * kAtom + at) = z;
-                        *reinterpret_cast<uint4*>(st + 4 * kAtom + at) = z;
 #pragma unroll
-                        for (int q = 0; q < kTerms; ++q)
-                            *reinterpret_cast<uint4*>(terms + q * kAtom + at) = z;
+                        for (int q = 2; q < 5; ++q) sts128(st + q * kAtom + at, 0u, 0u, 0u, 0u);
+#pragma unroll
+                        for (int q = 0; q < kTerms; ++q) sts128(tm + q * kAtom + at, 0u, 0u, 0u, 0u);
                     }
                 }
                 fence_proxy_async_smem();
                 mbar_arrive(smem_u32(b_vready));
             }
         }
-    } else if (warp < 16) {
+    } else if (warp < 20) {
         // ===================== X =====================
         const int k = (warp & 3) * 32 + lane;           // X's row = tensor-memory lane
-        const int vc = warp < 12 ? 0 : 32;              // X's columns: 32 a thread
+        const int vc = warp < 16 ? 0 : 32;              // X's columns: 32 a thread
         const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+#pragma unroll 1
         for (int it = blockIdx.x; it < tp.items; it += gridDim.x) {
             const Item im = item_of<kAgg>(tp, it);
             if (im.skip || im.rg.seq == g.nseq) continue;
@@ -486,18 +539,16 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
             float* ag = im.cut ? jb.agg + ((int64_t)ridx * g.H + im.h) * elems + at : nullptr;
             const float* in = kAgg ? nullptr : (im.cut ? ag : (jb.init ? jb.init + so : nullptr));
             f32x2 X[16];
-            {
-                float x0[32];
 #pragma unroll
-                for (int v = 0; v < 32; ++v)
-                    x0[v] = in != nullptr && k < jb.DK && v < nv ? in[(int64_t)v * jb.sv] : 0.f;
-#pragma unroll
-                for (int v = 0; v < 16; ++v) X[v] = pair(x0[2 * v], x0[2 * v + 1]);
+            for (int v = 0; v < 16; ++v) {   // nv is a multiple of 16
+                const bool ok = in != nullptr && k < jb.DK && 2 * v < nv;
+                X[v] = pair(ok ? in[(int64_t)(2 * v) * jb.sv] : 0.f, ok ? in[(int64_t)(2 * v + 1) * jb.sv] : 0.f);
             }
             const float a2 = la_log2_decay(g.a, im.h);
             const bool fac = factored(a2);
             float f_hi, f_lo;
             la_decay_pow(g.a, im.h, kC, f_hi, f_lo);
+#pragma unroll 1
             for (int x = 0; x < im.nch; ++x, ++c) {
                 const int s = c & 1, ci = jb.rev ? im.nch - 1 - x : x;
                 const int n = min(kC, im.rg.len - ci * kC);
@@ -505,34 +556,34 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                     // in the factored form the row factor of out is lam^{i'}
                     const float m = fac ? la_exp2(a2, jb.rev ? n - kC : 1) : 1.f;
                     const f32x2 m2 = pair(m, m);
-                    if (c > 0) mbar_wait(smem_u32(b_xdone), (c - 1) & 1, err, 1u);
+                    if (c > 0) wait_on(smem_u32(b_xdone), (c - 1) & 1, err);
 #pragma unroll
                     for (int ch = 0; ch < 4; ++ch)
-                        *reinterpret_cast<uint4*>(xs + k * kRow + (((vc / 8 + ch) ^ (k & 7)) << 4)) =
-                            make_uint4(pack2(mul2(X[4 * ch], m2)), pack2(mul2(X[4 * ch + 1], m2)),
-                                       pack2(mul2(X[4 * ch + 2], m2)), pack2(mul2(X[4 * ch + 3], m2)));
+                        sts128(smem_u32(xs) + k * kRow + (((vc / 8 + ch) ^ (k & 7)) << 4),
+                               pack2(mul2(X[4 * ch], m2)), pack2(mul2(X[4 * ch + 1], m2)),
+                               pack2(mul2(X[4 * ch + 2], m2)), pack2(mul2(X[4 * ch + 3], m2)));
                     fence_proxy_async_smem();
                     mbar_arrive(smem_u32(b_sready));
                 }
                 float hi = f_hi, lo = f_lo;
                 if (n < kC) la_decay_pow(g.a, im.h, n, hi, lo);
                 const float cu = fac ? la_exp2(a2, jb.rev ? kC : n - 1) : 1.f;
-                mbar_wait(smem_u32(b_udone), c & 1, err, 1u);
+                wait_on(smem_u32(b_udone), c & 1, err);
                 tc_fence_after();
                 const f32x2 hi2 = pair(hi, hi), lo2 = pair(lo, lo), cu2 = pair(cu, cu);
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    uint32_t u[kTerms][16];
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t u[kTerms][8];
                     __syncwarp();
 #pragma unroll
                     for (int y = 0; y < kTerms; ++y)
-                        tmem_ld_x16(tmem + lane_off + kU + y * 64 + vc + q * 16, u[y]);
+                        tmem_ld_x8(tmem + lane_off + kU + y * 64 + vc + q * 8, u[y]);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
+                    for (int e = 0; e < 4; ++e) {
                         const f32x2 u2 = add2(pair(u[0][2 * e], u[0][2 * e + 1]),
                                               add2(pair(u[1][2 * e], u[1][2 * e + 1]), pair(u[2][2 * e], u[2][2 * e + 1])));
-                        f32x2& X2 = X[q * 8 + e];
+                        f32x2& X2 = X[q * 4 + e];
                         X2 = fma2(X2, hi2, fma2(X2, lo2, mul2(cu2, u2)));
                     }
                 }
@@ -555,8 +606,9 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
         }
     } else if (!kAgg) {
         // ===================== out =====================
-        const int i = (warp - 16) * 32 + lane;
-        const uint32_t lane_off = (uint32_t)((warp - 16) * 32) << 16;
+        const int i = (warp - 20) * 32 + lane;
+        const uint32_t lane_off = (uint32_t)((warp - 20) * 32) << 16;
+#pragma unroll 1
         for (int it = blockIdx.x; it < tp.items; it += gridDim.x) {
             const Item im = item_of<kAgg>(tp, it);
             const LaJob& jb = tp.p.job[im.job];
@@ -572,53 +624,63 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
             }
             const float a2 = la_log2_decay(g.a, im.h);
             const bool fac = factored(a2);
+#pragma unroll 1
             for (int x = 0; x < im.nch; ++x, ++c) {
                 const int ci = jb.rev ? im.nch - 1 - x : x;
                 const int n = min(kC, im.rg.len - ci * kC);
                 const float f = jb.s_out * (fac ? la_exp2(a2, jb.rev ? kC - 1 - i : i)
                                                 : exp2f(a2 * (float)(jb.rev ? n - 1 - i : i + 1)));
                 const int64_t e0 = (int64_t)(im.rg.t0 + ci * kC + i) * os + oh;
-                mbar_wait(smem_u32(b_odone), c & 1, err, 1u);
+                wait_on(smem_u32(b_odone), c & 1, err);
                 tc_fence_after();
                 const f32x2 f2 = pair(f, f), s2 = pair(jb.s_out, jb.s_out);
 #pragma unroll 1
-                for (int b = 0; b < 4; ++b) {   // 16 columns at a time
-                    uint32_t p[16];
-                    f32x2 r[8];
+                for (int b = 0; b < 2; ++b) {   // 32 columns at a time
+                    uint32_t p[32];
                     __syncwarp();
-                    tmem_ld_x16(tmem + lane_off + kO + b * 16, p);
+                    tmem_ld_x32(tmem + lane_off + kO + b * 32, p);
+                    f32x2 r[16];
                     if (fac) {
                         tmem_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) r[e] = mul2(f2, pair(p[2 * e], p[2 * e + 1]));
+                        for (int e = 0; e < 16; ++e) r[e] = mul2(f2, pair(p[2 * e], p[2 * e + 1]));
                     } else {
-                        uint32_t q[16];
-                        tmem_ld_x16(tmem + lane_off + kW + (c & 1) * 128 + 64 + b * 16, q);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            r[e] = fma2(f2, pair(p[2 * e], p[2 * e + 1]), mul2(s2, pair(q[2 * e], q[2 * e + 1])));
+                        for (int h = 0; h < 2; ++h) {
+                            uint32_t q[16];
+                            tmem_ld_x16(tmem + lane_off + kW + (c & 1) * 128 + 64 + b * 32 + h * 16, q);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                r[8 * h + e] = fma2(f2, pair(p[16 * h + 2 * e], p[16 * h + 2 * e + 1]),
+                                                    mul2(s2, pair(q[2 * e], q[2 * e + 1])));
+                        }
                     }
-                    if (b == 3) {
+                    if (b == 1) {
                         tc_fence_before();
                         mbar_arrive(smem_u32(b_ofree));
                     }
-                    if (i < n && b * 16 < nv) {
-                        const int64_t e = e0 + b * 16;
-                        if (jb.out_f32) {
-                            ulonglong2* d = reinterpret_cast<ulonglong2*>(static_cast<float*>(jb.out) + e);
+                    if (i < n) {
 #pragma unroll
-                            for (int y = 0; y < 4; ++y) d[y] = make_ulonglong2(r[2 * y], r[2 * y + 1]);
-                        } else {
-                            uint32_t w[8];
+                        for (int h = 0; h < 2; ++h) {
+                            const int col = b * 32 + h * 16;
+                            if (col >= nv) continue;
+                            if (jb.out_f32) {
+                                ulonglong2* d = reinterpret_cast<ulonglong2*>(static_cast<float*>(jb.out) + e0 + col);
 #pragma unroll
-                            for (int y = 0; y < 8; ++y) w[y] = pack2(r[y]);
-                            __nv_bfloat16* d = static_cast<__nv_bfloat16*>(jb.out) + e;
-                            if ((reinterpret_cast<uintptr_t>(d) & 31) == 0) {
-                                st_v8(d, w);
+                                for (int y = 0; y < 4; ++y) d[y] = make_ulonglong2(r[8 * h + 2 * y], r[8 * h + 2 * y + 1]);
                             } else {
-                                reinterpret_cast<uint4*>(d)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-                                reinterpret_cast<uint4*>(d)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                                uint32_t w[8];
+#pragma unroll
+                                for (int y = 0; y < 8; ++y) w[y] = pack2(r[8 * h + y]);
+                                __nv_bfloat16* d = static_cast<__nv_bfloat16*>(jb.out) + e0 + col;
+                                if ((reinterpret_cast<uintptr_t>(d) & 31) == 0) {
+                                    st_v8(d, w);
+                                } else {
+                                    reinterpret_cast<uint4*>(d)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                                    reinterpret_cast<uint4*>(d)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                                }
                             }
                         }
                     }
