@@ -7,13 +7,13 @@
 //     W   = A B^T                                   128 x 128 x DK
 //     P   = s_in W o lam^{-j} [i >= j]              (bf16, tensor memory)
 //     out = s_out lam^i o (A (lam X) + P C)         128 x 64 x DK, 128 x 64 x 128
-//     U   = B^T (s_in lam^{-j} o C)                 DK x 64 x 128
-//     X   <- lam^n X + lam^{n-1} U
-// (backwards the decay of X and U is one step longer).  Rows and columns carry
+//     U   = B^T (s_in lam^{n-1-j} o C)              DK x 64 x 128
+//     X   <- lam^n X + U
+// (backwards X and U have decayed one step less and one more).  Rows and columns carry
 // the decay as separate factors, so that out is one accumulator and P costs one
 // product for each element; that is safe while lam^-127 <= 2^40.  For heads that
 // forget faster the exact form runs: lam^{i-j} element by element, A X and P C
-// in two accumulators, U with weights lam^{n-1-j}.
+// in two accumulators.
 // Every operand is read once per chain from HBM (a and b once per 64 columns of
 // c, from L2 the second time) and no state leaves the chip between chunks.
 //
@@ -25,16 +25,16 @@
 // CUDA cores, where it is rounded to nearest (how the tensor core's accumulator
 // rounds is not documented, and a chain adds it up over hundreds of chunks).
 //
-// Persistent CTAs of 26 warps, one per SM:
+// Persistent CTAs of 30 warps, one per SM:
 //   0-7   P: tensor memory -> decay, mask -> tensor memory (bf16, in place; two
 //         warpgroups, half of the columns each)
-//   8-11  C's scaled terms (a thread owns token row j); zeroes the rows of a
-//         ragged chunk that belong to other tokens, whatever they hold
-//   12-19 X in registers (a thread owns 32 columns of a row): bf16 copy for A X,
+//   8-15  C's scaled terms (a thread owns half of a token's row); zeroes the rows
+//         of a ragged chunk that belong to other tokens, whatever they hold
+//   16-23 X in registers (a thread owns 32 columns of a row): bf16 copy for A X,
 //         update with U, stored states
-//   20-23 out (a thread owns a token row)
-//   24    TMA, two stages of A, B and C tiles (80 KB each)
-//   25    MMA issue: U(c), A X(c), W(c + 1), P C(c)
+//   24-27 out (a thread owns a token row)
+//   28    TMA, two stages of A, B and C tiles (80 KB each)
+//   29    MMA issue: U(c), W(c + 1), A X(c), P C(c)
 // The roles' loops are kept short (packed fp32 arithmetic, little unrolling): six
 // codes run side by side on each scheduler, and fully unrolled they spent most of
 // their time on instruction fetches.
@@ -53,8 +53,8 @@ __device__ unsigned int g_la_error;  // bit 0: a bounded wait gave up
 constexpr int kC = 128;                       // tokens per chunk
 constexpr int kRow = 128;                     // bytes of a tile row (64 columns)
 constexpr int kAtom = kC * kRow;              // 16 KB: 128 rows of 64 columns
-constexpr int kThreads = 832;
-constexpr int kTmaWarp = 24, kMmaWarp = 25;
+constexpr int kThreads = 960;
+constexpr int kTmaWarp = 28, kMmaWarp = 29;
 constexpr int kStage = 5 * kAtom;             // A (2 atoms), B (2), C (1)
 constexpr int kTerms = 3;
 constexpr int kSmem = 2 * kStage + kTerms * kAtom + kAtom + 1024 + 1024;
@@ -212,9 +212,16 @@ __device__ __forceinline__ void mma_steps(uint32_t d, uint64_t a, uint64_t b, in
 template <bool kAgg>
 __global__ void __launch_bounds__(kThreads, 1)
 linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps maps) {
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>(
-        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    // aligned by declaration, not by arithmetic: its addresses are then constants
+    // and cost no registers
+    extern __shared__ __align__(1024) uint8_t smem[];
+    if ((smem_u32(smem) & 1023u) != 0u) {
+        if (threadIdx.x == 0) {
+            atomicOr(&g_la_error, 1u);
+            report_timeout_to_host(&g_la_error, tp.host_err);
+        }
+        return;
+    }
     uint8_t* terms = smem + 2 * kStage;
     uint8_t* xs = terms + kTerms * kAtom;
     uint64_t* bars = reinterpret_cast<uint64_t*>(xs + kAtom);
@@ -226,7 +233,7 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
     uint64_t* b_pready = bars + 10;   // [2] P written (256)
     uint64_t* b_udone = bars + 12;    // U computed, terms read (commit)
     uint64_t* b_ufree = bars + 13;    // U read (256)
-    uint64_t* b_vready = bars + 14;   // terms written (128)
+    uint64_t* b_vready = bars + 14;   // terms written (256)
     uint64_t* b_sready = bars + 15;   // bf16 X written (256)
     uint64_t* b_xdone = bars + 16;    // A X computed: the bf16 X may change (commit)
     uint64_t* b_odone = bars + 17;    // out computed (commit)
@@ -246,7 +253,7 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
         }
         mbar_init(smem_u32(b_udone), 1);
         mbar_init(smem_u32(b_ufree), 256);
-        mbar_init(smem_u32(b_vready), 128);
+        mbar_init(smem_u32(b_vready), 256);
         mbar_init(smem_u32(b_sready), 256);
         mbar_init(smem_u32(b_xdone), 1);
         mbar_init(smem_u32(b_odone), 1);
@@ -406,39 +413,36 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                         } else {
                             const int j0 = b * 16;
                             uint32_t v[16];
-                            f32x2 r[8];
                             __syncwarp();
                             tmem_ld_x16(base + j0, v);
                             if (fac || rel > 0) {
                                 const uint32_t ct = fac ? ptab + 4 * j0 : vt + 4 * (j0 & 31);
-                                uint4 t[4];
-#pragma unroll
-                                for (int e4 = 0; e4 < 4; ++e4) t[e4] = lds128(ct + 16 * e4);
+                                // exact: lam^{i-j} as a row factor times a column factor, both <= 1
+                                const float u = fac ? 1.f : exp2f(a2 * (float)(jb.rev ? (j0 & ~31) - row : row - (j0 & ~31) - 31)) * jb.s_in;
+                                const f32x2 u2 = pair(u, u);
                                 tmem_wait_ld();
 #pragma unroll
                                 for (int e4 = 0; e4 < 4; ++e4) {
-                                    r[2 * e4] = mul2(pair(v[4 * e4], v[4 * e4 + 1]), pair(t[e4].x, t[e4].y));
-                                    r[2 * e4 + 1] = mul2(pair(v[4 * e4 + 2], v[4 * e4 + 3]), pair(t[e4].z, t[e4].w));
-                                }
-                                if (!fac) {
-                                    // lam^{i-j} as a row factor times a column factor, both <= 1
-                                    const float u = exp2f(a2 * (float)(jb.rev ? (j0 & ~31) - row : row - (j0 & ~31) - 31)) * jb.s_in;
-                                    const f32x2 u2 = pair(u, u);
-#pragma unroll
-                                    for (int e = 0; e < 8; ++e) r[e] = mul2(r[e], u2);
+                                    const uint4 t = lds128(ct + 16 * e4);
+                                    f32x2 r0 = mul2(pair(v[4 * e4], v[4 * e4 + 1]), pair(t.x, t.y));
+                                    f32x2 r1 = mul2(pair(v[4 * e4 + 2], v[4 * e4 + 3]), pair(t.z, t.w));
+                                    if (!fac) {
+                                        r0 = mul2(r0, u2);
+                                        r1 = mul2(r1, u2);
+                                    }
+                                    o[2 * e4] = pack2(r0);
+                                    o[2 * e4 + 1] = pack2(r1);
                                 }
                             } else {
                                 tmem_wait_ld();
 #pragma unroll
                                 for (int e = 0; e < 8; ++e) {
                                     const int d = (j0 & 31) + 2 * e - lane;   // above the diagonal: masked below
-                                    r[e] = mul2(pair(v[2 * e], v[2 * e + 1]),
-                                                pair(lds32(ptab + 4 * ((jb.rev ? d : -d) & 31)) * jb.s_in,
-                                                     lds32(ptab + 4 * ((jb.rev ? d + 1 : -d - 1) & 31)) * jb.s_in));
+                                    o[e] = pack2(mul2(pair(v[2 * e], v[2 * e + 1]),
+                                                      pair(lds32(ptab + 4 * ((jb.rev ? d : -d) & 31)) * jb.s_in,
+                                                           lds32(ptab + 4 * ((jb.rev ? d + 1 : -d - 1) & 31)) * jb.s_in)));
                                 }
                             }
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) o[e] = pack2(r[e]);
                             // a select, never a product, drops what is above the diagonal
                             // or (backwards) past the chunk's tokens: columns lo .. hi stay
                             if (rel == 0 || (n < kC && jb.rev)) {
@@ -460,70 +464,70 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                 }
             }
         }
-    } else if (warp < 12) {
+    } else if (warp < 16) {
         // ===================== scaled terms of C =====================
-        const int row = (warp - 8) * 32 + lane;
+
+        const int row = (warp & 3) * 32 + lane, ch0 = warp < 12 ? 0 : 4;   // half of the row's columns
 #pragma unroll 1
         for (int it = blockIdx.x; it < tp.items; it += gridDim.x) {
             const Item im = item_of<kAgg>(tp, it);
             const LaJob& jb = tp.p.job[im.job];
             const float a2 = la_log2_decay(g.a, im.h);
-            const bool fac = factored(a2);
-            const float wf = la_exp2(-a2, jb.rev ? kC - 1 - row : row) * jb.s_in;
 #pragma unroll 1
             for (int x = 0; x < im.nch; ++x, ++c) {
                 const int s = c & 1, ci = jb.rev ? im.nch - 1 - x : x;
                 const int n = min(kC, im.rg.len - ci * kC);
-                const float w = fac ? wf : exp2f(a2 * (float)(jb.rev ? row + 1 : n - 1 - row)) * jb.s_in;
+                const float w = la_exp2(a2, jb.rev ? row + 1 : max(n - 1 - row, 0)) * jb.s_in;
                 const f32x2 w2 = pair(w, w);
                 wait_on(smem_u32(b_fc + s), (c >> 1) & 1, err);
-                if (n < kC) wait_on(smem_u32(b_fab + s), (c >> 1) & 1, err);
-                if (c > 0) wait_on(smem_u32(b_udone), (c - 1) & 1, err);
                 const uint32_t st = smem_u32(smem + s * kStage), tm = smem_u32(terms);
-                if (row < n) {
-#pragma unroll 1
-                    for (int ch = 0; ch < 8; ++ch) {
-                        const int at = row * kRow + ((ch ^ (row & 7)) << 4);
-                        const uint4 q = lds128(st + 4 * kAtom + at);
-                        const uint32_t in[4] = {q.x, q.y, q.z, q.w};
-                        uint32_t t[kTerms][4];
+                // the terms of this thread's 32 columns are ready in registers when the
+                // last U lets go of their tiles; a row of other tokens gives zeros
+                uint32_t t[4][kTerms][4];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            // 24 bits as three times 8, cut off rather than rounded:
-                            // the three add up to the product exactly
-                            f32x2 r = mul2(pair(lo16(in[e]), hi16(in[e])), w2);
+                for (int ch = 0; ch < 4; ++ch) {
+                    const uint4 q = lds128(st + 4 * kAtom + row * kRow + (((ch0 + ch) ^ (row & 7)) << 4));
+                    const uint32_t in[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-                            for (int y = 0; y < kTerms; ++y) {
-                                float a, b;
-                                unpair(r, a, b);
-                                t[y][e] = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
-                                if (y + 1 < kTerms)
-                                    r = add2(r, pair(-hi16(__float_as_uint(a)), -hi16(__float_as_uint(b))));
-                            }
+                    for (int e = 0; e < 4; ++e) {
+                        // 24 bits as three times 8, cut off rather than rounded: the
+                        // three add up to the product exactly
+                        f32x2 r = row < n ? mul2(pair(lo16(in[e]), hi16(in[e])), w2) : 0ull;
+#pragma unroll
+                        for (int y = 0; y < kTerms; ++y) {
+                            float a, b;
+                            unpair(r, a, b);
+                            t[ch][y][e] = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+                            if (y + 1 < kTerms)
+                                r = add2(r, pair(-hi16(__float_as_uint(a)), -hi16(__float_as_uint(b))));
                         }
-#pragma unroll
-                        for (int y = 0; y < kTerms; ++y)
-                            sts128(tm + y * kAtom + at, t[y][0], t[y][1], t[y][2], t[y][3]);
-                    }
-                } else {
-                    // a row of other tokens: nothing of it may reach a product
-#pragma unroll 1
-                    for (int ch = 0; ch < 8; ++ch) {
-                        const int at = row * kRow + (ch << 4);
-#pragma unroll
-                        for (int q = 2; q < 5; ++q) sts128(st + q * kAtom + at, 0u, 0u, 0u, 0u);
-#pragma unroll
-                        for (int q = 0; q < kTerms; ++q) sts128(tm + q * kAtom + at, 0u, 0u, 0u, 0u);
                     }
                 }
+                if (n < kC) {
+                    wait_on(smem_u32(b_fab + s), (c >> 1) & 1, err);
+                    if (row >= n) {   // nothing of such a row may reach a product
+#pragma unroll 1
+                        for (int ch = ch0; ch < ch0 + 4; ++ch)
+#pragma unroll
+                            for (int q = 2; q < 5; ++q) sts128(st + q * kAtom + row * kRow + (ch << 4), 0u, 0u, 0u, 0u);
+                    }
+                }
+                if (c > 0) wait_on(smem_u32(b_udone), (c - 1) & 1, err);
+#pragma unroll
+                for (int ch = 0; ch < 4; ++ch)
+#pragma unroll
+                    for (int y = 0; y < kTerms; ++y)
+                        sts128(tm + y * kAtom + row * kRow + (((ch0 + ch) ^ (row & 7)) << 4),
+                               t[ch][y][0], t[ch][y][1], t[ch][y][2], t[ch][y][3]);
                 fence_proxy_async_smem();
                 mbar_arrive(smem_u32(b_vready));
             }
         }
-    } else if (warp < 20) {
+    } else if (warp < 24) {
         // ===================== X =====================
+
         const int k = (warp & 3) * 32 + lane;           // X's row = tensor-memory lane
-        const int vc = warp < 16 ? 0 : 32;              // X's columns: 32 a thread
+        const int vc = warp < 20 ? 0 : 32;              // X's columns: 32 a thread
         const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
 #pragma unroll 1
         for (int it = blockIdx.x; it < tp.items; it += gridDim.x) {
@@ -567,24 +571,23 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                 }
                 float hi = f_hi, lo = f_lo;
                 if (n < kC) la_decay_pow(g.a, im.h, n, hi, lo);
-                const float cu = fac ? la_exp2(a2, jb.rev ? kC : n - 1) : 1.f;
                 wait_on(smem_u32(b_udone), c & 1, err);
                 tc_fence_after();
-                const f32x2 hi2 = pair(hi, hi), lo2 = pair(lo, lo), cu2 = pair(cu, cu);
+                const f32x2 hi2 = pair(hi, hi), lo2 = pair(lo, lo);
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    uint32_t u[kTerms][8];
+                for (int q = 0; q < 8; ++q) {
+                    uint32_t u0[4], u1[4], u2[4];
                     __syncwarp();
-#pragma unroll
-                    for (int y = 0; y < kTerms; ++y)
-                        tmem_ld_x8(tmem + lane_off + kU + y * 64 + vc + q * 8, u[y]);
+                    tmem_ld_x4(tmem + lane_off + kU + vc + q * 4, u0);
+                    tmem_ld_x4(tmem + lane_off + kU + 64 + vc + q * 4, u1);
+                    tmem_ld_x4(tmem + lane_off + kU + 128 + vc + q * 4, u2);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const f32x2 u2 = add2(pair(u[0][2 * e], u[0][2 * e + 1]),
-                                              add2(pair(u[1][2 * e], u[1][2 * e + 1]), pair(u[2][2 * e], u[2][2 * e + 1])));
-                        f32x2& X2 = X[q * 4 + e];
-                        X2 = fma2(X2, hi2, fma2(X2, lo2, mul2(cu2, u2)));
+                    for (int e = 0; e < 2; ++e) {
+                        const f32x2 u = add2(pair(u0[2 * e], u0[2 * e + 1]),
+                                             add2(pair(u1[2 * e], u1[2 * e + 1]), pair(u2[2 * e], u2[2 * e + 1])));
+                        f32x2& X2 = X[q * 2 + e];
+                        X2 = fma2(X2, hi2, fma2(X2, lo2, u));
                     }
                 }
                 tc_fence_before();
@@ -606,8 +609,8 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
         }
     } else if (!kAgg) {
         // ===================== out =====================
-        const int i = (warp - 20) * 32 + lane;
-        const uint32_t lane_off = (uint32_t)((warp - 20) * 32) << 16;
+        const int i = (warp - 24) * 32 + lane;
+        const uint32_t lane_off = (uint32_t)((warp - 24) * 32) << 16;
 #pragma unroll 1
         for (int it = blockIdx.x; it < tp.items; it += gridDim.x) {
             const Item im = item_of<kAgg>(tp, it);
@@ -635,52 +638,39 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                 tc_fence_after();
                 const f32x2 f2 = pair(f, f), s2 = pair(jb.s_out, jb.s_out);
 #pragma unroll 1
-                for (int b = 0; b < 2; ++b) {   // 32 columns at a time
-                    uint32_t p[32];
+                for (int b = 0; b < 4; ++b) {   // 16 columns at a time
+                    uint32_t p[16];
+                    f32x2 r[8];
                     __syncwarp();
-                    tmem_ld_x32(tmem + lane_off + kO + b * 32, p);
-                    f32x2 r[16];
-                    if (fac) {
+                    tmem_ld_x16(tmem + lane_off + kO + b * 16, p);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) r[e] = mul2(f2, pair(p[2 * e], p[2 * e + 1]));
+                    if (!fac) {
+                        tmem_ld_x16(tmem + lane_off + kW + (c & 1) * 128 + 64 + b * 16, p);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) r[e] = mul2(f2, pair(p[2 * e], p[2 * e + 1]));
-                    } else {
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            uint32_t q[16];
-                            tmem_ld_x16(tmem + lane_off + kW + (c & 1) * 128 + 64 + b * 32 + h * 16, q);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int e = 0; e < 8; ++e)
-                                r[8 * h + e] = fma2(f2, pair(p[16 * h + 2 * e], p[16 * h + 2 * e + 1]),
-                                                    mul2(s2, pair(q[2 * e], q[2 * e + 1])));
-                        }
+                        for (int e = 0; e < 8; ++e) r[e] = fma2(s2, pair(p[2 * e], p[2 * e + 1]), r[e]);
                     }
-                    if (b == 1) {
+                    if (b == 3) {
                         tc_fence_before();
                         mbar_arrive(smem_u32(b_ofree));
                     }
-                    if (i < n) {
+                    if (i < n && b * 16 < nv) {
+                        if (jb.out_f32) {
+                            ulonglong2* d = reinterpret_cast<ulonglong2*>(static_cast<float*>(jb.out) + e0 + b * 16);
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const int col = b * 32 + h * 16;
-                            if (col >= nv) continue;
-                            if (jb.out_f32) {
-                                ulonglong2* d = reinterpret_cast<ulonglong2*>(static_cast<float*>(jb.out) + e0 + col);
+                            for (int y = 0; y < 4; ++y) d[y] = make_ulonglong2(r[2 * y], r[2 * y + 1]);
+                        } else {
+                            uint32_t w[8];
 #pragma unroll
-                                for (int y = 0; y < 4; ++y) d[y] = make_ulonglong2(r[8 * h + 2 * y], r[8 * h + 2 * y + 1]);
+                            for (int y = 0; y < 8; ++y) w[y] = pack2(r[y]);
+                            __nv_bfloat16* d = static_cast<__nv_bfloat16*>(jb.out) + e0 + b * 16;
+                            if ((reinterpret_cast<uintptr_t>(d) & 31) == 0) {
+                                st_v8(d, w);
                             } else {
-                                uint32_t w[8];
-#pragma unroll
-                                for (int y = 0; y < 8; ++y) w[y] = pack2(r[8 * h + y]);
-                                __nv_bfloat16* d = static_cast<__nv_bfloat16*>(jb.out) + e0 + col;
-                                if ((reinterpret_cast<uintptr_t>(d) & 31) == 0) {
-                                    st_v8(d, w);
-                                } else {
-                                    reinterpret_cast<uint4*>(d)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-                                    reinterpret_cast<uint4*>(d)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-                                }
+                                reinterpret_cast<uint4*>(d)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                                reinterpret_cast<uint4*>(d)[1] = make_uint4(w[4], w[5], w[6], w[7]);
                             }
                         }
                     }
