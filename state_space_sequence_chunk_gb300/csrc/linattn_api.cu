@@ -26,7 +26,7 @@ int sm_count() {
     return sms;
 }
 
-ssd_status make_la(const ssd_linattn_dims* d, bool packed, La* p) {
+ssd_status make_la(const ssd_linattn_dims* d, bool packed, bool backward, La* p) {
     if (!d) return SSD_ERR_NULL;
     if (d->dtype != SSD_F32 && d->dtype != SSD_BF16) return SSD_ERR_DTYPE;
     if (d->reserved != 0 || d->nseqs < 0 || d->tokens < 0 || d->max_seqlen < 0) return SSD_ERR_SHAPE;
@@ -53,11 +53,13 @@ ssd_status make_la(const ssd_linattn_dims* d, bool packed, La* p) {
     g.nseq = (int)p->n; g.H = (int)p->H; g.T = (int)p->T;
     g.L = packed || p->n == 0 ? 0 : (int)(p->T / p->n);
     g.a = nullptr;
-    // Ranges: about four for every SM if the work were spread evenly, none
-    // shorter than 512 tokens.  A sequence that fits one range is not cut; longer
-    // ones pay a second reading of two operands and gain the whole GPU.
-    const int64_t cols = ((p->K > p->V ? p->K : p->V) + kLaCols - 1) / kLaCols;
-    int64_t R = p->T * p->H * cols / (4 * (int64_t)sm_count());
+    // Ranges: half of what an SM would get if the work were spread evenly (so that
+    // the longest of them, taken last, adds at most that), none shorter than 512
+    // tokens.  A sequence that fits one range is not cut; longer ones pay a second
+    // reading of two operands, and gain the whole GPU.
+    const int64_t kb = (p->K + kLaCols - 1) / kLaCols, vb = (p->V + kLaCols - 1) / kLaCols;
+    const int64_t cols = backward ? 2 * kb + vb : vb;
+    int64_t R = p->T * p->H * cols / (2 * (int64_t)sm_count());
     R = (R + 127) / 128 * 128;
     if (R < 512) R = 512;
     int64_t longest = packed ? (d->max_seqlen ? d->max_seqlen : p->T) : g.L;
@@ -80,9 +82,8 @@ size_t span(int64_t T, int64_t stride, int64_t w, int es) {
 }
 
 cudaError_t run_jobs(LaParams& p, int dtype, cudaStream_t st) {
-    const int sms = sm_count();
     auto pass = [&](int mode) {
-        return dtype == SSD_BF16 ? launch_linattn_tc(p, mode, sms, st)
+        return dtype == SSD_BF16 ? launch_linattn_tc(p, mode, st)
                                  : launch_linattn_simt(p, dtype, mode, st);
     };
     cudaError_t e = cudaSuccess;
@@ -105,7 +106,7 @@ size_t ssd_linattn_workspace_bytes(const ssd_linattn_dims* d, int backward) {
     size_t need = 0;
     for (int packed = 0; packed < 2; ++packed) {
         La p;
-        if (make_la(d, packed != 0, &p) != SSD_OK) continue;
+        if (make_la(d, packed != 0, backward != 0, &p) != SSD_OK) continue;
         const size_t b = backward ? 3 * p.agg_bytes + part_bytes(p) : p.agg_bytes;
         if (b > need) need = b;
     }
@@ -117,7 +118,7 @@ ssd_status ssd_linattn_fwd(const ssd_linattn_dims* d, const void* q, const void*
                            const float* init_state, void* o, float* final_state, void* workspace,
                            size_t workspace_bytes, void* stream) {
     La p;
-    ssd_status s = make_la(d, cu_seqlens != nullptr, &p);
+    ssd_status s = make_la(d, cu_seqlens != nullptr, false, &p);
     if (s != SSD_OK) return s;
     if (p.n == 0 && p.T == 0) return SSD_OK;
     if (!isfinite(scale)) return SSD_ERR_SHAPE;
@@ -160,7 +161,7 @@ ssd_status ssd_linattn_bwd(const ssd_linattn_dims* d, const void* q, const void*
                            float* dinit_state, void* workspace, size_t workspace_bytes,
                            void* stream) {
     La p;
-    ssd_status s = make_la(d, cu_seqlens != nullptr, &p);
+    ssd_status s = make_la(d, cu_seqlens != nullptr, true, &p);
     if (s != SSD_OK) return s;
     if (p.n == 0 && p.T == 0) return SSD_OK;
     if (!isfinite(scale)) return SSD_ERR_SHAPE;
@@ -222,7 +223,7 @@ ssd_status ssd_linattn_step(const ssd_linattn_dims* d, const void* q, const void
                             const float* log_decay, float scale, const int32_t* slots, float* cache,
                             int64_t nslots, void* o, void* stream) {
     La p;
-    ssd_status s = make_la(d, true, &p);
+    ssd_status s = make_la(d, true, false, &p);
     if (s != SSD_OK) return s;
     if (p.n != p.T || nslots < 0 || !isfinite(scale)) return SSD_ERR_SHAPE;
     if (!slots && nslots < p.n) return SSD_ERR_SHAPE;

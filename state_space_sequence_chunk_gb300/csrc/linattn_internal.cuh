@@ -147,7 +147,7 @@ __device__ __forceinline__ void la_decay_pow(const float* a, int h, int n, float
 // Launchers.  `mode` 0: the main pass; 1: the ranges' own sums into agg.
 cudaError_t launch_linattn_simt(const LaParams& p, int dtype, int mode, cudaStream_t stream);
 // The same on the tensor cores (bf16).
-cudaError_t launch_linattn_tc(const LaParams& p, int mode, int sms, cudaStream_t stream);
+cudaError_t launch_linattn_tc(const LaParams& p, int mode, cudaStream_t stream);
 // agg -> the state at each range's start, in place.
 cudaError_t launch_linattn_scan(const LaParams& p, cudaStream_t stream);
 // out[t, g, :] = sum over the group's heads of part[t, h, :], rounded to `dtype`.

@@ -66,7 +66,7 @@ constexpr float kSpan = 40.f;
 
 struct TcParams {
     LaParams p;
-    int nvb, items;
+    int nvb;
     unsigned int* host_err;
 };
 struct TcMaps {
@@ -157,6 +157,26 @@ __device__ __forceinline__ float la_exp2(float a2, int n) {
     return fmaf(r, e * 0.6931471805599453f, r);
 }
 
+// Items are handed out by the hardware: the grid has one CTA for each, and a
+// running CTA takes the index of one that has not started, which is then not
+// launched (cluster launch control).  Ranges differ in length, so a fixed share
+// of them for each CTA left SMs idle.
+__device__ __forceinline__ void request_item(uint32_t slot, uint32_t bar) {
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];"
+        ::"r"(slot), "r"(bar) : "memory");
+}
+// The answer in `slot`: a CTA's index, or -1 when none is left.
+__device__ __forceinline__ int granted_item(uint32_t slot) {
+    int x;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\tld.shared.b128 r, [%1];\n\tmov.b32 %0, -1;\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %0, r;\n\t}"
+        : "=r"(x) : "r"(slot) : "memory");
+    return x;
+}
+
 // One item of a CTA's list: the columns of one job, of one head, of one range.
 struct Item {
     LaRange rg;
@@ -238,8 +258,11 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
     uint64_t* b_xdone = bars + 16;    // A X computed: the bf16 X may change (commit)
     uint64_t* b_odone = bars + 17;    // out computed (commit)
     uint64_t* b_ofree = bars + 18;    // out read (128)
-    uint32_t* holder = reinterpret_cast<uint32_t*>(bars + 19);
-    const uint32_t ptab = smem_u32(bars + 20);   // [128] fp32: column factors of P
+    uint64_t* b_ifull = bars + 19;    // [2] answer to an item request (tx)
+    uint64_t* b_ifree = bars + 21;    // [2] answer read (every warp that walks items)
+    uint32_t* holder = reinterpret_cast<uint32_t*>(bars + 23);
+    const uint32_t answers = smem_u32(bars + 24);   // [2] 16 bytes each
+    const uint32_t ptab = smem_u32(bars + 28);      // [128] fp32: column factors of P
 
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
@@ -250,6 +273,10 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
             mbar_init(smem_u32(b_ec + s), 1);
             mbar_init(smem_u32(b_wdone + s), 1);
             mbar_init(smem_u32(b_pready + s), 256);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(smem_u32(b_ifull + s), 1);
+            mbar_init(smem_u32(b_ifree + s), kAgg ? 18 : kThreads / 32);
         }
         mbar_init(smem_u32(b_udone), 1);
         mbar_init(smem_u32(b_ufree), 256);
@@ -269,11 +296,27 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
     const LaGeom& g = tp.p.g;
     // every role walks the same items and counts chunks in c: barrier phases
     // follow from the count alone
-    int c = 0;
+    int c = 0, k_item = 0;
+    auto next_item = [&]() {
+        const int slot = k_item & 1;
+        wait_on(smem_u32(b_ifull + slot), (k_item >> 1) & 1, err);
+        const int it = granted_item(answers + 16 * slot);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(b_ifree + slot));
+        ++k_item;
+        return it < 0 ? -1 : uniform(it);
+    };
 
     if (warp == kTmaWarp) {
 #pragma unroll 1
-        for (int it = blockIdx.x; it < tp.items; it += gridDim.x) {
+        for (int it = blockIdx.x; it >= 0; it = next_item()) {
+            if (lane == 0) {   // the next item, while this one runs
+                const int slot = k_item & 1;
+                wait_on(smem_u32(b_ifree + slot), ((k_item >> 1) & 1) ^ 1, err);
+                mbar_arrive_expect_tx(smem_u32(b_ifull + slot), 16);
+                request_item(answers + 16 * slot, smem_u32(b_ifull + slot));
+            }
             const Item im = item_of<kAgg>(tp, it);
             const LaJob& jb = tp.p.job[im.job];
             if (lane == 0) {
@@ -303,7 +346,7 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
         constexpr uint32_t kIdO = make_idesc(1, 128, 64, 0, 1);
         constexpr uint32_t kIdU = make_idesc(1, 128, 64 * kTerms, 1, 1);
 #pragma unroll 1
-        for (int it = blockIdx.x; it < tp.items; it += gridDim.x) {
+        for (int it = blockIdx.x; it >= 0; it = next_item()) {
             const Item im = item_of<kAgg>(tp, it);
             const int nch = uniform(im.nch), ks = uniform(tp.p.job[im.job].DK / 16);
             const int fac = uniform(factored(la_log2_decay(g.a, im.h)) ? 1 : 0);
@@ -378,7 +421,7 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
             const int quad = warp & 3, row = quad * 32 + lane;
             const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
 #pragma unroll 1
-            for (int it = blockIdx.x; it < tp.items; it += gridDim.x) {
+            for (int it = blockIdx.x; it >= 0; it = next_item()) {
                 const Item im = item_of<kAgg>(tp, it);
                 if (im.nch == 0) continue;
                 const LaJob& jb = tp.p.job[im.job];
@@ -469,7 +512,7 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
 
         const int row = (warp & 3) * 32 + lane, ch0 = warp < 12 ? 0 : 4;   // half of the row's columns
 #pragma unroll 1
-        for (int it = blockIdx.x; it < tp.items; it += gridDim.x) {
+        for (int it = blockIdx.x; it >= 0; it = next_item()) {
             const Item im = item_of<kAgg>(tp, it);
             const LaJob& jb = tp.p.job[im.job];
             const float a2 = la_log2_decay(g.a, im.h);
@@ -530,7 +573,7 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
         const int vc = warp < 20 ? 0 : 32;              // X's columns: 32 a thread
         const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
 #pragma unroll 1
-        for (int it = blockIdx.x; it < tp.items; it += gridDim.x) {
+        for (int it = blockIdx.x; it >= 0; it = next_item()) {
             const Item im = item_of<kAgg>(tp, it);
             if (im.skip || im.rg.seq == g.nseq) continue;
             const LaJob& jb = tp.p.job[im.job];
@@ -612,7 +655,7 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
         const int i = (warp - 24) * 32 + lane;
         const uint32_t lane_off = (uint32_t)((warp - 24) * 32) << 16;
 #pragma unroll 1
-        for (int it = blockIdx.x; it < tp.items; it += gridDim.x) {
+        for (int it = blockIdx.x; it >= 0; it = next_item()) {
             const Item im = item_of<kAgg>(tp, it);
             const LaJob& jb = tp.p.job[im.job];
             const int nv = min(kLaCols, jb.DV - im.v0);
@@ -698,7 +741,7 @@ bool encode(CUtensorMap* m, const void* base, int D, int heads, int64_t stride, 
 
 }  // namespace
 
-cudaError_t launch_linattn_tc(const LaParams& p, int mode, int sms, cudaStream_t stream) {
+cudaError_t launch_linattn_tc(const LaParams& p, int mode, cudaStream_t stream) {
     TcParams tp;
     TcMaps maps;
     tp.p = p;
@@ -714,13 +757,12 @@ cudaError_t launch_linattn_tc(const LaParams& p, int mode, int sms, cudaStream_t
             return cudaErrorInvalidValue;
     }
     const int64_t items = (int64_t)p.g.range_cap * p.g.H * p.njobs * tp.nvb;
-    if (items >= (1LL << 31) - sms) return cudaErrorInvalidValue;
-    tp.items = (int)items;
+    if (items >= (1LL << 31)) return cudaErrorInvalidValue;
     tp.host_err = host_timeout_word();
     auto k = mode ? linattn_tc<true> : linattn_tc<false>;
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
-    k<<<(unsigned)(items < sms ? items : sms), kThreads, kSmem, stream>>>(tp, maps);
+    k<<<(unsigned)items, kThreads, kSmem, stream>>>(tp, maps);
     return cudaGetLastError();
 }
 
