@@ -177,29 +177,60 @@ __device__ __forceinline__ int granted_item(uint32_t slot) {
     return x;
 }
 
-// One item of a CTA's list: the columns of one job, of one head, of one range.
+// One item: 64 columns of one job, of one head, of one range.  The TMA warp
+// works it out, a chunk or more before the others need it, and leaves it in
+// shared memory: found by every role for itself, each change of item cost the
+// time of two or three chunks.
 struct Item {
-    LaRange rg;
-    int job, h, v0, nch;
-    bool cut, last, skip;
+    int seq, ridx, t0, len;        // sequence (nseq: rows of none), range, its rows
+    int job, h, v0, nch;           // nch < 0: no more items
+    int cut, last;
+    float a2, hi, lo;              // log2 of the decay; the decay over a chunk
+    int pad[3];
 };
+static_assert(sizeof(Item) == 64, "two slots of 64 bytes");
+
 template <bool kAgg>
-__device__ __noinline__ Item item_of(const TcParams& tp, int it) {
+__device__ __noinline__ void decode_item(const TcParams& tp, int it, Item* slot) {
     Item r;
-    __syncwarp();   // la_find is collective
     const int vb = it % tp.nvb;
     int x = it / tp.nvb;
     r.job = x % tp.p.njobs;
     x /= tp.p.njobs;
     r.h = x % tp.p.g.H;
-    r.rg = la_find(tp.p.g, x / tp.p.g.H);
+    r.ridx = x / tp.p.g.H;
+    const float a = tp.p.g.a[r.h];
+    const LaRange rg = la_find(tp.p.g, r.ridx);
+    r.seq = rg.seq;
+    r.t0 = rg.t0;
+    r.len = rg.len;
     r.v0 = vb * kLaCols;
     const LaJob& jb = tp.p.job[r.job];
-    r.cut = tp.p.g.split && r.rg.n > 1;
-    r.last = jb.rev ? r.rg.r == 0 : r.rg.r == r.rg.n - 1;
-    r.skip = r.rg.seq < 0 || r.v0 >= jb.DV || (kAgg && (!r.cut || r.last || r.rg.seq == tp.p.g.nseq));
-    r.nch = r.skip || r.rg.seq == tp.p.g.nseq ? 0 : (r.rg.len + kC - 1) / kC;
-    return r;
+    r.cut = tp.p.g.split && rg.n > 1;
+    r.last = jb.rev ? rg.r == 0 : rg.r == rg.n - 1;
+    const bool none = rg.seq < 0 || r.v0 >= jb.DV || (kAgg && (!r.cut || r.last || rg.seq == tp.p.g.nseq));
+    r.nch = none || rg.seq == tp.p.g.nseq ? 0 : (rg.len + kC - 1) / kC;
+    if (none) r.seq = -1;
+    r.a2 = la_log2_decay(&a, 0);
+    la_decay_pow(&a, 0, kC, r.hi, r.lo);
+    r.pad[0] = r.pad[1] = r.pad[2] = 0;
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) *slot = r;
+    // the state that the item starts from, to L2
+    if (!kAgg && !none && rg.seq != tp.p.g.nseq) {
+        const int64_t elems = (int64_t)jb.DK * jb.DV;
+        const float* in = r.cut ? jb.agg + ((int64_t)r.ridx * tp.p.g.H + r.h) * elems
+                                : (jb.init ? jb.init + ((int64_t)rg.seq * tp.p.g.H + r.h) * elems : nullptr);
+        const int nv = min(kLaCols, jb.DV - r.v0);
+        const int rows = jb.sk == 1 ? nv : jb.DK, width = jb.sk == 1 ? jb.DK : nv, pitch = jb.sk == 1 ? jb.sv : jb.sk;
+        if (in != nullptr) {
+            in += (int64_t)r.v0 * jb.sv;
+            const int lines = (width + 31) / 32;
+            for (int e = lane; e < rows * lines; e += 32)
+                prefetch_l2(in + (int64_t)(e / lines) * pitch + (e % lines) * 32);
+        }
+    }
+    __syncwarp();
 }
 
 // One lane of a converged warp.  The compiler knows such a branch to be uniform
@@ -258,11 +289,13 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
     uint64_t* b_xdone = bars + 16;    // A X computed: the bf16 X may change (commit)
     uint64_t* b_odone = bars + 17;    // out computed (commit)
     uint64_t* b_ofree = bars + 18;    // out read (128)
-    uint64_t* b_ifull = bars + 19;    // [2] answer to an item request (tx)
-    uint64_t* b_ifree = bars + 21;    // [2] answer read (every warp that walks items)
-    uint32_t* holder = reinterpret_cast<uint32_t*>(bars + 23);
-    const uint32_t answers = smem_u32(bars + 24);   // [2] 16 bytes each
-    const uint32_t ptab = smem_u32(bars + 28);      // [128] fp32: column factors of P
+    uint64_t* b_answer = bars + 19;   // answer to an item request (tx)
+    uint64_t* b_iready = bars + 20;   // [2] item decoded (1)
+    uint64_t* b_ifree = bars + 22;    // [2] item read (every other warp that walks items)
+    uint32_t* holder = reinterpret_cast<uint32_t*>(bars + 24);
+    const uint32_t answer = smem_u32(bars + 26);    // 16 bytes
+    Item* items = reinterpret_cast<Item*>(bars + 28);   // [2]
+    const uint32_t ptab = smem_u32(bars + 44);      // [128] fp32: column factors of P
 
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
@@ -275,9 +308,10 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
             mbar_init(smem_u32(b_pready + s), 256);
         }
         for (int s = 0; s < 2; ++s) {
-            mbar_init(smem_u32(b_ifull + s), 1);
-            mbar_init(smem_u32(b_ifree + s), kAgg ? 18 : kThreads / 32);
+            mbar_init(smem_u32(b_iready + s), 1);
+            mbar_init(smem_u32(b_ifree + s), kAgg ? 17 : kThreads / 32 - 1);
         }
+        mbar_init(smem_u32(b_answer), 1);
         mbar_init(smem_u32(b_udone), 1);
         mbar_init(smem_u32(b_ufree), 256);
         mbar_init(smem_u32(b_vready), 256);
@@ -297,59 +331,82 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
     // every role walks the same items and counts chunks in c: barrier phases
     // follow from the count alone
     int c = 0, k_item = 0;
-    auto next_item = [&]() {
+    auto read_item = [&](Item& im) {
         const int slot = k_item & 1;
-        wait_on(smem_u32(b_ifull + slot), (k_item >> 1) & 1, err);
-        const int it = granted_item(answers + 16 * slot);
-        fence_proxy_async_smem();
+        wait_on(smem_u32(b_iready + slot), (k_item >> 1) & 1, err);
+        const uint32_t at = smem_u32(items) + slot * 64;
+        const uint4 q0 = lds128(at), q1 = lds128(at + 16), q2 = lds128(at + 32);
+        im.seq = q0.x; im.ridx = q0.y; im.t0 = q0.z; im.len = q0.w;
+        im.job = q1.x; im.h = q1.y; im.v0 = q1.z; im.nch = q1.w;
+        im.cut = q2.x; im.last = q2.y; im.a2 = __uint_as_float(q2.z); im.hi = __uint_as_float(q2.w);
+        im.lo = lds32(at + 48);
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(b_ifree + slot));
         ++k_item;
-        return it < 0 ? -1 : uniform(it);
+        return im.nch >= 0;
     };
+    Item im;
 
     if (warp == kTmaWarp) {
+        decode_item<kAgg>(tp, blockIdx.x, items);
+        if (lane == 0) mbar_arrive(smem_u32(b_iready));
 #pragma unroll 1
-        for (int it = blockIdx.x; it >= 0; it = next_item()) {
-            if (lane == 0) {   // the next item, while this one runs
-                const int slot = k_item & 1;
-                wait_on(smem_u32(b_ifree + slot), ((k_item >> 1) & 1) ^ 1, err);
-                mbar_arrive_expect_tx(smem_u32(b_ifull + slot), 16);
-                request_item(answers + 16 * slot, smem_u32(b_ifull + slot));
+        for (;; ++k_item) {
+            const uint32_t at = smem_u32(items) + (k_item & 1) * 64;
+            const uint4 q0 = lds128(at), q1 = lds128(at + 16);
+            const int t0 = uniform(q0.z), nch = uniform(q1.w), h = uniform(q1.y), v0 = uniform(q1.z);
+            if (nch < 0) break;
+            const int jn = uniform(q1.x);
+            const LaJob& jb = tp.p.job[jn];
+            const CUtensorMap* m = maps.m[jn];
+            const int ka = (jb.DK + 63) / 64, ha = h / jb.dA, hb = h / jb.dB, hc = h / jb.dC, rev = jb.rev;
+            if (elect_one()) {   // the next item, while this one runs
+                mbar_arrive_expect_tx(smem_u32(b_answer), 16);
+                request_item(answer, smem_u32(b_answer));
             }
-            const Item im = item_of<kAgg>(tp, it);
-            const LaJob& jb = tp.p.job[im.job];
-            if (lane == 0) {
-                const int ka = (jb.DK + 63) / 64;
-                const CUtensorMap* m = maps.m[im.job];
-                const int ha = im.h / jb.dA, hb = im.h / jb.dB, hc = im.h / jb.dC;
+            // the first chunk's loads, then the next item's decoding, then the rest
 #pragma unroll 1
-                for (int x = 0; x < im.nch; ++x, ++c) {
-                    const int s = c & 1, t = im.rg.t0 + (jb.rev ? im.nch - 1 - x : x) * kC;
-                    const uint32_t free = ((c >> 1) & 1) ^ 1, st = smem_u32(smem + s * kStage);
-                    const uint32_t fab = smem_u32(b_fab + s), fc = smem_u32(b_fc + s);
-                    wait_on(smem_u32(b_eab + s), free, err);
-                    mbar_arrive_expect_tx(fab, (kAgg ? 1 : 2) * ka * kAtom);
-                    for (int a = 0; a < ka; ++a) {
-                        if (!kAgg) tma_load_3d(st + a * kAtom, m + 0, fab, a * 64, ha, t);
-                        tma_load_3d(st + (2 + a) * kAtom, m + 1, fab, a * 64, hb, t);
+            for (int part = 0; part < 2; ++part) {
+                if (elect_one()) {
+#pragma unroll 1
+                    for (int x = part; x < (part == 0 ? min(nch, 1) : nch); ++x) {
+                        const int cc = c + x, s = cc & 1, t = t0 + (rev ? nch - 1 - x : x) * kC;
+                        const uint32_t free = ((cc >> 1) & 1) ^ 1, st = smem_u32(smem) + s * kStage;
+                        const uint32_t fab = smem_u32(b_fab + s), fc = smem_u32(b_fc + s);
+                        mbar_wait(smem_u32(b_eab + s), free, err, 1u);
+                        mbar_arrive_expect_tx(fab, (kAgg ? 1 : 2) * ka * kAtom);
+                        for (int a = 0; a < ka; ++a) {
+                            if (!kAgg) tma_load_3d(st + a * kAtom, m + 0, fab, a * 64, ha, t);
+                            tma_load_3d(st + (2 + a) * kAtom, m + 1, fab, a * 64, hb, t);
+                        }
+                        mbar_wait(smem_u32(b_ec + s), free, err, 1u);
+                        mbar_arrive_expect_tx(fc, kAtom);
+                        tma_load_3d(st + 4 * kAtom, m + 2, fc, v0, hc, t);
                     }
-                    wait_on(smem_u32(b_ec + s), free, err);
-                    mbar_arrive_expect_tx(fc, kAtom);
-                    tma_load_3d(st + 4 * kAtom, m + 2, fc, im.v0, hc, t);
+                }
+                __syncwarp();
+                if (part == 0) {
+                    const int slot = (k_item + 1) & 1;
+                    wait_on(smem_u32(b_answer), k_item & 1, err);
+                    const int it = uniform(granted_item(answer));
+                    fence_proxy_async_smem();
+                    wait_on(smem_u32(b_ifree + slot), (((k_item + 1) >> 1) & 1) ^ 1, err);
+                    if (it >= 0) decode_item<kAgg>(tp, it, items + slot);
+                    else if (lane == 0) items[slot].nch = -1;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(b_iready + slot));
                 }
             }
-            __syncwarp();
+            c += nch;
         }
     } else if (warp == kMmaWarp) {
         constexpr uint32_t kIdW = make_idesc(1, 128, 128, 0, 0);
         constexpr uint32_t kIdO = make_idesc(1, 128, 64, 0, 1);
         constexpr uint32_t kIdU = make_idesc(1, 128, 64 * kTerms, 1, 1);
 #pragma unroll 1
-        for (int it = blockIdx.x; it >= 0; it = next_item()) {
-            const Item im = item_of<kAgg>(tp, it);
+        while (read_item(im)) {
             const int nch = uniform(im.nch), ks = uniform(tp.p.job[im.job].DK / 16);
-            const int fac = uniform(factored(la_log2_decay(g.a, im.h)) ? 1 : 0);
+            const int fac = uniform(factored(im.a2) ? 1 : 0);
             if (elect_one()) {
                 // x = -1: the W of the item's first chunk
 #pragma unroll 1
@@ -421,11 +478,10 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
             const int quad = warp & 3, row = quad * 32 + lane;
             const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
 #pragma unroll 1
-            for (int it = blockIdx.x; it >= 0; it = next_item()) {
-                const Item im = item_of<kAgg>(tp, it);
+            while (read_item(im)) {
                 if (im.nch == 0) continue;
                 const LaJob& jb = tp.p.job[im.job];
-                const float a2 = la_log2_decay(g.a, im.h);
+                const float a2 = im.a2;
                 const bool fac = factored(a2);
                 bar_p();                        // the table's last readers are done
                 // factored: lam^{-j'} s_in; exact: lam^j (the first 32 are used) and,
@@ -437,7 +493,7 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
 #pragma unroll 1
                 for (int x = 0; x < im.nch; ++x, ++c) {
                     const int s = c & 1, ci = jb.rev ? im.nch - 1 - x : x;
-                    const int n = min(kC, im.rg.len - ci * kC);
+                    const int n = min(kC, im.len - ci * kC);
                     wait_on(smem_u32(b_wdone + s), (c >> 1) & 1, err);
                     tc_fence_after();
                     const uint32_t base = tmem + lane_off + kW + s * 128;
@@ -512,14 +568,13 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
 
         const int row = (warp & 3) * 32 + lane, ch0 = warp < 12 ? 0 : 4;   // half of the row's columns
 #pragma unroll 1
-        for (int it = blockIdx.x; it >= 0; it = next_item()) {
-            const Item im = item_of<kAgg>(tp, it);
+        while (read_item(im)) {
             const LaJob& jb = tp.p.job[im.job];
-            const float a2 = la_log2_decay(g.a, im.h);
+            const float a2 = im.a2;
 #pragma unroll 1
             for (int x = 0; x < im.nch; ++x, ++c) {
                 const int s = c & 1, ci = jb.rev ? im.nch - 1 - x : x;
-                const int n = min(kC, im.rg.len - ci * kC);
+                const int n = min(kC, im.len - ci * kC);
                 const float w = la_exp2(a2, jb.rev ? row + 1 : max(n - 1 - row, 0)) * jb.s_in;
                 const f32x2 w2 = pair(w, w);
                 wait_on(smem_u32(b_fc + s), (c >> 1) & 1, err);
@@ -573,17 +628,14 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
         const int vc = warp < 20 ? 0 : 32;              // X's columns: 32 a thread
         const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
 #pragma unroll 1
-        for (int it = blockIdx.x; it >= 0; it = next_item()) {
-            const Item im = item_of<kAgg>(tp, it);
-            if (im.skip || im.rg.seq == g.nseq) continue;
+        while (read_item(im)) {
+            if (im.seq < 0 || im.seq == g.nseq) continue;
             const LaJob& jb = tp.p.job[im.job];
             const int nv = min(kLaCols, jb.DV - im.v0) - vc;
             const int64_t elems = (int64_t)jb.DK * jb.DV;
             const int64_t at = (int64_t)k * jb.sk + (int64_t)(im.v0 + vc) * jb.sv;
-            const int64_t so = ((int64_t)im.rg.seq * g.H + im.h) * elems + at;
-            // the range's number is the item's: item = ((range H + h) jobs + job) nvb + vb
-            const int ridx = it / tp.nvb / tp.p.njobs / g.H;
-            float* ag = im.cut ? jb.agg + ((int64_t)ridx * g.H + im.h) * elems + at : nullptr;
+            const int64_t so = ((int64_t)im.seq * g.H + im.h) * elems + at;
+            float* ag = im.cut ? jb.agg + ((int64_t)im.ridx * g.H + im.h) * elems + at : nullptr;
             const float* in = kAgg ? nullptr : (im.cut ? ag : (jb.init ? jb.init + so : nullptr));
             f32x2 X[16];
 #pragma unroll
@@ -591,14 +643,12 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                 const bool ok = in != nullptr && k < jb.DK && 2 * v < nv;
                 X[v] = pair(ok ? in[(int64_t)(2 * v) * jb.sv] : 0.f, ok ? in[(int64_t)(2 * v + 1) * jb.sv] : 0.f);
             }
-            const float a2 = la_log2_decay(g.a, im.h);
+            const float a2 = im.a2;
             const bool fac = factored(a2);
-            float f_hi, f_lo;
-            la_decay_pow(g.a, im.h, kC, f_hi, f_lo);
 #pragma unroll 1
             for (int x = 0; x < im.nch; ++x, ++c) {
                 const int s = c & 1, ci = jb.rev ? im.nch - 1 - x : x;
-                const int n = min(kC, im.rg.len - ci * kC);
+                const int n = min(kC, im.len - ci * kC);
                 if (!kAgg) {
                     // in the factored form the row factor of out is lam^{i'}
                     const float m = fac ? la_exp2(a2, jb.rev ? n - kC : 1) : 1.f;
@@ -612,7 +662,7 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                     fence_proxy_async_smem();
                     mbar_arrive(smem_u32(b_sready));
                 }
-                float hi = f_hi, lo = f_lo;
+                float hi = im.hi, lo = im.lo;
                 if (n < kC) la_decay_pow(g.a, im.h, n, hi, lo);
                 wait_on(smem_u32(b_udone), c & 1, err);
                 tc_fence_after();
@@ -655,28 +705,27 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
         const int i = (warp - 24) * 32 + lane;
         const uint32_t lane_off = (uint32_t)((warp - 24) * 32) << 16;
 #pragma unroll 1
-        for (int it = blockIdx.x; it >= 0; it = next_item()) {
-            const Item im = item_of<kAgg>(tp, it);
+        while (read_item(im)) {
             const LaJob& jb = tp.p.job[im.job];
             const int nv = min(kLaCols, jb.DV - im.v0);
             const int64_t os = (int64_t)g.H * jb.DV, oh = (int64_t)im.h * jb.DV + im.v0;
-            if (im.rg.seq == g.nseq && !im.skip) {       // tokens of no sequence: zeros
-                for (int x = i; x < im.rg.len * (nv / 16); x += 128) {
-                    const int64_t e = (int64_t)(im.rg.t0 + x / (nv / 16)) * os + oh + x % (nv / 16) * 16;
+            if (im.seq == g.nseq) {                   // tokens of no sequence: zeros
+                for (int x = i; x < im.len * (nv / 16); x += 128) {
+                    const int64_t e = (int64_t)(im.t0 + x / (nv / 16)) * os + oh + x % (nv / 16) * 16;
                     uint4* d = jb.out_f32 ? reinterpret_cast<uint4*>(static_cast<float*>(jb.out) + e)
                                           : reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(jb.out) + e);
                     for (int q = 0; q < (jb.out_f32 ? 4 : 2); ++q) d[q] = make_uint4(0u, 0u, 0u, 0u);
                 }
             }
-            const float a2 = la_log2_decay(g.a, im.h);
+            const float a2 = im.a2;
             const bool fac = factored(a2);
 #pragma unroll 1
             for (int x = 0; x < im.nch; ++x, ++c) {
                 const int ci = jb.rev ? im.nch - 1 - x : x;
-                const int n = min(kC, im.rg.len - ci * kC);
+                const int n = min(kC, im.len - ci * kC);
                 const float f = jb.s_out * (fac ? la_exp2(a2, jb.rev ? kC - 1 - i : i)
                                                 : exp2f(a2 * (float)(jb.rev ? n - 1 - i : i + 1)));
-                const int64_t e0 = (int64_t)(im.rg.t0 + ci * kC + i) * os + oh;
+                const int64_t e0 = (int64_t)(im.t0 + ci * kC + i) * os + oh;
                 wait_on(smem_u32(b_odone), c & 1, err);
                 tc_fence_after();
                 const f32x2 f2 = pair(f, f), s2 = pair(jb.s_out, jb.s_out);
