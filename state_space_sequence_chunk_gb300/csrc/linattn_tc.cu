@@ -5,13 +5,13 @@
 // 128 tokens.  With i, j the rows of a chunk (counted from its end when the walk
 // is backwards), n its tokens and X the state before it:
 //     W   = A B^T                                   128 x 128 x DK
-//     P   = s_in W o lam^{-j} [i >= j]              (bf16, tensor memory)
-//     out = s_out lam^i o (A (lam X) + P C)         128 x 64 x DK, 128 x 64 x 128
+//     P   = s_in W o lam^{64-j} [i >= j]            (bf16, tensor memory)
+//     out = s_out lam^{i-64} o (A (lam^65 X) + P C) 128 x 64 x DK, 128 x 64 x 128
 //     U   = B^T (s_in lam^{n-1-j} o C)              DK x 64 x 128
 //     X   <- lam^n X + U
 // (backwards X and U have decayed one step less and one more).  Rows and columns carry
 // the decay as separate factors, so that out is one accumulator and P costs one
-// product for each element; that is safe while lam^-127 <= 2^40.  For heads that
+// product for each element; that is safe while lam^127 >= 2^-120.  For heads that
 // forget faster the exact form runs: lam^{i-j} element by element, A X and P C
 // in two accumulators.
 // Every operand is read once per chain from HBM (a and b once per 64 columns of
@@ -55,14 +55,18 @@ constexpr int kRow = 128;                     // bytes of a tile row (64 columns
 constexpr int kAtom = kC * kRow;              // 16 KB: 128 rows of 64 columns
 constexpr int kThreads = 960;
 constexpr int kTmaWarp = 28, kMmaWarp = 29;
-constexpr int kStage = 5 * kAtom;             // A (2 atoms), B (2), C (1)
+constexpr int kStage = 4 * kAtom;             // A (2 atoms), B (2)
+constexpr int kCs = 3;                        // C tiles
 constexpr int kTerms = 3;
-constexpr int kSmem = 2 * kStage + kTerms * kAtom + kAtom + 1024 + 1024;
+constexpr int kTerm = kAtom / 2;              // a term of 64 tokens
+constexpr int kSmem = 2 * kStage + kCs * kAtom + kTerms * kTerm + kAtom + 1024;
 // tensor memory columns
 constexpr uint32_t kW = 0;                    // W / P, two buffers of 128
 constexpr uint32_t kO = 256, kU = 320;        // out; U's three terms
-// A head's decay over a chunk's 127 steps is at most 2^kSpan for the factored form.
-constexpr float kSpan = 40.f;
+// The factored form takes heads whose decay over a chunk's 127 steps is at least
+// 2^-kSpan: row and column factors, counted from the middle, are within 2^+-60.
+constexpr float kSpan = 120.f;
+constexpr int kMid = 64;
 
 struct TcParams {
     LaParams p;
@@ -70,7 +74,7 @@ struct TcParams {
     unsigned int* host_err;
 };
 struct TcMaps {
-    CUtensorMap m[3][3];   // job, operand (A, B, C)
+    CUtensorMap m[3][4];   // job, operand (A, B, C, out)
 };
 
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
@@ -133,12 +137,6 @@ __device__ __forceinline__ void sts32(uint32_t a, float v) {
     asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
 }
 __device__ __forceinline__ void bar_p() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
-__device__ __forceinline__ void st_v8(void* p, const uint32_t (&w)[8]) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
-                 "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                 : "memory");
-}
-
 // mbar_wait with its slow path out of line: the roles' loops share the
 // instruction cache.
 __device__ __noinline__ void wait_slow(uint32_t bar, uint32_t parity, unsigned int* err) {
@@ -273,48 +271,49 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
         }
         return;
     }
-    uint8_t* terms = smem + 2 * kStage;
-    uint8_t* xs = terms + kTerms * kAtom;
+    uint8_t* ctile = smem + 2 * kStage;
+    uint8_t* terms = ctile + kCs * kAtom;
+    uint8_t* xs = terms + kTerms * kTerm;
     uint64_t* bars = reinterpret_cast<uint64_t*>(xs + kAtom);
     uint64_t* b_fab = bars;           // [2] stage's A and B loaded (tx)
-    uint64_t* b_fc = bars + 2;        // [2] stage's C loaded (tx)
-    uint64_t* b_eab = bars + 4;       // [2] A and B read by every product (commit)
-    uint64_t* b_ec = bars + 6;        // [2] C read by every product (commit)
-    uint64_t* b_wdone = bars + 8;     // [2] W computed (commit)
-    uint64_t* b_pready = bars + 10;   // [2] P written (256)
-    uint64_t* b_udone = bars + 12;    // U computed, terms read (commit)
-    uint64_t* b_ufree = bars + 13;    // U read (256)
-    uint64_t* b_vready = bars + 14;   // terms written (256)
-    uint64_t* b_sready = bars + 15;   // bf16 X written (256)
-    uint64_t* b_xdone = bars + 16;    // A X computed: the bf16 X may change (commit)
-    uint64_t* b_odone = bars + 17;    // out computed (commit)
-    uint64_t* b_ofree = bars + 18;    // out read (128)
-    uint64_t* b_answer = bars + 19;   // answer to an item request (tx)
-    uint64_t* b_iready = bars + 20;   // [2] item decoded (1)
-    uint64_t* b_ifree = bars + 22;    // [2] item read (every other warp that walks items)
-    uint32_t* holder = reinterpret_cast<uint32_t*>(bars + 24);
-    const uint32_t answer = smem_u32(bars + 26);    // 16 bytes
-    Item* items = reinterpret_cast<Item*>(bars + 28);   // [2]
-    const uint32_t ptab = smem_u32(bars + 44);      // [128] fp32: column factors of P
+    uint64_t* b_eab = bars + 2;       // [2] A and B read by every product (commit)
+    uint64_t* b_fc = bars + 4;        // [3] C tile loaded (tx)
+    uint64_t* b_ec = bars + 7;        // [3] C read by every product, and out stored from it
+    uint64_t* b_wdone = bars + 10;    // [2] W computed (commit)
+    uint64_t* b_pready = bars + 12;   // [2] P written (256)
+    uint64_t* b_vready = bars + 14;   // [2] terms of a half of the tokens written (128)
+    uint64_t* b_udone = bars + 16;    // [2] U's half computed, its terms read (commit)
+    uint64_t* b_ufree = bars + 18;    // U read (256)
+    uint64_t* b_sready = bars + 19;   // bf16 X written (256)
+    uint64_t* b_xdone = bars + 20;    // A X computed: the bf16 X may change (commit)
+    uint64_t* b_odone = bars + 21;    // out computed (commit)
+    uint64_t* b_ofree = bars + 22;    // out read (128)
+    uint64_t* b_answer = bars + 23;   // answer to an item request (tx)
+    uint64_t* b_iready = bars + 24;   // [2] item decoded (1)
+    uint64_t* b_ifree = bars + 26;    // [2] item read (every other warp that walks items)
+    uint32_t* holder = reinterpret_cast<uint32_t*>(bars + 28);
+    const uint32_t answer = smem_u32(bars + 30);    // 16 bytes
+    Item* items = reinterpret_cast<Item*>(bars + 32);   // [2]
+    const uint32_t ptab = smem_u32(bars + 48);      // [128] fp32: column factors of P
 
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int s = 0; s < 2; ++s) {
             mbar_init(smem_u32(b_fab + s), 1);
-            mbar_init(smem_u32(b_fc + s), 1);
             mbar_init(smem_u32(b_eab + s), 1);
-            mbar_init(smem_u32(b_ec + s), 1);
             mbar_init(smem_u32(b_wdone + s), 1);
             mbar_init(smem_u32(b_pready + s), 256);
-        }
-        for (int s = 0; s < 2; ++s) {
+            mbar_init(smem_u32(b_vready + s), 128);
+            mbar_init(smem_u32(b_udone + s), 1);
             mbar_init(smem_u32(b_iready + s), 1);
             mbar_init(smem_u32(b_ifree + s), kAgg ? 17 : kThreads / 32 - 1);
         }
+        for (int s = 0; s < kCs; ++s) {
+            mbar_init(smem_u32(b_fc + s), 1);
+            mbar_init(smem_u32(b_ec + s), 1);
+        }
         mbar_init(smem_u32(b_answer), 1);
-        mbar_init(smem_u32(b_udone), 1);
         mbar_init(smem_u32(b_ufree), 256);
-        mbar_init(smem_u32(b_vready), 256);
         mbar_init(smem_u32(b_sready), 256);
         mbar_init(smem_u32(b_xdone), 1);
         mbar_init(smem_u32(b_odone), 1);
@@ -368,20 +367,28 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
 #pragma unroll 1
             for (int part = 0; part < 2; ++part) {
                 if (elect_one()) {
+                    // C tiles are three deep and go one chunk ahead of A and B: their
+                    // scaled terms take the longest to prepare
 #pragma unroll 1
-                    for (int x = part; x < (part == 0 ? min(nch, 1) : nch); ++x) {
-                        const int cc = c + x, s = cc & 1, t = t0 + (rev ? nch - 1 - x : x) * kC;
-                        const uint32_t free = ((cc >> 1) & 1) ^ 1, st = smem_u32(smem) + s * kStage;
-                        const uint32_t fab = smem_u32(b_fab + s), fc = smem_u32(b_fc + s);
-                        mbar_wait(smem_u32(b_eab + s), free, err, 1u);
-                        mbar_arrive_expect_tx(fab, (kAgg ? 1 : 2) * ka * kAtom);
-                        for (int a = 0; a < ka; ++a) {
-                            if (!kAgg) tma_load_3d(st + a * kAtom, m + 0, fab, a * 64, ha, t);
-                            tma_load_3d(st + (2 + a) * kAtom, m + 1, fab, a * 64, hb, t);
+                    for (int x = part == 0 ? -1 : 1; x < (part == 0 ? min(nch, 1) : nch); ++x) {
+                        const int cc = c + x, s = cc & 1;
+                        if (x >= 0) {
+                            const int t = t0 + (rev ? nch - 1 - x : x) * kC;
+                            const uint32_t st = smem_u32(smem) + s * kStage, fab = smem_u32(b_fab + s);
+                            mbar_wait(smem_u32(b_eab + s), ((cc >> 1) & 1) ^ 1, err, 1u);
+                            mbar_arrive_expect_tx(fab, (kAgg ? 1 : 2) * ka * kAtom);
+                            for (int a = 0; a < ka; ++a) {
+                                if (!kAgg) tma_load_3d(st + a * kAtom, m + 0, fab, a * 64, ha, t);
+                                tma_load_3d(st + (2 + a) * kAtom, m + 1, fab, a * 64, hb, t);
+                            }
                         }
-                        mbar_wait(smem_u32(b_ec + s), free, err, 1u);
-                        mbar_arrive_expect_tx(fc, kAtom);
-                        tma_load_3d(st + 4 * kAtom, m + 2, fc, v0, hc, t);
+                        if (x + 1 < nch) {
+                            const int t = t0 + (rev ? nch - 2 - x : x + 1) * kC, c1 = cc + 1, s3 = c1 % kCs;
+                            const uint32_t fc = smem_u32(b_fc) + 8 * s3;
+                            mbar_wait(smem_u32(b_ec) + 8 * s3, ((c1 / kCs) & 1) ^ 1, err, 1u);
+                            mbar_arrive_expect_tx(fc, kAtom);
+                            tma_load_3d(smem_u32(ctile) + s3 * kAtom, m + 2, fc, v0, hc, t);
+                        }
                     }
                 }
                 __syncwarp();
@@ -415,25 +422,7 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                     const uint32_t st = smem_u32(smem) + s * kStage;
                     const int s1 = s ^ 1, use1 = (cc + 1) >> 1;
                     const uint32_t st1 = smem_u32(smem) + s1 * kStage;
-                    // W of the next chunk goes first, if its tiles are there (and the exact
-                    // form does not hold its buffer): P is then built a chunk ahead, and
-                    // the tensor pipe has work while the last out is read.
                     bool w_due = !kAgg && x + 1 < nch;
-                    if (x >= 0) {
-                        if (kAgg) mbar_wait(smem_u32(b_fab + s), use & 1, err, 1u);
-                        // U = B^T (scaled C), its three terms side by side: B is read once
-                        mbar_wait(smem_u32(b_vready), cc & 1, err, 1u);
-                        mbar_wait(smem_u32(b_ufree), (cc & 1) ^ 1, err, 1u);
-                        tc_fence_after();
-                        mma_steps<false, false>(tmem + kU, smem_desc_sw128(st + 2 * kAtom, kAtom, 8 * kRow),
-                                                smem_desc_sw128(smem_u32(terms), kAtom, 8 * kRow), 8, kIdU);
-                        mma_commit(smem_u32(b_udone));
-                        if (kAgg) {
-                            mma_commit(smem_u32(b_eab + s));
-                            mma_commit(smem_u32(b_ec + s));
-                        }
-                    }
-                    if (kAgg) continue;
                     const auto w_product = [&]() {
                         w_due = false;
                         mbar_wait(smem_u32(b_fab + s1), use1 & 1, err, 1u);
@@ -442,8 +431,39 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                                               smem_desc_sw128(st1 + 2 * kAtom, 16, 8 * kRow), ks, kIdW);
                         mma_commit(smem_u32(b_wdone + s1));
                     };
+                    const auto u_half = [&](int half) {
+                        const uint64_t ad = smem_desc_sw128(st + 2 * kAtom + half * kTerm, kAtom, 8 * kRow);
+                        const uint64_t bd = smem_desc_sw128(smem_u32(terms), kTerm, 8 * kRow);
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk) {
+                            const uint32_t o = (uint32_t)(kk * 16 * kRow) >> 4;
+                            mma_f16_ss(tmem + kU, ad + o, bd + o, kIdU, half + kk > 0 ? 1u : 0u);
+                        }
+                    };
                     if (x >= 0) {
+                        if (kAgg) mbar_wait(smem_u32(b_fab + s), use & 1, err, 1u);
+                        // U = B^T (scaled C), its three terms side by side: B is read once
+                        mbar_wait(smem_u32(b_vready), cc & 1, err, 1u);
+                        mbar_wait(smem_u32(b_ufree), (cc & 1) ^ 1, err, 1u);
+                        tc_fence_after();
+                        u_half(0);
+                        mma_commit(smem_u32(b_udone));
+                        // W of the next chunk goes before the rest, if its tiles are there
+                        // (and the exact form does not hold its buffer): P is then built a
+                        // chunk ahead, and the tensor pipe has work while the last out is
+                        // read
                         if (w_due && fac && mbar_try_wait(smem_u32(b_fab + s1), use1 & 1)) w_product();
+                        mbar_wait(smem_u32(b_vready + 1), cc & 1, err, 1u);
+                        tc_fence_after();
+                        u_half(1);
+                        mma_commit(smem_u32(b_udone + 1));
+                        if (kAgg) {
+                            mma_commit(smem_u32(b_eab + s));
+                            mma_commit(smem_u32(b_ec) + 8 * (cc % kCs));
+                        }
+                    }
+                    if (kAgg) continue;
+                    if (x >= 0) {
                         // out = A X
                         mbar_wait(smem_u32(b_sready), cc & 1, err, 1u);
                         mbar_wait(smem_u32(b_ofree), (cc & 1) ^ 1, err, 1u);
@@ -453,10 +473,10 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                         mma_commit(smem_u32(b_xdone));
                         mma_commit(smem_u32(b_eab + s));
                         // out += P C; in the exact form, beside P's columns in W's buffer
-                        mbar_wait(smem_u32(b_fc + s), use & 1, err, 1u);
+                        mbar_wait(smem_u32(b_fc) + 8 * (cc % kCs), (cc / kCs) & 1, err, 1u);
                         mbar_wait(smem_u32(b_pready + s), use & 1, err, 1u);
                         tc_fence_after();
-                        const uint64_t bd = smem_desc_sw128(st + 4 * kAtom, 8 * kRow, 8 * kRow);
+                        const uint64_t bd = smem_desc_sw128(smem_u32(ctile) + (cc % kCs) * kAtom, 8 * kRow, 8 * kRow);
                         const uint32_t to = tmem + (fac ? kO : kW + s * 128 + 64);
                         const uint32_t pa = tmem + kW + s * 128, pb = pa + (fac ? 32 : 0);
 #pragma unroll
@@ -464,7 +484,6 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                             mma_f16_ts(to, (kk < 4 ? pa : pb) + kk * 8, bd + (uint64_t)((kk * 16 * kRow) >> 4),
                                        kIdO, kk > 0 ? 1u : (uint32_t)fac);
                         mma_commit(smem_u32(b_odone));
-                        mma_commit(smem_u32(b_ec + s));
                     }
                     if (w_due) w_product();
                 }
@@ -484,9 +503,9 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                 const float a2 = im.a2;
                 const bool fac = factored(a2);
                 bar_p();                        // the table's last readers are done
-                // factored: lam^{-j'} s_in; exact: lam^j (the first 32 are used) and,
+                // factored: lam^{mid-j'} s_in; exact: lam^j (the first 32 are used) and,
                 // from 32 on, lam^{31-j}
-                if (warp < 4) sts32(ptab + 4 * row, fac ? la_exp2(-a2, jb.rev ? kC - 1 - row : row) * jb.s_in
+                if (warp < 4) sts32(ptab + 4 * row, fac ? la_exp2(a2, kMid - (jb.rev ? kC - 1 - row : row)) * jb.s_in
                                           : exp2f(a2 * (float)(row < 32 ? row : max(63 - row, 0))));
                 bar_p();
                 const uint32_t vt = jb.rev ? ptab : ptab + 32 * 4;
@@ -566,7 +585,8 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
     } else if (warp < 16) {
         // ===================== scaled terms of C =====================
 
-        const int row = (warp & 3) * 32 + lane, ch0 = warp < 12 ? 0 : 4;   // half of the row's columns
+        // a warpgroup has half of the tokens, a thread half of a token's columns
+        const int half = warp >= 12, row = half * 64 + (threadIdx.x & 63), ch0 = threadIdx.x & 64 ? 4 : 0;
 #pragma unroll 1
         while (read_item(im)) {
             const LaJob& jb = tp.p.job[im.job];
@@ -577,14 +597,15 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                 const int n = min(kC, im.len - ci * kC);
                 const float w = la_exp2(a2, jb.rev ? row + 1 : max(n - 1 - row, 0)) * jb.s_in;
                 const f32x2 w2 = pair(w, w);
-                wait_on(smem_u32(b_fc + s), (c >> 1) & 1, err);
-                const uint32_t st = smem_u32(smem + s * kStage), tm = smem_u32(terms);
+                wait_on(smem_u32(b_fc) + 8 * (c % kCs), (c / kCs) & 1, err);
+                const uint32_t st = smem_u32(smem) + s * kStage, tm = smem_u32(terms) - half * kTerm;
+                const uint32_t ct = smem_u32(ctile) + (c % kCs) * kAtom;
                 // the terms of this thread's 32 columns are ready in registers when the
                 // last U lets go of their tiles; a row of other tokens gives zeros
                 uint32_t t[4][kTerms][4];
 #pragma unroll
                 for (int ch = 0; ch < 4; ++ch) {
-                    const uint4 q = lds128(st + 4 * kAtom + row * kRow + (((ch0 + ch) ^ (row & 7)) << 4));
+                    const uint4 q = lds128(ct + row * kRow + (((ch0 + ch) ^ (row & 7)) << 4));
                     const uint32_t in[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
@@ -606,19 +627,25 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                     if (row >= n) {   // nothing of such a row may reach a product
 #pragma unroll 1
                         for (int ch = ch0; ch < ch0 + 4; ++ch)
-#pragma unroll
-                            for (int q = 2; q < 5; ++q) sts128(st + q * kAtom + row * kRow + (ch << 4), 0u, 0u, 0u, 0u);
+{
+                            const int at = row * kRow + (ch << 4);
+                            sts128(st + 2 * kAtom + at, 0u, 0u, 0u, 0u);
+                            sts128(st + 3 * kAtom + at, 0u, 0u, 0u, 0u);
+                            sts128(ct + at, 0u, 0u, 0u, 0u);
+                        }
                     }
                 }
-                if (c > 0) wait_on(smem_u32(b_udone), (c - 1) & 1, err);
+                // the halves take turns in the same tiles
+                if (half) wait_on(smem_u32(b_udone), c & 1, err);
+                else if (c > 0) wait_on(smem_u32(b_udone + 1), (c - 1) & 1, err);
 #pragma unroll
                 for (int ch = 0; ch < 4; ++ch)
 #pragma unroll
                     for (int y = 0; y < kTerms; ++y)
-                        sts128(tm + y * kAtom + row * kRow + (((ch0 + ch) ^ (row & 7)) << 4),
+                        sts128(tm + y * kTerm + row * kRow + (((ch0 + ch) ^ (row & 7)) << 4),
                                t[ch][y][0], t[ch][y][1], t[ch][y][2], t[ch][y][3]);
                 fence_proxy_async_smem();
-                mbar_arrive(smem_u32(b_vready));
+                mbar_arrive(smem_u32(b_vready + half));
             }
         }
     } else if (warp < 24) {
@@ -651,7 +678,7 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                 const int n = min(kC, im.len - ci * kC);
                 if (!kAgg) {
                     // in the factored form the row factor of out is lam^{i'}
-                    const float m = fac ? la_exp2(a2, jb.rev ? n - kC : 1) : 1.f;
+                    const float m = fac ? la_exp2(a2, (jb.rev ? n - kC : 1) + kMid) : 1.f;
                     const f32x2 m2 = pair(m, m);
                     if (c > 0) wait_on(smem_u32(b_xdone), (c - 1) & 1, err);
 #pragma unroll
@@ -664,7 +691,7 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                 }
                 float hi = im.hi, lo = im.lo;
                 if (n < kC) la_decay_pow(g.a, im.h, n, hi, lo);
-                wait_on(smem_u32(b_udone), c & 1, err);
+                wait_on(smem_u32(b_udone + 1), c & 1, err);
                 tc_fence_after();
                 const f32x2 hi2 = pair(hi, hi), lo2 = pair(lo, lo);
 #pragma unroll
@@ -723,12 +750,19 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
             for (int x = 0; x < im.nch; ++x, ++c) {
                 const int ci = jb.rev ? im.nch - 1 - x : x;
                 const int n = min(kC, im.len - ci * kC);
-                const float f = jb.s_out * (fac ? la_exp2(a2, jb.rev ? kC - 1 - i : i)
+                const float f = jb.s_out * (fac ? la_exp2(a2, (jb.rev ? kC - 1 - i : i) - kMid)
                                                 : exp2f(a2 * (float)(jb.rev ? n - 1 - i : i + 1)));
                 const int64_t e0 = (int64_t)(im.t0 + ci * kC + i) * os + oh;
                 wait_on(smem_u32(b_odone), c & 1, err);
                 tc_fence_after();
                 const f32x2 f2 = pair(f, f), s2 = pair(jb.s_out, jb.s_out);
+                // A full chunk's bf16 rows go out by TMA from the chunk's C tile, which
+                // nothing reads any more: stored from registers, a row to a thread, they
+                // took a fifth of the shared-memory and L1 data path that bounds the
+                // kernel.  The rows behind a ragged chunk's belong to others, so that
+                // one is stored row by row.
+                const bool tile = n == kC && !jb.out_f32;
+                const uint32_t ct = smem_u32(ctile) + (c % kCs) * kAtom;
 #pragma unroll 1
                 for (int b = 0; b < 4; ++b) {   // 16 columns at a time
                     uint32_t p[16];
@@ -748,27 +782,38 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                         tc_fence_before();
                         mbar_arrive(smem_u32(b_ofree));
                     }
-                    if (i < n && b * 16 < nv) {
+                    uint32_t w[8];
+#pragma unroll
+                    for (int y = 0; y < 8; ++y) w[y] = pack2(r[y]);
+                    if (tile) {
+                        sts128(ct + i * kRow + (((2 * b) ^ (i & 7)) << 4), w[0], w[1], w[2], w[3]);
+                        sts128(ct + i * kRow + (((2 * b + 1) ^ (i & 7)) << 4), w[4], w[5], w[6], w[7]);
+                    } else if (i < n && b * 16 < nv) {
                         if (jb.out_f32) {
                             ulonglong2* d = reinterpret_cast<ulonglong2*>(static_cast<float*>(jb.out) + e0 + b * 16);
 #pragma unroll
                             for (int y = 0; y < 4; ++y) d[y] = make_ulonglong2(r[2 * y], r[2 * y + 1]);
                         } else {
-                            uint32_t w[8];
-#pragma unroll
-                            for (int y = 0; y < 8; ++y) w[y] = pack2(r[y]);
-                            __nv_bfloat16* d = static_cast<__nv_bfloat16*>(jb.out) + e0 + b * 16;
-                            if ((reinterpret_cast<uintptr_t>(d) & 31) == 0) {
-                                st_v8(d, w);
-                            } else {
-                                reinterpret_cast<uint4*>(d)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-                                reinterpret_cast<uint4*>(d)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-                            }
+                            uint4* d = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(jb.out) + e0 + b * 16);
+                            d[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                            d[1] = make_uint4(w[4], w[5], w[6], w[7]);
                         }
                     }
                 }
+                if (tile) fence_proxy_async_smem();
+                asm volatile("bar.sync 2, 128;" ::: "memory");
+                if (warp == 24 && lane == 0) {
+                    if (tile) {
+                        tma_store_3d(maps.m[im.job] + 3, ct, im.v0, im.h, im.t0 + ci * kC);
+                        bulk_commit_group();
+                        bulk_wait_group_read0();
+                    }
+                    mbar_arrive(smem_u32(b_ec) + 8 * (c % kCs));
+                }
+                __syncwarp();
             }
         }
+        if (warp == 24 && lane == 0) bulk_wait_group0();
     }
     tc_fence_before();
     __syncthreads();
@@ -802,7 +847,8 @@ cudaError_t launch_linattn_tc(const LaParams& p, int mode, cudaStream_t stream) 
         tp.nvb = n > tp.nvb ? n : tp.nvb;
         if (p.g.T > 0 && (!encode(&maps.m[j][0], b.A, b.DK, b.hA, b.sA, p.g.T) ||
                           !encode(&maps.m[j][1], b.B, b.DK, b.hB, b.sB, p.g.T) ||
-                          !encode(&maps.m[j][2], b.C, b.DV, b.hC, b.sC, p.g.T)))
+                          !encode(&maps.m[j][2], b.C, b.DV, b.hC, b.sC, p.g.T) ||
+                          (!b.out_f32 && !encode(&maps.m[j][3], b.out, b.DV, p.g.H, (int64_t)p.g.H * b.DV, p.g.T))))
             return cudaErrorInvalidValue;
     }
     const int64_t items = (int64_t)p.g.range_cap * p.g.H * p.njobs * tp.nvb;
