@@ -420,36 +420,58 @@ def ssd_fwd_noalloc(x, dt, A, B, C, D=None, init_state=None, chunk_size: int = 2
     return y, final_out
 
 
+# The calls below are often made for a single token, where the host's work is
+# most of their time: pointers go as plain integers, and a contiguous tensor's
+# rows need no further look.
+_DTYPE_CODE = {torch.bfloat16: SSD_BF16, torch.float32: SSD_F32}
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_int() -> int:
+    if _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
+    return torch.cuda.current_stream().cuda_stream
+
+
 def _dtype_code(t: torch.Tensor, name: str) -> int:
-    if t.dtype == torch.bfloat16:
-        return SSD_BF16
-    if t.dtype == torch.float32:
-        return SSD_F32
-    raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+    code = _DTYPE_CODE.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+    return code
 
 
 def _typed(t, name: str, dtype, shape):
     """t, checked: None passes, else dtype and shape have to be these."""
-    if t is None:
-        return None
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if t is not None:
+        if t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     return t
 
 
-def _row_ptr(t, inner: int):
-    """Pointer and row stride of a tensor [rows, ...] whose rows are contiguous
+def _addr(t):
+    """Address of a contiguous CUDA tensor (None passes)."""
+    if t is None:
+        return None
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError("tensors must be contiguous CUDA tensors")
+    return t.data_ptr()
+
+
+def _rows(t, inner: int):
+    """Address and row stride of a tensor [rows, ...] whose rows are contiguous
     (`inner` elements each) and evenly spaced."""
     if not t.is_cuda:
         raise ValueError("tensors must be CUDA tensors")
+    if t.is_contiguous():
+        return t.data_ptr(), inner
     want = 1
     for n, s in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
         if n != 1 and s != want:
             raise ValueError("each row (all dimensions but the first) must be contiguous")
         want *= n
-    return ctypes.c_void_p(t.data_ptr()), (t.stride(0) if t.shape[0] > 1 else inner)
+    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else inner)
 
 
 def _linattn_dims(q, k, v, log_decay, nseqs, max_seqlen):
@@ -457,12 +479,13 @@ def _linattn_dims(q, k, v, log_decay, nseqs, max_seqlen):
         raise ValueError("q and k must be [tokens, G, K] and v [tokens, H, V]")
     T, G, K = q.shape
     H, V = v.shape[1:]
-    _typed(k, "k", q.dtype, (T, G, K))
-    _typed(v, "v", q.dtype, (T, H, V))
+    dt = q.dtype
+    _typed(k, "k", dt, (T, G, K))
+    _typed(v, "v", dt, (T, H, V))
     _typed(log_decay, "log_decay", torch.float32, (H,))
-    (qp, qs), (kp, ks), (vp, vs) = _row_ptr(q, G * K), _row_ptr(k, G * K), _row_ptr(v, H * V)
-    d = LinattnDims(nseqs, T, H, G, K, V, qs, ks, vs, int(max_seqlen), _dtype_code(q, "q"), 0)
-    return d, (qp, kp, vp)
+    (qp, qs), (kp, ks), (vp, vs) = _rows(q, G * K), _rows(k, G * K), _rows(v, H * V)
+    d = LinattnDims(nseqs, T, H, G, K, V, qs, ks, vs, max_seqlen, _dtype_code(q, "q"), 0)
+    return d, qp, kp, vp
 
 
 def _linattn_nseqs(cu_seqlens, nseqs):
@@ -494,9 +517,9 @@ def linattn_fwd(q, k, v, log_decay, cu_seqlens=None, scale: float = None, init_s
     preparations for long sequences where there are none.
     Returns ``(o [tokens, H, V], final_state [nseqs, H, V, K] float32 or None)``.
     """
-    lib = load_library()
+    lib = _lib or load_library()
     n = _linattn_nseqs(cu_seqlens, nseqs)
-    d, (qp, kp, vp) = _linattn_dims(q, k, v, log_decay, n, max_seqlen)
+    d, qp, kp, vp = _linattn_dims(q, k, v, log_decay, n, max_seqlen)
     T, H, V = v.shape
     K = q.shape[2]
     _typed(init_state, "init_state", torch.float32, (n, H, V, K))
@@ -509,9 +532,9 @@ def linattn_fwd(q, k, v, log_decay, cu_seqlens=None, scale: float = None, init_s
         if fin is None:
             fin = torch.empty((n, H, V, K), dtype=torch.float32, device=q.device)
     workspace, nbytes = _linattn_workspace(lib, d, 0, workspace, q.device)
-    _check(lib.ssd_linattn_fwd(ctypes.byref(d), qp, kp, vp, _ptr(log_decay),
-                               K ** -0.5 if scale is None else float(scale), _ptr(cu_seqlens),
-                               _ptr(init_state), _ptr(o), _ptr(fin), _ptr(workspace), nbytes, _stream()))
+    _check(lib.ssd_linattn_fwd(ctypes.byref(d), qp, kp, vp, _addr(log_decay),
+                               K ** -0.5 if scale is None else float(scale), _addr(cu_seqlens),
+                               _addr(init_state), _addr(o), _addr(fin), _addr(workspace), nbytes, _stream_int()))
     return o, fin
 
 
@@ -519,9 +542,9 @@ def linattn_bwd(q, k, v, dout, log_decay, cu_seqlens=None, scale: float = None, 
                 dfinal_state=None, nseqs: int = 1, max_seqlen: int = 0, workspace=None):
     """The gradient of linattn_fwd from dout [tokens, H, V] and dfinal_state (None: 0).
     Returns ``(dq, dk, dv, dinit_state)``; dinit_state is None without an init_state."""
-    lib = load_library()
+    lib = _lib or load_library()
     n = _linattn_nseqs(cu_seqlens, nseqs)
-    d, (qp, kp, vp) = _linattn_dims(q, k, v, log_decay, n, max_seqlen)
+    d, qp, kp, vp = _linattn_dims(q, k, v, log_decay, n, max_seqlen)
     T, H, V = v.shape
     K = q.shape[2]
     _typed(dout, "dout", q.dtype, (T, H, V))
@@ -531,10 +554,10 @@ def linattn_bwd(q, k, v, dout, log_decay, cu_seqlens=None, scale: float = None, 
     dq, dk, dv = new(q.shape, q.dtype), new(k.shape, q.dtype), new(v.shape, q.dtype)
     d0 = None if init_state is None else new((n, H, V, K), torch.float32)
     workspace, nbytes = _linattn_workspace(lib, d, 1, workspace, q.device)
-    _check(lib.ssd_linattn_bwd(ctypes.byref(d), qp, kp, vp, _ptr(dout), _ptr(log_decay),
-                               K ** -0.5 if scale is None else float(scale), _ptr(cu_seqlens),
-                               _ptr(init_state), _ptr(dfinal_state), _ptr(dq), _ptr(dk), _ptr(dv),
-                               _ptr(d0), _ptr(workspace), nbytes, _stream()))
+    _check(lib.ssd_linattn_bwd(ctypes.byref(d), qp, kp, vp, _addr(dout), _addr(log_decay),
+                               K ** -0.5 if scale is None else float(scale), _addr(cu_seqlens),
+                               _addr(init_state), _addr(dfinal_state), _addr(dq), _addr(dk), _addr(dv),
+                               _addr(d0), _addr(workspace), nbytes, _stream_int()))
     return dq, dk, dv, d0
 
 
@@ -544,8 +567,8 @@ def linattn_step(q, k, v, log_decay, cache, slots=None, scale: float = None, out
     in place; ``slots`` [b] int32 says which is whose (row b's slot is b without it;
     a negative one marks a row without a stream, whose output is 0).
     Returns o [b, H, V]."""
-    lib = load_library()
-    d, (qp, kp, vp) = _linattn_dims(q, k, v, log_decay, q.shape[0], 0)
+    lib = _lib or load_library()
+    d, qp, kp, vp = _linattn_dims(q, k, v, log_decay, q.shape[0], 0)
     b, H, V = v.shape
     K = q.shape[2]
     _typed(cache, "cache", torch.float32, (cache.shape[0], H, V, K))
@@ -553,9 +576,9 @@ def linattn_step(q, k, v, log_decay, cache, slots=None, scale: float = None, out
     o = _typed(out, "out", q.dtype, (b, H, V))
     if o is None:
         o = torch.empty((b, H, V), dtype=q.dtype, device=q.device)
-    _check(lib.ssd_linattn_step(ctypes.byref(d), qp, kp, vp, _ptr(log_decay),
-                                K ** -0.5 if scale is None else float(scale), _ptr(slots), _ptr(cache),
-                                cache.shape[0], _ptr(o), _stream()))
+    _check(lib.ssd_linattn_step(ctypes.byref(d), qp, kp, vp, _addr(log_decay),
+                                K ** -0.5 if scale is None else float(scale), _addr(slots), _addr(cache),
+                                cache.shape[0], _addr(o), _stream_int()))
     return o
 
 
@@ -572,8 +595,8 @@ def _norm_dims(r, y, z, w_post, alpha, w_pre, gate, ngroups, eps):
     _typed(z, "z", y.dtype, (T, D))
     for name, w in (("w_post", w_post), ("alpha", alpha), ("w_pre", w_pre)):
         _typed(w, name, torch.float32, (D,))
-    yp, ys = _row_ptr(y, D)
-    zp, zs = (None, 0) if z is None or gate is None else _row_ptr(z, D)
+    yp, ys = _rows(y, D)
+    zp, zs = (None, 0) if z is None or gate is None else _rows(z, D)
     d = NormDims(T, D, int(ngroups), ys, zs, GATES[gate], float(eps), _dtype_code(y, "y"),
                  _dtype_code(r, "r"), 0)
     return d, yp, zp
@@ -590,7 +613,7 @@ def block_norm_fwd(r, y, w_pre, z=None, w_post=None, alpha=None, gate=None, ngro
     bfloat16.  The weights are float32 [width].  Rows of y and z may be slices.
     ``r_out`` may be r.  Returns ``(r_out, n)``, with ``return_rstd`` also the pair
     of factors that block_norm_bwd needs."""
-    lib = load_library()
+    lib = _lib or load_library()
     d, yp, zp = _norm_dims(r, y, z, w_post, alpha, w_pre, gate, ngroups, eps)
     T, D = y.shape
     ro = _typed(r_out, "r_out", r.dtype, (T, D))
@@ -603,9 +626,9 @@ def block_norm_fwd(r, y, w_pre, z=None, w_post=None, alpha=None, gate=None, ngro
     if return_rstd:
         rstd = (torch.empty((T, int(ngroups)), dtype=torch.float32, device=y.device),
                 torch.empty((T,), dtype=torch.float32, device=y.device))
-    _check(lib.ssd_block_norm_fwd(ctypes.byref(d), _ptr(r), yp, zp, _ptr(w_post), _ptr(alpha),
-                                  _ptr(w_pre), _ptr(ro), _ptr(n), _ptr(rstd[0]) if rstd else None,
-                                  _ptr(rstd[1]) if rstd else None, _stream()))
+    _check(lib.ssd_block_norm_fwd(ctypes.byref(d), _addr(r), yp, zp, _addr(w_post), _addr(alpha),
+                                  _addr(w_pre), _addr(ro), _addr(n), _addr(rstd[0]) if rstd else None,
+                                  _addr(rstd[1]) if rstd else None, _stream_int()))
     return (ro, n, rstd) if return_rstd else (ro, n)
 
 
@@ -614,7 +637,7 @@ def block_norm_bwd(r, y, w_pre, dr_out, dn, rstd, z=None, w_post=None, alpha=Non
     """The gradient of block_norm_fwd (same inputs, and its ``rstd``) from dr_out and
     dn.  Returns a dict: dr, dy, dz (None without a gate), dw_pre, dw_post and
     dalpha (None where the weight is None)."""
-    lib = load_library()
+    lib = _lib or load_library()
     d, yp, zp = _norm_dims(r, y, z, w_post, alpha, w_pre, gate, ngroups, eps)
     T, D = y.shape
     _typed(dr_out, "dr_out", r.dtype, (T, D))
@@ -629,9 +652,9 @@ def block_norm_bwd(r, y, w_pre, dr_out, dn, rstd, z=None, w_post=None, alpha=Non
     if workspace is None and need > 0:
         workspace = torch.empty(need, dtype=torch.uint8, device=y.device)
     nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(lib.ssd_block_norm_bwd(ctypes.byref(d), _ptr(r), yp, zp, _ptr(w_post), _ptr(alpha),
-                                  _ptr(w_pre), _ptr(dr_out), _ptr(dn), _ptr(rstd[0]), _ptr(rstd[1]),
-                                  _ptr(g["dr"]), _ptr(g["dy"]), _ptr(g["dz"]), _ptr(g["dw_post"]),
-                                  _ptr(g["dalpha"]), _ptr(g["dw_pre"]), _ptr(workspace), nbytes,
-                                  _stream()))
+    _check(lib.ssd_block_norm_bwd(ctypes.byref(d), _addr(r), yp, zp, _addr(w_post), _addr(alpha),
+                                  _addr(w_pre), _addr(dr_out), _addr(dn), _addr(rstd[0]), _addr(rstd[1]),
+                                  _addr(g["dr"]), _addr(g["dy"]), _addr(g["dz"]), _addr(g["dw_post"]),
+                                  _addr(g["dalpha"]), _addr(g["dw_pre"]), _addr(workspace), nbytes,
+                                  _stream_int()))
     return g

@@ -19,7 +19,7 @@ ssd_status make_norm(const ssd_norm_dims* d, NormParams* p) {
     if ((d->dtype != SSD_F32 && d->dtype != SSD_BF16) || (d->rdtype != SSD_F32 && d->rdtype != SSD_BF16))
         return SSD_ERR_DTYPE;
     if (d->dtype == SSD_F32 && d->rdtype != SSD_F32) return SSD_ERR_DTYPE;
-    if (d->reserved != 0 || d->tokens < 0 || d->tokens > (1LL << 31)) return SSD_ERR_SHAPE;
+    if (d->reserved != 0 || d->tokens < 0 || d->tokens > (1LL << 31) - 1) return SSD_ERR_SHAPE;
     if (d->gate != SSD_GATE_NONE && d->gate != SSD_GATE_SILU && d->gate != SSD_GATE_SIGMOID)
         return SSD_ERR_SHAPE;
     if (d->width < 8 || d->width > 16384 || d->ngroups < 1 || d->width % d->ngroups != 0 ||
@@ -81,7 +81,7 @@ ssd_status ssd_block_norm_fwd(const ssd_norm_dims* d, const void* r, const void*
     if ((s = pre_launch()) != SSD_OK) return s;
     p.r = r; p.y = y; p.z = z; p.w_post = w_post; p.alpha = alpha; p.w_pre = w_pre;
     p.r_out = r_out; p.n = n; p.rstd_post = rstd_post; p.rstd_pre = rstd_pre;
-    return from_cuda(launch_block_norm_fwd(p, d->dtype, d->rdtype, sm_count(), (cudaStream_t)stream));
+    return from_cuda(launch_block_norm_fwd(p, d->dtype, d->rdtype, (cudaStream_t)stream));
 }
 
 size_t ssd_block_norm_bwd_workspace_bytes(const ssd_norm_dims* d) {
