@@ -22,10 +22,10 @@
 // traffic, and the registers they would take hold more rows in flight instead.
 // Forwards, a CTA (or, for rows of up to 512 columns, a warp) runs one row.
 // Backwards, CTAs are persistent: a thread keeps the same columns for all its
-// rows, loads the next row while it computes one, and adds its columns' sums in
-// shared memory; each CTA leaves one partial sum, and a second kernel adds those
-// in a fixed order.
+// rows and adds its columns' sums in shared memory; each CTA leaves one partial
+// sum, and a second kernel adds those in a fixed order.
 #include "block_norm.cuh"
+#include "f32x2.cuh"
 
 namespace ssd {
 namespace {
@@ -43,46 +43,48 @@ __device__ __forceinline__ void load(Raw<float>& r, const float* p) {
 __device__ __forceinline__ void load(Raw<__nv_bfloat16>& r, const __nv_bfloat16* p) {
     r.a = __ldg(reinterpret_cast<const uint4*>(p));
 }
-__device__ __forceinline__ void unpack2(uint32_t v, float& a, float& b) {
-    a = __uint_as_float(v << 16);
-    b = __uint_as_float(v & 0xFFFF0000u);
+__device__ __forceinline__ f32x2 widen(uint32_t v) { return pair(v << 16, v & 0xFFFF0000u); }
+__device__ __forceinline__ void unpack(const Raw<float>& r, f32x2 (&f)[4]) {
+    f[0] = pair(r.a.x, r.a.y);
+    f[1] = pair(r.a.z, r.a.w);
+    f[2] = pair(r.b.x, r.b.y);
+    f[3] = pair(r.b.z, r.b.w);
 }
-__device__ __forceinline__ void unpack(const Raw<float>& r, float (&f)[8]) {
-    f[0] = r.a.x; f[1] = r.a.y; f[2] = r.a.z; f[3] = r.a.w;
-    f[4] = r.b.x; f[5] = r.b.y; f[6] = r.b.z; f[7] = r.b.w;
+__device__ __forceinline__ void unpack(const Raw<__nv_bfloat16>& r, f32x2 (&f)[4]) {
+    f[0] = widen(r.a.x);
+    f[1] = widen(r.a.y);
+    f[2] = widen(r.a.z);
+    f[3] = widen(r.a.w);
 }
-__device__ __forceinline__ void unpack(const Raw<__nv_bfloat16>& r, float (&f)[8]) {
-    unpack2(r.a.x, f[0], f[1]); unpack2(r.a.y, f[2], f[3]);
-    unpack2(r.a.z, f[4], f[5]); unpack2(r.a.w, f[6], f[7]);
-}
-__device__ __forceinline__ void load8(const float* p, float (&f)[8]) {
+__device__ __forceinline__ void load8(const float* p, f32x2 (&f)[4]) {
     Raw<float> r;
     load(r, p);
     unpack(r, f);
 }
+__device__ __forceinline__ f32x2 both(float v) { return pair(v, v); }
 // alpha o w_post of eight columns
-__device__ __forceinline__ void scale8(const NormParams& p, int j, float (&cw)[8]) {
+__device__ __forceinline__ void scale8(const NormParams& p, int j, f32x2 (&cw)[4]) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) cw[e] = 1.f;
+    for (int e = 0; e < 4; ++e) cw[e] = both(1.f);
     if (p.w_post) load8(p.w_post + 8 * j, cw);
     if (p.alpha) {
-        float t[8];
+        f32x2 t[4];
         load8(p.alpha + 8 * j, t);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) cw[e] *= t[e];
+        for (int e = 0; e < 4; ++e) cw[e] = mul2(cw[e], t[e]);
     }
 }
-__device__ __forceinline__ void store8(float* p, const float (&f)[8]) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+__device__ __forceinline__ void store8(float* p, const f32x2 (&f)[4]) {
+    reinterpret_cast<ulonglong2*>(p)[0] = make_ulonglong2(f[0], f[1]);
+    reinterpret_cast<ulonglong2*>(p)[1] = make_ulonglong2(f[2], f[3]);
 }
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-    const __nv_bfloat162 t = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&t);
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const f32x2 (&f)[4]) {
+    *reinterpret_cast<uint4*>(p) = make_uint4(pack2(f[0]), pack2(f[1]), pack2(f[2]), pack2(f[3]));
 }
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&f)[8]) {
-    *reinterpret_cast<uint4*>(p) = make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]),
-                                              pack2(f[4], f[5]), pack2(f[6], f[7]));
+__device__ __forceinline__ float sum2(f32x2 v) {
+    float a, b;
+    unpair(v, a, b);
+    return a + b;
 }
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -155,16 +157,20 @@ __device__ __forceinline__ float sigmoid(float z) {
     if (sizeof(T) == 2) return __fdividef(1.f, 1.f + __expf(-z));
     return 1.f / (1.f + expf(-z));
 }
-// Gate and derivative from z and s = sigmoid(z).
-__device__ __forceinline__ float gate_of(int kind, float z, float s) {
-    return kind == SSD_GATE_NONE ? 1.f : kind == SSD_GATE_SILU ? z * s : s;
+// s = sigmoid(z) (1 without a gate), m = z for SiLU and 1 else: the gate is s m,
+// its derivative s ([SiLU] + m (1 - s)).
+template <typename T>
+__device__ __forceinline__ f32x2 sigmoid2(int kind, f32x2 z) {
+    if (kind == SSD_GATE_NONE) return both(1.f);
+    float a, b;
+    unpair(z, a, b);
+    return pair(sigmoid<T>(a), sigmoid<T>(b));
 }
-__device__ __forceinline__ float dgate_of(int kind, float z, float s) {
-    return kind == SSD_GATE_NONE ? 0.f : kind == SSD_GATE_SILU ? s * (1.f + z * (1.f - s)) : s * (1.f - s);
-}
+__device__ __forceinline__ f32x2 factor2(int kind, f32x2 z) { return kind == SSD_GATE_SILU ? z : both(1.f); }
 
 template <typename T, typename R, int NV, bool kWarp>
-__global__ void __launch_bounds__(kWarp ? 128 : 512) block_norm_fwd(const __grid_constant__ NormParams p) {
+__global__ void __launch_bounds__(kWarp ? 128 : 512, !kWarp && NV == 2 && sizeof(T) == 2 ? 2 : 1)
+block_norm_fwd(const __grid_constant__ NormParams p) {
     extern __shared__ float sm[];
     const int first = kWarp ? threadIdx.x & 31 : threadIdx.x, stride = kWarp ? 32 : blockDim.x;
     const int sub = kWarp ? threadIdx.x >> 5 : 0;
@@ -186,47 +192,49 @@ __global__ void __launch_bounds__(kWarp ? 128 : 512) block_norm_fwd(const __grid
             load(r[i], static_cast<const R*>(p.r) + row * p.D + 8 * j);
         }
     }
-    float part[NV], rp[NV][8];
+    float part[NV];
+    f32x2 rp[NV][4];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        float f[8];
+        f32x2 f[4], v = 0ull;
         unpack(y[i], f);
-        part[i] = 0.f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) part[i] = fmaf(f[e], f[e], part[i]);
+        for (int e = 0; e < 4; ++e) v = fma2(f[e], f[e], v);
+        part[i] = sum2(v);
     }
     group_sum<NV, kWarp>(p, part, sm, grp, first, stride);
-    float sq = 0.f;
+    f32x2 sq2 = 0ull;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int j = first + i * stride;
         if (j < p.vecs) {
             const float rs = rsqrtf(part[i] * inv_gw + p.eps);
             if (p.rstd_post && j % p.gvecs == 0) p.rstd_post[row * p.ngroups + j / p.gvecs] = rs;
-            float cw[8], yf[8], zf[8];
+            f32x2 cw[4], yf[4], zf[4];
             scale8(p, j, cw);
             unpack(y[i], yf);
             unpack(z[i], zf);
             unpack(r[i], rp[i]);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float a = gate_of(p.gate, zf[e], sigmoid<T>(zf[e]));
-                rp[i][e] = fmaf(cw[e] * a, yf[e] * rs, rp[i][e]);
-                sq = fmaf(rp[i][e], rp[i][e], sq);
+            for (int e = 0; e < 4; ++e) {
+                const f32x2 a = mul2(sigmoid2<T>(p.gate, zf[e]), factor2(p.gate, zf[e]));
+                rp[i][e] = fma2(mul2(cw[e], a), mul2(yf[e], both(rs)), rp[i][e]);
+                sq2 = fma2(rp[i][e], rp[i][e], sq2);
             }
             store8(static_cast<R*>(p.r_out) + row * p.D + 8 * j, rp[i]);
         }
     }
+    const float sq = sum2(sq2);
     const float q = rsqrtf(row_sum<kWarp>(sq, sm + 32) * inv_d + p.eps);
     if (p.rstd_pre && first == 0) p.rstd_pre[row] = q;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int j = first + i * stride;
         if (j < p.vecs) {
-            float wp[8];
+            f32x2 wp[4];
             load8(p.w_pre + 8 * j, wp);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) rp[i][e] *= q * wp[e];
+            for (int e = 0; e < 4; ++e) rp[i][e] = mul2(rp[i][e], mul2(wp[e], both(q)));
             store8(static_cast<T*>(p.n) + row * p.D + 8 * j, rp[i]);
         }
     }
@@ -263,21 +271,27 @@ struct Row {
     }
 };
 
-// Registers: kPrefetch holds two rows.  `acc` in shared memory: per vector four
-// float4 a thread (E's eight columns, then w_pre's), strided by the block.
-template <typename T, typename R, int NV, bool kWarp, bool kPrefetch>
-__global__ void __launch_bounds__(kWarp ? 128 : 640) block_norm_bwd(const __grid_constant__ NormParams p) {
+// The columns' sums lie in shared memory: per vector four pairs of pairs a thread
+// (E's eight columns, then w_pre's), strided by the block.  CTAs of up to 256
+// threads are bounded to 80 registers, three to an SM (fp32: two).  (Measured at 16384 x 2048
+// bf16 and slower: four to an SM, which spills; weights and sums in registers, the
+// next row fetched ahead, two to an SM.)
+template <typename T, typename R, int NV, bool kWarp, bool kSmall>
+__global__ void __launch_bounds__(kWarp ? 128 : kSmall ? 256 : 640, kWarp ? 4 : !kSmall ? 1 : sizeof(T) == 2 ? 3 : 2)
+block_norm_bwd(const __grid_constant__ NormParams p) {
     extern __shared__ float sm[];
     const int first = kWarp ? threadIdx.x & 31 : threadIdx.x, stride = kWarp ? 32 : blockDim.x;
     const int rpb = kWarp ? blockDim.x >> 5 : 1, sub = kWarp ? threadIdx.x >> 5 : 0;
     float* grp = sm + 96 + (kWarp ? sub * p.grp_floats : 0);
-    float4* acc = reinterpret_cast<float4*>(sm + 96 + ((p.grp_floats * rpb + 3) & ~3)) + threadIdx.x;
+    ulonglong2* acc = reinterpret_cast<ulonglong2*>(sm + 96 + ((p.grp_floats * rpb + 3) & ~3)) + threadIdx.x;
 #pragma unroll
-    for (int i = 0; i < 4 * NV; ++i) acc[i * blockDim.x] = make_float4(0.f, 0.f, 0.f, 0.f);
-    const auto add8 = [&](int at, const float (&f)[8]) {
-        float4 a = acc[at * blockDim.x], b = acc[(at + 1) * blockDim.x];
-        a.x += f[0]; a.y += f[1]; a.z += f[2]; a.w += f[3];
-        b.x += f[4]; b.y += f[5]; b.z += f[6]; b.w += f[7];
+    for (int i = 0; i < 4 * NV; ++i) acc[i * blockDim.x] = make_ulonglong2(0ull, 0ull);
+    const auto add8 = [&](int at, const f32x2 (&f)[4]) {
+        ulonglong2 a = acc[at * blockDim.x], b = acc[(at + 1) * blockDim.x];
+        a.x = add2(a.x, f[0]);
+        a.y = add2(a.y, f[1]);
+        b.x = add2(b.x, f[2]);
+        b.y = add2(b.y, f[3]);
         acc[at * blockDim.x] = a;
         acc[(at + 1) * blockDim.x] = b;
     };
@@ -285,39 +299,36 @@ __global__ void __launch_bounds__(kWarp ? 128 : 640) block_norm_bwd(const __grid
     const int64_t step = (int64_t)gridDim.x * rpb;
     // the last reduction's buffer alternates: a row may have no other barrier
     float* buf = sm + 32;
-    Row<T, R, NV> cur, nxt;
+    Row<T, R, NV> cur;
     cur.clear();
-    if (kPrefetch) nxt.clear();
-    int64_t row = (int64_t)blockIdx.x * rpb + sub;
-    if (kPrefetch && row < p.T) cur.fetch(p, row, first, stride);
-    for (; row < p.T; row += step) {
-        if (!kPrefetch) cur.fetch(p, row, first, stride);
-        else if (row + step < p.T) nxt.fetch(p, row + step, first, stride);
+    for (int64_t row = (int64_t)blockIdx.x * rpb + sub; row < p.T; row += step) {
+        cur.fetch(p, row, first, stride);
         // rh = r' rsqrt; the mean of e o rh over the row
-        float dot = 0.f, u[NV][8], sg[NV][8];
+        f32x2 dot2 = 0ull, u[NV][4], sg[NV][4];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int j = first + i * stride;
             if (j < p.vecs) {
-                float cw[8], wp[8], yf[8], zf[8], dnf[8], t[8];
+                f32x2 cw[4], wp[4], yf[4], zf[4], dnf[4], t[4];
                 scale8(p, j, cw);
                 load8(p.w_pre + 8 * j, wp);
                 unpack(cur.y[i], yf);
                 unpack(cur.z[i], zf);
                 unpack(cur.r[i], u[i]);
                 unpack(cur.dn[i], dnf);
+                const f32x2 rs2 = both(cur.rs[i]), q2 = both(cur.q);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    sg[i][e] = sigmoid<T>(zf[e]);
-                    const float a = gate_of(p.gate, zf[e], sg[i][e]);
-                    u[i][e] = fmaf(cw[e] * a, yf[e] * cur.rs[i], u[i][e]) * cur.q;
-                    t[e] = dnf[e] * u[i][e];
-                    dot = fmaf(wp[e], t[e], dot);
+                for (int e = 0; e < 4; ++e) {
+                    sg[i][e] = sigmoid2<T>(p.gate, zf[e]);
+                    const f32x2 a = mul2(sg[i][e], factor2(p.gate, zf[e]));
+                    u[i][e] = mul2(fma2(mul2(cw[e], a), mul2(yf[e], rs2), u[i][e]), q2);
+                    t[e] = mul2(dnf[e], u[i][e]);
+                    dot2 = fma2(wp[e], t[e], dot2);
                 }
                 add8(4 * i + 2, t);
             }
         }
-        dot = row_sum<kWarp>(dot, buf) * inv_d;
+        const float dot = row_sum<kWarp>(sum2(dot2), buf) * inv_d;
         buf = buf == sm + 32 ? sm + 64 : sm + 32;
         float part[NV];
 #pragma unroll
@@ -325,23 +336,28 @@ __global__ void __launch_bounds__(kWarp ? 128 : 640) block_norm_bwd(const __grid
             const int j = first + i * stride;
             part[i] = 0.f;
             if (j < p.vecs) {
-                float cw[8], wp[8], yf[8], zf[8], dnf[8], gf[8], t[8];
+                f32x2 cw[4], wp[4], yf[4], zf[4], dnf[4], gf[4], t[4], v = 0ull;
                 scale8(p, j, cw);
                 load8(p.w_pre + 8 * j, wp);
                 unpack(cur.y[i], yf);
                 unpack(cur.z[i], zf);
                 unpack(cur.dn[i], dnf);
                 unpack(cur.g[i], gf);
+                const f32x2 rs2 = both(cur.rs[i]), q2 = both(cur.q), ndot2 = both(-dot);
+                const f32x2 silu = both(p.gate == SSD_GATE_SILU ? 1.f : 0.f), one = both(1.f), neg = both(-1.f);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float a = gate_of(p.gate, zf[e], sg[i][e]);
-                    const float yh = yf[e] * cur.rs[i];
-                    gf[e] = fmaf(cur.q, fmaf(wp[e], dnf[e], -u[i][e] * dot), gf[e]);
-                    t[e] = gf[e] * a * yh;
-                    u[i][e] = gf[e] * cw[e] * a;
-                    zf[e] = gf[e] * cw[e] * yh * dgate_of(p.gate, zf[e], sg[i][e]);
-                    part[i] = fmaf(u[i][e], yh, part[i]);
+                for (int e = 0; e < 4; ++e) {
+                    const f32x2 m = factor2(p.gate, zf[e]), s = sg[i][e];
+                    const f32x2 yh = mul2(yf[e], rs2);
+                    gf[e] = fma2(q2, fma2(wp[e], dnf[e], mul2(u[i][e], ndot2)), gf[e]);
+                    const f32x2 ga = mul2(gf[e], mul2(s, m));
+                    t[e] = mul2(ga, yh);
+                    u[i][e] = mul2(ga, cw[e]);
+                    const f32x2 da = mul2(s, fma2(m, fma2(s, neg, one), silu));
+                    zf[e] = mul2(mul2(gf[e], cw[e]), mul2(yh, da));
+                    v = fma2(u[i][e], yh, v);
                 }
+                part[i] = sum2(v);
                 add8(4 * i, t);
                 store8(static_cast<R*>(p.dr) + row * p.D + 8 * j, gf);
                 if (p.gate != SSD_GATE_NONE) store8(static_cast<T*>(p.dz) + row * p.D + 8 * j, zf);
@@ -352,15 +368,14 @@ __global__ void __launch_bounds__(kWarp ? 128 : 640) block_norm_bwd(const __grid
         for (int i = 0; i < NV; ++i) {
             const int j = first + i * stride;
             if (j < p.vecs) {
-                const float m = part[i] * inv_gw;
-                float yf[8];
+                const f32x2 rs2 = both(cur.rs[i]), nm2 = both(-part[i] * inv_gw);
+                f32x2 yf[4];
                 unpack(cur.y[i], yf);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) u[i][e] = cur.rs[i] * fmaf(-yf[e] * cur.rs[i], m, u[i][e]);
+                for (int e = 0; e < 4; ++e) u[i][e] = mul2(rs2, fma2(mul2(yf[e], rs2), nm2, u[i][e]));
                 store8(static_cast<T*>(p.dy) + row * p.D + 8 * j, u[i]);
             }
         }
-        if (kPrefetch) cur = nxt;
     }
     float* pe = p.partial + ((int64_t)blockIdx.x * rpb + sub) * 2 * p.D;
 #pragma unroll
@@ -369,7 +384,7 @@ __global__ void __launch_bounds__(kWarp ? 128 : 640) block_norm_bwd(const __grid
         if (j < p.vecs) {
 #pragma unroll
             for (int x = 0; x < 4; ++x)
-                reinterpret_cast<float4*>(pe + (x >> 1) * p.D + 8 * j)[x & 1] = acc[(4 * i + x) * blockDim.x];
+                reinterpret_cast<ulonglong2*>(pe + (x >> 1) * p.D + 8 * j)[x & 1] = acc[(4 * i + x) * blockDim.x];
         }
     }
 }
@@ -425,9 +440,8 @@ cudaError_t go(NormParams& p, bool backward, int64_t grid, cudaStream_t stream) 
     const size_t bytes = shared_bytes(p, c, backward);
     void (*k)(NormParams) = nullptr;
     if (backward)
-        // two rows at once where they fit the registers
-        k = c.warp ? (c.nv == 1 ? block_norm_bwd<T, R, 1, true, sizeof(T) == 2> : block_norm_bwd<T, R, 2, true, false>)
-          : c.nv == 1 ? block_norm_bwd<T, R, 1, false, sizeof(T) == 2>
+        k = c.warp ? (c.nv == 1 ? block_norm_bwd<T, R, 1, true, true> : block_norm_bwd<T, R, 2, true, true>)
+          : c.nv == 1 ? (c.threads <= 256 ? block_norm_bwd<T, R, 1, false, true> : block_norm_bwd<T, R, 1, false, false>)
           : c.nv == 2 ? block_norm_bwd<T, R, 2, false, false> : block_norm_bwd<T, R, 4, false, false>;
     else
         k = c.warp ? (c.nv == 1 ? block_norm_fwd<T, R, 1, true> : block_norm_fwd<T, R, 2, true>)
@@ -450,17 +464,17 @@ cudaError_t dispatch(NormParams& p, int dtype, int rdtype, bool backward, int64_
 
 }  // namespace
 
-int block_norm_grid(int64_t T, int vecs, int sms) {
+int block_norm_grid(int64_t T, int vecs, int dtype, int sms) {
     const Cut c = cut_of(vecs, true);
     const int rpb = c.warp ? c.threads / 32 : 1;
-    const int per = 640 / c.threads;   // by registers
+    const int per = c.warp ? 4 : c.threads <= 256 ? (dtype == SSD_BF16 ? 3 : 2) * 256 / c.threads : 640 / c.threads;   // by registers
     const int64_t rows = (T + rpb - 1) / rpb, full = (int64_t)sms * per;
     return (int)(rows < full ? rows : full);
 }
 
-int block_norm_parts(int64_t T, int vecs, int sms) {
+int block_norm_parts(int64_t T, int vecs, int dtype, int sms) {
     const Cut c = cut_of(vecs, true);
-    return block_norm_grid(T, vecs, sms) * (c.warp ? c.threads / 32 : 1);
+    return block_norm_grid(T, vecs, dtype, sms) * (c.warp ? c.threads / 32 : 1);
 }
 
 cudaError_t launch_block_norm_fwd(NormParams& p, int dtype, int rdtype, cudaStream_t st) {
@@ -470,12 +484,12 @@ cudaError_t launch_block_norm_fwd(NormParams& p, int dtype, int rdtype, cudaStre
 }
 
 cudaError_t launch_block_norm_bwd(NormParams& p, int dtype, int rdtype, int sms, cudaStream_t st) {
-    const int grid = p.T > 0 ? block_norm_grid(p.T, p.vecs, sms) : 0;
+    const int grid = p.T > 0 ? block_norm_grid(p.T, p.vecs, dtype, sms) : 0;
     if (grid > 0) {
         const cudaError_t e = dispatch(p, dtype, rdtype, true, grid, st);
         if (e != cudaSuccess) return e;
     }
-    const int parts = grid > 0 ? block_norm_parts(p.T, p.vecs, sms) : 0;
+    const int parts = grid > 0 ? block_norm_parts(p.T, p.vecs, dtype, sms) : 0;
     block_norm_reduce<<<dim3((unsigned)(p.D + 31) / 32, 2), 512, 0, st>>>(p, parts);
     return cudaGetLastError();
 }

@@ -19,8 +19,8 @@ struct NormParams {
 };
 
 // CTAs of the gradient's kernel, and partial column sums that it leaves.
-int block_norm_grid(int64_t T, int vecs, int sms);
-int block_norm_parts(int64_t T, int vecs, int sms);
+int block_norm_grid(int64_t T, int vecs, int dtype, int sms);
+int block_norm_parts(int64_t T, int vecs, int dtype, int sms);
 cudaError_t launch_block_norm_fwd(NormParams& p, int dtype, int rdtype, cudaStream_t stream);
 cudaError_t launch_block_norm_bwd(NormParams& p, int dtype, int rdtype, int sms, cudaStream_t stream);
 

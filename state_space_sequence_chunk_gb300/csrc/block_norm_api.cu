@@ -87,7 +87,7 @@ ssd_status ssd_block_norm_fwd(const ssd_norm_dims* d, const void* r, const void*
 size_t ssd_block_norm_bwd_workspace_bytes(const ssd_norm_dims* d) {
     NormParams p;
     if (make_norm(d, &p) != SSD_OK || p.T == 0) return 0;
-    return (size_t)block_norm_parts(p.T, p.vecs, sm_count()) * 2 * p.D * 4;
+    return (size_t)block_norm_parts(p.T, p.vecs, d->dtype, sm_count()) * 2 * p.D * 4;
 }
 
 ssd_status ssd_block_norm_bwd(const ssd_norm_dims* d, const void* r, const void* y, const void* z,
