@@ -53,18 +53,19 @@ ssd_status make_la(const ssd_linattn_dims* d, bool packed, bool backward, La* p)
     g.nseq = (int)p->n; g.H = (int)p->H; g.T = (int)p->T;
     g.L = packed || p->n == 0 ? 0 : (int)(p->T / p->n);
     g.a = nullptr;
-    // Ranges: half of what an SM would get if the work were spread evenly (so that
-    // the longest of them, taken last, adds at most that), none shorter than 512
-    // tokens.  A sequence that fits one range is not cut; longer ones pay a second
-    // reading of two operands, and gain the whole GPU.
+    // A sequence is cut only if it is longer than what an SM gets when the work is
+    // spread evenly, into ranges of half of that (so that the one taken last adds at
+    // most half), none shorter than 512 tokens: ranges pay a second reading of two
+    // operands and gain the whole GPU.
     const int64_t kb = (p->K + kLaCols - 1) / kLaCols, vb = (p->V + kLaCols - 1) / kLaCols;
     const int64_t cols = backward ? 2 * kb + vb : vb;
-    int64_t R = p->T * p->H * cols / (2 * (int64_t)sm_count());
+    const int64_t share = p->T * p->H * cols / sm_count();
+    int64_t R = share / 2;
     R = (R + 127) / 128 * 128;
     if (R < 512) R = 512;
     int64_t longest = packed ? (d->max_seqlen ? d->max_seqlen : p->T) : g.L;
     if (longest > p->T) longest = p->T;
-    g.split = longest > R;
+    g.split = longest > R && longest > share;
     g.R = g.split ? (int)R : (int)(p->T > 0 ? (p->T + 127) / 128 * 128 : 128);
     const int64_t cap = g.split ? p->T / R + p->n + 1 : p->n + 1;
     if (cap > (1LL << 24)) return SSD_ERR_SHAPE;
