@@ -34,7 +34,7 @@
 //         update with U, stored states
 //   24-27 out (a thread owns a token row)
 //   28    TMA, two stages of A, B and C tiles (80 KB each)
-//   29    MMA issue: W(c), P C(c - 1), U(c), A X(c)
+//   29    MMA issue: U(c), W(c + 1), A X(c), P C(c)
 // The roles' loops are kept short (packed fp32 arithmetic, little unrolling): six
 // codes run side by side on each scheduler, and fully unrolled they spent most of
 // their time on instruction fetches.
@@ -373,44 +373,27 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
         constexpr uint32_t kIdW = make_idesc(1, 128, 128, 0, 0);
         constexpr uint32_t kIdO = make_idesc(1, 128, 64, 0, 1);
         constexpr uint32_t kIdU = make_idesc(1, 128, 64 * kTerms, 1, 1);
-        // out(pc) += P C; in the exact form, beside P's columns in W's buffer
-        const auto p_product = [&](int pc, int pf) {
-            const int s = pc & 1;
-            mbar_wait(smem_u32(b_fc) + 8 * (pc % kCs), (pc / kCs) & 1, err, 1u);
-            mbar_wait(smem_u32(b_pready + s), (pc >> 1) & 1, err, 1u);
-            tc_fence_after();
-            const uint64_t bd = smem_desc_sw128(smem_u32(ctile) + (pc % kCs) * kAtom, 8 * kRow, 8 * kRow);
-            const uint32_t to = tmem + (pf ? kO : kW + s * 128 + 64);
-            const uint32_t pa = tmem + kW + s * 128, pb = pa + (pf ? 32 : 0);
-#pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-                mma_f16_ts(to, (kk < 4 ? pa : pb) + kk * 8, bd + (uint64_t)((kk * 16 * kRow) >> 4), kIdO,
-                           kk > 0 ? 1u : (uint32_t)pf);
-            mma_commit(smem_u32(b_odone));
-        };
-        int last_fac = 0, pending = 0;   // the last chunk's P C is still to be issued
 #pragma unroll 1
         while (read_item(im)) {
             const int nch = uniform(im.nch), ks = uniform(tp.p.job[im.job].DK / 16);
             const int fac = uniform(factored(im.a2) ? 1 : 0);
-            if (nch == 0) {
-                // nothing here to issue it with, and no end to such items: the warps
-                // that wait for it would hold up the next one's announcement
-                if (!kAgg && pending && elect_one()) p_product(c - 1, last_fac);
-                __syncwarp();
-                pending = 0;
-                continue;
-            }
             if (elect_one()) {
-                // Per chunk W(c), P C(c - 1), U(c) in two halves, A X(c).  The previous
-                // chunk's last product waits for P, built meanwhile; it fills the time
-                // in which U's second half is prepared, and the time in which out is
-                // read is filled by U.  A and B stay for one round only, so that two
-                // stages keep the loads ahead.
+                // x = -1: the W of the item's first chunk
 #pragma unroll 1
-                for (int x = 0; x < nch; ++x) {
+                for (int x = kAgg ? 0 : -1; x < nch; ++x) {
                     const int cc = c + x, s = cc & 1, use = cc >> 1;
                     const uint32_t st = smem_u32(smem) + s * kStage;
+                    const int s1 = s ^ 1, use1 = (cc + 1) >> 1;
+                    const uint32_t st1 = smem_u32(smem) + s1 * kStage;
+                    bool w_due = !kAgg && x + 1 < nch;
+                    const auto w_product = [&]() {
+                        w_due = false;
+                        mbar_wait(smem_u32(b_fab + s1), use1 & 1, err, 1u);
+                        tc_fence_after();
+                        mma_steps<true, true>(tmem + kW + s1 * 128, smem_desc_sw128(st1, 16, 8 * kRow),
+                                              smem_desc_sw128(st1 + 2 * kAtom, 16, 8 * kRow), ks, kIdW);
+                        mma_commit(smem_u32(b_wdone + s1));
+                    };
                     const auto u_half = [&](int half) {
                         const uint64_t ad = smem_desc_sw128(st + 2 * kAtom + half * kTerm, kAtom, 8 * kRow);
                         const uint64_t bd = smem_desc_sw128(smem_u32(terms), kTerm, 8 * kRow);
@@ -420,51 +403,54 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                             mma_f16_ss(tmem + kU, ad + o, bd + o, kIdU, half + kk > 0 ? 1u : 0u);
                         }
                     };
-                    bool p_due = !kAgg && (x > 0 || pending);
-                    const int pf = x > 0 ? fac : last_fac;
-                    if (p_due && !mbar_try_wait(smem_u32(b_fab + s), use & 1)) {
-                        p_product(cc - 1, pf);   // no tiles yet for W
-                        p_due = false;
-                    }
-                    mbar_wait(smem_u32(b_fab + s), use & 1, err, 1u);
-                    if (!kAgg) {
+                    if (x >= 0) {
+                        if (kAgg) mbar_wait(smem_u32(b_fab + s), use & 1, err, 1u);
+                        // U = B^T (scaled C), its three terms side by side: B is read once
+                        mbar_wait(smem_u32(b_vready), cc & 1, err, 1u);
+                        mbar_wait(smem_u32(b_ufree), (cc & 1) ^ 1, err, 1u);
                         tc_fence_after();
-                        mma_steps<true, true>(tmem + kW + s * 128, smem_desc_sw128(st, 16, 8 * kRow),
-                                              smem_desc_sw128(st + 2 * kAtom, 16, 8 * kRow), ks, kIdW);
-                        mma_commit(smem_u32(b_wdone + s));
-                    }
-                    if (p_due) p_product(cc - 1, pf);
-                    // U = B^T (scaled C), its three terms side by side: B is read once
-                    mbar_wait(smem_u32(b_vready), cc & 1, err, 1u);
-                    mbar_wait(smem_u32(b_ufree), (cc & 1) ^ 1, err, 1u);
-                    tc_fence_after();
-                    u_half(0);
-                    mma_commit(smem_u32(b_udone));
-                    mbar_wait(smem_u32(b_vready + 1), cc & 1, err, 1u);
-                    tc_fence_after();
-                    u_half(1);
-                    mma_commit(smem_u32(b_udone + 1));
-                    if (kAgg) {
-                        mma_commit(smem_u32(b_ec) + 8 * (cc % kCs));
-                    } else {
-                        // out = A X
-                        mbar_wait(smem_u32(b_sready), cc & 1, err, 1u);
-                        mbar_wait(smem_u32(b_ofree), (cc & 1) ^ 1, err, 1u);
+                        u_half(0);
+                        mma_commit(smem_u32(b_udone));
+                        mbar_wait(smem_u32(b_vready + 1), cc & 1, err, 1u);
                         tc_fence_after();
-                        mma_steps<true, false>(tmem + kO, smem_desc_sw128(st, 16, 8 * kRow),
-                                               smem_desc_sw128(smem_u32(xs), 8 * kRow, 8 * kRow), ks, kIdO);
-                        mma_commit(smem_u32(b_xdone));
+                        u_half(1);
+                        mma_commit(smem_u32(b_udone + 1));
+                        if (kAgg) {
+                            mma_commit(smem_u32(b_eab + s));
+                            mma_commit(smem_u32(b_ec) + 8 * (cc % kCs));
+                        } else {
+                            // W of the next chunk, if its tiles are there (and the exact form
+                            // does not hold its buffer): P is then built a chunk ahead, and
+                            // the tensor pipe has work while the last out is read
+                            if (w_due && fac && mbar_try_wait(smem_u32(b_fab + s1), use1 & 1)) w_product();
+                            // out = A X
+                            mbar_wait(smem_u32(b_sready), cc & 1, err, 1u);
+                            mbar_wait(smem_u32(b_ofree), (cc & 1) ^ 1, err, 1u);
+                            tc_fence_after();
+                            mma_steps<true, false>(tmem + kO, smem_desc_sw128(st, 16, 8 * kRow),
+                                                   smem_desc_sw128(smem_u32(xs), 8 * kRow, 8 * kRow), ks, kIdO);
+                            mma_commit(smem_u32(b_xdone));
+                            mma_commit(smem_u32(b_eab + s));
+                            // out += P C; in the exact form, beside P's columns in W's buffer
+                            mbar_wait(smem_u32(b_fc) + 8 * (cc % kCs), (cc / kCs) & 1, err, 1u);
+                            mbar_wait(smem_u32(b_pready + s), use & 1, err, 1u);
+                            tc_fence_after();
+                            const uint64_t bd = smem_desc_sw128(smem_u32(ctile) + (cc % kCs) * kAtom, 8 * kRow, 8 * kRow);
+                            const uint32_t to = tmem + (fac ? kO : kW + s * 128 + 64);
+                            const uint32_t pa = tmem + kW + s * 128, pb = pa + (fac ? 32 : 0);
+#pragma unroll
+                            for (int kk = 0; kk < 8; ++kk)
+                                mma_f16_ts(to, (kk < 4 ? pa : pb) + kk * 8, bd + (uint64_t)((kk * 16 * kRow) >> 4),
+                                           kIdO, kk > 0 ? 1u : (uint32_t)fac);
+                            mma_commit(smem_u32(b_odone));
+                        }
                     }
-                    mma_commit(smem_u32(b_eab + s));
+                    if (w_due) w_product();
                 }
             }
             __syncwarp();
             c += nch;
-            last_fac = fac;
-            pending = 1;
         }
-        if (!kAgg && pending && elect_one()) p_product(c - 1, last_fac);
-        __syncwarp();
     } else if (warp < 8) {
         // ===================== P =====================
         if (!kAgg) {
@@ -737,28 +723,7 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                 // one is stored row by row.
                 const bool tile = n == kC && !jb.out_f32;
                 const uint32_t ct = smem_u32(ctile) + (c % kCs) * kAtom;
-#pragma unroll 1
-                for (int b = 0; b < 4; ++b) {   // 16 columns at a time
-                    uint32_t p[16];
-                    f32x2 r[8];
-                    __syncwarp();
-                    tmem_ld_x16(tmem + lane_off + kO + b * 16, p);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) r[e] = mul2(f2, pair(p[2 * e], p[2 * e + 1]));
-                    if (!fac) {
-                        tmem_ld_x16(tmem + lane_off + kW + (c & 1) * 128 + 64 + b * 16, p);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) r[e] = fma2(s2, pair(p[2 * e], p[2 * e + 1]), r[e]);
-                    }
-                    if (b == 3) {
-                        tc_fence_before();
-                        mbar_arrive(smem_u32(b_ofree));
-                    }
-                    uint32_t w[8];
-#pragma unroll
-                    for (int y = 0; y < 8; ++y) w[y] = pack2(r[y]);
+                const auto put = [&](int b, const uint32_t (&w)[8], const f32x2 (&r)[8]) {   // 16 columns
                     if (tile) {
                         sts128(ct + i * kRow + (((2 * b) ^ (i & 7)) << 4), w[0], w[1], w[2], w[3]);
                         sts128(ct + i * kRow + (((2 * b + 1) ^ (i & 7)) << 4), w[4], w[5], w[6], w[7]);
@@ -772,6 +737,52 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                             d[0] = make_uint4(w[0], w[1], w[2], w[3]);
                             d[1] = make_uint4(w[4], w[5], w[6], w[7]);
                         }
+                    }
+                };
+                if (fac && tile) {
+                    // the next chunk's product waits for the accumulator: it is given up
+                    // as soon as its second half is in registers
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {
+                        uint32_t p[32];
+                        __syncwarp();
+                        tmem_ld_x32(tmem + lane_off + kO + hf * 32, p);
+                        tmem_wait_ld();
+                        if (hf == 1) {
+                            tc_fence_before();
+                            mbar_arrive(smem_u32(b_ofree));
+                        }
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int y = 0; y < 4; ++y) w[y] = pack2(mul2(f2, pair(p[8 * q + 2 * y], p[8 * q + 2 * y + 1])));
+                            sts128(ct + i * kRow + (((4 * hf + q) ^ (i & 7)) << 4), w[0], w[1], w[2], w[3]);
+                        }
+                    }
+                } else {
+#pragma unroll 1
+                    for (int b = 0; b < 4; ++b) {
+                        uint32_t p[16], w[8];
+                        f32x2 r[8];
+                        __syncwarp();
+                        tmem_ld_x16(tmem + lane_off + kO + b * 16, p);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) r[e] = mul2(f2, pair(p[2 * e], p[2 * e + 1]));
+                        if (!fac) {
+                            tmem_ld_x16(tmem + lane_off + kW + (c & 1) * 128 + 64 + b * 16, p);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) r[e] = fma2(s2, pair(p[2 * e], p[2 * e + 1]), r[e]);
+                        }
+                        if (b == 3) {
+                            tc_fence_before();
+                            mbar_arrive(smem_u32(b_ofree));
+                        }
+#pragma unroll
+                        for (int y = 0; y < 8; ++y) w[y] = pack2(r[y]);
+                        put(b, w, r);
                     }
                 }
                 if (tile) fence_proxy_async_smem();
