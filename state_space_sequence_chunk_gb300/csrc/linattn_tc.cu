@@ -56,14 +56,23 @@ constexpr int kRow = 128;                     // bytes of a tile row (64 columns
 constexpr int kAtom = kC * kRow;              // 16 KB: 128 rows of 64 columns
 constexpr int kThreads = 960;
 constexpr int kTmaWarp = 28, kMmaWarp = 29;
-constexpr int kStage = 4 * kAtom;             // A (2 atoms), B (2)
-constexpr int kCs = 3;                        // C tiles
 constexpr int kTerms = 3;
 constexpr int kTerm = kAtom / 2;              // a term of 64 tokens
-constexpr int kSmem = 2 * kStage + kCs * kAtom + kTerms * kTerm + kAtom + 1024;
+// What the two passes keep: C tiles, buffers for a half's terms (with one, the
+// halves take turns), accumulators for U.  The pass over the ranges' own sums
+// has no A, W and out.
+template <bool kAgg> struct Cfg {
+    static constexpr int kCs = kAgg ? 4 : 3;
+    static constexpr int kTb = kAgg ? 2 : 1;
+    static constexpr int kUb = kAgg ? 2 : 1;
+    static constexpr int kB = kAgg ? 0 : 2 * kAtom;      // a stage: A (2 atoms), B (2)
+    static constexpr int kStage = kB + 2 * kAtom;
+    static constexpr int kSmem = 2 * kStage + kCs * kAtom + kTb * kTerms * kTerm + (kAgg ? 0 : kAtom) + 1024;
+    static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
+};
 // tensor memory columns
 constexpr uint32_t kW = 0;                    // W / P, two buffers of 128
-constexpr uint32_t kO = 256, kU = 320;        // out; U's three terms
+constexpr uint32_t kO = 256, kUMain = 320;    // out; U's three terms
 // The factored form takes heads whose decay over a chunk's 127 steps is at least
 // 2^-kSpan: row and column factors, counted from the middle, are within 2^+-60.
 constexpr float kSpan = 120.f;
@@ -234,30 +243,33 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
         }
         return;
     }
+    constexpr int kB = Cfg<kAgg>::kB, kStage = Cfg<kAgg>::kStage, kCs = Cfg<kAgg>::kCs, kTb = Cfg<kAgg>::kTb, kUb = Cfg<kAgg>::kUb;
+    constexpr uint32_t kU = kAgg ? 0 : kUMain;
     uint8_t* ctile = smem + 2 * kStage;
     uint8_t* terms = ctile + kCs * kAtom;
-    uint8_t* xs = terms + kTerms * kTerm;
-    uint64_t* bars = reinterpret_cast<uint64_t*>(xs + kAtom);
+    uint8_t* xs = terms + kTb * kTerms * kTerm;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(xs + (kAgg ? 0 : kAtom));
     uint64_t* b_fab = bars;           // [2] stage's A and B loaded (tx)
     uint64_t* b_eab = bars + 2;       // [2] A and B read by every product (commit)
-    uint64_t* b_fc = bars + 4;        // [3] C tile loaded (tx)
-    uint64_t* b_ec = bars + 7;        // [3] C read by every product, and out stored from it
-    uint64_t* b_wdone = bars + 10;    // [2] W computed (commit)
-    uint64_t* b_pready = bars + 12;   // [2] P written (256)
-    uint64_t* b_vready = bars + 14;   // [2] terms of a half of the tokens written (128)
-    uint64_t* b_udone = bars + 16;    // [2] U's half computed, its terms read (commit)
-    uint64_t* b_ufree = bars + 18;    // U read (256)
-    uint64_t* b_sready = bars + 19;   // bf16 X written (256)
-    uint64_t* b_xdone = bars + 20;    // A X computed: the bf16 X may change (commit)
-    uint64_t* b_odone = bars + 21;    // out computed (commit)
-    uint64_t* b_ofree = bars + 22;    // out read (128)
-    uint64_t* b_answer = bars + 23;   // answer to an item request (tx)
-    uint64_t* b_iready = bars + 24;   // [2] item decoded (1)
-    uint64_t* b_ifree = bars + 26;    // [2] item read (every other warp that walks items)
-    uint32_t* holder = reinterpret_cast<uint32_t*>(bars + 28);
-    const uint32_t answer = smem_u32(bars + 30);    // 16 bytes
-    Item* items = reinterpret_cast<Item*>(bars + 32);   // [2]
-    const uint32_t ptab = smem_u32(bars + 48);      // [128] fp32: column factors of P
+    uint64_t* b_fc = bars + 4;        // [4] C tile loaded (tx)
+    uint64_t* b_ec = bars + 8;        // [4] C read by every product, and out stored from it
+    uint64_t* b_wdone = bars + 12;    // [2] W computed (commit)
+    uint64_t* b_pready = bars + 14;   // [2] P written (256)
+    uint64_t* b_vready = bars + 16;   // [2] terms of a half of the tokens written (128)
+    uint64_t* b_udone = bars + 18;    // [2] U's half computed, its terms read (commit)
+    uint64_t* b_ux = bars + 20;       // [2] U computed (commit)
+    uint64_t* b_ufree = bars + 22;    // [2] U read (256)
+    uint64_t* b_sready = bars + 24;   // bf16 X written (256)
+    uint64_t* b_xdone = bars + 25;    // A X computed: the bf16 X may change (commit)
+    uint64_t* b_odone = bars + 26;    // out computed (commit)
+    uint64_t* b_ofree = bars + 27;    // out read (128)
+    uint64_t* b_answer = bars + 28;   // answer to an item request (tx)
+    uint64_t* b_iready = bars + 29;   // [2] item decoded (1)
+    uint64_t* b_ifree = bars + 31;    // [2] item read (every other warp that walks items)
+    uint32_t* holder = reinterpret_cast<uint32_t*>(bars + 33);
+    const uint32_t answer = smem_u32(bars + 34);    // 16 bytes
+    Item* items = reinterpret_cast<Item*>(bars + 36);   // [2]
+    const uint32_t ptab = smem_u32(bars + 52);      // [128] fp32: column factors of P
 
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
@@ -268,6 +280,8 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
             mbar_init(smem_u32(b_pready + s), 256);
             mbar_init(smem_u32(b_vready + s), 128);
             mbar_init(smem_u32(b_udone + s), 1);
+            mbar_init(smem_u32(b_ux + s), 1);
+            mbar_init(smem_u32(b_ufree + s), 256);
             mbar_init(smem_u32(b_iready + s), 1);
             mbar_init(smem_u32(b_ifree + s), kAgg ? 17 : kThreads / 32 - 1);
         }
@@ -276,7 +290,6 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
             mbar_init(smem_u32(b_ec + s), 1);
         }
         mbar_init(smem_u32(b_answer), 1);
-        mbar_init(smem_u32(b_ufree), 256);
         mbar_init(smem_u32(b_sready), 256);
         mbar_init(smem_u32(b_xdone), 1);
         mbar_init(smem_u32(b_odone), 1);
@@ -342,7 +355,7 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                             mbar_arrive_expect_tx(fab, (kAgg ? 1 : 2) * ka * kAtom);
                             for (int a = 0; a < ka; ++a) {
                                 if (!kAgg) tma_load_3d(st + a * kAtom, m + 0, fab, a * 64, ha, t);
-                                tma_load_3d(st + (2 + a) * kAtom, m + 1, fab, a * 64, hb, t);
+                                tma_load_3d(st + kB + a * kAtom, m + 1, fab, a * 64, hb, t);
                             }
                         }
                         if (x + 1 < nch) {
@@ -391,23 +404,26 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                         mbar_wait(smem_u32(b_fab + s1), use1 & 1, err, 1u);
                         tc_fence_after();
                         mma_steps<true, true>(tmem + kW + s1 * 128, smem_desc_sw128(st1, 16, 8 * kRow),
-                                              smem_desc_sw128(st1 + 2 * kAtom, 16, 8 * kRow), ks, kIdW);
+                                              smem_desc_sw128(st1 + kB, 16, 8 * kRow), ks, kIdW);
                         mma_commit(smem_u32(b_wdone + s1));
                     };
                     const auto u_half = [&](int half) {
-                        const uint64_t ad = smem_desc_sw128(st + 2 * kAtom + half * kTerm, kAtom, 8 * kRow);
-                        const uint64_t bd = smem_desc_sw128(smem_u32(terms), kTerm, 8 * kRow);
+                        const uint64_t ad = smem_desc_sw128(st + kB + half * kTerm, kAtom, 8 * kRow);
+                        const uint64_t bd = smem_desc_sw128(
+                            smem_u32(terms) + (kTb == 2 ? half * kTerms * kTerm : 0), kTerm, 8 * kRow);
+                        const uint32_t ud = tmem + kU + (kUb == 2 ? (cc & 1) * 64 * kTerms : 0);
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk) {
                             const uint32_t o = (uint32_t)(kk * 16 * kRow) >> 4;
-                            mma_f16_ss(tmem + kU, ad + o, bd + o, kIdU, half + kk > 0 ? 1u : 0u);
+                            mma_f16_ss(ud, ad + o, bd + o, kIdU, half + kk > 0 ? 1u : 0u);
                         }
                     };
                     if (x >= 0) {
                         if (kAgg) mbar_wait(smem_u32(b_fab + s), use & 1, err, 1u);
                         // U = B^T (scaled C), its three terms side by side: B is read once
                         mbar_wait(smem_u32(b_vready), cc & 1, err, 1u);
-                        mbar_wait(smem_u32(b_ufree), (cc & 1) ^ 1, err, 1u);
+                        if (kUb == 2) mbar_wait(smem_u32(b_ufree + s), (use & 1) ^ 1, err, 1u);
+                        else mbar_wait(smem_u32(b_ufree), (cc & 1) ^ 1, err, 1u);
                         tc_fence_after();
                         u_half(0);
                         mma_commit(smem_u32(b_udone));
@@ -415,6 +431,7 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                         tc_fence_after();
                         u_half(1);
                         mma_commit(smem_u32(b_udone + 1));
+                        mma_commit(smem_u32(b_ux + (kUb == 2 ? s : 0)));
                         if (kAgg) {
                             mma_commit(smem_u32(b_eab + s));
                             mma_commit(smem_u32(b_ec) + 8 * (cc % kCs));
@@ -558,7 +575,7 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                 const float w = la_exp2(a2, jb.rev ? row + 1 : max(n - 1 - row, 0)) * jb.s_in;
                 const f32x2 w2 = pair(w, w);
                 wait_on(smem_u32(b_fc) + 8 * (c % kCs), (c / kCs) & 1, err);
-                const uint32_t st = smem_u32(smem) + s * kStage, tm = smem_u32(terms) - half * kTerm;
+                const uint32_t st = smem_u32(smem) + s * kStage, tm = smem_u32(terms) + half * (kTb == 2 ? (kTerms - 1) * kTerm : -kTerm);
                 const uint32_t ct = smem_u32(ctile) + (c % kCs) * kAtom;
                 // the terms of this thread's 32 columns are ready in registers when the
                 // last U lets go of their tiles; a row of other tokens gives zeros
@@ -589,15 +606,19 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                         for (int ch = ch0; ch < ch0 + 4; ++ch)
 {
                             const int at = row * kRow + (ch << 4);
-                            sts128(st + 2 * kAtom + at, 0u, 0u, 0u, 0u);
-                            sts128(st + 3 * kAtom + at, 0u, 0u, 0u, 0u);
+                            sts128(st + kB + at, 0u, 0u, 0u, 0u);
+                            sts128(st + kB + kAtom + at, 0u, 0u, 0u, 0u);
                             sts128(ct + at, 0u, 0u, 0u, 0u);
                         }
                     }
                 }
-                // the halves take turns in the same tiles
-                if (half) wait_on(smem_u32(b_udone), c & 1, err);
-                else if (c > 0) wait_on(smem_u32(b_udone + 1), (c - 1) & 1, err);
+                if (kTb == 2) {
+                    if (c > 0) wait_on(smem_u32(b_udone + half), (c - 1) & 1, err);
+                } else if (half) {   // the halves take turns in the same tiles
+                    wait_on(smem_u32(b_udone), c & 1, err);
+                } else if (c > 0) {
+                    wait_on(smem_u32(b_udone + 1), (c - 1) & 1, err);
+                }
 #pragma unroll
                 for (int ch = 0; ch < 4; ++ch)
 #pragma unroll
@@ -651,16 +672,18 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                 }
                 float hi = im.hi, lo = im.lo;
                 if (n < kC) la_decay_pow(g.a, im.h, n, hi, lo);
-                wait_on(smem_u32(b_udone + 1), c & 1, err);
+                if (kUb == 2) wait_on(smem_u32(b_ux + (c & 1)), (c >> 1) & 1, err);
+                else wait_on(smem_u32(b_ux), c & 1, err);
                 tc_fence_after();
+                const uint32_t ub = tmem + lane_off + kU + vc + (kUb == 2 ? (c & 1) * 64 * kTerms : 0);
                 const f32x2 hi2 = pair(hi, hi), lo2 = pair(lo, lo);
 #pragma unroll
                 for (int q = 0; q < 8; ++q) {
                     uint32_t u0[4], u1[4], u2[4];
                     __syncwarp();
-                    tmem_ld_x4(tmem + lane_off + kU + vc + q * 4, u0);
-                    tmem_ld_x4(tmem + lane_off + kU + 64 + vc + q * 4, u1);
-                    tmem_ld_x4(tmem + lane_off + kU + 128 + vc + q * 4, u2);
+                    tmem_ld_x4(ub + q * 4, u0);
+                    tmem_ld_x4(ub + 64 + q * 4, u1);
+                    tmem_ld_x4(ub + 128 + q * 4, u2);
                     tmem_wait_ld();
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
@@ -671,7 +694,7 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                     }
                 }
                 tc_fence_before();
-                mbar_arrive(smem_u32(b_ufree));
+                mbar_arrive(smem_u32(b_ufree + (kUb == 2 ? (c & 1) : 0)));
             }
             float* outst = kAgg ? ag : (im.last && jb.fin ? jb.fin + so : nullptr);
             if (outst != nullptr && k < jb.DK) {
@@ -840,9 +863,10 @@ cudaError_t launch_linattn_tc(const LaParams& p, int mode, cudaStream_t stream) 
     if (items >= (1LL << 31)) return cudaErrorInvalidValue;
     tp.host_err = host_timeout_word();
     auto k = mode ? linattn_tc<true> : linattn_tc<false>;
-    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    const int smem = mode ? Cfg<true>::kSmem : Cfg<false>::kSmem;
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    k<<<(unsigned)items, kThreads, kSmem, stream>>>(tp, maps);
+    k<<<(unsigned)items, kThreads, smem, stream>>>(tp, maps);
     return cudaGetLastError();
 }
 
