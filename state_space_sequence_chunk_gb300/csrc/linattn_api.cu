@@ -55,14 +55,15 @@ ssd_status make_la(const ssd_linattn_dims* d, bool packed, bool backward, La* p)
     g.a = nullptr;
     // A sequence is cut only if it is longer than what an SM gets when the work is
     // spread evenly, into ranges of half of that (so that the one taken last adds at
-    // most half), none shorter than 512 tokens: ranges pay a second reading of two
+    // most half), none shorter than 512 tokens (fp32: 128): ranges pay a second reading of two
     // operands and gain the whole GPU.
     const int64_t kb = (p->K + kLaCols - 1) / kLaCols, vb = (p->V + kLaCols - 1) / kLaCols;
     const int64_t cols = backward ? 2 * kb + vb : vb;
     const int64_t share = p->T * p->H * cols / sm_count();
     int64_t R = share / 2;
     R = (R + 127) / 128 * 128;
-    if (R < 512) R = 512;
+    const int64_t least = d->dtype == SSD_F32 ? 128 : 512;   // fp32 chunks take longer
+    if (R < least) R = least;
     int64_t longest = packed ? (d->max_seqlen ? d->max_seqlen : p->T) : g.L;
     if (longest > p->T) longest = p->T;
     g.split = longest > R && longest > share;
@@ -85,7 +86,7 @@ size_t span(int64_t T, int64_t stride, int64_t w, int es) {
 cudaError_t run_jobs(LaParams& p, int dtype, cudaStream_t st) {
     auto pass = [&](int mode) {
         return dtype == SSD_BF16 ? launch_linattn_tc(p, mode, st)
-                                 : launch_linattn_simt(p, dtype, mode, st);
+                                 : launch_linattn_simt(p, mode, st);
     };
     cudaError_t e = cudaSuccess;
     if (p.g.split) {

@@ -144,9 +144,9 @@ __device__ __forceinline__ void la_decay_pow(const float* a, int h, int n, float
 }
 #endif
 
-// Launchers.  `mode` 0: the main pass; 1: the ranges' own sums into agg.
-cudaError_t launch_linattn_simt(const LaParams& p, int dtype, int mode, cudaStream_t stream);
-// The same on the tensor cores (bf16).
+// Launchers.  `mode` 0: the main pass; 1: the ranges' own sums into agg.  fp32
+// operands on the CUDA cores, bf16 ones on the tensor cores.
+cudaError_t launch_linattn_simt(const LaParams& p, int mode, cudaStream_t stream);
 cudaError_t launch_linattn_tc(const LaParams& p, int mode, cudaStream_t stream);
 // agg -> the state at each range's start, in place.
 cudaError_t launch_linattn_scan(const LaParams& p, cudaStream_t stream);

@@ -1,6 +1,6 @@
-// linattn_simt.cu -- linear attention on the CUDA cores, and the small kernels
-// shared with the tensor-core form: the scan over ranges and the sum over the
-// heads of a group.
+// linattn_simt.cu -- linear attention on the CUDA cores (fp32 operands), and the
+// small kernels shared with the tensor-core form: the scan over ranges and the sum
+// over the heads of a group.
 //
 // Per chunk of 64 tokens with i, j its rows (forwards; backwards the exponents
 // are mirrored):
@@ -9,7 +9,10 @@
 //     X <- lam^n X + s_in B^T (lam^{n-1-j} o C)
 // in fp32 FMAs on shared-memory tiles: 256 threads, each with a 4 x 4 block of
 // P and of the output and an 8 x 4 block of X.  fp32 operands need it: a TF32
-// product keeps 11 bits of them.
+// product keeps 11 bits of them.  Bound by the FMAs and their shared-memory
+// operands: 85 us for 2 x 2048 tokens, 8 heads of 64 x 64, in three launches of
+// 28 (the ranges' own sums), 9 (scan) and 55 us.  Ranges go down to 128 tokens
+// here (186 us with 512): two chunks each keep 256 CTAs busy, two on an SM.
 #include "linattn_internal.cuh"
 
 namespace ssd {
@@ -18,16 +21,25 @@ namespace {
 constexpr int kC = 64;            // tokens per chunk
 constexpr int kPitch = kC + 4;    // floats per row of a tile with kC columns
 constexpr int kThreads = 256;
-constexpr int kMaxK = 128;
 
+// Tiles by the head sizes of the call, so that two CTAs share an SM for DK <= 64.
 struct Smem {
-    float At[kMaxK * kPitch];     // A transposed: [k][i]
-    float Bt[kMaxK * kPitch];     // B transposed: [k][j]
-    float X[kMaxK * kPitch];      // state [k][v]
-    float Cv[kC * kPitch];        // C: [j][v]
-    float Pt[kC * kPitch];        // P transposed: [j][i]
-    float lamp[kC + 1];           // lam^0 .. lam^64
-    LaRange rg;
+    float *Bt, *X, *Cv;       // B transposed [k][j]; state [k][v]; C [j][v]
+    float *At, *Pt;           // A transposed [k][i]; P transposed [j][i] (main pass only)
+    float* lamp;              // lam^0 .. lam^64
+    LaRange* rg;
+    __device__ Smem(float* base, int dk, bool agg) {
+        Bt = base;
+        X = Bt + dk * kPitch;
+        Cv = X + dk * kPitch;
+        At = Cv + kC * kPitch;
+        Pt = At + (agg ? 0 : dk * kPitch);
+        lamp = Pt + (agg ? 0 : kC * kPitch);
+        rg = reinterpret_cast<LaRange*>(lamp + kC + 4);
+    }
+    static size_t bytes(int dk, bool agg) {
+        return ((size_t)(agg ? 2 : 3) * dk * kPitch + (agg ? 1 : 2) * kC * kPitch + kC + 4) * 4 + sizeof(LaRange);
+    }
 };
 
 __device__ __forceinline__ float4 ld4(const float* p) { return *reinterpret_cast<const float4*>(p); }
@@ -35,16 +47,9 @@ __device__ __forceinline__ void unpack(const float* p, float (&f)[4]) {
     const float4 v = __ldg(reinterpret_cast<const float4*>(p));
     f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
 }
-__device__ __forceinline__ void unpack(const __nv_bfloat16* p, float (&f)[4]) {
-    const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
-    f[0] = __uint_as_float(v.x << 16); f[1] = __uint_as_float(v.x & 0xFFFF0000u);
-    f[2] = __uint_as_float(v.y << 16); f[3] = __uint_as_float(v.y & 0xFFFF0000u);
-}
-
 // rows [t0, t0 + n) of an operand, D columns, transposed into dst[d][row]; rows
 // past n are zero (whatever memory holds there)
-template <typename T>
-__device__ __forceinline__ void load_t(float* dst, const T* src, int64_t stride, int n, int D) {
+__device__ __forceinline__ void load_t(float* dst, const float* src, int64_t stride, int n, int D) {
     const int row = threadIdx.x & (kC - 1);
     for (int d = (threadIdx.x / kC) * 4; d < D; d += (kThreads / kC) * 4) {
         float f[4] = {0.f, 0.f, 0.f, 0.f};
@@ -62,24 +67,24 @@ __device__ __forceinline__ void fma44(float (&acc)[4][4], const float4& a, const
         for (int y = 0; y < 4; ++y) acc[x][y] = fmaf(av[x], bv[y], acc[x][y]);
 }
 
-template <typename T, bool kAgg>
-__global__ void __launch_bounds__(kThreads) linattn_simt(const __grid_constant__ LaParams p) {
-    extern __shared__ __align__(16) uint8_t raw[];
-    Smem& s = *reinterpret_cast<Smem*>(raw);
+template <bool kAgg>
+__global__ void __launch_bounds__(kThreads, 2) linattn_simt(const __grid_constant__ LaParams p) {
+    extern __shared__ __align__(16) float raw[];
     const LaGeom& g = p.g;
     const LaJob& jb = p.job[blockIdx.z];
+    const Smem s(raw, jb.DK, kAgg);
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     const int nvb = (jb.DV + kLaCols - 1) / kLaCols;
     const int h = blockIdx.y / nvb, v0 = (blockIdx.y - h * nvb) * kLaCols;
     if (h >= g.H) return;
     if (tid < 32) {
         const LaRange r = la_find(g, blockIdx.x);
-        if (tid == 0) s.rg = r;
+        if (tid == 0) *s.rg = r;
     }
     const float a2 = la_log2_decay(g.a, h);
     if (tid <= kC) s.lamp[tid] = exp2f(a2 * (float)tid);
     __syncthreads();
-    const LaRange rg = s.rg;
+    const LaRange rg = *s.rg;
     if (rg.seq < 0) return;
     const int nv = min(kLaCols, jb.DV - v0);
     if (rg.seq == g.nseq) {               // tokens of no sequence: zeros
@@ -87,8 +92,7 @@ __global__ void __launch_bounds__(kThreads) linattn_simt(const __grid_constant__
         for (int i = tid; i < rg.len * nv; i += kThreads) {
             const int t = i / nv, v = i - t * nv;
             const int64_t at = ((int64_t)(rg.t0 + t) * g.H + h) * jb.DV + v0 + v;
-            if (jb.out_f32) static_cast<float*>(jb.out)[at] = 0.f;
-            else static_cast<T*>(jb.out)[at] = from_f32<T>(0.f);
+            static_cast<float*>(jb.out)[at] = 0.f;
         }
         return;
     }
@@ -103,9 +107,9 @@ __global__ void __launch_bounds__(kThreads) linattn_simt(const __grid_constant__
         const int k = i % jb.DK, v = i / jb.DK;
         s.X[k * kPitch + v] = in && v < nv ? in[(int64_t)k * jb.sk + (int64_t)(v0 + v) * jb.sv] : 0.f;
     }
-    const T* Ap = static_cast<const T*>(jb.A) + (int64_t)(h / jb.dA) * jb.DK;
-    const T* Bp = static_cast<const T*>(jb.B) + (int64_t)(h / jb.dB) * jb.DK;
-    const T* Cp = static_cast<const T*>(jb.C) + (int64_t)(h / jb.dC) * jb.DV + v0;
+    const float* Ap = static_cast<const float*>(jb.A) + (int64_t)(h / jb.dA) * jb.DK;
+    const float* Bp = static_cast<const float*>(jb.B) + (int64_t)(h / jb.dB) * jb.DK;
+    const float* Cp = static_cast<const float*>(jb.C) + (int64_t)(h / jb.dC) * jb.DV + v0;
     const int nch = (rg.len + kC - 1) / kC;
     float cf_hi, cf_lo;
     la_decay_pow(g.a, h, kC, cf_hi, cf_lo);
@@ -155,13 +159,7 @@ __global__ void __launch_bounds__(kThreads) linattn_simt(const __grid_constant__
 #pragma unroll
                 for (int y = 0; y < 4; ++y) r[y] = jb.s_out * fmaf(f, o1[x][y], o2[x][y]);
                 const int64_t at = ((int64_t)(t0 + i) * g.H + h) * jb.DV + v0 + tx * 4;
-                if (jb.out_f32) {
-                    *reinterpret_cast<float4*>(static_cast<float*>(jb.out) + at) = make_float4(r[0], r[1], r[2], r[3]);
-                } else {
-                    T* dst = static_cast<T*>(jb.out) + at;
-#pragma unroll
-                    for (int y = 0; y < 4; ++y) dst[y] = from_f32<T>(r[y]);
-                }
+                *reinterpret_cast<float4*>(static_cast<float*>(jb.out) + at) = make_float4(r[0], r[1], r[2], r[3]);
             }
         }
         // X <- lam^n X + s_in B^T (w o C); every thread reads and writes its own 8 x 4
@@ -288,26 +286,26 @@ __global__ void __launch_bounds__(256) linattn_group_sum(const float* __restrict
     dst[3] = from_f32<T>(a.w);
 }
 
-template <typename T, bool kAgg>
+template <bool kAgg>
 cudaError_t go(const LaParams& p, cudaStream_t stream) {
-    int nvb = 1;
+    int nvb = 1, dk = 0;
     for (int j = 0; j < p.njobs; ++j) {
         const int n = (p.job[j].DV + kLaCols - 1) / kLaCols;
         nvb = n > nvb ? n : nvb;
+        dk = p.job[j].DK > dk ? p.job[j].DK : dk;
     }
-    auto k = linattn_simt<T, kAgg>;
-    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem));
+    const size_t bytes = Smem::bytes(dk, kAgg);
+    auto k = linattn_simt<kAgg>;
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
     if (e != cudaSuccess) return e;
-    k<<<dim3((unsigned)p.g.range_cap, (unsigned)(p.g.H * nvb), (unsigned)p.njobs), kThreads, sizeof(Smem), stream>>>(p);
+    k<<<dim3((unsigned)p.g.range_cap, (unsigned)(p.g.H * nvb), (unsigned)p.njobs), kThreads, bytes, stream>>>(p);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_linattn_simt(const LaParams& p, int dtype, int mode, cudaStream_t stream) {
-    if (dtype == SSD_BF16)
-        return mode ? go<__nv_bfloat16, true>(p, stream) : go<__nv_bfloat16, false>(p, stream);
-    return mode ? go<float, true>(p, stream) : go<float, false>(p, stream);
+cudaError_t launch_linattn_simt(const LaParams& p, int mode, cudaStream_t stream) {
+    return mode ? go<true>(p, stream) : go<false>(p, stream);
 }
 
 cudaError_t launch_linattn_scan(const LaParams& p, cudaStream_t stream) {

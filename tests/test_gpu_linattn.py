@@ -150,6 +150,78 @@ def test_decays(dtype, decay):
     assert off(num(grads[0]), want[2]) < TOL[dtype] and off(num(grads[1]), want[3]) < TOL[dtype]
 
 
+@pytest.mark.parametrize("decay", [[-0.60, -0.66], [-0.655, -0.3]])
+def test_fast_decays_and_large_values(decay):
+    """Decays on both sides of the one up to which a chunk's decay is applied as row
+    and column factors, and values whose products leave fp16's range."""
+    lens = [300, 129]
+    x = make("bf16", lens, 2, 2, 128, 64, True, seed=9, decay=decay)
+    for n in ("q", "k", "v", "dout"):
+        x[n] = (300 * x[n].float()).bfloat16()
+    d = dev(x)
+    o, fin = ssd.linattn_fwd(d["q"], d["k"], d["v"], d["a"], cu_seqlens=d["cu"], init_state=d["S0"])
+    g = ssd.linattn_bwd(d["q"], d["k"], d["v"], d["dout"], d["a"], cu_seqlens=d["cu"],
+                        init_state=d["S0"], dfinal_state=d["dfin"])
+    sync_ok()
+    want = ref(x, lens, 128 ** -0.5, grads=True)
+    for h in range(2):
+        assert off(num(o[:, h]), want[0][:, h]) < TOL["bf16"]
+        assert off(num(fin[:, h]), want[1][:, h]) < TOL["f32"]
+        for i in range(3):
+            assert off(num(g[i][:, h]), want[2 + i][:, h]) < TOL["bf16"]
+        assert off(num(g[3][:, h]), want[5][:, h]) < TOL["f32"]
+
+
+def test_long_sequences_among_many_empty_ones():
+    """Sequences cut into ranges, many that are empty, and no bound of the lengths:
+    most of the work list has nothing to do, and every sequence's state arrives."""
+    lens = [0] * 40 + [1500] + [0] * 200 + [2100, 1] + [0] * 60
+    x = make("bf16", lens, 2, 2, 64, 64, True, seed=10)
+    d = dev(x)
+    o, fin = ssd.linattn_fwd(d["q"], d["k"], d["v"], d["a"], cu_seqlens=d["cu"], init_state=d["S0"])
+    g = ssd.linattn_bwd(d["q"], d["k"], d["v"], d["dout"], d["a"], cu_seqlens=d["cu"],
+                        init_state=d["S0"], dfinal_state=d["dfin"])
+    sync_ok()
+    want = ref(x, lens, 64 ** -0.5, grads=True)
+    assert off(num(o), want[0]) < TOL["bf16"] and off(num(fin), want[1]) < TOL["f32"]
+    for i in range(3):
+        assert off(num(g[i]), want[2 + i]) < TOL["bf16"]
+    assert off(num(g[3]), want[5]) < TOL["f32"]
+    empty = [s for s, L in enumerate(lens) if L == 0]
+    assert torch.equal(fin[empty], d["S0"][empty])
+
+
+def test_rows_far_apart():
+    """Rows whose offsets pass 2^31 elements give what a compact copy gives."""
+    T, wide = 70000, 32768
+    base = torch.empty(T, wide, dtype=torch.bfloat16, device="cuda")   # 4.6 GB
+    torch.manual_seed(0)
+    cut = lambda at, n: base[:, at:at + n]
+    q, k, v = cut(0, 64).view(T, 1, 64), cut(16384, 64).view(T, 1, 64), cut(32768 - 128, 128).view(T, 2, 64)
+    for t in (q, k, v):
+        t.copy_(torch.randn(t.shape, device="cuda"))
+    a = torch.tensor([-0.01, -0.2], device="cuda")
+    cu = torch.tensor([0, 100, 69000, 70000], dtype=torch.int32, device="cuda")
+    o, fin = ssd.linattn_fwd(q, k, v, a, cu_seqlens=cu)
+    o1, fin1 = ssd.linattn_fwd(q.contiguous(), k.contiguous(), v.contiguous(), a, cu_seqlens=cu)
+    sync_ok()
+    assert torch.equal(o, o1) and torch.equal(fin, fin1)
+
+
+def test_cache_past_32_bits():
+    """A slot whose offset passes 2^31 elements of the cache."""
+    H, V, K, nslots = 32, 128, 128, 4200
+    cache = torch.empty(nslots, H, V, K, device="cuda")                # 8.8 GB
+    x = make("bf16", [1, 1], H, H, K, V, True, seed=11)
+    d = dev(x)
+    slots = torch.tensor([nslots - 1, 3], dtype=torch.int32, device="cuda")
+    cache[slots.long()] = d["S0"]
+    o = ssd.linattn_step(d["q"], d["k"], d["v"], d["a"], cache, slots=slots)
+    small = d["S0"].clone()
+    o1 = ssd.linattn_step(d["q"], d["k"], d["v"], d["a"], small)
+    assert torch.equal(o, o1) and torch.equal(cache[slots.long()], small)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_other_rows_do_not_leak(dtype):
     """NaN and infinities in another sequence and in rows of no sequence; the
