@@ -109,13 +109,8 @@ __device__ __forceinline__ void sts32(uint32_t a, float v) {
     asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
 }
 __device__ __forceinline__ void bar_p() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
-// mbar_wait with its slow path out of line: the roles' loops share the
-// instruction cache.
-__device__ __noinline__ void wait_slow(uint32_t bar, uint32_t parity, unsigned int* err) {
-    mbar_wait(bar, parity, err, 1u);
-}
 __device__ __forceinline__ void wait_on(uint32_t bar, uint32_t parity, unsigned int* err) {
-    if (!mbar_try_wait(bar, parity)) wait_slow(bar, parity, err);
+    mbar_wait(bar, parity, err, 1u);
 }
 
 __device__ __forceinline__ bool factored(float a2) { return a2 * -127.f <= kSpan; }
@@ -161,7 +156,7 @@ struct Item {
 static_assert(sizeof(Item) == 64, "two slots of 64 bytes");
 
 template <bool kAgg>
-__device__ __noinline__ void decode_item(const TcParams& tp, int it, Item* slot) {
+__device__ __forceinline__ void decode_item(const TcParams& tp, int it, Item* slot) {
     Item r;
     const int vb = it % tp.nvb;
     int x = it / tp.nvb;
@@ -351,7 +346,7 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                         if (x >= 0) {
                             const int t = t0 + (rev ? nch - 1 - x : x) * kC;
                             const uint32_t st = smem_u32(smem) + s * kStage, fab = smem_u32(b_fab + s);
-                            mbar_wait(smem_u32(b_eab + s), ((cc >> 1) & 1) ^ 1, err, 1u);
+                            wait_on(smem_u32(b_eab + s), ((cc >> 1) & 1) ^ 1, err);
                             mbar_arrive_expect_tx(fab, (kAgg ? 1 : 2) * ka * kAtom);
                             for (int a = 0; a < ka; ++a) {
                                 if (!kAgg) tma_load_3d(st + a * kAtom, m + 0, fab, a * 64, ha, t);
@@ -361,7 +356,7 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                         if (x + 1 < nch) {
                             const int t = t0 + (rev ? nch - 2 - x : x + 1) * kC, c1 = cc + 1, s3 = c1 % kCs;
                             const uint32_t fc = smem_u32(b_fc) + 8 * s3;
-                            mbar_wait(smem_u32(b_ec) + 8 * s3, ((c1 / kCs) & 1) ^ 1, err, 1u);
+                            wait_on(smem_u32(b_ec) + 8 * s3, ((c1 / kCs) & 1) ^ 1, err);
                             mbar_arrive_expect_tx(fc, kAtom);
                             tma_load_3d(smem_u32(ctile) + s3 * kAtom, m + 2, fc, v0, hc, t);
                         }
@@ -401,7 +396,7 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                     bool w_due = !kAgg && x + 1 < nch;
                     const auto w_product = [&]() {
                         w_due = false;
-                        mbar_wait(smem_u32(b_fab + s1), use1 & 1, err, 1u);
+                        wait_on(smem_u32(b_fab + s1), use1 & 1, err);
                         tc_fence_after();
                         mma_steps<true, true>(tmem + kW + s1 * 128, smem_desc_sw128(st1, 16, 8 * kRow),
                                               smem_desc_sw128(st1 + kB, 16, 8 * kRow), ks, kIdW);
@@ -419,15 +414,15 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                         }
                     };
                     if (x >= 0) {
-                        if (kAgg) mbar_wait(smem_u32(b_fab + s), use & 1, err, 1u);
+                        if (kAgg) wait_on(smem_u32(b_fab + s), use & 1, err);
                         // U = B^T (scaled C), its three terms side by side: B is read once
-                        mbar_wait(smem_u32(b_vready), cc & 1, err, 1u);
-                        if (kUb == 2) mbar_wait(smem_u32(b_ufree + s), (use & 1) ^ 1, err, 1u);
-                        else mbar_wait(smem_u32(b_ufree), (cc & 1) ^ 1, err, 1u);
+                        wait_on(smem_u32(b_vready), cc & 1, err);
+                        if (kUb == 2) wait_on(smem_u32(b_ufree + s), (use & 1) ^ 1, err);
+                        else wait_on(smem_u32(b_ufree), (cc & 1) ^ 1, err);
                         tc_fence_after();
                         u_half(0);
                         mma_commit(smem_u32(b_udone));
-                        mbar_wait(smem_u32(b_vready + 1), cc & 1, err, 1u);
+                        wait_on(smem_u32(b_vready + 1), cc & 1, err);
                         tc_fence_after();
                         u_half(1);
                         mma_commit(smem_u32(b_udone + 1));
@@ -441,16 +436,16 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                             // the tensor pipe has work while the last out is read
                             if (w_due && fac && mbar_try_wait(smem_u32(b_fab + s1), use1 & 1)) w_product();
                             // out = A X
-                            mbar_wait(smem_u32(b_sready), cc & 1, err, 1u);
-                            mbar_wait(smem_u32(b_ofree), (cc & 1) ^ 1, err, 1u);
+                            wait_on(smem_u32(b_sready), cc & 1, err);
+                            wait_on(smem_u32(b_ofree), (cc & 1) ^ 1, err);
                             tc_fence_after();
                             mma_steps<true, false>(tmem + kO, smem_desc_sw128(st, 16, 8 * kRow),
                                                    smem_desc_sw128(smem_u32(xs), 8 * kRow, 8 * kRow), ks, kIdO);
                             mma_commit(smem_u32(b_xdone));
                             mma_commit(smem_u32(b_eab + s));
                             // out += P C; in the exact form, beside P's columns in W's buffer
-                            mbar_wait(smem_u32(b_fc) + 8 * (cc % kCs), (cc / kCs) & 1, err, 1u);
-                            mbar_wait(smem_u32(b_pready + s), use & 1, err, 1u);
+                            wait_on(smem_u32(b_fc) + 8 * (cc % kCs), (cc / kCs) & 1, err);
+                            wait_on(smem_u32(b_pready + s), use & 1, err);
                             tc_fence_after();
                             const uint64_t bd = smem_desc_sw128(smem_u32(ctile) + (cc % kCs) * kAtom, 8 * kRow, 8 * kRow);
                             const uint32_t to = tmem + (fac ? kO : kW + s * 128 + 64);
