@@ -109,8 +109,22 @@ __device__ __forceinline__ void sts32(uint32_t a, float v) {
     asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
 }
 __device__ __forceinline__ void bar_p() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+// mbar_wait (the same bounds) in as few instructions as it takes: the roles' loops
+// share the instruction cache, and there are two dozen waits in them.
 __device__ __forceinline__ void wait_on(uint32_t bar, uint32_t parity, unsigned int* err) {
-    mbar_wait(bar, parity, err, 1u);
+    if (mbar_try_wait(bar, parity)) return;
+    const uint32_t t0 = (uint32_t)clock();
+#pragma unroll 1
+    while (!mbar_try_wait(bar, parity)) {
+        const uint32_t dt = (uint32_t)clock() - t0;
+        if (dt > (uint32_t)kWaitSlowCycles) {
+            volatile unsigned int* e = err;
+            if (*e != 0u || dt > (uint32_t)kWaitLimitCycles) {
+                *e = 1u;
+                return;
+            }
+        }
+    }
 }
 
 __device__ __forceinline__ bool factored(float a2) { return a2 * -127.f <= kSpan; }
