@@ -53,20 +53,37 @@ ssd_status make_la(const ssd_linattn_dims* d, bool packed, bool backward, La* p)
     g.nseq = (int)p->n; g.H = (int)p->H; g.T = (int)p->T;
     g.L = packed || p->n == 0 ? 0 : (int)(p->T / p->n);
     g.a = nullptr;
-    // A sequence is cut only if it is longer than what an SM gets when the work is
-    // spread evenly, into ranges of half of that (so that the one taken last adds at
-    // most half), none shorter than 512 tokens (fp32: 128): ranges pay a second reading of two
-    // operands and gain the whole GPU.
+    // A sequence is cut into ranges where a chain of its whole length would keep the
+    // other SMs waiting: if it is longer than what an SM gets when the work is spread
+    // evenly and longer by more than the cut costs, which reads two operands twice
+    // (another 0.4 of the share) and launches twice more (about 6 chunks' time;
+    // without that margin, 1280 tokens on 150 chains took 66 us cut and 31 whole).
     const int64_t kb = (p->K + kLaCols - 1) / kLaCols, vb = (p->V + kLaCols - 1) / kLaCols;
     const int64_t cols = backward ? 2 * kb + vb : vb;
-    const int64_t share = p->T * p->H * cols / sm_count();
-    int64_t R = share / 2;
-    R = (R + 127) / 128 * 128;
+    const int64_t sms = sm_count(), share = p->T * p->H * cols / sms;
     const int64_t least = d->dtype == SSD_F32 ? 128 : 512;   // fp32 chunks take longer
-    if (R < least) R = least;
     int64_t longest = packed ? (d->max_seqlen ? d->max_seqlen : p->T) : g.L;
     if (longest > p->T) longest = p->T;
-    g.split = longest > R && longest > share;
+    int64_t R = (share / 2 + 127) / 128 * 128;
+    if (R < least) R = least;
+    g.split = longest > R && longest > share + (d->dtype == SSD_F32 ? 0 : share / 2 + 768);
+    // Half a share, so that the range taken last adds at most half; where the lengths
+    // are known, the number of ranges that fills the SMs in the shortest time (a range
+    // costs 2 chunks more than its own): one sequence of 65536 tokens on 24 chains in
+    // 12.7 ranges of half a share left a third round of 8 items, 234 us instead of 190.
+    if (g.split && (p->n == 1 || !packed)) {
+        const int64_t L = packed ? p->T : g.L, slots = sms * (d->dtype == SSD_F32 ? 2 : 1);
+        int64_t best = INT64_MAX;
+        for (int64_t n = 2; n <= 64; ++n) {
+            const int64_t r = ((L + n - 1) / n + 127) / 128 * 128;
+            if (r < least) break;
+            const int64_t cost = (p->n * p->H * cols * n + slots - 1) / slots * (r / 128 + 2);
+            if (cost < best) {
+                best = cost;
+                R = r;
+            }
+        }
+    }
     g.R = g.split ? (int)R : (int)(p->T > 0 ? (p->T + 127) / 128 * 128 : 128);
     const int64_t cap = g.split ? p->T / R + p->n + 1 : p->n + 1;
     if (cap > (1LL << 24)) return SSD_ERR_SHAPE;

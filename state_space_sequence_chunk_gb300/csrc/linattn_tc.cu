@@ -612,8 +612,7 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                     wait_on(smem_u32(b_fab + s), (c >> 1) & 1, err);
                     if (row >= n) {   // nothing of such a row may reach a product
 #pragma unroll 1
-                        for (int ch = ch0; ch < ch0 + 4; ++ch)
-{
+                        for (int ch = ch0; ch < ch0 + 4; ++ch) {
                             const int at = row * kRow + (ch << 4);
                             sts128(st + kB + at, 0u, 0u, 0u, 0u);
                             sts128(st + kB + kAtom + at, 0u, 0u, 0u, 0u);
