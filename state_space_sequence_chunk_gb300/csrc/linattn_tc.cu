@@ -239,7 +239,9 @@ __device__ __forceinline__ void mma_steps(uint32_t d, uint64_t a, uint64_t b, in
     }
 }
 
-template <bool kAgg>
+// kPart: some job's outputs are fp32, for a sum over a group's heads.  (Without
+// them the code is shorter, which the other calls feel.)
+template <bool kAgg, bool kPart>
 __global__ void __launch_bounds__(kThreads, 1)
 linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps maps) {
     // aligned by declaration, not by arithmetic: its addresses are then constants
@@ -395,25 +397,29 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
         constexpr uint32_t kIdW = make_idesc(1, 128, 128, 0, 0);
         constexpr uint32_t kIdO = make_idesc(1, 128, 64, 0, 1);
         constexpr uint32_t kIdU = make_idesc(1, 128, 64 * kTerms, 1, 1);
+        bool ahead = false;   // the item's first W has been issued with the item before it
 #pragma unroll 1
         while (read_item(im)) {
             const int nch = uniform(im.nch), ks = uniform(tp.p.job[im.job].DK / 16);
             const int fac = uniform(factored(im.a2) ? 1 : 0);
+            // x = -1: the W of the item's first chunk
+            const int x0 = kAgg || ahead ? 0 : -1;
+            ahead = false;
             if (elect_one()) {
-                // x = -1: the W of the item's first chunk
 #pragma unroll 1
-                for (int x = kAgg ? 0 : -1; x < nch; ++x) {
+                for (int x = x0; x < nch; ++x) {
                     const int cc = c + x, s = cc & 1, use = cc >> 1;
                     const uint32_t st = smem_u32(smem) + s * kStage;
                     const int s1 = s ^ 1, use1 = (cc + 1) >> 1;
                     const uint32_t st1 = smem_u32(smem) + s1 * kStage;
                     bool w_due = !kAgg && x + 1 < nch;
+                    int ks_w = ks;
                     const auto w_product = [&]() {
                         w_due = false;
                         wait_on(smem_u32(b_fab + s1), use1 & 1, err);
                         tc_fence_after();
                         mma_steps<true, true>(tmem + kW + s1 * 128, smem_desc_sw128(st1, 16, 8 * kRow),
-                                              smem_desc_sw128(st1 + kB, 16, 8 * kRow), ks, kIdW);
+                                              smem_desc_sw128(st1 + kB, 16, 8 * kRow), ks_w, kIdW);
                         mma_commit(smem_u32(b_wdone + s1));
                     };
                     const auto u_half = [&](int half) {
@@ -448,6 +454,14 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                             // W of the next chunk, if its tiles are there (and the exact form
                             // does not hold its buffer): P is then built a chunk ahead, and
                             // the tensor pipe has work while the last out is read
+                            if (x + 1 == nch && mbar_try_wait(smem_u32(b_iready + (k_item & 1)), (k_item >> 1) & 1)) {
+                                // the first W of the next item, if that is known by now
+                                const uint4 q1 = lds128(smem_u32(items) + (k_item & 1) * 64 + 16);
+                                if ((int)q1.w > 0) {
+                                    w_due = ahead = true;
+                                    ks_w = tp.p.job[q1.x].DK / 16;
+                                }
+                            }
                             if (w_due && fac && mbar_try_wait(smem_u32(b_fab + s1), use1 & 1)) w_product();
                             // out = A X
                             wait_on(smem_u32(b_sready), cc & 1, err);
@@ -475,100 +489,99 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                 }
             }
             __syncwarp();
+            ahead = __any_sync(0xffffffffu, ahead);
             c += nch;
         }
-    } else if (warp < 8) {
+    } else if (!kAgg && warp < 8) {
         // ===================== P =====================
-        if (!kAgg) {
-            const int quad = warp & 3, row = quad * 32 + lane;
-            const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
+        const int quad = warp & 3, row = quad * 32 + lane;
+        const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
 #pragma unroll 1
-            while (read_item(im)) {
-                if (im.nch == 0) continue;
-                const LaJob& jb = tp.p.job[im.job];
-                const float a2 = im.a2;
-                const bool fac = factored(a2);
-                bar_p();                        // the table's last readers are done
-                // factored: lam^{mid-j'} s_in; exact: lam^j (the first 32 are used) and,
-                // from 32 on, lam^{31-j}
-                if (warp < 4) sts32(ptab + 4 * row, fac ? la_exp2(a2, kMid - (jb.rev ? kC - 1 - row : row)) * jb.s_in
-                                          : exp2f(a2 * (float)(row < 32 ? row : max(63 - row, 0))));
-                bar_p();
-                const uint32_t vt = jb.rev ? ptab : ptab + 32 * 4;
+        while (read_item(im)) {
+            if (im.nch == 0) continue;
+            const LaJob& jb = tp.p.job[im.job];
+            const float a2 = im.a2;
+            const bool fac = factored(a2);
+            bar_p();                        // the table's last readers are done
+            // factored: lam^{mid-j'} s_in; exact: lam^j (the first 32 are used) and,
+            // from 32 on, lam^{31-j}
+            if (warp < 4) sts32(ptab + 4 * row, fac ? la_exp2(a2, kMid - (jb.rev ? kC - 1 - row : row)) * jb.s_in
+                                      : exp2f(a2 * (float)(row < 32 ? row : max(63 - row, 0))));
+            bar_p();
+            const uint32_t vt = jb.rev ? ptab : ptab + 32 * 4;
 #pragma unroll 1
-                for (int x = 0; x < im.nch; ++x, ++c) {
-                    const int s = c & 1, ci = jb.rev ? im.nch - 1 - x : x;
-                    const int n = min(kC, im.len - ci * kC);
-                    wait_on(smem_u32(b_wdone + s), (c >> 1) & 1, err);
-                    tc_fence_after();
-                    const uint32_t base = tmem + lane_off + kW + s * 128;
-                    // 16 columns at a time, in place: each half's packed columns lie
-                    // within its own and behind its reads.  (The exact form needs the
-                    // upper half's columns for its second accumulator, so one warpgroup
-                    // packs all into the lower.)
-                    const int b0 = warp < 4 ? 0 : fac ? 4 : 8, b1 = warp < 4 && fac ? 4 : 8;
+            for (int x = 0; x < im.nch; ++x, ++c) {
+                const int s = c & 1, ci = jb.rev ? im.nch - 1 - x : x;
+                const int n = min(kC, im.len - ci * kC);
+                wait_on(smem_u32(b_wdone + s), (c >> 1) & 1, err);
+                tc_fence_after();
+                const uint32_t base = tmem + lane_off + kW + s * 128;
+                // 16 columns at a time, in place: each half's packed columns lie
+                // within its own and behind its reads.  (The exact form needs the
+                // upper half's columns for its second accumulator, so one warpgroup
+                // packs all into the lower.)
+                const int b0 = warp < 4 ? 0 : fac ? 4 : 8, b1 = warp < 4 && fac ? 4 : 8;
 #pragma unroll 1
-                    for (int b = b0; b < b1; ++b) {
-                        const int rel = jb.rev ? (b >> 1) - quad : quad - (b >> 1);
-                        uint32_t o[8];
-                        if (rel < 0) {
+                for (int b = b0; b < b1; ++b) {
+                    const int rel = jb.rev ? (b >> 1) - quad : quad - (b >> 1);
+                    uint32_t o[8];
+                    if (rel < 0) {
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) o[e] = 0u;
-                        } else {
-                            const int j0 = b * 16;
-                            uint32_t v[16];
-                            __syncwarp();
-                            tmem_ld_x16(base + j0, v);
-                            if (fac || rel > 0) {
-                                const uint32_t ct = fac ? ptab + 4 * j0 : vt + 4 * (j0 & 31);
-                                // exact: lam^{i-j} as a row factor times a column factor, both <= 1
-                                const float u = fac ? 1.f : exp2f(a2 * (float)(jb.rev ? (j0 & ~31) - row : row - (j0 & ~31) - 31)) * jb.s_in;
-                                const f32x2 u2 = pair(u, u);
-                                tmem_wait_ld();
+                        for (int e = 0; e < 8; ++e) o[e] = 0u;
+                    } else {
+                        const int j0 = b * 16;
+                        uint32_t v[16];
+                        __syncwarp();
+                        tmem_ld_x16(base + j0, v);
+                        if (fac || rel > 0) {
+                            const uint32_t ct = fac ? ptab + 4 * j0 : vt + 4 * (j0 & 31);
+                            // exact: lam^{i-j} as a row factor times a column factor, both <= 1
+                            const float u = fac ? 1.f : exp2f(a2 * (float)(jb.rev ? (j0 & ~31) - row : row - (j0 & ~31) - 31)) * jb.s_in;
+                            const f32x2 u2 = pair(u, u);
+                            tmem_wait_ld();
 #pragma unroll
-                                for (int e4 = 0; e4 < 4; ++e4) {
-                                    const uint4 t = lds128(ct + 16 * e4);
-                                    f32x2 r0 = mul2(pair(v[4 * e4], v[4 * e4 + 1]), pair(t.x, t.y));
-                                    f32x2 r1 = mul2(pair(v[4 * e4 + 2], v[4 * e4 + 3]), pair(t.z, t.w));
-                                    if (!fac) {
-                                        r0 = mul2(r0, u2);
-                                        r1 = mul2(r1, u2);
-                                    }
-                                    o[2 * e4] = pack2(r0);
-                                    o[2 * e4 + 1] = pack2(r1);
+                            for (int e4 = 0; e4 < 4; ++e4) {
+                                const uint4 t = lds128(ct + 16 * e4);
+                                f32x2 r0 = mul2(pair(v[4 * e4], v[4 * e4 + 1]), pair(t.x, t.y));
+                                f32x2 r1 = mul2(pair(v[4 * e4 + 2], v[4 * e4 + 3]), pair(t.z, t.w));
+                                if (!fac) {
+                                    r0 = mul2(r0, u2);
+                                    r1 = mul2(r1, u2);
                                 }
-                            } else {
-                                tmem_wait_ld();
-#pragma unroll
-                                for (int e = 0; e < 8; ++e) {
-                                    const int d = (j0 & 31) + 2 * e - lane;   // above the diagonal: masked below
-                                    o[e] = pack2(mul2(pair(v[2 * e], v[2 * e + 1]),
-                                                      pair(lds32(ptab + 4 * ((jb.rev ? d : -d) & 31)) * jb.s_in,
-                                                           lds32(ptab + 4 * ((jb.rev ? d + 1 : -d - 1) & 31)) * jb.s_in)));
-                                }
+                                o[2 * e4] = pack2(r0);
+                                o[2 * e4 + 1] = pack2(r1);
                             }
-                            // a select, never a product, drops what is above the diagonal
-                            // or (backwards) past the chunk's tokens: columns lo .. hi stay
-                            if (rel == 0 || (n < kC && jb.rev)) {
-                                const int lo = (jb.rev && rel == 0 ? row : 0) - j0;
-                                const int hi = (jb.rev ? n - 1 : rel == 0 ? row : kC) - j0;
+                        } else {
+                            tmem_wait_ld();
 #pragma unroll
-                                for (int e = 0; e < 8; ++e) {
-                                    if (2 * e < lo || 2 * e > hi) o[e] &= 0xFFFF0000u;
-                                    if (2 * e + 1 < lo || 2 * e + 1 > hi) o[e] &= 0x0000FFFFu;
-                                }
+                            for (int e = 0; e < 8; ++e) {
+                                const int d = (j0 & 31) + 2 * e - lane;   // above the diagonal: masked below
+                                o[e] = pack2(mul2(pair(v[2 * e], v[2 * e + 1]),
+                                                  pair(lds32(ptab + 4 * ((jb.rev ? d : -d) & 31)) * jb.s_in,
+                                                       lds32(ptab + 4 * ((jb.rev ? d + 1 : -d - 1) & 31)) * jb.s_in)));
                             }
                         }
-                        __syncwarp();
-                        tmem_st_x8(base + b * 8 + (b0 == 4 ? 32 : 0), o);
+                        // a select, never a product, drops what is above the diagonal
+                        // or (backwards) past the chunk's tokens: columns lo .. hi stay
+                        if (rel == 0 || (n < kC && jb.rev)) {
+                            const int lo = (jb.rev && rel == 0 ? row : 0) - j0;
+                            const int hi = (jb.rev ? n - 1 : rel == 0 ? row : kC) - j0;
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                if (2 * e < lo || 2 * e > hi) o[e] &= 0xFFFF0000u;
+                                if (2 * e + 1 < lo || 2 * e + 1 > hi) o[e] &= 0x0000FFFFu;
+                            }
+                        }
                     }
-                    tmem_wait_st();
-                    tc_fence_before();
-                    mbar_arrive(smem_u32(b_pready + s));
+                    __syncwarp();
+                    tmem_st_x8(base + b * 8 + (b0 == 4 ? 32 : 0), o);
                 }
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(smem_u32(b_pready + s));
             }
         }
-    } else if (warp < 16) {
+    } else if (warp >= 8 && warp < 16) {
         // ===================== scaled terms of C =====================
 
         // a warpgroup has half of the tokens, a thread half of a token's columns
@@ -637,7 +650,7 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                 mbar_arrive(smem_u32(b_vready + half));
             }
         }
-    } else if (warp < 24) {
+    } else if (warp >= 16 && warp < 24) {
         // ===================== X =====================
 
         const int k = (warp & 3) * 32 + lane;           // X's row = tensor-memory lane
@@ -663,7 +676,7 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
             const bool fac = factored(a2);
 #pragma unroll 1
             for (int x = 0; x < im.nch; ++x, ++c) {
-                const int s = c & 1, ci = jb.rev ? im.nch - 1 - x : x;
+                const int ci = jb.rev ? im.nch - 1 - x : x;
                 const int n = min(kC, im.len - ci * kC);
                 if (!kAgg) {
                     // in the factored form the row factor of out is lam^{i'}
@@ -718,7 +731,7 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
             }
             __syncwarp();
         }
-    } else if (!kAgg) {
+    } else if (!kAgg && warp >= 24) {
         // ===================== out =====================
         const int i = (warp - 24) * 32 + lane;
         const uint32_t lane_off = (uint32_t)((warp - 24) * 32) << 16;
@@ -726,13 +739,14 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
         while (read_item(im)) {
             const LaJob& jb = tp.p.job[im.job];
             const int nv = min(kLaCols, jb.DV - im.v0);
+            const bool f32o = kPart && jb.out_f32;
             const int64_t os = (int64_t)g.H * jb.DV, oh = (int64_t)im.h * jb.DV + im.v0;
             if (im.seq == g.nseq) {                   // tokens of no sequence: zeros
                 for (int x = i; x < im.len * (nv / 16); x += 128) {
                     const int64_t e = (int64_t)(im.t0 + x / (nv / 16)) * os + oh + x % (nv / 16) * 16;
-                    uint4* d = jb.out_f32 ? reinterpret_cast<uint4*>(static_cast<float*>(jb.out) + e)
+                    uint4* d = f32o ? reinterpret_cast<uint4*>(static_cast<float*>(jb.out) + e)
                                           : reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(jb.out) + e);
-                    for (int q = 0; q < (jb.out_f32 ? 4 : 2); ++q) d[q] = make_uint4(0u, 0u, 0u, 0u);
+                    for (int q = 0; q < (f32o ? 4 : 2); ++q) d[q] = make_uint4(0u, 0u, 0u, 0u);
                 }
             }
             const float a2 = im.a2;
@@ -752,14 +766,14 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                 // took a fifth of the shared-memory and L1 data path that bounds the
                 // kernel.  The rows behind a ragged chunk's belong to others, so that
                 // one is stored row by row.
-                const bool tile = n == kC && !jb.out_f32;
+                const bool tile = n == kC && (fac || !f32o);
                 const uint32_t ct = smem_u32(ctile) + (c % kCs) * kAtom;
                 const auto put = [&](int b, const uint32_t (&w)[8], const f32x2 (&r)[8]) {   // 16 columns
                     if (tile) {
                         sts128(ct + i * kRow + (((2 * b) ^ (i & 7)) << 4), w[0], w[1], w[2], w[3]);
                         sts128(ct + i * kRow + (((2 * b + 1) ^ (i & 7)) << 4), w[4], w[5], w[6], w[7]);
                     } else if (i < n && b * 16 < nv) {
-                        if (jb.out_f32) {
+                        if (f32o) {
                             ulonglong2* d = reinterpret_cast<ulonglong2*>(static_cast<float*>(jb.out) + e0 + b * 16);
 #pragma unroll
                             for (int y = 0; y < 4; ++y) d[y] = make_ulonglong2(r[2 * y], r[2 * y + 1]);
@@ -782,6 +796,27 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                         if (hf == 1) {
                             tc_fence_before();
                             mbar_arrive(smem_u32(b_ofree));
+                        }
+                        if (f32o) {   // 32 columns fill the tile: in two turns
+                            if (hf == 1) asm volatile("bar.sync 2, 128;" ::: "memory");
+#pragma unroll
+                            for (int q = 0; q < 8; ++q) {
+                                const f32x2 r0 = mul2(f2, pair(p[4 * q], p[4 * q + 1]));
+                                const f32x2 r1 = mul2(f2, pair(p[4 * q + 2], p[4 * q + 3]));
+                                sts128(ct + i * kRow + ((q ^ (i & 7)) << 4), (uint32_t)r0, (uint32_t)(r0 >> 32),
+                                       (uint32_t)r1, (uint32_t)(r1 >> 32));
+                            }
+                            if (hf == 0) {
+                                fence_proxy_async_smem();
+                                asm volatile("bar.sync 2, 128;" ::: "memory");
+                                if (warp == 24 && lane == 0) {
+                                    tma_store_3d(maps.m[im.job] + 3, ct, im.v0, im.h, im.t0 + ci * kC);
+                                    bulk_commit_group();
+                                    bulk_wait_group_read0();
+                                }
+                                __syncwarp();
+                            }
+                            continue;
                         }
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
@@ -820,9 +855,13 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                 asm volatile("bar.sync 2, 128;" ::: "memory");
                 if (warp == 24 && lane == 0) {
                     if (tile) {
-                        tma_store_3d(maps.m[im.job] + 3, ct, im.v0, im.h, im.t0 + ci * kC);
-                        bulk_commit_group();
-                        bulk_wait_group_read0();
+                        // columns past DV are cut off, but a tile may not start there
+                        const int v1 = im.v0 + (f32o ? 32 : 0);
+                        if (v1 < jb.DV) {
+                            tma_store_3d(maps.m[im.job] + 3, ct, v1, im.h, im.t0 + ci * kC);
+                            bulk_commit_group();
+                            bulk_wait_group_read0();
+                        }
                     }
                     mbar_arrive(smem_u32(b_ec) + 8 * (c % kCs));
                 }
@@ -841,12 +880,13 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
     }
 }
 
-bool encode(CUtensorMap* m, const void* base, int D, int heads, int64_t stride, int T) {
+bool encode(CUtensorMap* m, const void* base, int D, int heads, int64_t stride, int T, bool f32 = false) {
+    const uint64_t es = f32 ? 4 : 2;
     const uint64_t dims[3] = {(uint64_t)D, (uint64_t)heads, (uint64_t)T};
-    const uint64_t str[2] = {(uint64_t)D * 2, (uint64_t)stride * 2};
-    const uint32_t box[3] = {64, 1, kC};
-    return encode_tmap(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, str, box,
-                       CU_TENSOR_MAP_SWIZZLE_128B);
+    const uint64_t str[2] = {(uint64_t)D * es, (uint64_t)stride * es};
+    const uint32_t box[3] = {f32 ? 32u : 64u, 1, kC};   // rows of 128 bytes
+    return encode_tmap(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims,
+                       str, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 }  // namespace
@@ -857,20 +897,22 @@ cudaError_t launch_linattn_tc(const LaParams& p, int mode, cudaStream_t stream) 
     tp.p = p;
     tp.nvb = 1;
     memset(&maps, 0, sizeof(maps));
+    bool part = false;
     for (int j = 0; j < p.njobs; ++j) {
         const LaJob& b = p.job[j];
         const int n = (b.DV + kLaCols - 1) / kLaCols;
         tp.nvb = n > tp.nvb ? n : tp.nvb;
+        part = part || b.out_f32;
         if (p.g.T > 0 && (!encode(&maps.m[j][0], b.A, b.DK, b.hA, b.sA, p.g.T) ||
                           !encode(&maps.m[j][1], b.B, b.DK, b.hB, b.sB, p.g.T) ||
                           !encode(&maps.m[j][2], b.C, b.DV, b.hC, b.sC, p.g.T) ||
-                          (!b.out_f32 && !encode(&maps.m[j][3], b.out, b.DV, p.g.H, (int64_t)p.g.H * b.DV, p.g.T))))
+                          !encode(&maps.m[j][3], b.out, b.DV, p.g.H, (int64_t)p.g.H * b.DV, p.g.T, b.out_f32 != 0)))
             return cudaErrorInvalidValue;
     }
     const int64_t items = (int64_t)p.g.range_cap * p.g.H * p.njobs * tp.nvb;
     if (items >= (1LL << 31)) return cudaErrorInvalidValue;
     tp.host_err = host_timeout_word();
-    auto k = mode ? linattn_tc<true> : linattn_tc<false>;
+    auto k = mode ? linattn_tc<true, false> : part ? linattn_tc<false, true> : linattn_tc<false, false>;
     const int smem = mode ? Cfg<true>::kSmem : Cfg<false>::kSmem;
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
