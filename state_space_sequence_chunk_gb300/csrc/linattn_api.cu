@@ -231,10 +231,8 @@ ssd_status ssd_linattn_bwd(const ssd_linattn_dims* d, const void* q, const void*
                       0, 1, scale, 1.f, 1, K, dfinal_state, dinit_state, agg[2]};
     cudaStream_t st = (cudaStream_t)stream;
     cudaError_t e = run_jobs(lp, d->dtype, st);
-    if (shared && p.T > 0) {
-        if (e == cudaSuccess) e = launch_linattn_group_sum(part[0], dq, p.T, G, hpg, K, d->dtype, st);
-        if (e == cudaSuccess) e = launch_linattn_group_sum(part[1], dk, p.T, G, hpg, K, d->dtype, st);
-    }
+    if (e == cudaSuccess && shared && p.T > 0)
+        e = launch_linattn_group_sum(part, dq, dk, p.T, G, hpg, K, d->dtype, st);
     return from_cuda(e);
 }
 

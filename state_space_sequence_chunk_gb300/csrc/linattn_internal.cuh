@@ -150,9 +150,9 @@ cudaError_t launch_linattn_simt(const LaParams& p, int mode, cudaStream_t stream
 cudaError_t launch_linattn_tc(const LaParams& p, int mode, cudaStream_t stream);
 // agg -> the state at each range's start, in place.
 cudaError_t launch_linattn_scan(const LaParams& p, cudaStream_t stream);
-// out[t, g, :] = sum over the group's heads of part[t, h, :], rounded to `dtype`.
-cudaError_t launch_linattn_group_sum(const float* part, void* out, int64_t T, int G, int hpg, int D,
-                                     int dtype, cudaStream_t stream);
+// out[t, g, :] = sum over the group's heads of part[t, h, :], rounded to `dtype`; two of them.
+cudaError_t launch_linattn_group_sum(const float* const part[2], void* out0, void* out1, int64_t T, int G,
+                                     int hpg, int D, int dtype, cudaStream_t stream);
 cudaError_t launch_linattn_step(const ssd_linattn_dims& d, int64_t qs, int64_t ks, int64_t vs,
                                 const void* q, const void* k, const void* v, const float* a,
                                 float scale, const int* slots, float* cache, int64_t nslots,

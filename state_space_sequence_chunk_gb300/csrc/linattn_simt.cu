@@ -265,25 +265,31 @@ __global__ void __launch_bounds__(256) linattn_scan(const __grid_constant__ LaPa
     }
 }
 
+// Both gradients of shared heads in one launch (blockIdx.y): small ones are all
+// launch latency.
 template <typename T>
-__global__ void __launch_bounds__(256) linattn_group_sum(const float* __restrict__ part,
-                                                         T* __restrict__ out, int64_t n4, int hpg,
-                                                         int d4) {
+__global__ void __launch_bounds__(256) linattn_group_sum(const float* __restrict__ part0, const float* __restrict__ part1,
+                                                         T* __restrict__ out0, T* __restrict__ out1, int64_t n4,
+                                                         int hpg, int d4) {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i >= n4) return;
     const int64_t row = i / d4;   // (token, group)
     const int col = (int)(i - row * d4);
-    const float4* src = reinterpret_cast<const float4*>(part) + row * hpg * d4 + col;
+    const float4* src = reinterpret_cast<const float4*>(blockIdx.y ? part1 : part0) + row * hpg * d4 + col;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int x = 0; x < hpg; ++x) {
         const float4 v = src[(int64_t)x * d4];
         a.x += v.x; a.y += v.y; a.z += v.z; a.w += v.w;
     }
-    T* dst = out + 4 * i;
-    dst[0] = from_f32<T>(a.x);
-    dst[1] = from_f32<T>(a.y);
-    dst[2] = from_f32<T>(a.z);
-    dst[3] = from_f32<T>(a.w);
+    T* dst = (blockIdx.y ? out1 : out0) + 4 * i;
+    if constexpr (sizeof(T) == 2) {
+        union { __nv_bfloat162 h[2]; uint2 u; } w;
+        w.h[0] = __floats2bfloat162_rn(a.x, a.y);
+        w.h[1] = __floats2bfloat162_rn(a.z, a.w);
+        *reinterpret_cast<uint2*>(dst) = w.u;
+    } else {
+        *reinterpret_cast<float4*>(dst) = a;
+    }
 }
 
 template <bool kAgg>
@@ -315,14 +321,15 @@ cudaError_t launch_linattn_scan(const LaParams& p, cudaStream_t stream) {
     return cudaGetLastError();
 }
 
-cudaError_t launch_linattn_group_sum(const float* part, void* out, int64_t T, int G, int hpg, int D,
-                                     int dtype, cudaStream_t stream) {
+cudaError_t launch_linattn_group_sum(const float* const part[2], void* out0, void* out1, int64_t T, int G,
+                                     int hpg, int D, int dtype, cudaStream_t stream) {
     const int64_t n4 = T * G * (D / 4);
-    const unsigned blocks = (unsigned)((n4 + 255) / 256);
+    const dim3 grid((unsigned)((n4 + 255) / 256), 2);
     if (dtype == SSD_BF16)
-        linattn_group_sum<__nv_bfloat16><<<blocks, 256, 0, stream>>>(part, (__nv_bfloat16*)out, n4, hpg, D / 4);
+        linattn_group_sum<__nv_bfloat16><<<grid, 256, 0, stream>>>(part[0], part[1], (__nv_bfloat16*)out0,
+                                                                   (__nv_bfloat16*)out1, n4, hpg, D / 4);
     else
-        linattn_group_sum<float><<<blocks, 256, 0, stream>>>(part, (float*)out, n4, hpg, D / 4);
+        linattn_group_sum<float><<<grid, 256, 0, stream>>>(part[0], part[1], (float*)out0, (float*)out1, n4, hpg, D / 4);
     return cudaGetLastError();
 }
 

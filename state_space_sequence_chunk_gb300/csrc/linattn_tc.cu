@@ -33,7 +33,7 @@
 //   16-23 X in registers (a thread owns 32 columns of a row): bf16 copy for A X,
 //         update with U, stored states
 //   24-27 out (a thread owns a token row)
-//   28    TMA, two stages of A, B and C tiles (80 KB each)
+//   28    TMA, two stages of A and B tiles (64 KB each), three C tiles; the next item
 //   29    MMA issue: U(c), W(c + 1), A X(c), P C(c)
 // The roles' loops are kept short (packed fp32 arithmetic, little unrolling): six
 // codes run side by side on each scheduler, and fully unrolled they spent most of
@@ -58,16 +58,17 @@ constexpr int kThreads = 960;
 constexpr int kTmaWarp = 28, kMmaWarp = 29;
 constexpr int kTerms = 3;
 constexpr int kTerm = kAtom / 2;              // a term of 64 tokens
-// What the two passes keep: C tiles, buffers for a half's terms (with one, the
-// halves take turns), accumulators for U.  The pass over the ranges' own sums
-// has no A, W and out.
+// What the two passes keep: stages of A and B, C tiles, buffers for a half's terms
+// (with one, the halves take turns), accumulators for U.  The pass over the ranges'
+// own sums has no A, W and out.
 template <bool kAgg> struct Cfg {
     static constexpr int kCs = kAgg ? 4 : 3;
+    static constexpr int kSt = kAgg ? 3 : 2;
     static constexpr int kTb = kAgg ? 2 : 1;
     static constexpr int kUb = kAgg ? 2 : 1;
     static constexpr int kB = kAgg ? 0 : 2 * kAtom;      // a stage: A (2 atoms), B (2)
     static constexpr int kStage = kB + 2 * kAtom;
-    static constexpr int kSmem = 2 * kStage + kCs * kAtom + kTb * kTerms * kTerm + (kAgg ? 0 : kAtom) + 1024;
+    static constexpr int kSmem = kSt * kStage + kCs * kAtom + kTb * kTerms * kTerm + (kAgg ? 0 : kAtom) + 1024;
     static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
 };
 // tensor memory columns
@@ -127,6 +128,8 @@ __device__ __forceinline__ void wait_on(uint32_t bar, uint32_t parity, unsigned 
     }
 }
 
+__device__ __forceinline__ void ld_cols(uint32_t at, uint32_t (&r)[4]) { tmem_ld_x4(at, r); }
+__device__ __forceinline__ void ld_cols(uint32_t at, uint32_t (&r)[8]) { tmem_ld_x8(at, r); }
 __device__ __forceinline__ bool factored(float a2) { return a2 * -127.f <= kSpan; }
 // 2^(a2 n), with the product's rounding put back: n a2 can be as large as kSpan,
 // where a rounding of the exponent would be one of the result's last bits.
@@ -254,14 +257,14 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
         }
         return;
     }
-    constexpr int kB = Cfg<kAgg>::kB, kStage = Cfg<kAgg>::kStage, kCs = Cfg<kAgg>::kCs, kTb = Cfg<kAgg>::kTb, kUb = Cfg<kAgg>::kUb;
+    constexpr int kB = Cfg<kAgg>::kB, kStage = Cfg<kAgg>::kStage, kCs = Cfg<kAgg>::kCs, kTb = Cfg<kAgg>::kTb, kSt = Cfg<kAgg>::kSt, kUb = Cfg<kAgg>::kUb;
     constexpr uint32_t kU = kAgg ? 0 : kUMain;
-    uint8_t* ctile = smem + 2 * kStage;
+    uint8_t* ctile = smem + kSt * kStage;
     uint8_t* terms = ctile + kCs * kAtom;
     uint8_t* xs = terms + kTb * kTerms * kTerm;
     uint64_t* bars = reinterpret_cast<uint64_t*>(xs + (kAgg ? 0 : kAtom));
-    uint64_t* b_fab = bars;           // [2] stage's A and B loaded (tx)
-    uint64_t* b_eab = bars + 2;       // [2] A and B read by every product (commit)
+    uint64_t* b_fab = bars;           // [3] stage's A and B loaded (tx)
+    uint64_t* b_eab = bars + 33;      // [3] A and B read by every product (commit)
     uint64_t* b_fc = bars + 4;        // [4] C tile loaded (tx)
     uint64_t* b_ec = bars + 8;        // [4] C read by every product, and out stored from it
     uint64_t* b_wdone = bars + 12;    // [2] W computed (commit)
@@ -277,16 +280,14 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
     uint64_t* b_answer = bars + 28;   // answer to an item request (tx)
     uint64_t* b_iready = bars + 29;   // [2] item decoded (1)
     uint64_t* b_ifree = bars + 31;    // [2] item read (every other warp that walks items)
-    uint32_t* holder = reinterpret_cast<uint32_t*>(bars + 33);
-    const uint32_t answer = smem_u32(bars + 34);    // 16 bytes
-    Item* items = reinterpret_cast<Item*>(bars + 36);   // [2]
-    const uint32_t ptab = smem_u32(bars + 52);      // [128] fp32: column factors of P
+    uint32_t* holder = reinterpret_cast<uint32_t*>(bars + 3);
+    const uint32_t answer = smem_u32(bars + 36);    // 16 bytes
+    Item* items = reinterpret_cast<Item*>(bars + 38);   // [2]
+    const uint32_t ptab = smem_u32(bars + 54);      // [128] fp32: column factors of P
 
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int s = 0; s < 2; ++s) {
-            mbar_init(smem_u32(b_fab + s), 1);
-            mbar_init(smem_u32(b_eab + s), 1);
             mbar_init(smem_u32(b_wdone + s), 1);
             mbar_init(smem_u32(b_pready + s), 256);
             mbar_init(smem_u32(b_vready + s), 128);
@@ -295,6 +296,10 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
             mbar_init(smem_u32(b_ufree + s), 256);
             mbar_init(smem_u32(b_iready + s), 1);
             mbar_init(smem_u32(b_ifree + s), kAgg ? 17 : kThreads / 32 - 1);
+        }
+        for (int s = 0; s < kSt; ++s) {
+            mbar_init(smem_u32(b_fab + s), 1);
+            mbar_init(smem_u32(b_eab + s), 1);
         }
         for (int s = 0; s < kCs; ++s) {
             mbar_init(smem_u32(b_fc + s), 1);
@@ -358,11 +363,11 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                     // scaled terms take the longest to prepare
 #pragma unroll 1
                     for (int x = part == 0 ? -1 : 1; x < (part == 0 ? min(nch, 1) : nch); ++x) {
-                        const int cc = c + x, s = cc & 1;
+                        const int cc = c + x, s = kSt == 2 ? cc & 1 : cc % kSt;
                         if (x >= 0) {
                             const int t = t0 + (rev ? nch - 1 - x : x) * kC;
                             const uint32_t st = smem_u32(smem) + s * kStage, fab = smem_u32(b_fab + s);
-                            wait_on(smem_u32(b_eab + s), ((cc >> 1) & 1) ^ 1, err);
+                            wait_on(smem_u32(b_eab + s), ((cc / kSt) & 1) ^ 1, err);
                             mbar_arrive_expect_tx(fab, (kAgg ? 1 : 2) * ka * kAtom);
                             for (int a = 0; a < ka; ++a) {
                                 if (!kAgg) tma_load_3d(st + a * kAtom, m + 0, fab, a * 64, ha, t);
@@ -408,8 +413,8 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
             if (elect_one()) {
 #pragma unroll 1
                 for (int x = x0; x < nch; ++x) {
-                    const int cc = c + x, s = cc & 1, use = cc >> 1;
-                    const uint32_t st = smem_u32(smem) + s * kStage;
+                    const int cc = c + x, s = cc & 1, use = cc >> 1, sb = kSt == 2 ? s : cc % kSt;
+                    const uint32_t st = smem_u32(smem) + sb * kStage;
                     const int s1 = s ^ 1, use1 = (cc + 1) >> 1;
                     const uint32_t st1 = smem_u32(smem) + s1 * kStage;
                     bool w_due = !kAgg && x + 1 < nch;
@@ -434,7 +439,7 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                         }
                     };
                     if (x >= 0) {
-                        if (kAgg) wait_on(smem_u32(b_fab + s), use & 1, err);
+                        if (kAgg) wait_on(smem_u32(b_fab + sb), (cc / kSt) & 1, err);
                         // U = B^T (scaled C), its three terms side by side: B is read once
                         wait_on(smem_u32(b_vready), cc & 1, err);
                         if (kUb == 2) wait_on(smem_u32(b_ufree + s), (use & 1) ^ 1, err);
@@ -448,7 +453,7 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                         mma_commit(smem_u32(b_udone + 1));
                         mma_commit(smem_u32(b_ux + (kUb == 2 ? s : 0)));
                         if (kAgg) {
-                            mma_commit(smem_u32(b_eab + s));
+                            mma_commit(smem_u32(b_eab + sb));
                             mma_commit(smem_u32(b_ec) + 8 * (cc % kCs));
                         } else {
                             // W of the next chunk, if its tiles are there (and the exact form
@@ -583,7 +588,6 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
         }
     } else if (warp >= 8 && warp < 16) {
         // ===================== scaled terms of C =====================
-
         // a warpgroup has half of the tokens, a thread half of a token's columns
         const int half = warp >= 12, row = half * 64 + (threadIdx.x & 63), ch0 = threadIdx.x & 64 ? 4 : 0;
 #pragma unroll 1
@@ -592,7 +596,7 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
             const float a2 = im.a2;
 #pragma unroll 1
             for (int x = 0; x < im.nch; ++x, ++c) {
-                const int s = c & 1, ci = jb.rev ? im.nch - 1 - x : x;
+                const int s = kSt == 2 ? c & 1 : c % kSt, ci = jb.rev ? im.nch - 1 - x : x;
                 const int n = min(kC, im.len - ci * kC);
                 const float w = la_exp2(a2, jb.rev ? row + 1 : max(n - 1 - row, 0)) * jb.s_in;
                 const f32x2 w2 = pair(w, w);
@@ -622,7 +626,7 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                     }
                 }
                 if (n < kC) {
-                    wait_on(smem_u32(b_fab + s), (c >> 1) & 1, err);
+                    wait_on(smem_u32(b_fab + s), (c / kSt) & 1, err);
                     if (row >= n) {   // nothing of such a row may reach a product
 #pragma unroll 1
                         for (int ch = ch0; ch < ch0 + 4; ++ch) {
@@ -652,7 +656,6 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
         }
     } else if (warp >= 16 && warp < 24) {
         // ===================== X =====================
-
         const int k = (warp & 3) * 32 + lane;           // X's row = tensor-memory lane
         const int vc = warp < 20 ? 0 : 32;              // X's columns: 32 a thread
         const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
@@ -698,19 +701,23 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                 tc_fence_after();
                 const uint32_t ub = tmem + lane_off + kU + vc + (kUb == 2 ? (c & 1) * 64 * kTerms : 0);
                 const f32x2 hi2 = pair(hi, hi), lo2 = pair(lo, lo);
+                // a wait for each 4 columns of the three terms; the pass over ranges' sums
+                // has no other work to cover it and the registers for 8 (84 -> 79 us for
+                // 24 chains of 65536 tokens)
+                constexpr int kQ = kAgg ? 8 : 4;
 #pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    uint32_t u0[4], u1[4], u2[4];
+                for (int q = 0; q < 32 / kQ; ++q) {
+                    uint32_t u0[kQ], u1[kQ], u2[kQ];
                     __syncwarp();
-                    tmem_ld_x4(ub + q * 4, u0);
-                    tmem_ld_x4(ub + 64 + q * 4, u1);
-                    tmem_ld_x4(ub + 128 + q * 4, u2);
+                    ld_cols(ub + q * kQ, u0);
+                    ld_cols(ub + 64 + q * kQ, u1);
+                    ld_cols(ub + 128 + q * kQ, u2);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
+                    for (int e = 0; e < kQ / 2; ++e) {
                         const f32x2 u = add2(pair(u0[2 * e], u0[2 * e + 1]),
                                              add2(pair(u1[2 * e], u1[2 * e + 1]), pair(u2[2 * e], u2[2 * e + 1])));
-                        f32x2& X2 = X[q * 2 + e];
+                        f32x2& X2 = X[q * (kQ / 2) + e];
                         X2 = fma2(X2, hi2, fma2(X2, lo2, u));
                     }
                 }
