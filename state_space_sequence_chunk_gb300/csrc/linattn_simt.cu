@@ -7,12 +7,17 @@
 //     P = s_in (A B^T) o lam^{i-j} [i >= j]
 //     out = s_out (P C + lam^{i+1} o (A X))
 //     X <- lam^n X + s_in B^T (lam^{n-1-j} o C)
-// in fp32 FMAs on shared-memory tiles: 256 threads, each with a 4 x 4 block of
-// P and of the output and an 8 x 4 block of X.  fp32 operands need it: a TF32
-// product keeps 11 bits of them.  Bound by the FMAs and their shared-memory
-// operands: 85 us for 2 x 2048 tokens, 8 heads of 64 x 64, in three launches of
-// 28 (the ranges' own sums), 9 (scan) and 55 us.  Ranges go down to 128 tokens
-// here (186 us with 512): two chunks each keep 256 CTAs busy, two on an SM.
+// in packed fp32 FMAs on shared-memory tiles: 256 threads, each with a 4 x 4 block of
+// P, of the output and of X (two of X for DK > 64).  fp32 operands need it: a TF32
+// product keeps 11 bits of them.  B is kept twice, transposed for P and by rows, times
+// its decays, for X: read transposed there, X's product took 10000 to 14000 cycles of
+// a chunk, and takes 3500.  Bound by instruction issue: a 64 x 64 x 64 product is 15
+// instructions for each of 64 steps, 4 warps on a scheduler (two CTAs on an SM): 3840
+// cycles, measured 3400 to 4500; the tiles' loads are another 4000 to 5000 of a chunk's
+// 20000.  70 us for 2 x 2048 tokens, 8 heads of 64 x 64, in three launches of about 18
+// (the ranges' own sums), 7 (scan) and 42 us.  Ranges go down to 128 tokens here: two
+// chunks each keep 256 CTAs busy, two on an SM.
+#include "f32x2.cuh"
 #include "linattn_internal.cuh"
 
 namespace ssd {
@@ -24,48 +29,52 @@ constexpr int kThreads = 256;
 
 // Tiles by the head sizes of the call, so that two CTAs share an SM for DK <= 64.
 struct Smem {
-    float *Bt, *X, *Cv;       // B transposed [k][j]; state [k][v]; C [j][v]
-    float *At, *Pt;           // A transposed [k][i]; P transposed [j][i] (main pass only)
+    float *X, *Cv;            // state [k][v]; C [j][v]
+    float* Bw;                // s_in lam^{n-1-j} o B [j][k], rows of dk + 4
+    float *At, *Bt, *Pt;      // A and B transposed [k][i]; P transposed [j][i] (main pass only)
     float* lamp;              // lam^0 .. lam^64
     LaRange* rg;
     __device__ Smem(float* base, int dk, bool agg) {
-        Bt = base;
-        X = Bt + dk * kPitch;
+        X = base;
         Cv = X + dk * kPitch;
-        At = Cv + kC * kPitch;
-        Pt = At + (agg ? 0 : dk * kPitch);
+        Bw = Cv + kC * kPitch;
+        At = Bw + kC * (dk + 4);
+        Bt = At + (agg ? 0 : dk * kPitch);
+        Pt = Bt + (agg ? 0 : dk * kPitch);
         lamp = Pt + (agg ? 0 : kC * kPitch);
         rg = reinterpret_cast<LaRange*>(lamp + kC + 4);
     }
     static size_t bytes(int dk, bool agg) {
-        return ((size_t)(agg ? 2 : 3) * dk * kPitch + (agg ? 1 : 2) * kC * kPitch + kC + 4) * 4 + sizeof(LaRange);
+        return ((size_t)(agg ? 1 : 3) * dk * kPitch + (size_t)kC * (dk + 4) + (agg ? 1 : 2) * kC * kPitch + kC + 4) * 4 +
+               sizeof(LaRange);
     }
 };
 
 __device__ __forceinline__ float4 ld4(const float* p) { return *reinterpret_cast<const float4*>(p); }
-__device__ __forceinline__ void unpack(const float* p, float (&f)[4]) {
-    const float4 v = __ldg(reinterpret_cast<const float4*>(p));
-    f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
-}
-// rows [t0, t0 + n) of an operand, D columns, transposed into dst[d][row]; rows
-// past n are zero (whatever memory holds there)
-__device__ __forceinline__ void load_t(float* dst, const float* src, int64_t stride, int n, int D) {
-    const int row = threadIdx.x & (kC - 1);
-    for (int d = (threadIdx.x / kC) * 4; d < D; d += (kThreads / kC) * 4) {
-        float f[4] = {0.f, 0.f, 0.f, 0.f};
-        if (row < n) unpack(src + (int64_t)row * stride + d, f);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) dst[(d + e) * kPitch + row] = f[e];
-    }
-}
+__device__ __forceinline__ void st4(float* p, const float4& v) { *reinterpret_cast<float4*>(p) = v; }
 
-__device__ __forceinline__ void fma44(float (&acc)[4][4], const float4& a, const float4& b) {
-    const float av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
+// a 4 x 4 block, in pairs along its rows
+struct Acc {
+    f32x2 v[4][2];
+    __device__ __forceinline__ Acc() {
 #pragma unroll
-    for (int x = 0; x < 4; ++x)
+        for (int x = 0; x < 4; ++x) v[x][0] = v[x][1] = 0ull;
+    }
+    __device__ __forceinline__ void fma(const float4& a, const float4& b) {
+        const float av[4] = {a.x, a.y, a.z, a.w};
+        const f32x2 b0 = pair(b.x, b.y), b1 = pair(b.z, b.w);
 #pragma unroll
-        for (int y = 0; y < 4; ++y) acc[x][y] = fmaf(av[x], bv[y], acc[x][y]);
-}
+        for (int x = 0; x < 4; ++x) {
+            const f32x2 a2 = pair(av[x], av[x]);
+            v[x][0] = fma2(a2, b0, v[x][0]);
+            v[x][1] = fma2(a2, b1, v[x][1]);
+        }
+    }
+    __device__ __forceinline__ void row(int x, float (&f)[4]) const {
+        unpair(v[x][0], f[0], f[1]);
+        unpair(v[x][1], f[2], f[3]);
+    }
+};
 
 template <bool kAgg>
 __global__ void __launch_bounds__(kThreads, 2) linattn_simt(const __grid_constant__ LaParams p) {
@@ -103,10 +112,19 @@ __global__ void __launch_bounds__(kThreads, 2) linattn_simt(const __grid_constan
     const int64_t so = ((int64_t)rg.seq * g.H + h) * elems;
     float* ag = cut ? jb.agg + ((int64_t)blockIdx.x * g.H + h) * elems : nullptr;
     const float* in = kAgg ? nullptr : (cut ? ag : (jb.init ? jb.init + so : nullptr));
-    for (int i = tid; i < jb.DK * kLaCols; i += kThreads) {
-        const int k = i % jb.DK, v = i / jb.DK;
+    // neighbouring threads along whichever of the stored state's axes is contiguous
+    const bool kfirst = jb.sk == 1;
+    const auto each = [&](const auto& f) {   // every (k, v) of the state's block
+        for (int m = 0; m < (kfirst ? jb.DK : kLaCols); m += 64) {
+            const int fast = m + (tid & 63);
+#pragma unroll 8
+            for (int slow = tid >> 6; slow < (kfirst ? kLaCols : jb.DK); slow += kThreads / 64)
+                if (!kfirst || fast < jb.DK) f(kfirst ? fast : slow, kfirst ? slow : fast);
+        }
+    };
+    each([&](int k, int v) {
         s.X[k * kPitch + v] = in && v < nv ? in[(int64_t)k * jb.sk + (int64_t)(v0 + v) * jb.sv] : 0.f;
-    }
+    });
     const float* Ap = static_cast<const float*>(jb.A) + (int64_t)(h / jb.dA) * jb.DK;
     const float* Bp = static_cast<const float*>(jb.B) + (int64_t)(h / jb.dB) * jb.DK;
     const float* Cp = static_cast<const float*>(jb.C) + (int64_t)(h / jb.dC) * jb.DV + v0;
@@ -116,97 +134,118 @@ __global__ void __launch_bounds__(kThreads, 2) linattn_simt(const __grid_constan
     for (int ci = 0; ci < nch; ++ci) {
         const int c = jb.rev ? nch - 1 - ci : ci;
         const int t0 = rg.t0 + c * kC, n = min(kC, rg.len - c * kC);
-        __syncthreads();
-        if (!kAgg) load_t(s.At, Ap + (int64_t)t0 * jb.sA, jb.sA, n, jb.DK);
-        load_t(s.Bt, Bp + (int64_t)t0 * jb.sB, jb.sB, n, jb.DK);
-        for (int i = tid; i < kC * (kLaCols / 4); i += kThreads) {
-            const int row = i / (kLaCols / 4), v = (i % (kLaCols / 4)) * 4;
-            float f[4] = {0.f, 0.f, 0.f, 0.f};
-            if (row < n && v < nv) unpack(Cp + (int64_t)(t0 + row) * jb.sC + v, f);
-            *reinterpret_cast<float4*>(s.Cv + row * kPitch + v) = make_float4(f[0], f[1], f[2], f[3]);
+        if (ci > 0) __syncthreads();
+        {
+            // every load of a tile before its first store; rows past n are zero,
+            // whatever memory holds there
+            const int row = tid & (kC - 1);
+            const bool in_n = row < n;
+            const float w = in_n ? s.lamp[jb.rev ? row + 1 : n - 1 - row] * jb.s_in : 0.f;
+            const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+            float4 cv[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int r = (tid >> 4) + 16 * e, v = (tid & 15) * 4;
+                cv[e] = r < n && v < nv ? __ldg(reinterpret_cast<const float4*>(Cp + (int64_t)(t0 + r) * jb.sC + v)) : zero;
+            }
+            for (int d0 = (tid / kC) * 4; d0 < jb.DK; d0 += 64) {
+                float4 a[4], b[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int d = d0 + 16 * e;
+                    const bool ok = in_n && d < jb.DK;
+                    b[e] = ok ? __ldg(reinterpret_cast<const float4*>(Bp + (int64_t)(t0 + row) * jb.sB + d)) : zero;
+                    if (!kAgg) a[e] = ok ? __ldg(reinterpret_cast<const float4*>(Ap + (int64_t)(t0 + row) * jb.sA + d)) : zero;
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int d = d0 + 16 * e;
+                    if (d >= jb.DK) break;
+                    st4(s.Bw + row * (jb.DK + 4) + d, make_float4(b[e].x * w, b[e].y * w, b[e].z * w, b[e].w * w));
+                    if (!kAgg) {
+                        const float av[4] = {a[e].x, a[e].y, a[e].z, a[e].w}, bv[4] = {b[e].x, b[e].y, b[e].z, b[e].w};
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            s.At[(d + x) * kPitch + row] = av[x];
+                            s.Bt[(d + x) * kPitch + row] = bv[x];
+                        }
+                    }
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) st4(s.Cv + ((tid >> 4) + 16 * e) * kPitch + (tid & 15) * 4, cv[e]);
         }
         __syncthreads();
         if (!kAgg) {
-            float acc[4][4] = {};
+            {
+                Acc acc;
 #pragma unroll 4
-            for (int k = 0; k < jb.DK; ++k)
-                fma44(acc, ld4(s.At + k * kPitch + ty * 4), ld4(s.Bt + k * kPitch + tx * 4));
+                for (int k = 0; k < jb.DK; ++k)
+                    acc.fma(ld4(s.Bt + k * kPitch + tx * 4), ld4(s.At + k * kPitch + ty * 4));
 #pragma unroll
-            for (int y = 0; y < 4; ++y) {
-                const int j = tx * 4 + y;
-                float w[4];
+                for (int y = 0; y < 4; ++y) {
+                    const int j = tx * 4 + y;
+                    float f[4];
+                    acc.row(y, f);
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const int i = ty * 4 + x, d = jb.rev ? j - i : i - j;
-                    w[x] = d >= 0 ? acc[x][y] * (s.lamp[d] * jb.s_in) : 0.f;
+                    for (int x = 0; x < 4; ++x) {
+                        const int i = ty * 4 + x, d = jb.rev ? j - i : i - j;
+                        f[x] = d >= 0 && j < n ? f[x] * (s.lamp[d] * jb.s_in) : 0.f;
+                    }
+                    st4(s.Pt + j * kPitch + ty * 4, make_float4(f[0], f[1], f[2], f[3]));
                 }
-                *reinterpret_cast<float4*>(s.Pt + j * kPitch + ty * 4) = make_float4(w[0], w[1], w[2], w[3]);
             }
-            float o1[4][4] = {}, o2[4][4] = {};
+            Acc o1, o2;
 #pragma unroll 4
             for (int k = 0; k < jb.DK; ++k)
-                fma44(o1, ld4(s.At + k * kPitch + ty * 4), ld4(s.X + k * kPitch + tx * 4));
+                o1.fma(ld4(s.At + k * kPitch + ty * 4), ld4(s.X + k * kPitch + tx * 4));
             __syncthreads();
 #pragma unroll 4
             for (int j = 0; j < kC; ++j)
-                fma44(o2, ld4(s.Pt + j * kPitch + ty * 4), ld4(s.Cv + j * kPitch + tx * 4));
+                o2.fma(ld4(s.Pt + j * kPitch + ty * 4), ld4(s.Cv + j * kPitch + tx * 4));
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
                 const int i = ty * 4 + x;
                 if (i >= n || tx * 4 >= nv) continue;
                 const float f = s.lamp[jb.rev ? n - 1 - i : i + 1];
-                float r[4];
-#pragma unroll
-                for (int y = 0; y < 4; ++y) r[y] = jb.s_out * fmaf(f, o1[x][y], o2[x][y]);
+                float r1[4], r2[4];
+                o1.row(x, r1);
+                o2.row(x, r2);
                 const int64_t at = ((int64_t)(t0 + i) * g.H + h) * jb.DV + v0 + tx * 4;
-                *reinterpret_cast<float4*>(static_cast<float*>(jb.out) + at) = make_float4(r[0], r[1], r[2], r[3]);
+                st4(static_cast<float*>(jb.out) + at,
+                    make_float4(jb.s_out * fmaf(f, r1[0], r2[0]), jb.s_out * fmaf(f, r1[1], r2[1]),
+                                jb.s_out * fmaf(f, r1[2], r2[2]), jb.s_out * fmaf(f, r1[3], r2[3])));
             }
         }
-        // X <- lam^n X + s_in B^T (w o C); every thread reads and writes its own 8 x 4
-        if (ty * 8 < jb.DK) {
-            float u[2][4][4] = {};
-            for (int j = 0; j < n; j += 4) {
-                float4 b[8], cc[4];
+        // X <- lam^n X + (w o B)^T C; every thread reads and writes its own 4 x 4 (two
+        // of them for DK > 64)
+        float hi = cf_hi, lo = cf_lo;
+        if (n < kC) la_decay_pow(g.a, h, n, hi, lo);
+        for (int k0 = ty * 4; k0 < jb.DK; k0 += 64) {
+            Acc u;
+#pragma unroll 4
+            for (int j = 0; j < kC; ++j)
+                u.fma(ld4(s.Bw + j * (jb.DK + 4) + k0), ld4(s.Cv + j * kPitch + tx * 4));
 #pragma unroll
-                for (int x = 0; x < 8; ++x) b[x] = ld4(s.Bt + (ty * 8 + x) * kPitch + j);
-#pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                    const int jj = j + y;
-                    const float w = jj < n ? s.lamp[jb.rev ? jj + 1 : n - 1 - jj] * jb.s_in : 0.f;
-                    cc[y] = ld4(s.Cv + jj * kPitch + tx * 4);
-                    cc[y].x *= w; cc[y].y *= w; cc[y].z *= w; cc[y].w *= w;
-                }
-#pragma unroll
-                for (int x2 = 0; x2 < 2; ++x2)
-#pragma unroll
-                    for (int y = 0; y < 4; ++y) {
-                        const float4* bb = b + 4 * x2;
-                        const float4 col = y == 0 ? make_float4(bb[0].x, bb[1].x, bb[2].x, bb[3].x)
-                                         : y == 1 ? make_float4(bb[0].y, bb[1].y, bb[2].y, bb[3].y)
-                                         : y == 2 ? make_float4(bb[0].z, bb[1].z, bb[2].z, bb[3].z)
-                                                  : make_float4(bb[0].w, bb[1].w, bb[2].w, bb[3].w);
-                        fma44(u[x2], col, cc[y]);
-                    }
+            for (int x = 0; x < 4; ++x) {
+                float f[4];
+                u.row(x, f);
+                float* X = s.X + (k0 + x) * kPitch + tx * 4;
+                float4 q = ld4(X);
+                q.x = fmaf(q.x, hi, fmaf(q.x, lo, f[0]));
+                q.y = fmaf(q.y, hi, fmaf(q.y, lo, f[1]));
+                q.z = fmaf(q.z, hi, fmaf(q.z, lo, f[2]));
+                q.w = fmaf(q.w, hi, fmaf(q.w, lo, f[3]));
+                st4(X, q);
             }
-            float hi = cf_hi, lo = cf_lo;
-            if (n < kC) la_decay_pow(g.a, h, n, hi, lo);
-#pragma unroll
-            for (int x2 = 0; x2 < 2; ++x2)
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    float* X = s.X + (ty * 8 + 4 * x2 + x) * kPitch + tx * 4;
-#pragma unroll
-                    for (int y = 0; y < 4; ++y) X[y] = fmaf(X[y], hi, fmaf(X[y], lo, u[x2][x][y]));
-                }
         }
     }
     __syncthreads();
     float* outst = kAgg ? ag : (last && jb.fin ? jb.fin + so : nullptr);
     if (outst == nullptr) return;
-    for (int i = tid; i < jb.DK * nv; i += kThreads) {
-        const int k = i % jb.DK, v = i / jb.DK;
-        outst[(int64_t)k * jb.sk + (int64_t)(v0 + v) * jb.sv] = s.X[k * kPitch + v];
-    }
+    each([&](int k, int v) {
+        if (v < nv) outst[(int64_t)k * jb.sk + (int64_t)(v0 + v) * jb.sv] = s.X[k * kPitch + v];
+    });
 }
 
 // One thread per state element of (sequence, head): walks the sequence's
@@ -241,17 +280,17 @@ __global__ void __launch_bounds__(256) linattn_scan(const __grid_constant__ LaPa
     float f_hi, f_lo, t_hi, t_lo;
     la_decay_pow(g.a, h, g.R, f_hi, f_lo);
     la_decay_pow(g.a, h, len - (n - 1) * g.R, t_hi, t_lo);
-    // four ranges' sums in flight
-    for (int i0 = 0; i0 < n; i0 += 4) {
-        float4 u[4];
+    // eight ranges' sums in flight: the walk is all latency
+    for (int i0 = 0; i0 < n; i0 += 8) {
+        float4 u[8];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
+        for (int q = 0; q < 8; ++q) {
             const int i = i0 + q, r = jb.rev ? n - 1 - i : i;
             if (i < n - 1)
                 u[q] = *reinterpret_cast<const float4*>(jb.agg + ((int64_t)(s_base + r) * g.H + h) * elems + e);
         }
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
+        for (int q = 0; q < 8; ++q) {
             const int i = i0 + q, r = jb.rev ? n - 1 - i : i;
             if (i >= n) break;
             *reinterpret_cast<float4*>(jb.agg + ((int64_t)(s_base + r) * g.H + h) * elems + e) = S;
