@@ -18,7 +18,8 @@
 // c, from L2 the second time) and no state leaves the chip between chunks.
 //
 // Precision.  P and the X that multiplies A are rounded to bf16 (as operands of
-// a product whose result is rounded to bf16).  X itself must not be: it is kept
+// a product whose result is rounded to bf16; P in two terms for a chunk of few
+// tokens).  X itself must not be: it is kept
 // in fp32 registers and U is exact to fp32: C's scaled rows are cut into three
 // bf16 terms of 8 bits each, multiplied side by side (N = 192) into separate
 // accumulators and added from the smallest up.  X <- lam^n X + U runs on the
@@ -76,6 +77,7 @@ constexpr uint32_t kW = 0;                    // W / P, two buffers of 128
 constexpr uint32_t kO = 256, kUMain = 320;    // out; U's three terms
 // The factored form takes heads whose decay over a chunk's 127 steps is at least
 // 2^-kSpan: row and column factors, counted from the middle, are within 2^+-60.
+// (A product a b beyond 2^67 would overflow in it and one below 2^-66 vanish.)
 constexpr float kSpan = 120.f;
 constexpr int kMid = 64;
 
@@ -131,6 +133,40 @@ __device__ __forceinline__ void wait_on(uint32_t bar, uint32_t parity, unsigned 
 __device__ __forceinline__ void ld_cols(uint32_t at, uint32_t (&r)[4]) { tmem_ld_x4(at, r); }
 __device__ __forceinline__ void ld_cols(uint32_t at, uint32_t (&r)[8]) { tmem_ld_x8(at, r); }
 __device__ __forceinline__ bool factored(float a2) { return a2 * -127.f <= kSpan; }
+// A chunk of so few tokens leaves the second half of P's contraction free: it holds
+// P's second terms there (and P is then good to 16 bits), for tokens whose output is
+// a sum of a few products, or of one.  (In the exact form the columns behind are taken.)
+__device__ __forceinline__ bool few(int n, bool fac) { return n <= (fac ? 64 : 32); }
+// P of such a chunk, a row to a thread.  Not inlined: the roles' loops share the
+// instruction cache (in line, a training step of 16384 tokens took 333 us, not 325).
+__device__ __noinline__ void few_p(uint32_t base, uint32_t ptab, int row, int n, float a2, float s_in, bool fac, int rev) {
+#pragma unroll 1
+    for (int j0 = 0; j0 < 64; j0 += 8) {
+        uint32_t v[8] = {}, hi[4], lo[4];
+        __syncwarp();
+        if (fac || j0 < 32) tmem_ld_x8(base + j0, v);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) {
+            float r[2], l[2];
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                const int j = j0 + e + y, d = rev ? j - row : row - j;
+                const float w = fac ? lds32(ptab + 4 * j) : exp2f(a2 * (float)max(d, 0)) * s_in;
+                r[y] = d >= 0 && j < n ? __uint_as_float(v[e + y]) * w : 0.f;
+            }
+            hi[e / 2] = pack2(r[0], r[1]);
+            l[0] = r[0] - lo16(hi[e / 2]);
+            l[1] = r[1] - hi16(hi[e / 2]);
+            // an infinity or a NaN is the first term's alone
+            lo[e / 2] = pack2(fabsf(l[0]) < INFINITY ? l[0] : 0.f, fabsf(l[1]) < INFINITY ? l[1] : 0.f);
+        }
+        __syncwarp();
+        tmem_st_x4(base + j0 / 2, hi);
+        tmem_st_x4(base + j0 / 2 + (fac ? 64 : 32), lo);
+    }
+    tmem_wait_st();
+}
 // 2^(a2 n), with the product's rounding put back: n a2 can be as large as kSpan,
 // where a rounding of the exponent would be one of the result's last bits.
 __device__ __forceinline__ float la_exp2(float a2, int n) {
@@ -410,6 +446,8 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
             // x = -1: the W of the item's first chunk
             const int x0 = kAgg || ahead ? 0 : -1;
             ahead = false;
+            // the item's only chunk that may be of few tokens
+            const int few_x = uniform(!few(im.len - (nch - 1) * kC, fac) ? -1 : tp.p.job[im.job].rev ? 0 : nch - 1);
             if (elect_one()) {
 #pragma unroll 1
                 for (int x = x0; x < nch; ++x) {
@@ -483,9 +521,12 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                             const uint64_t bd = smem_desc_sw128(smem_u32(ctile) + (cc % kCs) * kAtom, 8 * kRow, 8 * kRow);
                             const uint32_t to = tmem + (fac ? kO : kW + s * 128 + 64);
                             const uint32_t pa = tmem + kW + s * 128, pb = pa + (fac ? 32 : 0);
+                            // the second half of the contraction: tokens 64 .. 127, or for a
+                            // chunk of few tokens their second terms
+                            const uint64_t be = bd - (x == few_x ? (uint64_t)((64 * kRow) >> 4) : 0);
 #pragma unroll
                             for (int kk = 0; kk < 8; ++kk)
-                                mma_f16_ts(to, (kk < 4 ? pa : pb) + kk * 8, bd + (uint64_t)((kk * 16 * kRow) >> 4),
+                                mma_f16_ts(to, (kk < 4 ? pa : pb) + kk * 8, (kk < 4 ? bd : be) + (uint64_t)((kk * 16 * kRow) >> 4),
                                            kIdO, kk > 0 ? 1u : (uint32_t)fac);
                             mma_commit(smem_u32(b_odone));
                         }
@@ -521,6 +562,12 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                 wait_on(smem_u32(b_wdone + s), (c >> 1) & 1, err);
                 tc_fence_after();
                 const uint32_t base = tmem + lane_off + kW + s * 128;
+                if (few(n, fac)) {
+                    if (warp < 4 && quad * 32 < n) few_p(base, ptab, row, n, a2, jb.s_in, fac, jb.rev);
+                    tc_fence_before();
+                    mbar_arrive(smem_u32(b_pready + s));
+                    continue;
+                }
                 // 16 columns at a time, in place: each half's packed columns lie
                 // within its own and behind its reads.  (The exact form needs the
                 // upper half's columns for its second accumulator, so one warpgroup

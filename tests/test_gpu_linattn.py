@@ -172,6 +172,45 @@ def test_fast_decays_and_large_values(decay):
         assert off(num(g[3][:, h]), want[5][:, h]) < TOL["f32"]
 
 
+def test_few_tokens_keep_both_terms():
+    """Without a state, an output of a chunk of few tokens (64; 32 for fast decays) is a
+    sum of a few products, or one: its weights keep 16 bits.  Element by element, with
+    A the sum of the products' magnitudes: 2^-8 of the result for its own rounding, and
+    2^-14 A for the weights (2^-16), their sums over K (K 2^-24 < 2^-16) and exponentials."""
+    lens = [1] * 20 + [2, 5, 31, 32, 33, 63, 64]
+    x = make("bf16", lens, 2, 2, 96, 64, False, seed=12, decay=[-0.01, -0.9])
+    d = dev(x)
+    o, _ = ssd.linattn_fwd(d["q"], d["k"], d["v"], d["a"], cu_seqlens=d["cu"])
+    g = ssd.linattn_bwd(d["q"], d["k"], d["v"], d["dout"], d["a"], cu_seqlens=d["cu"])
+    sync_ok()
+    args = [f64(x[n]) for n in ("q", "k", "v")]
+    run = lambda f: linattn(*[f(t) for t in args], x["a"].numpy(), lens, 96 ** -0.5, None, f(f64(x["dout"])))
+    want, mag = run(lambda t: t), run(np.abs)
+    for h, n in ((0, sum(lens)), (1, sum(lens[:24]))):
+        for i, t in ((0, o), (2, g[0]), (3, g[1]), (4, g[2])):
+            err = np.abs(num(t) - want[i])[:n, h]
+            bound = 2.0 ** -8 * np.abs(want[i]) + 2.0 ** -14 * mag[i]
+            assert (err <= bound[:n, h]).all(), (h, i)
+
+
+def test_one_long_sequence():
+    """A single sequence's ranges are made to fill the GPU (their number follows from
+    the length alone), with and without offsets; so are those of equal sequences."""
+    for lens in ([5000], [2600, 2600]):
+        x = make("bf16", lens, 2, 1, 32, 48, True, seed=13)
+        d = dev(x)
+        for kw in (dict(cu_seqlens=d["cu"], max_seqlen=max(lens)), dict(nseqs=len(lens))):
+            o, fin = ssd.linattn_fwd(d["q"], d["k"], d["v"], d["a"], init_state=d["S0"], **kw)
+            g = ssd.linattn_bwd(d["q"], d["k"], d["v"], d["dout"], d["a"], init_state=d["S0"],
+                                dfinal_state=d["dfin"], **kw)
+            sync_ok()
+            want = ref(x, lens, 32 ** -0.5, grads=True)
+            assert off(num(o), want[0]) < TOL["bf16"] and off(num(fin), want[1]) < TOL["f32"]
+            for i in range(3):
+                assert off(num(g[i]), want[2 + i]) < TOL["bf16"]
+            assert off(num(g[3]), want[5]) < TOL["f32"]
+
+
 def test_long_sequences_among_many_empty_ones():
     """Sequences cut into ranges, many that are empty, and no bound of the lengths:
     most of the work list has nothing to do, and every sequence's state arrives."""
