@@ -35,7 +35,7 @@
 //         update with U, stored states
 //   24-27 out (a thread owns a token row)
 //   28    TMA, two stages of A and B tiles (64 KB each), three C tiles; the next item
-//   29    MMA issue: U(c), W(c + 1), A X(c), P C(c)
+//   29    MMA issue: U(c)'s first half, W(c + 1), its second half, A X(c), P C(c)
 // The roles' loops are kept short (packed fp32 arithmetic, little unrolling): six
 // codes run side by side on each scheduler, and fully unrolled they spent most of
 // their time on instruction fetches.
@@ -128,6 +128,25 @@ __device__ __forceinline__ void wait_on(uint32_t bar, uint32_t parity, unsigned 
             }
         }
     }
+}
+
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    return ok != 0;
+}
+// Whether the first barrier's phase completes before the second's (or within 64 looks).
+__device__ __forceinline__ bool first_of(uint32_t a, uint32_t a_parity, uint32_t b, uint32_t b_parity) {
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i) {
+        if (mbar_test(a, a_parity)) return true;
+        if (mbar_test(b, b_parity)) break;
+    }
+    return false;
 }
 
 __device__ __forceinline__ void ld_cols(uint32_t at, uint32_t (&r)[4]) { tmem_ld_x4(at, r); }
@@ -485,6 +504,26 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                         tc_fence_after();
                         u_half(0);
                         mma_commit(smem_u32(b_udone));
+                        if (!kAgg) {
+                            // the last out is read: its accumulator is free, and in the exact form
+                            // W's buffer
+                            wait_on(smem_u32(b_ofree), (cc & 1) ^ 1, err);
+                            if (x + 1 == nch && mbar_try_wait(smem_u32(b_iready + (k_item & 1)), (k_item >> 1) & 1)) {
+                                // the first W of the next item, if that is known by now
+                                const uint4 q1 = lds128(smem_u32(items) + (k_item & 1) * 64 + 16);
+                                if ((int)q1.w > 0) {
+                                    w_due = ahead = true;
+                                    ks_w = tp.p.job[q1.x].DK / 16;
+                                }
+                            }
+                            // W of the next chunk, if its tiles are there before the other half's
+                            // terms: P is then built a chunk ahead, and the tensor pipe has work
+                            // while the terms are written.  (Behind U, and not looked for in
+                            // turns with the terms: 295 us instead of 277 for a prompt of 65536
+                            // tokens, 24 heads of 128 x 64.  Waited for: 158 instead of 150 us for
+                            // 16384 tokens whose tiles come from HBM, 32 heads of 128 x 128.)
+                            if (w_due && first_of(smem_u32(b_fab + s1), use1 & 1, smem_u32(b_vready + 1), cc & 1)) w_product();
+                        }
                         wait_on(smem_u32(b_vready + 1), cc & 1, err);
                         tc_fence_after();
                         u_half(1);
@@ -494,21 +533,8 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                             mma_commit(smem_u32(b_eab + sb));
                             mma_commit(smem_u32(b_ec) + 8 * (cc % kCs));
                         } else {
-                            // W of the next chunk, if its tiles are there (and the exact form
-                            // does not hold its buffer): P is then built a chunk ahead, and
-                            // the tensor pipe has work while the last out is read
-                            if (x + 1 == nch && mbar_try_wait(smem_u32(b_iready + (k_item & 1)), (k_item >> 1) & 1)) {
-                                // the first W of the next item, if that is known by now
-                                const uint4 q1 = lds128(smem_u32(items) + (k_item & 1) * 64 + 16);
-                                if ((int)q1.w > 0) {
-                                    w_due = ahead = true;
-                                    ks_w = tp.p.job[q1.x].DK / 16;
-                                }
-                            }
-                            if (w_due && fac && mbar_try_wait(smem_u32(b_fab + s1), use1 & 1)) w_product();
                             // out = A X
                             wait_on(smem_u32(b_sready), cc & 1, err);
-                            wait_on(smem_u32(b_ofree), (cc & 1) ^ 1, err);
                             tc_fence_after();
                             mma_steps<true, false>(tmem + kO, smem_desc_sw128(st, 16, 8 * kRow),
                                                    smem_desc_sw128(smem_u32(xs), 8 * kRow, 8 * kRow), ks, kIdO);
