@@ -26,6 +26,7 @@
 // sum, and a second kernel adds those in a fixed order.
 #include "block_norm.cuh"
 #include "f32x2.cuh"
+#include "sm100_ptx.cuh"
 
 namespace ssd {
 namespace {
@@ -280,6 +281,7 @@ template <typename T, typename R, int NV, bool kWarp, bool kSmall>
 __global__ void __launch_bounds__(kWarp ? 128 : kSmall ? 256 : 640, kWarp ? 4 : !kSmall ? 1 : sizeof(T) == 2 ? 3 : 2)
 block_norm_bwd(const __grid_constant__ NormParams p) {
     extern __shared__ float sm[];
+    grid_launch_dependents();   // the partials' sum may set itself up
     const int first = kWarp ? threadIdx.x & 31 : threadIdx.x, stride = kWarp ? 32 : blockDim.x;
     const int rpb = kWarp ? blockDim.x >> 5 : 1, sub = kWarp ? threadIdx.x >> 5 : 0;
     float* grp = sm + 96 + (kWarp ? sub * p.grp_floats : 0);
@@ -394,6 +396,7 @@ block_norm_bwd(const __grid_constant__ NormParams p) {
 __global__ void __launch_bounds__(512) block_norm_reduce(const __grid_constant__ NormParams p, int nparts) {
     __shared__ float sh[16][33];
     const int x = threadIdx.x & 31, w = threadIdx.x >> 5, c = blockIdx.x * 32 + x;
+    grid_dependency_wait();
     float v = 0.f;
     if (c < p.D) {
         const float* src = p.partial + (int64_t)blockIdx.y * p.D + c;
@@ -490,8 +493,7 @@ cudaError_t launch_block_norm_bwd(NormParams& p, int dtype, int rdtype, int sms,
         if (e != cudaSuccess) return e;
     }
     const int parts = grid > 0 ? block_norm_parts(p.T, p.vecs, dtype, sms) : 0;
-    block_norm_reduce<<<dim3((unsigned)(p.D + 31) / 32, 2), 512, 0, st>>>(p, parts);
-    return cudaGetLastError();
+    return launch_chained(block_norm_reduce, dim3((unsigned)(p.D + 31) / 32, 2), dim3(512), 0, st, grid > 0, p, parts);
 }
 
 }  // namespace ssd

@@ -14,11 +14,13 @@
 // a chunk, and takes 3500.  Bound by instruction issue: a 64 x 64 x 64 product is 15
 // instructions for each of 64 steps, 4 warps on a scheduler (two CTAs on an SM): 3840
 // cycles, measured 3400 to 4500; the tiles' loads are another 4000 to 5000 of a chunk's
-// 20000.  70 us for 2 x 2048 tokens, 8 heads of 64 x 64, in three launches of about 18
-// (the ranges' own sums), 7 (scan) and 42 us.  Ranges go down to 128 tokens here: two
+// 20000.  67.5 us for 2 x 2048 tokens, 8 heads of 64 x 64, in three launches of about 18
+// (the ranges' own sums), 7 (scan) and 41 us, chained so that each one's set-up overlaps
+// the end of the one before (69.7 us without).  Ranges go down to 128 tokens here: two
 // chunks each keep 256 CTAs busy, two on an SM.
 #include "f32x2.cuh"
 #include "linattn_internal.cuh"
+#include "sm100_ptx.cuh"
 
 namespace ssd {
 namespace {
@@ -86,6 +88,7 @@ __global__ void __launch_bounds__(kThreads, 2) linattn_simt(const __grid_constan
     const int nvb = (jb.DV + kLaCols - 1) / kLaCols;
     const int h = blockIdx.y / nvb, v0 = (blockIdx.y - h * nvb) * kLaCols;
     if (h >= g.H) return;
+    if (kAgg) grid_launch_dependents();
     if (tid < 32) {
         const LaRange r = la_find(g, blockIdx.x);
         if (tid == 0) *s.rg = r;
@@ -110,6 +113,7 @@ __global__ void __launch_bounds__(kThreads, 2) linattn_simt(const __grid_constan
     if (kAgg && (!cut || last)) return;
     const int64_t elems = (int64_t)jb.DK * jb.DV;
     const int64_t so = ((int64_t)rg.seq * g.H + h) * elems;
+    if (!kAgg) grid_dependency_wait();
     float* ag = cut ? jb.agg + ((int64_t)blockIdx.x * g.H + h) * elems : nullptr;
     const float* in = kAgg ? nullptr : (cut ? ag : (jb.init ? jb.init + so : nullptr));
     // neighbouring threads along whichever of the stored state's axes is contiguous
@@ -255,6 +259,7 @@ __global__ void __launch_bounds__(256) linattn_scan(const __grid_constant__ LaPa
     const LaJob& jb = p.job[blockIdx.z];
     const int seq = blockIdx.x / eblocks, eb = blockIdx.x - seq * eblocks, h = blockIdx.y;
     __shared__ int s_base, s_lo, s_hi;
+    grid_launch_dependents();
     if (threadIdx.x < 32) {   // ranges before this sequence
         int sum = 0;
         for (int s = threadIdx.x; s < seq; s += 32) {
@@ -270,6 +275,7 @@ __global__ void __launch_bounds__(256) linattn_scan(const __grid_constant__ LaPa
         }
     }
     __syncthreads();
+    grid_dependency_wait();
     const int n = la_count(g, seq, s_lo, s_hi), len = s_hi - s_lo;
     if (n <= 1 || s_base + n > g.range_cap) return;
     const int elems = jb.DK * jb.DV;
@@ -343,8 +349,8 @@ cudaError_t go(const LaParams& p, cudaStream_t stream) {
     auto k = linattn_simt<kAgg>;
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
     if (e != cudaSuccess) return e;
-    k<<<dim3((unsigned)p.g.range_cap, (unsigned)(p.g.H * nvb), (unsigned)p.njobs), kThreads, bytes, stream>>>(p);
-    return cudaGetLastError();
+    return launch_chained(k, dim3((unsigned)p.g.range_cap, (unsigned)(p.g.H * nvb), (unsigned)p.njobs), dim3(kThreads), bytes,
+                          stream, !kAgg && p.g.split, p);
 }
 
 }  // namespace
@@ -356,8 +362,8 @@ cudaError_t launch_linattn_simt(const LaParams& p, int mode, cudaStream_t stream
 cudaError_t launch_linattn_scan(const LaParams& p, cudaStream_t stream) {
     const int elems = p.job[0].DK * p.job[0].DV;   // the same product for every job
     const int eblocks = (elems / 4 + 255) / 256;
-    linattn_scan<<<dim3((unsigned)(p.g.nseq * eblocks), (unsigned)p.g.H, (unsigned)p.njobs), 256, 0, stream>>>(p, eblocks);
-    return cudaGetLastError();
+    return launch_chained(linattn_scan, dim3((unsigned)(p.g.nseq * eblocks), (unsigned)p.g.H, (unsigned)p.njobs), dim3(256), 0,
+                          stream, true, p, eblocks);
 }
 
 cudaError_t launch_linattn_group_sum(const float* const part[2], void* out0, void* out1, int64_t T, int G,
