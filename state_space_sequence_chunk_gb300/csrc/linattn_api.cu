@@ -56,8 +56,9 @@ ssd_status make_la(const ssd_linattn_dims* d, bool packed, bool backward, La* p)
     // A sequence is cut into ranges where a chain of its whole length would keep the
     // other SMs waiting: if it is longer than what an SM gets when the work is spread
     // evenly and longer by more than the cut costs, which reads two operands twice
-    // (another 0.4 of the share) and launches twice more (about 6 chunks' time;
-    // without that margin, 1280 tokens on 150 chains took 66 us cut and 31 whole).
+    // (another 0.4 of the share) and launches twice more (about 7 chunks' time).  One
+    // sequence of 4096 tokens, cut and whole: 36 and 79 us on 24 chains, 76 and 82 on
+    // 76; of 1280 on 150 chains, 69 and 31.
     const int64_t kb = (p->K + kLaCols - 1) / kLaCols, vb = (p->V + kLaCols - 1) / kLaCols;
     const int64_t cols = backward ? 2 * kb + vb : vb;
     const int64_t sms = sm_count(), share = p->T * p->H * cols / sms;
@@ -66,11 +67,11 @@ ssd_status make_la(const ssd_linattn_dims* d, bool packed, bool backward, La* p)
     if (longest > p->T) longest = p->T;
     int64_t R = (share / 2 + 127) / 128 * 128;
     if (R < least) R = least;
-    g.split = longest > R && longest > share + (d->dtype == SSD_F32 ? 0 : share / 2 + 768);
+    g.split = longest > R && longest > share + (d->dtype == SSD_F32 ? 0 : share / 2 + 896);
     // Half a share, so that the range taken last adds at most half; where the lengths
     // are known, the number of ranges that fills the SMs in the shortest time (a range
     // costs 2 chunks more than its own): one sequence of 65536 tokens on 24 chains in
-    // 12.7 ranges of half a share left a third round of 8 items, 234 us instead of 190.
+    // 12.7 ranges of half a share left a third round of 8 items, 316 us instead of 303.
     if (g.split && (p->n == 1 || !packed)) {
         const int64_t L = packed ? p->T : g.L, slots = sms * (d->dtype == SSD_F32 ? 2 : 1);
         int64_t best = INT64_MAX;
