@@ -130,6 +130,12 @@ __device__ __forceinline__ void wait_on(uint32_t bar, uint32_t parity, unsigned 
     }
 }
 
+// After a wait that gave up: time for the copies and products in flight to end
+// before the CTA's shared and tensor memory are given back.
+__device__ __noinline__ void settle() {
+    const uint32_t t0 = (uint32_t)clock();
+    while ((uint32_t)clock() - t0 < (uint32_t)kWaitSlowCycles) {}
+}
 __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
@@ -952,8 +958,11 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
     }
     tc_fence_before();
     __syncthreads();
-    if (threadIdx.x == 0) report_timeout_to_host(err, tp.host_err);
     if (warp == kMmaWarp) {
+        if (lane == 0) {
+            if (*reinterpret_cast<volatile unsigned int*>(err) != 0u) settle();
+            report_timeout_to_host(err, tp.host_err);
+        }
         __syncwarp();
         tc_fence_after();
         tmem_dealloc(tmem, 512);
