@@ -233,7 +233,39 @@ struct Item {
 };
 static_assert(sizeof(Item) == 64, "two slots of 64 bytes");
 
-template <bool kAgg>
+// The idx-th longest sequence, when none is cut and there are fewer than 32 (rows of
+// no sequence come last): the SMs then end together, also where a long sequence
+// stands behind short ones (329 -> 303 us for a training step on six sequences of 1477
+// to 3868 tokens, 16 heads of 128 x 128).  One warp.
+__device__ __forceinline__ LaRange longest(const LaGeom& g, int idx) {
+    const int lane = threadIdx.x & 31;
+    int lo = 0, hi = 0, key = -1;
+    if (lane <= g.nseq) {
+        la_bounds(g, lane, lo, hi);
+        if (la_count(g, lane, lo, hi) > 0) key = lane < g.nseq ? hi - lo : -1;
+    }
+    int rank = 0;
+#pragma unroll 1
+    for (int o = 0; o <= g.nseq; ++o) {
+        const int k = __shfl_sync(0xffffffffu, key, o);
+        rank += k > key || (k == key && o < lane) ? 1 : 0;
+    }
+    const int src = __ffs(__ballot_sync(0xffffffffu, lane <= g.nseq && rank == idx)) - 1;
+    LaRange r;
+    r.seq = -1;
+    r.r = r.n = r.t0 = r.len = r.slen = 0;
+    if (src < 0) return r;
+    lo = __shfl_sync(0xffffffffu, lo, src);
+    hi = __shfl_sync(0xffffffffu, hi, src);
+    r.n = la_count(g, src, lo, hi);
+    if (r.n == 0) return r;
+    r.seq = src;
+    r.t0 = lo;
+    r.len = r.slen = hi - lo;
+    return r;
+}
+
+template <bool kAgg, bool kSplit>
 __device__ __forceinline__ void decode_item(const TcParams& tp, int it, Item* slot) {
     Item r;
     const int vb = it % tp.nvb;
@@ -243,13 +275,13 @@ __device__ __forceinline__ void decode_item(const TcParams& tp, int it, Item* sl
     r.h = x % tp.p.g.H;
     r.ridx = x / tp.p.g.H;
     const float a = tp.p.g.a[r.h];
-    const LaRange rg = la_find(tp.p.g, r.ridx);
+    const LaRange rg = !kSplit && tp.p.g.nseq < 32 ? longest(tp.p.g, r.ridx) : la_find(tp.p.g, r.ridx);
     r.seq = rg.seq;
     r.t0 = rg.t0;
     r.len = rg.len;
     r.v0 = vb * kLaCols;
     const LaJob& jb = tp.p.job[r.job];
-    r.cut = tp.p.g.split && rg.n > 1;
+    r.cut = kSplit && rg.n > 1;
     r.last = jb.rev ? rg.r == 0 : rg.r == rg.n - 1;
     const bool none = rg.seq < 0 || r.v0 >= jb.DV || (kAgg && (!r.cut || r.last || rg.seq == tp.p.g.nseq));
     r.nch = none || rg.seq == tp.p.g.nseq ? 0 : (rg.len + kC - 1) / kC;
@@ -303,9 +335,10 @@ __device__ __forceinline__ void mma_steps(uint32_t d, uint64_t a, uint64_t b, in
     }
 }
 
-// kPart: some job's outputs are fp32, for a sum over a group's heads.  (Without
-// them the code is shorter, which the other calls feel.)
-template <bool kAgg, bool kPart>
+// kPart: some job's outputs are fp32, for a sum over a group's heads.  kSplit: long
+// sequences are cut.  (Without what the others need the code is shorter, which every
+// call feels: with one instance for both, a cut prompt took 288 us instead of 278.)
+template <bool kAgg, bool kPart, bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1)
 linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps maps) {
     // aligned by declaration, not by arithmetic: its addresses are then constants
@@ -400,7 +433,7 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
     Item im;
 
     if (warp == kTmaWarp) {
-        decode_item<kAgg>(tp, blockIdx.x, items);
+        decode_item<kAgg, kSplit>(tp, blockIdx.x, items);
         if (lane == 0) mbar_arrive(smem_u32(b_iready));
 #pragma unroll 1
         for (;; ++k_item) {
@@ -451,7 +484,7 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                     const int it = uniform(granted_item(answer));
                     fence_proxy_async_smem();
                     wait_on(smem_u32(b_ifree + slot), (((k_item + 1) >> 1) & 1) ^ 1, err);
-                    if (it >= 0) decode_item<kAgg>(tp, it, items + slot);
+                    if (it >= 0) decode_item<kAgg, kSplit>(tp, it, items + slot);
                     else if (lane == 0) items[slot].nch = -1;
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_u32(b_iready + slot));
@@ -1001,7 +1034,9 @@ cudaError_t launch_linattn_tc(const LaParams& p, int mode, cudaStream_t stream) 
     const int64_t items = (int64_t)p.g.range_cap * p.g.H * p.njobs * tp.nvb;
     if (items >= (1LL << 31)) return cudaErrorInvalidValue;
     tp.host_err = host_timeout_word();
-    auto k = mode ? linattn_tc<true, false> : part ? linattn_tc<false, true> : linattn_tc<false, false>;
+    auto k = mode ? linattn_tc<true, false, true>
+           : p.g.split ? (part ? linattn_tc<false, true, true> : linattn_tc<false, false, true>)
+                       : (part ? linattn_tc<false, true, false> : linattn_tc<false, false, false>);
     const int smem = mode ? Cfg<true>::kSmem : Cfg<false>::kSmem;
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
