@@ -24,6 +24,11 @@
 // Backwards, CTAs are persistent: a thread keeps the same columns for all its
 // rows and adds its columns' sums in shared memory; each CTA leaves one partial
 // sum, and a second kernel adds those in a fixed order.
+//
+// Forwards, 16384 rows of 5120 bf16 columns with an fp32 residual stream: 190 us, 92 %
+// of the copy rate.  Both directions, 16384 x 2048 bf16: 199 us, 65 %: backwards a row's
+// loads are in flight only behind the row before it, and its 3 CTAs an SM do not cover
+// that (37 % of the warps, 49 % of the DRAM rate under the profiler).
 #include "block_norm.cuh"
 #include "f32x2.cuh"
 #include "sm100_ptx.cuh"

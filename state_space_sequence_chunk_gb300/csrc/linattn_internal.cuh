@@ -11,7 +11,7 @@
 // walked forwards (o = F(q, k; v), dq = F(do, v; k)) or backwards
 // (dk = F(v, do; q), dv = F(k, q; do)); backwards the state that enters a
 // token has not been decayed yet, which only shifts two exponents by one.
-// A kernel runs up to three such jobs in one launch (blockIdx.z).
+// A kernel runs up to three such jobs in one launch.
 //
 // A chain (sequence, head, 64 columns of c) can be cut into ranges of R tokens
 // when there are too few chains to fill the GPU: a first launch sums every

@@ -39,6 +39,14 @@
 // The roles' loops are kept short (packed fp32 arithmetic, little unrolling): six
 // codes run side by side on each scheduler, and fully unrolled they spent most of
 // their time on instruction fetches.
+//
+// A chunk takes about 4000 cycles of an SM: 1900 of products and 3000 of shared-memory
+// traffic (400 KB) side by side, and between them a chain that bounds it (terms, half of U,
+// terms, half of U, state, and the issuing warp's fetches at each turn of its loop).
+// 16384 packed tokens, 32 heads of 128 x 128: 151 us, 58 % of the copy rate on the bytes
+// that must move; one sequence of 65536, 24 heads of 128 x 64 with shared q and k: 278 us
+// in three launches (79 + 11 + 188); a training step of 16384 tokens, 16 heads of
+// 128 x 128: 304 us.
 #include <cuda.h>
 #include <string.h>
 
