@@ -555,7 +555,7 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                             // the last out is read: its accumulator is free, and in the exact form
                             // W's buffer
                             wait_on(smem_u32(b_ofree), (cc & 1) ^ 1, err);
-                            if (x + 1 == nch && mbar_try_wait(smem_u32(b_iready + (k_item & 1)), (k_item >> 1) & 1)) {
+                            if (x + 1 == nch && mbar_test(smem_u32(b_iready + (k_item & 1)), (k_item >> 1) & 1)) {
                                 // the first W of the next item, if that is known by now
                                 const uint4 q1 = lds128(smem_u32(items) + (k_item & 1) * 64 + 16);
                                 if ((int)q1.w > 0) {
