@@ -78,7 +78,9 @@ ssd_status make_la(const ssd_linattn_dims* d, bool packed, bool backward, La* p)
         for (int64_t n = 2; n <= 64; ++n) {
             const int64_t r = ((L + n - 1) / n + 127) / 128 * 128;
             if (r < least) break;
-            const int64_t cost = (p->n * p->H * cols * n + slots - 1) / slots * (r / 128 + 2);
+            // (ranges end at multiples of r of all rows: one more where r does not divide L)
+            const int64_t m = n + (p->n > 1 && L % r != 0);
+            const int64_t cost = (p->n * p->H * cols * m + slots - 1) / slots * (r / 128 + 2);
             if (cost < best) {
                 best = cost;
                 R = r;
@@ -86,7 +88,7 @@ ssd_status make_la(const ssd_linattn_dims* d, bool packed, bool backward, La* p)
         }
     }
     g.R = g.split ? (int)R : (int)(p->T > 0 ? (p->T + 127) / 128 * 128 : 128);
-    const int64_t cap = g.split ? p->T / R + p->n + 1 : p->n + 1;
+    const int64_t cap = g.split ? p->T / R + p->n + 2 : p->n + 1;
     if (cap > (1LL << 24)) return SSD_ERR_SHAPE;
     g.range_cap = (int)cap;
     p->agg_bytes = g.split ? round_up256((size_t)(cap * p->H * p->K * p->V) * 4) : 0;

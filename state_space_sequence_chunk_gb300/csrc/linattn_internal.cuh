@@ -31,7 +31,7 @@ struct LaGeom {
     int T, L;            // tokens in all; tokens of a sequence when cu is NULL
     int R;               // tokens per range
     int split;           // ranges run independently, from the states in `agg`
-    int range_cap;       // grid size in ranges (an upper bound of their number)
+    int range_cap;       // how far the numbers of ranges go
     const float* a;      // log decay [H]
 };
 
@@ -60,9 +60,8 @@ struct LaParams {
 // Where a range lies.  seq == nseq: tokens past the last sequence (their
 // outputs are zero); seq < 0: no such range.
 struct LaRange {
-    int seq, r, n;       // sequence, range within it, ranges of the sequence
-    int t0, len;         // first token and tokens of the range
-    int slen;            // tokens of the whole sequence
+    int seq, first, last;   // sequence; whether the range is its first and its last
+    int t0, len;            // first token and tokens of the range
 };
 
 #ifdef __CUDACC__
@@ -76,48 +75,47 @@ __device__ __forceinline__ void la_bounds(const LaGeom& g, int s, int& lo, int& 
         hi = s < g.nseq ? lo + g.L : lo;
     }
 }
-__device__ __forceinline__ int la_count(const LaGeom& g, int s, int lo, int hi) {
-    const int len = hi - lo, n = len / g.R + (len % g.R != 0);
-    return s < g.nseq && n == 0 ? 1 : n;   // an empty sequence still passes its state on
-}
-// Range number `idx` in the order of the sequences; executed by one whole warp.
+// Range number `idx`; executed by one whole warp.  Sequences are cut at multiples of R
+// of the packed rows: numbers 0 .. nseq are the ranges that begin a sequence (or the rows of none), nseq +
+// 1 + j the one that begins at row j R inside one.  So a range is found in a search of
+// cu at most, in steps of 32 (a count over all sequences before it made 16384
+// sequences of one token take 266 ms).
 __device__ __forceinline__ LaRange la_find(const LaGeom& g, int idx) {
-    const int lane = threadIdx.x & 31;
-    LaRange res;
-    res.seq = -1;
-    res.r = res.n = res.t0 = res.len = res.slen = 0;
-    int base = 0;
-    for (int s0 = 0; s0 <= g.nseq; s0 += 32) {
-        const int s = s0 + lane;
-        int lo = 0, hi = 0, n = 0;
-        if (s <= g.nseq) {
-            la_bounds(g, s, lo, hi);
-            n = la_count(g, s, lo, hi);
+    LaRange r;
+    r.seq = -1;
+    r.first = r.last = 1;
+    r.t0 = r.len = 0;
+    int lo, hi;
+    if (idx <= g.nseq) {
+        la_bounds(g, idx, lo, hi);
+        const int end = g.split ? min(hi, (lo / g.R + 1) * g.R) : hi;
+        if (idx == g.nseq && lo == hi) return r;
+        r.seq = idx;
+        r.last = end == hi;
+        r.t0 = lo;
+        r.len = end - lo;
+    } else {
+        const int lane = threadIdx.x & 31, x = (idx - g.nseq - 1) * g.R;
+        if (x >= g.T) return r;
+        // cu[0 .. at) <= x, and n entries to look at
+        int at = g.cu != nullptr ? 0 : x / g.L + 1, n = g.cu != nullptr ? g.nseq + 1 : 0;
+        while (n > 0) {
+            const int step = (n + 31) / 32, o = lane * step;
+            const int c = __popc(__ballot_sync(0xffffffffu, o < n && g.cu[at + min(o, n - 1)] <= x));
+            if (c == 0) break;
+            at += (c - 1) * step + 1;
+            n = min(step - 1, n - (c - 1) * step - 1);
         }
-        int inc = n;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, inc, o);
-            if (lane >= o) inc += v;
-        }
-        const int first = base + inc - n;
-        const unsigned hit = __ballot_sync(0xffffffffu, n > 0 && idx >= first && idx < first + n);
-        if (hit != 0u) {
-            const int src = __ffs(hit) - 1;
-            const int r = idx - __shfl_sync(0xffffffffu, first, src);
-            lo = __shfl_sync(0xffffffffu, lo, src);
-            hi = __shfl_sync(0xffffffffu, hi, src);
-            res.seq = s0 + src;
-            res.r = r;
-            res.n = __shfl_sync(0xffffffffu, n, src);
-            res.t0 = lo + r * g.R;
-            res.len = min(g.R, hi - res.t0);
-            res.slen = hi - lo;
-            return res;
-        }
-        base += __shfl_sync(0xffffffffu, inc, 31);
+        if (at == 0) return r;
+        la_bounds(g, at - 1, lo, hi);
+        if (lo >= x || hi <= x) return r;   // a sequence begins here, or no content of cu says where
+        r.seq = at - 1;
+        r.first = 0;
+        r.t0 = x;
+        r.len = min(g.R, hi - x);
+        r.last = x + r.len == hi;
     }
-    return res;
+    return r;
 }
 
 // log2 of the head's decay: 0 or less.  -inf (no memory) becomes a finite value

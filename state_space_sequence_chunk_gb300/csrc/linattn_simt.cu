@@ -108,8 +108,8 @@ __global__ void __launch_bounds__(kThreads, 2) linattn_simt(const __grid_constan
         }
         return;
     }
-    const bool cut = g.split && rg.n > 1;
-    const bool last = jb.rev ? rg.r == 0 : rg.r == rg.n - 1;
+    const bool cut = g.split && !(rg.first && rg.last);
+    const bool last = jb.rev ? rg.first : rg.last;
     if (kAgg && (!cut || last)) return;
     const int64_t elems = (int64_t)jb.DK * jb.DV;
     const int64_t so = ((int64_t)rg.seq * g.H + h) * elems;
@@ -258,34 +258,25 @@ __global__ void __launch_bounds__(256) linattn_scan(const __grid_constant__ LaPa
     const LaGeom& g = p.g;
     const LaJob& jb = p.job[blockIdx.z];
     const int seq = blockIdx.x / eblocks, eb = blockIdx.x - seq * eblocks, h = blockIdx.y;
-    __shared__ int s_base, s_lo, s_hi;
     grid_launch_dependents();
-    if (threadIdx.x < 32) {   // ranges before this sequence
-        int sum = 0;
-        for (int s = threadIdx.x; s < seq; s += 32) {
-            int lo, hi;
-            la_bounds(g, s, lo, hi);
-            sum += la_count(g, s, lo, hi);
-        }
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (threadIdx.x == 0) {
-            int lo, hi;
-            la_bounds(g, seq, lo, hi);
-            s_base = sum; s_lo = lo; s_hi = hi;
-        }
-    }
-    __syncthreads();
+    int lo, hi;
+    la_bounds(g, seq, lo, hi);
+    const int n = hi > lo ? (hi - 1) / g.R - lo / g.R + 1 : 1, first = (lo / g.R + 1) * g.R - lo;
     grid_dependency_wait();
-    const int n = la_count(g, seq, s_lo, s_hi), len = s_hi - s_lo;
-    if (n <= 1 || s_base + n > g.range_cap) return;
+    if (n <= 1) return;
     const int elems = jb.DK * jb.DV;
     const int e = (eb * 256 + threadIdx.x) * 4;
     if (e >= elems) return;
     float4 S = make_float4(0.f, 0.f, 0.f, 0.f);
     if (jb.init) S = *reinterpret_cast<const float4*>(jb.init + ((int64_t)seq * g.H + h) * elems + e);
-    float f_hi, f_lo, t_hi, t_lo;
+    float b_hi, b_lo, f_hi, f_lo, t_hi, t_lo;   // over the first range, a whole one, the last
+    la_decay_pow(g.a, h, first, b_hi, b_lo);
     la_decay_pow(g.a, h, g.R, f_hi, f_lo);
-    la_decay_pow(g.a, h, len - (n - 1) * g.R, t_hi, t_lo);
+    la_decay_pow(g.a, h, hi - lo - first - (n - 2) * g.R, t_hi, t_lo);
+    const auto state = [&](int r) {
+        const int id = r == 0 ? seq : g.nseq + 1 + lo / g.R + r;
+        return reinterpret_cast<float4*>(jb.agg + ((int64_t)id * g.H + h) * elems + e);
+    };
     // eight ranges' sums in flight: the walk is all latency
     for (int i0 = 0; i0 < n; i0 += 8) {
         float4 u[8];
@@ -293,19 +284,19 @@ __global__ void __launch_bounds__(256) linattn_scan(const __grid_constant__ LaPa
         for (int q = 0; q < 8; ++q) {
             const int i = i0 + q, r = jb.rev ? n - 1 - i : i;
             if (i < n - 1)
-                u[q] = *reinterpret_cast<const float4*>(jb.agg + ((int64_t)(s_base + r) * g.H + h) * elems + e);
+                u[q] = *state(r);
         }
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
             const int i = i0 + q, r = jb.rev ? n - 1 - i : i;
             if (i >= n) break;
-            *reinterpret_cast<float4*>(jb.agg + ((int64_t)(s_base + r) * g.H + h) * elems + e) = S;
+            *state(r) = S;
             if (i == n - 1) break;   // the last range's pass writes the final state
-            const float hi = r == n - 1 ? t_hi : f_hi, lo = r == n - 1 ? t_lo : f_lo;
-            S.x = fmaf(S.x, hi, fmaf(S.x, lo, u[q].x));
-            S.y = fmaf(S.y, hi, fmaf(S.y, lo, u[q].y));
-            S.z = fmaf(S.z, hi, fmaf(S.z, lo, u[q].z));
-            S.w = fmaf(S.w, hi, fmaf(S.w, lo, u[q].w));
+            const float d_hi = r == n - 1 ? t_hi : r == 0 ? b_hi : f_hi, d_lo = r == n - 1 ? t_lo : r == 0 ? b_lo : f_lo;
+            S.x = fmaf(S.x, d_hi, fmaf(S.x, d_lo, u[q].x));
+            S.y = fmaf(S.y, d_hi, fmaf(S.y, d_lo, u[q].y));
+            S.z = fmaf(S.z, d_hi, fmaf(S.z, d_lo, u[q].z));
+            S.w = fmaf(S.w, d_hi, fmaf(S.w, d_lo, u[q].w));
         }
     }
 }

@@ -250,7 +250,7 @@ __device__ __forceinline__ LaRange longest(const LaGeom& g, int idx) {
     int lo = 0, hi = 0, key = -1;
     if (lane <= g.nseq) {
         la_bounds(g, lane, lo, hi);
-        if (la_count(g, lane, lo, hi) > 0) key = lane < g.nseq ? hi - lo : -1;
+        if (lane < g.nseq) key = hi - lo;
     }
     int rank = 0;
 #pragma unroll 1
@@ -261,15 +261,15 @@ __device__ __forceinline__ LaRange longest(const LaGeom& g, int idx) {
     const int src = __ffs(__ballot_sync(0xffffffffu, lane <= g.nseq && rank == idx)) - 1;
     LaRange r;
     r.seq = -1;
-    r.r = r.n = r.t0 = r.len = r.slen = 0;
+    r.first = r.last = 1;
+    r.t0 = r.len = 0;
     if (src < 0) return r;
     lo = __shfl_sync(0xffffffffu, lo, src);
     hi = __shfl_sync(0xffffffffu, hi, src);
-    r.n = la_count(g, src, lo, hi);
-    if (r.n == 0) return r;
+    if (src == g.nseq && lo == hi) return r;
     r.seq = src;
     r.t0 = lo;
-    r.len = r.slen = hi - lo;
+    r.len = hi - lo;
     return r;
 }
 
@@ -289,8 +289,8 @@ __device__ __forceinline__ void decode_item(const TcParams& tp, int it, Item* sl
     r.len = rg.len;
     r.v0 = vb * kLaCols;
     const LaJob& jb = tp.p.job[r.job];
-    r.cut = kSplit && rg.n > 1;
-    r.last = jb.rev ? rg.r == 0 : rg.r == rg.n - 1;
+    r.cut = kSplit && !(rg.first && rg.last);
+    r.last = jb.rev ? rg.first : rg.last;
     const bool none = rg.seq < 0 || r.v0 >= jb.DV || (kAgg && (!r.cut || r.last || rg.seq == tp.p.g.nseq));
     r.nch = none || rg.seq == tp.p.g.nseq ? 0 : (rg.len + kC - 1) / kC;
     if (none) r.seq = -1;

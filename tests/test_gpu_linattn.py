@@ -193,6 +193,26 @@ def test_few_tokens_keep_both_terms():
             assert (err <= bound[:n, h]).all(), (h, i)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("long", [0, 2500])
+def test_very_many_sequences(dtype, long):
+    """More sequences than two steps of the search over their offsets tell apart, of 0
+    to 3 tokens, by themselves and with a long one among them that is cut."""
+    lens = [i % 4 for i in range(700)] + [long] + [(3 * i) % 4 for i in range(700)]
+    x = make(dtype, lens, 1, 1, 16, 32, True, seed=14)
+    d = dev(x)
+    for max_seqlen in (0, max(lens)):
+        kw = dict(cu_seqlens=d["cu"], init_state=d["S0"], max_seqlen=max_seqlen)
+        o, fin = ssd.linattn_fwd(d["q"], d["k"], d["v"], d["a"], **kw)
+        g = ssd.linattn_bwd(d["q"], d["k"], d["v"], d["dout"], d["a"], dfinal_state=d["dfin"], **kw)
+        sync_ok()
+        want = ref(x, lens, 16 ** -0.5, grads=True)
+        assert off(num(o), want[0]) < TOL[dtype] and off(num(fin), want[1]) < TOL["f32"]
+        for i in range(3):
+            assert off(num(g[i]), want[2 + i]) < TOL[dtype]
+        assert off(num(g[3]), want[5]) < TOL["f32"]
+
+
 def test_one_long_sequence():
     """A single sequence's ranges are made to fill the GPU (their number follows from
     the length alone), with and without offsets; so are those of equal sequences."""
