@@ -91,7 +91,7 @@ ssd_status make_la(const ssd_linattn_dims* d, bool packed, bool backward, La* p)
     const int64_t cap = g.split ? p->T / R + p->n + 2 : p->n + 1;
     if (cap > (1LL << 24)) return SSD_ERR_SHAPE;
     g.range_cap = (int)cap;
-    p->agg_bytes = g.split ? round_up256((size_t)(cap * p->H * p->K * p->V) * 4) : 0;
+    p->agg_bytes = g.split ? round_up256((size_t)(la_slots(p->T, R) * p->H * p->K * p->V) * 4) : 0;
     return SSD_OK;
 }
 

@@ -48,7 +48,7 @@ struct LaJob {
     int sk, sv;                  // element strides of X's rows (DK) and columns (DV) in a stored state
     const float* init;           // [nseq, H, DK x DV], or NULL
     float* fin;                  // likewise, or NULL
-    float* agg;                  // [range_cap, H, DK x DV] when split
+    float* agg;                  // [la_slots, H, DK x DV] when split
 };
 
 struct LaParams {
@@ -62,7 +62,11 @@ struct LaParams {
 struct LaRange {
     int seq, first, last;   // sequence; whether the range is its first and its last
     int t0, len;            // first token and tokens of the range
+    int slot;               // where its state is in agg, if its sequence is cut
 };
+// Slots of agg: j for the range that begins at row j R, T / R + 1 + j for one that
+// begins a sequence and ends there.  So they do not grow with the sequences.
+__host__ __device__ inline int64_t la_slots(int64_t T, int64_t R) { return 2 * (T / R + 1); }
 
 #ifdef __CUDACC__
 __device__ __forceinline__ void la_bounds(const LaGeom& g, int s, int& lo, int& hi) {
@@ -84,7 +88,7 @@ __device__ __forceinline__ LaRange la_find(const LaGeom& g, int idx) {
     LaRange r;
     r.seq = -1;
     r.first = r.last = 1;
-    r.t0 = r.len = 0;
+    r.t0 = r.len = r.slot = 0;
     int lo, hi;
     if (idx <= g.nseq) {
         la_bounds(g, idx, lo, hi);
@@ -94,6 +98,7 @@ __device__ __forceinline__ LaRange la_find(const LaGeom& g, int idx) {
         r.last = end == hi;
         r.t0 = lo;
         r.len = end - lo;
+        r.slot = g.T / g.R + 2 + lo / g.R;
     } else {
         const int lane = threadIdx.x & 31, x = (idx - g.nseq - 1) * g.R;
         if (x >= g.T) return r;
@@ -110,6 +115,7 @@ __device__ __forceinline__ LaRange la_find(const LaGeom& g, int idx) {
         la_bounds(g, at - 1, lo, hi);
         if (lo >= x || hi <= x) return r;   // a sequence begins here, or no content of cu says where
         r.seq = at - 1;
+        r.slot = idx - g.nseq - 1;
         r.first = 0;
         r.t0 = x;
         r.len = min(g.R, hi - x);

@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(kThreads, 2) linattn_simt(const __grid_constan
     const int64_t elems = (int64_t)jb.DK * jb.DV;
     const int64_t so = ((int64_t)rg.seq * g.H + h) * elems;
     if (!kAgg) grid_dependency_wait();
-    float* ag = cut ? jb.agg + ((int64_t)blockIdx.x * g.H + h) * elems : nullptr;
+    float* ag = cut ? jb.agg + ((int64_t)rg.slot * g.H + h) * elems : nullptr;
     const float* in = kAgg ? nullptr : (cut ? ag : (jb.init ? jb.init + so : nullptr));
     // neighbouring threads along whichever of the stored state's axes is contiguous
     const bool kfirst = jb.sk == 1;
@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(256) linattn_scan(const __grid_constant__ LaPa
     la_decay_pow(g.a, h, g.R, f_hi, f_lo);
     la_decay_pow(g.a, h, hi - lo - first - (n - 2) * g.R, t_hi, t_lo);
     const auto state = [&](int r) {
-        const int id = r == 0 ? seq : g.nseq + 1 + lo / g.R + r;
+        const int id = r == 0 ? g.T / g.R + 2 + lo / g.R : lo / g.R + r;
         return reinterpret_cast<float4*>(jb.agg + ((int64_t)id * g.H + h) * elems + e);
     };
     // eight ranges' sums in flight: the walk is all latency

@@ -233,7 +233,7 @@ __device__ __forceinline__ int granted_item(uint32_t slot) {
 // shared memory: found by every role for itself, each change of item cost the
 // time of two or three chunks.
 struct Item {
-    int seq, ridx, t0, len;        // sequence (nseq: rows of none), range, its rows
+    int seq, ridx, t0, len;        // sequence (nseq: rows of none), range (its slot of agg), its rows
     int job, h, v0, nch;           // nch < 0: no more items
     int cut, last;
     float a2, hi, lo;              // log2 of the decay; the decay over a chunk
@@ -262,7 +262,7 @@ __device__ __forceinline__ LaRange longest(const LaGeom& g, int idx) {
     LaRange r;
     r.seq = -1;
     r.first = r.last = 1;
-    r.t0 = r.len = 0;
+    r.t0 = r.len = r.slot = 0;
     if (src < 0) return r;
     lo = __shfl_sync(0xffffffffu, lo, src);
     hi = __shfl_sync(0xffffffffu, hi, src);
@@ -285,6 +285,7 @@ __device__ __forceinline__ void decode_item(const TcParams& tp, int it, Item* sl
     const float a = tp.p.g.a[r.h];
     const LaRange rg = !kSplit && tp.p.g.nseq < 32 ? longest(tp.p.g, r.ridx) : la_find(tp.p.g, r.ridx);
     r.seq = rg.seq;
+    r.ridx = rg.slot;
     r.t0 = rg.t0;
     r.len = rg.len;
     r.v0 = vb * kLaCols;
