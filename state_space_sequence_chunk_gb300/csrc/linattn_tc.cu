@@ -44,7 +44,7 @@
 // traffic (400 KB) side by side, and between them a chain that bounds it (terms, half of U,
 // terms, half of U, state, and the issuing warp's fetches at each turn of its loop).
 // 16384 packed tokens, 32 heads of 128 x 128: 150 us, 58 % of the copy rate on the bytes
-// that must move; one sequence of 65536, 24 heads of 128 x 64 with shared q and k: 281 us
+// that must move; one sequence of 65536, 24 heads of 128 x 64 with shared q and k: 283 us
 // in three launches (80, 15 and 183); a training step of 16384 tokens, 16 heads of
 // 128 x 128: 304 us.
 #include <cuda.h>
