@@ -461,7 +461,9 @@ def _addr(t):
 
 def _rows(t, inner: int):
     """Address and row stride of a tensor [rows, ...] whose rows are contiguous
-    (`inner` elements each) and evenly spaced."""
+    (`inner` elements each) and evenly spaced.  Rows that share memory, as a tensor
+    expanded over its rows has them, are refused: the library reads a stride of 0 as
+    contiguous rows, which lie past the end of such a tensor's one."""
     if not t.is_cuda:
         raise ValueError("tensors must be CUDA tensors")
     if t.is_contiguous():
@@ -471,6 +473,8 @@ def _rows(t, inner: int):
         if n != 1 and s != want:
             raise ValueError("each row (all dimensions but the first) must be contiguous")
         want *= n
+    if t.shape[0] > 1 and t.stride(0) < inner:
+        raise ValueError("rows must not share memory (a tensor expanded over its rows needs .contiguous())")
     return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else inner)
 
 
