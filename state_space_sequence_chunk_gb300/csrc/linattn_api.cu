@@ -67,7 +67,8 @@ ssd_status make_la(const ssd_linattn_dims* d, bool packed, bool backward, La* p)
     if (longest > p->T) longest = p->T;
     int64_t R = (share / 2 + 127) / 128 * 128;
     if (R < least) R = least;
-    g.split = longest > R && longest > share + (d->dtype == SSD_F32 ? 0 : share / 2 + 896);
+    // (without a sequence there is none to cut: every row's result is 0)
+    g.split = p->n > 0 && longest > R && longest > share + (d->dtype == SSD_F32 ? 0 : share / 2 + 896);
     // Half a share, so that the range taken last adds at most half; where the lengths
     // are known, the number of ranges that fills the SMs in the shortest time (a range
     // costs 2 chunks more than its own): one sequence of 65536 tokens on 24 chains in

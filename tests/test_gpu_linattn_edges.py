@@ -1,0 +1,72 @@
+"""Linear attention at the edges of what its arguments may be: no sequence, rows of no
+sequence behind long ones."""
+import numpy as np
+import pytest
+import torch
+
+import state_space_sequence_chunk_gb300 as ssd
+from linattn_ref import off
+from test_gpu_linattn import DT, TOL, dev, make, num, ref, sync_ok
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("tokens", [1, 200, 10000])
+@pytest.mark.parametrize("H,G", [(4, 4), (4, 2)])
+def test_rows_without_a_sequence(dtype, tokens, H, G):
+    """Offsets [0]: every row belongs to no sequence, whatever it holds, and its
+    results are 0; the calls after that one are as ever."""
+    x = dev(make(dtype, [tokens], H, G, 64, 64, False))
+    for n in ("q", "k", "v", "dout"):
+        x[n][::7] = float("nan")
+    cu = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = torch.full((tokens, H, 64), 7.0, dtype=DT[dtype], device="cuda")
+    for max_seqlen in (0, 100):
+        o, fin = ssd.linattn_fwd(x["q"], x["k"], x["v"], x["a"], cu_seqlens=cu, max_seqlen=max_seqlen, out=out)
+        g = ssd.linattn_bwd(x["q"], x["k"], x["v"], x["dout"], x["a"], cu_seqlens=cu, max_seqlen=max_seqlen)
+        sync_ok()
+        assert o is out and fin.shape == (0, H, 64, 64) and g[3] is None
+        for t in (o, *g[:3]):
+            assert torch.all(t == 0)
+        out.fill_(7.0)
+    # the runtime has no error left over
+    w = torch.ones(64, device="cuda")
+    ssd.block_norm_fwd(torch.ones(3, 64, device="cuda"), torch.ones(3, 64, device="cuda"), w)
+    sync_ok()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_long_tail_of_no_sequence(dtype):
+    """Rows of no sequence, longer than a range, behind a sequence that is cut and behind
+    one that is not."""
+    for lens, pad, max_seqlen in (([2500, 3], 3000, 0), ([300, 200], 3000, 300)):
+        x = make(dtype, lens, 2, 1, 32, 80, True, seed=15)
+        for n in ("q", "k", "v", "dout"):
+            x[n] = torch.cat([x[n], torch.full((pad, *x[n].shape[1:]), float("inf"), dtype=x[n].dtype)])
+        d = dev(x)
+        kw = dict(cu_seqlens=d["cu"], init_state=d["S0"], max_seqlen=max_seqlen)
+        o, fin = ssd.linattn_fwd(d["q"], d["k"], d["v"], d["a"], **kw)
+        g = ssd.linattn_bwd(d["q"], d["k"], d["v"], d["dout"], d["a"], dfinal_state=d["dfin"], **kw)
+        sync_ok()
+        T = sum(lens)
+        want = ref({n: t if n in ("a", "S0", "dfin", "cu") else t[:T] for n, t in x.items()}, lens, 32 ** -0.5,
+                   grads=True)
+        for t, w in ((o, want[0]), *zip(g[:3], want[2:5])):
+            assert off(num(t[:T]), w) < TOL[dtype] and torch.all(t[T:] == 0)
+        assert off(num(fin), want[1]) < TOL["f32"] and off(num(g[3]), want[5]) < TOL["f32"]
+
+
+def test_rows_that_share_memory_are_refused():
+    x = dev(make("bf16", [40], 2, 1, 32, 64, False))
+    f = lambda **kw: ssd.linattn_fwd(**{**dict(q=x["q"], k=x["k"], v=x["v"], log_decay=x["a"]), **kw})
+    f()
+    for n in ("q", "k", "v"):
+        with pytest.raises(ValueError):
+            f(**{n: x[n][:1].expand(x[n].shape)})
+    r, y = torch.ones(4, 64, device="cuda"), torch.ones(4, 64, device="cuda")
+    w = torch.ones(64, device="cuda")
+    for kw in (dict(y=y[:1].expand(4, 64), z=y), dict(y=y, z=y[:1].expand(4, 64))):
+        with pytest.raises(ValueError):
+            ssd.block_norm_fwd(r, w_pre=w, gate="silu", **kw)
+    sync_ok()
