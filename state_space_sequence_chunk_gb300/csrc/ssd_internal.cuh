@@ -159,7 +159,13 @@ inline bool overlap(Range a, Range b) {
     return a.lo != 0 && b.lo != 0 && a.hi > a.lo && b.hi > b.lo && a.lo < b.hi && b.lo < a.hi;
 }
 inline bool aligned16(const void* p) { return p == nullptr || ((uintptr_t)p & 15u) == 0; }
-inline ssd_status from_cuda(cudaError_t e) { return e == cudaSuccess ? SSD_OK : SSD_ERR_CUDA; }
+// An entry point's status for what its launches returned.  A failure is reported
+// here and taken from the runtime, which would report it once more to whoever looks next.
+inline ssd_status from_cuda(cudaError_t e) {
+    if (e == cudaSuccess) return SSD_OK;
+    cudaGetLastError();
+    return SSD_ERR_CUDA;
+}
 // Checks made after the arguments are validated and before anything is
 // enqueued: the device's compute capability, then whether a bounded wait in
 // an earlier launch on this device has given up (reported once, as
