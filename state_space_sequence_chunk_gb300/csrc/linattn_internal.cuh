@@ -124,6 +124,16 @@ __device__ __forceinline__ LaRange la_find(const LaGeom& g, int idx) {
     return r;
 }
 
+// f(row, piece) for every piece of `rows` rows of `pieces` each (16 at most), shared out
+// among `nthreads`.  Rows and pieces are counted apart: rows of no sequence can be 2^30,
+// and their pieces do not fit 32 bits.
+template <typename F>
+__host__ __device__ __forceinline__ void la_zero_rows(int rows, int pieces, int thread, int nthreads, const F& f) {
+    const int step = nthreads / pieces, t = thread / pieces;
+    if (t >= step) return;
+    for (int row = t; row < rows; row += step) f(row, thread - t * pieces);
+}
+
 // log2 of the head's decay: 0 or less.  -inf (no memory) becomes a finite value
 // whose every power but the 0th is 0; a NaN stays one.
 __device__ __forceinline__ float la_log2_decay(const float* a, int h) {

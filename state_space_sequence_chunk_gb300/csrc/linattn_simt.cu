@@ -101,11 +101,10 @@ __global__ void __launch_bounds__(kThreads, 2) linattn_simt(const __grid_constan
     const int nv = min(kLaCols, jb.DV - v0);
     if (rg.seq == g.nseq) {               // tokens of no sequence: zeros
         if (kAgg) return;
-        for (int i = tid; i < rg.len * nv; i += kThreads) {
-            const int t = i / nv, v = i - t * nv;
-            const int64_t at = ((int64_t)(rg.t0 + t) * g.H + h) * jb.DV + v0 + v;
-            static_cast<float*>(jb.out)[at] = 0.f;
-        }
+        la_zero_rows(rg.len, nv / 4, tid, kThreads, [&](int t, int v) {
+            st4(static_cast<float*>(jb.out) + ((int64_t)(rg.t0 + t) * g.H + h) * jb.DV + v0 + 4 * v,
+                make_float4(0.f, 0.f, 0.f, 0.f));
+        });
         return;
     }
     const bool cut = g.split && !(rg.first && rg.last);

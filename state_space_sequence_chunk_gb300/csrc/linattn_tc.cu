@@ -870,12 +870,12 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
             const bool f32o = kPart && jb.out_f32;
             const int64_t os = (int64_t)g.H * jb.DV, oh = (int64_t)im.h * jb.DV + im.v0;
             if (im.seq == g.nseq) {                   // tokens of no sequence: zeros
-                for (int x = i; x < im.len * (nv / 16); x += 128) {
-                    const int64_t e = (int64_t)(im.t0 + x / (nv / 16)) * os + oh + x % (nv / 16) * 16;
+                la_zero_rows(im.len, nv / 16, i, 128, [&](int t, int v) {
+                    const int64_t e = (int64_t)(im.t0 + t) * os + oh + v * 16;
                     uint4* d = f32o ? reinterpret_cast<uint4*>(static_cast<float*>(jb.out) + e)
                                           : reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(jb.out) + e);
                     for (int q = 0; q < (f32o ? 4 : 2); ++q) d[q] = make_uint4(0u, 0u, 0u, 0u);
-                }
+                });
             }
             const float a2 = im.a2;
             const bool fac = factored(a2);

@@ -1,6 +1,5 @@
 """Linear attention at the edges of what its arguments may be: no sequence, rows of no
 sequence behind long ones."""
-import numpy as np
 import pytest
 import torch
 
@@ -70,3 +69,20 @@ def test_rows_that_share_memory_are_refused():
         with pytest.raises(ValueError):
             ssd.block_norm_fwd(r, w_pre=w, gate="silu", **kw)
     sync_ok()
+
+
+def test_more_rows_of_no_sequence_than_32_bits_count():
+    """2^25 rows of 64 columns behind a short sequence, uncut: their elements pass 2^31."""
+    T, K, V = (1 << 25) + 100, 16, 64
+    q = torch.zeros(T, 1, K, device="cuda")
+    v = torch.zeros(T, 1, V, device="cuda")                      # 8.6 GB, and as much for o
+    out = torch.full((T, 1, V), 7.0, device="cuda")
+    torch.manual_seed(16)
+    q[:100], v[:100] = torch.randn(100, 1, K, device="cuda"), torch.randn(100, 1, V, device="cuda")
+    a = torch.tensor([-0.1], device="cuda")
+    cu = torch.tensor([0, 100], dtype=torch.int32, device="cuda")
+    o, _ = ssd.linattn_fwd(q, q, v, a, cu_seqlens=cu, max_seqlen=100, out=out)
+    want, _ = ssd.linattn_fwd(q[:100], q[:100], v[:100], a)
+    sync_ok()
+    assert o is out and torch.equal(o[:100], want)
+    assert not torch.any(o[100:])
