@@ -317,9 +317,11 @@ size_t ssd_linattn_workspace_bytes(const ssd_linattn_dims* d, int backward);
  * prompt.  With lam = exp(log_decay[h]), for each sequence and head, from
  * S = init_state (or 0) and for its tokens t in order:
  *   S <- lam S + v_t k_t^T  (vdim x kdim)        o_t = scale S q_t
- * evaluated chunk by chunk: fp32 sums and state, o rounded once to `dtype`.
- * In bf16 the products inside a chunk (q.k; backwards v.dout and k.q too) carry their
- * decay as two factors within 2^+-60: one beyond 2^67 overflows, one below 2^-66 is lost.
+ * evaluated chunk by chunk: fp32 sums and state.  In bf16 the last products of o have an
+ * operand each that is rounded to bf16 besides o itself: the decayed q.k inside a chunk (to
+ * 16 bits in a chunk of up to 64 tokens) and the copy of the state that q is multiplied
+ * with.  So o, and likewise dq, dk and dv, are off by 0.0023 in the 2-norm where one
+ * rounding alone gives 0.0017; states are held and returned in fp32.
  *   log_decay    [nheads] fp32, <= 0 (a larger value counts as 0; -inf: no memory).
  *   cu_seqlens   [nseqs + 1] int32 on the device: sequence s is the rows
  *                cu_seqlens[s] .. cu_seqlens[s + 1] - 1; cu_seqlens[0] == 0, not

@@ -5,15 +5,19 @@
 // 128 tokens.  With i, j the rows of a chunk (counted from its end when the walk
 // is backwards), n its tokens and X the state before it:
 //     W   = A B^T                                   128 x 128 x DK
-//     P   = s_in W o lam^{64-j} [i >= j]            (bf16, tensor memory)
-//     out = s_out lam^{i-64} o (A (lam^65 X) + P C) 128 x 64 x DK, 128 x 64 x 128
+//     P   = s_in W o lam^{i-j} [i >= j]             (bf16, tensor memory)
+//     out = s_out (lam^{i+1} o (A X) + P C)         128 x 64 x DK, 128 x 64 x 128
 //     U   = B^T (s_in lam^{n-1-j} o C)              DK x 64 x 128
 //     X   <- lam^n X + U
-// (backwards X and U have decayed one step less and one more).  Rows and columns carry
-// the decay as separate factors, so that out is one accumulator and P costs one
-// product for each element; that is safe while lam^127 >= 2^-120.  For heads that
-// forget faster the exact form runs: lam^{i-j} element by element, A X and P C
-// in two accumulators.
+// (backwards X and U have decayed one step less and one more).  No factor is above 1:
+// lam^{i-j} is taken as a power up to the column's block of 32 times one within it, and
+// the rows of A X get theirs in the accumulator, before P C is added to it.  So products
+// and states of any size that fp32 holds come through, however fast the head forgets.
+// (Row and column factors about the chunk's middle, lam^{i-64} and lam^{64-j}, save that
+// pass over the accumulator, but reach 2^+-60 for a head with lam = 1/2: a product or a
+// state beyond 2^67 overflowed, one below 2^-66 was lost.  They took 151 us instead of 154
+// for the packed prompt below, 283 instead of 271 for the long one, 303 instead of 320 for
+// the training step.)
 // Every operand is read once per chain from HBM (a and b once per 64 columns of
 // c, from L2 the second time) and no state leaves the chip between chunks.
 //
@@ -83,11 +87,6 @@ template <bool kAgg> struct Cfg {
 // tensor memory columns
 constexpr uint32_t kW = 0;                    // W / P, two buffers of 128
 constexpr uint32_t kO = 256, kUMain = 320;    // out; U's three terms
-// The factored form takes heads whose decay over a chunk's 127 steps is at least
-// 2^-kSpan: row and column factors, counted from the middle, are within 2^+-60.
-// (A product a b beyond 2^67 would overflow in it and one below 2^-66 vanish.)
-constexpr float kSpan = 120.f;
-constexpr int kMid = 64;
 
 struct TcParams {
     LaParams p;
@@ -165,19 +164,18 @@ __device__ __forceinline__ bool first_of(uint32_t a, uint32_t a_parity, uint32_t
 
 __device__ __forceinline__ void ld_cols(uint32_t at, uint32_t (&r)[4]) { tmem_ld_x4(at, r); }
 __device__ __forceinline__ void ld_cols(uint32_t at, uint32_t (&r)[8]) { tmem_ld_x8(at, r); }
-__device__ __forceinline__ bool factored(float a2) { return a2 * -127.f <= kSpan; }
 // A chunk of so few tokens leaves the second half of P's contraction free: it holds
 // P's second terms there (and P is then good to 16 bits), for tokens whose output is
-// a sum of a few products, or of one.  (In the exact form the columns behind are taken.)
-__device__ __forceinline__ bool few(int n, bool fac) { return n <= (fac ? 64 : 32); }
+// a sum of a few products, or of one.
+__device__ __forceinline__ bool few(int n) { return n <= 64; }
 // P of such a chunk, a row to a thread.  Not inlined: the roles' loops share the
 // instruction cache (in line, a training step of 16384 tokens took 333 us, not 325).
-__device__ __noinline__ void few_p(uint32_t base, uint32_t ptab, int row, int n, float a2, float s_in, bool fac, int rev) {
+__device__ __noinline__ void few_p(uint32_t base, int row, int n, float a2, float s_in, int rev) {
 #pragma unroll 1
     for (int j0 = 0; j0 < 64; j0 += 8) {
-        uint32_t v[8] = {}, hi[4], lo[4];
+        uint32_t v[8], hi[4], lo[4];
         __syncwarp();
-        if (fac || j0 < 32) tmem_ld_x8(base + j0, v);
+        tmem_ld_x8(base + j0, v);
         tmem_wait_ld();
 #pragma unroll
         for (int e = 0; e < 8; e += 2) {
@@ -185,7 +183,7 @@ __device__ __noinline__ void few_p(uint32_t base, uint32_t ptab, int row, int n,
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
                 const int j = j0 + e + y, d = rev ? j - row : row - j;
-                const float w = fac ? lds32(ptab + 4 * j) : exp2f(a2 * (float)max(d, 0)) * s_in;
+                const float w = exp2f(a2 * (float)max(d, 0)) * s_in;
                 r[y] = d >= 0 && j < n ? __uint_as_float(v[e + y]) * w : 0.f;
             }
             hi[e / 2] = pack2(r[0], r[1]);
@@ -196,7 +194,7 @@ __device__ __noinline__ void few_p(uint32_t base, uint32_t ptab, int row, int n,
         }
         __syncwarp();
         tmem_st_x4(base + j0 / 2, hi);
-        tmem_st_x4(base + j0 / 2 + (fac ? 64 : 32), lo);
+        tmem_st_x4(base + j0 / 2 + 64, lo);
     }
     tmem_wait_st();
 }
@@ -380,6 +378,7 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
     uint64_t* b_xdone = bars + 25;    // A X computed: the bf16 X may change (commit)
     uint64_t* b_odone = bars + 26;    // out computed (commit)
     uint64_t* b_ofree = bars + 27;    // out read (128)
+    uint64_t* b_scaled = bars + 118;  // A X has its rows' decay (128)
     uint64_t* b_answer = bars + 28;   // answer to an item request (tx)
     uint64_t* b_iready = bars + 29;   // [2] item decoded (1)
     uint64_t* b_ifree = bars + 31;    // [2] item read (every other warp that walks items)
@@ -410,6 +409,7 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
         }
         mbar_init(smem_u32(b_answer), 1);
         mbar_init(smem_u32(b_sready), 256);
+        mbar_init(smem_u32(b_scaled), 128);
         mbar_init(smem_u32(b_xdone), 1);
         mbar_init(smem_u32(b_odone), 1);
         mbar_init(smem_u32(b_ofree), 128);
@@ -509,12 +509,11 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
 #pragma unroll 1
         while (read_item(im)) {
             const int nch = uniform(im.nch), ks = uniform(tp.p.job[im.job].DK / 16);
-            const int fac = uniform(factored(im.a2) ? 1 : 0);
             // x = -1: the W of the item's first chunk
             const int x0 = kAgg || ahead ? 0 : -1;
             ahead = false;
             // the item's only chunk that may be of few tokens
-            const int few_x = uniform(!few(im.len - (nch - 1) * kC, fac) ? -1 : tp.p.job[im.job].rev ? 0 : nch - 1);
+            const int few_x = uniform(!few(im.len - (nch - 1) * kC) ? -1 : tp.p.job[im.job].rev ? 0 : nch - 1);
             if (elect_one()) {
 #pragma unroll 1
                 for (int x = x0; x < nch; ++x) {
@@ -543,6 +542,13 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                             mma_f16_ss(ud, ad + o, bd + o, kIdU, half + kk > 0 ? 1u : 0u);
                         }
                     };
+                    const auto x_product = [&]() {   // out = A X
+                        wait_on(smem_u32(b_sready), cc & 1, err);
+                        tc_fence_after();
+                        mma_steps<true, false>(tmem + kO, smem_desc_sw128(st, 16, 8 * kRow),
+                                               smem_desc_sw128(smem_u32(xs), 8 * kRow, 8 * kRow), ks, kIdO);
+                        mma_commit(smem_u32(b_xdone));
+                    };
                     if (x >= 0) {
                         if (kAgg) wait_on(smem_u32(b_fab + sb), (cc / kSt) & 1, err);
                         // U = B^T (scaled C), its three terms side by side: B is read once
@@ -553,8 +559,7 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                         u_half(0);
                         mma_commit(smem_u32(b_udone));
                         if (!kAgg) {
-                            // the last out is read: its accumulator is free, and in the exact form
-                            // W's buffer
+                            // the last out is read: its accumulator is free
                             wait_on(smem_u32(b_ofree), (cc & 1) ^ 1, err);
                             if (x + 1 == nch && mbar_test(smem_u32(b_iready + (k_item & 1)), (k_item >> 1) & 1)) {
                                 // the first W of the next item, if that is known by now
@@ -571,37 +576,34 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                             // tokens, 24 heads of 128 x 64.  Waited for: 158 instead of 150 us for
                             // 16384 tokens whose tiles come from HBM, 32 heads of 128 x 128.)
                             if (w_due && first_of(smem_u32(b_fab + s1), use1 & 1, smem_u32(b_vready + 1), cc & 1)) w_product();
+                            // A X too: the out role gives its rows their decay meanwhile.  (Before
+                            // W: the training step in 327 us instead of 320; not waited for: 329;
+                            // after U: 323, and the packed prompt in 156 instead of 154.)
+                            x_product();
                         }
                         wait_on(smem_u32(b_vready + 1), cc & 1, err);
                         tc_fence_after();
                         u_half(1);
                         mma_commit(smem_u32(b_udone + 1));
                         mma_commit(smem_u32(b_ux + (kUb == 2 ? s : 0)));
+                        mma_commit(smem_u32(b_eab + sb));
                         if (kAgg) {
-                            mma_commit(smem_u32(b_eab + sb));
                             mma_commit(smem_u32(b_ec) + 8 * (cc % kCs));
                         } else {
-                            // out = A X
-                            wait_on(smem_u32(b_sready), cc & 1, err);
-                            tc_fence_after();
-                            mma_steps<true, false>(tmem + kO, smem_desc_sw128(st, 16, 8 * kRow),
-                                                   smem_desc_sw128(smem_u32(xs), 8 * kRow, 8 * kRow), ks, kIdO);
-                            mma_commit(smem_u32(b_xdone));
-                            mma_commit(smem_u32(b_eab + s));
-                            // out += P C; in the exact form, beside P's columns in W's buffer
+                            // out += P C
                             wait_on(smem_u32(b_fc) + 8 * (cc % kCs), (cc / kCs) & 1, err);
                             wait_on(smem_u32(b_pready + s), use & 1, err);
+                            wait_on(smem_u32(b_scaled), cc & 1, err);
                             tc_fence_after();
                             const uint64_t bd = smem_desc_sw128(smem_u32(ctile) + (cc % kCs) * kAtom, 8 * kRow, 8 * kRow);
-                            const uint32_t to = tmem + (fac ? kO : kW + s * 128 + 64);
-                            const uint32_t pa = tmem + kW + s * 128, pb = pa + (fac ? 32 : 0);
+                            const uint32_t pa = tmem + kW + s * 128, pb = pa + 32;
                             // the second half of the contraction: tokens 64 .. 127, or for a
                             // chunk of few tokens their second terms
                             const uint64_t be = bd - (x == few_x ? (uint64_t)((64 * kRow) >> 4) : 0);
 #pragma unroll
                             for (int kk = 0; kk < 8; ++kk)
-                                mma_f16_ts(to, (kk < 4 ? pa : pb) + kk * 8, (kk < 4 ? bd : be) + (uint64_t)((kk * 16 * kRow) >> 4),
-                                           kIdO, kk > 0 ? 1u : (uint32_t)fac);
+                                mma_f16_ts(tmem + kO, (kk < 4 ? pa : pb) + kk * 8, (kk < 4 ? bd : be) + (uint64_t)((kk * 16 * kRow) >> 4),
+                                           kIdO, 1u);
                             mma_commit(smem_u32(b_odone));
                         }
                     }
@@ -621,12 +623,9 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
             if (im.nch == 0) continue;
             const LaJob& jb = tp.p.job[im.job];
             const float a2 = im.a2;
-            const bool fac = factored(a2);
             bar_p();                        // the table's last readers are done
-            // factored: lam^{mid-j'} s_in; exact: lam^j (the first 32 are used) and,
-            // from 32 on, lam^{31-j}
-            if (warp < 4) sts32(ptab + 4 * row, fac ? la_exp2(a2, kMid - (jb.rev ? kC - 1 - row : row)) * jb.s_in
-                                      : exp2f(a2 * (float)(row < 32 ? row : max(63 - row, 0))));
+            // s_in lam^j for j < 32 and, from there on, s_in lam^{31-j}
+            if (warp < 2) sts32(ptab + 4 * row, exp2f(a2 * (float)(row < 32 ? row : 63 - row)) * jb.s_in);
             bar_p();
             const uint32_t vt = jb.rev ? ptab : ptab + 32 * 4;
 #pragma unroll 1
@@ -636,17 +635,15 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                 wait_on(smem_u32(b_wdone + s), (c >> 1) & 1, err);
                 tc_fence_after();
                 const uint32_t base = tmem + lane_off + kW + s * 128;
-                if (few(n, fac)) {
-                    if (warp < 4 && quad * 32 < n) few_p(base, ptab, row, n, a2, jb.s_in, fac, jb.rev);
+                if (few(n)) {
+                    if (warp < 4 && quad * 32 < n) few_p(base, row, n, a2, jb.s_in, jb.rev);
                     tc_fence_before();
                     mbar_arrive(smem_u32(b_pready + s));
                     continue;
                 }
                 // 16 columns at a time, in place: each half's packed columns lie
-                // within its own and behind its reads.  (The exact form needs the
-                // upper half's columns for its second accumulator, so one warpgroup
-                // packs all into the lower.)
-                const int b0 = warp < 4 ? 0 : fac ? 4 : 8, b1 = warp < 4 && fac ? 4 : 8;
+                // within its own and behind its reads
+                const int b0 = warp < 4 ? 0 : 4, b1 = b0 + 4;
 #pragma unroll 1
                 for (int b = b0; b < b1; ++b) {
                     const int rel = jb.rev ? (b >> 1) - quad : quad - (b >> 1);
@@ -659,23 +656,17 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                         uint32_t v[16];
                         __syncwarp();
                         tmem_ld_x16(base + j0, v);
-                        if (fac || rel > 0) {
-                            const uint32_t ct = fac ? ptab + 4 * j0 : vt + 4 * (j0 & 31);
-                            // exact: lam^{i-j} as a row factor times a column factor, both <= 1
-                            const float u = fac ? 1.f : exp2f(a2 * (float)(jb.rev ? (j0 & ~31) - row : row - (j0 & ~31) - 31)) * jb.s_in;
+                        if (rel > 0) {
+                            const uint32_t ct = vt + 4 * (j0 & 31);
+                            // lam^{i-j} as a row factor times a column factor, both <= 1
+                            const float u = exp2f(a2 * (float)(jb.rev ? (j0 & ~31) - row : row - (j0 & ~31) - 31));
                             const f32x2 u2 = pair(u, u);
                             tmem_wait_ld();
 #pragma unroll
                             for (int e4 = 0; e4 < 4; ++e4) {
                                 const uint4 t = lds128(ct + 16 * e4);
-                                f32x2 r0 = mul2(pair(v[4 * e4], v[4 * e4 + 1]), pair(t.x, t.y));
-                                f32x2 r1 = mul2(pair(v[4 * e4 + 2], v[4 * e4 + 3]), pair(t.z, t.w));
-                                if (!fac) {
-                                    r0 = mul2(r0, u2);
-                                    r1 = mul2(r1, u2);
-                                }
-                                o[2 * e4] = pack2(r0);
-                                o[2 * e4 + 1] = pack2(r1);
+                                o[2 * e4] = pack2(mul2(pair(v[4 * e4], v[4 * e4 + 1]), mul2(pair(t.x, t.y), u2)));
+                                o[2 * e4 + 1] = pack2(mul2(pair(v[4 * e4 + 2], v[4 * e4 + 3]), mul2(pair(t.z, t.w), u2)));
                             }
                         } else {
                             tmem_wait_ld();
@@ -683,8 +674,8 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                             for (int e = 0; e < 8; ++e) {
                                 const int d = (j0 & 31) + 2 * e - lane;   // above the diagonal: masked below
                                 o[e] = pack2(mul2(pair(v[2 * e], v[2 * e + 1]),
-                                                  pair(lds32(ptab + 4 * ((jb.rev ? d : -d) & 31)) * jb.s_in,
-                                                       lds32(ptab + 4 * ((jb.rev ? d + 1 : -d - 1) & 31)) * jb.s_in)));
+                                                  pair(lds32(ptab + 4 * ((jb.rev ? d : -d) & 31)),
+                                                       lds32(ptab + 4 * ((jb.rev ? d + 1 : -d - 1) & 31)))));
                             }
                         }
                         // a select, never a product, drops what is above the diagonal
@@ -796,22 +787,16 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                 const bool ok = in != nullptr && k < jb.DK && 2 * v < nv;
                 X[v] = pair(ok ? in[(int64_t)(2 * v) * jb.sv] : 0.f, ok ? in[(int64_t)(2 * v + 1) * jb.sv] : 0.f);
             }
-            const float a2 = im.a2;
-            const bool fac = factored(a2);
 #pragma unroll 1
             for (int x = 0; x < im.nch; ++x, ++c) {
                 const int ci = jb.rev ? im.nch - 1 - x : x;
                 const int n = min(kC, im.len - ci * kC);
                 if (!kAgg) {
-                    // in the factored form the row factor of out is lam^{i'}
-                    const float m = fac ? la_exp2(a2, (jb.rev ? n - kC : 1) + kMid) : 1.f;
-                    const f32x2 m2 = pair(m, m);
                     if (c > 0) wait_on(smem_u32(b_xdone), (c - 1) & 1, err);
 #pragma unroll
                     for (int ch = 0; ch < 4; ++ch)
                         sts128(smem_u32(xs) + k * kRow + (((vc / 8 + ch) ^ (k & 7)) << 4),
-                               pack2(mul2(X[4 * ch], m2)), pack2(mul2(X[4 * ch + 1], m2)),
-                               pack2(mul2(X[4 * ch + 2], m2)), pack2(mul2(X[4 * ch + 3], m2)));
+                               pack2(X[4 * ch]), pack2(X[4 * ch + 1]), pack2(X[4 * ch + 2]), pack2(X[4 * ch + 3]));
                     fence_proxy_async_smem();
                     mbar_arrive(smem_u32(b_sready));
                 }
@@ -878,41 +863,44 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                 });
             }
             const float a2 = im.a2;
-            const bool fac = factored(a2);
+            const f32x2 f2 = pair(jb.s_out, jb.s_out);
 #pragma unroll 1
             for (int x = 0; x < im.nch; ++x, ++c) {
                 const int ci = jb.rev ? im.nch - 1 - x : x;
                 const int n = min(kC, im.len - ci * kC);
-                const float f = jb.s_out * (fac ? la_exp2(a2, (jb.rev ? kC - 1 - i : i) - kMid)
-                                                : exp2f(a2 * (float)(jb.rev ? n - 1 - i : i + 1)));
                 const int64_t e0 = (int64_t)(im.t0 + ci * kC + i) * os + oh;
+                // A X in place: each row its decay, before P C is added
+                const float d = exp2f(a2 * (float)(jb.rev ? max(n - 1 - i, 0) : i + 1));
+                const f32x2 d2 = pair(d, d);
+                wait_on(smem_u32(b_xdone), c & 1, err);
+                tc_fence_after();
+#pragma unroll 1
+                for (int b = 0; b < 64; b += 16) {
+                    uint32_t p[16];
+                    __syncwarp();
+                    tmem_ld_x16(tmem + lane_off + kO + b, p);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const f32x2 r = mul2(d2, pair(p[2 * e], p[2 * e + 1]));
+                        p[2 * e] = (uint32_t)r;
+                        p[2 * e + 1] = (uint32_t)(r >> 32);
+                    }
+                    tmem_st_x16(tmem + lane_off + kO + b, p);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(smem_u32(b_scaled));
                 wait_on(smem_u32(b_odone), c & 1, err);
                 tc_fence_after();
-                const f32x2 f2 = pair(f, f), s2 = pair(jb.s_out, jb.s_out);
                 // A full chunk's bf16 rows go out by TMA from the chunk's C tile, which
                 // nothing reads any more: stored from registers, a row to a thread, they
                 // took a fifth of the shared-memory and L1 data path that bounds the
                 // kernel.  The rows behind a ragged chunk's belong to others, so that
                 // one is stored row by row.
-                const bool tile = n == kC && (fac || !f32o);
+                const bool tile = n == kC;
                 const uint32_t ct = smem_u32(ctile) + (c % kCs) * kAtom;
-                const auto put = [&](int b, const uint32_t (&w)[8], const f32x2 (&r)[8]) {   // 16 columns
-                    if (tile) {
-                        sts128(ct + i * kRow + (((2 * b) ^ (i & 7)) << 4), w[0], w[1], w[2], w[3]);
-                        sts128(ct + i * kRow + (((2 * b + 1) ^ (i & 7)) << 4), w[4], w[5], w[6], w[7]);
-                    } else if (i < n && b * 16 < nv) {
-                        if (f32o) {
-                            ulonglong2* d = reinterpret_cast<ulonglong2*>(static_cast<float*>(jb.out) + e0 + b * 16);
-#pragma unroll
-                            for (int y = 0; y < 4; ++y) d[y] = make_ulonglong2(r[2 * y], r[2 * y + 1]);
-                        } else {
-                            uint4* d = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(jb.out) + e0 + b * 16);
-                            d[0] = make_uint4(w[0], w[1], w[2], w[3]);
-                            d[1] = make_uint4(w[4], w[5], w[6], w[7]);
-                        }
-                    }
-                };
-                if (fac && tile) {
+                if (tile) {
                     // the next chunk's product waits for the accumulator: it is given up
                     // as soon as its second half is in registers
 #pragma unroll
@@ -957,26 +945,27 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                 } else {
 #pragma unroll 1
                     for (int b = 0; b < 4; ++b) {
-                        uint32_t p[16], w[8];
+                        uint32_t p[16];
                         f32x2 r[8];
                         __syncwarp();
                         tmem_ld_x16(tmem + lane_off + kO + b * 16, p);
                         tmem_wait_ld();
 #pragma unroll
                         for (int e = 0; e < 8; ++e) r[e] = mul2(f2, pair(p[2 * e], p[2 * e + 1]));
-                        if (!fac) {
-                            tmem_ld_x16(tmem + lane_off + kW + (c & 1) * 128 + 64 + b * 16, p);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) r[e] = fma2(s2, pair(p[2 * e], p[2 * e + 1]), r[e]);
-                        }
                         if (b == 3) {
                             tc_fence_before();
                             mbar_arrive(smem_u32(b_ofree));
                         }
+                        if (i >= n || b * 16 >= nv) continue;
+                        if (f32o) {
+                            ulonglong2* d = reinterpret_cast<ulonglong2*>(static_cast<float*>(jb.out) + e0 + b * 16);
 #pragma unroll
-                        for (int y = 0; y < 8; ++y) w[y] = pack2(r[y]);
-                        put(b, w, r);
+                            for (int y = 0; y < 4; ++y) d[y] = make_ulonglong2(r[2 * y], r[2 * y + 1]);
+                        } else {
+                            uint4* d = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(jb.out) + e0 + b * 16);
+                            d[0] = make_uint4(pack2(r[0]), pack2(r[1]), pack2(r[2]), pack2(r[3]));
+                            d[1] = make_uint4(pack2(r[4]), pack2(r[5]), pack2(r[6]), pack2(r[7]));
+                        }
                     }
                 }
                 if (tile) fence_proxy_async_smem();

@@ -86,3 +86,37 @@ def test_more_rows_of_no_sequence_than_32_bits_count():
     sync_ok()
     assert o is out and torch.equal(o[:100], want)
     assert not torch.any(o[100:])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("power", [95, -95])
+def test_range_of_fp32(dtype, power):
+    """States and products near the ends of fp32's range come through in both directions,
+    whatever the decay: each case is an ordinary one with two operands times 2^(power / 2)
+    or a state and its operand times 2^power, whose results are those times powers of two."""
+    lens = [300, 129, 40]
+    decay = [-0.6, -0.3, -0.01, -2.0]
+    x = make(dtype, lens, 4, 4, 64, 64, True, seed=17, decay=decay)
+    d = dev(x)
+    kw = dict(cu_seqlens=d["cu"])
+    want = ref(x, lens, 0.125, grads=True)
+    s, h = 2.0 ** power, 2.0 ** (power // 2)
+
+    def run(q=1.0, k=1.0, v=1.0, dout=1.0, S0=1.0, dfin=1.0):
+        m = {n: d[n] * f for n, f in (("q", q), ("k", k), ("v", v), ("dout", dout), ("S0", S0), ("dfin", dfin))}
+        o, fin = ssd.linattn_fwd(m["q"], m["k"], m["v"], d["a"], init_state=m["S0"], scale=0.125, **kw)
+        g = ssd.linattn_bwd(m["q"], m["k"], m["v"], m["dout"], d["a"], init_state=m["S0"], scale=0.125,
+                            dfinal_state=m["dfin"], **kw)
+        sync_ok()
+        return o, fin, *g
+
+    def near(got, factors):
+        for i, (t, f) in enumerate(zip(got, factors)):
+            for head in range(4):
+                assert off(num(t[:, head]) / f, want[i][:, head]) < TOL["f32" if i in (1, 5) else dtype], (i, head)
+
+    # o, final state, dq, dk, dv, dS0
+    near(run(v=s, S0=s), (s, s, s, s, 1, 1))
+    near(run(dout=s, dfin=s), (1, 1, s, s, s, s))
+    near(run(q=h, k=h, S0=h, dfin=h), (h * h, h, h, h, h * h, h))
+    near(run(v=h, dout=h, S0=h, dfin=h), (h, h, h * h, h * h, h, h))
