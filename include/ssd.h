@@ -195,8 +195,10 @@ unsigned int ssd_take_device_errors(void);
  * publishing the state at the end of each CTA's work range, so that the CTA
  * that continues the chain waits in vain.  That wait is bounded (about 1 s of
  * SM clock): it gives up, sets bit 0 of the error word and the launch ends
- * early with undefined hiddens / final_state (and y).  The device context stays
- * usable; ssd_take_device_errors() reports and clears the bit.  Pass 0 to
+ * early with undefined hiddens / final_state (and y).  Likewise bf16 linear
+ * attention (prompts and gradients) loads nothing, its waits for the tiles give up,
+ * set bit 3, and the call ends early with undefined outputs.  The device context
+ * stays usable; ssd_take_device_errors() reports and clears the bits.  Pass 0 to
  * restore normal operation.  Not for production use.  Returns SSD_ERR_CUDA if
  * the flag cannot be written.
  */

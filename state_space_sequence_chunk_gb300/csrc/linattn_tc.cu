@@ -54,6 +54,8 @@
 #include <cuda.h>
 #include <string.h>
 
+#include <atomic>
+
 #include "f32x2.cuh"
 #include "linattn_internal.cuh"
 #include "sm100_ptx.cuh"
@@ -62,7 +64,12 @@
 namespace ssd {
 namespace {
 
-__device__ unsigned int g_la_error;  // bit 0: a bounded wait gave up
+// The number of the last launch in which a bounded wait gave up, or 0: by it the other
+// waits of that launch learn to give up too, and no later launch is taken for it.
+__device__ unsigned int g_la_error;
+// Test hook (ssd_debug_withhold_handoffs): nonzero makes the TMA warps load nothing, so
+// that the first waits run out.
+__device__ unsigned int g_la_withhold;
 
 constexpr int kC = 128;                       // tokens per chunk
 constexpr int kRow = 128;                     // bytes of a tile row (64 columns)
@@ -91,6 +98,7 @@ constexpr uint32_t kO = 256, kUMain = 320;    // out; U's three terms
 struct TcParams {
     LaParams p;
     int nvb;
+    unsigned int launch;       // number of the launch, not 0
     unsigned int* host_err;
 };
 struct TcMaps {
@@ -120,21 +128,39 @@ __device__ __forceinline__ void sts32(uint32_t a, float v) {
 }
 __device__ __forceinline__ void bar_p() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 // mbar_wait (the same bounds) in as few instructions as it takes: the roles' loops
-// share the instruction cache, and there are two dozen waits in them.
-__device__ __forceinline__ void wait_on(uint32_t bar, uint32_t parity, unsigned int* err) {
+// share the instruction cache, and there are two dozen waits in them.  A thread whose
+// wait gave up is gone: it waits for nothing more, walks its item to the end, whatever
+// that computes, and leaves.  (Leaving after a chunk took a vote in every chunk of every
+// role: the long prompt in 294 us instead of 278.)
+struct Watch {
+    unsigned int launch;
+    uint32_t slow;   // cycles after which a wait looks at the launch's error word; 0: gone
+    __device__ __forceinline__ bool gone() const { return slow == 0u; }
+};
+__device__ __forceinline__ void wait_on(uint32_t bar, uint32_t parity, Watch& w) {
     if (mbar_try_wait(bar, parity)) return;
     const uint32_t t0 = (uint32_t)clock();
 #pragma unroll 1
     while (!mbar_try_wait(bar, parity)) {
         const uint32_t dt = (uint32_t)clock() - t0;
-        if (dt > (uint32_t)kWaitSlowCycles) {
-            volatile unsigned int* e = err;
-            if (*e != 0u || dt > (uint32_t)kWaitLimitCycles) {
-                *e = 1u;
+        if (dt > w.slow) {
+            volatile unsigned int* e = &g_la_error;
+            if (*e == w.launch || dt > (uint32_t)kWaitLimitCycles) {
+                *e = w.launch;
+                w.slow = 0u;
                 return;
             }
         }
     }
+}
+// Whether `v` holds for any of a named barrier's threads, which wait for one another:
+// the warps of a role that uses one leave together.
+template <int kId, int kThr>
+__device__ __forceinline__ bool any_of(bool v) {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, %2, %3, p;\n\t"
+                 "selp.u32 %0, 1, 0, q;\n\t}" : "=r"(r) : "r"((uint32_t)v), "n"(kId), "n"(kThr) : "memory");
+    return r != 0u;
 }
 
 // After a wait that gave up: time for the copies and products in flight to end
@@ -353,7 +379,7 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
     extern __shared__ __align__(1024) uint8_t smem[];
     if ((smem_u32(smem) & 1023u) != 0u) {
         if (threadIdx.x == 0) {
-            atomicOr(&g_la_error, 1u);
+            g_la_error = tp.launch;
             report_timeout_to_host(&g_la_error, tp.host_err);
         }
         return;
@@ -420,7 +446,7 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, *holder, 0);
-    unsigned int* err = &g_la_error;
+    Watch err = {tp.launch, (uint32_t)kWaitSlowCycles};
     const LaGeom& g = tp.p.g;
     // every role walks the same items and counts chunks in c: barrier phases
     // follow from the count alone
@@ -437,12 +463,16 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(b_ifree + slot));
         ++k_item;
-        return im.nch >= 0;
+        return im.nch >= 0 && !__any_sync(0xffffffffu, err.gone());
     };
     Item im;
 
     if (warp == kTmaWarp) {
-        decode_item<kAgg, kSplit>(tp, blockIdx.x, items);
+        const volatile unsigned int* failed = &g_la_error;
+        const unsigned int failed0 = *failed, held = *const_cast<const volatile unsigned int*>(&g_la_withhold);
+        if (failed0 != tp.launch) decode_item<kAgg, kSplit>(tp, blockIdx.x, items);
+        else if (lane == 0) items[0].nch = -1;
+        __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(b_iready));
 #pragma unroll 1
         for (;; ++k_item) {
@@ -450,6 +480,8 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
             const uint4 q0 = lds128(at), q1 = lds128(at + 16);
             const int t0 = uniform(q0.z), nch = uniform(q1.w), h = uniform(q1.y), v0 = uniform(q1.z);
             if (nch < 0) break;
+            const int loads = held ? 0 : nch;
+            const unsigned int failed1 = *failed;
             const int jn = uniform(q1.x);
             const LaJob& jb = tp.p.job[jn];
             const CUtensorMap* m = maps.m[jn];
@@ -465,22 +497,24 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                     // C tiles are three deep and go one chunk ahead of A and B: their
                     // scaled terms take the longest to prepare
 #pragma unroll 1
-                    for (int x = part == 0 ? -1 : 1; x < (part == 0 ? min(nch, 1) : nch); ++x) {
+                    for (int x = part == 0 ? -1 : 1; x < (part == 0 ? min(loads, 1) : loads); ++x) {
                         const int cc = c + x, s = kSt == 2 ? cc & 1 : cc % kSt;
                         if (x >= 0) {
                             const int t = t0 + (rev ? nch - 1 - x : x) * kC;
                             const uint32_t st = smem_u32(smem) + s * kStage, fab = smem_u32(b_fab + s);
                             wait_on(smem_u32(b_eab + s), ((cc / kSt) & 1) ^ 1, err);
+                            if (err.gone()) break;
                             mbar_arrive_expect_tx(fab, (kAgg ? 1 : 2) * ka * kAtom);
                             for (int a = 0; a < ka; ++a) {
                                 if (!kAgg) tma_load_3d(st + a * kAtom, m + 0, fab, a * 64, ha, t);
                                 tma_load_3d(st + kB + a * kAtom, m + 1, fab, a * 64, hb, t);
                             }
                         }
-                        if (x + 1 < nch) {
+                        if (x + 1 < loads) {
                             const int t = t0 + (rev ? nch - 2 - x : x + 1) * kC, c1 = cc + 1, s3 = c1 % kCs;
                             const uint32_t fc = smem_u32(b_fc) + 8 * s3;
                             wait_on(smem_u32(b_ec) + 8 * s3, ((c1 / kCs) & 1) ^ 1, err);
+                            if (err.gone()) break;
                             mbar_arrive_expect_tx(fc, kAtom);
                             tma_load_3d(smem_u32(ctile) + s3 * kAtom, m + 2, fc, v0, hc, t);
                         }
@@ -493,12 +527,14 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                     const int it = uniform(granted_item(answer));
                     fence_proxy_async_smem();
                     wait_on(smem_u32(b_ifree + slot), (((k_item + 1) >> 1) & 1) ^ 1, err);
-                    if (it >= 0) decode_item<kAgg, kSplit>(tp, it, items + slot);
+                    if (__any_sync(0xffffffffu, err.gone())) break;
+                    if (it >= 0 && failed1 != tp.launch) decode_item<kAgg, kSplit>(tp, it, items + slot);
                     else if (lane == 0) items[slot].nch = -1;
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_u32(b_iready + slot));
                 }
             }
+            if (__any_sync(0xffffffffu, err.gone())) break;
             c += nch;
         }
     } else if (warp == kMmaWarp) {
@@ -608,9 +644,11 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                         }
                     }
                     if (w_due) w_product();
+                    if (err.gone()) break;
                 }
             }
             __syncwarp();
+            if (__any_sync(0xffffffffu, err.gone())) break;
             ahead = __any_sync(0xffffffffu, ahead);
             c += nch;
         }
@@ -619,11 +657,12 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
         const int quad = warp & 3, row = quad * 32 + lane;
         const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
 #pragma unroll 1
-        while (read_item(im)) {
+        for (;;) {
+            const bool item = read_item(im);
+            if (any_of<1, 256>(!item)) break;   // and the table's last readers are done
             if (im.nch == 0) continue;
             const LaJob& jb = tp.p.job[im.job];
             const float a2 = im.a2;
-            bar_p();                        // the table's last readers are done
             // s_in lam^j for j < 32 and, from there on, s_in lam^{31-j}
             if (warp < 2) sts32(ptab + 4 * row, exp2f(a2 * (float)(row < 32 ? row : 63 - row)) * jb.s_in);
             bar_p();
@@ -849,7 +888,9 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
         const int i = (warp - 24) * 32 + lane;
         const uint32_t lane_off = (uint32_t)((warp - 24) * 32) << 16;
 #pragma unroll 1
-        while (read_item(im)) {
+        for (;;) {
+            const bool item = read_item(im);
+            if (any_of<2, 128>(!item)) break;
             const LaJob& jb = tp.p.job[im.job];
             const int nv = min(kLaCols, jb.DV - im.v0);
             const bool f32o = kPart && jb.out_f32;
@@ -991,8 +1032,8 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
     __syncthreads();
     if (warp == kMmaWarp) {
         if (lane == 0) {
-            if (*reinterpret_cast<volatile unsigned int*>(err) != 0u) settle();
-            report_timeout_to_host(err, tp.host_err);
+            if (*const_cast<const volatile unsigned int*>(&g_la_error) == tp.launch) settle();
+            report_timeout_to_host(&g_la_error, tp.host_err);
         }
         __syncwarp();
         tc_fence_after();
@@ -1031,6 +1072,8 @@ cudaError_t launch_linattn_tc(const LaParams& p, int mode, cudaStream_t stream) 
     }
     const int64_t items = (int64_t)p.g.range_cap * p.g.H * p.njobs * tp.nvb;
     if (items >= (1LL << 31)) return cudaErrorInvalidValue;
+    static std::atomic<unsigned int> launches{0};
+    do tp.launch = ++launches; while (tp.launch == 0u);
     tp.host_err = host_timeout_word();
     auto k = mode ? linattn_tc<true, false, true>
            : p.g.split ? (part ? linattn_tc<false, true, true> : linattn_tc<false, false, true>)
@@ -1040,6 +1083,10 @@ cudaError_t launch_linattn_tc(const LaParams& p, int mode, cudaStream_t stream) 
     if (e != cudaSuccess) return e;
     k<<<(unsigned)items, kThreads, smem, stream>>>(tp, maps);
     return cudaGetLastError();
+}
+
+cudaError_t set_linattn_withhold(unsigned int on) {
+    return cudaMemcpyToSymbol(g_la_withhold, &on, sizeof(on));
 }
 
 unsigned int take_linattn_error() {

@@ -140,7 +140,8 @@ int ssd_abi_version(void) { return SSD_ABI_VERSION; }
 unsigned int ssd_take_device_errors(void) { return take_errors(); }
 
 ssd_status ssd_debug_withhold_handoffs(int on) {
-    return from_cuda(set_fwd_pass_state_withhold(on ? 1u : 0u));
+    const cudaError_t e = set_fwd_pass_state_withhold(on ? 1u : 0u);
+    return from_cuda(e != cudaSuccess ? e : set_linattn_withhold(on ? 1u : 0u));
 }
 
 const char* ssd_status_string(ssd_status s) {

@@ -127,6 +127,8 @@ unsigned int take_fwd_pass_state_error();
 cudaError_t set_fwd_pass_state_withhold(unsigned int on);
 unsigned int take_compute_out_error();
 unsigned int take_linattn_error();
+// Likewise: nonzero makes linear attention's tensor-core kernel withhold its loads.
+cudaError_t set_linattn_withhold(unsigned int on);
 
 // Launch kern on stream, with programmatic dependent launch when pdl is set
 // (the kernel then waits on the previous grid with griddepcontrol.wait before
