@@ -72,6 +72,18 @@ struct Acc {
             v[x][1] = fma2(a2, b1, v[x][1]);
         }
     }
+    // rows from or up to the y-th alone: what is not added may be an infinity or a NaN
+    __device__ __forceinline__ void fma_part(const float4& a, const float4& b, int y, bool up_to) {
+        const float av[4] = {a.x, a.y, a.z, a.w};
+        const f32x2 b0 = pair(b.x, b.y), b1 = pair(b.z, b.w);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            if (up_to ? x > y : x < y) continue;
+            const f32x2 a2 = pair(av[x], av[x]);
+            v[x][0] = fma2(a2, b0, v[x][0]);
+            v[x][1] = fma2(a2, b1, v[x][1]);
+        }
+    }
     __device__ __forceinline__ void row(int x, float (&f)[4]) const {
         unpair(v[x][0], f[0], f[1]);
         unpair(v[x][1], f[2], f[3]);
@@ -203,9 +215,20 @@ __global__ void __launch_bounds__(kThreads, 2) linattn_simt(const __grid_constan
             for (int k = 0; k < jb.DK; ++k)
                 o1.fma(ld4(s.At + k * kPitch + ty * 4), ld4(s.X + k * kPitch + tx * 4));
             __syncthreads();
+            // the rows of C that a row of out may see, and no others: 0 times an infinity
+            // or a NaN of a later token would be one
+            if (!jb.rev)
 #pragma unroll 4
-            for (int j = 0; j < kC; ++j)
-                o2.fma(ld4(s.Pt + j * kPitch + ty * 4), ld4(s.Cv + j * kPitch + tx * 4));
+                for (int j = 0; j < ty * 4; ++j)
+                    o2.fma(ld4(s.Pt + j * kPitch + ty * 4), ld4(s.Cv + j * kPitch + tx * 4));
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+                o2.fma_part(ld4(s.Pt + (ty * 4 + y) * kPitch + ty * 4), ld4(s.Cv + (ty * 4 + y) * kPitch + tx * 4), y,
+                            jb.rev != 0);
+            if (jb.rev)
+#pragma unroll 4
+                for (int j = ty * 4 + 4; j < kC; ++j)
+                    o2.fma(ld4(s.Pt + j * kPitch + ty * 4), ld4(s.Cv + j * kPitch + tx * 4));
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
                 const int i = ty * 4 + x;

@@ -88,7 +88,7 @@ template <bool kAgg> struct Cfg {
     static constexpr int kUb = kAgg ? 2 : 1;
     static constexpr int kB = kAgg ? 0 : 2 * kAtom;      // a stage: A (2 atoms), B (2)
     static constexpr int kStage = kB + 2 * kAtom;
-    static constexpr int kSmem = kSt * kStage + kCs * kAtom + kTb * kTerms * kTerm + (kAgg ? 0 : kAtom) + 1024;
+    static constexpr int kSmem = kSt * kStage + kCs * kAtom + kTb * kTerms * kTerm + (kAgg ? 0 : kAtom + 1024) + 1024;
     static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
 };
 // tensor memory columns
@@ -221,6 +221,42 @@ __device__ __noinline__ void few_p(uint32_t base, int row, int n, float a2, floa
         __syncwarp();
         tmem_st_x4(base + j0 / 2, hi);
         tmem_st_x4(base + j0 / 2 + 64, lo);
+    }
+    tmem_wait_st();
+}
+// Infinities and NaN in C.  The products above P's diagonal are 0 times C's later rows, and
+// would hand such a value to the rows before it.  It is taken out of the C tile, and the
+// first row (counted in the walk's direction) that had one is kept for each column: from
+// there on the column's results become NaN.  U, and with it the state, takes the value.
+struct Spoilt {
+    uint32_t first, any;   // of a C tile: int [64], and whether there is one
+};
+__device__ __forceinline__ bool spoils(uint32_t v) { return (v & 0x7F80u) == 0x7F80u; }   // a bf16
+__device__ __noinline__ void take_out(uint32_t row_at, int row, int ch0, int place, Spoilt sp) {
+#pragma unroll 1
+    for (int v = ch0 * 8; v < ch0 * 8 + 32; ++v) {
+        const uint32_t at = row_at + (((v >> 3) ^ (row & 7)) << 4) + 2 * (v & 7);
+        uint16_t x;
+        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(at) : "memory");
+        if (spoils(x)) {
+            asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"((uint16_t)0) : "memory");
+            asm volatile("red.shared.min.s32 [%0], %1;" ::"r"(sp.first + 4 * v), "r"(place) : "memory");
+        }
+    }
+    asm volatile("st.shared.u32 [%0], %1;" ::"r"(sp.any), "r"(1) : "memory");
+}
+// The out role's part, on the accumulator of a row; one warp.
+__device__ __noinline__ void spoil(uint32_t acc, int place, Spoilt sp) {
+#pragma unroll 1
+    for (int v = 0; v < 64; v += 8) {
+        uint32_t p[8];
+        __syncwarp();
+        tmem_ld_x8(acc + v, p);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (place >= __float_as_int(lds32(sp.first + 4 * (v + e)))) p[e] = 0x7FFFFFFFu;
+        tmem_st_x8(acc + v, p);
     }
     tmem_wait_st();
 }
@@ -412,6 +448,8 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
     const uint32_t answer = smem_u32(bars + 36);    // 16 bytes
     Item* items = reinterpret_cast<Item*>(bars + 38);   // [2]
     const uint32_t ptab = smem_u32(bars + 54);      // [128] fp32: column factors of P
+    // of C tile s: the rows from which its columns are spoilt, and whether any is
+    const auto spoilt = [&](int s) { return Spoilt{smem_u32(bars + 128) + 256 * s, smem_u32(bars + 128) + 768 + 4 * s}; };
 
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
@@ -441,6 +479,7 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
         mbar_init(smem_u32(b_ofree), 128);
         fence_mbar_init();
     }
+    if (!kAgg && threadIdx.x < 195) reinterpret_cast<int*>(bars + 128)[threadIdx.x] = threadIdx.x < 192 ? kC : 0;
     if (warp == kMmaWarp) tmem_alloc(smem_u32(holder), 512);
     tc_fence_before();
     __syncthreads();
@@ -756,11 +795,16 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                 const uint32_t ct = smem_u32(ctile) + (c % kCs) * kAtom;
                 // the terms of this thread's 32 columns are ready in registers when the
                 // last U lets go of their tiles; a row of other tokens gives zeros
-                uint32_t t[4][kTerms][4];
+                uint32_t t[4][kTerms][4], most = 0u;
 #pragma unroll
                 for (int ch = 0; ch < 4; ++ch) {
                     const uint4 q = lds128(ct + row * kRow + (((ch0 + ch) ^ (row & 7)) << 4));
                     const uint32_t in[4] = {q.x, q.y, q.z, q.w};
+                    if (!kAgg) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)   // the largest magnitudes, a NaN above all
+                            asm("max.NaN.xorsign.abs.bf16x2 %0, %0, %1;" : "+r"(most) : "r"(in[e]));
+                    }
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         // 24 bits as three times 8, cut off rather than rounded: the
@@ -776,6 +820,8 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                         }
                     }
                 }
+                if (!kAgg && (spoils(most) || spoils(most >> 16)) && row < n)
+                    take_out(ct + row * kRow, row, ch0, jb.rev ? kC - 1 - row : row, spoilt(c % kCs));
                 if (n < kC) {
                     wait_on(smem_u32(b_fab + s), (c / kSt) & 1, err);
                     if (row >= n) {   // nothing of such a row may reach a product
@@ -934,6 +980,8 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                 mbar_arrive(smem_u32(b_scaled));
                 wait_on(smem_u32(b_odone), c & 1, err);
                 tc_fence_after();
+                const Spoilt sp = spoilt(c % kCs);
+                if (__float_as_int(lds32(sp.any)) != 0) spoil(tmem + lane_off + kO, jb.rev ? kC - 1 - i : i, sp);
                 // A full chunk's bf16 rows go out by TMA from the chunk's C tile, which
                 // nothing reads any more: stored from registers, a row to a thread, they
                 // took a fifth of the shared-memory and L1 data path that bounds the
@@ -1020,6 +1068,10 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                             bulk_commit_group();
                             bulk_wait_group_read0();
                         }
+                    }
+                    if (__float_as_int(lds32(sp.any)) != 0) {   // the tile's next chunk starts anew
+                        for (int v = 0; v < 64; ++v) sts32(sp.first + 4 * v, __int_as_float(kC));
+                        sts32(sp.any, __int_as_float(0));
                     }
                     mbar_arrive(smem_u32(b_ec) + 8 * (c % kCs));
                 }

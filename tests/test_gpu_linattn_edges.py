@@ -120,3 +120,50 @@ def test_range_of_fp32(dtype, power):
     near(run(dout=s, dfin=s), (1, 1, s, s, s, s))
     near(run(q=h, k=h, S0=h, dfin=h), (h * h, h, h, h, h * h, h))
     near(run(v=h, dout=h, S0=h, dfin=h), (h, h, h * h, h * h, h, h))
+
+
+# which rows of each output depend on token t's row of each input: those from t on, up to
+# t, t's alone, or none
+SEEN = {"q": dict(o="only", dq=None, dk="upto", dv="upto"), "k": dict(o="from", dq="from", dk=None, dv="only"),
+        "v": dict(o="from", dq="from", dk="only", dv=None), "dout": dict(o=None, dq="only", dk="upto", dv="upto")}
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("length,token", [(400, 0), (400, 5), (400, 63), (400, 64), (400, 127), (400, 128), (400, 333),
+                                          (400, 399), (40, 17), (2600, 1500), (1, 0)])
+def test_a_token_reaches_no_row_that_does_not_see_it(dtype, length, token):
+    """An infinity or a NaN in one token's row: the rows that depend on it are not finite,
+    all others have the bits they had without it."""
+    x = make(dtype, [length], 2, 2, 32, 80, True, seed=21, decay=[-0.05, -0.4])
+    kw = lambda d: dict(cu_seqlens=d["cu"], init_state=d["S0"])
+
+    def run(d):
+        o, fin = ssd.linattn_fwd(d["q"], d["k"], d["v"], d["a"], **kw(d))
+        dq, dk, dv, d0 = ssd.linattn_bwd(d["q"], d["k"], d["v"], d["dout"], d["a"], dfinal_state=d["dfin"], **kw(d))
+        sync_ok()
+        return dict(o=o, dq=dq, dk=dk, dv=dv), fin, d0
+
+    clean, fin0, d00 = run(dev(x))
+    rows = torch.arange(length, device="cuda")
+    for name, sees in SEEN.items():
+        for value, column in ((float("inf"), slice(None)), (float("nan"), 7)):
+            d = dev(x)
+            d[name][token, 0, column] = value
+            got, fin, d0 = run(d)
+            for out, how in sees.items():
+                hit = {"from": rows >= token, "upto": rows <= token, "only": rows == token, None: rows < 0}[how]
+                g, c = got[out][:, 0], clean[out][:, 0]
+                assert torch.equal(g[~hit], c[~hit]), (name, out)
+                assert torch.equal(got[out][:, 1], clean[out][:, 1]), (name, out)
+                # v and dout share their columns with o and dv, and k and q with dq and dk:
+                # there the other columns are as they were
+                same = column != slice(None) and (name, out) in (("v", "o"), ("k", "dq"), ("q", "dk"), ("dout", "dv"))
+                if same:
+                    rest = [i for i in range(g.shape[1]) if i != column]
+                    assert torch.equal(g[:, rest], c[:, rest]), (name, out)
+                    assert not torch.isfinite(g[hit][:, column]).any(), (name, out)
+                else:
+                    assert not torch.isfinite(g[hit]).any(), (name, out)
+            # the states: the final one sees k and v, the initial one's gradient q and dout
+            assert torch.equal(fin, fin0) == (name in ("q", "dout"))
+            assert torch.equal(d0, d00) == (name in ("k", "v"))
