@@ -798,7 +798,8 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                 uint32_t t[4][kTerms][4], most = 0u;
 #pragma unroll
                 for (int ch = 0; ch < 4; ++ch) {
-                    const uint4 q = lds128(ct + row * kRow + (((ch0 + ch) ^ (row & 7)) << 4));
+                    uint4 q = lds128(ct + row * kRow + (((ch0 + ch) ^ (row & 7)) << 4));
+                    if (row >= n) q = make_uint4(0u, 0u, 0u, 0u);   // a row of other tokens
                     const uint32_t in[4] = {q.x, q.y, q.z, q.w};
                     if (!kAgg) {
 #pragma unroll
@@ -809,7 +810,7 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                     for (int e = 0; e < 4; ++e) {
                         // 24 bits as three times 8, cut off rather than rounded: the
                         // three add up to the product exactly
-                        f32x2 r = row < n ? mul2(pair(lo16(in[e]), hi16(in[e])), w2) : 0ull;
+                        f32x2 r = mul2(pair(lo16(in[e]), hi16(in[e])), w2);
 #pragma unroll
                         for (int y = 0; y < kTerms; ++y) {
                             float a, b;
@@ -820,7 +821,7 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                         }
                     }
                 }
-                if (!kAgg && (spoils(most) || spoils(most >> 16)) && row < n)
+                if (!kAgg && (spoils(most) || spoils(most >> 16)))
                     take_out(ct + row * kRow, row, ch0, jb.rev ? kC - 1 - row : row, spoilt(c % kCs));
                 if (n < kC) {
                     wait_on(smem_u32(b_fab + s), (c / kSt) & 1, err);
