@@ -167,3 +167,54 @@ def test_a_token_reaches_no_row_that_does_not_see_it(dtype, length, token):
             # the states: the final one sees k and v, the initial one's gradient q and dout
             assert torch.equal(fin, fin0) == (name in ("q", "dout"))
             assert torch.equal(d0, d00) == (name in ("k", "v"))
+
+
+def bf16_rounding(want):
+    """2-norm of what one rounding to bf16 adds to a result, over the result's."""
+    return off(num(torch.from_numpy(want).bfloat16()), want)
+
+
+@pytest.mark.parametrize("lens,H,G,K,V", [([1000, 300], 4, 4, 128, 128), ([700], 6, 2, 96, 80), ([3000], 2, 1, 64, 64)])
+def test_bf16_has_one_rounding_more_than_its_own(lens, H, G, K, V):
+    """Each term of an output has one operand rounded to bf16 (a weight, or the state), so
+    that the terms' independent errors add up to what one rounding of the output makes;
+    with the output's own, sqrt(2) of that.  A tenth more for the spread of a sample."""
+    x = make("bf16", lens, H, G, K, V, True, seed=22)
+    d = dev(x)
+    kw = dict(cu_seqlens=d["cu"], init_state=d["S0"])
+    o, _ = ssd.linattn_fwd(d["q"], d["k"], d["v"], d["a"], **kw)
+    g = ssd.linattn_bwd(d["q"], d["k"], d["v"], d["dout"], d["a"], dfinal_state=d["dfin"], **kw)
+    sync_ok()
+    want = ref(x, lens, K ** -0.5, grads=True)
+    for t, w in ((o, want[0]), *zip(g[:3], want[2:5])):
+        assert off(num(t), w) < 1.1 * 2 ** 0.5 * bf16_rounding(w)
+
+
+def test_calls_in_a_graph():
+    """Every call can be captured: a replay gives the bits of a call."""
+    x = dev(make("bf16", [700, 90], 4, 2, 64, 64, True, seed=23))
+    s = dev(make("bf16", [1, 1], 4, 2, 64, 64, True, seed=24))
+    r, w = torch.randn(790, 256, device="cuda"), torch.ones(256, device="cuda")
+    kw = dict(cu_seqlens=x["cu"], init_state=x["S0"])
+
+    def calls(cache):
+        o, fin = ssd.linattn_fwd(x["q"], x["k"], x["v"], x["a"], **kw)
+        g = ssd.linattn_bwd(x["q"], x["k"], x["v"], x["dout"], x["a"], dfinal_state=x["dfin"], **kw)
+        y = ssd.linattn_step(s["q"], s["k"], s["v"], s["a"], cache)
+        ro, n, rstd = ssd.block_norm_fwd(r, o.reshape(790, 256), w, ngroups=4, return_rstd=True)
+        gn = ssd.block_norm_bwd(r, o.reshape(790, 256), w, ro, n, rstd, ngroups=4)
+        return [o, fin, *g, y, ro, n, gn["dr"], gn["dy"], gn["dw_pre"]]
+
+    calls(s["S0"].clone())
+    eager_cache, cache = s["S0"].clone(), s["S0"].clone()
+    want = calls(eager_cache)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = calls(cache)
+    for t in got:
+        t.zero_()
+    graph.replay()
+    sync_ok()
+    assert torch.equal(cache, eager_cache)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
