@@ -299,7 +299,8 @@ ssd_status ssd_gdn_chunk_fwd_o(const ssd_gdn_dims* d, const float* q, const floa
  *   kdim, vdim    16 .. 128, multiples of 16.  Strides: multiples of 16 bytes.
  *   max_seqlen    no sequence is longer, or 0 if the caller does not know; it
  *     only guides how the work is cut, a longer sequence is still right.
- *   nheads <= 4096, nseqs <= 2^20, tokens <= 2^30. */
+ *   nheads <= 4096, nseqs <= 2^20, tokens <= 2^30; for bf16 prompts and gradients,
+ *     nseqs * nheads < 2^28 (a little more is SSD_ERR_SHAPE or served). */
 typedef struct {
     int64_t nseqs, tokens, nheads, ngroups, kdim, vdim;
     int64_t q_stride, k_stride, v_stride;

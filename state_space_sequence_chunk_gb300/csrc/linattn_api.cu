@@ -96,6 +96,17 @@ ssd_status make_la(const ssd_linattn_dims* d, bool packed, bool backward, La* p)
     return SSD_OK;
 }
 
+// make_la for a whole prompt or its gradient, whose launch has a CTA for each range, head,
+// job and 64 columns: their number has to fit a grid (in bf16, where all are in one
+// dimension of it).
+ssd_status make_prompt(const ssd_linattn_dims* d, bool packed, bool backward, La* p) {
+    const ssd_status s = make_la(d, packed, backward, p);
+    if (s != SSD_OK || d->dtype != SSD_BF16) return s;
+    const int64_t cols = backward && p->K > p->V ? p->K : p->V;
+    const int64_t items = p->g.range_cap * p->H * (backward ? 3 : 1) * ((cols + kLaCols - 1) / kLaCols);
+    return items < (1LL << 31) ? SSD_OK : SSD_ERR_SHAPE;
+}
+
 size_t part_bytes(const La& p) {   // per-head dq and dk, before the sum over a group
     return p.hpg > 1 ? 2 * round_up256((size_t)(p.T * p.H * p.K) * 4) : 0;
 }
@@ -129,7 +140,7 @@ size_t ssd_linattn_workspace_bytes(const ssd_linattn_dims* d, int backward) {
     size_t need = 0;
     for (int packed = 0; packed < 2; ++packed) {
         La p;
-        if (make_la(d, packed != 0, backward != 0, &p) != SSD_OK) continue;
+        if (make_prompt(d, packed != 0, backward != 0, &p) != SSD_OK) continue;
         const size_t b = backward ? 3 * p.agg_bytes + part_bytes(p) : p.agg_bytes;
         if (b > need) need = b;
     }
@@ -141,7 +152,7 @@ ssd_status ssd_linattn_fwd(const ssd_linattn_dims* d, const void* q, const void*
                            const float* init_state, void* o, float* final_state, void* workspace,
                            size_t workspace_bytes, void* stream) {
     La p;
-    ssd_status s = make_la(d, cu_seqlens != nullptr, false, &p);
+    ssd_status s = make_prompt(d, cu_seqlens != nullptr, false, &p);
     if (s != SSD_OK) return s;
     if (p.n == 0 && p.T == 0) return SSD_OK;
     if (!isfinite(scale)) return SSD_ERR_SHAPE;
@@ -184,7 +195,7 @@ ssd_status ssd_linattn_bwd(const ssd_linattn_dims* d, const void* q, const void*
                            float* dinit_state, void* workspace, size_t workspace_bytes,
                            void* stream) {
     La p;
-    ssd_status s = make_la(d, cu_seqlens != nullptr, true, &p);
+    ssd_status s = make_prompt(d, cu_seqlens != nullptr, true, &p);
     if (s != SSD_OK) return s;
     if (p.n == 0 && p.T == 0) return SSD_OK;
     if (!isfinite(scale)) return SSD_ERR_SHAPE;

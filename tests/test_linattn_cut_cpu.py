@@ -55,3 +55,22 @@ def test_ranges_of_a_batch_that_may_hold_one_long_sequence(lib):
     part = 2 * 4001 * 4 * 64 * 4
     assert need(lib, 8, 4001, 4, 2, 64, 128, backward=1, max_seqlen=1527) == part
     assert need(lib, 8, 4001, 4, 2, 64, 128, backward=1, max_seqlen=1528) == 3 * slots(4001, 512) * state + part
+
+
+@pytest.mark.parametrize("backward", [0, 1])
+def test_more_work_than_a_grid_holds_is_refused_as_sizes(lib, backward):
+    """2^20 sequences of 2 rows in bf16: up to 2^28 chains are served, more than a grid
+    has CTAs for are refused before anything is enqueued; fp32 has a grid of its own."""
+    ptrs = [ctypes.c_void_p(0x10000000000000 * (i + 1)) for i in range(13)]
+    big, one = ctypes.c_size_t(1 << 62), ctypes.c_float(1.0)
+
+    def call(H, dtype):
+        d = ctypes.byref(ssd.LinattnDims(1 << 20, 1 << 21, H, H, 16, 128, 0, 0, 0, 2, dtype, 0))
+        if backward:
+            return lib.ssd_linattn_bwd(d, *ptrs[:5], one, *ptrs[5:13], big, None)
+        return lib.ssd_linattn_fwd(d, *ptrs[:4], one, *ptrs[4:9], big, None)
+
+    assert call(4096, ssd.SSD_BF16) == 2 and call(1024 if not backward else 512, ssd.SSD_BF16) == 2
+    if not torch.cuda.is_available():      # past validation there is no device to launch on
+        assert call(255, ssd.SSD_BF16) in (6, 7)
+        assert call(4096, ssd.SSD_F32) in (6, 7)
