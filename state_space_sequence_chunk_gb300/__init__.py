@@ -18,6 +18,10 @@ Entry points (same names as the C ABI):
   attention with a decay for each head: prompts, their gradient, single tokens.
 * :func:`block_norm_fwd`, :func:`block_norm_bwd` -- the norms before and after a
   block with its gate and residual scale, and their gradient.
+
+None of these is recorded by autograd: what they return is cut from the graph, also of
+inputs that require a gradient.  A training step calls the ``_bwd`` functions, from an
+``autograd.Function`` for instance (``examples/linear_attention_block.py`` has one for each pair).
 """
 from __future__ import annotations
 

@@ -4,16 +4,6 @@
 namespace ssd {
 namespace {
 
-int sm_count() {
-    int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-        cudaGetLastError();
-        return 152;
-    }
-    return sms;
-}
-
 ssd_status make_norm(const ssd_norm_dims* d, NormParams* p) {
     if (!d) return SSD_ERR_NULL;
     if ((d->dtype != SSD_F32 && d->dtype != SSD_BF16) || (d->rdtype != SSD_F32 && d->rdtype != SSD_BF16))
@@ -40,10 +30,6 @@ ssd_status make_norm(const ssd_norm_dims* d, NormParams* p) {
     q.eps = d->eps;
     *p = q;
     return SSD_OK;
-}
-
-size_t span(int64_t T, int64_t stride, int64_t w, int es) {
-    return T > 0 ? (size_t)((T - 1) * stride + w) * es : 0;
 }
 
 }  // namespace

@@ -14,18 +14,6 @@ struct La {
     size_t agg_bytes;    // one job's range states
 };
 
-int sm_count() {
-    // without a device (validation on a host that has none) the cut is made for
-    // this GPU's number of SMs
-    int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-        cudaGetLastError();
-        return 152;
-    }
-    return sms;
-}
-
 ssd_status make_la(const ssd_linattn_dims* d, bool packed, bool backward, La* p) {
     if (!d) return SSD_ERR_NULL;
     if (d->dtype != SSD_F32 && d->dtype != SSD_BF16) return SSD_ERR_DTYPE;
@@ -109,10 +97,6 @@ ssd_status make_prompt(const ssd_linattn_dims* d, bool packed, bool backward, La
 
 size_t part_bytes(const La& p) {   // per-head dq and dk, before the sum over a group
     return p.hpg > 1 ? 2 * round_up256((size_t)(p.T * p.H * p.K) * 4) : 0;
-}
-// bytes from the first to one past the last element of a strided [T, w] operand
-size_t span(int64_t T, int64_t stride, int64_t w, int es) {
-    return T > 0 ? (size_t)((T - 1) * stride + w) * es : 0;
 }
 
 cudaError_t run_jobs(LaParams& p, int dtype, cudaStream_t st) {

@@ -168,6 +168,21 @@ inline ssd_status from_cuda(cudaError_t e) {
     cudaGetLastError();
     return SSD_ERR_CUDA;
 }
+// Bytes from the first to one past the last element of a strided [T, w] operand.
+inline size_t span(int64_t T, int64_t stride, int64_t w, int es) {
+    return T > 0 ? (size_t)((T - 1) * stride + w) * es : 0;
+}
+// SMs of the current device; without one (validation on a host that has none), those of
+// the GPU that this is built for.
+inline int sm_count() {
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+        cudaGetLastError();
+        return 152;
+    }
+    return sms;
+}
 // Checks made after the arguments are validated and before anything is
 // enqueued: the device's compute capability, then whether a bounded wait in
 // an earlier launch on this device has given up (reported once, as
