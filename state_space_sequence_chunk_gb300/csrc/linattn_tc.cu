@@ -188,8 +188,6 @@ __device__ __forceinline__ bool first_of(uint32_t a, uint32_t a_parity, uint32_t
     return false;
 }
 
-__device__ __forceinline__ void ld_cols(uint32_t at, uint32_t (&r)[4]) { tmem_ld_x4(at, r); }
-__device__ __forceinline__ void ld_cols(uint32_t at, uint32_t (&r)[8]) { tmem_ld_x8(at, r); }
 // A chunk of so few tokens leaves the second half of P's contraction free: it holds
 // P's second terms there (and P is then good to 16 bits), for tokens whose output is
 // a sum of a few products, or of one.
@@ -333,7 +331,7 @@ __device__ __forceinline__ LaRange longest(const LaGeom& g, int idx) {
     return r;
 }
 
-template <bool kAgg, bool kSplit>
+template <bool kAgg>
 __device__ __forceinline__ void decode_item(const TcParams& tp, int it, Item* slot) {
     Item r;
     const int vb = it % tp.nvb;
@@ -343,14 +341,14 @@ __device__ __forceinline__ void decode_item(const TcParams& tp, int it, Item* sl
     r.h = x % tp.p.g.H;
     r.ridx = x / tp.p.g.H;
     const float a = tp.p.g.a[r.h];
-    const LaRange rg = !kSplit && tp.p.g.nseq < 32 ? longest(tp.p.g, r.ridx) : la_find(tp.p.g, r.ridx);
+    const LaRange rg = !tp.p.g.split && tp.p.g.nseq < 32 ? longest(tp.p.g, r.ridx) : la_find(tp.p.g, r.ridx);
     r.seq = rg.seq;
     r.ridx = rg.slot;
     r.t0 = rg.t0;
     r.len = rg.len;
     r.v0 = vb * kLaCols;
     const LaJob& jb = tp.p.job[r.job];
-    r.cut = kSplit && !(rg.first && rg.last);
+    r.cut = tp.p.g.split && !(rg.first && rg.last);
     r.last = jb.rev ? rg.first : rg.last;
     const bool none = rg.seq < 0 || r.v0 >= jb.DV || (kAgg && (!r.cut || r.last || rg.seq == tp.p.g.nseq));
     r.nch = none || rg.seq == tp.p.g.nseq ? 0 : (rg.len + kC - 1) / kC;
@@ -404,10 +402,9 @@ __device__ __forceinline__ void mma_steps(uint32_t d, uint64_t a, uint64_t b, in
     }
 }
 
-// kPart: some job's outputs are fp32, for a sum over a group's heads.  kSplit: long
-// sequences are cut.  (Without what the others need the code is shorter, which every
-// call feels: with one instance for both, a cut prompt took 288 us instead of 278.)
-template <bool kAgg, bool kPart, bool kSplit>
+// kPart: some job's outputs are fp32, for a sum over a group's heads.  (Without what the
+// others need the code is shorter, which every call feels.)
+template <bool kAgg, bool kPart>
 __global__ void __launch_bounds__(kThreads, 1)
 linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps maps) {
     // aligned by declaration, not by arithmetic: its addresses are then constants
@@ -509,7 +506,7 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
     if (warp == kTmaWarp) {
         const volatile unsigned int* failed = &g_la_error;
         const unsigned int failed0 = *failed, held = *const_cast<const volatile unsigned int*>(&g_la_withhold);
-        if (failed0 != tp.launch) decode_item<kAgg, kSplit>(tp, blockIdx.x, items);
+        if (failed0 != tp.launch) decode_item<kAgg>(tp, blockIdx.x, items);
         else if (lane == 0) items[0].nch = -1;
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(b_iready));
@@ -567,7 +564,7 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                     fence_proxy_async_smem();
                     wait_on(smem_u32(b_ifree + slot), (((k_item + 1) >> 1) & 1) ^ 1, err);
                     if (__any_sync(0xffffffffu, err.gone())) break;
-                    if (it >= 0 && failed1 != tp.launch) decode_item<kAgg, kSplit>(tp, it, items + slot);
+                    if (it >= 0 && failed1 != tp.launch) decode_item<kAgg>(tp, it, items + slot);
                     else if (lane == 0) items[slot].nch = -1;
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_u32(b_iready + slot));
@@ -893,23 +890,19 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                 tc_fence_after();
                 const uint32_t ub = tmem + lane_off + kU + vc + (kUb == 2 ? (c & 1) * 64 * kTerms : 0);
                 const f32x2 hi2 = pair(hi, hi), lo2 = pair(lo, lo);
-                // a wait for each 4 columns of the three terms; the pass over ranges' sums
-                // has no other work to cover it and the registers for 8 (84 -> 79 us for
-                // 24 chains of 65536 tokens)
-                constexpr int kQ = kAgg ? 8 : 4;
 #pragma unroll
-                for (int q = 0; q < 32 / kQ; ++q) {
-                    uint32_t u0[kQ], u1[kQ], u2[kQ];
+                for (int q = 0; q < 8; ++q) {   // 4 columns of the three terms
+                    uint32_t u0[4], u1[4], u2[4];
                     __syncwarp();
-                    ld_cols(ub + q * kQ, u0);
-                    ld_cols(ub + 64 + q * kQ, u1);
-                    ld_cols(ub + 128 + q * kQ, u2);
+                    tmem_ld_x4(ub + q * 4, u0);
+                    tmem_ld_x4(ub + 64 + q * 4, u1);
+                    tmem_ld_x4(ub + 128 + q * 4, u2);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < kQ / 2; ++e) {
+                    for (int e = 0; e < 2; ++e) {
                         const f32x2 u = add2(pair(u0[2 * e], u0[2 * e + 1]),
                                              add2(pair(u1[2 * e], u1[2 * e + 1]), pair(u2[2 * e], u2[2 * e + 1])));
-                        f32x2& X2 = X[q * (kQ / 2) + e];
+                        f32x2& X2 = X[q * 2 + e];
                         X2 = fma2(X2, hi2, fma2(X2, lo2, u));
                     }
                 }
@@ -1128,9 +1121,8 @@ cudaError_t launch_linattn_tc(const LaParams& p, int mode, cudaStream_t stream) 
     static std::atomic<unsigned int> launches{0};
     do tp.launch = ++launches; while (tp.launch == 0u);
     tp.host_err = host_timeout_word();
-    auto k = mode ? linattn_tc<true, false, true>
-           : p.g.split ? (part ? linattn_tc<false, true, true> : linattn_tc<false, false, true>)
-                       : (part ? linattn_tc<false, true, false> : linattn_tc<false, false, false>);
+    auto k = mode ? linattn_tc<true, false>
+           : part ? linattn_tc<false, true> : linattn_tc<false, false>;
     const int smem = mode ? Cfg<true>::kSmem : Cfg<false>::kSmem;
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
