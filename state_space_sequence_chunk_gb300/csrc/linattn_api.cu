@@ -42,11 +42,16 @@ ssd_status make_la(const ssd_linattn_dims* d, bool packed, bool backward, La* p)
     g.L = packed || p->n == 0 ? 0 : (int)(p->T / p->n);
     g.a = nullptr;
     // A sequence is cut into ranges where a chain of its whole length would keep the
-    // other SMs waiting: if it is longer than what an SM gets when the work is spread
-    // evenly and longer by more than the cut costs, which reads two operands twice
-    // (another 0.4 of the share) and launches twice more (about 7 chunks' time).  One
-    // sequence of 4096 tokens, cut and whole: 36 and 79 us on 24 chains, 76 and 82 on
-    // 76; of 1280 on 150 chains, 69 and 31.
+    // other SMs waiting: where it is longer than what an SM gets when the work is spread
+    // evenly, by what the cut costs.  That is a second reading of two operands and, with
+    // all SMs at work, a slower chunk (together another 9/8 of the share in bf16, 2/5 in
+    // fp32, whose chunks are bound by arithmetic), and two launches (some 9 chunks' time
+    // in bf16, 1.4 in fp32).  One bf16 sequence, heads of 128 x 64, cut and whole: 2048
+    // tokens on 24 heads 35 and 37 us, on 38 42 and 38; 4096 on 38 59 and 66 to 71, on 50
+    // 68 to 74 and 67 to 72, on 76 107 and 77; 16384 on 64 195 to 227 and 244 to 257, on
+    // 76 330 and 260; gradients: 16384 on 8 161 to 213 and 254 to 318, on 24 390 to 515
+    // and 268 to 386.  fp32: 1024 on 76 210 and 260 to 275, on 100 283 to 300 and 260 to
+    // 275; 4096 on 100 955 to 985 and 1024 to 1058, on 128 1400 and 1050.
     const int64_t kb = (p->K + kLaCols - 1) / kLaCols, vb = (p->V + kLaCols - 1) / kLaCols;
     const int64_t cols = backward ? 2 * kb + vb : vb;
     const int64_t sms = sm_count(), share = p->T * p->H * cols / sms;
@@ -56,11 +61,12 @@ ssd_status make_la(const ssd_linattn_dims* d, bool packed, bool backward, La* p)
     int64_t R = (share / 2 + 127) / 128 * 128;
     if (R < least) R = least;
     // (without a sequence there is none to cut: every row's result is 0)
-    g.split = p->n > 0 && longest > R && longest > share + (d->dtype == SSD_F32 ? 0 : share / 2 + 896);
+    g.split = p->n > 0 && longest > R &&
+              longest > share + (d->dtype == SSD_F32 ? share * 2 / 5 + 176 : share * 9 / 8 + 1152);
     // Half a share, so that the range taken last adds at most half; where the lengths
     // are known, the number of ranges that fills the SMs in the shortest time (a range
     // costs 2 chunks more than its own): one sequence of 65536 tokens on 24 chains in
-    // 12.7 ranges of half a share left a third round of 8 items, 316 us instead of 303.
+    // 12.7 ranges of half a share left a third round of 8 items, 293 us instead of 279.
     if (g.split && (p->n == 1 || !packed)) {
         const int64_t L = packed ? p->T : g.L, slots = sms * (d->dtype == SSD_F32 ? 2 : 1);
         int64_t best = INT64_MAX;

@@ -42,19 +42,19 @@ def test_ranges_of_a_batch_that_may_hold_one_long_sequence(lib):
     """8 sequences of 4001 rows in all (which 8 does not divide: where it does, the query
     covers equal lengths too), 4 heads of 64 x 128: an SM's even share is 210 rows (two
     blocks of 64 columns a head), so that a sequence of more than 512 rows, and of more
-    than 210 + 105 + 896, is cut at multiples of 512."""
+    than 210 + 236 + 1152, is cut at multiples of 512."""
     state = 4 * 64 * 128 * 4
-    assert need(lib, 8, 4001, 4, 2, 64, 128, max_seqlen=1211) == 0
-    assert need(lib, 8, 4001, 4, 2, 64, 128, max_seqlen=1212) == slots(4001, 512) * state
+    assert need(lib, 8, 4001, 4, 2, 64, 128, max_seqlen=1598) == 0
+    assert need(lib, 8, 4001, 4, 2, 64, 128, max_seqlen=1599) == slots(4001, 512) * state
     assert need(lib, 8, 4001, 4, 2, 64, 128) == slots(4001, 512) * state
-    # fp32: from one row more than the least range of 128 rows and the share
-    assert need(lib, 8, 4001, 4, 2, 64, 128, ssd.SSD_F32, max_seqlen=210) == 0
-    assert need(lib, 8, 4001, 4, 2, 64, 128, ssd.SSD_F32, max_seqlen=211) == slots(4001, 128) * state
-    # the gradient runs three of them, four blocks of columns a head (a share of 421), and
-    # keeps dq and dk of each head beside them
+    # fp32: of more than the least range of 128 rows, and of more than 210 + 84 + 176
+    assert need(lib, 8, 4001, 4, 2, 64, 128, ssd.SSD_F32, max_seqlen=470) == 0
+    assert need(lib, 8, 4001, 4, 2, 64, 128, ssd.SSD_F32, max_seqlen=471) == slots(4001, 128) * state
+    # the gradient runs three of them, four blocks of columns a head (a share of 421: from
+    # 421 + 473 + 1152), and keeps dq and dk of each head beside them
     part = 2 * 4001 * 4 * 64 * 4
-    assert need(lib, 8, 4001, 4, 2, 64, 128, backward=1, max_seqlen=1527) == part
-    assert need(lib, 8, 4001, 4, 2, 64, 128, backward=1, max_seqlen=1528) == 3 * slots(4001, 512) * state + part
+    assert need(lib, 8, 4001, 4, 2, 64, 128, backward=1, max_seqlen=2046) == part
+    assert need(lib, 8, 4001, 4, 2, 64, 128, backward=1, max_seqlen=2047) == 3 * slots(4001, 512) * state + part
 
 
 @pytest.mark.parametrize("backward", [0, 1])
