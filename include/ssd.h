@@ -337,8 +337,9 @@ size_t ssd_linattn_workspace_bytes(const ssd_linattn_dims* d, int backward);
  *   final_state  output [nseqs, nheads, vdim, kdim] fp32, or NULL to skip; it may
  *                be init_state itself.  A sequence of no tokens passes its state on.
  * What other sequences' rows hold, NaN and infinities among it, never reaches a
- * sequence's results.  The result does not depend on the order in which the GPU
- * runs the work.  `workspace`: see above.
+ * sequence's results; within a sequence they reach the rows that depend on them and
+ * no others (as a NaN where the sum would be infinite).  The result does not depend
+ * on the order in which the GPU runs the work.  `workspace`: see above.
  */
 ssd_status ssd_linattn_fwd(const ssd_linattn_dims* d, const void* q, const void* k, const void* v,
                            const float* log_decay, float scale, const int32_t* cu_seqlens,

