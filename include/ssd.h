@@ -431,6 +431,159 @@ ssd_status ssd_block_norm_bwd(const ssd_norm_dims* d, const void* r, const void*
                               float* dalpha, float* dw_pre, void* workspace, size_t workspace_bytes,
                               void* stream);
 
+/* Activation of the short convolution: a(p) = p or p sigmoid(p). */
+typedef enum { SSD_ACT_NONE = 0, SSD_ACT_SILU = 1 } ssd_act;
+
+/* Sizes of the short convolution over packed rows.  `tokens` rows of `dim` channels
+ * (8 .. 65536, a multiple of 8) in all, `nseqs` sequences (for ssd_short_conv_step:
+ * nseqs == tokens rows of one token each), `width` taps (2 .. 8).  Rows of x lie
+ * x_stride elements apart (0: contiguous; a multiple of 16 bytes), so that x can be a
+ * column range of one projection's output.  nseqs <= 2^20, tokens <= 2^30. */
+typedef struct {
+    int64_t nseqs, tokens, dim, width;
+    int64_t x_stride;
+    int32_t activation; /* ssd_act */
+    int32_t dtype;      /* ssd_dtype of x, out, the states and their gradients */
+    int32_t reserved;   /* must be 0 */
+} ssd_short_conv_dims;
+
+/*
+ * ssd_short_conv_fwd -- a depthwise causal convolution over the rows of packed
+ * sequences (ssd_causal_conv1d's rows are channels; here they are tokens, as every
+ * projection leaves them).  For each sequence, with the width - 1 rows before it
+ * taken from init_state (0 without one):
+ *   p_t = bias + sum_k weight[:, k] x_{t - width + 1 + k}        out_t = a(p_t)
+ *   x            [tokens, dim].   weight [dim, width] fp32; bias [dim] fp32 or NULL (0).
+ *   cu_seqlens   as for ssd_linattn_fwd; rows of no sequence get an output of 0.
+ *   init_state   [nseqs, width - 1, dim], oldest row first, or NULL.
+ *   out          output [tokens, dim].
+ *   final_state  output [nseqs, width - 1, dim]: the last width - 1 rows before the
+ *                sequence's end (those of a shorter sequence begin with rows of its
+ *                initial state), or NULL to skip.
+ * fp32 sums, one rounding.  Outputs must not overlap an input or each other
+ * (SSD_ERR_ALIAS).  No workspace.
+ */
+ssd_status ssd_short_conv_fwd(const ssd_short_conv_dims* d, const void* x, const float* weight,
+                              const float* bias, const int32_t* cu_seqlens, const void* init_state,
+                              void* out, void* final_state, void* stream);
+
+/* Bytes of device workspace of ssd_short_conv_bwd; 0 if `d` is invalid or empty. */
+size_t ssd_short_conv_bwd_workspace_bytes(const ssd_short_conv_dims* d);
+
+/*
+ * ssd_short_conv_bwd -- the gradient of ssd_short_conv_fwd from dout [tokens, dim] and
+ * dfinal_state (like final_state, or NULL for 0): dx [tokens, dim] (0 in rows of no
+ * sequence), dweight [dim, width] and dbias [dim] fp32 (dbias may be NULL to skip),
+ * dinit_state (or NULL to skip).  Sums over tokens are added in a fixed order.
+ */
+ssd_status ssd_short_conv_bwd(const ssd_short_conv_dims* d, const void* x, const float* weight,
+                              const float* bias, const int32_t* cu_seqlens, const void* init_state,
+                              const void* dout, const void* dfinal_state, void* dx, float* dweight,
+                              float* dbias, void* dinit_state, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+/*
+ * ssd_short_conv_step -- the same for one more token of each of nseqs streams: row b
+ * of x continues the stream whose last width - 1 rows are in slot slots[b] of the
+ * cache (NULL: slot b), which are moved up by one in place; out[b] is its output.
+ *   slots   [nseqs] int32 on the device.  A value outside 0 .. nslots - 1 marks a row
+ *           without a stream: its output is 0 and no slot is touched.  No slot may
+ *           occur twice in a call.
+ *   cache   [nslots, width - 1, dim] in `dtype` (the layout of final_state).
+ */
+ssd_status ssd_short_conv_step(const ssd_short_conv_dims* d, const void* x, const float* weight,
+                               const float* bias, const int32_t* slots, void* cache,
+                               int64_t nslots, void* out, void* stream);
+
+/* Sizes of the selective scan: `tokens` rows of `dim` channels (8 .. 65536) in all,
+ * `nseqs` sequences, `dstate` states (1 .. 64) for each channel; channel d reads group
+ * d / (dim / ngroups) of B and C (dim / ngroups a multiple of 8).
+ *   x, dt, z [tokens, dim], B, C [tokens, ngroups, dstate] in `dtype`.  Rows lie
+ *     x_stride ... C_stride elements apart (0: contiguous); those of x, dt and z are
+ *     multiples of 16 bytes.  B and C need no alignment beyond their type's, nor do
+ *     their strides: they may be any column range of one projection's output.
+ *   dt_softplus   whether delta is softplus(dt + dt_bias) (1) or dt + dt_bias (0).
+ *   max_seqlen    as for ssd_linattn_dims.   nseqs <= 2^20, tokens <= 2^30. */
+typedef struct {
+    int64_t nseqs, tokens, dim, dstate, ngroups;
+    int64_t x_stride, dt_stride, z_stride, B_stride, C_stride;
+    int64_t max_seqlen;
+    int32_t dt_softplus;
+    int32_t dtype;      /* ssd_dtype of x, dt, z, B, C, y and their gradients */
+    int32_t reserved;   /* must be 0 */
+} ssd_selscan_dims;
+
+/* Tokens between two of the states that ssd_selscan_fwd leaves for ssd_selscan_bwd. */
+#define SSD_SELSCAN_CHUNK 32
+
+/* Bytes of device workspace of ssd_selscan_fwd (backward = 0) or ssd_selscan_bwd
+ * (backward != 0); 0 if none is needed or `d` is invalid. */
+size_t ssd_selscan_workspace_bytes(const ssd_selscan_dims* d, int backward);
+
+/*
+ * ssd_selscan_fwd -- the selective state space scan, whose decay differs for every
+ * state of every channel (ssd_fwd has one for each head).  For each sequence and
+ * channel, from h = init_state (or 0) and for its tokens t in order:
+ *   delta = softplus(dt_t + dt_bias)
+ *   h[n] <- exp(delta A[n]) h[n] + delta x_t B_t[n]
+ *   y_t = (sum_n C_t[n] h[n] + D x_t) z_t sigmoid(z_t)
+ *   A            [dim, dstate] fp32, in earnest negative (-inf: no memory).
+ *   D, dt_bias   [dim] fp32 or NULL (0).   z  NULL: no gate.
+ *   cu_seqlens   as for ssd_linattn_fwd; rows of no sequence get a y of 0.
+ *   init_state   [nseqs, dim, dstate] fp32, or NULL for 0.
+ *   y            output [tokens, dim].
+ *   final_state  output [nseqs, dim, dstate] fp32, or NULL to skip; it may be
+ *                init_state itself.  A sequence of no tokens passes its state on.
+ *   states       output [tokens / 32 + nseqs, dim, dstate] fp32, or NULL to skip: the
+ *                state before each 32nd token of each sequence, sequence s's from row
+ *                cu_seqlens[s] / 32 + s on; for ssd_selscan_bwd.
+ * fp32 states and sums, one rounding of y.  What other sequences' rows hold never
+ * reaches a sequence's results.  The result does not depend on the order in which the
+ * GPU runs the work.
+ */
+ssd_status ssd_selscan_fwd(const ssd_selscan_dims* d, const void* x, const void* dt, const float* A,
+                           const void* B, const void* C, const float* D, const void* z,
+                           const float* dt_bias, const int32_t* cu_seqlens, const float* init_state,
+                           void* y, float* final_state, float* states, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/*
+ * ssd_selscan_bwd -- the gradient of ssd_selscan_fwd.  With gy = dout z sigmoid(z) and
+ * r the gradient of h, from q = dfinal_state (or 0) and for a sequence's tokens in
+ * reverse order:
+ *   r = q + gy_t C_t;   u = sum_n r B_t;   w = r exp(delta A) h_{t-1};   q = exp(delta A) r
+ *   dx_t = delta u + D gy_t          ddelta_t = x_t u + sum_n A w
+ *   dA += delta_t w      dB_t += delta x_t r      dC_t += gy_t h_t      dD += gy_t x_t
+ *   ddt = ddelta (times softplus')   ddt_bias += ddt
+ *   dz_t = dout_t (C_t.h_t + D x_t) silu'(z_t)                 dinit_state = q at the end
+ * Inputs as for ssd_selscan_fwd, with `states` as it left them (init_state is their
+ * first) and dout [tokens, dim].  Outputs: dx, ddt, dz [tokens, dim] and dB, dC
+ * [tokens, ngroups, dstate], contiguous, in `dtype` (0 in rows of no sequence; dz is not
+ * written without z); dA [dim, dstate], dD, ddt_bias [dim] fp32 (the last two may be
+ * NULL to skip); dinit_state fp32, or NULL to skip.  Sums over channels, tokens and
+ * sequences are added in a fixed order.  Outputs must not overlap an input or each
+ * other (SSD_ERR_ALIAS).
+ */
+ssd_status ssd_selscan_bwd(const ssd_selscan_dims* d, const void* x, const void* dt, const float* A,
+                           const void* B, const void* C, const float* D, const void* z,
+                           const float* dt_bias, const int32_t* cu_seqlens, const float* states,
+                           const void* dout, const float* dfinal_state, void* dx, void* ddt,
+                           float* dA, void* dB, void* dC, float* dD, void* dz, float* ddt_bias,
+                           float* dinit_state, void* workspace, size_t workspace_bytes,
+                           void* stream);
+
+/*
+ * ssd_selscan_step -- the selective scan for one more token of each of nseqs ==
+ * tokens streams, whose states lie in a cache: row b of x, dt, z, B and C continues the
+ * state in slot slots[b] (NULL: slot b), which is updated in place; y[b] is its output.
+ *   slots   as for ssd_linattn_step.
+ *   cache   [nslots, dim, dstate] fp32 (the layout of final_state).
+ */
+ssd_status ssd_selscan_step(const ssd_selscan_dims* d, const void* x, const void* dt, const float* A,
+                            const void* B, const void* C, const float* D, const void* z,
+                            const float* dt_bias, const int32_t* slots, float* cache,
+                            int64_t nslots, void* y, void* stream);
+
 /* Size of the fixed device scratch buffer used by ssd_fwd_noalloc: 32 MiB. */
 #define SSD_NOALLOC_WORKSPACE_BYTES ((size_t)32 << 20)
 

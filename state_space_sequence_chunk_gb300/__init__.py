@@ -18,6 +18,10 @@ Entry points (same names as the C ABI):
   attention with a decay for each head: prompts, their gradient, single tokens.
 * :func:`block_norm_fwd`, :func:`block_norm_bwd` -- the norms before and after a
   block with its gate and residual scale, and their gradient.
+* :func:`short_conv_fwd`, :func:`short_conv_bwd`, :func:`short_conv_step` -- the
+  depthwise causal convolution over packed rows: prompts, gradient, single tokens.
+* :func:`selscan_fwd`, :func:`selscan_bwd`, :func:`selscan_step` -- the selective
+  scan, with a decay for every state of every channel: the same three.
 
 None of these is recorded by autograd: what they return is cut from the graph, also of
 inputs that require a gradient.  A training step calls the ``_bwd`` functions, from an
@@ -45,8 +49,12 @@ EXPORTS = ["ssd_abi_version", "ssd_status_string", "ssd_fwd_workspace_bytes",
            "ssd_causal_conv1d", "ssd_gdn_chunk_fwd_h", "ssd_gdn_chunk_fwd_o",
            "ssd_fwd_host_staging_bytes", "ssd_fwd_host", "ssd_linattn_workspace_bytes",
            "ssd_linattn_fwd", "ssd_linattn_bwd", "ssd_linattn_step", "ssd_block_norm_fwd",
-           "ssd_block_norm_bwd_workspace_bytes", "ssd_block_norm_bwd"]
+           "ssd_block_norm_bwd_workspace_bytes", "ssd_block_norm_bwd", "ssd_short_conv_fwd",
+           "ssd_short_conv_bwd_workspace_bytes", "ssd_short_conv_bwd", "ssd_short_conv_step",
+           "ssd_selscan_workspace_bytes", "ssd_selscan_fwd", "ssd_selscan_bwd", "ssd_selscan_step"]
 GATES = {None: 0, "silu": 1, "sigmoid": 2}
+ACTIVATIONS = {None: 0, "silu": 1}
+SELSCAN_CHUNK = 32
 
 
 class SSDError(RuntimeError):
@@ -78,6 +86,18 @@ class NormDims(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int64) for n in ("tokens", "width", "ngroups", "y_stride", "z_stride")] + [
         ("gate", ctypes.c_int32), ("eps", ctypes.c_float), ("dtype", ctypes.c_int32),
         ("rdtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class ShortConvDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("nseqs", "tokens", "dim", "width", "x_stride")] + [
+        ("activation", ctypes.c_int32), ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class SelscanDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in
+                ("nseqs", "tokens", "dim", "dstate", "ngroups", "x_stride", "dt_stride", "z_stride",
+                 "B_stride", "C_stride", "max_seqlen")] + [
+        ("dt_softplus", ctypes.c_int32), ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 class Dims(ctypes.Structure):
@@ -153,6 +173,23 @@ def load_library(path: str = LIB_PATH):
         lib.ssd_block_norm_bwd_workspace_bytes.restype = sz
         lib.ssd_block_norm_bwd.argtypes = [nd] + [vp] * 17 + [sz, vp]
         lib.ssd_block_norm_bwd.restype = ctypes.c_int
+        cd, sd = ctypes.POINTER(ShortConvDims), ctypes.POINTER(SelscanDims)
+        lib.ssd_short_conv_fwd.argtypes = [cd] + [vp] * 8
+        lib.ssd_short_conv_fwd.restype = ctypes.c_int
+        lib.ssd_short_conv_bwd_workspace_bytes.argtypes = [cd]
+        lib.ssd_short_conv_bwd_workspace_bytes.restype = sz
+        lib.ssd_short_conv_bwd.argtypes = [cd] + [vp] * 12 + [sz, vp]
+        lib.ssd_short_conv_bwd.restype = ctypes.c_int
+        lib.ssd_short_conv_step.argtypes = [cd] + [vp] * 5 + [i64, vp, vp]
+        lib.ssd_short_conv_step.restype = ctypes.c_int
+        lib.ssd_selscan_workspace_bytes.argtypes = [sd, ctypes.c_int]
+        lib.ssd_selscan_workspace_bytes.restype = sz
+        lib.ssd_selscan_fwd.argtypes = [sd] + [vp] * 14 + [sz, vp]
+        lib.ssd_selscan_fwd.restype = ctypes.c_int
+        lib.ssd_selscan_bwd.argtypes = [sd] + [vp] * 22 + [sz, vp]
+        lib.ssd_selscan_bwd.restype = ctypes.c_int
+        lib.ssd_selscan_step.argtypes = [sd] + [vp] * 10 + [i64, vp, vp]
+        lib.ssd_selscan_step.restype = ctypes.c_int
         _lib = lib
         return lib
 
@@ -667,3 +704,211 @@ def block_norm_bwd(r, y, w_pre, dr_out, dn, rstd, z=None, w_post=None, alpha=Non
                                   _addr(g["dalpha"]), _addr(g["dw_pre"]), _addr(workspace), nbytes,
                                   _stream_int()))
     return g
+
+
+def _here(x, *others):
+    """The calls below launch on the current device: operands of another one, or of two,
+    are refused."""
+    dev = torch.cuda.current_device() if x.is_cuda else -1
+    for t in (x,) + others:
+        if t is not None and (not t.is_cuda or t.get_device() != dev):
+            raise ValueError("tensors must be CUDA tensors on the current device")
+
+
+def _seqs(cu_seqlens, nseqs):
+    if cu_seqlens is None:
+        return int(nseqs)
+    if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+        raise ValueError("cu_seqlens must be a 1-D int32 tensor of nseqs + 1 values")
+    return cu_seqlens.numel() - 1
+
+
+def _space(need: int, workspace, device):
+    if workspace is None and need > 0:
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    return workspace, 0 if workspace is None else workspace.numel() * workspace.element_size()
+
+
+def _new(t, name, dtype, shape, device):
+    """The caller's output, checked, or a new one."""
+    return torch.empty(shape, dtype=dtype, device=device) if t is None else _typed(t, name, dtype, shape)
+
+
+def _short_conv_dims(x, weight, bias, activation, nseqs):
+    if x.dim() != 2 or weight.dim() != 2:
+        raise ValueError("x must be [tokens, dim] and weight [dim, width]")
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"activation must be one of {list(ACTIVATIONS)}, got {activation!r}")
+    T, D = x.shape
+    W = weight.shape[1]
+    _typed(weight, "weight", torch.float32, (D, W))
+    _typed(bias, "bias", torch.float32, (D,))
+    xp, xs = _rows(x, D)
+    return ShortConvDims(nseqs, T, D, W, xs, ACTIVATIONS[activation], _dtype_code(x, "x"), 0), xp
+
+
+def short_conv_fwd(x, weight, bias=None, activation=None, cu_seqlens=None, init_state=None,
+                   nseqs: int = 1, return_final_state: bool = True, out=None, final_out=None):
+    """Depthwise causal convolution over the rows of packed sequences:
+    out_t = act(bias + sum_k weight[:, k] x_{t - W + 1 + k}), ``activation`` None or "silu".
+
+    x [tokens, dim] (bfloat16 or float32; its rows may be slices of a wider tensor's) holds
+    the sequences one after another: ``cu_seqlens`` (int32, nseqs + 1) says where each
+    begins, or without it they are ``nseqs`` of equal length.  weight [dim, W] and bias
+    [dim] are float32.  init_state [nseqs, W - 1, dim] in x's dtype holds the rows before
+    each sequence, oldest first (0 without it).
+    Returns ``(out [tokens, dim], final_state [nseqs, W - 1, dim] or None)``.
+    """
+    lib = _lib or load_library()
+    n = _seqs(cu_seqlens, nseqs)
+    _here(x, weight, bias, cu_seqlens, init_state, out, final_out)
+    d, xp = _short_conv_dims(x, weight, bias, activation, n)
+    T, D = x.shape
+    state = (n, weight.shape[1] - 1, D)
+    _typed(init_state, "init_state", x.dtype, state)
+    o = _new(out, "out", x.dtype, (T, D), x.device)
+    fin = _new(final_out, "final_out", x.dtype, state, x.device) if return_final_state else None
+    _check(lib.ssd_short_conv_fwd(ctypes.byref(d), xp, _addr(weight), _addr(bias), _addr(cu_seqlens),
+                                  _addr(init_state), _addr(o), _addr(fin), _stream_int()))
+    return o, fin
+
+
+def short_conv_bwd(x, weight, dout, bias=None, activation=None, cu_seqlens=None, init_state=None,
+                   dfinal_state=None, nseqs: int = 1, workspace=None):
+    """The gradient of short_conv_fwd from dout [tokens, dim] and dfinal_state (None: 0).
+    Returns a dict: dx, dweight, dbias (None without a bias) and dinit_state (None without
+    an init_state)."""
+    lib = _lib or load_library()
+    n = _seqs(cu_seqlens, nseqs)
+    _here(x, weight, dout, bias, cu_seqlens, init_state, dfinal_state, workspace)
+    d, xp = _short_conv_dims(x, weight, bias, activation, n)
+    T, D = x.shape
+    state = (n, weight.shape[1] - 1, D)
+    _typed(dout, "dout", x.dtype, (T, D))
+    _typed(init_state, "init_state", x.dtype, state)
+    _typed(dfinal_state, "dfinal_state", x.dtype, state)
+    new = lambda shape, dt: torch.empty(shape, dtype=dt, device=x.device)
+    g = {"dx": new((T, D), x.dtype), "dweight": new(weight.shape, torch.float32),
+         "dbias": None if bias is None else new((D,), torch.float32),
+         "dinit_state": None if init_state is None else new(state, x.dtype)}
+    workspace, nbytes = _space(int(lib.ssd_short_conv_bwd_workspace_bytes(ctypes.byref(d))), workspace, x.device)
+    _check(lib.ssd_short_conv_bwd(ctypes.byref(d), xp, _addr(weight), _addr(bias), _addr(cu_seqlens),
+                                  _addr(init_state), _addr(dout), _addr(dfinal_state), _addr(g["dx"]),
+                                  _addr(g["dweight"]), _addr(g["dbias"]), _addr(g["dinit_state"]),
+                                  _addr(workspace), nbytes, _stream_int()))
+    return g
+
+
+def short_conv_step(x, weight, cache, bias=None, activation=None, slots=None, out=None):
+    """The same convolution for one more token of each row's stream: x [b, dim]; ``cache``
+    [nslots, W - 1, dim] in x's dtype holds each stream's last rows (short_conv_fwd's final
+    states) and is moved up by one in place; ``slots`` [b] int32 says which is whose (row
+    b's slot is b without it; a negative one marks a row without a stream, whose output is
+    0; no slot may occur twice).  Returns out [b, dim]."""
+    lib = _lib or load_library()
+    _here(x, weight, cache, bias, slots, out)
+    d, xp = _short_conv_dims(x, weight, bias, activation, x.shape[0])
+    b, D = x.shape
+    _typed(cache, "cache", x.dtype, (cache.shape[0], weight.shape[1] - 1, D))
+    _typed(slots, "slots", torch.int32, (b,))
+    o = _new(out, "out", x.dtype, (b, D), x.device)
+    _check(lib.ssd_short_conv_step(ctypes.byref(d), xp, _addr(weight), _addr(bias), _addr(slots), _addr(cache),
+                                   cache.shape[0], _addr(o), _stream_int()))
+    return o
+
+
+def _selscan_dims(x, dt, A, B, C, D, z, dt_bias, dt_softplus, nseqs, max_seqlen):
+    if x.dim() != 2 or A.dim() != 2 or B.dim() != 3:
+        raise ValueError("x must be [tokens, dim], A [dim, N], B and C [tokens, G, N]")
+    T, W = x.shape
+    N, G = A.shape[1], B.shape[1]
+    _typed(dt, "dt", x.dtype, (T, W))
+    _typed(z, "z", x.dtype, (T, W))
+    _typed(A, "A", torch.float32, (W, N))
+    _typed(B, "B", x.dtype, (T, G, N))
+    _typed(C, "C", x.dtype, (T, G, N))
+    _typed(D, "D", torch.float32, (W,))
+    _typed(dt_bias, "dt_bias", torch.float32, (W,))
+    (xp, xs), (tp, ts), (Bp, Bs), (Cp, Cs) = _rows(x, W), _rows(dt, W), _rows(B, G * N), _rows(C, G * N)
+    zp, zs = (None, 0) if z is None else _rows(z, W)
+    d = SelscanDims(nseqs, T, W, N, G, xs, ts, zs, Bs, Cs, max_seqlen, 1 if dt_softplus else 0,
+                    _dtype_code(x, "x"), 0)
+    return d, (xp, tp, _addr(A), Bp, Cp, _addr(D), zp, _addr(dt_bias))
+
+
+def selscan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus: bool = False,
+                cu_seqlens=None, init_state=None, nseqs: int = 1, max_seqlen: int = 0,
+                return_final_state: bool = True, return_states: bool = False, workspace=None,
+                out=None, final_out=None):
+    """The selective state space scan: with delta = softplus(dt + dt_bias) (or dt + dt_bias),
+    h_t = exp(delta_t A) h_{t-1} + delta_t x_t B_t and y_t = (C_t . h_t + D x_t) silu(z_t),
+    with N states and decays for each channel.
+
+    x, dt, z [tokens, dim] and B, C [tokens, G, N] share one dtype (bfloat16 or float32) and
+    hold the sequences one after another: ``cu_seqlens`` (int32, nseqs + 1) says where each
+    begins, or without it they are ``nseqs`` of equal length.  Channel d reads group
+    d // (dim // G) of B and C.  Rows may be slices of a wider tensor's; those of B and C
+    need no alignment.  A [dim, N], D, dt_bias [dim] and init_state [nseqs, dim, N] are
+    float32; D, z and dt_bias may be None.  ``max_seqlen`` (0: not known) spares the
+    preparations for long sequences where there are none.
+    Returns ``(y [tokens, dim], final_state [nseqs, dim, N] float32 or None)``, with
+    ``return_states`` also the states on the way that selscan_bwd needs,
+    [tokens // SELSCAN_CHUNK + nseqs, dim, N] float32.
+    """
+    lib = _lib or load_library()
+    n = _seqs(cu_seqlens, nseqs)
+    _here(x, dt, A, B, C, D, z, dt_bias, cu_seqlens, init_state, workspace, out, final_out)
+    d, args = _selscan_dims(x, dt, A, B, C, D, z, dt_bias, dt_softplus, n, max_seqlen)
+    T, W = x.shape
+    N = A.shape[1]
+    _typed(init_state, "init_state", torch.float32, (n, W, N))
+    y = _new(out, "out", x.dtype, (T, W), x.device)
+    fin = _new(final_out, "final_out", torch.float32, (n, W, N), x.device) if return_final_state else None
+    states = torch.empty((T // SELSCAN_CHUNK + n, W, N), dtype=torch.float32, device=x.device) if return_states else None
+    workspace, nbytes = _space(int(lib.ssd_selscan_workspace_bytes(ctypes.byref(d), 0)), workspace, x.device)
+    _check(lib.ssd_selscan_fwd(ctypes.byref(d), *args, _addr(cu_seqlens), _addr(init_state), _addr(y), _addr(fin),
+                               _addr(states), _addr(workspace), nbytes, _stream_int()))
+    return (y, fin, states) if return_states else (y, fin)
+
+
+def selscan_bwd(x, dt, A, B, C, dout, states, D=None, z=None, dt_bias=None, dt_softplus: bool = False,
+                cu_seqlens=None, dfinal_state=None, nseqs: int = 1, max_seqlen: int = 0,
+                return_dinit: bool = False, workspace=None):
+    """The gradient of selscan_fwd (same inputs, and its ``states``) from dout [tokens, dim] and
+    dfinal_state (None: 0).  Returns a dict: dx, ddt, dA, dB, dC, dD, dz and ddt_bias (each None
+    where the input is None) and dinit_state (None unless ``return_dinit``)."""
+    lib = _lib or load_library()
+    n = _seqs(cu_seqlens, nseqs)
+    _here(x, dt, A, B, C, dout, states, D, z, dt_bias, cu_seqlens, dfinal_state, workspace)
+    d, args = _selscan_dims(x, dt, A, B, C, D, z, dt_bias, dt_softplus, n, max_seqlen)
+    T, W = x.shape
+    N = A.shape[1]
+    _typed(dout, "dout", x.dtype, (T, W))
+    _typed(states, "states", torch.float32, (T // SELSCAN_CHUNK + n, W, N))
+    _typed(dfinal_state, "dfinal_state", torch.float32, (n, W, N))
+    like = lambda t: None if t is None else torch.empty(t.shape, dtype=t.dtype, device=x.device)
+    g = {"dx": like(x), "ddt": like(dt), "dA": like(A), "dB": like(B), "dC": like(C), "dD": like(D), "dz": like(z),
+         "ddt_bias": like(dt_bias),
+         "dinit_state": torch.empty((n, W, N), dtype=torch.float32, device=x.device) if return_dinit else None}
+    workspace, nbytes = _space(int(lib.ssd_selscan_workspace_bytes(ctypes.byref(d), 1)), workspace, x.device)
+    _check(lib.ssd_selscan_bwd(ctypes.byref(d), *args, _addr(cu_seqlens), _addr(states), _addr(dout),
+                               _addr(dfinal_state), *(_addr(t) for t in g.values()), _addr(workspace), nbytes,
+                               _stream_int()))
+    return g
+
+
+def selscan_step(x, dt, A, B, C, cache, D=None, z=None, dt_bias=None, dt_softplus: bool = False,
+                 slots=None, out=None):
+    """The selective scan for one more token of each row's stream: x, dt, z [b, dim],
+    B, C [b, G, N]; ``cache`` [nslots, dim, N] float32 holds the states and is updated in
+    place; ``slots`` as for short_conv_step.  Returns y [b, dim]."""
+    lib = _lib or load_library()
+    _here(x, dt, A, B, C, cache, D, z, dt_bias, slots, out)
+    d, args = _selscan_dims(x, dt, A, B, C, D, z, dt_bias, dt_softplus, x.shape[0], 0)
+    b, W = x.shape
+    _typed(cache, "cache", torch.float32, (cache.shape[0], W, A.shape[1]))
+    _typed(slots, "slots", torch.int32, (b,))
+    y = _new(out, "out", x.dtype, (b, W), x.device)
+    _check(lib.ssd_selscan_step(ctypes.byref(d), *args, _addr(slots), _addr(cache), cache.shape[0], _addr(y),
+                                _stream_int()))
+    return y

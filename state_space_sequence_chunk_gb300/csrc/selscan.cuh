@@ -1,0 +1,205 @@
+// selscan.cuh -- shared declarations of the selective-scan kernels (not part of the ABI).
+//
+// Per channel d with N states, for the tokens t of a sequence in order:
+//     delta_t = softplus(dt_t + dt_bias)  (or dt_t + dt_bias)
+//     h_t[n] = exp(delta_t A[n]) h_{t-1}[n] + delta_t x_t B_t[n]
+//     y_t = (sum_n C_t[n] h_t[n] + D x_t) silu(z_t)
+// Unlike the SSD's, the decay differs for every state of every channel, so no
+// matrix product evaluates it: each (token, channel, state) takes one exponential
+// and four multiply-adds' worth of fp32.  An SM does 32 exponentials and 128
+// multiply-adds a clock, so both pipes are the bound at once, at 4 clocks for 32
+// elements a quarter-SM.
+//
+// A sequence is walked by one warp for each 32 / lanes-a-channel channels.  Where
+// that leaves SMs idle it is cut into ranges of R tokens: a first launch walks each
+// range from a zero state and keeps its end and its sum of delta (the range
+// multiplies a state by exp(A sum delta)), a scan makes the states at the ranges'
+// starts, and the main launch walks the ranges independently.
+#pragma once
+
+#include "f32x2.cuh"
+
+namespace ssd {
+
+struct ScanGeom {
+    const int* cu;       // first token of each sequence [nseq + 1], or NULL: equal lengths L
+    int nseq, T, L;
+    int R;               // tokens of a range; above T: no sequence is cut
+    int items;           // ranges of sequences: T / R + nseq at most
+};
+
+struct ScanParams {
+    ScanGeom g;
+    int D, N, G, cpg;    // channels, states, groups, channels of a group
+    int softplus;
+    int vecB, vecC;      // rows of B (C) can be read in vectors of four
+    const void *x, *dt, *z, *B, *C;
+    int64_t xs, dts, zs, Bs, Cs;     // elements from one row to the next
+    const float *A, *Dk, *bias;
+    const float* init;   // [nseq, D, N] or NULL
+    float* fin;          // likewise
+    float* states;       // [T / kScanChunk + nseq, D, N]: before each kScanChunk-th token, or NULL
+    void* y;
+    float *agg, *aggd;   // [items, D, N] and [items, D] where sequences are cut
+    // gradient
+    const void* dout;
+    const float* dfin;
+    void *dx, *ddt, *dz, *dB, *dC;
+    float *dA, *dD, *dbias, *dinit;
+    float* part;         // [tiles of a group, T, G, 2, N]: the terms of dB and dC
+    float *partA, *partD; // [slots, D, N] and [slots, 2, D]: the terms of dA, of dD and dbias
+    int slots, per_slot; // items / per_slot slots, each with the terms of per_slot items
+};
+
+constexpr int kScanChunk = SSD_SELSCAN_CHUNK;   // tokens between two stored states
+
+// What an item of a launch is: rows t0 .. t0 + len of sequence seq.
+struct ScanItem {
+    int seq, t0, len, first, last;
+    int row0;            // number of the sequence's first stored state
+    int done;            // tokens of the sequence before t0
+};
+
+#ifdef __CUDACC__
+__device__ __forceinline__ void scan_bounds(const ScanGeom& g, int s, int& lo, int& hi) {
+    // clamped, so that no content of cu leads out of the tensors
+    if (g.cu != nullptr) {
+        lo = min(max(g.cu[s], 0), g.T);
+        hi = min(max(g.cu[s + 1], lo), g.T);
+    } else {
+        lo = s * g.L;
+        hi = lo + g.L;
+    }
+}
+__device__ __forceinline__ int scan_base(const ScanGeom& g, int s) {
+    const int lo = g.cu != nullptr ? min(max(g.cu[s], 0), g.T) : s * g.L;
+    return lo / g.R + s;
+}
+// Item i: sequence s's ranges are numbered from cu[s] / R + s on, which leaves room
+// for all of them.  Found in steps of 32; executed by a whole warp.  False: no such range.
+__device__ __forceinline__ bool scan_find(const ScanGeom& g, int i, ScanItem& it) {
+    int s = i;
+    if (g.R <= g.T) {
+        const int lane = threadIdx.x & 31;
+        int at = 0, n = g.nseq;          // the last s with base(s) <= i is in at .. at + n - 1
+        while (n > 1) {
+            const int step = (n + 31) / 32, o = lane * step;
+            const int c = __popc(__ballot_sync(0xffffffffu, o < n && scan_base(g, at + min(o, n - 1)) <= i));
+            const int k = max(c, 1) - 1;
+            at += k * step;
+            n = min(step, n - k * step);
+        }
+        s = at;
+    }
+    int lo, hi;
+    scan_bounds(g, s, lo, hi);
+    const int64_t off = (int64_t)(i - (g.R <= g.T ? scan_base(g, s) : s)) * g.R;
+    if (off < 0 || (off > 0 && off >= hi - lo)) return false;
+    it.seq = s;
+    it.done = (int)off;
+    it.t0 = lo + (int)off;
+    it.len = min(g.R, hi - it.t0);
+    it.first = off == 0;
+    it.last = it.t0 + it.len == hi;
+    it.row0 = lo / kScanChunk + s;
+    return true;
+}
+
+__device__ __forceinline__ float ex2(float v) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ float rcp(float v) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ f32x2 ex2_2(f32x2 v) {
+    float a, b;
+    unpair(v, a, b);
+    return pair(ex2(a), ex2(b));
+}
+// exp(-|v|).  The product with log2(e) is rounded; in fp32 calls its remainder is
+// added back (log2(e) in two floats), so that the result is good to the
+// exponential's own error also where v is large.
+template <bool EXACT> __device__ __forceinline__ float exp_neg_abs(float v) {
+    const float m = -fabsf(v), p = m * kLog2e;
+    float e = ex2(p);
+    if (EXACT) {
+        const float lo = fmaf(m, kLog2e, -p) + m * 1.925963033500e-8f;   // log2(e) - kLog2e
+        if (p > -126.f) e = fmaf(e * 0.69314718f, lo, e);
+    }
+    return e;
+}
+// log(1 + e) for e in [0, 1], from log(1 + e) = 2 atanh(e / (2 + e)): the quotient is at
+// most 1/3, and atanh(s) / s is fitted by a polynomial in s^2 (Chebyshev interpolation on
+// [0, 1/9], off by 8e-9).  Small e keep their relative precision, which log(1 + e) loses.
+__device__ __forceinline__ float log1p_unit(float e) {
+    const float s = e * rcp(2.f + e), u = s * s;
+    float q = fmaf(u, 0.14078889787197113f, 0.13982579112052917f);
+    q = fmaf(u, q, 0.20012298226356506f);
+    q = fmaf(u, q, 0.3333316147327423f);
+    return 2.f * fmaf(u * s, q, s);
+}
+// softplus(v) = max(v, 0) + log(1 + exp(-|v|)); a NaN stays one.
+template <bool EXACT> __device__ __forceinline__ float softplus(float v) {
+    const float l = log1p_unit(exp_neg_abs<EXACT>(v));
+    return v > 0.f ? v + l : l;
+}
+// its derivative, 1 / (1 + exp(-v))
+template <bool EXACT> __device__ __forceinline__ float softplus_grad(float v) {
+    const float e = exp_neg_abs<EXACT>(v), r = rcp(1.f + e);
+    return v >= 0.f ? r : e * r;
+}
+__device__ __forceinline__ float sigmoid(float z) { return rcp(1.f + ex2(-z * kLog2e)); }
+
+// A log2(e), so that the decays are base-2 exponentials; -inf (no memory) becomes a finite
+// value whose every power but the 0th is 0.
+__device__ __forceinline__ float scan_rate(float a) {
+    const float v = a * kLog2e;
+    return v < -1e37f ? -1e37f : v;
+}
+
+// Four consecutive states of a row of B or C from n on, 0 beyond N.
+template <typename T> __device__ __forceinline__ float4 load_states(const T* p, int n, int N, bool vec);
+template <> __device__ __forceinline__ float4 load_states(const float* p, int n, int N, bool vec) {
+    if (vec) return n < N ? __ldg(reinterpret_cast<const float4*>(p + n)) : make_float4(0.f, 0.f, 0.f, 0.f);
+    return make_float4(n < N ? __ldg(p + n) : 0.f, n + 1 < N ? __ldg(p + n + 1) : 0.f,
+                       n + 2 < N ? __ldg(p + n + 2) : 0.f, n + 3 < N ? __ldg(p + n + 3) : 0.f);
+}
+template <> __device__ __forceinline__ float4 load_states(const __nv_bfloat16* p, int n, int N, bool vec) {
+    if (vec) {
+        const uint2 v = n < N ? __ldg(reinterpret_cast<const uint2*>(p + n)) : make_uint2(0u, 0u);
+        return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u),
+                           __uint_as_float(v.y << 16), __uint_as_float(v.y & 0xFFFF0000u));
+    }
+    return make_float4(n < N ? to_f32(p[n]) : 0.f, n + 1 < N ? to_f32(p[n + 1]) : 0.f,
+                       n + 2 < N ? to_f32(p[n + 2]) : 0.f, n + 3 < N ? to_f32(p[n + 3]) : 0.f);
+}
+#endif
+
+// Launchers.  kScanSums: the ranges' own ends into agg and aggd; kScanRevSums: the same
+// backwards, of the gradient that leaves each at its start.
+enum ScanMode { kScanMain = 0, kScanSums = 1, kScanRevSums = 2 };
+cudaError_t launch_selscan_fwd(const ScanParams& p, int dtype, ScanMode mode, cudaStream_t stream);
+// agg -> the state at each range's start, in place (rev: the gradient entering each range's end).
+cudaError_t launch_selscan_ranges(const ScanParams& p, int rev, cudaStream_t stream);
+
+// The gradient's main pass and the sums of its terms; channels of a tile of `part`.
+int selscan_bwd_channels(int N);
+cudaError_t launch_selscan_bwd(const ScanParams& p, int dtype, cudaStream_t stream);
+
+struct ScanStep {
+    int D, N, G, cpg, softplus;
+    int64_t batch, nslots;
+    const void *x, *dt, *z, *B, *C;
+    int64_t xs, dts, zs, Bs, Cs;
+    const float *A, *Dk, *bias;
+    const int* slots;
+    float* cache;
+    void* y;
+};
+cudaError_t launch_selscan_step(const ScanStep& p, int dtype, cudaStream_t stream);
+
+}  // namespace ssd
