@@ -90,10 +90,20 @@ __device__ __forceinline__ bool scan_find(const ScanGeom& g, int i, ScanItem& it
             n = min(step, n - k * step);
         }
         s = at;
+    } else if (g.nseq <= 32 && g.nseq > 1) {
+        // whole sequences, longest first: a long one that begins last would keep the GPU waiting
+        const int lane = threadIdx.x & 31;
+        int lo = 0, hi = 0, rank = 0;
+        if (lane < g.nseq) scan_bounds(g, lane, lo, hi);
+        for (int j = 0; j < g.nseq; ++j) {
+            const int len = __shfl_sync(0xffffffffu, hi - lo, j);
+            rank += len > hi - lo || (len == hi - lo && j < lane);
+        }
+        s = __ffs(__ballot_sync(0xffffffffu, lane < g.nseq && rank == i)) - 1;
     }
     int lo, hi;
     scan_bounds(g, s, lo, hi);
-    const int64_t off = (int64_t)(i - (g.R <= g.T ? scan_base(g, s) : s)) * g.R;
+    const int64_t off = g.R <= g.T ? (int64_t)(i - scan_base(g, s)) * g.R : 0;
     if (off < 0 || (off > 0 && off >= hi - lo)) return false;
     it.seq = s;
     it.done = (int)off;
@@ -142,10 +152,30 @@ __device__ __forceinline__ float log1p_unit(float e) {
     q = fmaf(u, q, 0.3333316147327423f);
     return 2.f * fmaf(u * s, q, s);
 }
+__device__ __forceinline__ f32x2 both(float a) { return pair(a, a); }
+__device__ __forceinline__ f32x2 log1p_unit2(f32x2 e) {
+    float a, b;
+    unpair(add2(e, both(2.f)), a, b);
+    const f32x2 s = mul2(e, pair(rcp(a), rcp(b))), u = mul2(s, s);
+    f32x2 q = fma2(u, both(0.14078889787197113f), both(0.13982579112052917f));
+    q = fma2(u, q, both(0.20012298226356506f));
+    q = fma2(u, q, both(0.3333316147327423f));
+    return fma2(mul2(u, s), q, s);            // half of it
+}
 // softplus(v) = max(v, 0) + log(1 + exp(-|v|)); a NaN stays one.
 template <bool EXACT> __device__ __forceinline__ float softplus(float v) {
-    const float l = log1p_unit(exp_neg_abs<EXACT>(v));
-    return v > 0.f ? v + l : l;
+    return fmaxf(v, 0.f) + log1p_unit(exp_neg_abs<EXACT>(v));
+}
+template <bool EXACT> __device__ __forceinline__ f32x2 softplus2(float a, float b) {
+    const f32x2 l = log1p_unit2(pair(exp_neg_abs<EXACT>(a), exp_neg_abs<EXACT>(b)));
+    return fma2(both(2.f), l, pair(fmaxf(a, 0.f), fmaxf(b, 0.f)));
+}
+// z sigmoid(z) of two numbers
+__device__ __forceinline__ f32x2 silu2(f32x2 z) {
+    float a, b;
+    unpair(mul2(z, both(-kLog2e)), a, b);
+    unpair(add2(pair(ex2(a), ex2(b)), both(1.f)), a, b);
+    return mul2(z, pair(rcp(a), rcp(b)));
 }
 // its derivative, 1 / (1 + exp(-v))
 template <bool EXACT> __device__ __forceinline__ float softplus_grad(float v) {
@@ -159,6 +189,21 @@ __device__ __forceinline__ float sigmoid(float z) { return rcp(1.f + ex2(-z * kL
 __device__ __forceinline__ float scan_rate(float a) {
     const float v = a * kLog2e;
     return v < -1e37f ? -1e37f : v;
+}
+
+// One step of a butterfly: of M values a lane keeps the half that its bit names, summed
+// with its partner's.
+template <int M> __device__ __forceinline__ void halve(float* v, int lane, int bit) {
+    if (M > 1) {
+        const bool up = (lane & bit) != 0;
+#pragma unroll
+        for (int i = 0; i < M / 2; ++i) {
+            const float keep = up ? v[i + M / 2] : v[i], send = up ? v[i] : v[i + M / 2];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, bit);
+        }
+    } else {
+        v[0] += __shfl_xor_sync(0xffffffffu, v[0], bit);
+    }
 }
 
 // Four consecutive states of a row of B or C from n on, 0 beyond N.

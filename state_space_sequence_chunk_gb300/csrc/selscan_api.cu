@@ -51,16 +51,27 @@ ssd_status make(const ssd_selscan_dims* d, bool packed, bool backward, Scan* out
     q.states = (size_t)(q.n * q.D * q.N) * 4;
     q.checkpoints = (size_t)((q.T / kScanChunk + q.n) * q.D * q.N) * 4;
 
-    // A sequence is cut where a chain of its whole length would keep the other SMs waiting.
+    // A sequence is cut where a chain of its whole length would keep the other SMs waiting.  A
+    // warp by itself takes 104 ns a token; the cut's two passes take 225 ps for each token
+    // and warp when all SMs work, and some 50 us of launches and ramps.  Whole and cut, us:
+    // 16 states, 8192 tokens of 2048 channels (64 warps) 860 and 146, the same in 6
+    // sequences 214 and 148; 16384 tokens of 5120 in 12 sequences 421 and 592; 16384 of 2048
+    // in 40 195 and 271; 512 of 5120 61 and 71.
     const int64_t warps = backward ? q.G * ((p.cpg + (q.N <= 16 ? 15 : 7)) / (q.N <= 16 ? 16 : 8))
                                    : q.G * ((p.cpg * (q.N <= 16 ? 1 : q.N <= 32 ? 2 : 4) + 31) / 32);
-    const int64_t slots = (int64_t)sm_count() * 4 * (backward ? 2 : 4), share = q.T * warps / slots;
+    const int64_t sms = sm_count(), work = q.T * warps;
     int64_t longest = packed ? (d->max_seqlen ? d->max_seqlen : q.T) : g.L;
     if (longest > q.T) longest = q.T;
     g.R = INT_MAX;
-    if (q.n > 0 && longest > 2 * share + 256) {
-        int64_t R = (share / 2 + 63) / 64 * 64;
-        if (R < 128) R = 128;
+    if (backward) {
+        const int64_t share = work / (8 * sms), R = (share / 2 + 63) / 64 * 64;
+        if (q.n > 0 && longest > 2 * share + 256 && longest > (R < 128 ? 128 : R)) g.R = (int)(R < 128 ? 128 : R);
+    } else if (q.n > 0 && longest > work / (3 * sms) + 512) {
+        // several ranges for each warp that is resident, but not shorter than 128 tokens
+        // (8192 tokens of 2048 channels: ranges of 128, 256, 512 tokens 146, 160, 197 us;
+        // 65536 of 1536: 128, 384, 512: 769, 728, 755)
+        int64_t R = (work / (54 * sms) + 31) / 32 * 32;
+        R = R < 128 ? 128 : R > 512 ? 512 : R;
         if (R < longest) g.R = (int)R;
     }
     const bool cut = g.R <= q.T;

@@ -57,21 +57,6 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, const float (&v)[4]) {
 }
 __device__ __forceinline__ void spread(float4 v, float (&o)[4]) { o[0] = v.x; o[1] = v.y; o[2] = v.z; o[3] = v.w; }
 
-// One step of a butterfly: of M values a lane keeps the half that its bit names, summed
-// with its partner's.
-template <int M> __device__ __forceinline__ void halve(float* v, int lane, int bit) {
-    if (M > 1) {
-        const bool up = (lane & bit) != 0;
-#pragma unroll
-        for (int i = 0; i < M / 2; ++i) {
-            const float keep = up ? v[i + M / 2] : v[i], send = up ? v[i] : v[i + M / 2];
-            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, bit);
-        }
-    } else {
-        v[0] += __shfl_xor_sync(0xffffffffu, v[0], bit);
-    }
-}
-
 template <int S> __device__ __forceinline__ void load_states_row(f32x2 (&h)[S / 2], const float* p, int n0, int N, bool in) {
 #pragma unroll
     for (int i = 0; i < S / 2; ++i) {

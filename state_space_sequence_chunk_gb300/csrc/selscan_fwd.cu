@@ -2,14 +2,25 @@
 //
 // One warp walks 32 / LPC channels of a sequence (or of a range of it), a lane
 // holding S states of one channel in registers: with 16 states a lane is a
-// channel, so the sum over the states needs no other lane, and x, dt, z and y go
-// straight between its registers and memory (64 bytes a row and warp, whole
-// sectors).  Tiles of eight tokens: the next tile's loads are in flight while this
-// one is computed; its delta and u = delta x are made first, all eight side by
-// side, and the rows of B and C, which every lane reads, pass through shared
-// memory as fp32.  The recurrence itself is the packed fp32 instructions' work: per
-// pair of states two products, two multiply-adds and two exponentials.
+// channel, so the sum over the states needs no other lane.  Tiles of eight tokens
+// of x, dt and z come by cp.async, 16 bytes a lane, three tiles ahead (loaded into
+// registers one tile ahead, as in a first version, a warp by itself waited for
+// memory at every tile: 121 ns a token instead of 101); the rows of B and C, which
+// every lane reads, wait in registers and pass through shared memory as fp32.  A
+// tile's delta and u = delta x are made first, all eight side by side.  The
+// recurrence itself is the packed fp32 instructions' work: per pair of states two
+// products, two multiply-adds and two exponentials.
+//
+// What bounds it: for 16 states a token costs a warp 100 instructions, 91 clocks of
+// the multiply-add pipe and 81 of the exponential's, of which three warps a
+// quarter-SM (168 registers) keep some 60 % busy.  16384 tokens of 5120 channels in
+// 12 sequences: 421 us.  Eight states a lane, two lanes a channel (more warps, but
+// every row of B and C is read twice as often for the same work): 455 us, four
+// states: 594.  Making the next tile's delta between this one's tokens: 433.
+#include <type_traits>
+
 #include "selscan.cuh"
+#include "sm100_ptx.cuh"
 
 namespace ssd {
 namespace {
@@ -17,6 +28,7 @@ namespace {
 constexpr int kTok = 8;      // tokens of a tile
 constexpr int kWarps = 2;    // warps of a CTA, each on its own
 constexpr int kZeroItems = 64;
+constexpr int kStages = 4;   // tiles of x, dt and z in shared memory
 
 template <typename T> struct Raw4;                        // four states as loaded
 template <> struct Raw4<float> { float4 v; };
@@ -81,21 +93,29 @@ template <int S> __device__ __forceinline__ void store_row(const f32x2 (&h)[S / 
 // zero; or, from its last token to its first, what the range adds to the gradient q that
 // leaves it at its start: q <- exp(delta A) (q + gy C).
 template <typename T, int S, int LPC, int MODE>
-__global__ void __launch_bounds__(kWarps * 32) selscan_walk(const __grid_constant__ ScanParams p) {
-    constexpr int kCh = 32 / LPC, NP = S * LPC, kVec = kTok * NP / 4, kPer = (kVec + 31) / 32;
+__global__ void __launch_bounds__(kWarps * 32, S == 16 && LPC == 1 ? 6 : 1) selscan_walk(const __grid_constant__ ScanParams p) {
+    constexpr int kCh = 32 / LPC, NP = S * LPC, kVec = kTok * NP / 4, kPer = (kVec + 31) / 32, kOwn = kTok / LPC;
     constexpr bool kExact = sizeof(T) == 4, SUMS = MODE != kScanMain, REV = MODE == kScanRevSums;
-    __shared__ __align__(16) float sB[kWarps][2][kTok][NP];
-    __shared__ __align__(16) float sC[SUMS ? 1 : kWarps][2][kTok][NP];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    constexpr int kPieces = kTok * kCh * sizeof(T) / 16;    // 16-byte pieces of a tile of x, of dt and of z
+    constexpr int kRowPieces = kCh * sizeof(T) / 16, kCopies = (3 * kPieces + 31) / 32;
+    struct Warp {
+        T raw[kStages][3][kTok][kCh];
+        float B[2][kTok][NP];
+        float C[SUMS ? 1 : 2][kTok][NP];
+        float du[LPC > 1 ? 2 : 1][LPC > 1 ? kCh : 1][2 * kTok + 4];
+    };
+    extern __shared__ __align__(16) unsigned char smem[];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = lane % LPC;
     const int tpg = (p.cpg + kCh - 1) / kCh, tiles = tpg * p.G, ctas = (tiles + kWarps - 1) / kWarps;
     const int item = blockIdx.x / ctas, tile = (blockIdx.x - item * ctas) * kWarps + warp;
     if (tile >= tiles) return;
-    const int grp = tile / tpg, ch = (tile - grp * tpg) * kCh + lane / LPC;
+    Warp& w = reinterpret_cast<Warp*>(smem)[warp];
+    const int grp = tile / tpg, c0 = (tile - grp * tpg) * kCh, cl = lane / LPC, ch = c0 + cl;
     const bool in = ch < p.cpg;
-    const int d = grp * p.cpg + min(ch, p.cpg - 1), n0 = (lane % LPC) * S;
+    const int d = grp * p.cpg + min(ch, p.cpg - 1), n0 = part * S;
     if (!SUMS && item >= p.g.items) {            // rows of no sequence
         const int end = min(max(p.g.cu[p.g.nseq], 0), p.g.T);
-        if (in && lane % LPC == 0)
+        if (in && part == 0)
             for (int64_t t = end + (item - p.g.items); t < p.g.T; t += kZeroItems)
                 static_cast<T*>(p.y)[t * p.D + d] = from_f32<T>(0.f);
         return;
@@ -122,101 +142,200 @@ __global__ void __launch_bounds__(kWarps * 32) selscan_walk(const __grid_constan
     // backwards, gy = dout silu(z) takes x's place and C takes B's
     const int64_t row0 = REV ? it.t0 + it.len - 1 : it.t0, dir = REV ? -1 : 1;
     const int64_t xs = dir * (REV ? p.D : p.xs), ts = dir * p.dts, zs = dir * p.zs, Bs = dir * (REV ? p.Cs : p.Bs);
-    const T* xp = static_cast<const T*>(REV ? p.dout : p.x) + row0 * (REV ? p.D : p.xs) + d;
-    const T* tp = static_cast<const T*>(p.dt) + row0 * p.dts + d;
-    const bool gated = MODE != kScanSums && p.z != nullptr;
-    const T* zp = gated ? static_cast<const T*>(p.z) + row0 * p.zs + d : nullptr;
-    const T* Bp = static_cast<const T*>(REV ? p.C : p.B) + row0 * (REV ? p.Cs : p.Bs) + (int64_t)grp * p.N;
-    const T* Cp = static_cast<const T*>(p.C) + row0 * p.Cs + (int64_t)grp * p.N;
-    const bool vecB = (REV ? p.vecC : p.vecB) != 0;
-    T* yp = static_cast<T*>(p.y) + (int64_t)it.t0 * p.D + d;
-
-    T xr[kTok], tr[kTok], zr[kTok];
-    Raw4<T> br[kPer], cr[kPer];
-    auto prefetch = [&](int t0) {
+    const bool gated = MODE != kScanSums && p.z != nullptr, vecB = (REV ? p.vecC : p.vecB) != 0;
+    T* yp = static_cast<T*>(p.y) + (int64_t)it.t0 * p.D + (int64_t)part * p.D + d;
+    const int brow = lane / (NP / 4), bcol = lane % (NP / 4) * 4;     // its first vector of a tile's B (C)
+    const T* Bp = static_cast<const T*>(REV ? p.C : p.B) + row0 * (REV ? p.Cs : p.Bs) + brow * Bs + (int64_t)grp * p.N;
+    const T* Cp = static_cast<const T*>(p.C) + row0 * p.Cs + brow * p.Cs + (int64_t)grp * p.N;
+    // the lane's pieces of a tile of x, dt and z: where from, and how far the next tile is
+    const T* src[kCopies];
+    int64_t step[kCopies];
+    int crow[kCopies];                       // row in the tile, or behind all rows: nothing to copy
+    uint32_t dst[kCopies];
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int v = i * 32 + lane, t = t0 + v / (NP / 4), n = v % (NP / 4) * 4;
-            const bool ok = (kVec % 32 == 0 || v < kVec) && t < it.len;
-            fetch(br[i], Bp + t * Bs, ok ? n : p.N, p.N, vecB);
-            if (!SUMS) fetch(cr[i], Cp + t * p.Cs, ok ? n : p.N, p.N, p.vecC != 0);
-        }
+    for (int i = 0; i < kCopies; ++i) {
+        const int v = i * 32 + lane, k = v / kPieces, r = v % kPieces / kRowPieces, c = v % kRowPieces * (16 / (int)sizeof(T));
+        const int64_t stride = k == 0 ? xs : k == 1 ? ts : zs;
+        const T* from = static_cast<const T*>(k == 0 ? (REV ? p.dout : p.x) : k == 1 ? p.dt : p.z);
+        const int64_t first = row0 * (k == 0 ? (REV ? p.D : p.xs) : k == 1 ? p.dts : p.zs);
+        const bool ok = k < (gated ? 3 : 2) && c0 + c < p.cpg;
+        crow[i] = ok ? r : 1 << 30;
+        src[i] = ok ? from + first + r * stride + (int64_t)grp * p.cpg + c0 + c : static_cast<const T*>(p.x);
+        step[i] = ok ? kTok * stride : 0;
+        dst[i] = k < 3 ? smem_u32(&w.raw[0][0][0][0]) + 16 * v : 0u;
+    }
+    auto copy = [&](int t0, int stage) {     // the tile at t0; zeros behind the range's end
 #pragma unroll
-        for (int t = 0; t < kTok; ++t) {
-            const bool ok = t0 + t < it.len;
-            const T zero = from_f32<T>(0.f);
-            tr[t] = ok ? __ldg(tp + (t0 + t) * ts) : zero;
-            xr[t] = ok ? __ldg(xp + (t0 + t) * xs) : zero;
-            if (gated) zr[t] = ok ? __ldg(zp + (t0 + t) * zs) : zero;
+        for (int i = 0; i < kCopies; ++i) {
+            if ((i + 1) * 32 <= 3 * kPieces || i * 32 + lane < 3 * kPieces)
+                cp_async_16(dst[i] + stage * (int)sizeof(w.raw[0]), src[i], (int64_t)t0 + crow[i] < it.len ? 16u : 0u);
+            src[i] += step[i];
         }
     };
-    float total = 0.f;
-    prefetch(0);
-    for (int t0 = 0; t0 < it.len; t0 += kTok) {
-        const int buf = (t0 / kTok) & 1;
-        if (!SUMS && p.states != nullptr && (it.done + t0) % kScanChunk == 0)
-            store_row<S>(h, p.states + ((int64_t)(it.row0 + (it.done + t0) / kScanChunk) * p.D + d) * p.N, n0, p.N, in);
+    // B and C of the next tile wait in registers
+    Raw4<T> br[kPer], cr[kPer];
+    auto prefetch = [&](int t0) {
+        constexpr int kStep = 128 / NP;                               // rows from one vector to the next
+        static_assert(kPer == 1 || kPer * kStep == kTok, "a lane's vectors are a tile's");
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const bool ok = (kVec % 32 == 0 || lane < kVec) && t0 + brow + i * kStep < it.len;
+            fetch(br[i], Bp + i * kStep * Bs, ok ? bcol : p.N, p.N, vecB);
+            if (!SUMS) fetch(cr[i], Cp + i * kStep * p.Cs, ok ? bcol : p.N, p.N, p.vecC != 0);
+        }
+        Bp += kTok * Bs;
+        if (!SUMS) Cp += kTok * p.Cs;
+    };
+    f32x2 total = 0ull;
+    struct Own {
+        f32x2 x[kOwn / 2], gate[kOwn / 2];   // of its own tokens, in pairs
+        float2 du[LPC > 1 ? 1 : kTok];       // a lane with all of a channel: delta and u
+    };
+    // delta and u of the tile at t0 into shared memory, and B and C; rows behind the range's
+    // end multiply the state by 1 and add nothing (their x and dout are zeros)
+    auto prepare = [&](int t0, Own& o) {
+        const int at = t0 / kTok, buf = at & 1, stage = at % kStages;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             const int v = i * 32 + lane;
             if (kVec % 32 == 0 || v < kVec) {
-                *reinterpret_cast<float4*>(&sB[warp][buf][0][0] + 4 * v) = widen(br[i]);
-                if (!SUMS) *reinterpret_cast<float4*>(&sC[SUMS ? 0 : warp][buf][0][0] + 4 * v) = widen(cr[i]);
+                *reinterpret_cast<float4*>(&w.B[buf][0][0] + 4 * v) = widen(br[i]);
+                if (!SUMS) *reinterpret_cast<float4*>(&w.C[SUMS ? 0 : buf][0][0] + 4 * v) = widen(cr[i]);
             }
         }
-        __syncwarp();
-        float delta[kTok], u[kTok], x[kTok], gate[kTok];
+        auto raw2 = [&](int k, int i) {
+            return pair(to_f32(w.raw[stage][k][2 * i * LPC + part][cl]), to_f32(w.raw[stage][k][(2 * i + 1) * LPC + part][cl]));
+        };
+        f32x2 dl[kOwn / 2];
 #pragma unroll
-        for (int t = 0; t < kTok; ++t) {
-            const float v = to_f32(tr[t]) + bias;
-            // rows past the end multiply the state by 1 and add nothing
-            delta[t] = t0 + t < it.len ? (p.softplus ? softplus<kExact>(v) : v) : 0.f;
-            x[t] = to_f32(xr[t]);
-            if (gated) {
-                const float z = to_f32(zr[t]);
-                gate[t] = z * sigmoid(z);
-            }
-            if (REV) u[t] = t0 + t < it.len ? (gated ? x[t] * gate[t] : x[t]) : 0.f;
-            else u[t] = delta[t] * x[t];
-            if (SUMS) total += delta[t];
+        for (int i = 0; i < kOwn / 2; ++i) {
+            dl[i] = add2(raw2(1, i), both(bias));
+            o.x[i] = raw2(0, i);
         }
-        if (t0 + kTok < it.len) prefetch(t0 + kTok);
+        if (p.softplus)
+#pragma unroll
+            for (int i = 0; i < kOwn / 2; ++i) {
+                float a, b;
+                unpair(dl[i], a, b);
+                dl[i] = softplus2<kExact>(a, b);
+            }
+        if (MODE != kScanSums)
+#pragma unroll
+            for (int i = 0; i < kOwn / 2; ++i) o.gate[i] = both(1.f);
+        if (gated)
+#pragma unroll
+            for (int i = 0; i < kOwn / 2; ++i) o.gate[i] = silu2(raw2(2, i));
+        float* row = &w.du[LPC > 1 ? buf : 0][LPC > 1 ? cl : 0][0];
+#pragma unroll
+        for (int i = 0; i < kOwn / 2; ++i) {
+            const int t = t0 + 2 * i * LPC + part;
+            float a, b, c, e;
+            unpair(dl[i], a, b);
+            dl[i] = pair(t < it.len ? a : 0.f, t + LPC < it.len ? b : 0.f);
+            if (SUMS) total = add2(total, dl[i]);
+            unpair(dl[i], a, b);
+            unpair(REV ? mul2(o.x[i], o.gate[i]) : mul2(dl[i], o.x[i]), c, e);
+            if (LPC > 1) {                   // the channel's other lanes need them too
+                *reinterpret_cast<float2*>(row + 2 * (2 * i * LPC + part)) = make_float2(a, c);
+                *reinterpret_cast<float2*>(row + 2 * ((2 * i + 1) * LPC + part)) = make_float2(b, e);
+            } else {
+                o.du[(2 * i) % (LPC > 1 ? 1 : kTok)] = make_float2(a, c);
+                o.du[(2 * i + 1) % (LPC > 1 ? 1 : kTok)] = make_float2(b, e);
+            }
+        }
+    };
+    auto tokens = [&](int t0, const Own& o, auto full) {
+        constexpr bool kFull = decltype(full)::value;
+        const int buf = (t0 / kTok) & 1;
+        auto token = [&](int t, f32x2& delta, f32x2& u) {                  // each twice, for pairs of states
+            const float2 v = LPC > 1 ? *reinterpret_cast<const float2*>(&w.du[LPC > 1 ? buf : 0][LPC > 1 ? cl : 0][2 * t])
+                                     : o.du[t % (LPC > 1 ? 1 : kTok)];
+            delta = both(v.x);
+            u = both(v.y);
+        };
+        // the next token's decays are made while this one's are used
+        f32x2 a[S / 2], dn, u, un;
+        float y[LPC];
+        token(0, dn, un);
+#pragma unroll
+        for (int i = 0; i < S / 2; ++i) a[i] = ex2_2(mul2(dn, a2[i]));
 #pragma unroll
         for (int t = 0; t < kTok; ++t) {
-            const f32x2 dd = pair(delta[t], delta[t]), uu = pair(u[t], u[t]);
-            f32x2 y0 = pair(0.f, 0.f), y1 = y0;
+            u = un;
+            if (t + 1 < kTok) token(t + 1, dn, un);
+            f32x2 y0 = 0ull, y1 = 0ull;
 #pragma unroll
             for (int i = 0; i < S / 4; ++i) {
-                const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(&sB[warp][buf][t][n0 + 4 * i]);
-                const f32x2 a0 = ex2_2(mul2(dd, a2[2 * i])), a1 = ex2_2(mul2(dd, a2[2 * i + 1]));
-                if (REV) {
-                    h[2 * i] = mul2(a0, fma2(uu, b.x, h[2 * i]));
-                    h[2 * i + 1] = mul2(a1, fma2(uu, b.y, h[2 * i + 1]));
-                } else {
-                    h[2 * i] = fma2(a0, h[2 * i], mul2(uu, b.x));
-                    h[2 * i + 1] = fma2(a1, h[2 * i + 1], mul2(uu, b.y));
+                const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(&w.B[buf][t][n0 + 4 * i]);
+                f32x2 an0 = 0ull, an1 = 0ull;
+                if (t + 1 < kTok) {
+                    an0 = ex2_2(mul2(dn, a2[2 * i]));
+                    an1 = ex2_2(mul2(dn, a2[2 * i + 1]));
                 }
+                if (REV) {
+                    h[2 * i] = mul2(a[2 * i], fma2(u, b.x, h[2 * i]));
+                    h[2 * i + 1] = mul2(a[2 * i + 1], fma2(u, b.y, h[2 * i + 1]));
+                } else {
+                    h[2 * i] = fma2(a[2 * i], h[2 * i], mul2(u, b.x));
+                    h[2 * i + 1] = fma2(a[2 * i + 1], h[2 * i + 1], mul2(u, b.y));
+                }
+                a[2 * i] = an0;
+                a[2 * i + 1] = an1;
                 if (!SUMS) {
-                    const ulonglong2 c = *reinterpret_cast<const ulonglong2*>(&sC[SUMS ? 0 : warp][buf][t][n0 + 4 * i]);
-                    y0 = fma2(c.x, h[2 * i], y0);
-                    y1 = fma2(c.y, h[2 * i + 1], y1);
+                    const ulonglong2 c = *reinterpret_cast<const ulonglong2*>(&w.C[SUMS ? 0 : buf][t][n0 + 4 * i]);
+                    y0 = i == 0 ? mul2(c.x, h[0]) : fma2(c.x, h[2 * i], y0);
+                    y1 = i == 0 ? mul2(c.y, h[1]) : fma2(c.y, h[2 * i + 1], y1);
                 }
             }
             if (!SUMS) {
                 float lo, hi;
                 unpair(add2(y0, y1), lo, hi);
-                float y = lo + hi;
-#pragma unroll
-                for (int off = LPC / 2; off > 0; off >>= 1) y += __shfl_xor_sync(0xffffffffu, y, off);
-                y = fmaf(skip, x[t], y);
-                if (gated) y *= gate[t];
-                if (in && lane % LPC == 0 && t0 + t < it.len) yp[(int64_t)(t0 + t) * p.D] = from_f32<T>(y);
+                y[t % LPC] = lo + hi;
+                if (t % LPC == LPC - 1) {          // of the last LPC tokens a lane gets its own one's sum
+                    if (LPC >= 4) halve<LPC>(y, lane, LPC / 2);
+                    if (LPC >= 2) halve<2>(y, lane, 1);
+                    const int i = t / LPC;
+                    float x0, x1, g0, g1;
+                    unpair(o.x[i / 2], x0, x1);
+                    unpair(o.gate[i / 2], g0, g1);
+                    const float v = fmaf(skip, i & 1 ? x1 : x0, y[0]) * (i & 1 ? g1 : g0);
+                    if (in && (kFull || t0 + i * LPC + part < it.len)) *yp = from_f32<T>(v);
+                    yp += (int64_t)LPC * p.D;
+                }
             }
         }
+    };
+#pragma unroll
+    for (int i = 0; i + 1 < kStages; ++i) {
+        copy(i * kTok, i);
+        cp_async_commit();
     }
+    prefetch(0);
+    auto step_of = [&](int t0, auto full) {
+        cp_async_wait_group<kStages - 2>();
+        __syncwarp();                        // the tile's rows are there; the tile before it is done
+        copy(t0 + (kStages - 1) * kTok, (t0 / kTok + kStages - 1) % kStages);
+        cp_async_commit();
+        if (!SUMS && p.states != nullptr && (it.done + t0) % kScanChunk == 0)
+            store_row<S>(h, p.states + ((int64_t)(it.row0 + (it.done + t0) / kScanChunk) * p.D + d) * p.N, n0, p.N, in);
+        Own own;
+        prepare(t0, own);
+        prefetch(t0 + kTok);
+        __syncwarp();
+        tokens(t0, own, full);
+    };
+    int t0 = 0;
+    for (; t0 + kTok <= it.len; t0 += kTok) step_of(t0, std::true_type());
+    if (t0 < it.len) step_of(t0, std::false_type());
+    cp_async_wait_group<0>();
     if (SUMS) {
         store_row<S>(h, p.agg + ((int64_t)item * p.D + d) * p.N, n0, p.N, in);
-        if (in && lane % LPC == 0) p.aggd[(int64_t)item * p.D + d] = total;
+        float sum, odd;
+        unpair(total, sum, odd);
+        sum += odd;
+#pragma unroll
+        for (int bit = LPC / 2; bit > 0; bit /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, bit);
+        if (in && part == 0) p.aggd[(int64_t)item * p.D + d] = sum;
     } else if (p.fin != nullptr && it.last) {
         store_row<S>(h, p.fin + row, n0, p.N, in);
     }
@@ -265,7 +384,15 @@ cudaError_t go(const ScanParams& p, ScanMode mode, cudaStream_t stream) {
     if (items == 0) return cudaSuccess;
     auto k = mode == kScanMain ? selscan_walk<T, S, LPC, kScanMain>
            : mode == kScanSums ? selscan_walk<T, S, LPC, kScanSums> : selscan_walk<T, S, LPC, kScanRevSums>;
-    k<<<(unsigned)(items * ctas), kWarps * 32, 0, stream>>>(p);
+    constexpr int NP = S * LPC, kCh = 32 / LPC;
+    // (shared memory of a warp as the kernel lays it out)
+    const int bytes = kWarps * (kStages * 3 * kTok * kCh * (int)sizeof(T) + (mode == kScanMain ? 4 : 3) * kTok * NP * 4 +
+                                (LPC > 1 ? 2 * kCh : 1) * (2 * kTok + 4) * 4);
+    if (bytes > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e != cudaSuccess) return e;
+    }
+    k<<<(unsigned)(items * ctas), kWarps * 32, bytes, stream>>>(p);
     return cudaGetLastError();
 }
 
