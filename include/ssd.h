@@ -514,7 +514,7 @@ typedef struct {
 } ssd_selscan_dims;
 
 /* Tokens between two of the states that ssd_selscan_fwd leaves for ssd_selscan_bwd. */
-#define SSD_SELSCAN_CHUNK 32
+#define SSD_SELSCAN_CHUNK 16
 
 /* Bytes of device workspace of ssd_selscan_fwd (backward = 0) or ssd_selscan_bwd
  * (backward != 0); 0 if none is needed or `d` is invalid. */
@@ -534,9 +534,9 @@ size_t ssd_selscan_workspace_bytes(const ssd_selscan_dims* d, int backward);
  *   y            output [tokens, dim].
  *   final_state  output [nseqs, dim, dstate] fp32, or NULL to skip; it may be
  *                init_state itself.  A sequence of no tokens passes its state on.
- *   states       output [tokens / 32 + nseqs, dim, dstate] fp32, or NULL to skip: the
- *                state before each 32nd token of each sequence, sequence s's from row
- *                cu_seqlens[s] / 32 + s on; for ssd_selscan_bwd.
+ *   states       output [tokens / 16 + nseqs, dim, dstate] fp32, or NULL to skip: the
+ *                state before each 16th token of each sequence, sequence s's from row
+ *                cu_seqlens[s] / 16 + s on; for ssd_selscan_bwd.
  * fp32 states and sums, one rounding of y.  What other sequences' rows hold never
  * reaches a sequence's results.  The result does not depend on the order in which the
  * GPU runs the work.

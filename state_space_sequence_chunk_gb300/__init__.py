@@ -54,7 +54,7 @@ EXPORTS = ["ssd_abi_version", "ssd_status_string", "ssd_fwd_workspace_bytes",
            "ssd_selscan_workspace_bytes", "ssd_selscan_fwd", "ssd_selscan_bwd", "ssd_selscan_step"]
 GATES = {None: 0, "silu": 1, "sigmoid": 2}
 ACTIVATIONS = {None: 0, "silu": 1}
-SELSCAN_CHUNK = 32
+SELSCAN_CHUNK = 16
 
 
 class SSDError(RuntimeError):

@@ -222,6 +222,28 @@ template <> __device__ __forceinline__ float4 load_states(const __nv_bfloat16* p
     return make_float4(n < N ? to_f32(p[n]) : 0.f, n + 1 < N ? to_f32(p[n + 1]) : 0.f,
                        n + 2 < N ? to_f32(p[n + 2]) : 0.f, n + 3 < N ? to_f32(p[n + 3]) : 0.f);
 }
+template <typename T> struct Raw4;                        // four states as loaded
+template <> struct Raw4<float> { float4 v; };
+template <> struct Raw4<__nv_bfloat16> { uint2 v; };
+__device__ __forceinline__ void fetch(Raw4<float>& r, const float* p, int n, int N, bool vec) {
+    r.v = load_states(p, n, N, vec);
+}
+__device__ __forceinline__ void fetch(Raw4<__nv_bfloat16>& r, const __nv_bfloat16* p, int n, int N, bool vec) {
+    if (vec) {
+        r.v = n < N ? __ldg(reinterpret_cast<const uint2*>(p + n)) : make_uint2(0u, 0u);
+    } else {
+        const unsigned short* q = reinterpret_cast<const unsigned short*>(p);
+        uint32_t e[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) e[i] = n + i < N ? (uint32_t)__ldg(q + n + i) : 0u;
+        r.v = make_uint2(e[0] | e[1] << 16, e[2] | e[3] << 16);
+    }
+}
+__device__ __forceinline__ float4 widen(const Raw4<float>& r) { return r.v; }
+__device__ __forceinline__ float4 widen(const Raw4<__nv_bfloat16>& r) {
+    return make_float4(__uint_as_float(r.v.x << 16), __uint_as_float(r.v.x & 0xFFFF0000u),
+                       __uint_as_float(r.v.y << 16), __uint_as_float(r.v.y & 0xFFFF0000u));
+}
 #endif
 
 // Launchers.  kScanSums: the ranges' own ends into agg and aggd; kScanRevSums: the same

@@ -4,58 +4,106 @@
 //     r = q + gy C;  u = sum_n r B;  w = r a h_{t-1};  q = a r          (a = exp(delta A))
 //     dx = delta u + D gy    ddelta = x u + sum_n A w    dA += delta w
 //     dB = sum over channels of delta x r                dC = sum over channels of gy h
-// A range of a sequence is walked backwards in chunks of 32 tokens, from the states that
+// A range of a sequence is walked backwards in chunks of 16 tokens, from the states that
 // the forward pass stored.  In a chunk the states are made forwards once and kept every
 // K tokens (in shared memory); then, slab of K tokens by slab from the last one, the
 // decays a and the products a h_{t-1} are made again and kept in registers while the
-// slab is walked backwards.
+// slab is walked backwards.  A chunk's rows of x, dt, dout and z and its stored state
+// come by cp.async while the chunk behind it is computed.
 //
-// A lane holds C channels x S states and a warp 8 C channels x 4 S states, because two
-// sums cross lanes: over the states (4 lanes) for dx, ddelta and y, and over the
-// channels (8 lanes, then the CTA's warps, then a kernel of its own over the tiles) for
-// dB and dC.  Each is a butterfly that halves the values with every step, so that a
-// token costs 2 S - 1 shuffles and 3 C / 2 more.
+// A lane holds C channels x S states and a warp 8 C channels x 4 S states.  Two sums
+// cross lanes.  Over the states (the 4 lanes of a row, for dx, ddelta and y): a product of
+// the tensor cores, rows x lanes by lanes x tokens, whose second operand is 1 in the
+// token's column, so that eight tokens' sums lie ready in eight columns.  dt_bias's
+// gradient is summed in fp32 from them, so u and sum A w go in two terms of 11 bits;
+// y, which only dz (in the operands' type) needs, in one where that type is bf16.  Over the
+// channels (the 8 rows, then the CTA's warps, then a kernel of its own over the tiles; for
+// dB and dC): in bf16 a first product moves the values, state by channel, so that the
+// channels lie in the 4 lanes, and a second one sums them (each rounds its terms to 11
+// bits towards 0, a quarter of what rounding the result to bf16 loses at most); in fp32 by
+// shuffles.
+//
+// What bounds it: a token takes a warp of 16 channels and 16 states some 200
+// instructions, 64 of them packed multiply-adds, and the registers (224 to 255) leave
+// two warps a quarter-SM, which issue in every second clock.  8192 tokens of 2048
+// channels in 6 sequences: 470 us a call, 685 without the cut into ranges.  Sums by
+// shuffles and rows loaded where they are used: 617; pairs of channels instead of
+// states, or delta and u stored in pairs: 539, 509 (more moves for the tensor cores'
+// operands, more shared memory traffic); slabs of 2 tokens and three warps a quarter-SM: 485,
+// of 8 tokens: 646.
 #include <type_traits>
 
 #include "selscan.cuh"
+#include "sm100_ptx.cuh"
 
 namespace ssd {
 namespace {
 
 constexpr int kChunk = kScanChunk;
 
-template <int S> struct Plan {                 // N <= 4 S
+template <typename T, int S> struct Plan {     // N <= 4 S
     static constexpr int C = S <= 4 ? 2 : 1;   // channels a lane
-    static constexpr int K = S <= 8 ? 8 : 4;   // tokens of a slab
+    static constexpr int K = S <= 8 ? 4 : 2;   // tokens of a slab
     static constexpr int kWarps = S <= 8 ? 4 : 2;
     static constexpr int kCh = 8 * C;          // channels of a warp
     static constexpr int NP = 4 * S;
     static constexpr int kSlabs = kChunk / K;
-    // shared memory, in floats
-    static constexpr int kBC = 2 * kChunk * NP;                  // B and C, for all warps
-    static constexpr int kDu = kChunk * kCh * 2;                 // (delta, u) of each token and channel
-    static constexpr int kGy = kChunk * kCh;
-    static constexpr int kStart = (kSlabs - 1) * C * S * 32;     // the state before each slab but the first
-    static constexpr int kDbc = kChunk * 2 * NP;                 // the warp's terms of dB and dC
-    static constexpr int kRed = 3 * K * kCh;                     // u, sum A w and C.h of a slab
-    static constexpr int kWarp = kDu + kGy + kStart + kDbc + kRed;
-    static constexpr int kBytes = (kBC + kWarps * kWarp) * 4;
+    static constexpr int kTiles = (S + 3) / 4; // tiles of 16 states in the sums over channels
+    struct Warp {                              // shared memory of a warp
+        T raw[2][4][kChunk][kCh];              // x, dt, dout and z of a chunk and the next
+        float check[2][C * S * 32];            // the stored states, as the lanes hold them
+        float start[kSlabs - 1][C * S * 32];   // the state before each slab but the first
+        // (rows padded so that lanes that write different rows meet different banks)
+        float du[kChunk][2 * kCh + 8];         // delta and u = delta x of each channel
+        float gy[kChunk][kCh + 8];
+        float dbc[kChunk][2 * NP + 4];         // the warp's terms of dB and dC
+    };
+    struct Cta {
+        float bc[2][kChunk][NP];               // B and C
+        Warp w[kWarps];
+    };
 };
 
-// Four channels of a row.
-__device__ __forceinline__ float4 load4(const float* p) { return __ldg(reinterpret_cast<const float4*>(p)); }
-__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
-    const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
-    return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u),
-                       __uint_as_float(v.y << 16), __uint_as_float(v.y & 0xFFFF0000u));
+// Products of 16 x 4 (16 x 8) and 4 x 8 (8 x 8) numbers whose low 13 bits are not looked at.
+__device__ __forceinline__ void mma4(float (&c)[4], float a0, float a1, float b) {
+    asm("mma.sync.aligned.m16n8k4.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5}, {%6}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(__float_as_uint(a0)), "r"(__float_as_uint(a1)), "r"(__float_as_uint(b)));
 }
-__device__ __forceinline__ void store4(float* p, const float (&v)[4]) {
-    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+__device__ __forceinline__ void mma8(float (&c)[4], const float (&a)[4], float b0, float b1) {
+    asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(__float_as_uint(a[0])), "r"(__float_as_uint(a[1])), "r"(__float_as_uint(a[2])), "r"(__float_as_uint(a[3])),
+          "r"(__float_as_uint(b0)), "r"(__float_as_uint(b1)));
 }
-__device__ __forceinline__ void store4(__nv_bfloat16* p, const float (&v)[4]) {
-    *reinterpret_cast<uint2*>(p) = make_uint2(pack2(v[0], v[1]), pack2(v[2], v[3]));
+// Adds to column `col` of c the sums of v0 (rows 0 .. 7) and v1 (8 .. 15) over the four lanes
+// of a row; hot is 1 in the lanes whose row number is col, else 0.  EXACT: in two terms, so
+// that 22 bits of v count.
+template <bool EXACT> __device__ __forceinline__ void add_rows(float (&c)[4], float v0, float v1, float hot) {
+    mma4(c, v0, v1, hot);
+    if (EXACT) {
+        const float h0 = __uint_as_float(__float_as_uint(v0) & 0xFFFFE000u), h1 = __uint_as_float(__float_as_uint(v1) & 0xFFFFE000u);
+        mma4(c, v0 - h0, v1 - h1, hot);
+    }
 }
-__device__ __forceinline__ void spread(float4 v, float (&o)[4]) { o[0] = v.x; o[1] = v.y; o[2] = v.z; o[3] = v.w; }
+
+// Four channels of a row, zeros.
+__device__ __forceinline__ void zero4(float* p) { *reinterpret_cast<float4*>(p) = make_float4(0.f, 0.f, 0.f, 0.f); }
+__device__ __forceinline__ void zero4(__nv_bfloat16* p) { *reinterpret_cast<uint2*>(p) = make_uint2(0u, 0u); }
+// Two channels of a row.
+__device__ __forceinline__ f32x2 load2(const float* p) { return *reinterpret_cast<const unsigned long long*>(p); }
+__device__ __forceinline__ f32x2 load2(const __nv_bfloat16* p) {
+    const uint32_t v = *reinterpret_cast<const uint32_t*>(p);
+    return pair(v << 16, v & 0xFFFF0000u);
+}
+__device__ __forceinline__ void store2(float* p, f32x2 v) { *reinterpret_cast<f32x2*>(p) = v; }
+__device__ __forceinline__ void store2(__nv_bfloat16* p, f32x2 v) { *reinterpret_cast<uint32_t*>(p) = pack2(v); }
+__device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src, uint32_t bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_8(uint32_t dst, const void* src, uint32_t bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
 
 template <int S> __device__ __forceinline__ void load_states_row(f32x2 (&h)[S / 2], const float* p, int n0, int N, bool in) {
 #pragma unroll
@@ -97,19 +145,14 @@ template <int S> __device__ __forceinline__ void lds(f32x2 (&v)[S / 2], const fl
 }
 
 template <typename T, int S>
-__global__ void __launch_bounds__(Plan<S>::kWarps * 32) selscan_bwd(const __grid_constant__ ScanParams p) {
-    using P = Plan<S>;
-    constexpr int C = P::C, K = P::K, kCh = P::kCh, NP = P::NP, H = S / 2;
+__global__ void __launch_bounds__(Plan<T, S>::kWarps * 32, S <= 4 ? 2 : 1) selscan_bwd(const __grid_constant__ ScanParams p) {
+    using P = Plan<T, S>;
+    constexpr int C = P::C, K = P::K, kCh = P::kCh, NP = P::NP, H = S / 2, kThreads = P::kWarps * 32;
     constexpr bool kExact = sizeof(T) == 4;
-    extern __shared__ __align__(16) float smem[];
+    extern __shared__ __align__(16) unsigned char smem[];
+    typename P::Cta& sh = *reinterpret_cast<typename P::Cta*>(smem);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q4 = lane & 3;
-    float* sB = smem;                                  // [kChunk][NP]
-    float* sC = sB + kChunk * NP;
-    float* sDu = smem + P::kBC + warp * P::kWarp;      // [kChunk][kCh][2]
-    float* sGy = sDu + P::kDu;                         // [kChunk][kCh]
-    float* sStart = sGy + P::kGy;                      // [slab - 1][C S][32]
-    float* sDbc = sStart + P::kStart;                  // [kChunk][2][NP]
-    float* sRed = sDbc + P::kDbc;                      // u, v, y: [K][kCh] each
+    typename P::Warp& w = sh.w[warp];
 
     constexpr int kTile = P::kWarps * kCh;
     const int tpg = (p.cpg + kTile - 1) / kTile, tiles = tpg * p.G;
@@ -117,51 +160,45 @@ __global__ void __launch_bounds__(Plan<S>::kWarps * 32) selscan_bwd(const __grid
     const int grp = tile / tpg, tg = tile - grp * tpg;
     const int c0 = tg * kTile + warp * kCh;            // the warp's first channel in the group
     const int n0 = q4 * S;
-    // element-wise work: a quad of channels of one row a lane
-    constexpr int kQuads = kCh / 4, kRows = 32 / kQuads;
-    const int er = lane / kQuads, ec = lane % kQuads * 4;
-    const bool ein = c0 + ec < p.cpg;
-    const int64_t ed = (int64_t)grp * p.cpg + c0 + ec;
-
     if (slot >= p.slots) {                             // rows of no sequence
-        const int end = min(max(p.g.cu[p.g.nseq], 0), p.g.T), step = gridDim.x / tiles - p.slots;
-        const float zero[4] = {0.f, 0.f, 0.f, 0.f};
-        if (ein)
-            for (int64_t t = end + (int64_t)(slot - p.slots) * kRows + er; t < p.g.T; t += (int64_t)step * kRows) {
-                store4(static_cast<T*>(p.dx) + t * p.D + ed, zero);
-                store4(static_cast<T*>(p.ddt) + t * p.D + ed, zero);
-                if (p.z != nullptr) store4(static_cast<T*>(p.dz) + t * p.D + ed, zero);
+        constexpr int kQuads = kCh / 4, kRows = 32 / kQuads;
+        const int end = min(max(p.g.cu[p.g.nseq], 0), p.g.T), step = gridDim.x / tiles - p.slots, ch = c0 + lane % kQuads * 4;
+        if (ch < p.cpg)
+            for (int64_t t = end + (int64_t)(slot - p.slots) * kRows + lane / kQuads; t < p.g.T; t += (int64_t)step * kRows) {
+                const int64_t at = t * p.D + (int64_t)grp * p.cpg + ch;
+                zero4(static_cast<T*>(p.dx) + at);
+                zero4(static_cast<T*>(p.ddt) + at);
+                if (p.z != nullptr) zero4(static_cast<T*>(p.dz) + at);
             }
         return;
     }
-    int64_t dch[C];
-    bool in[C];
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-        in[c] = c0 + g * C + c < p.cpg;
-        dch[c] = (int64_t)grp * p.cpg + c0 + g * C + c;
-    }
+    // A lane's channels are all in the group or none (groups and C are even).
+    const bool in = c0 + g * C < p.cpg;
+    const int64_t dch = (int64_t)grp * p.cpg + (in ? c0 + g * C : 0);
     f32x2 dA[C][H], qv[C][H], a2[C][H];
-#pragma unroll
-    for (int c = 0; c < C; ++c)
-#pragma unroll
-        for (int i = 0; i < H; ++i) dA[c][i] = 0ull;
-    float dD[4] = {0.f, 0.f, 0.f, 0.f}, db[4] = {0.f, 0.f, 0.f, 0.f};
-    float bias[4] = {0.f, 0.f, 0.f, 0.f}, skip[4] = {0.f, 0.f, 0.f, 0.f};
-    if (ein) {
-        if (p.bias != nullptr) spread(load4(p.bias + ed), bias);
-        if (p.Dk != nullptr) spread(load4(p.Dk + ed), skip);
-    }
+    float dD[C], db[C], bias[C], skip[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-        load_states_row<S>(a2[c], p.A + dch[c] * p.N, n0, p.N, in[c]);
+        load_states_row<S>(a2[c], p.A + (dch + c) * p.N, n0, p.N, in);
 #pragma unroll
         for (int i = 0; i < H; ++i) {
             float a, b;
             unpair(a2[c][i], a, b);
             a2[c][i] = pair(scan_rate(a), scan_rate(b));
+            dA[c][i] = 0ull;
         }
+        dD[c] = db[c] = 0.f;
+        bias[c] = p.bias != nullptr ? p.bias[dch + c] : 0.f;
+        skip[c] = p.Dk != nullptr ? p.Dk[dch + c] : 0.f;
     }
+    // the rows that a lane's values go to in the sums over channels: value s of lane (g, q) to
+    // row 4 q + s % 4 of its tile
+    float pick[2][4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            pick[i][j] = (g & 3) == 2 * i + j / 2 && q4 == (g >> 2) + 2 * (j & 1) ? 1.f : 0.f;
     const bool cut = p.g.R <= p.g.T, gated = p.z != nullptr;
     for (int item = slot * p.per_slot; item < min((slot + 1) * p.per_slot, p.g.items); ++item) {
         ScanItem it;
@@ -171,82 +208,134 @@ __global__ void __launch_bounds__(Plan<S>::kWarps * 32) selscan_bwd(const __grid
 #pragma unroll
             for (int i = 0; i < H; ++i) qv[c][i] = 0ull;
             if (cut && !(it.first && it.last))
-                load_states_row<S>(qv[c], p.agg + ((int64_t)item * p.D + dch[c]) * p.N, n0, p.N, in[c]);
+                load_states_row<S>(qv[c], p.agg + ((int64_t)item * p.D + dch + c) * p.N, n0, p.N, in);
             else if (p.dfin != nullptr)
-                load_states_row<S>(qv[c], p.dfin + ((int64_t)it.seq * p.D + dch[c]) * p.N, n0, p.N, in[c]);
+                load_states_row<S>(qv[c], p.dfin + ((int64_t)it.seq * p.D + dch + c) * p.N, n0, p.N, in);
         }
-        const T* x = static_cast<const T*>(p.x) + it.t0 * p.xs + ed;
-        const T* dt = static_cast<const T*>(p.dt) + it.t0 * p.dts + ed;
-        const T* z = static_cast<const T*>(p.z) + it.t0 * p.zs + ed;
-        const T* dout = static_cast<const T*>(p.dout) + (int64_t)it.t0 * p.D + ed;
-        for (int chunk = (it.len - 1) / kChunk; chunk >= 0 && it.len > 0; --chunk) {
-            const int t0 = chunk * kChunk, nt = min(kChunk, it.len - t0);
-            // B and C of the chunk, 0 behind the range's end
-            for (int i = threadIdx.x; i < kChunk * NP / 4; i += P::kWarps * 32) {
-                const int t = i / (NP / 4), n = i % (NP / 4) * 4;
-                const int64_t row = (int64_t)it.t0 + t0 + t;
-                const int from = t < nt ? n : p.N;
-                *reinterpret_cast<float4*>(sB + 4 * i) =
-                    load_states(static_cast<const T*>(p.B) + row * p.Bs + (int64_t)grp * p.N, from, p.N, p.vecB != 0);
-                *reinterpret_cast<float4*>(sC + 4 * i) =
-                    load_states(static_cast<const T*>(p.C) + row * p.Cs + (int64_t)grp * p.N, from, p.N, p.vecC != 0);
-            }
-            for (int r0 = 0; r0 < kChunk; r0 += kRows) {
-                const int t = r0 + er;
-                float du[8], gy[4];
-                if (ein && t < nt) {
-                    float xv[4], tv[4], gv[4], zv[4];
-                    spread(load4(x + (int64_t)(t0 + t) * p.xs), xv);
-                    spread(load4(dt + (int64_t)(t0 + t) * p.dts), tv);
-                    spread(load4(dout + (int64_t)(t0 + t) * p.D), gv);
-                    if (gated) spread(load4(z + (int64_t)(t0 + t) * p.zs), zv);
+        // A chunk's rows of x, dt, dout and z and its stored state, zeros behind the range's end.
+        auto copy = [&](int chunk, int buf) {
+            const int nt = min(kChunk, it.len - chunk * kChunk);
+            const int64_t row0 = it.t0 + (int64_t)chunk * kChunk;
+            constexpr int kPieces = kCh * (int)sizeof(T), kRow = kPieces / kChunk;     // 16-byte pieces: all, of a row
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float v = tv[i] + bias[i], delta = p.softplus ? softplus<kExact>(v) : v;
-                        du[2 * i] = delta;
-                        du[2 * i + 1] = delta * xv[i];
-                        gy[i] = gated ? gv[i] * zv[i] * sigmoid(zv[i]) : gv[i];
-                    }
-                } else {
+            for (int k = 0; k < 4; ++k) {
+                const T* base = static_cast<const T*>(k == 0 ? p.x : k == 1 ? p.dt : k == 2 ? p.dout : p.z);
+                const int64_t stride = k == 0 ? p.xs : k == 1 ? p.dts : k == 2 ? p.D : p.zs;
+                if (k == 3 && !gated) break;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) du[2 * i] = du[2 * i + 1] = gy[i] = 0.f;
+                for (int v = 0; v < kPieces; v += 32) {
+                    const int r = (v + lane) / kRow, c = (v + lane) % kRow * (16 / (int)sizeof(T));
+                    const bool ok = r < nt && c0 + c < p.cpg;
+                    const T* from = ok ? base + (row0 + r) * stride + (int64_t)grp * p.cpg + c0 + c : base;
+                    if (v + 32 <= kPieces || v + lane < kPieces)
+                        cp_async_16(smem_u32(&w.raw[buf][k][0][0]) + 16 * (v + lane), from, ok ? 16u : 0u);
                 }
-                *reinterpret_cast<float4*>(sDu + (t * kCh + ec) * 2) = make_float4(du[0], du[1], du[2], du[3]);
-                *reinterpret_cast<float4*>(sDu + (t * kCh + ec) * 2 + 4) = make_float4(du[4], du[5], du[6], du[7]);
-                *reinterpret_cast<float4*>(sGy + t * kCh + ec) = make_float4(gy[0], gy[1], gy[2], gy[3]);
+            }
+            const float* st = p.states + ((it.row0 + it.done / kChunk + chunk) * (int64_t)p.D + dch) * p.N;
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+#pragma unroll
+                for (int i = 0; i < H; ++i) {
+                    const int n = n0 + 2 * i;
+                    const float* from = st + (int64_t)c * p.N + n;
+                    const uint32_t to = smem_u32(&w.check[buf][(c * H + i) * 64 + lane * 2]);
+                    if (p.N % 2 == 0) {
+                        cp_async_8(to, in && n < p.N ? from : p.states, in && n < p.N ? 8u : 0u);
+                    } else {
+                        cp_async_4(to, in && n < p.N ? from : p.states, in && n < p.N ? 4u : 0u);
+                        cp_async_4(to + 4, in && n + 1 < p.N ? from + 1 : p.states, in && n + 1 < p.N ? 4u : 0u);
+                    }
+                }
+        };
+        // B's and C's rows of the next chunk wait in registers.
+        constexpr int kVec = kChunk * NP / 4, kPer = (2 * kVec + kThreads - 1) / kThreads;
+        Raw4<T> bc[kPer];
+        auto prefetch = [&](int chunk) {
+            const int nt = min(kChunk, it.len - chunk * kChunk);
+            const int64_t row0 = it.t0 + (int64_t)chunk * kChunk;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                const int v = i * kThreads + threadIdx.x, m = v % kVec, t = m / (NP / 4), n = m % (NP / 4) * 4;
+                const bool ok = v < 2 * kVec && t < nt;
+                if (v < kVec) fetch(bc[i], static_cast<const T*>(p.B) + (row0 + t) * p.Bs + (int64_t)grp * p.N, ok ? n : p.N, p.N, p.vecB != 0);
+                else fetch(bc[i], static_cast<const T*>(p.C) + (row0 + t) * p.Cs + (int64_t)grp * p.N, ok ? n : p.N, p.N, p.vecC != 0);
+            }
+        };
+        const int chunks = (it.len + kChunk - 1) / kChunk;
+        if (chunks > 0) {
+            copy(chunks - 1, 0);
+            prefetch(chunks - 1);
+        }
+        cp_async_commit();
+        for (int chunk = chunks - 1, buf = 0; chunk >= 0; --chunk, buf ^= 1) {
+            const int t0 = chunk * kChunk, nt = min(kChunk, it.len - t0);
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                const int v = i * kThreads + threadIdx.x;
+                if (2 * kVec % kThreads == 0 || v < 2 * kVec) *reinterpret_cast<float4*>(&sh.bc[0][0][0] + 4 * v) = widen(bc[i]);
+            }
+            cp_async_wait_group<0>();
+            __syncwarp();
+            if (chunk > 0) {
+                copy(chunk - 1, buf ^ 1);
+                prefetch(chunk - 1);
+            }
+            cp_async_commit();
+            auto raw = [&](int k, int t) {             // the lane's channels of a row
+                const T* r = &w.raw[buf][k][t][g * C];
+                return C == 2 ? load2(r) : both(to_f32(*r));
+            };
+#pragma unroll
+            for (int e = 0; e < kChunk / 4; ++e) {
+                const int t = 4 * e + q4;
+                float v0, v1;
+                unpair(raw(1, t), v0, v1);
+                v0 += bias[0];
+                v1 += bias[C - 1];
+                f32x2 dl = p.softplus ? softplus2<kExact>(v0, v1) : pair(v0, v1);
+                if (t >= nt) dl = 0ull;                // rows past the end leave the state alone (their x and dout are 0)
+                const f32x2 u = mul2(dl, raw(0, t)), gy = gated ? mul2(raw(2, t), silu2(raw(3, t))) : raw(2, t);
+                float u0, u1;
+                unpair(dl, v0, v1);
+                unpair(u, u0, u1);
+                if (C == 2) {
+                    *reinterpret_cast<float4*>(&w.du[t][2 * g * C]) = make_float4(v0, u0, v1, u1);
+                    *reinterpret_cast<f32x2*>(&w.gy[t][g * C]) = gy;
+                } else {
+                    *reinterpret_cast<float2*>(&w.du[t][2 * g]) = make_float2(v0, u0);
+                    unpair(gy, v0, v1);
+                    w.gy[t][g] = v0;
+                }
             }
             __syncthreads();
-            // delta and u (and gy) of the lane's channels for a token
+            // delta and u of the lane's channels for a token
             auto channel = [&](int t, f32x2 (&dd)[C], f32x2 (&uu)[C]) {
                 if (C == 2) {
-                    const float4 v = *reinterpret_cast<const float4*>(sDu + (t * kCh + g * 2) * 2);
-                    dd[0] = pair(v.x, v.x); uu[0] = pair(v.y, v.y);
-                    dd[C - 1] = pair(v.z, v.z); uu[C - 1] = pair(v.w, v.w);
+                    const float4 v = *reinterpret_cast<const float4*>(&w.du[t][2 * g * C]);
+                    dd[0] = both(v.x); uu[0] = both(v.y);
+                    dd[C - 1] = both(v.z); uu[C - 1] = both(v.w);
                 } else {
-                    const float2 v = *reinterpret_cast<const float2*>(sDu + (t * kCh + g) * 2);
-                    dd[0] = pair(v.x, v.x); uu[0] = pair(v.y, v.y);
+                    const float2 v = *reinterpret_cast<const float2*>(&w.du[t][2 * g]);
+                    dd[0] = both(v.x); uu[0] = both(v.y);
                 }
             };
             const int slabs = (nt + K - 1) / K;
             f32x2 h[C][H];
-            {
-                const int64_t at = it.row0 + (it.done + t0) / kChunk;
+            auto start_of = [&](int sl) {
+                const float* from = sl == 0 ? w.check[buf] : w.start[sl - 1];
 #pragma unroll
                 for (int c = 0; c < C; ++c)
-                    load_states_row<S>(h[c], p.states + (at * p.D + dch[c]) * p.N, n0, p.N, in[c]);
-            }
-            f32x2 first[C][H];
 #pragma unroll
-            for (int c = 0; c < C; ++c)
-#pragma unroll
-                for (int i = 0; i < H; ++i) first[c][i] = h[c][i];
+                    for (int i = 0; i < H; ++i) h[c][i] = *reinterpret_cast<const f32x2*>(from + (c * H + i) * 64 + lane * 2);
+            };
+            start_of(0);
             for (int sl = 0; sl + 1 < slabs; ++sl) {
 #pragma unroll
                 for (int k = 0; k < K; ++k) {
                     const int t = sl * K + k;
                     f32x2 dd[C], uu[C], B[H];
                     channel(t, dd, uu);
-                    lds<S>(B, sB + t * NP + n0);
+                    lds<S>(B, &sh.bc[0][t][n0]);
 #pragma unroll
                     for (int c = 0; c < C; ++c)
 #pragma unroll
@@ -256,25 +345,33 @@ __global__ void __launch_bounds__(Plan<S>::kWarps * 32) selscan_bwd(const __grid
 #pragma unroll
                 for (int c = 0; c < C; ++c)
 #pragma unroll
-                    for (int i = 0; i < H; ++i)
-                        *reinterpret_cast<f32x2*>(sStart + ((sl * C + c) * H + i) * 64 + lane * 2) = h[c][i];
+                    for (int i = 0; i < H; ++i) *reinterpret_cast<f32x2*>(&w.start[sl][(c * H + i) * 64 + lane * 2]) = h[c][i];
             }
+            // of eight tokens (columns): u, sum A w and C.h by channel, dB and dC by state
+            float au[4], av[4], ay[4], ab[2][P::kTiles][4];
+            auto clear = [&] {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    au[i] = av[i] = ay[i] = 0.f;
+#pragma unroll
+                    for (int j = 0; j < P::kTiles; ++j) ab[0][j][i] = ab[1][j][i] = 0.f;
+                }
+            };
+            clear();
             for (int sl = slabs - 1; sl >= 0; --sl) {
+                start_of(sl);
+                float hot[K];                          // 1 in the lanes whose row is the token's column
 #pragma unroll
-                for (int c = 0; c < C; ++c)
-#pragma unroll
-                    for (int i = 0; i < H; ++i)
-                        h[c][i] = sl == 0 ? first[c][i]
-                                          : *reinterpret_cast<const f32x2*>(sStart + (((sl - 1) * C + c) * H + i) * 64 + lane * 2);
+                for (int k = 0; k < K; ++k) hot[k] = g == (sl * K & 7) + k ? 1.f : 0.f;
                 f32x2 a[K][C][H], ah[K][C][H];
 #pragma unroll
                 for (int k = 0; k < K; ++k) {
                     const int t = sl * K + k;
                     f32x2 dd[C], uu[C], B[H], Cv[H];
                     channel(t, dd, uu);
-                    lds<S>(B, sB + t * NP + n0);
-                    if (gated) lds<S>(Cv, sC + t * NP + n0);
-                    float y[C];
+                    lds<S>(B, &sh.bc[0][t][n0]);
+                    lds<S>(Cv, &sh.bc[1][t][n0]);
+                    float y[2] = {0.f, 0.f};
 #pragma unroll
                     for (int c = 0; c < C; ++c) {
                         f32x2 ys = 0ull;
@@ -283,110 +380,142 @@ __global__ void __launch_bounds__(Plan<S>::kWarps * 32) selscan_bwd(const __grid
                             a[k][c][i] = ex2_2(mul2(dd[c], a2[c][i]));
                             ah[k][c][i] = mul2(a[k][c][i], h[c][i]);
                             h[c][i] = fma2(uu[c], B[i], ah[k][c][i]);
-                            if (gated) ys = fma2(Cv[i], h[c][i], ys);
+                            ys = i == 0 ? mul2(Cv[i], h[c][i]) : fma2(Cv[i], h[c][i], ys);
                         }
                         float lo, hi;
                         unpair(ys, lo, hi);
                         y[c] = lo + hi;
                     }
-                    if (gated) {                       // only dz needs y
-                        halve<C>(y, lane, 2);
-                        halve<1>(y, lane, 1);
-                        if ((lane & 1) == 0 && (C == 2 || q4 == 0))
-                            sRed[(2 * K + k) * kCh + g * C + (C == 2 ? q4 >> 1 : 0)] = y[0];
-                    }
+                    add_rows<kExact>(ay, y[0], y[1], hot[k]);          // for dz
                 }
 #pragma unroll
                 for (int k = K - 1; k >= 0; --k) {
                     const int t = sl * K + k;
-                    f32x2 dd[C], uu[C], B[H], Cv[H];
+                    f32x2 dd[C], uu[C], B[H], Cv[H], gg[C];
                     channel(t, dd, uu);
-                    lds<S>(B, sB + t * NP + n0);
-                    lds<S>(Cv, sC + t * NP + n0);
+                    if (C == 2) {
+                        const float2 v = *reinterpret_cast<const float2*>(&w.gy[t][g * C]);
+                        gg[0] = both(v.x);
+                        gg[C - 1] = both(v.y);
+                    } else {
+                        gg[0] = both(w.gy[t][g]);
+                    }
+                    lds<S>(B, &sh.bc[0][t][n0]);
+                    lds<S>(Cv, &sh.bc[1][t][n0]);
                     f32x2 dB[H], dC[H];
-                    float red[2 * C];
+                    float u[2] = {0.f, 0.f}, v[2] = {0.f, 0.f};
 #pragma unroll
                     for (int c = 0; c < C; ++c) {
-                        const float gyv = sGy[t * kCh + g * C + c];
-                        const f32x2 gg = pair(gyv, gyv);
                         f32x2 us = 0ull, vs = 0ull;
 #pragma unroll
                         for (int i = 0; i < H; ++i) {
-                            const f32x2 r = fma2(gg, Cv[i], qv[c][i]), hh = fma2(uu[c], B[i], ah[k][c][i]);
-                            dC[i] = c == 0 ? mul2(gg, hh) : fma2(gg, hh, dC[i]);
+                            const f32x2 r = fma2(gg[c], Cv[i], qv[c][i]), hh = fma2(uu[c], B[i], ah[k][c][i]);
+                            dC[i] = c == 0 ? mul2(gg[c], hh) : fma2(gg[c], hh, dC[i]);
                             dB[i] = c == 0 ? mul2(uu[c], r) : fma2(uu[c], r, dB[i]);
-                            us = fma2(r, B[i], us);
-                            const f32x2 w = mul2(r, ah[k][c][i]);
-                            vs = fma2(w, a2[c][i], vs);
-                            dA[c][i] = fma2(dd[c], w, dA[c][i]);
+                            us = i == 0 ? mul2(r, B[i]) : fma2(r, B[i], us);
+                            const f32x2 rah = mul2(r, ah[k][c][i]);
+                            vs = i == 0 ? mul2(rah, a2[c][i]) : fma2(rah, a2[c][i], vs);
+                            dA[c][i] = fma2(dd[c], rah, dA[c][i]);
                             qv[c][i] = mul2(a[k][c][i], r);
                         }
                         float lo, hi;
                         unpair(us, lo, hi);
-                        red[c] = lo + hi;
+                        u[c] = lo + hi;
                         unpair(vs, lo, hi);
-                        red[C + c] = lo + hi;
+                        v[c] = lo + hi;
                     }
-                    halve<2 * C>(red, lane, 2);
-                    halve<C>(red, lane, 1);            // u of channel 0, 1, sum A w of 0, 1 (C = 1: u, u, ..)
-                    if (C == 2 || (lane & 1) == 0)
-                        sRed[((q4 >> 1) * K + k) * kCh + g * C + (C == 2 ? q4 & 1 : 0)] = red[0];
-                    float bc[2 * S];
+                    add_rows<true>(au, u[0], u[1], hot[k]);       // (dt_bias's gradient is in fp32)
+                    add_rows<true>(av, v[0], v[1], hot[k]);
+                    if (kExact) {                      // fp32: sums over the channels by shuffles
+                        float part[2 * S];
 #pragma unroll
-                    for (int i = 0; i < H; ++i) {
-                        unpair(dB[i], bc[2 * i], bc[2 * i + 1]);
-                        unpair(dC[i], bc[S + 2 * i], bc[S + 2 * i + 1]);
-                    }
-                    halve<2 * S>(bc, lane, 16);
-                    halve<S>(bc, lane, 8);
-                    halve<S / 2>(bc, lane, 4);
-                    // value g of 2 S / 8 each; with S = 2 lanes differing in bit 2 hold the same
-                    constexpr int kLeft = S >= 4 ? S / 4 : 1;
-                    if (S >= 4 || (lane & 4) == 0)
-#pragma unroll
-                        for (int i = 0; i < kLeft; ++i) {
-                            const int v = S >= 4 ? g * kLeft + i : g >> 1;     // 0 .. S - 1: dB, then dC
-                            sDbc[(t * 2 + v / S) * NP + n0 + v % S] = bc[i];
+                        for (int i = 0; i < H; ++i) {
+                            unpair(dB[i], part[2 * i], part[2 * i + 1]);
+                            unpair(dC[i], part[S + 2 * i], part[S + 2 * i + 1]);
                         }
-                }
-                __syncwarp();
-                if (er < K && sl * K + er < nt && ein) {
-                    const int t = sl * K + er;
-                    float xv[4], tv[4], gv[4], zv[4], us[4], vs[4], ys[4], ox[4], ot[4], oz[4];
-                    spread(load4(x + (int64_t)(t0 + t) * p.xs), xv);
-                    spread(load4(dt + (int64_t)(t0 + t) * p.dts), tv);
-                    spread(load4(dout + (int64_t)(t0 + t) * p.D), gv);
-                    if (gated) spread(load4(z + (int64_t)(t0 + t) * p.zs), zv);
-                    spread(*reinterpret_cast<const float4*>(sRed + er * kCh + ec), us);
-                    spread(*reinterpret_cast<const float4*>(sRed + (K + er) * kCh + ec), vs);
-                    if (gated) spread(*reinterpret_cast<const float4*>(sRed + (2 * K + er) * kCh + ec), ys);
+                        halve<2 * S>(part, lane, 16);
+                        halve<S>(part, lane, 8);
+                        halve<S / 2>(part, lane, 4);
+                        // value g of 2 S / 8 each; with S = 2 lanes differing in bit 2 hold the same
+                        constexpr int kLeft = S >= 4 ? S / 4 : 1;
+                        if (S >= 4 || (lane & 4) == 0)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float delta = sDu[(t * kCh + ec + i) * 2], gy = sGy[t * kCh + ec + i];
-                        ox[i] = fmaf(delta, us[i], skip[i] * gy);
-                        const float dd = fmaf(xv[i], us[i], vs[i] * 0.69314718055994531f);   // A = a2 ln 2
-                        ot[i] = p.softplus ? dd * softplus_grad<kExact>(tv[i] + bias[i]) : dd;
-                        if (gated) {
-                            const float sg = sigmoid(zv[i]);
-                            oz[i] = gv[i] * fmaf(skip[i], xv[i], ys[i]) * sg * fmaf(zv[i], 1.f - sg, 1.f);
-                        }
-                        dD[i] = fmaf(gy, xv[i], dD[i]);
-                        db[i] += ot[i];
+                            for (int i = 0; i < kLeft; ++i) {
+                                const int x = S >= 4 ? g * kLeft + i : g >> 1;     // 0 .. S - 1: dB, then dC
+                                w.dbc[t][x / S * NP + n0 + x % S] = part[i];
+                            }
+                    } else {
+                        // A first product moves the channels from the rows' lanes to the columns'
+                        // (state by channel), a second one sums them into the token's column.
+#pragma unroll
+                        for (int kind = 0; kind < 2; ++kind)
+#pragma unroll
+                            for (int j = 0; j < P::kTiles; ++j) {
+                                float m[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                                for (int i = 0; i < 2 && 2 * j + i < H; ++i) {
+                                    float lo, hi;
+                                    unpair(kind == 0 ? dB[2 * j + i] : dC[2 * j + i], lo, hi);
+                                    mma8(m, pick[i], lo, hi);
+                                }
+                                mma4(ab[kind][j], m[0] + m[1], m[2] + m[3], hot[k]);
+                            }
                     }
-                    const int64_t row = (int64_t)it.t0 + t0 + t;
-                    store4(static_cast<T*>(p.dx) + row * p.D + ed, ox);
-                    store4(static_cast<T*>(p.ddt) + row * p.D + ed, ot);
-                    if (gated) store4(static_cast<T*>(p.dz) + row * p.D + ed, oz);
                 }
-                __syncwarp();
+                if ((sl * K & 7) != 0) continue;
+                // eight tokens are complete: a lane's channels, two tokens
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int t = sl * K + 2 * q4 + e;
+                    if (t < nt && in) {
+                        float x[2], v[2], dy[2], z[2], ox[2], ot[2], oz[2];
+                        unpair(raw(0, t), x[0], x[1]);
+                        unpair(raw(1, t), v[0], v[1]);
+                        unpair(raw(2, t), dy[0], dy[1]);
+                        if (gated) unpair(raw(3, t), z[0], z[1]);
+#pragma unroll
+                        for (int c = 0; c < C; ++c) {
+                            const float delta = w.du[t][2 * (g * C + c)], gy = w.gy[t][g * C + c], u = au[2 * c + e];
+                            ox[c] = fmaf(delta, u, skip[c] * gy);
+                            const float dd = fmaf(x[c], u, av[2 * c + e] * 0.69314718055994531f);   // A = a2 ln 2
+                            ot[c] = p.softplus ? dd * softplus_grad<kExact>(v[c] + bias[c]) : dd;
+                            if (gated) {
+                                const float sg = sigmoid(z[c]);
+                                oz[c] = dy[c] * fmaf(skip[c], x[c], ay[2 * c + e]) * sg * fmaf(z[c], 1.f - sg, 1.f);
+                            }
+                            dD[c] = fmaf(gy, x[c], dD[c]);
+                            db[c] += ot[c];
+                        }
+                        auto put = [&](void* base, const float (&o)[2]) {
+                            T* r = static_cast<T*>(base) + ((int64_t)it.t0 + t0 + t) * p.D + dch;
+                            if (C == 2) store2(r, pair(o[0], o[C - 1]));
+                            else *r = from_f32<T>(o[0]);
+                        };
+                        put(p.dx, ox);
+                        put(p.ddt, ot);
+                        if (gated) put(p.dz, oz);
+                    }
+                }
+                if (!kExact) {
+#pragma unroll
+                    for (int kind = 0; kind < 2; ++kind)
+#pragma unroll
+                        for (int j = 0; j < P::kTiles; ++j)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {       // row g + 8 (i / 2): state of lane row / 4, value row % 4
+                                const int m = g + 8 * (i >> 1), t = sl * K + 2 * q4 + (i & 1);
+                                if (4 * j + (m & 3) < S) w.dbc[t][kind * NP + (m >> 2) * S + 4 * j + (m & 3)] = ab[kind][j][i];
+                            }
+                }
+                clear();
             }
             __syncthreads();
             // the CTA's terms of dB and dC: its warps' added in order
-            for (int i = threadIdx.x; i < nt * 2 * NP; i += P::kWarps * 32) {
+            for (int i = threadIdx.x; i < nt * 2 * NP; i += kThreads) {
                 const int t = i / (2 * NP), v = i % (2 * NP), n = v % NP;
                 float s = 0.f;
 #pragma unroll
-                for (int w = 0; w < P::kWarps; ++w) s += smem[P::kBC + w * P::kWarp + P::kDu + P::kGy + P::kStart + i];
+                for (int k = 0; k < P::kWarps; ++k) s += sh.w[k].dbc[t][v];
                 if (n < p.N)
                     p.part[((((int64_t)tg * p.g.T + it.t0 + t0 + t) * p.G + grp) * 2 + v / NP) * p.N + n] = s;
             }
@@ -394,22 +523,23 @@ __global__ void __launch_bounds__(Plan<S>::kWarps * 32) selscan_bwd(const __grid
         if (it.first && p.dinit != nullptr)
 #pragma unroll
             for (int c = 0; c < C; ++c)
-                store_states_row<S>(qv[c], p.dinit + ((int64_t)it.seq * p.D + dch[c]) * p.N, n0, p.N, in[c]);
+                store_states_row<S>(qv[c], p.dinit + ((int64_t)it.seq * p.D + dch + c) * p.N, n0, p.N, in);
     }
     // the slot's terms of dA, dD and dbias
 #pragma unroll
     for (int c = 0; c < C; ++c)
-        store_states_row<S>(dA[c], p.partA + ((int64_t)slot * p.D + dch[c]) * p.N, n0, p.N, in[c]);
+        store_states_row<S>(dA[c], p.partA + ((int64_t)slot * p.D + dch + c) * p.N, n0, p.N, in);
 #pragma unroll
-    for (int bit = kQuads; bit < 32; bit *= 2)
+    for (int c = 0; c < C; ++c) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            dD[i] += __shfl_xor_sync(0xffffffffu, dD[i], bit);
-            db[i] += __shfl_xor_sync(0xffffffffu, db[i], bit);
+        for (int bit = 1; bit < 4; bit *= 2) {
+            dD[c] += __shfl_xor_sync(0xffffffffu, dD[c], bit);
+            db[c] += __shfl_xor_sync(0xffffffffu, db[c], bit);
         }
-    if (er == 0 && ein) {
-        store4(p.partD + (int64_t)slot * 2 * p.D + ed, dD);
-        store4(p.partD + ((int64_t)slot * 2 + 1) * p.D + ed, db);
+        if (q4 == 0 && in) {
+            p.partD[(int64_t)slot * 2 * p.D + dch + c] = dD[c];
+            p.partD[((int64_t)slot * 2 + 1) * p.D + dch + c] = db[c];
+        }
     }
 }
 
@@ -449,14 +579,16 @@ __global__ void __launch_bounds__(128) selscan_sum_a(const __grid_constant__ Sca
 }
 
 template <typename T, int S> cudaError_t go(const ScanParams& p, cudaStream_t stream) {
-    using P = Plan<S>;
+    using P = Plan<T, S>;
     constexpr int kTile = P::kWarps * P::kCh;
     const int tpg = (p.cpg + kTile - 1) / kTile;
     const int64_t slots = p.slots + (p.g.cu != nullptr ? 16 : 0);
     if (slots > 0) {
-        const cudaError_t e = cudaFuncSetAttribute(selscan_bwd<T, S>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::kBytes);
+        cudaError_t e = cudaFuncSetAttribute(selscan_bwd<T, S>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(typename P::Cta));
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(selscan_bwd<T, S>, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
         if (e != cudaSuccess) return e;
-        selscan_bwd<T, S><<<(unsigned)(slots * tpg * p.G), P::kWarps * 32, P::kBytes, stream>>>(p);
+        selscan_bwd<T, S><<<(unsigned)(slots * tpg * p.G), P::kWarps * 32, (int)sizeof(typename P::Cta), stream>>>(p);
         const cudaError_t l = cudaGetLastError();
         if (l != cudaSuccess) return l;
     }

@@ -30,29 +30,6 @@ constexpr int kWarps = 2;    // warps of a CTA, each on its own
 constexpr int kZeroItems = 64;
 constexpr int kStages = 4;   // tiles of x, dt and z in shared memory
 
-template <typename T> struct Raw4;                        // four states as loaded
-template <> struct Raw4<float> { float4 v; };
-template <> struct Raw4<__nv_bfloat16> { uint2 v; };
-__device__ __forceinline__ void fetch(Raw4<float>& r, const float* p, int n, int N, bool vec) {
-    r.v = load_states(p, n, N, vec);
-}
-__device__ __forceinline__ void fetch(Raw4<__nv_bfloat16>& r, const __nv_bfloat16* p, int n, int N, bool vec) {
-    if (vec) {
-        r.v = n < N ? __ldg(reinterpret_cast<const uint2*>(p + n)) : make_uint2(0u, 0u);
-    } else {
-        const unsigned short* q = reinterpret_cast<const unsigned short*>(p);
-        uint32_t e[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) e[i] = n + i < N ? (uint32_t)__ldg(q + n + i) : 0u;
-        r.v = make_uint2(e[0] | e[1] << 16, e[2] | e[3] << 16);
-    }
-}
-__device__ __forceinline__ float4 widen(const Raw4<float>& r) { return r.v; }
-__device__ __forceinline__ float4 widen(const Raw4<__nv_bfloat16>& r) {
-    return make_float4(__uint_as_float(r.v.x << 16), __uint_as_float(r.v.x & 0xFFFF0000u),
-                       __uint_as_float(r.v.y << 16), __uint_as_float(r.v.y & 0xFFFF0000u));
-}
-
 template <int S> __device__ __forceinline__ void load_row(f32x2 (&h)[S / 2], const float* p, int n0, int N, bool in) {
 #pragma unroll
     for (int i = 0; i < S / 4; ++i) {
