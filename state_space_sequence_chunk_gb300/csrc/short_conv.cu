@@ -5,11 +5,17 @@
 // its initial state (0 without one):
 //     p_t = bias + sum_k w_k x_{t-W+1+k},    o_t = a(p_t),  a(p) = p or p sigmoid(p)
 //     g_t = do_t a'(p_t),  dx_t = sum_k w_k g_{t+W-1-k},  dw_k = sum_t g_t x_{t-W+1+k}
-// Bound by HBM: each row read once and written once.  A thread owns a vector of
-// channels (a warp 512 or 256 contiguous bytes of a row) and walks a tile of tokens
-// with the last W - 1 rows in registers, eight rows' loads in flight while eight are
-// computed; the W - 1 rows before a tile are read again (from L2, mostly).  Sequences
-// begin and end anywhere in a tile: the walk swaps its window there.
+// Each row is read once and written once.  A thread owns four channels (the gradient:
+// two) and walks a tile of tokens with the last W - 1 rows in registers, eight rows'
+// loads in flight while eight are computed; the W - 1 rows before a tile are read again
+// (from L2, mostly).  Sequences begin and end anywhere in a tile: the walk goes by its
+// part of each, with the window loaded anew.
+//
+// What bounds it: HBM and, in bf16, about as much the instructions, 45 for four channels
+// of a row.  16384 bf16 tokens of 5120 channels, 4 taps: 63 us, 5.3 TB/s (eight channels a
+// thread and checks in the loop instead of parts: 100; 32 tokens a tile: 71; two channels
+// 65); the gradient 112 us, 4.5 TB/s (four channels 121).  fp32, of 2048 channels: 48 us, 5.6 TB/s,
+// and 83 us, 4.9 TB/s.
 #include <type_traits>
 
 #include "short_conv.cuh"
@@ -19,6 +25,7 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kAhead = 8;        // rows loaded ahead
+constexpr int kFwdVec = 4, kBwdVec = 2;   // channels of a thread
 
 __device__ __forceinline__ float ex2(float v) {
     float r;
@@ -30,22 +37,9 @@ __device__ __forceinline__ float rcp(float v) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
     return r;
 }
-__device__ __forceinline__ float sigmoid(float z) { return rcp(1.f + ex2(-z * kLog2e)); }
 
 // V channels of a row: as loaded, and as pairs of floats.
 template <typename T, int V> struct Row;
-template <> struct Row<__nv_bfloat16, 8> {
-    uint4 r;
-    __device__ void load(const __nv_bfloat16* p) { r = __ldg(reinterpret_cast<const uint4*>(p)); }
-    __device__ void zero() { r = make_uint4(0u, 0u, 0u, 0u); }
-    __device__ void get(f32x2 (&v)[4]) const {
-        v[0] = pair(r.x << 16, r.x & 0xFFFF0000u); v[1] = pair(r.y << 16, r.y & 0xFFFF0000u);
-        v[2] = pair(r.z << 16, r.z & 0xFFFF0000u); v[3] = pair(r.w << 16, r.w & 0xFFFF0000u);
-    }
-    __device__ static void store(__nv_bfloat16* p, const f32x2 (&v)[4]) {
-        *reinterpret_cast<uint4*>(p) = make_uint4(pack2(v[0]), pack2(v[1]), pack2(v[2]), pack2(v[3]));
-    }
-};
 template <> struct Row<__nv_bfloat16, 4> {
     uint2 r;
     __device__ void load(const __nv_bfloat16* p) { r = __ldg(reinterpret_cast<const uint2*>(p)); }
@@ -56,6 +50,20 @@ template <> struct Row<__nv_bfloat16, 4> {
     __device__ static void store(__nv_bfloat16* p, const f32x2 (&v)[2]) {
         *reinterpret_cast<uint2*>(p) = make_uint2(pack2(v[0]), pack2(v[1]));
     }
+};
+template <> struct Row<__nv_bfloat16, 2> {
+    uint32_t r;
+    __device__ void load(const __nv_bfloat16* p) { r = __ldg(reinterpret_cast<const uint32_t*>(p)); }
+    __device__ void zero() { r = 0u; }
+    __device__ void get(f32x2 (&v)[1]) const { v[0] = pair(r << 16, r & 0xFFFF0000u); }
+    __device__ static void store(__nv_bfloat16* p, const f32x2 (&v)[1]) { *reinterpret_cast<uint32_t*>(p) = pack2(v[0]); }
+};
+template <> struct Row<float, 2> {
+    f32x2 r;
+    __device__ void load(const float* p) { r = __ldg(reinterpret_cast<const f32x2*>(p)); }
+    __device__ void zero() { r = 0ull; }
+    __device__ void get(f32x2 (&v)[1]) const { v[0] = r; }
+    __device__ static void store(float* p, const f32x2 (&v)[1]) { *reinterpret_cast<f32x2*>(p) = v[0]; }
 };
 template <> struct Row<float, 4> {
     ulonglong2 r;
@@ -104,12 +112,26 @@ __device__ __forceinline__ void row_of(const ShortConv& p, Row<T, V>& r, int W, 
 template <int V, int W> struct Taps {
     f32x2 w[W][V / 2], b[V / 2];
     __device__ void load(const ShortConv& p, int col) {
+        float f[V * W];                          // the V channels' taps lie together
+        const float* at = p.w + (int64_t)col * W;
+        if (V % 4 == 0) {                        // (16-byte vectors: V W is a multiple of four, and so is col W)
+#pragma unroll
+            for (int i = 0; i < V * W; i += 4) {
+                const float4 v = __ldg(reinterpret_cast<const float4*>(at + i));
+                f[i] = v.x; f[(i + 1) % (V * W)] = v.y; f[(i + 2) % (V * W)] = v.z; f[(i + 3) % (V * W)] = v.w;
+            }
+        } else {                                 // (8-byte vectors: both are even)
+#pragma unroll
+            for (int i = 0; i < V * W; i += 2) {
+                const float2 v = __ldg(reinterpret_cast<const float2*>(at + i));
+                f[i] = v.x; f[(i + 1) % (V * W)] = v.y;
+            }
+        }
 #pragma unroll
         for (int i = 0; i < V / 2; ++i) {
-            const float* at = p.w + (int64_t)(col + 2 * i) * W;
 #pragma unroll
-            for (int k = 0; k < W; ++k) w[k][i] = pair(__ldg(at + k), __ldg(at + W + k));
-            b[i] = p.bias != nullptr ? pair(__ldg(p.bias + col + 2 * i), __ldg(p.bias + col + 2 * i + 1)) : pair(0.f, 0.f);
+            for (int k = 0; k < W; ++k) w[k][i] = pair(f[2 * i * W + k], f[(2 * i + 1) * W + k]);
+            b[i] = p.bias != nullptr ? __ldg(reinterpret_cast<const f32x2*>(p.bias + col) + i) : 0ull;
         }
     }
     // bias + sum of taps: the window's W - 1 rows, then the present one
@@ -131,31 +153,30 @@ template <int N2, int M> __device__ __forceinline__ void shift(f32x2 (&win)[M][N
 #pragma unroll
     for (int i = 0; i < N2; ++i) win[M - 1][i] = now[i];
 }
+__device__ __forceinline__ f32x2 sigmoid2(f32x2 v) {
+    float a, b;
+    unpair(mul2(v, pair(-kLog2e, -kLog2e)), a, b);
+    unpair(add2(pair(ex2(a), ex2(b)), pair(1.f, 1.f)), a, b);
+    return pair(rcp(a), rcp(b));
+}
 template <int N2> __device__ __forceinline__ void activate(f32x2 (&v)[N2], int act) {
     if (act == SSD_ACT_NONE) return;
 #pragma unroll
-    for (int i = 0; i < N2; ++i) {
-        float a, b;
-        unpair(v[i], a, b);
-        v[i] = pair(a * sigmoid(a), b * sigmoid(b));
-    }
+    for (int i = 0; i < N2; ++i) v[i] = mul2(v[i], sigmoid2(v[i]));
 }
-// g = do a'(p): silu' = s (1 + p (1 - s)) with s = sigmoid(p)
+// g = do a'(p): silu' = s + p s (1 - s) with s = sigmoid(p)
 template <int N2> __device__ __forceinline__ void back(f32x2 (&g)[N2], const f32x2 (&pre)[N2], int act) {
     if (act == SSD_ACT_NONE) return;
 #pragma unroll
     for (int i = 0; i < N2; ++i) {
-        float a, b, ga, gb;
-        unpair(pre[i], a, b);
-        unpair(g[i], ga, gb);
-        const float sa = sigmoid(a), sb = sigmoid(b);
-        g[i] = pair(ga * sa * fmaf(a, 1.f - sa, 1.f), gb * sb * fmaf(b, 1.f - sb, 1.f));
+        const f32x2 s = sigmoid2(pre[i]), ps = mul2(pre[i], s);
+        g[i] = mul2(g[i], fma2(ps, fma2(s, pair(-1.f, -1.f), pair(1.f, 1.f)), s));
     }
 }
 
 template <typename T, int W>
-__global__ void __launch_bounds__(kThreads) short_conv_fwd(const __grid_constant__ ShortConv p) {
-    constexpr int V = 16 / sizeof(T), N2 = V / 2;
+__global__ void __launch_bounds__(kThreads, W <= 4 ? 4 : 1) short_conv_fwd(const __grid_constant__ ShortConv p) {
+    constexpr int V = kFwdVec, N2 = V / 2;
     const int vecs = p.D / V, blocks = (vecs + kThreads - 1) / kThreads;
     const int item = blockIdx.x / blocks, vec = (blockIdx.x - item * blocks) * kThreads + threadIdx.x;
     const bool in = vec < vecs;
@@ -177,60 +198,68 @@ __global__ void __launch_bounds__(kThreads) short_conv_fwd(const __grid_constant
         return;
     }
     const int t0 = item * p.TT, t1 = min(t0 + p.TT, p.T);
-    int s = find(p, t0), lo = 0, hi = p.T;
-    if (s < p.nseq) bounds(p, s, lo, hi);
+    int s = find(p, t0);
     if (!in) return;
     const T* x = static_cast<const T*>(p.x) + col;
     T* out = static_cast<T*>(p.out) + col;
-    Row<T, V> ahead[kAhead];
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i)
-        if (t0 + i < t1) ahead[i].load(x + (t0 + i) * p.xs);
     Taps<V, W> taps;
     taps.load(p, col);
-    f32x2 win[W - 1][N2];
-    auto enter = [&](int t) {                    // the window before row t of sequence s
-        Row<T, V> r[W - 1];
-#pragma unroll
-        for (int j = 0; j < W - 1; ++j) {
-            if (s < p.nseq) row_of<T, V>(p, r[j], W, s, lo, t - (W - 1) + j, col);
-            else r[j].zero();
+    // the tile's part of one sequence after another; rows of none behind the last
+    for (int a = t0; a < t1; ++s) {
+        int lo = 0, hi = 0;
+        for (; s < p.nseq; ++s) {
+            bounds(p, s, lo, hi);
+            if (hi > a) break;
         }
+        if (s >= p.nseq) {
+            f32x2 zero[N2];
 #pragma unroll
-        for (int j = 0; j < W - 1; ++j) r[j].get(win[j]);
-    };
-    enter(t0);
-    for (int t = t0; t < t1; t += kAhead) {
-        Row<T, V> cur[kAhead];
+            for (int k = 0; k < N2; ++k) zero[k] = pair(0.f, 0.f);
+            for (; a < t1; ++a) Row<T, V>::store(out + (int64_t)a * p.D, zero);
+            break;
+        }
+        const int b = min(hi, t1);
+        Row<T, V> ahead[kAhead];
+        const T* from = x + a * p.xs;            // the row loaded next
+        T* to = out + (int64_t)a * p.D;          // the row stored next
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
-            cur[i] = ahead[i];
-            if (t + kAhead + i < t1) ahead[i].load(x + (t + kAhead + i) * p.xs);
+            if (a + i < b) ahead[i].load(from);
+            from += p.xs;
         }
+        f32x2 win[W - 1][N2];
+        {
+            Row<T, V> r[W - 1];
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            if (t + i < t1) {
-                if (t + i == hi) {               // the next sequence that has rows, or none
-                    while (++s < p.nseq) {
-                        bounds(p, s, lo, hi);
-                        if (hi > t + i) break;
-                    }
-                    if (s >= p.nseq) hi = p.T;
-                    enter(t + i);
-                }
-                f32x2 now[N2], o[N2];
-                cur[i].get(now);
-                if (s < p.nseq) {
-                    taps.apply(win, now, o);
-                    activate(o, p.act);
-                    shift(win, now);
-                } else {
+            for (int j = 0; j < W - 1; ++j) row_of<T, V>(p, r[j], W, s, lo, a - (W - 1) + j, col);
 #pragma unroll
-                    for (int k = 0; k < N2; ++k) o[k] = pair(0.f, 0.f);
-                }
-                Row<T, V>::store(out + (int64_t)(t + i) * p.D, o);
+            for (int j = 0; j < W - 1; ++j) r[j].get(win[j]);
+        }
+        auto row = [&](const Row<T, V>& r) {
+            f32x2 now[N2], o[N2];
+            r.get(now);
+            taps.apply(win, now, o);
+            activate(o, p.act);
+            shift(win, now);
+            Row<T, V>::store(to, o);
+            to += p.D;
+        };
+        int t = a;
+        for (; t + kAhead <= b; t += kAhead) {
+            Row<T, V> cur[kAhead];
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                cur[i] = ahead[i];
+                if (t + kAhead + i < b) ahead[i].load(from);
+                from += p.xs;
             }
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) row(cur[i]);
         }
+#pragma unroll
+        for (int i = 0; i < kAhead - 1; ++i)
+            if (t + i < b) row(ahead[i]);
+        a = b;
     }
 }
 
@@ -239,8 +268,8 @@ __global__ void __launch_bounds__(kThreads) short_conv_fwd(const __grid_constant
 // and W - 1 rows further, whose g the tile's last rows of dx need.  The sums for dw and
 // db go into one row of partial sums per tile.
 template <typename T, int W>
-__global__ void __launch_bounds__(kThreads) short_conv_bwd(const __grid_constant__ ShortConv p) {
-    constexpr int V = 4, N2 = 2;
+__global__ void __launch_bounds__(kThreads, W <= 4 && sizeof(T) == 2 ? 5 : 1) short_conv_bwd(const __grid_constant__ ShortConv p) {
+    constexpr int V = kBwdVec, N2 = V / 2;
     const int vecs = p.D / V, blocks = (vecs + kThreads - 1) / kThreads;
     const int item = blockIdx.x / blocks, vec = (blockIdx.x - item * blocks) * kThreads + threadIdx.x;
     const bool in = vec < vecs;
@@ -311,7 +340,9 @@ __global__ void __launch_bounds__(kThreads) short_conv_bwd(const __grid_constant
             if (hi > a) break;
         }
         if (s >= p.nseq) {                       // rows of no sequence
-            const f32x2 zero[N2] = {z2, z2};
+            f32x2 zero[N2];
+#pragma unroll
+            for (int k = 0; k < N2; ++k) zero[k] = z2;
             for (; a < t1; ++a) Row<T, V>::store(dx + (int64_t)a * p.D, zero);
             break;
         }
@@ -329,48 +360,61 @@ __global__ void __launch_bounds__(kThreads) short_conv_bwd(const __grid_constant
 #pragma unroll
             for (int k = 0; k < N2; ++k) acc[j][k] = z2;
         Row<T, V> xa[kAhead], da[kAhead];
+        const T *xn = x + a * p.xs, *dn = dout + (int64_t)a * p.D;    // the rows loaded next
+        T* to = dx + (int64_t)(a - (W - 1)) * p.D;                    // the row finished next
+        auto fetch = [&](int t) {
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i)
-            if (a + i < lim) {
-                xa[i].load(x + (a + i) * p.xs);
-                da[i].load(dout + (int64_t)(a + i) * p.D);
+            for (int i = 0; i < kAhead; ++i) {
+                if (t + i < lim) {
+                    xa[i].load(xn);
+                    da[i].load(dn);
+                }
+                xn += p.xs;
+                dn += p.D;
             }
-        for (int t = a; t < lim; t += kAhead) {
+        };
+        fetch(a);
+        auto row = [&](const Row<T, V>& xr, const Row<T, V>& dr, int t, auto own) {
+            f32x2 now[N2], g[N2], pre[N2];
+            xr.get(now);
+            dr.get(g);
+            taps.apply(win, now, pre);
+            back(g, pre, p.act);
+#pragma unroll
+            for (int k = 0; k < N2; ++k) {
+                if (decltype(own)::value) {      // not a row that the next tile adds
+                    db[k] = add2(db[k], g[k]);
+#pragma unroll
+                    for (int j = 0; j < W - 1; ++j) dw[j][k] = fma2(g[k], win[j][k], dw[j][k]);
+                    dw[W - 1][k] = fma2(g[k], now[k], dw[W - 1][k]);
+                }
+#pragma unroll
+                for (int j = W - 1; j > 0; --j) acc[j][k] = fma2(taps.w[W - 1 - j][k], g[k], acc[j - 1][k]);
+                acc[0][k] = mul2(taps.w[W - 1][k], g[k]);
+            }
+            shift(win, now);
+            if (t - (W - 1) >= a) Row<T, V>::store(to, acc[W - 1]);
+            to += p.D;
+        };
+        int t = a;
+        for (; t + kAhead <= b; t += kAhead) {
             Row<T, V> xc[kAhead], dc[kAhead];
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) {
                 xc[i] = xa[i];
                 dc[i] = da[i];
-                if (t + kAhead + i < lim) {
-                    xa[i].load(x + (t + kAhead + i) * p.xs);
-                    da[i].load(dout + (int64_t)(t + kAhead + i) * p.D);
-                }
             }
+            fetch(t + kAhead);
 #pragma unroll
-            for (int i = 0; i < kAhead; ++i) {
-                if (t + i < lim) {
-                    f32x2 now[N2], g[N2], pre[N2];
-                    xc[i].get(now);
-                    dc[i].get(g);
-                    taps.apply(win, now, pre);
-                    back(g, pre, p.act);
-#pragma unroll
-                    for (int k = 0; k < N2; ++k) {
-                        if (t + i < b) {
-                            db[k] = add2(db[k], g[k]);
-#pragma unroll
-                            for (int j = 0; j < W - 1; ++j) dw[j][k] = fma2(g[k], win[j][k], dw[j][k]);
-                            dw[W - 1][k] = fma2(g[k], now[k], dw[W - 1][k]);
-                        }
-#pragma unroll
-                        for (int j = W - 1; j > 0; --j) acc[j][k] = fma2(taps.w[W - 1 - j][k], g[k], acc[j - 1][k]);
-                        acc[0][k] = mul2(taps.w[W - 1][k], g[k]);
-                    }
-                    shift(win, now);
-                    const int r = t + i - (W - 1);
-                    if (r >= a) Row<T, V>::store(dx + (int64_t)r * p.D, acc[W - 1]);
-                }
-            }
+            for (int i = 0; i < kAhead; ++i) row(xc[i], dc[i], t + i, std::true_type());
+        }
+        // the rest, fewer than kAhead rows, and up to W - 1 of the next tile
+        for (int i = 0; t + i < lim; ++i) {
+            Row<T, V> xr, dr;
+            xr.load(x + (t + i) * p.xs);
+            dr.load(dout + (int64_t)(t + i) * p.D);
+            if (t + i < b) row(xr, dr, t + i, std::true_type());
+            else row(xr, dr, t + i, std::false_type());
         }
         // the sequence's last rows, if it ends here: nothing follows but the final state's gradient
 #pragma unroll
@@ -393,9 +437,8 @@ __global__ void __launch_bounds__(kThreads) short_conv_bwd(const __grid_constant
     }
     float* part = p.part + (int64_t)item * (W + 1) * p.D + col;
 #pragma unroll
-    for (int j = 0; j < W; ++j)
-        *reinterpret_cast<ulonglong2*>(part + (int64_t)j * p.D) = make_ulonglong2(dw[j][0], dw[j][1]);
-    *reinterpret_cast<ulonglong2*>(part + (int64_t)W * p.D) = make_ulonglong2(db[0], db[1]);
+    for (int j = 0; j < W; ++j) Row<float, V>::store(part + (int64_t)j * p.D, dw[j]);
+    Row<float, V>::store(part + (int64_t)W * p.D, db);
 }
 
 // dw and db: the tiles' sums added in the tiles' order, in eight shares.
@@ -477,8 +520,8 @@ inline int64_t blocks_of(int D, int V) { return (D / V + kThreads - 1) / kThread
 
 int short_conv_tile(int64_t T, int D, int dtype, bool backward, int sms) {
     // long tiles re-read fewer rows; short ones where the long ones would leave SMs idle
-    const int64_t per = blocks_of(D, backward || dtype == SSD_F32 ? 4 : 8);
-    int tile = backward ? 64 : 32;
+    const int64_t per = blocks_of(D, backward ? kBwdVec : kFwdVec);
+    int tile = backward ? 128 : 64;
     while (tile > 8 && (T + tile - 1) / tile * per < 4 * sms) tile /= 2;
     return tile;
 }
@@ -488,7 +531,7 @@ cudaError_t launch_short_conv_fwd(ShortConv& p, int W, int dtype, int sms, cudaS
     p.tiles = (p.T + p.TT - 1) / p.TT;
     const int64_t items = p.tiles + (p.fin != nullptr ? (int64_t)p.nseq : 0);
     if (items == 0) return cudaSuccess;
-    const unsigned grid = (unsigned)(items * blocks_of(p.D, dtype == SSD_BF16 ? 8 : 4));
+    const unsigned grid = (unsigned)(items * blocks_of(p.D, kFwdVec));
     return by_width(W, [&](auto w) {
         if (dtype == SSD_BF16) short_conv_fwd<__nv_bfloat16, decltype(w)::value><<<grid, kThreads, 0, stream>>>(p);
         else short_conv_fwd<float, decltype(w)::value><<<grid, kThreads, 0, stream>>>(p);
@@ -501,7 +544,7 @@ cudaError_t launch_short_conv_bwd(ShortConv& p, int W, int dtype, int sms, cudaS
     p.tiles = (p.T + p.TT - 1) / p.TT;
     const int64_t items = p.tiles + (p.dinit != nullptr ? (int64_t)p.nseq : 0);
     if (items > 0) {
-        const unsigned grid = (unsigned)(items * blocks_of(p.D, 4));
+        const unsigned grid = (unsigned)(items * blocks_of(p.D, kBwdVec));
         const cudaError_t e = by_width(W, [&](auto w) {
             if (dtype == SSD_BF16) short_conv_bwd<__nv_bfloat16, decltype(w)::value><<<grid, kThreads, 0, stream>>>(p);
             else short_conv_bwd<float, decltype(w)::value><<<grid, kThreads, 0, stream>>>(p);

@@ -30,8 +30,8 @@ ssd_status make(const ssd_short_conv_dims* d, bool packed, Dims* out) {
     p.act = d->activation;
     q.rows = (size_t)(q.T * q.D) * q.es;
     q.states = (size_t)(q.n * (q.W - 1) * q.D) * q.es;
-    // a CTA for each tile of tokens or sequence and 128 vectors of channels: within a grid
-    if ((q.T / 8 + 1 + q.n) * ((q.D / 4 + 127) / 128) >= (1LL << 31)) return SSD_ERR_SHAPE;
+    // a CTA for each tile of tokens or sequence and 128 vectors of two channels: within a grid
+    if ((q.T / 8 + 1 + q.n) * ((q.D / 2 + 127) / 128) >= (1LL << 31)) return SSD_ERR_SHAPE;
     *out = q;
     return SSD_OK;
 }
