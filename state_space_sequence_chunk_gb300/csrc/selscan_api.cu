@@ -58,8 +58,8 @@ ssd_status make(const ssd_selscan_dims* d, bool packed, bool backward, Scan* out
     // sequences 214 and 148; 16384 tokens of 5120 in 12 sequences 421 and 592; 16384 of 2048
     // in 40 195 and 271; 512 of 5120 61 and 71.
     // Backwards a CTA of 64 (32, 16) channels takes 295 ns a token by itself, and the cut's
-    // passes 1.7 ns for each token and CTA: 8192 tokens of 2048 channels 2416 and 470, in 6
-    // sequences 685 and 470, 16384 of 2048 in 40 812 and 888.
+    // passes 1.7 ns for each token and CTA: 8192 tokens of 2048 channels 2416 and 470 (before the last steps), in 6
+    // sequences 650 and 454, 16384 of 2048 in 40 783 and 853.
     const int64_t bt = selscan_bwd_channels((int)q.N), tiles = (p.cpg + bt - 1) / bt;
     const int64_t warps = q.G * ((p.cpg * (q.N <= 16 ? 1 : q.N <= 32 ? 2 : 4) + 31) / 32);
     const int64_t sms = sm_count(), work = q.T * (backward ? tiles * q.G : warps);
@@ -69,7 +69,7 @@ ssd_status make(const ssd_selscan_dims* d, bool packed, bool backward, Scan* out
     if (q.n > 0 && longest > (backward ? work / (sms * 8 / 7) + 136 : work / (3 * sms) + 512)) {
         // several ranges for each warp that is resident, but not shorter than 128 tokens
         // (8192 tokens of 2048 channels: ranges of 128, 256, 512 tokens 146, 160, 197 us,
-        // backwards 470, 489, 541; 65536 of 1536: 128, 384, 512: 769, 728, 755)
+        // backwards 454, 474; 65536 of 1536: 128, 384, 512: 769, 728, 755)
         int64_t R = (work / ((backward ? 13 : 54) * sms) + 31) / 32 * 32;
         R = R < 128 ? 128 : R > 512 ? 512 : R;
         if (R < longest) g.R = (int)R;

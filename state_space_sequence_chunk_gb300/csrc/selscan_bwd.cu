@@ -24,9 +24,9 @@
 // shuffles.
 //
 // What bounds it: a token takes a warp of 16 channels and 16 states some 200
-// instructions, 64 of them packed multiply-adds, and the registers (224 to 255) leave
+// instructions, 63 of them packed multiply-adds, and the registers (200 to 255) leave
 // two warps a quarter-SM, which issue in every second clock.  8192 tokens of 2048
-// channels in 6 sequences: 470 us a call, 685 without the cut into ranges.  Sums by
+// channels in 6 sequences: 454 us a call, 650 without the cut into ranges.  Sums by
 // shuffles and rows loaded where they are used: 617; pairs of channels instead of
 // states, or delta and u stored in pairs: 539, 509 (more moves for the tensor cores'
 // operands, more shared memory traffic); slabs of 2 tokens and three warps a quarter-SM: 485,
@@ -176,7 +176,6 @@ __global__ void __launch_bounds__(Plan<T, S>::kWarps * 32, S <= 4 ? 2 : 1) selsc
     const bool in = c0 + g * C < p.cpg;
     const int64_t dch = (int64_t)grp * p.cpg + (in ? c0 + g * C : 0);
     f32x2 dA[C][H], qv[C][H], a2[C][H];
-    float dD[C], db[C], bias[C], skip[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
         load_states_row<S>(a2[c], p.A + (dch + c) * p.N, n0, p.N, in);
@@ -187,10 +186,10 @@ __global__ void __launch_bounds__(Plan<T, S>::kWarps * 32, S <= 4 ? 2 : 1) selsc
             a2[c][i] = pair(scan_rate(a), scan_rate(b));
             dA[c][i] = 0ull;
         }
-        dD[c] = db[c] = 0.f;
-        bias[c] = p.bias != nullptr ? p.bias[dch + c] : 0.f;
-        skip[c] = p.Dk != nullptr ? p.Dk[dch + c] : 0.f;
     }
+    auto per_channel = [&](const float* v) { return v != nullptr ? pair(v[dch], v[dch + C - 1]) : 0ull; };
+    const f32x2 bias = per_channel(p.bias), skip = per_channel(p.Dk);
+    f32x2 dD = 0ull, db = 0ull;
     // the rows that a lane's values go to in the sums over channels: value s of lane (g, q) to
     // row 4 q + s % 4 of its tile
     float pick[2][4];
@@ -289,10 +288,11 @@ __global__ void __launch_bounds__(Plan<T, S>::kWarps * 32, S <= 4 ? 2 : 1) selsc
             for (int e = 0; e < kChunk / 4; ++e) {
                 const int t = 4 * e + q4;
                 float v0, v1;
-                unpair(raw(1, t), v0, v1);
-                v0 += bias[0];
-                v1 += bias[C - 1];
-                f32x2 dl = p.softplus ? softplus2<kExact>(v0, v1) : pair(v0, v1);
+                f32x2 dl = add2(raw(1, t), bias);
+                if (p.softplus) {
+                    unpair(dl, v0, v1);
+                    dl = softplus2<kExact>(v0, v1);
+                }
                 if (t >= nt) dl = 0ull;                // rows past the end leave the state alone (their x and dout are 0)
                 const f32x2 u = mul2(dl, raw(0, t)), gy = gated ? mul2(raw(2, t), silu2(raw(3, t))) : raw(2, t);
                 float u0, u1;
@@ -468,32 +468,43 @@ __global__ void __launch_bounds__(Plan<T, S>::kWarps * 32, S <= 4 ? 2 : 1) selsc
                 for (int e = 0; e < 2; ++e) {
                     const int t = sl * K + 2 * q4 + e;
                     if (t < nt && in) {
-                        float x[2], v[2], dy[2], z[2], ox[2], ot[2], oz[2];
-                        unpair(raw(0, t), x[0], x[1]);
-                        unpair(raw(1, t), v[0], v[1]);
-                        unpair(raw(2, t), dy[0], dy[1]);
-                        if (gated) unpair(raw(3, t), z[0], z[1]);
-#pragma unroll
-                        for (int c = 0; c < C; ++c) {
-                            const float delta = w.du[t][2 * (g * C + c)], gy = w.gy[t][g * C + c], u = au[2 * c + e];
-                            ox[c] = fmaf(delta, u, skip[c] * gy);
-                            const float dd = fmaf(x[c], u, av[2 * c + e] * 0.69314718055994531f);   // A = a2 ln 2
-                            ot[c] = p.softplus ? dd * softplus_grad<kExact>(v[c] + bias[c]) : dd;
-                            if (gated) {
-                                const float sg = sigmoid(z[c]);
-                                oz[c] = dy[c] * fmaf(skip[c], x[c], ay[2 * c + e]) * sg * fmaf(z[c], 1.f - sg, 1.f);
-                            }
-                            dD[c] = fmaf(gy, x[c], dD[c]);
-                            db[c] += ot[c];
+                        // (one channel: both halves of a pair are it)
+                        const f32x2 x = raw(0, t), dy = raw(2, t), u = pair(au[e], C == 2 ? au[2 + e] : au[e]);
+                        f32x2 delta, gy;
+                        if (C == 2) {
+                            delta = pair(w.du[t][2 * g * C], w.du[t][2 * g * C + 2]);
+                            gy = *reinterpret_cast<const f32x2*>(&w.gy[t][g * C]);
+                        } else {
+                            delta = both(w.du[t][2 * g]);
+                            gy = both(w.gy[t][g]);
                         }
-                        auto put = [&](void* base, const float (&o)[2]) {
+                        const f32x2 ox = fma2(delta, u, mul2(skip, gy));
+                        f32x2 ot = fma2(x, u, mul2(pair(av[e], C == 2 ? av[2 + e] : av[e]), both(0.69314718055994531f)));   // A = a2 ln 2
+                        if (p.softplus) {
+                            float a, b;
+                            unpair(add2(raw(1, t), bias), a, b);
+                            ot = mul2(ot, pair(softplus_grad<kExact>(a), softplus_grad<kExact>(b)));
+                        }
+                        dD = fma2(gy, x, dD);
+                        db = add2(db, ot);
+                        auto put = [&](void* base, f32x2 o) {
                             T* r = static_cast<T*>(base) + ((int64_t)it.t0 + t0 + t) * p.D + dch;
-                            if (C == 2) store2(r, pair(o[0], o[C - 1]));
-                            else *r = from_f32<T>(o[0]);
+                            float a, b;
+                            unpair(o, a, b);
+                            if (C == 2) store2(r, o);
+                            else *r = from_f32<T>(a);
                         };
                         put(p.dx, ox);
                         put(p.ddt, ot);
-                        if (gated) put(p.dz, oz);
+                        if (gated) {
+                            // silu'(z) = s + z s (1 - s)
+                            const f32x2 z = raw(3, t);
+                            float a, b;
+                            unpair(z, a, b);
+                            const f32x2 s = pair(sigmoid(a), sigmoid(b)), zs = mul2(z, s);
+                            const f32x2 slope = fma2(zs, fma2(s, both(-1.f), both(1.f)), s);
+                            put(p.dz, mul2(mul2(dy, fma2(skip, x, pair(ay[e], C == 2 ? ay[2 + e] : ay[e]))), slope));
+                        }
                     }
                 }
                 if (!kExact) {
@@ -511,13 +522,26 @@ __global__ void __launch_bounds__(Plan<T, S>::kWarps * 32, S <= 4 ? 2 : 1) selsc
             }
             __syncthreads();
             // the CTA's terms of dB and dC: its warps' added in order
-            for (int i = threadIdx.x; i < nt * 2 * NP; i += kThreads) {
-                const int t = i / (2 * NP), v = i % (2 * NP), n = v % NP;
-                float s = 0.f;
+            for (int i = threadIdx.x; i < nt * NP / 2; i += kThreads) {
+                const int t = i / (NP / 2), v = i % (NP / 2) * 4, n = v % NP;      // four states of one token and kind
+                f32x2 s0 = 0ull, s1 = 0ull;
 #pragma unroll
-                for (int k = 0; k < P::kWarps; ++k) s += sh.w[k].dbc[t][v];
-                if (n < p.N)
-                    p.part[((((int64_t)tg * p.g.T + it.t0 + t0 + t) * p.G + grp) * 2 + v / NP) * p.N + n] = s;
+                for (int k = 0; k < P::kWarps; ++k) {
+                    const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(&sh.w[k].dbc[t][v]);
+                    s0 = add2(s0, f.x);
+                    s1 = add2(s1, f.y);
+                }
+                float* to = p.part + ((((int64_t)tg * p.g.T + it.t0 + t0 + t) * p.G + grp) * 2 + v / NP) * p.N + n;
+                if (p.N % 4 == 0) {
+                    if (n < p.N) *reinterpret_cast<ulonglong2*>(to) = make_ulonglong2(s0, s1);
+                } else {
+                    float f[4];
+                    unpair(s0, f[0], f[1]);
+                    unpair(s1, f[2], f[3]);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (n + k < p.N) to[k] = f[k];
+                }
             }
         }
         if (it.first && p.dinit != nullptr)
@@ -529,18 +553,19 @@ __global__ void __launch_bounds__(Plan<T, S>::kWarps * 32, S <= 4 ? 2 : 1) selsc
 #pragma unroll
     for (int c = 0; c < C; ++c)
         store_states_row<S>(dA[c], p.partA + ((int64_t)slot * p.D + dch + c) * p.N, n0, p.N, in);
+    float end[4];
+    unpair(dD, end[0], end[1]);
+    unpair(db, end[2], end[3]);
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int bit = 1; bit < 4; bit *= 2) {
-            dD[c] += __shfl_xor_sync(0xffffffffu, dD[c], bit);
-            db[c] += __shfl_xor_sync(0xffffffffu, db[c], bit);
+        for (int bit = 1; bit < 4; bit *= 2) end[i] += __shfl_xor_sync(0xffffffffu, end[i], bit);
+    if (q4 == 0 && in)
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            p.partD[(int64_t)slot * 2 * p.D + dch + c] = end[c];
+            p.partD[((int64_t)slot * 2 + 1) * p.D + dch + c] = end[2 + c];
         }
-        if (q4 == 0 && in) {
-            p.partD[(int64_t)slot * 2 * p.D + dch + c] = dD[c];
-            p.partD[((int64_t)slot * 2 + 1) * p.D + dch + c] = db[c];
-        }
-    }
 }
 
 // dB and dC: the tiles' terms in order; 0 in rows of no sequence.
