@@ -40,6 +40,7 @@ namespace ssd {
 namespace {
 
 constexpr int kChunk = kScanChunk;
+static_assert(kChunk == kMakeUp, "a chunk is what make_up is for");
 
 template <typename T, int S> struct Plan {     // N <= 4 S
     static constexpr int C = S <= 4 ? 2 : 1;   // channels a lane
@@ -284,6 +285,7 @@ __global__ void __launch_bounds__(Plan<T, S>::kWarps * 32, S <= 4 ? 2 : 1) selsc
                 const T* r = &w.raw[buf][k][t][g * C];
                 return C == 2 ? load2(r) : both(to_f32(*r));
             };
+            f32x2 sum = 0ull;                          // of delta over the chunk
 #pragma unroll
             for (int e = 0; e < kChunk / 4; ++e) {
                 const int t = 4 * e + q4;
@@ -294,6 +296,7 @@ __global__ void __launch_bounds__(Plan<T, S>::kWarps * 32, S <= 4 ? 2 : 1) selsc
                     dl = softplus2<kExact>(v0, v1);
                 }
                 if (t >= nt) dl = 0ull;                // rows past the end leave the state alone (their x and dout are 0)
+                sum = add2(sum, dl);
                 const f32x2 u = mul2(dl, raw(0, t)), gy = gated ? mul2(raw(2, t), silu2(raw(3, t))) : raw(2, t);
                 float u0, u1;
                 unpair(dl, v0, v1);
@@ -519,6 +522,16 @@ __global__ void __launch_bounds__(Plan<T, S>::kWarps * 32, S <= 4 ? 2 : 1) selsc
                             }
                 }
                 clear();
+            }
+            if (nt == kChunk) {
+                float of[2];
+                unpair(sum, of[0], of[1]);
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+#pragma unroll
+                    for (int bit = 1; bit < 4; bit *= 2) of[c] += __shfl_xor_sync(0xffffffffu, of[c], bit);
+                    make_up<H>(qv[c], a2[c], of[c]);
+                }
             }
             __syncthreads();
             // the CTA's terms of dB and dC: its warps' added in order

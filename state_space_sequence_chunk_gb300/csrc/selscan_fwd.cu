@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(kWarps * 32, S == 16 && LPC == 1 ? 6 : 1) sels
         Bp += kTok * Bs;
         if (!SUMS) Cp += kTok * p.Cs;
     };
-    f32x2 total = 0ull;
+    f32x2 total = 0ull, recent = 0ull;      // sums of delta: the range's, the last sixteen tokens'
     struct Own {
         f32x2 x[kOwn / 2], gate[kOwn / 2];   // of its own tokens, in pairs
         float2 du[LPC > 1 ? 1 : kTok];       // a lane with all of a channel: delta and u
@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(kWarps * 32, S == 16 && LPC == 1 ? 6 : 1) sels
             float a, b, c, e;
             unpair(dl[i], a, b);
             dl[i] = pair(t < it.len ? a : 0.f, t + LPC < it.len ? b : 0.f);
-            if (SUMS) total = add2(total, dl[i]);
+            recent = add2(recent, dl[i]);
             unpair(dl[i], a, b);
             unpair(REV ? mul2(o.x[i], o.gate[i]) : mul2(dl[i], o.x[i]), c, e);
             if (LPC > 1) {                   // the channel's other lanes need them too
@@ -300,6 +300,16 @@ __global__ void __launch_bounds__(kWarps * 32, S == 16 && LPC == 1 ? 6 : 1) sels
         prefetch(t0 + kTok);
         __syncwarp();
         tokens(t0, own, full);
+        if ((t0 + kTok) % kMakeUp == 0) {
+            float sum, odd;
+            unpair(recent, sum, odd);
+            sum += odd;
+#pragma unroll
+            for (int bit = LPC / 2; bit > 0; bit /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, bit);
+            make_up<S / 2>(h, a2, sum);
+            if (SUMS) total = add2(total, recent);
+            recent = 0ull;
+        }
     };
     int t0 = 0;
     for (; t0 + kTok <= it.len; t0 += kTok) step_of(t0, std::true_type());
@@ -308,7 +318,7 @@ __global__ void __launch_bounds__(kWarps * 32, S == 16 && LPC == 1 ? 6 : 1) sels
     if (SUMS) {
         store_row<S>(h, p.agg + ((int64_t)item * p.D + d) * p.N, n0, p.N, in);
         float sum, odd;
-        unpair(total, sum, odd);
+        unpair(add2(total, recent), sum, odd);
         sum += odd;
 #pragma unroll
         for (int bit = LPC / 2; bit > 0; bit /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, bit);

@@ -58,7 +58,8 @@ __global__ void __launch_bounds__(kThreads) selscan_step(const __grid_constant__
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        h[i] = fmaf(ex2(delta * scan_rate(a[i])), h[i], u * B[i]);
+        // h exp(delta A) as h + h (exp(delta A) - 1): thousands of calls multiply a state, one after another
+        h[i] = fmaf(u, B[i], fmaf(h[i], expm1f(delta * fmaxf(a[i], -1e37f)), h[i]));
         if (n + i < p.N) s = fmaf(C[i], h[i], s);
     }
     if (vec) {
