@@ -706,13 +706,28 @@ def block_norm_bwd(r, y, w_pre, dr_out, dn, rstd, z=None, w_post=None, alpha=Non
     return g
 
 
-def _here(x, *others):
-    """The calls below launch on the current device: operands of another one, or of two,
-    are refused."""
-    dev = torch.cuda.current_device() if x.is_cuda else -1
-    for t in (x,) + others:
-        if t is not None and (not t.is_cuda or t.get_device() != dev):
-            raise ValueError("tensors must be CUDA tensors on the current device")
+# The calls below launch on the current device: operands of another one, or of the host,
+# are refused where their addresses are taken.
+def _here(t, dev):
+    """Address of a contiguous tensor on device `dev` (None passes)."""
+    if t is None:
+        return None
+    if t.get_device() != dev or not t.is_contiguous():
+        raise ValueError("tensors must be contiguous CUDA tensors on the current device")
+    return t.data_ptr()
+
+
+def _rows_here(t, inner: int, dev):
+    """_rows, of a tensor on device `dev`."""
+    if t.get_device() != dev:
+        raise ValueError("tensors must be CUDA tensors on the current device")
+    if t.is_contiguous():
+        return t.data_ptr(), inner
+    return _rows(t, inner)
+
+
+def _stream_of(dev) -> int:
+    return _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream(dev).cuda_stream
 
 
 def _seqs(cu_seqlens, nseqs):
@@ -734,17 +749,19 @@ def _new(t, name, dtype, shape, device):
     return torch.empty(shape, dtype=dtype, device=device) if t is None else _typed(t, name, dtype, shape)
 
 
-def _short_conv_dims(x, weight, bias, activation, nseqs):
+def _short_conv_dims(x, weight, bias, activation, nseqs, dev):
     if x.dim() != 2 or weight.dim() != 2:
         raise ValueError("x must be [tokens, dim] and weight [dim, width]")
-    if activation not in ACTIVATIONS:
+    act = ACTIVATIONS.get(activation)
+    if act is None:
         raise ValueError(f"activation must be one of {list(ACTIVATIONS)}, got {activation!r}")
     T, D = x.shape
     W = weight.shape[1]
     _typed(weight, "weight", torch.float32, (D, W))
     _typed(bias, "bias", torch.float32, (D,))
-    xp, xs = _rows(x, D)
-    return ShortConvDims(nseqs, T, D, W, xs, ACTIVATIONS[activation], _dtype_code(x, "x"), 0), xp
+    xp, xs = _rows_here(x, D, dev)
+    return (ShortConvDims(nseqs, T, D, W, xs, act, _dtype_code(x, "x"), 0), T, D, W,
+            (xp, _here(weight, dev), _here(bias, dev)))
 
 
 def short_conv_fwd(x, weight, bias=None, activation=None, cu_seqlens=None, init_state=None,
@@ -761,15 +778,13 @@ def short_conv_fwd(x, weight, bias=None, activation=None, cu_seqlens=None, init_
     """
     lib = _lib or load_library()
     n = _seqs(cu_seqlens, nseqs)
-    _here(x, weight, bias, cu_seqlens, init_state, out, final_out)
-    d, xp = _short_conv_dims(x, weight, bias, activation, n)
-    T, D = x.shape
-    state = (n, weight.shape[1] - 1, D)
-    _typed(init_state, "init_state", x.dtype, state)
+    dev = torch.cuda.current_device()
+    d, T, D, W, args = _short_conv_dims(x, weight, bias, activation, n, dev)
+    _typed(init_state, "init_state", x.dtype, (n, W - 1, D))
     o = _new(out, "out", x.dtype, (T, D), x.device)
-    fin = _new(final_out, "final_out", x.dtype, state, x.device) if return_final_state else None
-    _check(lib.ssd_short_conv_fwd(ctypes.byref(d), xp, _addr(weight), _addr(bias), _addr(cu_seqlens),
-                                  _addr(init_state), _addr(o), _addr(fin), _stream_int()))
+    fin = _new(final_out, "final_out", x.dtype, (n, W - 1, D), x.device) if return_final_state else None
+    _check(lib.ssd_short_conv_fwd(ctypes.byref(d), *args, _here(cu_seqlens, dev), _here(init_state, dev),
+                                  _here(o, dev), _here(fin, dev), _stream_of(dev)))
     return o, fin
 
 
@@ -780,22 +795,20 @@ def short_conv_bwd(x, weight, dout, bias=None, activation=None, cu_seqlens=None,
     an init_state)."""
     lib = _lib or load_library()
     n = _seqs(cu_seqlens, nseqs)
-    _here(x, weight, dout, bias, cu_seqlens, init_state, dfinal_state, workspace)
-    d, xp = _short_conv_dims(x, weight, bias, activation, n)
-    T, D = x.shape
-    state = (n, weight.shape[1] - 1, D)
+    dev = torch.cuda.current_device()
+    d, T, D, W, args = _short_conv_dims(x, weight, bias, activation, n, dev)
+    state = (n, W - 1, D)
     _typed(dout, "dout", x.dtype, (T, D))
     _typed(init_state, "init_state", x.dtype, state)
     _typed(dfinal_state, "dfinal_state", x.dtype, state)
     new = lambda shape, dt: torch.empty(shape, dtype=dt, device=x.device)
-    g = {"dx": new((T, D), x.dtype), "dweight": new(weight.shape, torch.float32),
+    g = {"dx": new((T, D), x.dtype), "dweight": new((D, W), torch.float32),
          "dbias": None if bias is None else new((D,), torch.float32),
          "dinit_state": None if init_state is None else new(state, x.dtype)}
-    workspace, nbytes = _space(int(lib.ssd_short_conv_bwd_workspace_bytes(ctypes.byref(d))), workspace, x.device)
-    _check(lib.ssd_short_conv_bwd(ctypes.byref(d), xp, _addr(weight), _addr(bias), _addr(cu_seqlens),
-                                  _addr(init_state), _addr(dout), _addr(dfinal_state), _addr(g["dx"]),
-                                  _addr(g["dweight"]), _addr(g["dbias"]), _addr(g["dinit_state"]),
-                                  _addr(workspace), nbytes, _stream_int()))
+    workspace, nbytes = _space(lib.ssd_short_conv_bwd_workspace_bytes(ctypes.byref(d)), workspace, x.device)
+    _check(lib.ssd_short_conv_bwd(ctypes.byref(d), *args, _here(cu_seqlens, dev), _here(init_state, dev),
+                                  _here(dout, dev), _here(dfinal_state, dev), *(_here(t, dev) for t in g.values()),
+                                  _here(workspace, dev), nbytes, _stream_of(dev)))
     return g
 
 
@@ -806,18 +819,18 @@ def short_conv_step(x, weight, cache, bias=None, activation=None, slots=None, ou
     b's slot is b without it; a negative one marks a row without a stream, whose output is
     0; no slot may occur twice).  Returns out [b, dim]."""
     lib = _lib or load_library()
-    _here(x, weight, cache, bias, slots, out)
-    d, xp = _short_conv_dims(x, weight, bias, activation, x.shape[0])
-    b, D = x.shape
-    _typed(cache, "cache", x.dtype, (cache.shape[0], weight.shape[1] - 1, D))
+    dev = torch.cuda.current_device()
+    d, b, D, W, args = _short_conv_dims(x, weight, bias, activation, x.shape[0], dev)
+    n = cache.shape[0]
+    _typed(cache, "cache", x.dtype, (n, W - 1, D))
     _typed(slots, "slots", torch.int32, (b,))
     o = _new(out, "out", x.dtype, (b, D), x.device)
-    _check(lib.ssd_short_conv_step(ctypes.byref(d), xp, _addr(weight), _addr(bias), _addr(slots), _addr(cache),
-                                   cache.shape[0], _addr(o), _stream_int()))
+    _check(lib.ssd_short_conv_step(ctypes.byref(d), *args, _here(slots, dev), _here(cache, dev), n, _here(o, dev),
+                                   _stream_of(dev)))
     return o
 
 
-def _selscan_dims(x, dt, A, B, C, D, z, dt_bias, dt_softplus, nseqs, max_seqlen):
+def _selscan_dims(x, dt, A, B, C, D, z, dt_bias, dt_softplus, nseqs, max_seqlen, dev):
     if x.dim() != 2 or A.dim() != 2 or B.dim() != 3:
         raise ValueError("x must be [tokens, dim], A [dim, N], B and C [tokens, G, N]")
     T, W = x.shape
@@ -829,11 +842,12 @@ def _selscan_dims(x, dt, A, B, C, D, z, dt_bias, dt_softplus, nseqs, max_seqlen)
     _typed(C, "C", x.dtype, (T, G, N))
     _typed(D, "D", torch.float32, (W,))
     _typed(dt_bias, "dt_bias", torch.float32, (W,))
-    (xp, xs), (tp, ts), (Bp, Bs), (Cp, Cs) = _rows(x, W), _rows(dt, W), _rows(B, G * N), _rows(C, G * N)
-    zp, zs = (None, 0) if z is None else _rows(z, W)
+    (xp, xs), (tp, ts) = _rows_here(x, W, dev), _rows_here(dt, W, dev)
+    (Bp, Bs), (Cp, Cs) = _rows_here(B, G * N, dev), _rows_here(C, G * N, dev)
+    zp, zs = (None, 0) if z is None else _rows_here(z, W, dev)
     d = SelscanDims(nseqs, T, W, N, G, xs, ts, zs, Bs, Cs, max_seqlen, 1 if dt_softplus else 0,
                     _dtype_code(x, "x"), 0)
-    return d, (xp, tp, _addr(A), Bp, Cp, _addr(D), zp, _addr(dt_bias))
+    return d, T, W, N, (xp, tp, _here(A, dev), Bp, Cp, _here(D, dev), zp, _here(dt_bias, dev))
 
 
 def selscan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus: bool = False,
@@ -857,17 +871,15 @@ def selscan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus: bool 
     """
     lib = _lib or load_library()
     n = _seqs(cu_seqlens, nseqs)
-    _here(x, dt, A, B, C, D, z, dt_bias, cu_seqlens, init_state, workspace, out, final_out)
-    d, args = _selscan_dims(x, dt, A, B, C, D, z, dt_bias, dt_softplus, n, max_seqlen)
-    T, W = x.shape
-    N = A.shape[1]
+    dev = torch.cuda.current_device()
+    d, T, W, N, args = _selscan_dims(x, dt, A, B, C, D, z, dt_bias, dt_softplus, n, max_seqlen, dev)
     _typed(init_state, "init_state", torch.float32, (n, W, N))
     y = _new(out, "out", x.dtype, (T, W), x.device)
     fin = _new(final_out, "final_out", torch.float32, (n, W, N), x.device) if return_final_state else None
     states = torch.empty((T // SELSCAN_CHUNK + n, W, N), dtype=torch.float32, device=x.device) if return_states else None
-    workspace, nbytes = _space(int(lib.ssd_selscan_workspace_bytes(ctypes.byref(d), 0)), workspace, x.device)
-    _check(lib.ssd_selscan_fwd(ctypes.byref(d), *args, _addr(cu_seqlens), _addr(init_state), _addr(y), _addr(fin),
-                               _addr(states), _addr(workspace), nbytes, _stream_int()))
+    workspace, nbytes = _space(lib.ssd_selscan_workspace_bytes(ctypes.byref(d), 0), workspace, x.device)
+    _check(lib.ssd_selscan_fwd(ctypes.byref(d), *args, _here(cu_seqlens, dev), _here(init_state, dev), _here(y, dev),
+                               _here(fin, dev), _here(states, dev), _here(workspace, dev), nbytes, _stream_of(dev)))
     return (y, fin, states) if return_states else (y, fin)
 
 
@@ -879,10 +891,8 @@ def selscan_bwd(x, dt, A, B, C, dout, states, D=None, z=None, dt_bias=None, dt_s
     where the input is None) and dinit_state (None unless ``return_dinit``)."""
     lib = _lib or load_library()
     n = _seqs(cu_seqlens, nseqs)
-    _here(x, dt, A, B, C, dout, states, D, z, dt_bias, cu_seqlens, dfinal_state, workspace)
-    d, args = _selscan_dims(x, dt, A, B, C, D, z, dt_bias, dt_softplus, n, max_seqlen)
-    T, W = x.shape
-    N = A.shape[1]
+    dev = torch.cuda.current_device()
+    d, T, W, N, args = _selscan_dims(x, dt, A, B, C, D, z, dt_bias, dt_softplus, n, max_seqlen, dev)
     _typed(dout, "dout", x.dtype, (T, W))
     _typed(states, "states", torch.float32, (T // SELSCAN_CHUNK + n, W, N))
     _typed(dfinal_state, "dfinal_state", torch.float32, (n, W, N))
@@ -890,10 +900,10 @@ def selscan_bwd(x, dt, A, B, C, dout, states, D=None, z=None, dt_bias=None, dt_s
     g = {"dx": like(x), "ddt": like(dt), "dA": like(A), "dB": like(B), "dC": like(C), "dD": like(D), "dz": like(z),
          "ddt_bias": like(dt_bias),
          "dinit_state": torch.empty((n, W, N), dtype=torch.float32, device=x.device) if return_dinit else None}
-    workspace, nbytes = _space(int(lib.ssd_selscan_workspace_bytes(ctypes.byref(d), 1)), workspace, x.device)
-    _check(lib.ssd_selscan_bwd(ctypes.byref(d), *args, _addr(cu_seqlens), _addr(states), _addr(dout),
-                               _addr(dfinal_state), *(_addr(t) for t in g.values()), _addr(workspace), nbytes,
-                               _stream_int()))
+    workspace, nbytes = _space(lib.ssd_selscan_workspace_bytes(ctypes.byref(d), 1), workspace, x.device)
+    _check(lib.ssd_selscan_bwd(ctypes.byref(d), *args, _here(cu_seqlens, dev), _here(states, dev), _here(dout, dev),
+                               _here(dfinal_state, dev), *(_here(t, dev) for t in g.values()), _here(workspace, dev),
+                               nbytes, _stream_of(dev)))
     return g
 
 
@@ -903,12 +913,12 @@ def selscan_step(x, dt, A, B, C, cache, D=None, z=None, dt_bias=None, dt_softplu
     B, C [b, G, N]; ``cache`` [nslots, dim, N] float32 holds the states and is updated in
     place; ``slots`` as for short_conv_step.  Returns y [b, dim]."""
     lib = _lib or load_library()
-    _here(x, dt, A, B, C, cache, D, z, dt_bias, slots, out)
-    d, args = _selscan_dims(x, dt, A, B, C, D, z, dt_bias, dt_softplus, x.shape[0], 0)
-    b, W = x.shape
-    _typed(cache, "cache", torch.float32, (cache.shape[0], W, A.shape[1]))
+    dev = torch.cuda.current_device()
+    d, b, W, N, args = _selscan_dims(x, dt, A, B, C, D, z, dt_bias, dt_softplus, x.shape[0], 0, dev)
+    n = cache.shape[0]
+    _typed(cache, "cache", torch.float32, (n, W, N))
     _typed(slots, "slots", torch.int32, (b,))
     y = _new(out, "out", x.dtype, (b, W), x.device)
-    _check(lib.ssd_selscan_step(ctypes.byref(d), *args, _addr(slots), _addr(cache), cache.shape[0], _addr(y),
-                                _stream_int()))
+    _check(lib.ssd_selscan_step(ctypes.byref(d), *args, _here(slots, dev), _here(cache, dev), n, _here(y, dev),
+                                _stream_of(dev)))
     return y

@@ -53,25 +53,26 @@ ssd_status make(const ssd_selscan_dims* d, bool packed, bool backward, Scan* out
 
     // A sequence is cut where a chain of its whole length would keep the other SMs waiting.  A
     // warp by itself takes 104 ns a token; the cut's two passes take 225 ps for each token
-    // and warp when all SMs work, and some 50 us of launches and ramps.  Whole and cut, us:
-    // 16 states, 8192 tokens of 2048 channels (64 warps) 860 and 146, the same in 6
-    // sequences 214 and 148; 16384 tokens of 5120 in 12 sequences 421 and 592; 16384 of 2048
-    // in 40 195 and 271; 512 of 5120 61 and 71.
-    // Backwards a CTA of 64 (32, 16) channels takes 295 ns a token by itself, and the cut's
-    // passes 1.7 ns for each token and CTA: 8192 tokens of 2048 channels 2416 and 470 (before the last steps), in 6
-    // sequences 650 and 454, 16384 of 2048 in 40 783 and 853.
+    // and warp when all SMs work, and some 25 us of launches and ramps.  Whole and cut, us, 16
+    // states: 256 tokens of 2048 channels (64 warps) 35 and 39, 512 of 5120 64 and 46, 2048 of
+    // 2048 in 4 sequences 94 and 59, 8192 of 2048 860 and 154, in 6 sequences 224 and 154;
+    // 16384 of 5120 in 12 431 and 632; 16384 of 2048 in 40 207 and 281; 4096 of 768, 64 states, in 8
+    // 182 and 214.  Backwards a CTA of 64 (32, 16) channels takes 295 ns a token by itself, and
+    // the cut's passes 1.7 ns for each token and CTA: the same sizes 87 and 70, 162 and 113, 263 and
+    // 153, 2400 and 460, 650 and 460, -, 790 and 890, 444 and 459.
     const int64_t bt = selscan_bwd_channels((int)q.N), tiles = (p.cpg + bt - 1) / bt;
     const int64_t warps = q.G * ((p.cpg * (q.N <= 16 ? 1 : q.N <= 32 ? 2 : 4) + 31) / 32);
     const int64_t sms = sm_count(), work = q.T * (backward ? tiles * q.G : warps);
     int64_t longest = packed ? (d->max_seqlen ? d->max_seqlen : q.T) : g.L;
     if (longest > q.T) longest = q.T;
     g.R = INT_MAX;
-    if (q.n > 0 && longest > (backward ? work / (sms * 8 / 7) + 136 : work / (3 * sms) + 512)) {
-        // several ranges for each warp that is resident, but not shorter than 128 tokens
-        // (8192 tokens of 2048 channels: ranges of 128, 256, 512 tokens 146, 160, 197 us,
-        // backwards 454, 474; 65536 of 1536: 128, 384, 512: 769, 728, 755)
-        int64_t R = (work / ((backward ? 13 : 54) * sms) + 31) / 32 * 32;
-        R = R < 128 ? 128 : R > 512 ? 512 : R;
+    if (q.n > 0 && longest > (backward ? work / (sms * 8 / 7) + 136 : work / (3 * sms) + 256)) {
+        // several ranges for each warp that is resident, but not too short (2048 tokens of 1536
+        // channels: ranges of 32, 64, 96, 128, 256 tokens 51, 49, 48, 55, 65 us, backwards 124, 122,
+        // 122, 129, 151; 8192 of 2048: 64, 96, 128 160, 148, 150; 65536 of 1536: 128, 384, 512: 799, 759, 790)
+        int64_t R = (work / ((backward ? 13 : 54) * sms) + 16) / 32 * 32;
+        const int64_t least = backward ? 64 : 96;
+        R = R < least ? least : R > 512 ? 512 : R;
         if (R < longest) g.R = (int)R;
     }
     const bool cut = g.R <= q.T;

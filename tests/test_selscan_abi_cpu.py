@@ -206,34 +206,32 @@ def operands(**kw):
     (dict(z=Stand(torch.zeros(5, 16))), ValueError)])
 def test_scan_binding_refuses(kw, error):
     with pytest.raises(error):
-        ssd._selscan_dims(**operands(**kw), dt_softplus=True, nseqs=1, max_seqlen=0)
+        ssd._selscan_dims(**operands(**kw), dt_softplus=True, nseqs=1, max_seqlen=0, dev=0)
 
 
 def test_scan_binding_takes_column_ranges():
     wide = torch.zeros(6, 100)
-    d, _ = ssd._selscan_dims(**operands(x=Stand(wide[:, 32:48]), B=Stand(wide[:, 3:11].view(6, 2, 4))), dt_softplus=False,
-                             nseqs=1, max_seqlen=0)
+    d = ssd._selscan_dims(**operands(x=Stand(wide[:, 32:48]), B=Stand(wide[:, 3:11].view(6, 2, 4))), dt_softplus=False,
+                          nseqs=1, max_seqlen=0, dev=0)[0]
     assert (d.x_stride, d.B_stride, d.C_stride, d.dt_softplus) == (100, 100, 8, 0)
 
 
 def test_conv_binding_refuses():
     x, w, b = Stand(torch.zeros(6, 16)), Stand(torch.zeros(16, 4)), Stand(torch.zeros(16))
     with pytest.raises(ValueError):
-        ssd._short_conv_dims(x, w, b, "relu", 1)
+        ssd._short_conv_dims(x, w, b, "relu", 1, 0)
     with pytest.raises(ValueError):
-        ssd._short_conv_dims(Stand(torch.zeros(1, 16).expand(6, 16)), w, b, None, 1)
+        ssd._short_conv_dims(Stand(torch.zeros(1, 16).expand(6, 16)), w, b, None, 1, 0)
     with pytest.raises(ValueError):
-        ssd._short_conv_dims(x, Stand(torch.zeros(8, 4)), b, None, 1)
+        ssd._short_conv_dims(x, Stand(torch.zeros(8, 4)), b, None, 1, 0)
     with pytest.raises(TypeError):
-        ssd._short_conv_dims(x, w, Stand(torch.zeros(16, dtype=torch.bfloat16)), None, 1)
+        ssd._short_conv_dims(x, w, Stand(torch.zeros(16, dtype=torch.bfloat16)), None, 1, 0)
 
 
-def test_operands_of_another_device_are_refused(monkeypatch):
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
-    x = Stand(torch.zeros(2))
-    ssd._here(x, None, Stand(torch.zeros(2)))
-    for bad in (Stand(torch.zeros(2), 1), torch.zeros(2)):
+@pytest.mark.parametrize("name", ["x", "dt", "A", "B", "C", "D", "z", "dt_bias"])
+def test_operands_of_another_device_are_refused(name):
+    for bad in (Stand(operands()[name].t, 1), operands()[name].t):      # another GPU's, the host's
         with pytest.raises(ValueError):
-            ssd._here(x, bad)
-        with pytest.raises(ValueError):
-            ssd._here(bad, x)
+            ssd._selscan_dims(**operands(**{name: bad}), dt_softplus=True, nseqs=1, max_seqlen=0, dev=0)
+    with pytest.raises(ValueError):
+        ssd._selscan_dims(**operands(), dt_softplus=True, nseqs=1, max_seqlen=0, dev=1)   # the current one is another
