@@ -283,6 +283,7 @@ cudaError_t launch_selscan_bwd(const ScanParams& p, int dtype, cudaStream_t stre
 
 struct ScanStep {
     int D, N, G, cpg, softplus;
+    int vecB, vecC;      // as in ScanParams
     int64_t batch, nslots;
     const void *x, *dt, *z, *B, *C;
     int64_t xs, dts, zs, Bs, Cs;

@@ -267,6 +267,7 @@ ssd_status ssd_selscan_step(const ssd_selscan_dims* d, const void* x, const void
     const ScanParams& p = q.p;
     ScanStep t = {};
     t.D = p.D; t.N = p.N; t.G = p.G; t.cpg = p.cpg; t.softplus = p.softplus;
+    t.vecB = vectors(q, B, p.Bs); t.vecC = vectors(q, C, p.Cs);
     t.batch = q.n; t.nslots = nslots;
     t.x = x; t.dt = dt; t.z = z; t.B = B; t.C = C;
     t.xs = p.xs; t.dts = p.dts; t.zs = p.zs; t.Bs = p.Bs; t.Cs = p.Cs;

@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(kWarps * 32, S == 16 && LPC == 1 ? 6 : 1) sels
         const int64_t first = row0 * (k == 0 ? (REV ? p.D : p.xs) : k == 1 ? p.dts : p.zs);
         const bool ok = k < (gated ? 3 : 2) && c0 + c < p.cpg;
         crow[i] = ok ? r : 1 << 30;
-        src[i] = ok ? from + first + r * stride + (int64_t)grp * p.cpg + c0 + c : static_cast<const T*>(p.x);
+        src[i] = ok ? from + first + r * stride + (int64_t)grp * p.cpg + c0 + c : reinterpret_cast<const T*>(p.A);   // (x may be NULL)
         step[i] = ok ? kTok * stride : 0;
         dst[i] = k < 3 ? smem_u32(&w.raw[0][0][0][0]) + 16 * v : 0u;
     }

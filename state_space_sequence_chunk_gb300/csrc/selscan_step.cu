@@ -2,83 +2,144 @@
 //
 // For each row of the batch with a slot, per channel with N states:
 //     h <- exp(delta A) h + delta x B (in place at cache[slot]),  y = (C.h + D x) silu(z).
-// Bound by the states' traffic, 8 N bytes a channel, read once and written once.  A
-// lane holds four states of one channel, so that a warp moves 512 contiguous bytes of
-// the cache; the channel's own numbers are made by each of its lanes, which costs less
-// than handing them round.
+// Bound by the states' traffic, 8 N bytes a channel, read once and written once.  LPC
+// lanes hold a channel's states, four each, and V channels one after another: a warp
+// moves 512 contiguous bytes of the cache at a time, V of them in flight, B and C are read
+// once for V channels, and each of V lanes makes the numbers of one channel for the others.
 #include "selscan.cuh"
 
 namespace ssd {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kWarps = 4;
+
+__device__ __forceinline__ float max_nan(float a, float b) {    // a NaN stays one
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+// h exp(e).  Thousands of calls multiply a state, one after another, so near 1 it is h + h (exp(e) - 1),
+// by the Taylor polynomial (to e^6: off by 1.2e-8 of h at most), whose errors have no side in
+// common; where more goes in a token, by the fast exponential, with what rounds away of e log2(e)
+// added back: what is left of a large state keeps its own precision.
+__device__ __forceinline__ f32x2 decayed(f32x2 h, f32x2 e) {
+    float e0, e1, q0, q1, h0, h1;
+    unpair(e, e0, e1);
+    e0 = max_nan(e0, -200.f);                // (every power from here on is 0)
+    e1 = max_nan(e1, -200.f);
+    e = pair(e0, e1);
+    const f32x2 q = mul2(e, both(-kLog2e));
+    const f32x2 lo = fma2(e, both(1.925963033500e-8f), fma2(e, both(kLog2e), q));     // log2(e) - kLog2e
+    unpair(q, q0, q1);
+    const f32x2 x0 = pair(ex2(-q0), ex2(-q1)), x = fma2(x0, mul2(lo, both(0.69314718f)), x0);
+    f32x2 m = fma2(e, both(1.f / 720), both(1.f / 120));
+    m = fma2(e, m, both(1.f / 24));
+    m = fma2(e, m, both(1.f / 6));
+    m = fma2(e, m, both(0.5f));
+    m = mul2(e, fma2(e, m, both(1.f)));
+    const bool n0 = fabsf(e0) < 0.25f, n1 = fabsf(e1) < 0.25f;
+    float m0, m1, x1, x2;
+    unpair(m, m0, m1);
+    unpair(x, x1, x2);
+    unpair(h, h0, h1);
+    return fma2(h, pair(n0 ? m0 : x1, n1 ? m1 : x2), pair(n0 ? h0 : 0.f, n1 ? h1 : 0.f));
+}
 
 // LPC lanes hold a channel: N <= 4 LPC
 template <typename T, int LPC>
-__global__ void __launch_bounds__(kThreads) selscan_step(const __grid_constant__ ScanStep p) {
-    constexpr int kCh = kThreads / LPC;
+__global__ void __launch_bounds__(kWarps * 32) selscan_step(const __grid_constant__ ScanStep p) {
+    constexpr int V = LPC < 4 ? LPC : 4, kWide = 32 / LPC, kTile = V * kWide;   // channels of a lane, abreast, of a warp
     constexpr bool kExact = sizeof(T) == 4;
-    const int ctas = (p.D + kCh - 1) / kCh, b = blockIdx.x / ctas;
-    const int ch = (blockIdx.x - b * ctas) * kCh + threadIdx.x / LPC, part = threadIdx.x % LPC, n = 4 * part;
-    const bool in = ch < p.D;
-    const int d = min(ch, p.D - 1);
+    const int lane = threadIdx.x & 31, part = lane % LPC, n = 4 * part;
+    const int tpg = (p.cpg + kTile - 1) / kTile, tiles = tpg * p.G;
+    const int64_t item = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    if (item >= p.batch * tiles) return;
+    const int b = (int)(item / tiles), tile = (int)(item - (int64_t)b * tiles), grp = tile / tpg;
+    const int c0 = (tile - grp * tpg) * kTile + lane / LPC;
+    const int own = c0 + part % V * kWide;               // the channel whose numbers this lane makes
+    const bool in = own < p.cpg;
+    const int d = grp * p.cpg + min(own, p.cpg - 1);
     const int64_t slot = p.slots != nullptr ? p.slots[b] : b;
     T* y = static_cast<T*>(p.y) + (int64_t)b * p.D + d;
-    if (slot < 0 || slot >= p.nslots) {              // no stream in this row: a zero output
-        if (in && part == 0) *y = from_f32<T>(0.f);
+    if (slot < 0 || slot >= p.nslots) {                  // no stream in this row: a zero output
+        if (in && part < V) *y = from_f32<T>(0.f);
         return;
     }
-    const bool vec = p.N % 4 == 0, mine = in && n < p.N;
-    float* at = p.cache + (slot * p.D + d) * p.N + n;
-    const float* A = p.A + (int64_t)d * p.N + n;
-    float h[4], a[4];
-    if (vec) {
-        const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
-        const float4 hv = mine ? *reinterpret_cast<const float4*>(at) : z;
-        const float4 av = mine ? __ldg(reinterpret_cast<const float4*>(A)) : z;
-        h[0] = hv.x; h[1] = hv.y; h[2] = hv.z; h[3] = hv.w;
-        a[0] = av.x; a[1] = av.y; a[2] = av.z; a[3] = av.w;
-    } else {
+    const bool vec = p.N % 4 == 0;
+    float* at = p.cache + (slot * p.D + grp * p.cpg + c0) * p.N + n;
+    const float* A = p.A + (int64_t)(grp * p.cpg + c0) * p.N + n;
+    const int64_t step = (int64_t)kWide * p.N;           // from one of the lane's channels to the next
+    f32x2 h[V][2], a[V][2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const bool ok = mine && n + i < p.N;
-            h[i] = ok ? at[i] : 0.f;
-            a[i] = ok ? A[i] : 0.f;
+    for (int j = 0; j < V; ++j) {
+        const bool ok = c0 + j * kWide < p.cpg;
+        if (vec) {
+            ulonglong2 hv = make_ulonglong2(0ull, 0ull), av = hv;
+            if (ok && n < p.N) {
+                hv = *reinterpret_cast<const ulonglong2*>(at + j * step);
+                av = __ldg(reinterpret_cast<const ulonglong2*>(A + j * step));
+            }
+            h[j][0] = hv.x; h[j][1] = hv.y; a[j][0] = av.x; a[j][1] = av.y;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const bool ok0 = ok && n + 2 * i < p.N, ok1 = ok && n + 2 * i + 1 < p.N;
+                h[j][i] = pair(ok0 ? at[j * step + 2 * i] : 0.f, ok1 ? at[j * step + 2 * i + 1] : 0.f);
+                a[j][i] = pair(ok0 ? __ldg(A + j * step + 2 * i) : 0.f, ok1 ? __ldg(A + j * step + 2 * i + 1) : 0.f);
+            }
         }
     }
-    const int grp = d / p.cpg;
-    const float4 Bv = load_states(static_cast<const T*>(p.B) + b * p.Bs + (int64_t)grp * p.N, n, p.N, false);
-    const float4 Cv = load_states(static_cast<const T*>(p.C) + b * p.Cs + (int64_t)grp * p.N, n, p.N, false);
-    const float B[4] = {Bv.x, Bv.y, Bv.z, Bv.w}, C[4] = {Cv.x, Cv.y, Cv.z, Cv.w};
+    const float4 Bv = load_states(static_cast<const T*>(p.B) + b * p.Bs + (int64_t)grp * p.N, n, p.N, p.vecB != 0);
+    const float4 Cv = load_states(static_cast<const T*>(p.C) + b * p.Cs + (int64_t)grp * p.N, n, p.N, p.vecC != 0);
+    const f32x2 B[2] = {pair(Bv.x, Bv.y), pair(Bv.z, Bv.w)}, C[2] = {pair(Cv.x, Cv.y), pair(Cv.z, Cv.w)};
     const float x = to_f32(static_cast<const T*>(p.x)[b * p.xs + d]);
     const float v = to_f32(static_cast<const T*>(p.dt)[b * p.dts + d]) + (p.bias != nullptr ? p.bias[d] : 0.f);
     const float z = p.z != nullptr ? to_f32(static_cast<const T*>(p.z)[b * p.zs + d]) : 0.f;
     const float skip = p.Dk != nullptr ? p.Dk[d] : 0.f;
     const float delta = p.softplus ? softplus<kExact>(v) : v, u = delta * x;
-    float s = 0.f;
+    float s[V];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        // h exp(delta A) as h + h (exp(delta A) - 1): thousands of calls multiply a state, one after another
-        h[i] = fmaf(u, B[i], fmaf(h[i], expm1f(delta * fmaxf(a[i], -1e37f)), h[i]));
-        if (n + i < p.N) s = fmaf(C[i], h[i], s);
+    for (int j = 0; j < V; ++j) {
+        const int from = (lane & ~(V - 1)) | j;
+        const f32x2 dj = both(V > 1 ? __shfl_sync(0xffffffffu, delta, from) : delta);
+        const f32x2 uj = both(V > 1 ? __shfl_sync(0xffffffffu, u, from) : u);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            float a0, a1;
+            unpair(a[j][i], a0, a1);
+            h[j][i] = fma2(uj, B[i], decayed(h[j][i], mul2(dj, pair(max_nan(a0, -1e37f), max_nan(a1, -1e37f)))));
+        }
+        float lo, hi;
+        unpair(fma2(C[1], h[j][1], mul2(C[0], h[j][0])), lo, hi);    // (C is 0 beyond N, and h finite there)
+        s[j] = lo + hi;
+        if (c0 + j * kWide < p.cpg) {
+            if (vec) {
+                if (n < p.N) *reinterpret_cast<ulonglong2*>(at + j * step) = make_ulonglong2(h[j][0], h[j][1]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    unpair(h[j][i], lo, hi);
+                    if (n + 2 * i < p.N) at[j * step + 2 * i] = lo;
+                    if (n + 2 * i + 1 < p.N) at[j * step + 2 * i + 1] = hi;
+                }
+            }
+        }
     }
-    if (vec) {
-        if (mine) *reinterpret_cast<float4*>(at) = make_float4(h[0], h[1], h[2], h[3]);
-    } else {
+    // each lane gets its own channel's sum
+    if (V >= 4) halve<V>(s, lane, V / 2);
+    if (V >= 2) halve<2>(s, lane, 1);
+    float o = s[0];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (mine && n + i < p.N) at[i] = h[i];
-    }
-#pragma unroll
-    for (int off = LPC / 2; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-    s = fmaf(skip, x, s);
-    if (p.z != nullptr) s *= z * sigmoid(z);
-    if (in && part == 0) *y = from_f32<T>(s);
+    for (int off = LPC / 2; off >= V; off >>= 1) o += __shfl_xor_sync(0xffffffffu, o, off);
+    o = fmaf(skip, x, o);
+    if (p.z != nullptr) o *= z * sigmoid(z);
+    if (in && part < V) *y = from_f32<T>(o);
 }
 
 template <typename T, int LPC> cudaError_t go(const ScanStep& p, cudaStream_t stream) {
-    const int64_t ctas = (p.D + kThreads / LPC - 1) / (kThreads / LPC);
-    selscan_step<T, LPC><<<(unsigned)(ctas * p.batch), kThreads, 0, stream>>>(p);
+    constexpr int kTile = (LPC < 4 ? LPC : 4) * (32 / LPC);
+    const int64_t tiles = (int64_t)((p.cpg + kTile - 1) / kTile) * p.G;
+    selscan_step<T, LPC><<<(unsigned)((tiles * p.batch + kWarps - 1) / kWarps), kWarps * 32, 0, stream>>>(p);
     return cudaGetLastError();
 }
 

@@ -250,6 +250,42 @@ def test_extreme_decays(dtype):
     assert off(f64(y), want[0]) < TOL[dtype] and off(f64(fin), want[1]) < TOL["f32"]
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_a_token_that_forgets(dtype):
+    """Single tokens that leave little of a large state: what is left keeps its own precision.
+    delta A is between -40 and 0 and rounded once in fp32 and once in delta, which moves its
+    exponential by 40 * (2^-24 + 2^-21) at most, 2.2e-5 of each value; 1e-6 for the rest."""
+    n, D, N = 3, 32, 16
+    g = torch.Generator().manual_seed(9)
+    rnd = lambda *s: torch.randn(*s, generator=g)
+    x, dt = torch.zeros(n, D).to(DT[dtype]), (4.0 * torch.rand(n, D, generator=g)).to(DT[dtype])
+    A = -10.0 * torch.rand(D, N, generator=g)
+    h = 1e4 * (rnd(n, D, N) + 3.0)
+    B, C = rnd(n, 1, N).to(DT[dtype]), rnd(n, 1, N).to(DT[dtype])
+    want = h.double() * torch.exp(torch.nn.functional.softplus(dt.double())[:, :, None] * A.double())
+    cache = h.cuda()
+    ssd.selscan_step(x.cuda(), dt.cuda(), A.cuda(), B.cuda(), C.cuda(), cache, dt_softplus=True)
+    assert ((cache.double().cpu() - want).abs() <= 2.3e-5 * want.abs() + 1e-30).all()
+    # a rate that is not a number stays one in its own state
+    A[1, 2] = float("nan")
+    again = h.cuda()
+    ssd.selscan_step(x.cuda(), dt.cuda(), A.cuda(), B.cuda(), C.cuda(), again, dt_softplus=True)
+    assert again[:, 1, 2].isnan().all()
+    again[:, 1, 2] = cache[:, 1, 2]
+    assert torch.equal(again, cache)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_sequences_of_no_tokens_alone(dtype):
+    """No tokens at all: states and their gradients pass through, the others are zero."""
+    x = make(dtype, [0, 0], 0, 16, 16, 1, True, True, seed=10)
+    d = dev(x)
+    y, fin, st = ssd.selscan_fwd(*args(d), init_state=d["h0"], return_states=True, **options(d))
+    g = ssd.selscan_bwd(*args(d), d["dout"], st, dfinal_state=d["dfin"], return_dinit=True, **options(d))
+    assert y.shape == (0, 16) and torch.equal(fin, d["h0"]) and torch.equal(g["dinit_state"], d["dfin"])
+    assert not any(g[k].any() for k in ("dA", "dD", "ddt_bias"))
+
+
 def test_state_in_place_and_offsets_past_32_bits():
     D, T, n = 8192, 270000, 100
     g = torch.Generator(device="cuda").manual_seed(1)
