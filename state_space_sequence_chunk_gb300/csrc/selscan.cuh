@@ -230,27 +230,14 @@ template <int M> __device__ __forceinline__ void make_up(f32x2 (&h)[M], const f3
     }
 }
 
-// Four consecutive states of a row of B or C from n on, 0 beyond N.
-template <typename T> __device__ __forceinline__ float4 load_states(const T* p, int n, int N, bool vec);
-template <> __device__ __forceinline__ float4 load_states(const float* p, int n, int N, bool vec) {
-    if (vec) return n < N ? __ldg(reinterpret_cast<const float4*>(p + n)) : make_float4(0.f, 0.f, 0.f, 0.f);
-    return make_float4(n < N ? __ldg(p + n) : 0.f, n + 1 < N ? __ldg(p + n + 1) : 0.f,
-                       n + 2 < N ? __ldg(p + n + 2) : 0.f, n + 3 < N ? __ldg(p + n + 3) : 0.f);
-}
-template <> __device__ __forceinline__ float4 load_states(const __nv_bfloat16* p, int n, int N, bool vec) {
-    if (vec) {
-        const uint2 v = n < N ? __ldg(reinterpret_cast<const uint2*>(p + n)) : make_uint2(0u, 0u);
-        return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u),
-                           __uint_as_float(v.y << 16), __uint_as_float(v.y & 0xFFFF0000u));
-    }
-    return make_float4(n < N ? to_f32(p[n]) : 0.f, n + 1 < N ? to_f32(p[n + 1]) : 0.f,
-                       n + 2 < N ? to_f32(p[n + 2]) : 0.f, n + 3 < N ? to_f32(p[n + 3]) : 0.f);
-}
-template <typename T> struct Raw4;                        // four states as loaded
+// Four consecutive states of a row of B or C from n on, 0 beyond N: as loaded, and as floats.
+template <typename T> struct Raw4;
 template <> struct Raw4<float> { float4 v; };
 template <> struct Raw4<__nv_bfloat16> { uint2 v; };
 __device__ __forceinline__ void fetch(Raw4<float>& r, const float* p, int n, int N, bool vec) {
-    r.v = load_states(p, n, N, vec);
+    if (vec) r.v = n < N ? __ldg(reinterpret_cast<const float4*>(p + n)) : make_float4(0.f, 0.f, 0.f, 0.f);
+    else r.v = make_float4(n < N ? __ldg(p + n) : 0.f, n + 1 < N ? __ldg(p + n + 1) : 0.f,
+                           n + 2 < N ? __ldg(p + n + 2) : 0.f, n + 3 < N ? __ldg(p + n + 3) : 0.f);
 }
 __device__ __forceinline__ void fetch(Raw4<__nv_bfloat16>& r, const __nv_bfloat16* p, int n, int N, bool vec) {
     if (vec) {
