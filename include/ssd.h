@@ -538,7 +538,9 @@ size_t ssd_selscan_workspace_bytes(const ssd_selscan_dims* d, int backward);
  *                state before each 16th token of each sequence, sequence s's from row
  *                cu_seqlens[s] / 16 + s on; for ssd_selscan_bwd.
  * fp32 states and sums, one rounding of y.  What other sequences' rows hold never
- * reaches a sequence's results.  The result does not depend on the order in which the
+ * reaches a sequence's results; within one, a value that is not finite may make any
+ * later y and state of its channel a NaN, where the formula has an infinity, and in the
+ * gradients any of the sequence's.  The result does not depend on the order in which the
  * GPU runs the work.
  */
 ssd_status ssd_selscan_fwd(const ssd_selscan_dims* d, const void* x, const void* dt, const float* A,

@@ -26,11 +26,12 @@
 // What bounds it: a token takes a warp of 16 channels and 16 states some 200
 // instructions, 63 of them packed multiply-adds, and the registers (200 to 255) leave
 // two warps a quarter-SM, which issue in every second clock.  8192 tokens of 2048
-// channels in 6 sequences: 454 us a call, 650 without the cut into ranges.  Sums by
-// shuffles and rows loaded where they are used: 617; pairs of channels instead of
-// states, or delta and u stored in pairs: 539, 509 (more moves for the tensor cores'
-// operands, more shared memory traffic); slabs of 2 tokens and three warps a quarter-SM: 485,
-// of 8 tokens: 646.
+// channels in 6 sequences: 467 us a call, 670 without the cut into ranges.  Against
+// the form of that time (454 to 511 us before make_up): sums by shuffles and rows loaded where
+// they are used 617; pairs of channels instead of states, or delta and u stored in pairs: 539, 509 (more
+// moves for the tensor cores' operands, more shared memory traffic); slabs of 2 tokens 485, of 8
+// tokens 646.  More warps an SM, which the compiler's spills cost more than they
+// bring: CTAs of 3 warps, three an SM 608, of 2 warps, four 472, five 607.
 #include <type_traits>
 
 #include "selscan.cuh"
@@ -581,7 +582,7 @@ __global__ void __launch_bounds__(Plan<T, S>::kWarps * 32, S <= 4 ? 2 : 1) selsc
         }
 }
 
-// dB and dC: the tiles' terms in order; 0 in rows of no sequence.
+// dB and dC: the tiles' terms in order; 0 in rows of no sequence.  Bound by the terms' bytes.
 template <typename T>
 __global__ void __launch_bounds__(256) selscan_sum_bc(const __grid_constant__ ScanParams p, int tpg) {
     const int64_t per = (int64_t)p.g.T * p.G * 2 * p.N, e = (int64_t)blockIdx.x * 256 + threadIdx.x;

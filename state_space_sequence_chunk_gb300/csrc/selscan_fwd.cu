@@ -14,9 +14,10 @@
 // What bounds it: for 16 states a token costs a warp 100 instructions, 91 clocks of
 // the multiply-add pipe and 81 of the exponential's, of which three warps a
 // quarter-SM (168 registers) keep some 60 % busy.  16384 tokens of 5120 channels in
-// 12 sequences: 421 us.  Eight states a lane, two lanes a channel (more warps, but
-// every row of B and C is read twice as often for the same work): 455 us, four
-// states: 594.  Making the next tile's delta between this one's tokens: 433.
+// 12 sequences: 431 us (10 of them make_up).  Eight states a lane, two lanes a channel
+// (more warps, but every row of B and C is read twice as often for the same work) took
+// 1.08 times that, four states 1.41; the next tile's delta made between this one's tokens
+// 1.03; the products delta A by scalar instructions, which alone run faster beside the exponential, 1.03.
 #include <type_traits>
 
 #include "selscan.cuh"
@@ -329,7 +330,8 @@ __global__ void __launch_bounds__(kWarps * 32, S == 16 && LPC == 1 ? 6 : 1) sels
 }
 
 // The states at the starts of a sequence's ranges, in place of the ranges' own ends:
-// a thread for each state, the ranges in order, eight of them loaded ahead.  rev: from
+// a thread for each state, the ranges in order, eight of them loaded ahead.  Bound by the
+// latency of those loads where a sequence has many ranges, by the ends' bytes else.  rev: from
 // the last range to the first, the gradient that enters each at its end.
 __global__ void __launch_bounds__(128) selscan_ranges(const __grid_constant__ ScanParams p, int rev) {
     const int64_t per = (int64_t)p.D * p.N, e = (int64_t)blockIdx.x * 128 + threadIdx.x;

@@ -12,10 +12,10 @@
 // part of each, with the window loaded anew.
 //
 // What bounds it: HBM and, in bf16, about as much the instructions, 45 for four channels
-// of a row.  16384 bf16 tokens of 5120 channels, 4 taps: 63 us, 5.3 TB/s (eight channels a
-// thread and checks in the loop instead of parts: 100; 32 tokens a tile: 71; two channels
-// 65); the gradient 112 us, 4.5 TB/s (four channels 121).  fp32, of 2048 channels: 48 us, 5.6 TB/s,
-// and 83 us, 4.9 TB/s.
+// of a row.  16384 bf16 tokens of 5120 channels, 4 taps: 59 us, 5.7 TB/s (with other tiles: short_conv_tile; of
+// tiles of 64, two channels a thread took 1.03 times as long, eight, with checks in the loop instead of
+// parts, 1.6 times); the gradient 113 us, 4.5 TB/s (four channels 1.08 times).  fp32, of 2048
+// channels: 49 us, 5.5 TB/s, and 77 us, 5.2 TB/s.
 #include <type_traits>
 
 #include "short_conv.cuh"
@@ -174,12 +174,26 @@ template <int N2> __device__ __forceinline__ void back(f32x2 (&g)[N2], const f32
     }
 }
 
+// CTAs that an SM holds (by registers): the tile's length goes by it.
+constexpr int ctas_per_sm(int W, int bytes, bool backward) {
+    return W > 4 ? 3 : bytes == 2 ? 5 : backward ? 3 : 4;
+}
+// A warp's item (a tile of tokens, or behind those a sequence) and its lane's vector of the row:
+// shared out by warps, so that a row of 386 vectors takes 13 of them and not 4 CTAs.
+__device__ __forceinline__ bool warp_item(const ShortConv& p, int vecs, int& item, int& vec) {
+    // (the shuffle tells the compiler that all lanes have the same number)
+    const int warps = (vecs + 31) / 32, w = blockIdx.x * (kThreads / 32) + __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
+    item = w / warps;
+    vec = (w - item * warps) * 32 + (threadIdx.x & 31);
+    return item < p.items;
+}
+
 template <typename T, int W>
-__global__ void __launch_bounds__(kThreads, W <= 4 ? 4 : 1) short_conv_fwd(const __grid_constant__ ShortConv p) {
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(W, sizeof(T), false)) short_conv_fwd(const __grid_constant__ ShortConv p) {
     constexpr int V = kFwdVec, N2 = V / 2;
-    const int vecs = p.D / V, blocks = (vecs + kThreads - 1) / kThreads;
-    const int item = blockIdx.x / blocks, vec = (blockIdx.x - item * blocks) * kThreads + threadIdx.x;
-    const bool in = vec < vecs;
+    int item, vec;
+    if (!warp_item(p, p.D / V, item, vec)) return;
+    const bool in = vec < p.D / V;
     const int col = in ? vec * V : 0;
     if (item >= p.tiles) {                       // a sequence's final state: its last W - 1 rows
         const int s = item - p.tiles;
@@ -268,11 +282,11 @@ __global__ void __launch_bounds__(kThreads, W <= 4 ? 4 : 1) short_conv_fwd(const
 // and W - 1 rows further, whose g the tile's last rows of dx need.  The sums for dw and
 // db go into one row of partial sums per tile.
 template <typename T, int W>
-__global__ void __launch_bounds__(kThreads, W <= 4 && sizeof(T) == 2 ? 5 : 1) short_conv_bwd(const __grid_constant__ ShortConv p) {
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(W, sizeof(T), true)) short_conv_bwd(const __grid_constant__ ShortConv p) {
     constexpr int V = kBwdVec, N2 = V / 2;
-    const int vecs = p.D / V, blocks = (vecs + kThreads - 1) / kThreads;
-    const int item = blockIdx.x / blocks, vec = (blockIdx.x - item * blocks) * kThreads + threadIdx.x;
-    const bool in = vec < vecs;
+    int item, vec;
+    if (!warp_item(p, p.D / V, item, vec)) return;
+    const bool in = vec < p.D / V;
     const int col = in ? vec * V : 0;
     const T* x = static_cast<const T*>(p.x) + col;
     const T* dout = static_cast<const T*>(p.dout) + col;
@@ -441,7 +455,8 @@ __global__ void __launch_bounds__(kThreads, W <= 4 && sizeof(T) == 2 ? 5 : 1) sh
     Row<float, V>::store(part + (int64_t)W * p.D, db);
 }
 
-// dw and db: the tiles' sums added in the tiles' order, in eight shares.
+// dw and db: the tiles' sums added in the tiles' order, in eight shares, eight loads ahead:
+// bound by their latency (128 tiles: two turns).
 __global__ void __launch_bounds__(256) short_conv_sum(const __grid_constant__ ShortConv p, int W) {
     __shared__ float sh[8][32];
     const int lane = threadIdx.x & 31, share = threadIdx.x >> 5;
@@ -472,7 +487,9 @@ __global__ void __launch_bounds__(256) short_conv_sum(const __grid_constant__ Sh
     }
 }
 
-// One more token of each stream: the cache's W - 1 rows move up by one.
+// One more token of each stream: the cache's W - 1 rows move up by one.  All of a thread's
+// rows are loaded before the first is stored.  2048 streams of 2048 bf16 channels, 4 taps, 67 MB
+// moved: 13 us, 5.1 TB/s (some of it from L2); 64 streams 2.2 us, one 1.6.
 template <typename T, int W>
 __global__ void __launch_bounds__(kThreads) short_conv_step(const __grid_constant__ ShortConv p) {
     constexpr int V = 4, N2 = V / 2;
@@ -514,24 +531,40 @@ template <typename F> cudaError_t by_width(int W, const F& f) {
     }
 }
 
-inline int64_t blocks_of(int D, int V) { return (D / V + kThreads - 1) / kThreads; }
+unsigned grid_of(const ShortConv& p, int V) {
+    const int64_t warps = (int64_t)p.items * ((p.D / V + 31) / 32);
+    return (unsigned)((warps + kThreads / 32 - 1) / (kThreads / 32));
+}
 
 }  // namespace
 
-int short_conv_tile(int64_t T, int D, int dtype, bool backward, int sms) {
-    // long tiles re-read fewer rows; short ones where the long ones would leave SMs idle
-    const int64_t per = blocks_of(D, backward ? kBwdVec : kFwdVec);
-    int tile = backward ? 128 : 64;
-    while (tile > 8 && (T + tile - 1) / tile * per < 4 * sms) tile /= 2;
-    return tile;
+// Tokens of a tile: those of 8 .. 128 (backwards 256) that take the fewest rows of turns of the
+// whole GPU, a tile's start counted as 8 rows.  Long tiles re-read fewer rows, short ones share
+// few rows out among more SMs, and a last turn that is nearly empty costs as much as a full one: 16384 bf16 tokens of
+// 2048 channels, tiles of 64 (1.3 turns), 88 (one): 31.8, 27.2 us; of 5120, 64 (4.2), 72 (3): 63,
+// 59; backwards fp32, 128 (2.2), 144 (2): 84, 77.
+int short_conv_tile(int64_t T, int D, int W, int dtype, bool backward, int sms) {
+    const int64_t warps = (D / (backward ? kBwdVec : kFwdVec) + 31) / 32;
+    const int64_t resident = (int64_t)sms * ctas_per_sm(W, dtype == SSD_BF16 ? 2 : 4, backward);
+    int best = 8;
+    int64_t least = INT64_MAX;
+    for (int tile = 8; tile <= (backward ? 256 : 128); tile += 8) {
+        const int64_t ctas = ((T + tile - 1) / tile * warps + kThreads / 32 - 1) / (kThreads / 32);
+        const int64_t rows = (ctas + resident - 1) / resident * (tile + 8);
+        if (rows < least) {
+            least = rows;
+            best = tile;
+        }
+    }
+    return best;
 }
 
 cudaError_t launch_short_conv_fwd(ShortConv& p, int W, int dtype, int sms, cudaStream_t stream) {
-    p.TT = short_conv_tile(p.T, p.D, dtype, false, sms);
+    p.TT = short_conv_tile(p.T, p.D, W, dtype, false, sms);
     p.tiles = (p.T + p.TT - 1) / p.TT;
-    const int64_t items = p.tiles + (p.fin != nullptr ? (int64_t)p.nseq : 0);
-    if (items == 0) return cudaSuccess;
-    const unsigned grid = (unsigned)(items * blocks_of(p.D, kFwdVec));
+    p.items = p.tiles + (p.fin != nullptr ? p.nseq : 0);
+    if (p.items == 0) return cudaSuccess;
+    const unsigned grid = grid_of(p, kFwdVec);
     return by_width(W, [&](auto w) {
         if (dtype == SSD_BF16) short_conv_fwd<__nv_bfloat16, decltype(w)::value><<<grid, kThreads, 0, stream>>>(p);
         else short_conv_fwd<float, decltype(w)::value><<<grid, kThreads, 0, stream>>>(p);
@@ -540,11 +573,11 @@ cudaError_t launch_short_conv_fwd(ShortConv& p, int W, int dtype, int sms, cudaS
 }
 
 cudaError_t launch_short_conv_bwd(ShortConv& p, int W, int dtype, int sms, cudaStream_t stream) {
-    p.TT = short_conv_tile(p.T, p.D, dtype, true, sms);
+    p.TT = short_conv_tile(p.T, p.D, W, dtype, true, sms);
     p.tiles = (p.T + p.TT - 1) / p.TT;
-    const int64_t items = p.tiles + (p.dinit != nullptr ? (int64_t)p.nseq : 0);
-    if (items > 0) {
-        const unsigned grid = (unsigned)(items * blocks_of(p.D, kBwdVec));
+    p.items = p.tiles + (p.dinit != nullptr ? p.nseq : 0);
+    if (p.items > 0) {
+        const unsigned grid = grid_of(p, kBwdVec);
         const cudaError_t e = by_width(W, [&](auto w) {
             if (dtype == SSD_BF16) short_conv_bwd<__nv_bfloat16, decltype(w)::value><<<grid, kThreads, 0, stream>>>(p);
             else short_conv_bwd<float, decltype(w)::value><<<grid, kThreads, 0, stream>>>(p);
@@ -557,7 +590,7 @@ cudaError_t launch_short_conv_bwd(ShortConv& p, int W, int dtype, int sms, cudaS
 }
 
 cudaError_t launch_short_conv_step(const ShortConv& p, int W, int dtype, cudaStream_t stream) {
-    const unsigned grid = (unsigned)(p.batch * blocks_of(p.D, 4));
+    const unsigned grid = (unsigned)(p.batch * ((p.D / 4 + kThreads - 1) / kThreads));
     return by_width(W, [&](auto w) {
         if (dtype == SSD_BF16) short_conv_step<__nv_bfloat16, decltype(w)::value><<<grid, kThreads, 0, stream>>>(p);
         else short_conv_step<float, decltype(w)::value><<<grid, kThreads, 0, stream>>>(p);

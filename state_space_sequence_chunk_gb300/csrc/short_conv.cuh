@@ -16,11 +16,10 @@ struct ShortConv {
     const float *w, *bias;
     void *out, *fin, *dx, *dinit, *cache;
     float *dw, *db, *part;
-    int TT, tiles;               // tokens of a tile, tiles
+    int TT, tiles, items;        // tokens of a tile, tiles, tiles and sequences of their own
 };
 
-// Tokens of a tile: backward or not.
-int short_conv_tile(int64_t T, int D, int dtype, bool backward, int sms);
+int short_conv_tile(int64_t T, int D, int W, int dtype, bool backward, int sms);
 cudaError_t launch_short_conv_fwd(ShortConv& p, int W, int dtype, int sms, cudaStream_t stream);
 cudaError_t launch_short_conv_bwd(ShortConv& p, int W, int dtype, int sms, cudaStream_t stream);
 cudaError_t launch_short_conv_step(const ShortConv& p, int W, int dtype, cudaStream_t stream);

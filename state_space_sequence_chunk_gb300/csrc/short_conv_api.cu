@@ -30,15 +30,15 @@ ssd_status make(const ssd_short_conv_dims* d, bool packed, Dims* out) {
     p.act = d->activation;
     q.rows = (size_t)(q.T * q.D) * q.es;
     q.states = (size_t)(q.n * (q.W - 1) * q.D) * q.es;
-    // a CTA for each tile of tokens or sequence and 128 vectors of two channels: within a grid
-    if ((q.T / 8 + 1 + q.n) * ((q.D / 2 + 127) / 128) >= (1LL << 31)) return SSD_ERR_SHAPE;
+    // a warp for each tile of tokens or sequence and 32 vectors of two channels: their number is an int
+    if ((q.T / 8 + 1 + q.n) * ((q.D / 2 + 31) / 32) >= (1LL << 31) - 4) return SSD_ERR_SHAPE;
     *out = q;
     return SSD_OK;
 }
 
 size_t part_bytes(const Dims& q, int dtype) {
     if (q.T == 0) return 0;
-    const int tile = short_conv_tile(q.T, (int)q.D, dtype, true, sm_count());
+    const int tile = short_conv_tile(q.T, (int)q.D, (int)q.W, dtype, true, sm_count());
     return (size_t)((q.T + tile - 1) / tile * (q.W + 1) * q.D) * 4;
 }
 
