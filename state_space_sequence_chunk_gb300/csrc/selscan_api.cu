@@ -56,8 +56,8 @@ ssd_status make(const ssd_selscan_dims* d, bool packed, bool backward, Scan* out
     // and warp when all SMs work, and some 25 us of launches and ramps.  Whole and cut, us, 16
     // states: 256 tokens of 2048 channels (64 warps) 35 and 39, 512 of 5120 64 and 46, 2048 of
     // 2048 in 4 sequences 94 and 59, 8192 of 2048 860 and 154, in 6 sequences 224 and 154;
-    // 16384 of 5120 in 12 431 and 632; 16384 of 2048 in 40 207 and 281; 4096 of 768, 64 states, in 8
-    // 182 and 214.  Backwards a CTA of 64 (32, 16) channels takes 295 ns a token by itself, and
+    // 16384 of 5120 in 12 427 and 616; 16384 of 2048 in 40 197 and 275; 4096 of 768, 64 states, in 8
+    // 120 and 154.  Backwards a CTA of 64 (32, 16) channels takes 295 ns a token by itself, and
     // the cut's passes 1.7 ns for each token and CTA: the same sizes 87 and 70, 162 and 113, 263 and
     // 153, 2400 and 460, 650 and 460, -, 790 and 890, 444 and 459.
     const int64_t bt = selscan_bwd_channels((int)q.N), tiles = (p.cpg + bt - 1) / bt;

@@ -14,10 +14,13 @@
 // What bounds it: for 16 states a token costs a warp 100 instructions, 91 clocks of
 // the multiply-add pipe and 81 of the exponential's, of which three warps a
 // quarter-SM (168 registers) keep some 60 % busy.  16384 tokens of 5120 channels in
-// 12 sequences: 431 us (10 of them make_up).  Eight states a lane, two lanes a channel
+// 12 sequences: 427 us (10 of them make_up).  Eight states a lane, two lanes a channel
 // (more warps, but every row of B and C is read twice as often for the same work) took
 // 1.08 times that, four states 1.41; the next tile's delta made between this one's tokens
-// 1.03; the products delta A by scalar instructions, which alone run faster beside the exponential, 1.03.
+// 1.03; the products delta A by scalar instructions, which alone run faster beside the exponential, 1.03;
+// pairs of channels instead of states, delta and u through shared memory (fewer moves, more
+// shared memory traffic) 1.16; four warps a quarter-SM (128 registers, some spilled) 1.18; y by way of shared memory in
+// pieces of 16 bytes 1.01.
 #include <type_traits>
 
 #include "selscan.cuh"
@@ -171,14 +174,17 @@ __global__ void __launch_bounds__(kWarps * 32, S == 16 && LPC == 1 ? 6 : 1) sels
     };
     // delta and u of the tile at t0 into shared memory, and B and C; rows behind the range's
     // end multiply the state by 1 and add nothing (their x and dout are zeros)
-    auto prepare = [&](int t0, Own& o) {
+    auto prepare = [&](int t0, Own& o, auto full) {
         const int at = t0 / kTok, buf = at & 1, stage = at % kStages;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             const int v = i * 32 + lane;
             if (kVec % 32 == 0 || v < kVec) {
-                *reinterpret_cast<float4*>(&w.B[buf][0][0] + 4 * v) = widen(br[i]);
-                if (!SUMS) *reinterpret_cast<float4*>(&w.C[SUMS ? 0 : buf][0][0] + 4 * v) = widen(cr[i]);
+                // vector k of a row's lane q lies at k LPC + q, so that the lanes of a channel read other
+                // banks (8192 tokens of 2048 channels, 64 states: 491 us; each lane's own side by side 756)
+                const int r = v / (NP / 4), e = v % (NP / 4), at = e % (S / 4) * LPC + e / (S / 4);
+                *reinterpret_cast<float4*>(&w.B[buf][r][4 * at]) = widen(br[i]);
+                if (!SUMS) *reinterpret_cast<float4*>(&w.C[SUMS ? 0 : buf][r][4 * at]) = widen(cr[i]);
             }
         }
         auto raw2 = [&](int k, int i) {
@@ -208,8 +214,10 @@ __global__ void __launch_bounds__(kWarps * 32, S == 16 && LPC == 1 ? 6 : 1) sels
         for (int i = 0; i < kOwn / 2; ++i) {
             const int t = t0 + 2 * i * LPC + part;
             float a, b, c, e;
-            unpair(dl[i], a, b);
-            dl[i] = pair(t < it.len ? a : 0.f, t + LPC < it.len ? b : 0.f);
+            if (!decltype(full)::value) {
+                unpair(dl[i], a, b);
+                dl[i] = pair(t < it.len ? a : 0.f, t + LPC < it.len ? b : 0.f);
+            }
             recent = add2(recent, dl[i]);
             unpair(dl[i], a, b);
             unpair(REV ? mul2(o.x[i], o.gate[i]) : mul2(dl[i], o.x[i]), c, e);
@@ -244,7 +252,7 @@ __global__ void __launch_bounds__(kWarps * 32, S == 16 && LPC == 1 ? 6 : 1) sels
             f32x2 y0 = 0ull, y1 = 0ull;
 #pragma unroll
             for (int i = 0; i < S / 4; ++i) {
-                const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(&w.B[buf][t][n0 + 4 * i]);
+                const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(&w.B[buf][t][4 * (i * LPC + part)]);
                 f32x2 an0 = 0ull, an1 = 0ull;
                 if (t + 1 < kTok) {
                     an0 = ex2_2(mul2(dn, a2[2 * i]));
@@ -260,7 +268,7 @@ __global__ void __launch_bounds__(kWarps * 32, S == 16 && LPC == 1 ? 6 : 1) sels
                 a[2 * i] = an0;
                 a[2 * i + 1] = an1;
                 if (!SUMS) {
-                    const ulonglong2 c = *reinterpret_cast<const ulonglong2*>(&w.C[SUMS ? 0 : buf][t][n0 + 4 * i]);
+                    const ulonglong2 c = *reinterpret_cast<const ulonglong2*>(&w.C[SUMS ? 0 : buf][t][4 * (i * LPC + part)]);
                     y0 = i == 0 ? mul2(c.x, h[0]) : fma2(c.x, h[2 * i], y0);
                     y1 = i == 0 ? mul2(c.y, h[1]) : fma2(c.y, h[2 * i + 1], y1);
                 }
@@ -297,7 +305,7 @@ __global__ void __launch_bounds__(kWarps * 32, S == 16 && LPC == 1 ? 6 : 1) sels
         if (!SUMS && p.states != nullptr && (it.done + t0) % kScanChunk == 0)
             store_row<S>(h, p.states + ((int64_t)(it.row0 + (it.done + t0) / kScanChunk) * p.D + d) * p.N, n0, p.N, in);
         Own own;
-        prepare(t0, own);
+        prepare(t0, own, full);
         prefetch(t0 + kTok);
         __syncwarp();
         tokens(t0, own, full);
