@@ -55,7 +55,7 @@ ssd_status make(const ssd_selscan_dims* d, bool packed, bool backward, Scan* out
     // warp by itself takes 104 ns a token; the cut's two passes take 225 ps for each token
     // and warp when all SMs work, and some 25 us of launches and ramps.  Whole and cut, us, 16
     // states: 256 tokens of 2048 channels (64 warps) 35 and 39, 512 of 5120 64 and 46, 2048 of
-    // 2048 in 4 sequences 94 and 59, 8192 of 2048 860 and 154, in 6 sequences 224 and 154;
+    // 2048 in 4 sequences 94 and 59, 8192 of 2048 860 and 154, in 6 sequences 217 and 151;
     // 16384 of 5120 in 12 427 and 616; 16384 of 2048 in 40 197 and 275; 4096 of 768, 64 states, in 8
     // 120 and 154.  Backwards a CTA of 64 (32, 16) channels takes 295 ns a token by itself, and
     // the cut's passes 1.7 ns for each token and CTA: the same sizes 87 and 70, 162 and 113, 263 and
@@ -69,7 +69,7 @@ ssd_status make(const ssd_selscan_dims* d, bool packed, bool backward, Scan* out
     if (q.n > 0 && longest > (backward ? work / (sms * 8 / 7) + 136 : work / (3 * sms) + 256)) {
         // several ranges for each warp that is resident, but not too short (2048 tokens of 1536
         // channels: ranges of 32, 64, 96, 128, 256 tokens 51, 49, 48, 55, 65 us, backwards 124, 122,
-        // 122, 129, 151; 8192 of 2048: 64, 96, 128 160, 148, 150; 65536 of 1536: 128, 384, 512: 799, 759, 790)
+        // 122, 129, 151; 8192 of 2048: 64, 96, 128 160, 148, 150; 65536 of 1536: 96, 160, 384: 807, 767, 742)
         int64_t R = (work / ((backward ? 13 : 54) * sms) + 16) / 32 * 32;
         const int64_t least = backward ? 64 : 96;
         R = R < least ? least : R > 512 ? 512 : R;
