@@ -717,9 +717,19 @@ def _here(t, dev):
     return t.data_ptr()
 
 
-def _rows_here(t, inner: int, dev):
-    """_rows, of a tensor on device `dev`."""
-    if t.get_device() != dev:
+def _at(t, name, dtype, shape, dev):
+    """_typed and _here in one: a call's operands are many, and each test costs."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        return _here(_typed(t, name, dtype, shape), dev)
+    return t.data_ptr()
+
+
+def _rows_at(t, name, dtype, shape, inner, dev):
+    """_rows, of a tensor of this dtype and shape on device `dev`."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
+        _typed(t, name, dtype, shape)
         raise ValueError("tensors must be CUDA tensors on the current device")
     if t.is_contiguous():
         return t.data_ptr(), inner
@@ -744,9 +754,17 @@ def _space(need: int, workspace, device):
     return workspace, 0 if workspace is None else workspace.numel() * workspace.element_size()
 
 
-def _new(t, name, dtype, shape, device):
-    """The caller's output, checked, or a new one."""
-    return torch.empty(shape, dtype=dtype, device=device) if t is None else _typed(t, name, dtype, shape)
+def _out(t, name, dtype, shape, device, dev):
+    """The caller's output, checked, or a new one, and its address."""
+    if t is None:
+        t = torch.empty(shape, dtype=dtype, device=device)
+        return t, t.data_ptr()
+    return t, _at(t, name, dtype, shape, dev)
+
+
+def _ptrs(g):
+    """Addresses of new outputs."""
+    return (None if t is None else t.data_ptr() for t in g.values())
 
 
 def _short_conv_dims(x, weight, bias, activation, nseqs, dev):
@@ -757,11 +775,9 @@ def _short_conv_dims(x, weight, bias, activation, nseqs, dev):
         raise ValueError(f"activation must be one of {list(ACTIVATIONS)}, got {activation!r}")
     T, D = x.shape
     W = weight.shape[1]
-    _typed(weight, "weight", torch.float32, (D, W))
-    _typed(bias, "bias", torch.float32, (D,))
-    xp, xs = _rows_here(x, D, dev)
-    return (ShortConvDims(nseqs, T, D, W, xs, act, _dtype_code(x, "x"), 0), T, D, W,
-            (xp, _here(weight, dev), _here(bias, dev)))
+    wp, bp = _at(weight, "weight", torch.float32, (D, W), dev), _at(bias, "bias", torch.float32, (D,), dev)
+    xp, xs = _rows_at(x, "x", x.dtype, x.shape, D, dev)
+    return ShortConvDims(nseqs, T, D, W, xs, act, _dtype_code(x, "x"), 0), T, D, W, (xp, wp, bp)
 
 
 def short_conv_fwd(x, weight, bias=None, activation=None, cu_seqlens=None, init_state=None,
@@ -780,11 +796,11 @@ def short_conv_fwd(x, weight, bias=None, activation=None, cu_seqlens=None, init_
     n = _seqs(cu_seqlens, nseqs)
     dev = torch.cuda.current_device()
     d, T, D, W, args = _short_conv_dims(x, weight, bias, activation, n, dev)
-    _typed(init_state, "init_state", x.dtype, (n, W - 1, D))
-    o = _new(out, "out", x.dtype, (T, D), x.device)
-    fin = _new(final_out, "final_out", x.dtype, (n, W - 1, D), x.device) if return_final_state else None
-    _check(lib.ssd_short_conv_fwd(ctypes.byref(d), *args, _here(cu_seqlens, dev), _here(init_state, dev),
-                                  _here(o, dev), _here(fin, dev), _stream_of(dev)))
+    state = (n, W - 1, D)
+    ip = _at(init_state, "init_state", x.dtype, state, dev)
+    o, op = _out(out, "out", x.dtype, (T, D), x.device, dev)
+    fin, fp = _out(final_out, "final_out", x.dtype, state, x.device, dev) if return_final_state else (None, None)
+    _check(lib.ssd_short_conv_fwd(ctypes.byref(d), *args, _here(cu_seqlens, dev), ip, op, fp, _stream_of(dev)))
     return o, fin
 
 
@@ -798,16 +814,14 @@ def short_conv_bwd(x, weight, dout, bias=None, activation=None, cu_seqlens=None,
     dev = torch.cuda.current_device()
     d, T, D, W, args = _short_conv_dims(x, weight, bias, activation, n, dev)
     state = (n, W - 1, D)
-    _typed(dout, "dout", x.dtype, (T, D))
-    _typed(init_state, "init_state", x.dtype, state)
-    _typed(dfinal_state, "dfinal_state", x.dtype, state)
+    ip = _at(init_state, "init_state", x.dtype, state, dev)
+    gp, fp = _at(dout, "dout", x.dtype, (T, D), dev), _at(dfinal_state, "dfinal_state", x.dtype, state, dev)
     new = lambda shape, dt: torch.empty(shape, dtype=dt, device=x.device)
     g = {"dx": new((T, D), x.dtype), "dweight": new((D, W), torch.float32),
          "dbias": None if bias is None else new((D,), torch.float32),
          "dinit_state": None if init_state is None else new(state, x.dtype)}
     workspace, nbytes = _space(lib.ssd_short_conv_bwd_workspace_bytes(ctypes.byref(d)), workspace, x.device)
-    _check(lib.ssd_short_conv_bwd(ctypes.byref(d), *args, _here(cu_seqlens, dev), _here(init_state, dev),
-                                  _here(dout, dev), _here(dfinal_state, dev), *(_here(t, dev) for t in g.values()),
+    _check(lib.ssd_short_conv_bwd(ctypes.byref(d), *args, _here(cu_seqlens, dev), ip, gp, fp, *_ptrs(g),
                                   _here(workspace, dev), nbytes, _stream_of(dev)))
     return g
 
@@ -822,11 +836,9 @@ def short_conv_step(x, weight, cache, bias=None, activation=None, slots=None, ou
     dev = torch.cuda.current_device()
     d, b, D, W, args = _short_conv_dims(x, weight, bias, activation, x.shape[0], dev)
     n = cache.shape[0]
-    _typed(cache, "cache", x.dtype, (n, W - 1, D))
-    _typed(slots, "slots", torch.int32, (b,))
-    o = _new(out, "out", x.dtype, (b, D), x.device)
-    _check(lib.ssd_short_conv_step(ctypes.byref(d), *args, _here(slots, dev), _here(cache, dev), n, _here(o, dev),
-                                   _stream_of(dev)))
+    cp, sp = _at(cache, "cache", x.dtype, (n, W - 1, D), dev), _at(slots, "slots", torch.int32, (b,), dev)
+    o, op = _out(out, "out", x.dtype, (b, D), x.device, dev)
+    _check(lib.ssd_short_conv_step(ctypes.byref(d), *args, sp, cp, n, op, _stream_of(dev)))
     return o
 
 
@@ -835,19 +847,16 @@ def _selscan_dims(x, dt, A, B, C, D, z, dt_bias, dt_softplus, nseqs, max_seqlen,
         raise ValueError("x must be [tokens, dim], A [dim, N], B and C [tokens, G, N]")
     T, W = x.shape
     N, G = A.shape[1], B.shape[1]
-    _typed(dt, "dt", x.dtype, (T, W))
-    _typed(z, "z", x.dtype, (T, W))
-    _typed(A, "A", torch.float32, (W, N))
-    _typed(B, "B", x.dtype, (T, G, N))
-    _typed(C, "C", x.dtype, (T, G, N))
-    _typed(D, "D", torch.float32, (W,))
-    _typed(dt_bias, "dt_bias", torch.float32, (W,))
-    (xp, xs), (tp, ts) = _rows_here(x, W, dev), _rows_here(dt, W, dev)
-    (Bp, Bs), (Cp, Cs) = _rows_here(B, G * N, dev), _rows_here(C, G * N, dev)
-    zp, zs = (None, 0) if z is None else _rows_here(z, W, dev)
+    kind, rows, mix, f32 = x.dtype, (T, W), (T, G, N), torch.float32
+    xp, xs = _rows_at(x, "x", kind, rows, W, dev)
+    tp, ts = _rows_at(dt, "dt", kind, rows, W, dev)
+    zp, zs = (None, 0) if z is None else _rows_at(z, "z", kind, rows, W, dev)
+    Bp, Bs = _rows_at(B, "B", kind, mix, G * N, dev)
+    Cp, Cs = _rows_at(C, "C", kind, mix, G * N, dev)
+    Ap, Dp, bp = _at(A, "A", f32, (W, N), dev), _at(D, "D", f32, (W,), dev), _at(dt_bias, "dt_bias", f32, (W,), dev)
     d = SelscanDims(nseqs, T, W, N, G, xs, ts, zs, Bs, Cs, max_seqlen, 1 if dt_softplus else 0,
                     _dtype_code(x, "x"), 0)
-    return d, T, W, N, (xp, tp, _here(A, dev), Bp, Cp, _here(D, dev), zp, _here(dt_bias, dev))
+    return d, T, W, N, (xp, tp, Ap, Bp, Cp, Dp, zp, bp)
 
 
 def selscan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus: bool = False,
@@ -873,13 +882,14 @@ def selscan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus: bool 
     n = _seqs(cu_seqlens, nseqs)
     dev = torch.cuda.current_device()
     d, T, W, N, args = _selscan_dims(x, dt, A, B, C, D, z, dt_bias, dt_softplus, n, max_seqlen, dev)
-    _typed(init_state, "init_state", torch.float32, (n, W, N))
-    y = _new(out, "out", x.dtype, (T, W), x.device)
-    fin = _new(final_out, "final_out", torch.float32, (n, W, N), x.device) if return_final_state else None
+    state = (n, W, N)
+    ip = _at(init_state, "init_state", torch.float32, state, dev)
+    y, yp = _out(out, "out", x.dtype, (T, W), x.device, dev)
+    fin, fp = _out(final_out, "final_out", torch.float32, state, x.device, dev) if return_final_state else (None, None)
     states = torch.empty((T // SELSCAN_CHUNK + n, W, N), dtype=torch.float32, device=x.device) if return_states else None
     workspace, nbytes = _space(lib.ssd_selscan_workspace_bytes(ctypes.byref(d), 0), workspace, x.device)
-    _check(lib.ssd_selscan_fwd(ctypes.byref(d), *args, _here(cu_seqlens, dev), _here(init_state, dev), _here(y, dev),
-                               _here(fin, dev), _here(states, dev), _here(workspace, dev), nbytes, _stream_of(dev)))
+    _check(lib.ssd_selscan_fwd(ctypes.byref(d), *args, _here(cu_seqlens, dev), ip, yp, fp, _here(states, dev),
+                               _here(workspace, dev), nbytes, _stream_of(dev)))
     return (y, fin, states) if return_states else (y, fin)
 
 
@@ -893,17 +903,15 @@ def selscan_bwd(x, dt, A, B, C, dout, states, D=None, z=None, dt_bias=None, dt_s
     n = _seqs(cu_seqlens, nseqs)
     dev = torch.cuda.current_device()
     d, T, W, N, args = _selscan_dims(x, dt, A, B, C, D, z, dt_bias, dt_softplus, n, max_seqlen, dev)
-    _typed(dout, "dout", x.dtype, (T, W))
-    _typed(states, "states", torch.float32, (T // SELSCAN_CHUNK + n, W, N))
-    _typed(dfinal_state, "dfinal_state", torch.float32, (n, W, N))
+    sp = _at(states, "states", torch.float32, (T // SELSCAN_CHUNK + n, W, N), dev)
+    gp, fp = _at(dout, "dout", x.dtype, (T, W), dev), _at(dfinal_state, "dfinal_state", torch.float32, (n, W, N), dev)
     like = lambda t: None if t is None else torch.empty(t.shape, dtype=t.dtype, device=x.device)
     g = {"dx": like(x), "ddt": like(dt), "dA": like(A), "dB": like(B), "dC": like(C), "dD": like(D), "dz": like(z),
          "ddt_bias": like(dt_bias),
          "dinit_state": torch.empty((n, W, N), dtype=torch.float32, device=x.device) if return_dinit else None}
     workspace, nbytes = _space(lib.ssd_selscan_workspace_bytes(ctypes.byref(d), 1), workspace, x.device)
-    _check(lib.ssd_selscan_bwd(ctypes.byref(d), *args, _here(cu_seqlens, dev), _here(states, dev), _here(dout, dev),
-                               _here(dfinal_state, dev), *(_here(t, dev) for t in g.values()), _here(workspace, dev),
-                               nbytes, _stream_of(dev)))
+    _check(lib.ssd_selscan_bwd(ctypes.byref(d), *args, _here(cu_seqlens, dev), sp, gp, fp, *_ptrs(g),
+                               _here(workspace, dev), nbytes, _stream_of(dev)))
     return g
 
 
@@ -916,9 +924,7 @@ def selscan_step(x, dt, A, B, C, cache, D=None, z=None, dt_bias=None, dt_softplu
     dev = torch.cuda.current_device()
     d, b, W, N, args = _selscan_dims(x, dt, A, B, C, D, z, dt_bias, dt_softplus, x.shape[0], 0, dev)
     n = cache.shape[0]
-    _typed(cache, "cache", torch.float32, (n, W, N))
-    _typed(slots, "slots", torch.int32, (b,))
-    y = _new(out, "out", x.dtype, (b, W), x.device)
-    _check(lib.ssd_selscan_step(ctypes.byref(d), *args, _here(slots, dev), _here(cache, dev), n, _here(y, dev),
-                                _stream_of(dev)))
+    cp, sp = _at(cache, "cache", torch.float32, (n, W, N), dev), _at(slots, "slots", torch.int32, (b,), dev)
+    y, yp = _out(out, "out", x.dtype, (b, W), x.device, dev)
+    _check(lib.ssd_selscan_step(ctypes.byref(d), *args, sp, cp, n, yp, _stream_of(dev)))
     return y
