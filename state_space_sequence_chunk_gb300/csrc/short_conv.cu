@@ -258,17 +258,22 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(W, sizeof(T), false)) sh
             Row<T, V>::store(to, o);
             to += p.D;
         };
-        int t = a;
-        for (; t + kAhead <= b; t += kAhead) {
+        auto rows = [&](int t, auto all) {       // kAhead rows; `all`: as many follow them
             Row<T, V> cur[kAhead];
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) {
                 cur[i] = ahead[i];
-                if (t + kAhead + i < b) ahead[i].load(from);
+                if (decltype(all)::value || t + kAhead + i < b) ahead[i].load(from);
                 from += p.xs;
             }
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) row(cur[i]);
+        };
+        int t = a;
+        for (; t + 2 * kAhead <= b; t += kAhead) rows(t, std::true_type());
+        if (t + kAhead <= b) {
+            rows(t, std::false_type());
+            t += kAhead;
         }
 #pragma unroll
         for (int i = 0; i < kAhead - 1; ++i)
@@ -376,10 +381,10 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(W, sizeof(T), true)) sho
         Row<T, V> xa[kAhead], da[kAhead];
         const T *xn = x + a * p.xs, *dn = dout + (int64_t)a * p.D;    // the rows loaded next
         T* to = dx + (int64_t)(a - (W - 1)) * p.D;                    // the row finished next
-        auto fetch = [&](int t) {
+        auto fetch = [&](int t, auto all) {
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) {
-                if (t + i < lim) {
+                if (decltype(all)::value || t + i < lim) {
                     xa[i].load(xn);
                     da[i].load(dn);
                 }
@@ -387,8 +392,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(W, sizeof(T), true)) sho
                 dn += p.D;
             }
         };
-        fetch(a);
-        auto row = [&](const Row<T, V>& xr, const Row<T, V>& dr, int t, auto own) {
+        fetch(a, std::false_type());
+        // own: not a row that the next tile adds; inner: a row of the tile is finished
+        auto row = [&](const Row<T, V>& xr, const Row<T, V>& dr, int t, auto own, auto inner) {
             f32x2 now[N2], g[N2], pre[N2];
             xr.get(now);
             dr.get(g);
@@ -396,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(W, sizeof(T), true)) sho
             back(g, pre, p.act);
 #pragma unroll
             for (int k = 0; k < N2; ++k) {
-                if (decltype(own)::value) {      // not a row that the next tile adds
+                if (decltype(own)::value) {
                     db[k] = add2(db[k], g[k]);
 #pragma unroll
                     for (int j = 0; j < W - 1; ++j) dw[j][k] = fma2(g[k], win[j][k], dw[j][k]);
@@ -407,28 +413,34 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(W, sizeof(T), true)) sho
                 acc[0][k] = mul2(taps.w[W - 1][k], g[k]);
             }
             shift(win, now);
-            if (t - (W - 1) >= a) Row<T, V>::store(to, acc[W - 1]);
+            if (decltype(inner)::value || t - (W - 1) >= a) Row<T, V>::store(to, acc[W - 1]);
             to += p.D;
         };
-        int t = a;
-        for (; t + kAhead <= b; t += kAhead) {
+        auto rows = [&](int t, auto all) {       // kAhead rows; `all`: not the first ones, and as many follow
             Row<T, V> xc[kAhead], dc[kAhead];
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) {
                 xc[i] = xa[i];
                 dc[i] = da[i];
             }
-            fetch(t + kAhead);
+            fetch(t + kAhead, all);
 #pragma unroll
-            for (int i = 0; i < kAhead; ++i) row(xc[i], dc[i], t + i, std::true_type());
+            for (int i = 0; i < kAhead; ++i) row(xc[i], dc[i], t + i, std::true_type(), all);
+        };
+        int t = a;
+        if (t + kAhead <= b) {
+            rows(t, std::false_type());
+            t += kAhead;
         }
+        for (; t + kAhead <= b && t + 2 * kAhead <= lim; t += kAhead) rows(t, std::true_type());
+        for (; t + kAhead <= b; t += kAhead) rows(t, std::false_type());
         // the rest, fewer than kAhead rows, and up to W - 1 of the next tile
         for (int i = 0; t + i < lim; ++i) {
             Row<T, V> xr, dr;
             xr.load(x + (t + i) * p.xs);
             dr.load(dout + (int64_t)(t + i) * p.D);
-            if (t + i < b) row(xr, dr, t + i, std::true_type());
-            else row(xr, dr, t + i, std::false_type());
+            if (t + i < b) row(xr, dr, t + i, std::true_type(), std::false_type());
+            else row(xr, dr, t + i, std::false_type(), std::false_type());
         }
         // the sequence's last rows, if it ends here: nothing follows but the final state's gradient
 #pragma unroll
