@@ -15,7 +15,7 @@
 // cross lanes.  Over the states (the 4 lanes of a row, for dx, ddelta and y): a product of
 // the tensor cores, rows x lanes by lanes x tokens, whose second operand is 1 in the
 // token's column, so that eight tokens' sums lie ready in eight columns.  dt_bias's
-// gradient is summed in fp32 from them, so u and sum A w go in two terms of 11 bits;
+// gradient is summed in fp32 from them, so u and sum A w go in two terms of 11 bits (fp32: three, 520 -> 539 us);
 // y, which only dz (in the operands' type) needs, in one where that type is bf16.  Over the
 // channels (the 8 rows, then the CTA's warps, then a kernel of its own over the tiles; for
 // dB and dC): in bf16 a first product moves the values, state by channel, so that the
@@ -79,13 +79,13 @@ __device__ __forceinline__ void mma8(float (&c)[4], const float (&a)[4], float b
           "r"(__float_as_uint(b0)), "r"(__float_as_uint(b1)));
 }
 // Adds to column `col` of c the sums of v0 (rows 0 .. 7) and v1 (8 .. 15) over the four lanes
-// of a row; hot is 1 in the lanes whose row number is col, else 0.  EXACT: in two terms, so
-// that 22 bits of v count.
-template <bool EXACT> __device__ __forceinline__ void add_rows(float (&c)[4], float v0, float v1, float hot) {
-    mma4(c, v0, v1, hot);
-    if (EXACT) {
-        const float h0 = __uint_as_float(__float_as_uint(v0) & 0xFFFFE000u), h1 = __uint_as_float(__float_as_uint(v1) & 0xFFFFE000u);
-        mma4(c, v0 - h0, v1 - h1, hot);
+// of a row; hot is 1 in the lanes whose row number is col, else 0.  Each term counts 11 bits more of v.
+template <int TERMS> __device__ __forceinline__ void add_rows(float (&c)[4], float v0, float v1, float hot) {
+#pragma unroll
+    for (int i = 0; i < TERMS; ++i) {
+        mma4(c, v0, v1, hot);
+        v0 -= __uint_as_float(__float_as_uint(v0) & 0xFFFFE000u);
+        v1 -= __uint_as_float(__float_as_uint(v1) & 0xFFFFE000u);
     }
 }
 
@@ -147,7 +147,8 @@ template <int S> __device__ __forceinline__ void lds(f32x2 (&v)[S / 2], const fl
     }
 }
 
-template <typename T, int S>
+// FULL: the sums over channels, and y's, with all of their terms' bits.
+template <typename T, int S, bool FULL>
 __global__ void __launch_bounds__(Plan<T, S>::kWarps * 32, S <= 4 ? 2 : 1) selscan_bwd(const __grid_constant__ ScanParams p) {
     using P = Plan<T, S>;
     constexpr int C = P::C, K = P::K, kCh = P::kCh, NP = P::NP, H = S / 2, kThreads = P::kWarps * 32;
@@ -393,7 +394,7 @@ __global__ void __launch_bounds__(Plan<T, S>::kWarps * 32, S <= 4 ? 2 : 1) selsc
                         unpair(ys, lo, hi);
                         y[c] = lo + hi;
                     }
-                    add_rows<kExact>(ay, y[0], y[1], hot[k]);          // for dz
+                    add_rows<FULL ? 3 : 1>(ay, y[0], y[1], hot[k]);    // for dz
                 }
 #pragma unroll
                 for (int k = K - 1; k >= 0; --k) {
@@ -431,9 +432,9 @@ __global__ void __launch_bounds__(Plan<T, S>::kWarps * 32, S <= 4 ? 2 : 1) selsc
                         unpair(vs, lo, hi);
                         v[c] = lo + hi;
                     }
-                    add_rows<true>(au, u[0], u[1], hot[k]);       // (dt_bias's gradient is in fp32)
-                    add_rows<true>(av, v[0], v[1], hot[k]);
-                    if (kExact) {                      // fp32: sums over the channels by shuffles
+                    add_rows<FULL ? 3 : 2>(au, u[0], u[1], hot[k]);       // (dt_bias's gradient is in fp32)
+                    add_rows<FULL ? 3 : 2>(av, v[0], v[1], hot[k]);
+                    if (FULL) {                        // sums over the channels by shuffles
                         float part[2 * S];
 #pragma unroll
                         for (int i = 0; i < H; ++i) {
@@ -514,7 +515,7 @@ __global__ void __launch_bounds__(Plan<T, S>::kWarps * 32, S <= 4 ? 2 : 1) selsc
                         }
                     }
                 }
-                if (!kExact) {
+                if (!FULL) {
 #pragma unroll
                     for (int kind = 0; kind < 2; ++kind)
 #pragma unroll
@@ -620,17 +621,18 @@ __global__ void __launch_bounds__(128) selscan_sum_a(const __grid_constant__ Sca
     else if (p.dbias != nullptr) p.dbias[e - na - p.D] = s;
 }
 
-template <typename T, int S> cudaError_t go(const ScanParams& p, cudaStream_t stream) {
+template <typename T, int S, bool FULL> cudaError_t go(const ScanParams& p, cudaStream_t stream) {
     using P = Plan<T, S>;
+    constexpr auto kernel = selscan_bwd<T, S, FULL>;
     constexpr int kTile = P::kWarps * P::kCh;
     const int tpg = (p.cpg + kTile - 1) / kTile;
     const int64_t slots = p.slots + (p.g.cu != nullptr ? 16 : 0);
     if (slots > 0) {
-        cudaError_t e = cudaFuncSetAttribute(selscan_bwd<T, S>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(typename P::Cta));
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(typename P::Cta));
         if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(selscan_bwd<T, S>, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
         if (e != cudaSuccess) return e;
-        selscan_bwd<T, S><<<(unsigned)(slots * tpg * p.G), P::kWarps * 32, (int)sizeof(typename P::Cta), stream>>>(p);
+        kernel<<<(unsigned)(slots * tpg * p.G), P::kWarps * 32, (int)sizeof(typename P::Cta), stream>>>(p);
         const cudaError_t l = cudaGetLastError();
         if (l != cudaSuccess) return l;
     }
@@ -640,19 +642,26 @@ template <typename T, int S> cudaError_t go(const ScanParams& p, cudaStream_t st
     return cudaGetLastError();
 }
 
-template <typename T> cudaError_t by_states(const ScanParams& p, cudaStream_t stream) {
-    if (p.N <= 8) return go<T, 2>(p, stream);
-    if (p.N <= 16) return go<T, 4>(p, stream);
-    if (p.N <= 32) return go<T, 8>(p, stream);
-    return go<T, 16>(p, stream);
+template <typename T, bool FULL> cudaError_t by_states(const ScanParams& p, cudaStream_t stream) {
+    if (p.N <= 8) return go<T, 2, FULL>(p, stream);
+    if (p.N <= 16) return go<T, 4, FULL>(p, stream);
+    if (p.N <= 32) return go<T, 8, FULL>(p, stream);
+    return go<T, 16, FULL>(p, stream);
 }
+
+// bf16: where terms are cut to 11 bits, a token whose channels nearly cancel in dB or dC is off by
+// more than the rounding of its sum.  Among many tokens that is nothing; of few, it can be all of the result,
+// and time is the launches'.  Two tokens of 3560 channels, the worst of some: off by 0.0063, and with all bits by 0.0024; 33
+// tokens of 5120 channels take 62 us either way, 8192 of 2048 463 and some 500.
+constexpr int kFewTokens = 64;
 
 }  // namespace
 
 int selscan_bwd_channels(int N) { return N <= 16 ? 64 : N <= 32 ? 32 : 16; }
 
 cudaError_t launch_selscan_bwd(const ScanParams& p, int dtype, cudaStream_t stream) {
-    return dtype == SSD_BF16 ? by_states<__nv_bfloat16>(p, stream) : by_states<float>(p, stream);
+    if (dtype != SSD_BF16) return by_states<float, true>(p, stream);
+    return p.g.T <= kFewTokens ? by_states<__nv_bfloat16, true>(p, stream) : by_states<__nv_bfloat16, false>(p, stream);
 }
 
 }  // namespace ssd

@@ -276,6 +276,32 @@ def test_a_token_that_forgets(dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N", [8, 16, 48])
+def test_channels_that_cancel(dtype, N):
+    """Single tokens whose channels cancel in dB and dC: three of the same x and dt, with dout in
+    the ratio 4 : -3 : -1.  What is left is rounding: three of each term's factors (3 * 2^-24; the
+    channels share delta), and 24 terms' sum (24 * 2^-24): 1.7e-6 of the terms' absolute sum, 4e-6 allowed,
+    and the output's own half step."""
+    n, D = 2, 24
+    g = torch.Generator().manual_seed(11)
+    rnd = lambda *s: torch.randn(*s, generator=g)
+    three = lambda t: t.repeat_interleave(3, 1).to(DT[dtype])
+    x, dt = three(rnd(n, D // 3)), three(rnd(n, D // 3))
+    d = torch.randint(1, 16, (n, D // 3), generator=g).float()
+    dout = (three(d).float() * torch.tensor([1.0, -0.75, -0.25]).repeat(D // 3)).to(DT[dtype])
+    B, C, A = rnd(n, 1, N).to(DT[dtype]), rnd(n, 1, N).to(DT[dtype]), -torch.rand(D, N, generator=g)
+    ops = [t.cuda() for t in (x, dt, A, B, C)]
+    kw = dict(dt_softplus=True, nseqs=n)
+    _, _, st = ssd.selscan_fwd(*ops, return_states=True, **kw)
+    got = ssd.selscan_bwd(*ops, dout.cuda(), st, **kw)
+    terms = (torch.nn.functional.softplus(dt.double()) * x.double() * dout.double())
+    for k, other in (("dB", C), ("dC", B)):
+        want = terms.sum(1)[:, None, None] * other.double()
+        size = terms.abs().sum(1)[:, None, None] * other.double().abs()
+        assert ((got[k].double().cpu() - want).abs() <= want.abs() * torch.finfo(DT[dtype]).eps / 2 + 4e-6 * size).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_sequences_of_no_tokens_alone(dtype):
     """No tokens at all: states and their gradients pass through, the others are zero."""
     x = make(dtype, [0, 0], 0, 16, 16, 1, True, True, seed=10)
