@@ -57,9 +57,9 @@ ssd_status make(const ssd_selscan_dims* d, bool packed, bool backward, Scan* out
     // states: 256 tokens of 2048 channels (64 warps) 35 and 39, 512 of 5120 64 and 46, 2048 of
     // 2048 in 4 sequences 94 and 59, 8192 of 2048 860 and 154, in 6 sequences 217 and 151;
     // 16384 of 5120 in 12 427 and 616; 16384 of 2048 in 40 197 and 275; 4096 of 768, 64 states, in 8
-    // 120 and 154.  Backwards a CTA of 64 (32, 16) channels takes 295 ns a token by itself, and
-    // the cut's passes 1.7 ns for each token and CTA: the same sizes 87 and 70, 162 and 113, 263 and
-    // 153, 2400 and 460, 650 and 460, -, 790 and 890, 444 and 459.
+    // 120 and 154.  Backwards a CTA of 64 (32, 16) channels takes 310 ns a token by itself, and
+    // the cut's passes 1.8 ns for each token and CTA: the same sizes 96 and 65, 177 and 117, 282 and
+    // 158, 2490 and 486, 721 and 490, -, 850 and 936, 450 and 447.
     const int64_t bt = selscan_bwd_channels((int)q.N), tiles = (p.cpg + bt - 1) / bt;
     const int64_t warps = q.G * ((p.cpg * (q.N <= 16 ? 1 : q.N <= 32 ? 2 : 4) + 31) / 32);
     const int64_t sms = sm_count(), work = q.T * (backward ? tiles * q.G : warps);

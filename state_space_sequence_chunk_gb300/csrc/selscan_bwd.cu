@@ -18,16 +18,15 @@
 // gradient is summed in fp32 from them, so u and sum A w go in two terms of 11 bits (fp32: three, 520 -> 539 us);
 // y, which only dz (in the operands' type) needs, in one where that type is bf16.  Over the
 // channels (the 8 rows, then the CTA's warps, then a kernel of its own over the tiles; for
-// dB and dC): in bf16 a first product moves the values, state by channel, so that the
-// channels lie in the 4 lanes, and a second one sums them (each rounds its terms to 11
-// bits towards 0, a quarter of what rounding the result to bf16 loses at most); in fp32 by
-// shuffles.
+// dB and dC): by shuffles, in fp32.  Two more products of the tensor cores in bf16 calls (one to move the
+// channels into the 4 lanes, one to sum them) took 463 us instead of 490, but cut the terms to 11 bits, and a
+// token whose channels cancel was off by more than the rounding of its sum.
 //
 // What bounds it: a token takes a warp of 16 channels and 16 states some 200
-// instructions, 63 of them packed multiply-adds, and the registers (200 to 255) leave
+// instructions, 63 of them packed multiply-adds, and the registers (180 to 255) leave
 // two warps a quarter-SM, which issue in every second clock.  8192 tokens of 2048
-// channels in 6 sequences: 467 us a call, 670 without the cut into ranges.  Against
-// the form of that time (454 to 511 us before make_up): sums by shuffles and rows loaded where
+// channels in 6 sequences: 490 us a call.  Measured with the tensor cores' sums, against 463 (454
+// to 511 for the older ones): no cut into ranges 670; sums over states by shuffles too and rows loaded where
 // they are used 617; pairs of channels instead of states, or delta and u stored in pairs: 539, 509 (more
 // moves for the tensor cores' operands, more shared memory traffic); slabs of 2 tokens 485, of 8
 // tokens 646.  More warps an SM, which the compiler's spills cost more than they
@@ -50,7 +49,6 @@ template <typename T, int S> struct Plan {     // N <= 4 S
     static constexpr int kCh = 8 * C;          // channels of a warp
     static constexpr int NP = 4 * S;
     static constexpr int kSlabs = kChunk / K;
-    static constexpr int kTiles = (S + 3) / 4; // tiles of 16 states in the sums over channels
     struct Warp {                              // shared memory of a warp
         T raw[2][4][kChunk][kCh];              // x, dt, dout and z of a chunk and the next
         float check[2][C * S * 32];            // the stored states, as the lanes hold them
@@ -66,17 +64,11 @@ template <typename T, int S> struct Plan {     // N <= 4 S
     };
 };
 
-// Products of 16 x 4 (16 x 8) and 4 x 8 (8 x 8) numbers whose low 13 bits are not looked at.
+// The product of 16 x 4 and 4 x 8 numbers whose low 13 bits are not looked at.
 __device__ __forceinline__ void mma4(float (&c)[4], float a0, float a1, float b) {
     asm("mma.sync.aligned.m16n8k4.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5}, {%6}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(__float_as_uint(a0)), "r"(__float_as_uint(a1)), "r"(__float_as_uint(b)));
-}
-__device__ __forceinline__ void mma8(float (&c)[4], const float (&a)[4], float b0, float b1) {
-    asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(__float_as_uint(a[0])), "r"(__float_as_uint(a[1])), "r"(__float_as_uint(a[2])), "r"(__float_as_uint(a[3])),
-          "r"(__float_as_uint(b0)), "r"(__float_as_uint(b1)));
 }
 // Adds to column `col` of c the sums of v0 (rows 0 .. 7) and v1 (8 .. 15) over the four lanes
 // of a row; hot is 1 in the lanes whose row number is col, else 0.  Each term counts 11 bits more of v.
@@ -133,7 +125,7 @@ template <int S> __device__ __forceinline__ void store_states_row(const f32x2 (&
     }
 }
 // The S states of lane q of a row of B or C as pairs.  Vector i of four of lane q lies at 4 i + q: so
-// the four lanes read other banks (64 states of 8192 tokens and 2048 channels: 1900 us; each lane's own side by side 1917).
+// the four lanes read other banks (64 states of 8192 tokens and 2048 channels: 1.01 times as fast as each lane's own side by side).
 template <int S> __device__ __forceinline__ void lds(f32x2 (&v)[S / 2], const float* row, int q) {
     if (S == 2) {
         v[0] = *reinterpret_cast<const f32x2*>(row + 2 * q);
@@ -147,8 +139,7 @@ template <int S> __device__ __forceinline__ void lds(f32x2 (&v)[S / 2], const fl
     }
 }
 
-// FULL: the sums over channels, and y's, with all of their terms' bits.
-template <typename T, int S, bool FULL>
+template <typename T, int S>
 __global__ void __launch_bounds__(Plan<T, S>::kWarps * 32, S <= 4 ? 2 : 1) selscan_bwd(const __grid_constant__ ScanParams p) {
     using P = Plan<T, S>;
     constexpr int C = P::C, K = P::K, kCh = P::kCh, NP = P::NP, H = S / 2, kThreads = P::kWarps * 32;
@@ -194,14 +185,6 @@ __global__ void __launch_bounds__(Plan<T, S>::kWarps * 32, S <= 4 ? 2 : 1) selsc
     auto per_channel = [&](const float* v) { return v != nullptr ? pair(v[dch], v[dch + C - 1]) : 0ull; };
     const f32x2 bias = per_channel(p.bias), skip = per_channel(p.Dk);
     f32x2 dD = 0ull, db = 0ull;
-    // the rows that a lane's values go to in the sums over channels: value s of lane (g, q) to
-    // row 4 q + s % 4 of its tile
-    float pick[2][4];
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            pick[i][j] = (g & 3) == 2 * i + j / 2 && q4 == (g >> 2) + 2 * (j & 1) ? 1.f : 0.f;
     const bool cut = p.g.R <= p.g.T, gated = p.z != nullptr;
     for (int item = slot * p.per_slot; item < min((slot + 1) * p.per_slot, p.g.items); ++item) {
         ScanItem it;
@@ -355,15 +338,11 @@ __global__ void __launch_bounds__(Plan<T, S>::kWarps * 32, S <= 4 ? 2 : 1) selsc
 #pragma unroll
                     for (int i = 0; i < H; ++i) *reinterpret_cast<f32x2*>(&w.start[sl][(c * H + i) * 64 + lane * 2]) = h[c][i];
             }
-            // of eight tokens (columns): u, sum A w and C.h by channel, dB and dC by state
-            float au[4], av[4], ay[4], ab[2][P::kTiles][4];
+            // of eight tokens (columns): u, sum A w and C.h by channel
+            float au[4], av[4], ay[4];
             auto clear = [&] {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    au[i] = av[i] = ay[i] = 0.f;
-#pragma unroll
-                    for (int j = 0; j < P::kTiles; ++j) ab[0][j][i] = ab[1][j][i] = 0.f;
-                }
+                for (int i = 0; i < 4; ++i) au[i] = av[i] = ay[i] = 0.f;
             };
             clear();
             for (int sl = slabs - 1; sl >= 0; --sl) {
@@ -394,7 +373,7 @@ __global__ void __launch_bounds__(Plan<T, S>::kWarps * 32, S <= 4 ? 2 : 1) selsc
                         unpair(ys, lo, hi);
                         y[c] = lo + hi;
                     }
-                    add_rows<FULL ? 3 : 1>(ay, y[0], y[1], hot[k]);    // for dz
+                    add_rows<kExact ? 3 : 1>(ay, y[0], y[1], hot[k]);  // for dz
                 }
 #pragma unroll
                 for (int k = K - 1; k >= 0; --k) {
@@ -432,43 +411,25 @@ __global__ void __launch_bounds__(Plan<T, S>::kWarps * 32, S <= 4 ? 2 : 1) selsc
                         unpair(vs, lo, hi);
                         v[c] = lo + hi;
                     }
-                    add_rows<FULL ? 3 : 2>(au, u[0], u[1], hot[k]);       // (dt_bias's gradient is in fp32)
-                    add_rows<FULL ? 3 : 2>(av, v[0], v[1], hot[k]);
-                    if (FULL) {                        // sums over the channels by shuffles
-                        float part[2 * S];
+                    add_rows<kExact ? 3 : 2>(au, u[0], u[1], hot[k]);       // (dt_bias's gradient is in fp32)
+                    add_rows<kExact ? 3 : 2>(av, v[0], v[1], hot[k]);
+                    float part[2 * S];                 // the sums over the warp's channels
 #pragma unroll
-                        for (int i = 0; i < H; ++i) {
-                            unpair(dB[i], part[2 * i], part[2 * i + 1]);
-                            unpair(dC[i], part[S + 2 * i], part[S + 2 * i + 1]);
-                        }
-                        halve<2 * S>(part, lane, 16);
-                        halve<S>(part, lane, 8);
-                        halve<S / 2>(part, lane, 4);
-                        // value g of 2 S / 8 each; with S = 2 lanes differing in bit 2 hold the same
-                        constexpr int kLeft = S >= 4 ? S / 4 : 1;
-                        if (S >= 4 || (lane & 4) == 0)
-#pragma unroll
-                            for (int i = 0; i < kLeft; ++i) {
-                                const int x = S >= 4 ? g * kLeft + i : g >> 1;     // 0 .. S - 1: dB, then dC
-                                w.dbc[t][x / S * NP + n0 + x % S] = part[i];
-                            }
-                    } else {
-                        // A first product moves the channels from the rows' lanes to the columns'
-                        // (state by channel), a second one sums them into the token's column.
-#pragma unroll
-                        for (int kind = 0; kind < 2; ++kind)
-#pragma unroll
-                            for (int j = 0; j < P::kTiles; ++j) {
-                                float m[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                                for (int i = 0; i < 2 && 2 * j + i < H; ++i) {
-                                    float lo, hi;
-                                    unpair(kind == 0 ? dB[2 * j + i] : dC[2 * j + i], lo, hi);
-                                    mma8(m, pick[i], lo, hi);
-                                }
-                                mma4(ab[kind][j], m[0] + m[1], m[2] + m[3], hot[k]);
-                            }
+                    for (int i = 0; i < H; ++i) {
+                        unpair(dB[i], part[2 * i], part[2 * i + 1]);
+                        unpair(dC[i], part[S + 2 * i], part[S + 2 * i + 1]);
                     }
+                    halve<2 * S>(part, lane, 16);
+                    halve<S>(part, lane, 8);
+                    halve<S / 2>(part, lane, 4);
+                    // value g of 2 S / 8 each; with S = 2 lanes differing in bit 2 hold the same
+                    constexpr int kLeft = S >= 4 ? S / 4 : 1;
+                    if (S >= 4 || (lane & 4) == 0)
+#pragma unroll
+                        for (int i = 0; i < kLeft; ++i) {
+                            const int x = S >= 4 ? g * kLeft + i : g >> 1;     // 0 .. S - 1: dB, then dC
+                            w.dbc[t][x / S * NP + n0 + x % S] = part[i];
+                        }
                 }
                 if ((sl * K & 7) != 0) continue;
                 // eight tokens are complete: a lane's channels, two tokens
@@ -514,17 +475,6 @@ __global__ void __launch_bounds__(Plan<T, S>::kWarps * 32, S <= 4 ? 2 : 1) selsc
                             put(p.dz, mul2(mul2(dy, fma2(skip, x, pair(ay[e], C == 2 ? ay[2 + e] : ay[e]))), slope));
                         }
                     }
-                }
-                if (!FULL) {
-#pragma unroll
-                    for (int kind = 0; kind < 2; ++kind)
-#pragma unroll
-                        for (int j = 0; j < P::kTiles; ++j)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {       // row g + 8 (i / 2): state of lane row / 4, value row % 4
-                                const int m = g + 8 * (i >> 1), t = sl * K + 2 * q4 + (i & 1);
-                                if (4 * j + (m & 3) < S) w.dbc[t][kind * NP + (m >> 2) * S + 4 * j + (m & 3)] = ab[kind][j][i];
-                            }
                 }
                 clear();
             }
@@ -621,9 +571,9 @@ __global__ void __launch_bounds__(128) selscan_sum_a(const __grid_constant__ Sca
     else if (p.dbias != nullptr) p.dbias[e - na - p.D] = s;
 }
 
-template <typename T, int S, bool FULL> cudaError_t go(const ScanParams& p, cudaStream_t stream) {
+template <typename T, int S> cudaError_t go(const ScanParams& p, cudaStream_t stream) {
     using P = Plan<T, S>;
-    constexpr auto kernel = selscan_bwd<T, S, FULL>;
+    constexpr auto kernel = selscan_bwd<T, S>;
     constexpr int kTile = P::kWarps * P::kCh;
     const int tpg = (p.cpg + kTile - 1) / kTile;
     const int64_t slots = p.slots + (p.g.cu != nullptr ? 16 : 0);
@@ -642,26 +592,19 @@ template <typename T, int S, bool FULL> cudaError_t go(const ScanParams& p, cuda
     return cudaGetLastError();
 }
 
-template <typename T, bool FULL> cudaError_t by_states(const ScanParams& p, cudaStream_t stream) {
-    if (p.N <= 8) return go<T, 2, FULL>(p, stream);
-    if (p.N <= 16) return go<T, 4, FULL>(p, stream);
-    if (p.N <= 32) return go<T, 8, FULL>(p, stream);
-    return go<T, 16, FULL>(p, stream);
+template <typename T> cudaError_t by_states(const ScanParams& p, cudaStream_t stream) {
+    if (p.N <= 8) return go<T, 2>(p, stream);
+    if (p.N <= 16) return go<T, 4>(p, stream);
+    if (p.N <= 32) return go<T, 8>(p, stream);
+    return go<T, 16>(p, stream);
 }
-
-// bf16: where terms are cut to 11 bits, a token whose channels nearly cancel in dB or dC is off by
-// more than the rounding of its sum.  Among many tokens that is nothing; of few, it can be all of the result,
-// and time is the launches'.  Two tokens of 3560 channels, the worst of some: off by 0.0063, and with all bits by 0.0024; 33
-// tokens of 5120 channels take 62 us either way, 8192 of 2048 463 and some 500.
-constexpr int kFewTokens = 64;
 
 }  // namespace
 
 int selscan_bwd_channels(int N) { return N <= 16 ? 64 : N <= 32 ? 32 : 16; }
 
 cudaError_t launch_selscan_bwd(const ScanParams& p, int dtype, cudaStream_t stream) {
-    if (dtype != SSD_BF16) return by_states<float, true>(p, stream);
-    return p.g.T <= kFewTokens ? by_states<__nv_bfloat16, true>(p, stream) : by_states<__nv_bfloat16, false>(p, stream);
+    return dtype == SSD_BF16 ? by_states<__nv_bfloat16>(p, stream) : by_states<float>(p, stream);
 }
 
 }  // namespace ssd
