@@ -16,7 +16,7 @@
 // the tensor cores, rows x lanes by lanes x tokens, whose second operand is 1 in the
 // token's column, so that eight tokens' sums lie ready in eight columns.  dt_bias's
 // gradient is summed in fp32 from them, so u and sum A w go in two terms of 11 bits (fp32: three, 520 -> 539 us);
-// y, which only dz (in the operands' type) needs, in one where that type is bf16.  Over the
+// y in three, since its terms may cancel one another or D x (cut to 11 bits 4 % of dz's values were not the rounded ones).  Over the
 // channels (the 8 rows, then the CTA's warps, then a kernel of its own over the tiles; for
 // dB and dC): by shuffles, in fp32.  Two more products of the tensor cores in bf16 calls (one to move the
 // channels into the 4 lanes, one to sum them) took 463 us instead of 490, but cut the terms to 11 bits, and a
@@ -373,7 +373,7 @@ __global__ void __launch_bounds__(Plan<T, S>::kWarps * 32, S <= 4 ? 2 : 1) selsc
                         unpair(ys, lo, hi);
                         y[c] = lo + hi;
                     }
-                    add_rows<kExact ? 3 : 1>(ay, y[0], y[1], hot[k]);  // for dz
+                    add_rows<3>(ay, y[0], y[1], hot[k]);  // for dz: its terms may cancel, so all of their bits
                 }
 #pragma unroll
                 for (int k = K - 1; k >= 0; --k) {

@@ -1,0 +1,84 @@
+"""The selective scan value by value against the recurrence in 64 bits: sums whose terms
+cancel, gates and steps far from 0, states of every memory.  In what follows u = 2^-24, one
+rounding to fp32; the hardware's exponential is off by 4 u at most, its reciprocal by 2 u."""
+import numpy as np
+import pytest
+import torch
+
+import state_space_sequence_chunk_gb300 as ssd
+from selscan_ref import selscan, sigmoid
+from test_gpu_selscan import DT, args, dev, f64, make, options, ref
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+HALF = {"bf16": 2.0 ** -8, "f32": U}
+
+
+def near(got, want, slack):
+    """Every value within `slack` of the reference."""
+    off = np.abs(f64(got) - want) - slack
+    assert (off <= 0).all(), (float(off.max()), np.unravel_index(off.argmax(), off.shape), float((off > 0).mean()))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("kind", ["states", "skip"])
+@pytest.mark.parametrize("N", [8, 16, 48])
+def test_gate_gradient_where_states_cancel(dtype, kind, N):
+    """dz of single tokens, dout (C.h + D x) silu'(z), where the states' terms cancel one another
+    but for the 64th part of one, or D x but for 2^-9 of it.  A term has 3 roundings (delta x,
+    times B, times C), their sum as many as N / 8 + 5, D x one: 16 u of the terms' absolute sum.  |z| is 4
+    at most, so that silu' is off by 2^-18 of its two terms."""
+    n, D = 64, 24
+    g = torch.Generator().manual_seed(21)
+    rnd = lambda *s: torch.randn(*s, generator=g)
+    x, dout, z = rnd(n, D).to(DT[dtype]), rnd(n, D).to(DT[dtype]), rnd(n, D).clamp(-4, 4).to(DT[dtype])
+    dt = (0.02 + rnd(1, D).abs()).expand(n, D).to(DT[dtype]).contiguous()
+    A, skip = -torch.rand(D, N, generator=g), rnd(D)
+    if kind == "states":
+        half = rnd(n, N // 2).to(DT[dtype])
+        k = torch.randint(33, 64, (n, N // 2), generator=g).float() / 64
+        other = -k
+        other[:, 0] += 1 / 64
+        B, C = torch.cat([half, half], 1), torch.cat([k, other], 1).to(DT[dtype])
+        skip = torch.zeros(D)
+    else:
+        B, C = (rnd(1, N).expand(n, N).to(DT[dtype]).contiguous() for _ in range(2))
+        skip = (-dt[0].double() * (B[0].double() * C[0].double()).sum() * (1 - 2.0 ** -9)).float()
+    ops = [t.cuda() for t in (x, dt, A, B[:, None], C[:, None])]
+    kw = dict(D=skip.cuda(), z=z.cuda(), nseqs=n)
+    _, _, st = ssd.selscan_fwd(*ops, return_states=True, **kw)
+    got = ssd.selscan_bwd(*ops, dout.cuda(), st, **kw)["dz"]
+    x, dt, B, C, z, dout, skip = (f64(t) for t in (x, dt, B, C, z, dout, skip))
+    terms = (dt * x)[:, :, None] * (B * C)[:, None]
+    y, size = terms.sum(2) + skip * x, np.abs(terms).sum(2) + np.abs(skip * x)
+    s = sigmoid(z)
+    slope, parts = s * (1 + z * (1 - s)), s * (1 + np.abs(z) * (1 - s))
+    want = dout * y * slope
+    near(got, want, HALF[dtype] * np.abs(want) + 16 * U * np.abs(dout * slope) * size + 2.0 ** -18 * np.abs(dout * y) * parts)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N", [6, 16, 40])
+def test_every_value(dtype, N):
+    """y, dx, ddt, dz, dB and dC value by value: half a step of their type, and 2e-5 of the terms'
+    absolute sum (decays of a memory of 50 tokens, each off by 4 u; delta by 8 u)."""
+    lens = [70, 1, 33]
+    x = make(dtype, lens, 2, 24, N, 1, True, False, seed=22)
+    d = dev(x)
+    y, _, st = ssd.selscan_fwd(*args(d), return_states=True, **options(d))
+    g = ssd.selscan_bwd(*args(d), d["dout"], st, **options(d))
+    want_y, _, want = ref(x, lens, grads=True)
+    # the same sums of the terms' absolute values, the gate taken into dout
+    z, dout = f64(x["z"]), f64(x["dout"])
+    s = sigmoid(z)
+    dt, bias, X, Dk = f64(x["dt"]), f64(x["bias"]), np.abs(f64(x["x"])), np.abs(f64(x["D"]))
+    gy = np.abs(dout * z * s)
+    size_y, _, size = selscan(X, dt, f64(x["A"]), np.abs(f64(x["B"])), np.abs(f64(x["C"])), lens, Dk, None, bias, True, None, gy)
+    delta, slope = np.logaddexp(dt + bias, 0), sigmoid(dt + bias)
+    u = (size["dx"] - Dk * gy) / delta
+    sizes = {"dx": size["dx"], "dB": size["dB"], "dC": size["dC"], "ddt": (2 * X * u) * slope - size["ddt"],   # x u and |A| w, not x u - |A| w
+             "dz": np.abs(dout) * size_y * s * (1 + np.abs(z) * (1 - s))}
+    inside = slice(0, sum(lens))
+    near(y[inside], want_y[inside], (HALF[dtype] * np.abs(want_y) + 2e-5 * size_y * np.abs(z * s))[inside])
+    for k, v in sizes.items():
+        near(g[k][inside], want[k][inside], (HALF[dtype] * np.abs(want[k]) + 2e-5 * v)[inside])
