@@ -12,25 +12,22 @@
 // come by cp.async while the chunk behind it is computed.
 //
 // A lane holds C channels x S states and a warp 8 C channels x 4 S states.  Two sums
-// cross lanes.  Over the states (the 4 lanes of a row, for dx, ddelta and y): a product of
-// the tensor cores, rows x lanes by lanes x tokens, whose second operand is 1 in the
-// token's column, so that eight tokens' sums lie ready in eight columns.  dt_bias's
-// gradient is summed in fp32 from them, so u and sum A w go in two terms of 11 bits (fp32: three, 520 -> 539 us);
-// y in three, since its terms may cancel one another or D x (cut to 11 bits 4 % of dz's values were not the rounded ones).  Over the
-// channels (the 8 rows, then the CTA's warps, then a kernel of its own over the tiles; for
-// dB and dC): by shuffles, in fp32.  Two more products of the tensor cores in bf16 calls (one to move the
-// channels into the 4 lanes, one to sum them) took 463 us instead of 490, but cut the terms to 11 bits, and a
-// token whose channels cancel was off by more than the rounding of its sum.
+// cross lanes, both in fp32 by shuffles that halve the values a lane keeps at each step.  Over the
+// states (the 4 lanes of a row, for dx, ddelta and y): of a slab's four tokens each lane ends with
+// the sums of one, whose outputs it makes.  Over the channels (for dB and dC): the 8 rows, then the CTA's
+// warps, then a kernel of its own over the tiles.  As products of the tensor cores with ones the sums
+// over states took 502 us (terms cut to 11 bits, three of each, so that they keep all of theirs) and 493 (two; one for y) instead
+// of 457, and leaned to 0, by 4e-8 to 8e-8 of ddt_bias: those sums are not rounded to nearest.  The sums
+// over channels on the tensor cores took 6 % less of the call, cut to 11 bits: a token whose
+// channels cancel was off by more than the rounding of its sum.
 //
-// What bounds it: a token takes a warp of 16 channels and 16 states some 200
-// instructions, 63 of them packed multiply-adds, and the registers (180 to 255) leave
-// two warps a quarter-SM, which issue in every second clock.  8192 tokens of 2048
-// channels in 6 sequences: 490 us a call.  Measured with the tensor cores' sums, against 463 (454
-// to 511 for the older ones): no cut into ranges 670; sums over states by shuffles too and rows loaded where
-// they are used 617; pairs of channels instead of states, or delta and u stored in pairs: 539, 509 (more
-// moves for the tensor cores' operands, more shared memory traffic); slabs of 2 tokens 485, of 8
-// tokens 646.  More warps an SM, which the compiler's spills cost more than they
-// bring: CTAs of 3 warps, three an SM 608, of 2 warps, four 472, five 607.
+// What bounds it: the registers (168 to 255) leave two warps a quarter-SM, each waiting for its own
+// last results.  8192 tokens of 2048 channels in 6 sequences: 457 us a call.  Measured with the tensor cores'
+// sums over states and channels, against 463 (454 to 511 for the older ones): no cut into ranges 670; rows
+// loaded where they are used 617; pairs of channels instead of states, or delta and u stored in
+// pairs: 539, 509; slabs of 2 tokens 485, of 8 tokens 646; more warps an SM, which the
+// compiler's spills cost more than they bring: CTAs of 3 warps, three an SM 608, of 2 warps, four
+// 472, five 607.
 #include <type_traits>
 
 #include "selscan.cuh"
@@ -64,20 +61,16 @@ template <typename T, int S> struct Plan {     // N <= 4 S
     };
 };
 
-// The product of 16 x 4 and 4 x 8 numbers whose low 13 bits are not looked at.
-__device__ __forceinline__ void mma4(float (&c)[4], float a0, float a1, float b) {
-    asm("mma.sync.aligned.m16n8k4.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5}, {%6}, {%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(__float_as_uint(a0)), "r"(__float_as_uint(a1)), "r"(__float_as_uint(b)));
-}
-// Adds to column `col` of c the sums of v0 (rows 0 .. 7) and v1 (8 .. 15) over the four lanes
-// of a row; hot is 1 in the lanes whose row number is col, else 0.  Each term counts 11 bits more of v.
-template <int TERMS> __device__ __forceinline__ void add_rows(float (&c)[4], float v0, float v1, float hot) {
+// The sums over the four lanes of a row of K tokens' values of C channels, in fp32: lane q gets
+// those of token q % K, in v[0] (and v[1]).
+template <int K, int C> __device__ __forceinline__ void sum_row(float (&v)[K * C], int lane) {
+    if (K == 4) {
+        halve<K * C>(v, lane, 2);
+        halve<K * C / 2>(v, lane, 1);
+    } else {
+        halve<K * C>(v, lane, 1);
 #pragma unroll
-    for (int i = 0; i < TERMS; ++i) {
-        mma4(c, v0, v1, hot);
-        v0 -= __uint_as_float(__float_as_uint(v0) & 0xFFFFE000u);
-        v1 -= __uint_as_float(__float_as_uint(v1) & 0xFFFFE000u);
+        for (int c = 0; c < C; ++c) v[c] += __shfl_xor_sync(0xffffffffu, v[c], 2);
     }
 }
 
@@ -338,18 +331,9 @@ __global__ void __launch_bounds__(Plan<T, S>::kWarps * 32, S <= 4 ? 2 : 1) selsc
 #pragma unroll
                     for (int i = 0; i < H; ++i) *reinterpret_cast<f32x2*>(&w.start[sl][(c * H + i) * 64 + lane * 2]) = h[c][i];
             }
-            // of eight tokens (columns): u, sum A w and C.h by channel
-            float au[4], av[4], ay[4];
-            auto clear = [&] {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) au[i] = av[i] = ay[i] = 0.f;
-            };
-            clear();
             for (int sl = slabs - 1; sl >= 0; --sl) {
                 start_of(sl);
-                float hot[K];                          // 1 in the lanes whose row is the token's column
-#pragma unroll
-                for (int k = 0; k < K; ++k) hot[k] = g == (sl * K & 7) + k ? 1.f : 0.f;
+                float y[K * C], u[K * C], v[K * C];    // C.h, u and sum A w by token and channel
                 f32x2 a[K][C][H], ah[K][C][H];
 #pragma unroll
                 for (int k = 0; k < K; ++k) {
@@ -358,7 +342,6 @@ __global__ void __launch_bounds__(Plan<T, S>::kWarps * 32, S <= 4 ? 2 : 1) selsc
                     channel(t, dd, uu);
                     lds<S>(B, sh.bc[0][t], q4);
                     lds<S>(Cv, sh.bc[1][t], q4);
-                    float y[2] = {0.f, 0.f};
 #pragma unroll
                     for (int c = 0; c < C; ++c) {
                         f32x2 ys = 0ull;
@@ -371,10 +354,10 @@ __global__ void __launch_bounds__(Plan<T, S>::kWarps * 32, S <= 4 ? 2 : 1) selsc
                         }
                         float lo, hi;
                         unpair(ys, lo, hi);
-                        y[c] = lo + hi;
+                        y[k * C + c] = lo + hi;
                     }
-                    add_rows<3>(ay, y[0], y[1], hot[k]);  // for dz: its terms may cancel, so all of their bits
                 }
+                sum_row<K, C>(y, lane);
 #pragma unroll
                 for (int k = K - 1; k >= 0; --k) {
                     const int t = sl * K + k;
@@ -390,7 +373,6 @@ __global__ void __launch_bounds__(Plan<T, S>::kWarps * 32, S <= 4 ? 2 : 1) selsc
                     lds<S>(B, sh.bc[0][t], q4);
                     lds<S>(Cv, sh.bc[1][t], q4);
                     f32x2 dB[H], dC[H];
-                    float u[2] = {0.f, 0.f}, v[2] = {0.f, 0.f};
 #pragma unroll
                     for (int c = 0; c < C; ++c) {
                         f32x2 us = 0ull, vs = 0ull;
@@ -407,12 +389,10 @@ __global__ void __launch_bounds__(Plan<T, S>::kWarps * 32, S <= 4 ? 2 : 1) selsc
                         }
                         float lo, hi;
                         unpair(us, lo, hi);
-                        u[c] = lo + hi;
+                        u[k * C + c] = lo + hi;
                         unpair(vs, lo, hi);
-                        v[c] = lo + hi;
+                        v[k * C + c] = lo + hi;
                     }
-                    add_rows<kExact ? 3 : 2>(au, u[0], u[1], hot[k]);       // (dt_bias's gradient is in fp32)
-                    add_rows<kExact ? 3 : 2>(av, v[0], v[1], hot[k]);
                     float part[2 * S];                 // the sums over the warp's channels
 #pragma unroll
                     for (int i = 0; i < H; ++i) {
@@ -431,14 +411,14 @@ __global__ void __launch_bounds__(Plan<T, S>::kWarps * 32, S <= 4 ? 2 : 1) selsc
                             w.dbc[t][x / S * NP + n0 + x % S] = part[i];
                         }
                 }
-                if ((sl * K & 7) != 0) continue;
-                // eight tokens are complete: a lane's channels, two tokens
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int t = sl * K + 2 * q4 + e;
-                    if (t < nt && in) {
+                sum_row<K, C>(u, lane);
+                sum_row<K, C>(v, lane);
+                {
+                    // a lane's channels, one token of the slab
+                    const int t = sl * K + q4 % K;
+                    if (t < nt && in && q4 < K) {
                         // (one channel: both halves of a pair are it)
-                        const f32x2 x = raw(0, t), dy = raw(2, t), u = pair(au[e], C == 2 ? au[2 + e] : au[e]);
+                        const f32x2 x = raw(0, t), dy = raw(2, t), us = pair(u[0], u[C - 1]);
                         f32x2 delta, gy;
                         if (C == 2) {
                             delta = pair(w.du[t][2 * g * C], w.du[t][2 * g * C + 2]);
@@ -447,8 +427,8 @@ __global__ void __launch_bounds__(Plan<T, S>::kWarps * 32, S <= 4 ? 2 : 1) selsc
                             delta = both(w.du[t][2 * g]);
                             gy = both(w.gy[t][g]);
                         }
-                        const f32x2 ox = fma2(delta, u, mul2(skip, gy));
-                        f32x2 ot = fma2(x, u, mul2(pair(av[e], C == 2 ? av[2 + e] : av[e]), both(0.69314718055994531f)));   // A = a2 ln 2
+                        const f32x2 ox = fma2(delta, us, mul2(skip, gy));
+                        f32x2 ot = fma2(x, us, mul2(pair(v[0], v[C - 1]), both(0.69314718055994531f)));   // A = a2 ln 2
                         if (p.softplus) {
                             float a, b;
                             unpair(add2(raw(1, t), bias), a, b);
@@ -472,11 +452,10 @@ __global__ void __launch_bounds__(Plan<T, S>::kWarps * 32, S <= 4 ? 2 : 1) selsc
                             unpair(z, a, b);
                             const f32x2 s = pair(sigmoid(a), sigmoid(b)), zs = mul2(z, s);
                             const f32x2 slope = fma2(zs, fma2(s, both(-1.f), both(1.f)), s);
-                            put(p.dz, mul2(mul2(dy, fma2(skip, x, pair(ay[e], C == 2 ? ay[2 + e] : ay[e]))), slope));
+                            put(p.dz, mul2(mul2(dy, fma2(skip, x, pair(y[0], y[C - 1]))), slope));
                         }
                     }
                 }
-                clear();
             }
             if (nt == kChunk) {
                 float of[2];
