@@ -14,7 +14,7 @@
 // What bounds it: for 16 states a token costs a warp 100 instructions, 91 clocks of
 // the multiply-add pipe and 81 of the exponential's, of which three warps a
 // quarter-SM (168 registers) keep some 60 % busy.  16384 tokens of 5120 channels in
-// 12 sequences: 427 us (10 of them make_up).  Eight states a lane, two lanes a channel
+// 12 sequences: 436 us (20 of them make_up).  Eight states a lane, two lanes a channel
 // (more warps, but every row of B and C is read twice as often for the same work) took
 // 1.08 times that, four states 1.41; the next tile's delta made between this one's tokens
 // 1.03; the products delta A by scalar instructions, which alone run faster beside the exponential, 1.03;

@@ -102,3 +102,30 @@ def test_sums_over_states_lean_to_no_side(dtype, N):
     want = f64(x[0]) * f64(dout[0]) * (f64(B) * f64(C)).sum()
     lean = ((got - want) / want).mean()
     assert abs(lean) < 3.6e-8, lean
+
+
+@pytest.mark.parametrize("extra", [0, 1])
+@pytest.mark.parametrize("cut", [True, False])
+@pytest.mark.parametrize("rate", [1e-3, 1e-2, 0.04, 0.1, 1.0])
+def test_states_of_every_memory_lean_to_no_side(rate, cut, extra):
+    """2400 (2401) tokens whose states decay by `rate` a token on average: final states, and the
+    initial state's gradient, against 64 bits.  The fast exponential is low by 5.5e-9 on average
+    near 1 and by 2.4e-8 from 0.01 on, and a state of inputs of either sign remembers
+    exp(-2 rate) / (1 - exp(-2 rate)) tokens: what these lose together would be missing.  A third of that may be,
+    or 1e-7.  (Roundings: 0.7 u a token, of 500 tokens 16 u, of 1024 states' mean 0.5 u, 3e-8.)"""
+    lost = (5.5e-9 if rate < 2e-3 else 2.4e-8) * np.exp(-2 * rate) / (1 - np.exp(-2 * rate))
+    T, D, N = 2400 + extra, 64, 16
+    g = torch.Generator().manual_seed(24)
+    rnd = lambda *s: torch.randn(*s, generator=g)
+    uni = lambda *s: torch.rand(*s, generator=g)
+    x, B, C, dout = rnd(T, D), rnd(T, 1, N), rnd(T, 1, N), rnd(T, D)
+    dt, A = rate * (0.5 + uni(T, D)), -(0.8 + 0.4 * uni(D, N))
+    ops = [t.cuda() for t in (x, dt, A, B, C)]
+    # (a bound on the lengths that is too low only guides the cut: whole sequences)
+    kw = dict(cu_seqlens=torch.tensor([0, T], dtype=torch.int32, device="cuda"), max_seqlen=0 if cut else 1)
+    _, fin, st = ssd.selscan_fwd(*ops, return_states=True, **kw)
+    got = ssd.selscan_bwd(*ops, dout.cuda(), st, return_dinit=True, **kw)["dinit_state"]
+    _, wfin, want = selscan(*(f64(t) for t in (x, dt, A, B, C)), [T], softplus=False, dout=f64(dout))
+    for a, b in ((fin, wfin), (got, want["dinit_state"])):
+        lean = ((f64(a) - b) * b).sum() / (b * b).sum()
+        assert abs(lean) < max(lost / 3, 1e-7), lean
