@@ -136,7 +136,6 @@ template <typename T, int S>
 __global__ void __launch_bounds__(Plan<T, S>::kWarps * 32, S <= 4 ? 2 : 1) selscan_bwd(const __grid_constant__ ScanParams p) {
     using P = Plan<T, S>;
     constexpr int C = P::C, K = P::K, kCh = P::kCh, NP = P::NP, H = S / 2, kThreads = P::kWarps * 32;
-    constexpr bool kExact = sizeof(T) == 4;
     extern __shared__ __align__(16) unsigned char smem[];
     typename P::Cta& sh = *reinterpret_cast<typename P::Cta*>(smem);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q4 = lane & 3;
@@ -274,7 +273,7 @@ __global__ void __launch_bounds__(Plan<T, S>::kWarps * 32, S <= 4 ? 2 : 1) selsc
                 f32x2 dl = add2(raw(1, t), bias);
                 if (p.softplus) {
                     unpair(dl, v0, v1);
-                    dl = softplus2<kExact>(v0, v1);
+                    dl = softplus2(v0, v1);
                 }
                 if (t >= nt) dl = 0ull;                // rows past the end leave the state alone (their x and dout are 0)
                 sum = add2(sum, dl);
@@ -432,7 +431,7 @@ __global__ void __launch_bounds__(Plan<T, S>::kWarps * 32, S <= 4 ? 2 : 1) selsc
                         if (p.softplus) {
                             float a, b;
                             unpair(add2(raw(1, t), bias), a, b);
-                            ot = mul2(ot, pair(softplus_grad<kExact>(a), softplus_grad<kExact>(b)));
+                            ot = mul2(ot, pair(softplus_grad(a), softplus_grad(b)));
                         }
                         dD = fma2(gy, x, dD);
                         db = add2(db, ot);

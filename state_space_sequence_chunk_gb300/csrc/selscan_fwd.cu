@@ -14,7 +14,7 @@
 // What bounds it: for 16 states a token costs a warp 100 instructions, 91 clocks of
 // the multiply-add pipe and 81 of the exponential's, of which three warps a
 // quarter-SM (168 registers) keep some 60 % busy.  16384 tokens of 5120 channels in
-// 12 sequences: 436 us (20 of them make_up).  Eight states a lane, two lanes a channel
+// 12 sequences: 444 us (20 of them make_up).  Eight states a lane, two lanes a channel
 // (more warps, but every row of B and C is read twice as often for the same work) took
 // 1.08 times that, four states 1.41; the next tile's delta made between this one's tokens
 // 1.03; the products delta A by scalar instructions, which alone run faster beside the exponential, 1.03;
@@ -76,7 +76,7 @@ template <int S> __device__ __forceinline__ void store_row(const f32x2 (&h)[S / 
 template <typename T, int S, int LPC, int MODE>
 __global__ void __launch_bounds__(kWarps * 32, S == 16 && LPC == 1 ? 6 : 1) selscan_walk(const __grid_constant__ ScanParams p) {
     constexpr int kCh = 32 / LPC, NP = S * LPC, kVec = kTok * NP / 4, kPer = (kVec + 31) / 32, kOwn = kTok / LPC;
-    constexpr bool kExact = sizeof(T) == 4, SUMS = MODE != kScanMain, REV = MODE == kScanRevSums;
+    constexpr bool SUMS = MODE != kScanMain, REV = MODE == kScanRevSums;
     constexpr int kPieces = kTok * kCh * sizeof(T) / 16;    // 16-byte pieces of a tile of x, of dt and of z
     constexpr int kRowPieces = kCh * sizeof(T) / 16, kCopies = (3 * kPieces + 31) / 32;
     struct Warp {
@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(kWarps * 32, S == 16 && LPC == 1 ? 6 : 1) sels
             for (int i = 0; i < kOwn / 2; ++i) {
                 float a, b;
                 unpair(dl[i], a, b);
-                dl[i] = softplus2<kExact>(a, b);
+                dl[i] = softplus2(a, b);
             }
         if (MODE != kScanSums)
 #pragma unroll

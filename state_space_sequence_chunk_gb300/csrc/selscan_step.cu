@@ -16,25 +16,17 @@ namespace {
 
 constexpr int kWarps = 2;
 
-__device__ __forceinline__ float max_nan(float a, float b) {    // a NaN stays one
-    float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-    return r;
-}
 // h exp(e).  Thousands of calls multiply a state, one after another, so near 1 it is h + h (exp(e) - 1),
 // by the Taylor polynomial (to e^6: off by 1.2e-8 of h at most), whose errors have no side in
 // common; where more goes in a token, by the fast exponential, with what rounds away of e log2(e)
 // added back: what is left of a large state keeps its own precision.
 __device__ __forceinline__ f32x2 decayed(f32x2 h, f32x2 e) {
-    float e0, e1, q0, q1, h0, h1;
+    float e0, e1, h0, h1;
     unpair(e, e0, e1);
     e0 = max_nan(e0, -200.f);                // (every power from here on is 0)
     e1 = max_nan(e1, -200.f);
     e = pair(e0, e1);
-    const f32x2 q = mul2(e, both(-kLog2e));
-    const f32x2 lo = fma2(e, both(1.925963033500e-8f), fma2(e, both(kLog2e), q));     // log2(e) - kLog2e
-    unpair(q, q0, q1);
-    const f32x2 x0 = pair(ex2(-q0), ex2(-q1)), x = fma2(x0, mul2(lo, both(0.69314718f)), x0);
+    const f32x2 x = exp_in_range2(e);
     f32x2 m = fma2(e, both(1.f / 720), both(1.f / 120));
     m = fma2(e, m, both(1.f / 24));
     m = fma2(e, m, both(1.f / 6));
@@ -65,7 +57,6 @@ template <bool VEC> __device__ __forceinline__ void load4(f32x2 (&v)[2], const f
 template <typename T, int LPC, bool VEC>
 __global__ void __launch_bounds__(kWarps * 32, VEC ? 16 : 14) selscan_step(const __grid_constant__ ScanStep p) {
     constexpr int V = LPC < 4 ? LPC : 4, kWide = 32 / LPC, kTile = V * kWide;   // channels of a lane, abreast, of a warp
-    constexpr bool kExact = sizeof(T) == 4;
     const int lane = threadIdx.x & 31, part = lane % LPC, n = 4 * part;
     const int tpg = (p.cpg + kTile - 1) / kTile, tiles = tpg * p.G;
     const int64_t item = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
@@ -99,7 +90,7 @@ __global__ void __launch_bounds__(kWarps * 32, VEC ? 16 : 14) selscan_step(const
     const float4 Bv = widen(Br), Cv = widen(Cr);
     const f32x2 B[2] = {pair(Bv.x, Bv.y), pair(Bv.z, Bv.w)}, C[2] = {pair(Cv.x, Cv.y), pair(Cv.z, Cv.w)};
     const float x = to_f32(xr), v = to_f32(tr) + bias, z = to_f32(zr);
-    const float delta = p.softplus ? softplus<kExact>(v) : v, u = delta * x;
+    const float delta = p.softplus ? softplus(v) : v, u = delta * x;
     float s[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) {

@@ -129,3 +129,38 @@ def test_states_of_every_memory_lean_to_no_side(rate, cut, extra):
     for a, b in ((fin, wfin), (got, want["dinit_state"])):
         lean = ((f64(a) - b) * b).sum() / (b * b).sum()
         assert abs(lean) < max(lost / 3, 1e-7), lean
+
+
+def far(dtype):
+    """Numbers from -200 to 200, of the given type, dense where exponentials still count."""
+    v = torch.cat([torch.linspace(-200, 200, 353), torch.linspace(-90, -10, 511), torch.linspace(-10, 10, 160)])
+    return v.to(DT[dtype])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_steps_far_from_zero(dtype):
+    """delta = softplus(v) and its derivative for v from -200 to 200, of single tokens.  The exponential 5 u
+    (v log2(e) with its remainder, 4 u and a rounding), the quotient 2 + 1 + 1 u, the polynomial
+    and its sum 3 u, times x and B 2 u: 16 u allowed; the derivative 5 + 1 + 2 + 1 u and 4 products.  What is
+    below 2^-126 is flushed."""
+    v = far(dtype)
+    D, N = len(v), 4
+    g = torch.Generator().manual_seed(25)
+    rnd = lambda *s: torch.randn(*s, generator=g).to(DT[dtype])
+    x, B, C, dout = rnd(1, D), rnd(1, 1, N), rnd(1, 1, N), rnd(1, D)
+    A = torch.zeros(D, N)
+    ops = [t.cuda() for t in (x, v[None], A, B, C)]
+    kw = dict(dt_softplus=True, dt_bias=torch.zeros(D, device="cuda"))
+    _, fin, st = ssd.selscan_fwd(*ops, return_states=True, **kw)
+    cache = torch.zeros(1, D, N, device="cuda")
+    ssd.selscan_step(*ops, cache, **kw)
+    X, V, Bf, Cf = f64(x[0])[:, None], f64(v), f64(B[0]), f64(C[0])
+    want = np.logaddexp(V, 0)[:, None] * X * Bf
+    slack = 16 * U * np.abs(want) + 2.0 ** -125 * np.abs(X * Bf)
+    near(fin[0], want, slack)
+    near(cache[0], want, slack)
+    got = ssd.selscan_bwd(*ops, dout.cuda(), st, **kw)
+    terms = f64(x[0]) * f64(dout[0]) * (Bf * Cf).sum()
+    size = np.abs(f64(x[0]) * f64(dout[0])) * np.abs(Bf * Cf).sum()
+    slope = np.exp(-np.logaddexp(-V, 0))
+    near(got["ddt_bias"], terms * slope, 16 * U * size * slope + 2.0 ** -125 * size)
