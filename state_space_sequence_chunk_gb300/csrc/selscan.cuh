@@ -17,7 +17,7 @@
 // starts, and the main launch walks the ranges independently.
 #pragma once
 
-#include "f32x2.cuh"
+#include "approx.cuh"
 
 namespace ssd {
 
@@ -115,48 +115,6 @@ __device__ __forceinline__ bool scan_find(const ScanGeom& g, int i, ScanItem& it
     return true;
 }
 
-__device__ __forceinline__ float ex2(float v) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-    return r;
-}
-__device__ __forceinline__ float rcp(float v) {
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-    return r;
-}
-__device__ __forceinline__ f32x2 ex2_2(f32x2 v) {
-    float a, b;
-    unpair(v, a, b);
-    return pair(ex2(a), ex2(b));
-}
-__device__ __forceinline__ float max_nan(float a, float b) {    // a NaN stays one
-    float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ f32x2 both(float a) { return pair(a, a); }
-// exp(v).  The product with log2(e) is rounded; its remainder is added back (log2(e) in
-// two floats), so that the result is good to the exponential's own error also where v is large: without it
-// delta, and with it an fp32 state, is off by 7e-8 of it for each of |v| (2 % of the forward pass's time).  v from
-// -200 (every power from there on is 0) to 80.
-constexpr float kLog2eLow = 1.925963033500e-8f;       // log2(e) - kLog2e
-__device__ __forceinline__ float exp_in_range(float v) {
-    const float p = v * kLog2e, e = ex2(p);
-    return fmaf(e * 0.69314718f, fmaf(v, kLog2eLow, fmaf(v, kLog2e, -p)), e);
-}
-__device__ __forceinline__ f32x2 exp_in_range2(f32x2 v) {
-    const f32x2 q = mul2(v, both(-kLog2e)), lo = fma2(v, both(kLog2eLow), fma2(v, both(kLog2e), q));
-    float a, b;
-    unpair(q, a, b);
-    const f32x2 e = pair(ex2(-a), ex2(-b));
-    return fma2(e, mul2(lo, both(0.69314718f)), e);
-}
-// exp(-|v|); a NaN stays one.
-__device__ __forceinline__ float exp_neg_abs(float v) { return exp_in_range(max_nan(-fabsf(v), -200.f)); }
-__device__ __forceinline__ f32x2 exp_neg_abs2(float a, float b) {
-    return exp_in_range2(pair(max_nan(-fabsf(a), -200.f), max_nan(-fabsf(b), -200.f)));
-}
 // log(1 + e) for e in [0, 1], from log(1 + e) = 2 atanh(e / (2 + e)): the quotient is at
 // most 1/3, and atanh(s) / s is fitted by a polynomial in s^2 (Chebyshev interpolation on
 // [0, 1/9], off by 8e-9).  Small e keep their relative precision, which log(1 + e) loses.
@@ -182,19 +140,10 @@ __device__ __forceinline__ f32x2 softplus2(float a, float b) {
     const f32x2 l = log1p_unit2(exp_neg_abs2(a, b));
     return fma2(both(2.f), l, pair(fmaxf(a, 0.f), fmaxf(b, 0.f)));
 }
-// z sigmoid(z) of two numbers
-__device__ __forceinline__ f32x2 silu2(f32x2 z) {
-    float a, b;
-    unpair(mul2(z, both(-kLog2e)), a, b);
-    unpair(add2(pair(ex2(a), ex2(b)), both(1.f)), a, b);
-    return mul2(z, pair(rcp(a), rcp(b)));
-}
 // its derivative, 1 / (1 + exp(-v))
-__device__ __forceinline__ float softplus_grad(float v) {
-    const float e = exp_neg_abs(v), r = rcp(1.f + e);
-    return v >= 0.f ? r : e * r;
-}
-__device__ __forceinline__ float sigmoid(float z) { return rcp(1.f + ex2(-z * kLog2e)); }
+__device__ __forceinline__ float softplus_grad(float v) { return sigmoid<true>(v); }
+// z sigmoid(z) of two numbers
+template <bool EXACT> __device__ __forceinline__ f32x2 silu2(f32x2 z) { return mul2(z, sigmoid2<EXACT>(z)); }
 
 // A log2(e), so that the decays are base-2 exponentials; -inf (no memory) becomes a finite
 // value whose every power but the 0th is 0.

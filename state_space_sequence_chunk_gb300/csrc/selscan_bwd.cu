@@ -136,6 +136,7 @@ template <typename T, int S>
 __global__ void __launch_bounds__(Plan<T, S>::kWarps * 32, S <= 4 ? 2 : 1) selscan_bwd(const __grid_constant__ ScanParams p) {
     using P = Plan<T, S>;
     constexpr int C = P::C, K = P::K, kCh = P::kCh, NP = P::NP, H = S / 2, kThreads = P::kWarps * 32;
+    constexpr bool kExact = sizeof(T) == 4;
     extern __shared__ __align__(16) unsigned char smem[];
     typename P::Cta& sh = *reinterpret_cast<typename P::Cta*>(smem);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q4 = lane & 3;
@@ -277,7 +278,7 @@ __global__ void __launch_bounds__(Plan<T, S>::kWarps * 32, S <= 4 ? 2 : 1) selsc
                 }
                 if (t >= nt) dl = 0ull;                // rows past the end leave the state alone (their x and dout are 0)
                 sum = add2(sum, dl);
-                const f32x2 u = mul2(dl, raw(0, t)), gy = gated ? mul2(raw(2, t), silu2(raw(3, t))) : raw(2, t);
+                const f32x2 u = mul2(dl, raw(0, t)), gy = gated ? mul2(raw(2, t), silu2<kExact>(raw(3, t))) : raw(2, t);
                 float u0, u1;
                 unpair(dl, v0, v1);
                 unpair(u, u0, u1);
@@ -447,9 +448,7 @@ __global__ void __launch_bounds__(Plan<T, S>::kWarps * 32, S <= 4 ? 2 : 1) selsc
                         if (gated) {
                             // silu'(z) = s + z s (1 - s)
                             const f32x2 z = raw(3, t);
-                            float a, b;
-                            unpair(z, a, b);
-                            const f32x2 s = pair(sigmoid(a), sigmoid(b)), zs = mul2(z, s);
+                            const f32x2 s = sigmoid2<kExact>(z), zs = mul2(z, s);
                             const f32x2 slope = fma2(zs, fma2(s, both(-1.f), both(1.f)), s);
                             put(p.dz, mul2(mul2(dy, fma2(skip, x, pair(y[0], y[C - 1]))), slope));
                         }

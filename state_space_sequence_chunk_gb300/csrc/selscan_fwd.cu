@@ -76,7 +76,7 @@ template <int S> __device__ __forceinline__ void store_row(const f32x2 (&h)[S / 
 template <typename T, int S, int LPC, int MODE>
 __global__ void __launch_bounds__(kWarps * 32, S == 16 && LPC == 1 ? 6 : 1) selscan_walk(const __grid_constant__ ScanParams p) {
     constexpr int kCh = 32 / LPC, NP = S * LPC, kVec = kTok * NP / 4, kPer = (kVec + 31) / 32, kOwn = kTok / LPC;
-    constexpr bool SUMS = MODE != kScanMain, REV = MODE == kScanRevSums;
+    constexpr bool kExact = sizeof(T) == 4, SUMS = MODE != kScanMain, REV = MODE == kScanRevSums;
     constexpr int kPieces = kTok * kCh * sizeof(T) / 16;    // 16-byte pieces of a tile of x, of dt and of z
     constexpr int kRowPieces = kCh * sizeof(T) / 16, kCopies = (3 * kPieces + 31) / 32;
     struct Warp {
@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(kWarps * 32, S == 16 && LPC == 1 ? 6 : 1) sels
             for (int i = 0; i < kOwn / 2; ++i) o.gate[i] = both(1.f);
         if (gated)
 #pragma unroll
-            for (int i = 0; i < kOwn / 2; ++i) o.gate[i] = silu2(raw2(2, i));
+            for (int i = 0; i < kOwn / 2; ++i) o.gate[i] = silu2<kExact>(raw2(2, i));
         float* row = &w.du[LPC > 1 ? buf : 0][LPC > 1 ? cl : 0][0];
 #pragma unroll
         for (int i = 0; i < kOwn / 2; ++i) {

@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(kWarps * 32, VEC ? 16 : 14) selscan_step(const
 #pragma unroll
     for (int off = LPC / 2; off >= V; off >>= 1) o += __shfl_xor_sync(0xffffffffu, o, off);
     o = fmaf(skip, x, o);
-    if (p.z != nullptr) o *= z * sigmoid(z);
+    if (p.z != nullptr) o *= z * sigmoid<sizeof(T) == 4>(z);
     if (in && part < V) *y = from_f32<T>(o);
 }
 

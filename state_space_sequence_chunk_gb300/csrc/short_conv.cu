@@ -20,6 +20,7 @@
 // compiler mixes more rows, and spills (1.04 to 1.07 times as long, also with fewer CTAs an SM or rows ahead).
 #include <type_traits>
 
+#include "approx.cuh"
 #include "short_conv.cuh"
 
 namespace ssd {
@@ -28,17 +29,6 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kAhead = 8;        // rows loaded ahead
 constexpr int kFwdVec = 4, kBwdVec = 2;   // channels of a thread
-
-__device__ __forceinline__ float ex2(float v) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-    return r;
-}
-__device__ __forceinline__ float rcp(float v) {
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-    return r;
-}
 
 // V channels of a row: as loaded, and as pairs of floats.
 template <typename T, int V> struct Row;
@@ -155,23 +145,17 @@ template <int N2, int M> __device__ __forceinline__ void shift(f32x2 (&win)[M][N
 #pragma unroll
     for (int i = 0; i < N2; ++i) win[M - 1][i] = now[i];
 }
-__device__ __forceinline__ f32x2 sigmoid2(f32x2 v) {
-    float a, b;
-    unpair(mul2(v, pair(-kLog2e, -kLog2e)), a, b);
-    unpair(add2(pair(ex2(a), ex2(b)), pair(1.f, 1.f)), a, b);
-    return pair(rcp(a), rcp(b));
-}
-template <int N2> __device__ __forceinline__ void activate(f32x2 (&v)[N2], int act) {
+template <bool EXACT, int N2> __device__ __forceinline__ void activate(f32x2 (&v)[N2], int act) {
     if (act == SSD_ACT_NONE) return;
 #pragma unroll
-    for (int i = 0; i < N2; ++i) v[i] = mul2(v[i], sigmoid2(v[i]));
+    for (int i = 0; i < N2; ++i) v[i] = mul2(v[i], sigmoid2<EXACT>(v[i]));
 }
 // g = do a'(p): silu' = s + p s (1 - s) with s = sigmoid(p)
-template <int N2> __device__ __forceinline__ void back(f32x2 (&g)[N2], const f32x2 (&pre)[N2], int act) {
+template <bool EXACT, int N2> __device__ __forceinline__ void back(f32x2 (&g)[N2], const f32x2 (&pre)[N2], int act) {
     if (act == SSD_ACT_NONE) return;
 #pragma unroll
     for (int i = 0; i < N2; ++i) {
-        const f32x2 s = sigmoid2(pre[i]), ps = mul2(pre[i], s);
+        const f32x2 s = sigmoid2<EXACT>(pre[i]), ps = mul2(pre[i], s);
         g[i] = mul2(g[i], fma2(ps, fma2(s, pair(-1.f, -1.f), pair(1.f, 1.f)), s));
     }
 }
@@ -255,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(W, sizeof(T), false)) sh
             f32x2 now[N2], o[N2];
             r.get(now);
             taps.apply(win, now, o);
-            activate(o, p.act);
+            activate<sizeof(T) == 4>(o, p.act);
             shift(win, now);
             Row<T, V>::store(to, o);
             to += p.D;
@@ -327,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(W, sizeof(T), true)) sho
                 r.get(now);
                 q.get(g);
                 taps.apply(win, now, pre);
-                back(g, pre, p.act);
+                back<sizeof(T) == 4>(g, pre, p.act);
                 shift(win, now);
 #pragma unroll
                 for (int j = 0; j < W - 1; ++j)
@@ -401,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(W, sizeof(T), true)) sho
             xr.get(now);
             dr.get(g);
             taps.apply(win, now, pre);
-            back(g, pre, p.act);
+            back<sizeof(T) == 4>(g, pre, p.act);
 #pragma unroll
             for (int k = 0; k < N2; ++k) {
                 if (decltype(own)::value) {
@@ -526,7 +510,7 @@ __global__ void __launch_bounds__(kThreads) short_conv_step(const __grid_constan
         for (int j = 0; j < W - 1; ++j) r[j].get(win[j]);
         r[W - 1].get(now);
         taps.apply(win, now, o);
-        activate(o, p.act);
+        activate<sizeof(T) == 4>(o, p.act);
 #pragma unroll
         for (int j = 0; j < W - 1; ++j) *reinterpret_cast<decltype(r[j].r)*>(at + (int64_t)j * p.D) = r[j + 1].r;
     }

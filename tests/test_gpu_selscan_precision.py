@@ -164,3 +164,34 @@ def test_steps_far_from_zero(dtype):
     size = np.abs(f64(x[0]) * f64(dout[0])) * np.abs(Bf * Cf).sum()
     slope = np.exp(-np.logaddexp(-V, 0))
     near(got["ddt_bias"], terms * slope, 16 * U * size * slope + 2.0 ** -125 * size)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_gates_far_from_zero(dtype):
+    """silu(z) and its derivative for z from -200 to 200, of single tokens with D x alone.  fp32: the
+    exponential 5 u, the quotient 1 + 2 u, two products: 12 u allowed; the derivative s + z s (1 - s) 12 u of both
+    terms, and where s is nearly 1, z times the 6 u that it is off.  bf16: without the exponential's remainder,
+    which takes 1.2 u for each of |z|."""
+    z = far(dtype)
+    D, N = len(z), 4
+    g = torch.Generator().manual_seed(26)
+    rnd = lambda *s: torch.randn(*s, generator=g).to(DT[dtype])
+    x, dout, B = rnd(1, D), rnd(1, D), torch.zeros(1, 1, N, dtype=DT[dtype])
+    ops = [t.cuda() for t in (x, rnd(1, D), -torch.ones(D, N), B, B)]
+    kw = dict(D=torch.ones(D).cuda(), z=z[None].cuda())
+    y, _, st = ssd.selscan_fwd(*ops, return_states=True, **kw)
+    cache = torch.zeros(1, D, N, device="cuda")
+    y1 = ssd.selscan_step(*ops, cache, **kw)
+    got = ssd.selscan_bwd(*ops, dout.cuda(), st, **kw)
+    X, Z, G = f64(x[0]), f64(z), f64(dout[0])
+    s = np.exp(-np.logaddexp(-Z, 0))
+    more = 12 + (0 if dtype == "f32" else 1.2 * np.abs(Z))
+    flush = 2.0 ** -125 * np.abs(Z)
+    want = X * Z * s
+    for v in (y, y1):
+        near(v[0], want, (HALF[dtype] + more * U) * np.abs(want) + flush * np.abs(X))
+    want = G * X * s * (1 + Z * (1 - s))
+    size = np.abs(G * X) * ((more * s * (1 + np.abs(Z) * (1 - s)) + 6 * np.abs(Z) * s) * U + flush)
+    near(got["dz"][0], want, HALF[dtype] * np.abs(want) + size)
+    want = G * Z * s                                   # dx = D gy
+    near(got["dx"][0], want, (HALF[dtype] + more * U) * np.abs(want) + flush * np.abs(G))
