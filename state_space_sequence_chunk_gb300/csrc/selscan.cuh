@@ -172,26 +172,28 @@ template <int M> __device__ __forceinline__ void halve(float* v, int lane, int b
 // by half their size, x from 1e-5 to 1).  A state that remembers a thousand tokens is
 // multiplied a thousand times, and would be off by 5e-6 to 1e-5, always to the same side.  So every 16
 // tokens a state gets back what it lost on average, c of it, from the sum of its 16 exponents
-// X = |A| log2(e) sum of delta: c = min(5.5e-4 X, 16 * 2.75e-9 + 2.3e-6 X, 16 * 2.45e-8 / (1 + X)), which is 0
-// where nothing decays.  (2.75e-9 instead of 5.5e-9 because so small a share of h is rounded to a whole last
-// place of it, more often up than down.)  The 1 + X is for states that forget: of one that decays by x a
-// token, what is left of older tokens has lost 16 times, but is little of it.  Inputs of either sign, 2400 tokens in
-// one piece, decays of e^-d a token, d = 0.001, 0.01, 0.04, 0.1, 1: states off on average by 3e-7, -4e-8,
-// 7e-8, 5e-8, -1e-8 (without c -2.5e-6, -1.2e-6, -2.2e-7, -7e-8, -1e-8; without the 1 + X 3e-7, 2e-7, 3e-7, 3e-7,
-// 4e-7), their gradients about the same; 5 to 6 % of the forward pass's time, 3 of the gradient's.  What is left are the
-// single roundings, whose directions differ.
+// X = |A| log2(e) sum of delta: c = min(5.5e-4 X, 16 * 2.75e-9 + 2.3e-6 X, 16 * 2.45e-8, 16 * 2.45e-8 / (0.35 + 1.6 X)),
+// which is 0 where nothing decays.  (2.75e-9 instead of 5.5e-9 because so small a share of h is rounded to a whole
+// last place of it, more often up than down.)  The last is for states that forget: what is left of older tokens
+// has lost 16 times, but is little of the state.  It is fitted so that a state is as much too large behind the 16th token as
+// it is too small before it.  Inputs of either sign, 2400 tokens in one piece, decays of e^-d a token, d = 0.001,
+// 0.01, 0.02, 0.04, 0.1, 1: states off on average by 3e-7, 2e-7, 1e-7, 9e-8, 3e-8, -1e-8 behind a 16th token and by 3e-7,
+// 1e-8, -8e-8, -6e-8, -6e-8, 0 behind an 8th (without c -2.5e-6, -1.2e-6, -6.5e-7, -2.2e-7, -7e-8, -1e-8 everywhere;
+// without the last 3e-7, 2e-7, 2e-7, 3e-7, 3e-7, 4e-7 behind a 16th), their gradients about the same; 5 to 6 % of the
+// forward pass's time, 3 of the gradient's.  What is left are the single roundings, whose directions differ.
 constexpr int kMakeUp = 16;
 template <int M> __device__ __forceinline__ void make_up(f32x2 (&h)[M], const f32x2 (&a2)[M], float sum) {
-    const f32x2 s1 = both(-5.5e-4f * sum), s2 = both(-2.3e-6f * sum), s3 = both(-sum);
+    constexpr float kMost = kMakeUp * 2.45e-8f;          // c in units of this
+    const f32x2 s1 = both(-5.5e-4f / kMost * sum), s2 = both(-2.3e-6f / kMost * sum), s3 = both(-1.6f * sum);
 #pragma unroll
     for (int i = 0; i < M; ++i) {
         float a, b, c, d, e, f;
         unpair(mul2(a2[i], s1), a, b);
-        unpair(fma2(a2[i], s2, both(kMakeUp * 2.75e-9f)), c, d);
-        unpair(fma2(a2[i], s3, both(1.f)), e, f);
-        a = fmaxf(fminf(fminf(a, c), kMakeUp * 2.45e-8f * rcp(e)), 0.f);
-        b = fmaxf(fminf(fminf(b, d), kMakeUp * 2.45e-8f * rcp(f)), 0.f);
-        h[i] = fma2(h[i], pair(a, b), h[i]);
+        unpair(fma2(a2[i], s2, both(kMakeUp * 2.75e-9f / kMost)), c, d);
+        unpair(fma2(a2[i], s3, both(0.35f)), e, f);
+        a = __saturatef(fminf(fminf(a, c), rcp(e)));
+        b = __saturatef(fminf(fminf(b, d), rcp(f)));
+        h[i] = fma2(h[i], mul2(pair(a, b), both(kMost)), h[i]);
     }
 }
 

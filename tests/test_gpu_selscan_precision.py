@@ -131,6 +131,23 @@ def test_states_of_every_memory_lean_to_no_side(rate, cut, extra):
         assert abs(lean) < max(lost / 3, 1e-7), lean
 
 
+@pytest.mark.parametrize("rate", [1e-2, 0.02, 0.04, 0.1])
+def test_states_lean_to_no_side_between_corrections(rate):
+    """The same of 2408 tokens: the state gets back what 16 tokens lose (16 * 2.4e-8 at most) behind each 16th, and
+    should be as much too large there as too small before it, so nearly right behind an 8th: 1e-7 as
+    above and two tokens' loss."""
+    T, D, N = 2408, 64, 16
+    g = torch.Generator().manual_seed(28)
+    rnd = lambda *s: torch.randn(*s, generator=g)
+    uni = lambda *s: torch.rand(*s, generator=g)
+    x, B, dt, A = rnd(T, D), rnd(T, 1, N), rate * (0.5 + uni(T, D)), -(0.8 + 0.4 * uni(D, N))
+    cu = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+    _, fin = ssd.selscan_fwd(*(t.cuda() for t in (x, dt, A, B, B)), cu_seqlens=cu, max_seqlen=1)
+    _, want = selscan(*(f64(t) for t in (x, dt, A, B, B)), [T], softplus=False)
+    lean = ((f64(fin) - want) * want).sum() / (want * want).sum()
+    assert abs(lean) < 1.5e-7, lean
+
+
 def far(dtype):
     """Numbers from -200 to 200, of the given type, dense where exponentials still count."""
     v = torch.cat([torch.linspace(-200, 200, 353), torch.linspace(-90, -10, 511), torch.linspace(-10, 10, 160)])
