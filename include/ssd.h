@@ -438,7 +438,8 @@ typedef enum { SSD_ACT_NONE = 0, SSD_ACT_SILU = 1 } ssd_act;
  * (8 .. 65536, a multiple of 8) in all, `nseqs` sequences (for ssd_short_conv_step:
  * nseqs == tokens rows of one token each), `width` taps (2 .. 8).  Rows of x lie
  * x_stride elements apart (0: contiguous; a multiple of 16 bytes), so that x can be a
- * column range of one projection's output.  nseqs <= 2^20, tokens <= 2^30. */
+ * column range of one projection's output.  nseqs <= 2^20, tokens <= 2^30, and
+ * (tokens / 8 + nseqs + 1) * ceil(dim / 64) < 2^31 - 4, else SSD_ERR_SHAPE. */
 typedef struct {
     int64_t nseqs, tokens, dim, width;
     int64_t x_stride;
@@ -503,7 +504,11 @@ ssd_status ssd_short_conv_step(const ssd_short_conv_dims* d, const void* x, cons
  *     multiples of 16 bytes.  B and C need no alignment beyond their type's, nor do
  *     their strides: they may be any column range of one projection's output.
  *   dt_softplus   whether delta is softplus(dt + dt_bias) (1) or dt + dt_bias (0).
- *   max_seqlen    as for ssd_linattn_dims.   nseqs <= 2^20, tokens <= 2^30. */
+ *   max_seqlen    as for ssd_linattn_dims.  Without it any sequence may be as long as all
+ *                 of the tokens, and calls of many tokens are cut for that (12 prompts of
+ *                 16384 tokens in all, 5120 channels: 627 us instead of 447).
+ *   nseqs <= 2^20, tokens <= 2^30; (nseqs + tokens / 64 + 64) * (dim / 8 + 1) < 2^31 and
+ *   tokens * ngroups * dstate < 2^37 (a little more is SSD_ERR_SHAPE or served). */
 typedef struct {
     int64_t nseqs, tokens, dim, dstate, ngroups;
     int64_t x_stride, dt_stride, z_stride, B_stride, C_stride;
@@ -517,7 +522,11 @@ typedef struct {
 #define SSD_SELSCAN_CHUNK 16
 
 /* Bytes of device workspace of ssd_selscan_fwd (backward = 0) or ssd_selscan_bwd
- * (backward != 0); 0 if none is needed or `d` is invalid. */
+ * (backward != 0); 0 if none is needed or `d` is invalid.  Where sequences are cut into ranges
+ * of R tokens (64 .. 512), (tokens / R + nseqs) * dim * (dstate + 1) * 4 bytes; the gradient
+ * besides tokens * ngroups * dstate * 8 bytes for each tile of 64 channels of a group
+ * (32 where dstate > 16, 16 where dstate > 32: 32 bytes for each token and channel with 64
+ * states), and up to 512 * dim * (dstate + 2) * 4. */
 size_t ssd_selscan_workspace_bytes(const ssd_selscan_dims* d, int backward);
 
 /*
@@ -562,9 +571,9 @@ ssd_status ssd_selscan_fwd(const ssd_selscan_dims* d, const void* x, const void*
  * first) and dout [tokens, dim].  Outputs: dx, ddt, dz [tokens, dim] and dB, dC
  * [tokens, ngroups, dstate], contiguous, in `dtype` (0 in rows of no sequence; dz is not
  * written without z); dA [dim, dstate], dD, ddt_bias [dim] fp32 (the last two may be
- * NULL to skip); dinit_state fp32, or NULL to skip.  Sums over channels, tokens and
- * sequences are added in a fixed order.  Outputs must not overlap an input or each
- * other (SSD_ERR_ALIAS).
+ * NULL to skip); dinit_state fp32, or NULL to skip.  All sums are fp32, each output is
+ * rounded once; sums over channels, tokens and sequences are added in a fixed order.
+ * Outputs must not overlap an input or each other (SSD_ERR_ALIAS).
  */
 ssd_status ssd_selscan_bwd(const ssd_selscan_dims* d, const void* x, const void* dt, const float* A,
                            const void* B, const void* C, const float* D, const void* z,
