@@ -873,7 +873,9 @@ def selscan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus: bool 
     d // (dim // G) of B and C.  Rows may be slices of a wider tensor's; those of B and C
     need no alignment.  A [dim, N], D, dt_bias [dim] and init_state [nseqs, dim, N] are
     float32; D, z and dt_bias may be None.  ``max_seqlen`` (0: not known) spares the
-    preparations for long sequences where there are none.
+    preparations for long sequences where there are none: without it any sequence may be as
+    long as all of the tokens (12 prompts of 16384 tokens in all, 5120 channels: 627 us
+    instead of 447).
     Returns ``(y [tokens, dim], final_state [nseqs, dim, N] float32 or None)``, with
     ``return_states`` also the states on the way that selscan_bwd needs,
     [tokens // SELSCAN_CHUNK + nseqs, dim, N] float32.

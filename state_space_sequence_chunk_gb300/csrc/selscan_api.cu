@@ -52,14 +52,15 @@ ssd_status make(const ssd_selscan_dims* d, bool packed, bool backward, Scan* out
     q.checkpoints = (size_t)((q.T / kScanChunk + q.n) * q.D * q.N) * 4;
 
     // A sequence is cut where a chain of its whole length would keep the other SMs waiting.  A
-    // warp by itself takes 104 ns a token; the cut's two passes take 225 ps for each token
+    // warp by itself takes 113 ns a token; the cut's two passes take 240 ps for each token
     // and warp when all SMs work, and some 25 us of launches and ramps.  Whole and cut, us, 16
-    // states: 256 tokens of 2048 channels (64 warps) 35 and 39, 512 of 5120 64 and 46, 2048 of
-    // 2048 in 4 sequences 94 and 59, 8192 of 2048 860 and 154, in 6 sequences 217 and 151;
-    // 16384 of 5120 in 12 427 and 616; 16384 of 2048 in 40 197 and 275; 4096 of 768, 64 states, in 8
-    // 120 and 154.  Backwards a CTA of 64 (32, 16) channels takes 310 ns a token by itself, and
-    // the cut's passes 1.8 ns for each token and CTA: the same sizes 96 and 65, 177 and 117, 282 and
-    // 158, 2490 and 486, 721 and 490, -, 850 and 936, 450 and 447.
+    // states: 256 tokens of 2048 channels (64 warps) 37 and 40, 512 of 5120 63 and 47, 2048 of
+    // 2048 in 4 sequences 95 and 61, 8192 of 2048 929 and 152, in 6 sequences 227 and 155;
+    // 16384 of 5120 in 12 447 and 627; 16384 of 2048 in 40 207 and 293; 4096 of 768, 64 states, in 8
+    // 123 and 158.  Backwards a CTA of 64 (32, 16) channels takes 285 ns a token by itself, and
+    // the cut's passes 1.7 ns for each token and CTA: the same sizes 92 and 64, 167 and 113, 265 and
+    // 153, 2338 and 462, 672 and 465, -, 799 and 874, 448 and 447.  Where the longest sequence is not
+    // known it may be all of the tokens.
     const int64_t bt = selscan_bwd_channels((int)q.N), tiles = (p.cpg + bt - 1) / bt;
     const int64_t warps = q.G * ((p.cpg * (q.N <= 16 ? 1 : q.N <= 32 ? 2 : 4) + 31) / 32);
     const int64_t sms = sm_count(), work = q.T * (backward ? tiles * q.G : warps);
@@ -68,8 +69,8 @@ ssd_status make(const ssd_selscan_dims* d, bool packed, bool backward, Scan* out
     g.R = INT_MAX;
     if (q.n > 0 && longest > (backward ? work / (sms * 8 / 7) + 136 : work / (3 * sms) + 256)) {
         // several ranges for each warp that is resident, but not too short (2048 tokens of 1536
-        // channels: ranges of 32, 64, 96, 128, 256 tokens 51, 49, 48, 55, 65 us, backwards 124, 122,
-        // 122, 129, 151; 8192 of 2048: 64, 96, 128 160, 148, 150; 65536 of 1536: 96, 160, 384: 807, 767, 742)
+        // channels: ranges of 32, 64, 96, 128, 256 tokens 52, 49, 49, 57, 65 us, backwards 123, 123,
+        // 119, 131, 149; 8192 of 2048: 64, 96, 128 163, 153, 153; 65536 of 1536: 96, 160, 384: 842, 804, 779)
         int64_t R = (work / ((backward ? 13 : 54) * sms) + 16) / 32 * 32;
         const int64_t least = backward ? 64 : 96;
         R = R < least ? least : R > 512 ? 512 : R;

@@ -21,8 +21,9 @@
 // over channels on the tensor cores took 6 % less of the call, cut to 11 bits: a token whose
 // channels cancel was off by more than the rounding of its sum.
 //
-// What bounds it: the registers (168 to 255) leave two warps a quarter-SM, each waiting for its own
-// last results.  8192 tokens of 2048 channels in 6 sequences: 457 us a call.  Measured with the tensor cores'
+// What bounds it: the registers (243 for 16 states) leave two warps a quarter-SM, which issue in half of the
+// clocks and wait for their own last results; a token costs a warp of 16 channels 212 instructions.  8192
+// tokens of 2048 channels in 6 sequences: 466 us a call, 361 of them this kernel.  Tried with the tensor cores'
 // sums over states and channels, against 463 (454 to 511 for the older ones): no cut into ranges 670; rows
 // loaded where they are used 617; pairs of channels instead of states, or delta and u stored in
 // pairs: 539, 509; slabs of 2 tokens 485, of 8 tokens 646; more warps an SM, which the

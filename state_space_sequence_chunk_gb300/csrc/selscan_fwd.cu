@@ -5,17 +5,17 @@
 // channel, so the sum over the states needs no other lane.  Tiles of eight tokens
 // of x, dt and z come by cp.async, 16 bytes a lane, three tiles ahead (loaded into
 // registers one tile ahead, as in a first version, a warp by itself waited for
-// memory at every tile: 121 ns a token instead of 101); the rows of B and C, which
+// memory at every tile: 121 ns a token instead of 101 at that time); the rows of B and C, which
 // every lane reads, wait in registers and pass through shared memory as fp32.  A
 // tile's delta and u = delta x are made first, all eight side by side.  The
 // recurrence itself is the packed fp32 instructions' work: per pair of states two
 // products, two multiply-adds and two exponentials.
 //
-// What bounds it: for 16 states a token costs a warp 100 instructions, 91 clocks of
-// the multiply-add pipe and 81 of the exponential's, of which three warps a
-// quarter-SM (168 registers) keep some 60 % busy.  16384 tokens of 5120 channels in
-// 12 sequences: 444 us (20 of them make_up).  Eight states a lane, two lanes a channel
-// (more warps, but every row of B and C is read twice as often for the same work) took
+// What bounds it: for 16 states a token costs a warp 109 instructions (all that are executed, by tokens
+// and warps) and 196 clocks of its quarter-SM, in 52 % of which the multiply-add pipe works and in 44 % the
+// exponentials'; three warps a quarter-SM (166 registers) issue in 60 %.  16384 tokens of 5120 channels in
+// 12 sequences: 445 us (20 of them make_up).  Tried when it took 427 to 432: eight states a lane, two lanes a
+// channel (more warps, but every row of B and C is read twice as often for the same work) took
 // 1.08 times that, four states 1.41; the next tile's delta made between this one's tokens
 // 1.03; the products delta A by scalar instructions, which alone run faster beside the exponential, 1.03;
 // pairs of channels instead of states, delta and u through shared memory (fewer moves, more

@@ -11,11 +11,12 @@
 // (from L2, mostly).  Sequences begin and end anywhere in a tile: the walk goes by its
 // part of each, with the window loaded anew.
 //
-// What bounds it: HBM and, in bf16, about as much the instructions, 49 for four channels
-// of a row.  16384 bf16 tokens of 5120 channels, 4 taps: 59 us, 5.7 TB/s (with other tiles: short_conv_tile; of
+// What bounds it: forwards HBM, in bf16 with about half of the issue slots, 49 instructions for a row of four
+// channels a thread.  16384 bf16 tokens of 5120 channels, 4 taps: 59 us, 5.7 TB/s (with other tiles: short_conv_tile; of
 // tiles of 64, two channels a thread took 1.03 times as long, eight, with checks in the loop instead of
 // parts, 1.6 times); the gradient, 46 instructions for two channels, 108 us, 4.7 TB/s (four channels
-// 1.08 times; bounds in every group of rows 1.05).  fp32, of 2048 channels: 49 us, 5.5 TB/s, and
+// 1.08 times; bounds in every group of rows 1.05): neither HBM (62 %) nor the issue (51 %) is full, rows
+// come in bursts of eight that are waited for.  fp32, of 2048 channels: 50 us, 5.4 TB/s, and
 // 77 us, 5.2 TB/s.  The test for an activation stays in the row: with a kernel of its own for each, the
 // compiler mixes more rows, and spills (1.04 to 1.07 times as long, also with fewer CTAs an SM or rows ahead).
 #include <type_traits>
